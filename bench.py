@@ -99,7 +99,7 @@ def whole_job_rate(units_per_rank_step: float, steps: int, world: int, max_elaps
 
 # ----------------------------------------------------------------------------- ncu traffic
 
-KERNEL_SOURCES = {"decode_split+decode_combine": "decode.cu", "prefill_chunk": "prefill.cu",
+KERNEL_SOURCES = {"decode_split+decode_combine": "decode_kernel.cuh", "prefill_chunk": "prefill.cu",
                   "rope_append": "rope_append.cu"}
 
 

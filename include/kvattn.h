@@ -182,6 +182,76 @@ kvattn_status kvattn_rope_append_strided(const kvattn_config* cfg, const kvattn_
                                          int32_t max_blocks_per_seq, int32_t num_tokens, void* stream);
 
 /*
+ * kvattn_rotary_append -- kvattn_rope_append_strided with the rotary forms
+ * that models use besides adjacent pairs over the whole head: pairs of the
+ * head's two halves, a part of the head only, and speeds scaled for contexts
+ * longer than the one a model was trained on.
+ *
+ * [RoPE page], section 4 (the rotation of a pair) and [Engine page], section
+ * 3.2 (k and v go to the cache index equal to the position).  With R =
+ * rotary_dim (0: head_dim), b = cfg->rope_base, pair i < R / 2 of a head x is
+ *     KVATTN_ROPE_ADJACENT  (x[2i], x[2i + 1])
+ *     KVATTN_ROPE_HALF      (x[i], x[i + R/2])
+ * and a token at position m stores
+ *     x'0 = a (x0 cos(m f_i) - x1 sin(m f_i))
+ *     x'1 = a (x0 sin(m f_i) + x1 cos(m f_i))
+ * with a = amplitude (0: 1); dims R .. head_dim-1 are copied as they are.
+ * Speeds f_i in radians per position, s = factor:
+ *     KVATTN_ROPE_UNSCALED  b^(-2i/R)
+ *     KVATTN_ROPE_LINEAR    b^(-2i/R) / s   (positions pressed together)
+ *     KVATTN_ROPE_BASE      b'^(-2i/R), b' = b s^(R/(R-2))  (the slowest pair
+ *                           slows by s, the fastest keeps its speed)
+ *     KVATTN_ROPE_PARTS     b^(-2i/R) (g + (1 - g) / s), g = (t - low) /
+ *                           (high - low) held to [0, 1], t = original_len
+ *                           b^(-2i/R) / (2 pi): pairs of more than `high` turns
+ *                           over the original context keep their speed, pairs
+ *                           of fewer than `low` turns slow by s
+ * computed in double.  The products and sums of a rotation are fp32 and a
+ * stored element is rounded once: within half an ulp of its type plus
+ * 2^-21 a (|x0| + |x1|) of exact at any position.
+ *
+ * q, k, v, strides, q_out, positions, seq_ids, block_table as
+ * kvattn_rope_append_strided.  rotary_dim is a multiple of 16 up to head_dim.
+ * Errors: INVALID_ARG (null pointer, unknown layout or scaling, rope_base < 1,
+ * factor < 1, low < 0, high <= low, original_len <= 0, negative amplitude, a
+ * value that is not finite; the arguments of kvattn_rope_append_strided),
+ * UNSUPPORTED (rotary_dim), CUDA; device: BAD_INDEX (that token is skipped).
+ * num_tokens == 0 launches nothing.
+ *
+ * kvattn_rotary_append_fp8: the same into a kvattn_cache_fp8 (cfg->dtype
+ * KVATTN_BF16, head_dim 128): q as above, and each rotated k row (its bf16
+ * values) and each v row stored as kvattn_rope_append_fp8 stores them.
+ */
+typedef enum { KVATTN_ROPE_ADJACENT = 0, KVATTN_ROPE_HALF = 1 } kvattn_rope_layout;
+typedef enum {
+    KVATTN_ROPE_UNSCALED = 0,
+    KVATTN_ROPE_LINEAR = 1,
+    KVATTN_ROPE_BASE = 2,
+    KVATTN_ROPE_PARTS = 3
+} kvattn_rope_scaling;
+
+typedef struct {
+    int32_t layout;        /* kvattn_rope_layout */
+    int32_t rotary_dim;    /* R: a multiple of 16; 0 => head_dim */
+    int32_t scaling;       /* kvattn_rope_scaling */
+    float factor;          /* s (all scalings but UNSCALED) */
+    float original_len;    /* PARTS */
+    float low, high;       /* PARTS: turns over original_len */
+    float amplitude;       /* a; 0 => 1 */
+} kvattn_rotary;
+
+kvattn_status kvattn_rotary_append(const kvattn_config* cfg, const kvattn_rotary* rotary, const kvattn_cache* cache,
+                                   void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                   int64_t v_stride, void* q_out, const int32_t* positions, const int32_t* seq_ids,
+                                   const int32_t* block_table, int32_t num_seqs, int32_t max_blocks_per_seq,
+                                   int32_t num_tokens, void* stream);
+kvattn_status kvattn_rotary_append_fp8(const kvattn_config* cfg, const kvattn_rotary* rotary,
+                                       const kvattn_cache_fp8* cache, void* q, int64_t q_stride, const void* k,
+                                       int64_t k_stride, const void* v, int64_t v_stride, void* q_out,
+                                       const int32_t* positions, const int32_t* seq_ids, const int32_t* block_table,
+                                       int32_t num_seqs, int32_t max_blocks_per_seq, int32_t num_tokens, void* stream);
+
+/*
  * Multi-layer cache: one device allocation holding every layer's K area and V
  * area, so that one block id (one block-table entry, one allocator) names the
  * same block in all of them.
@@ -348,6 +418,40 @@ kvattn_status kvattn_decode_static_scratch(const kvattn_config* cfg, const kvatt
                                            void* out, void* stream);
 
 /*
+ * kvattn_decode_window -- kvattn_decode with a sliding window and sink tokens:
+ * the new token (position L - 1, L = seq_lens[b]) sees the keys
+ *     i < L  with  i >= L - window  or  i < num_sinks
+ * ([Engine page], section 3.3: the mask says which cached keys a query sees;
+ * the scores, softmax and merge are kvattn_decode's).
+ *
+ * Only blocks that hold a key the token sees are read: the other entries of a
+ * block-table row may be anything (-1 for blocks given back to the allocator
+ * when they slid out of the window), and what their slots, or unseen slots of
+ * blocks that are read, hold has no effect (NaN and infinities too).
+ *   window      >= 1; INT32_MAX sees the whole cache
+ *   num_sinks   >= 0
+ *   workspace   >= kvattn_decode_window_workspace_size(...) bytes, as
+ *               kvattn_decode's; calls that may overlap on the GPU (two
+ *               streams, two captured graphs) need one each
+ * The other arguments, results and errors as kvattn_decode.
+ *
+ * kvattn_decode_window_fp8: the same over a kvattn_cache_fp8, as
+ * kvattn_decode_fp8 (same workspace size).
+ */
+size_t kvattn_decode_window_workspace_size(const kvattn_config* cfg, int32_t batch, int32_t max_seq_len,
+                                           int32_t window, int32_t num_sinks, int32_t num_splits);
+kvattn_status kvattn_decode_window(const kvattn_config* cfg, const kvattn_cache* cache, const void* q,
+                                   const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                   int32_t batch, int32_t max_seq_len, int32_t window, int32_t num_sinks,
+                                   int32_t num_splits, void* out, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+kvattn_status kvattn_decode_window_fp8(const kvattn_config* cfg, const kvattn_cache_fp8* cache, const void* q,
+                                       const int32_t* block_table, int32_t max_blocks_per_seq,
+                                       const int32_t* seq_lens, int32_t batch, int32_t max_seq_len, int32_t window,
+                                       int32_t num_sinks, int32_t num_splits, void* out, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+/*
  * kvattn_prefill_chunk -- causal attention of chunks of new query tokens
  * against their sequences' caches, which already hold the chunks' own keys
  * (call kvattn_rope_append for the chunk tokens first).
@@ -416,6 +520,42 @@ kvattn_status kvattn_prefill_chunk_fp8(const kvattn_config* cfg, const kvattn_ca
                                        int32_t max_q_len, int32_t total_q, int64_t max_kv_tokens,
                                        void* out, void* workspace, size_t workspace_bytes,
                                        void* stream);
+
+/*
+ * kvattn_prefill_window -- kvattn_prefill_chunk with a sliding window and sink
+ * tokens: row r of chunk c, at position p = prefix_lens[c] + r, sees the keys
+ *     i <= p  with  i > p - window  or  i < num_sinks.
+ * The windowed mask of kvattn_decode_window for every row: a chunk of one row
+ * and kvattn_decode_window agree.
+ *
+ * Only blocks that hold a key some row of the chunk sees are read; the other
+ * table entries, and the slots that no row of the chunk sees, may be anything.
+ * V elements that some row of a chunk sees must be finite (a row's weight of a
+ * key it does not see is 0, and 0 times an infinity is not).
+ *   window      >= 1, num_sinks >= 0; sequences of up to 2^30 keys (a longer
+ *               one is a BAD_INDEX)
+ * The other arguments, results and errors as kvattn_prefill_chunk.
+ *
+ * kvattn_prefill_window_fp8: the same over a kvattn_cache_fp8, attending over
+ * the values of kvattn_prefill_chunk_fp8 (head_dim 128).  The pages that a
+ * chunk sees are expanded into `workspace`, at least
+ * kvattn_prefill_window_fp8_workspace_size(...) bytes (any alignment, any
+ * contents, free again once the stream has passed the call), which bounds them
+ * by max_q_len, window and num_sinks (0 for invalid arguments).  Errors in
+ * addition: WORKSPACE_TOO_SMALL.
+ */
+kvattn_status kvattn_prefill_window(const kvattn_config* cfg, const kvattn_cache* cache, const void* q,
+                                    const int32_t* cu_q_lens, const int32_t* prefix_lens, const int32_t* block_table,
+                                    int32_t max_blocks_per_seq, int32_t num_chunks, int32_t max_q_len,
+                                    int32_t total_q, int32_t window, int32_t num_sinks, void* out, void* stream);
+size_t kvattn_prefill_window_fp8_workspace_size(const kvattn_config* cfg, int32_t block_size,
+                                                int32_t max_blocks_per_seq, int32_t num_chunks, int32_t max_q_len,
+                                                int32_t window, int32_t num_sinks);
+kvattn_status kvattn_prefill_window_fp8(const kvattn_config* cfg, const kvattn_cache_fp8* cache, const void* q,
+                                        const int32_t* cu_q_lens, const int32_t* prefix_lens,
+                                        const int32_t* block_table, int32_t max_blocks_per_seq, int32_t num_chunks,
+                                        int32_t max_q_len, int32_t total_q, int32_t window, int32_t num_sinks,
+                                        void* out, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Waits for `stream`, then returns the device status word of the current

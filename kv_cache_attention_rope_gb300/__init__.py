@@ -42,6 +42,9 @@ EXPORTED = [
     "kvattn_allocator_refcount", "kvattn_table_grow", "kvattn_table_release",
     "kvattn_layered_cache_bytes", "kvattn_layer_cache", "kvattn_copy_blocks", "kvattn_copy_blocks_layered",
     "kvattn_table_fork", "kvattn_table_prepare_append", "kvattn_rope_append_fp8", "kvattn_decode_fp8",
+    "kvattn_rotary_append", "kvattn_rotary_append_fp8",
+    "kvattn_decode_window_workspace_size", "kvattn_decode_window", "kvattn_decode_window_fp8",
+    "kvattn_prefill_window", "kvattn_prefill_window_fp8_workspace_size", "kvattn_prefill_window_fp8",
 ]
 
 
@@ -66,6 +69,15 @@ class CacheDesc(ctypes.Structure):
 class CacheFP8Desc(ctypes.Structure):
     _fields_ = [("pool", ctypes.c_void_p), ("num_blocks", ctypes.c_int64), ("block_size", ctypes.c_int32)]
 
+
+class Rotary(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("factor", ctypes.c_float), ("original_len", ctypes.c_float), ("low", ctypes.c_float),
+                ("high", ctypes.c_float), ("amplitude", ctypes.c_float)]
+
+
+ROPE_LAYOUT = {"adjacent": 0, "half": 1}
+ROPE_SCALING = {"none": 0, "linear": 1, "base": 2, "parts": 3}
 
 FP8_PAGE_BYTES = 4224  # one (block, KV head, 16 tokens) page at head_dim 128
 
@@ -102,6 +114,18 @@ def _load():
         "kvattn_prefill_fp8_workspace_size": ([cfgp, i32, i32, i32, i64], sz),
         "kvattn_prefill_chunk_fp8": ([cfgp, ctypes.POINTER(CacheFP8Desc), p, p, p, p, i32, i32, i32, i32, i64, p, p,
                                       sz, p], ctypes.c_int),
+        "kvattn_rotary_append": ([cfgp, ctypes.POINTER(Rotary), cachep, p, i64, p, i64, p, i64, p, p, p, p, i32, i32,
+                                  i32, p], ctypes.c_int),
+        "kvattn_rotary_append_fp8": ([cfgp, ctypes.POINTER(Rotary), ctypes.POINTER(CacheFP8Desc), p, i64, p, i64, p,
+                                      i64, p, p, p, p, i32, i32, i32, p], ctypes.c_int),
+        "kvattn_decode_window_workspace_size": ([cfgp, i32, i32, i32, i32, i32], sz),
+        "kvattn_decode_window": ([cfgp, cachep, p, p, i32, p, i32, i32, i32, i32, i32, p, p, sz, p], ctypes.c_int),
+        "kvattn_decode_window_fp8": ([cfgp, ctypes.POINTER(CacheFP8Desc), p, p, i32, p, i32, i32, i32, i32, i32, p,
+                                      p, sz, p], ctypes.c_int),
+        "kvattn_prefill_window": ([cfgp, cachep, p, p, p, p, i32, i32, i32, i32, i32, i32, p, p], ctypes.c_int),
+        "kvattn_prefill_window_fp8_workspace_size": ([cfgp, i32, i32, i32, i32, i32, i32], sz),
+        "kvattn_prefill_window_fp8": ([cfgp, ctypes.POINTER(CacheFP8Desc), p, p, p, p, i32, i32, i32, i32, i32, i32,
+                                       p, p, sz, p], ctypes.c_int),
         "kvattn_get_device_status": ([p, ctypes.POINTER(i32)], ctypes.c_int),
         "kvattn_selftest_wait_timeout": ([i32, p], ctypes.c_int),
         "kvattn_allocator_create": ([i64, ctypes.POINTER(p)], ctypes.c_int),
@@ -454,6 +478,179 @@ def prefill_chunk_fp8(cfg: Config, cache: CacheFP8, q, cu_q_lens, prefix_lens, b
                                        _dev(out, "out", torch.bfloat16), _dev(workspace, "workspace"),
                                        workspace.numel(), _stream(stream)),
           "kvattn_prefill_chunk_fp8")
+    return out
+
+
+# ------------------------------------------------------------------ rotary forms, sliding windows
+
+def make_rotary(layout: str = "adjacent", rotary_dim: int = 0, scaling: str = "none", factor: float = 1.0,
+                original_len: float = 0.0, low: float = 1.0, high: float = 32.0, amplitude: float = 1.0) -> Rotary:
+    """The rotary form of kvattn_rotary_append: pairs "adjacent" or "half", rotary_dim rotated dims (0: the whole
+    head), speeds "none", "linear", "base" or "parts" scaled by factor, amplitude on the rotated dims."""
+    return Rotary(ROPE_LAYOUT[layout], rotary_dim, ROPE_SCALING[scaling], factor, original_len, low, high, amplitude)
+
+
+def _same_device(*tensors) -> None:
+    """Every tensor on the current CUDA device: kernels are launched there."""
+    current = _torch().cuda.current_device()
+    for t in tensors:
+        if t.is_cuda and t.get_device() != current:
+            raise ValueError(f"tensor on {t.device}, but cuda:{current} is the current device")
+
+
+def _shape(t, name: str, *shape) -> None:
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _check_cache(cfg: Config, cache, kind) -> None:
+    if type(cache) is not kind:
+        raise TypeError(f"cache must be a {kind.__name__}")
+    if cache.num_kv_heads != cfg.num_kv_heads or cache.head_dim != cfg.head_dim:
+        raise ValueError("cache heads / head_dim do not match the config")
+    if kind is Cache and dtype_code(cache.k_pool) != cfg.dtype:
+        raise TypeError("cache element type does not match the config")
+
+
+def _dtype(cfg: Config):
+    torch = _torch()
+    return torch.bfloat16 if cfg.dtype == BF16 else torch.float32
+
+
+def _rotary_append(fn, what, kind, cfg, rotary, cache, q, k, v, positions, seq_ids, block_table, stream, q_out):
+    torch = _torch()
+    _check_cache(cfg, cache, kind)
+    T, dt = q.shape[0], _dtype(cfg)
+    hq, hkv, d = cfg.num_q_heads, cfg.num_kv_heads, cfg.head_dim
+    qp, qs = _rows(q, "q", hq, d, dt)
+    kp, ks = _rows(k, "k", hkv, d, dt)
+    vp, vs = _rows(v, "v", hkv, d, dt)
+    if k.shape[0] != T or v.shape[0] != T:
+        raise ValueError("q, k and v differ in tokens")
+    _shape(positions, "positions", T)
+    _shape(seq_ids, "seq_ids", T)
+    qo = None
+    if q_out is not None:
+        _shape(q_out, "q_out", T, hq, d)
+        qo = _dev(q_out, "q_out", dt)
+    _same_device(q, k, v, positions, block_table)
+    check(fn(ctypes.byref(cfg), ctypes.byref(rotary), ctypes.byref(cache.desc), qp, qs, kp, ks, vp, vs, qo,
+             _dev(positions, "positions", torch.int32), _dev(seq_ids, "seq_ids", torch.int32),
+             _dev(block_table, "block_table", torch.int32), block_table.shape[0], block_table.shape[1], T,
+             _stream(stream)), what)
+
+
+def rotary_append(cfg: Config, rotary: Rotary, cache: Cache, q, k, v, positions, seq_ids, block_table, stream=None,
+                  q_out=None) -> None:
+    """kvattn_rotary_append: rotate q in place (or into q_out), write rotated k and raw v into the cache, in the
+    rotary form of make_rotary.  q, k, v as for rope_append (dense, or views of a fused QKV output)."""
+    _rotary_append(lib.kvattn_rotary_append, "kvattn_rotary_append", Cache, cfg, rotary, cache, q, k, v, positions,
+                   seq_ids, block_table, stream, q_out)
+
+
+def rotary_append_fp8(cfg: Config, rotary: Rotary, cache: CacheFP8, q, k, v, positions, seq_ids, block_table,
+                      stream=None, q_out=None) -> None:
+    """kvattn_rotary_append_fp8: rotary_append into an fp8 cache (bf16 q, k, v)."""
+    _rotary_append(lib.kvattn_rotary_append_fp8, "kvattn_rotary_append_fp8", CacheFP8, cfg, rotary, cache, q, k, v,
+                   positions, seq_ids, block_table, stream, q_out)
+
+
+def decode_window_workspace_size(cfg: Config, batch: int, max_seq_len: int, window: int, num_sinks: int = 0,
+                                 num_splits: int = 0) -> int:
+    """kvattn_decode_window_workspace_size (0 for invalid arguments)."""
+    return int(lib.kvattn_decode_window_workspace_size(ctypes.byref(cfg), batch, max_seq_len, window, num_sinks,
+                                                       num_splits))
+
+
+def _decode_window(fn, what, kind, cfg, cache, q, block_table, seq_lens, max_seq_len, window, num_sinks, out,
+                   workspace, num_splits, stream):
+    torch = _torch()
+    _check_cache(cfg, cache, kind)
+    B, dt = q.shape[0], _dtype(cfg)
+    _shape(q, "q", B, cfg.num_q_heads, cfg.head_dim)
+    _shape(seq_lens, "seq_lens", B)
+    if block_table.dim() != 2 or block_table.shape[0] < B:
+        raise ValueError(f"block_table must have a row for each of the {B} sequences")
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _shape(out, "out", *q.shape)
+    if workspace is None:
+        n = decode_window_workspace_size(cfg, B, max_seq_len, window, num_sinks, num_splits)
+        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+    _same_device(q, block_table, seq_lens, out, workspace)
+    check(fn(ctypes.byref(cfg), ctypes.byref(cache.desc), _dev(q, "q", dt),
+             _dev(block_table, "block_table", torch.int32), block_table.shape[1],
+             _dev(seq_lens, "seq_lens", torch.int32), B, max_seq_len, window, num_sinks, num_splits,
+             _dev(out, "out", dt), _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+             _stream(stream)), what)
+    return out
+
+
+def decode_window(cfg: Config, cache: Cache, q, block_table, seq_lens, max_seq_len: int, window: int,
+                  num_sinks: int = 0, out=None, workspace=None, num_splits: int = 0, stream=None):
+    """kvattn_decode_window: one query token per sequence against the last `window` cached tokens and the first
+    num_sinks.  Table entries of blocks that hold neither may be anything (-1 once they were freed)."""
+    return _decode_window(lib.kvattn_decode_window, "kvattn_decode_window", Cache, cfg, cache, q, block_table,
+                          seq_lens, max_seq_len, window, num_sinks, out, workspace, num_splits, stream)
+
+
+def decode_window_fp8(cfg: Config, cache: CacheFP8, q, block_table, seq_lens, max_seq_len: int, window: int,
+                      num_sinks: int = 0, out=None, workspace=None, num_splits: int = 0, stream=None):
+    """kvattn_decode_window_fp8: decode_window over an fp8 cache (bf16 q and output)."""
+    return _decode_window(lib.kvattn_decode_window_fp8, "kvattn_decode_window_fp8", CacheFP8, cfg, cache, q,
+                          block_table, seq_lens, max_seq_len, window, num_sinks, out, workspace, num_splits, stream)
+
+
+def _prefill_window_args(kind, cfg, cache, q, cu_q_lens, prefix_lens, block_table, out):
+    torch = _torch()
+    _check_cache(cfg, cache, kind)
+    n = prefix_lens.shape[0]
+    _shape(q, "q", q.shape[0], cfg.num_q_heads, cfg.head_dim)
+    _shape(cu_q_lens, "cu_q_lens", n + 1)
+    if block_table.dim() != 2 or block_table.shape[0] < n:
+        raise ValueError(f"block_table must have a row for each of the {n} chunks")
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _shape(out, "out", *q.shape)
+    _same_device(q, cu_q_lens, prefix_lens, block_table, out)
+    return out, n, (_dev(q, "q", torch.bfloat16), _dev(cu_q_lens, "cu_q_lens", torch.int32),
+                    _dev(prefix_lens, "prefix_lens", torch.int32), _dev(block_table, "block_table", torch.int32),
+                    block_table.shape[1], n)
+
+
+def prefill_window(cfg: Config, cache: Cache, q, cu_q_lens, prefix_lens, block_table, max_q_len: int, window: int,
+                   num_sinks: int = 0, out=None, stream=None):
+    """kvattn_prefill_window: causal attention of query chunks, each row over its last `window` keys and the first
+    num_sinks."""
+    out, _, args = _prefill_window_args(Cache, cfg, cache, q, cu_q_lens, prefix_lens, block_table, out)
+    check(lib.kvattn_prefill_window(ctypes.byref(cfg), ctypes.byref(cache.desc), *args, max_q_len, q.shape[0], window,
+                                    num_sinks, _dev(out, "out", q.dtype), _stream(stream)), "kvattn_prefill_window")
+    return out
+
+
+def prefill_window_fp8_workspace_size(cfg: Config, block_size: int, max_blocks_per_seq: int, num_chunks: int,
+                                      max_q_len: int, window: int, num_sinks: int = 0) -> int:
+    """kvattn_prefill_window_fp8_workspace_size (0 for invalid arguments)."""
+    return int(lib.kvattn_prefill_window_fp8_workspace_size(ctypes.byref(cfg), block_size, max_blocks_per_seq,
+                                                            num_chunks, max_q_len, window, num_sinks))
+
+
+def prefill_window_fp8(cfg: Config, cache: CacheFP8, q, cu_q_lens, prefix_lens, block_table, max_q_len: int,
+                       window: int, num_sinks: int = 0, out=None, workspace=None, stream=None):
+    """kvattn_prefill_window_fp8: prefill_window over an fp8 cache (bf16 q and output)."""
+    torch = _torch()
+    out, n, args = _prefill_window_args(CacheFP8, cfg, cache, q, cu_q_lens, prefix_lens, block_table, out)
+    if workspace is None:
+        size = prefill_window_fp8_workspace_size(cfg, cache.block_size, block_table.shape[1], n, max_q_len, window,
+                                                 num_sinks)
+        workspace = torch.empty(max(size, 256), dtype=torch.uint8, device=q.device)
+    _same_device(workspace)
+    check(lib.kvattn_prefill_window_fp8(ctypes.byref(cfg), ctypes.byref(cache.desc), *args, max_q_len, q.shape[0],
+                                        window, num_sinks, _dev(out, "out", q.dtype), _dev(workspace, "workspace"),
+                                        workspace.numel() * workspace.element_size(), _stream(stream)),
+          "kvattn_prefill_window_fp8")
     return out
 
 

@@ -153,6 +153,55 @@ void rope_tables(double base, int d, RopeArgs& a)
     }
 }
 
+bool rotary_ok(const kvattn_config* c, const kvattn_rotary* r)
+{
+    if (!r || (r->layout != KVATTN_ROPE_ADJACENT && r->layout != KVATTN_ROPE_HALF) || r->rotary_dim < 0 ||
+        !std::isfinite(r->amplitude) || r->amplitude < 0.f || c->rope_base < 1.f)
+        return false;
+    switch (r->scaling) {
+        case KVATTN_ROPE_UNSCALED: return true;
+        case KVATTN_ROPE_LINEAR:
+        case KVATTN_ROPE_BASE: return std::isfinite(r->factor) && r->factor >= 1.f;
+        case KVATTN_ROPE_PARTS:
+            return std::isfinite(r->factor) && r->factor >= 1.f && std::isfinite(r->original_len) &&
+                   r->original_len > 0.f && std::isfinite(r->low) && std::isfinite(r->high) && r->low >= 0.f &&
+                   r->high > r->low;
+    }
+    return false;
+}
+
+// Speed of pair i < rot / 2 in 2^-64 turns per position (kvattn_rotary_append
+// in kvattn.h states the formulas; with base and factor at least 1 it is below
+// 1 / (2 pi) turns).  A model's layers share one form: the last one computed by
+// this host thread is kept.
+void rotary_turns(const kvattn_config* c, const kvattn_rotary* r, int rot, uint64_t* turns)
+{
+    static thread_local kvattn_rotary last;
+    static thread_local float last_base = 0.f;
+    static thread_local int last_rot = 0;
+    static thread_local uint64_t kept[64];
+    if (last_rot != rot || last_base != c->rope_base || std::memcmp(&last, r, sizeof(last)) != 0) {
+        const double two_pi = 6.283185307179586476925286766559, s = r->factor;
+        double base = c->rope_base;
+        if (r->scaling == KVATTN_ROPE_BASE) base *= std::pow(s, (double)rot / (double)(rot - 2));
+        for (int i = 0; i < rot / 2; ++i) {
+            double f = std::pow(base, -2.0 * (double)i / (double)rot) / two_pi;
+            if (r->scaling == KVATTN_ROPE_LINEAR) {
+                f /= s;
+            } else if (r->scaling == KVATTN_ROPE_PARTS) {
+                const double g = ((double)r->original_len * f - r->low) / ((double)r->high - r->low);
+                const double share = std::min(1.0, std::max(0.0, g));
+                f = f * (share + (1.0 - share) / s);
+            }
+            kept[i] = (uint64_t)std::llrint(std::ldexp(f, 64));
+        }
+        last = *r;
+        last_base = c->rope_base;
+        last_rot = rot;
+    }
+    std::memcpy(turns, kept, sizeof(kept));
+}
+
 // One CTA waits on an mbarrier that nothing will complete, through the same
 // bounded wait every kernel uses; the wait runs out and records
 // KVATTN_ERR_TIMEOUT.
@@ -275,6 +324,109 @@ kvattn_status kvattn_rope_append_strided(const kvattn_config* cfg, const kvattn_
     if (!a.status) return KVATTN_ERR_CUDA;
     rope_tables((double)cfg->rope_base, cfg->head_dim, a);
     return launch_rope_append(a, static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+
+kvattn_status rotary_append_any(const kvattn_config* cfg, const kvattn_rotary* rotary, const kvattn_cache* cache,
+                                bool fp8, void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, void* q_out, const int32_t* positions, const int32_t* seq_ids,
+                                const int32_t* block_table, int32_t num_seqs, int32_t max_blocks_per_seq,
+                                int32_t num_tokens, void* stream)
+{
+    if (!config_ok(cfg) || !rotary_ok(cfg, rotary) || num_tokens < 0 || num_seqs <= 0) return KVATTN_ERR_INVALID_ARG;
+    const kvattn_status st = config_supported(cfg);
+    if (st != KVATTN_OK) return st;
+    if (fp8 && (cfg->dtype != KVATTN_BF16 || cfg->head_dim != 128)) return KVATTN_ERR_UNSUPPORTED;
+    const int rot = rotary->rotary_dim ? rotary->rotary_dim : cfg->head_dim;
+    if (rot > cfg->head_dim || rot % 16 != 0) return KVATTN_ERR_UNSUPPORTED;
+    if (!cache_ok(cache, max_blocks_per_seq) || (fp8 && cache->block_size % 16 != 0)) return KVATTN_ERR_INVALID_ARG;
+    const int64_t e = cfg->dtype == KVATTN_BF16 ? 2 : 4;
+    const int64_t qrow = (int64_t)cfg->num_q_heads * cfg->head_dim;
+    const int64_t kvrow = (int64_t)cfg->num_kv_heads * cfg->head_dim;
+    const int64_t max_stride = INT64_MAX / 4 / std::max<int64_t>(1, num_tokens);
+    if (q_stride < qrow || k_stride < kvrow || v_stride < kvrow) return KVATTN_ERR_INVALID_ARG;
+    if (q_stride > max_stride / e || k_stride > max_stride / e || v_stride > max_stride / e)
+        return KVATTN_ERR_INVALID_ARG;
+    if (((q_stride | k_stride | v_stride) * e) & 15) return KVATTN_ERR_INVALID_ARG;
+    if (num_tokens == 0) return KVATTN_OK;
+    if (!q || !k || !v || !positions || !seq_ids || !block_table) return KVATTN_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
+         reinterpret_cast<uintptr_t>(q_out)) & 15u)
+        return KVATTN_ERR_INVALID_ARG;
+    RotaryArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride * e;
+    a.k_stride = k_stride * e;
+    a.v_stride = v_stride * e;
+    a.q_out = q_out ? q_out : q;
+    a.q_out_stride = q_out ? qrow * e : a.q_stride;
+    a.fp8 = fp8 ? 1 : 0;
+    a.k_pool = cache->k_pool;
+    a.v_pool = cache->v_pool;
+    a.positions = positions;
+    a.seq_ids = seq_ids;
+    a.block_table = block_table;
+    a.num_blocks = cache->num_blocks;
+    a.block_size = cache->block_size;
+    a.num_seqs = num_seqs;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_tokens = num_tokens;
+    a.hq = cfg->num_q_heads;
+    a.hkv = cfg->num_kv_heads;
+    a.d = cfg->head_dim;
+    a.dtype = cfg->dtype;
+    a.half = rotary->layout == KVATTN_ROPE_HALF ? 1 : 0;
+    a.rot = rot;
+    a.amplitude = rotary->amplitude > 0.f ? rotary->amplitude : 1.f;
+    a.status = device_status_ptr();
+    if (!a.status) return KVATTN_ERR_CUDA;
+    rotary_turns(cfg, rotary, rot, a.turns);
+    const kvattn_status kst = launch_rotary_append(a, static_cast<cudaStream_t>(stream));
+    if (kst != KVATTN_OK || !fp8) return kst;
+    RopeArgs r;  // the V pages
+    std::memset(&r, 0, sizeof(r));
+    r.v = v;
+    r.v_stride = a.v_stride;
+    r.k_pool = cache->k_pool;
+    r.fp8 = 1;
+    r.positions = positions;
+    r.seq_ids = seq_ids;
+    r.block_table = block_table;
+    r.num_blocks = cache->num_blocks;
+    r.block_size = cache->block_size;
+    r.num_seqs = num_seqs;
+    r.max_blocks = max_blocks_per_seq;
+    r.num_tokens = num_tokens;
+    r.hkv = cfg->num_kv_heads;
+    return launch_append_v_fp8(r, static_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+kvattn_status kvattn_rotary_append(const kvattn_config* cfg, const kvattn_rotary* rotary, const kvattn_cache* cache,
+                                   void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                   int64_t v_stride, void* q_out, const int32_t* positions, const int32_t* seq_ids,
+                                   const int32_t* block_table, int32_t num_seqs, int32_t max_blocks_per_seq,
+                                   int32_t num_tokens, void* stream)
+{
+    return rotary_append_any(cfg, rotary, cache, false, q, q_stride, k, k_stride, v, v_stride, q_out, positions,
+                             seq_ids, block_table, num_seqs, max_blocks_per_seq, num_tokens, stream);
+}
+
+kvattn_status kvattn_rotary_append_fp8(const kvattn_config* cfg, const kvattn_rotary* rotary,
+                                       const kvattn_cache_fp8* cache, void* q, int64_t q_stride, const void* k,
+                                       int64_t k_stride, const void* v, int64_t v_stride, void* q_out,
+                                       const int32_t* positions, const int32_t* seq_ids, const int32_t* block_table,
+                                       int32_t num_seqs, int32_t max_blocks_per_seq, int32_t num_tokens, void* stream)
+{
+    if (!cache) return KVATTN_ERR_INVALID_ARG;
+    const kvattn_cache c{cache->pool, cache->pool, cache->num_blocks, cache->block_size};
+    return rotary_append_any(cfg, rotary, &c, true, q, q_stride, k, k_stride, v, v_stride, q_out, positions, seq_ids,
+                             block_table, num_seqs, max_blocks_per_seq, num_tokens, stream);
 }
 
 namespace {
@@ -402,7 +554,20 @@ size_t kvattn_decode_workspace_size(const kvattn_config* cfg, int32_t batch, int
 
 namespace {
 
-kvattn_status decode_any(const kvattn_config* cfg, const kvattn_cache* cache, bool fp8,
+// The window of a call; window == 0: the whole cache.
+struct DecodeWindow {
+    int32_t window, sinks;
+};
+
+// Most keys that one query sees, rounded up to whole 16-token tiles.
+int32_t window_span(int32_t max_seq_len, DecodeWindow w)
+{
+    if (w.window == 0) return max_seq_len;
+    const int64_t tiles = ((int64_t)w.sinks + 15) / 16 + ((int64_t)w.window + 14) / 16 + 1;
+    return (int32_t)std::min<int64_t>(max_seq_len, tiles * 16);
+}
+
+kvattn_status decode_any(const kvattn_config* cfg, const kvattn_cache* cache, bool fp8, DecodeWindow win,
                          const void* q, const int32_t* block_table, int32_t max_blocks_per_seq,
                          const int32_t* seq_lens, int32_t batch, int32_t max_seq_len, int32_t num_splits, void* out,
                          void* workspace, size_t workspace_bytes, void* stream)
@@ -410,8 +575,8 @@ kvattn_status decode_any(const kvattn_config* cfg, const kvattn_cache* cache, bo
     const kvattn_status st = decode_check(cfg, cache, fp8, q, block_table, max_blocks_per_seq, seq_lens, batch,
                                           max_seq_len, num_splits, out);
     if (st != KVATTN_OK || batch == 0) return st;
-    const DecodePlan p = decode_plan(batch, cfg->num_kv_heads, cfg->num_q_heads / cfg->num_kv_heads, max_seq_len,
-                                     num_splits);
+    const DecodePlan p = decode_plan(batch, cfg->num_kv_heads, cfg->num_q_heads / cfg->num_kv_heads,
+                                     window_span(max_seq_len, win), num_splits);
     const WorkspaceLayout wl = workspace_layout(cfg, batch, p.slots);
     if (p.slots > 1) {
         if (!workspace || workspace_bytes < wl.bytes) return KVATTN_ERR_WORKSPACE_TOO_SMALL;
@@ -445,7 +610,10 @@ kvattn_status decode_any(const kvattn_config* cfg, const kvattn_cache* cache, bo
     a.fp8 = fp8 ? 1 : 0;
     a.status = device_status_ptr();
     if (!a.status) return KVATTN_ERR_CUDA;
-    return launch_decode(a, static_cast<cudaStream_t>(stream));
+    a.window = win.window;
+    a.sinks = win.sinks;
+    return win.window ? launch_decode_window(a, static_cast<cudaStream_t>(stream))
+                      : launch_decode(a, static_cast<cudaStream_t>(stream));
 }
 
 }  // namespace
@@ -455,7 +623,7 @@ kvattn_status kvattn_decode(const kvattn_config* cfg, const kvattn_cache* cache,
                             int32_t batch, int32_t max_seq_len, int32_t num_splits, void* out, void* workspace,
                             size_t workspace_bytes, void* stream)
 {
-    return decode_any(cfg, cache, false, q, block_table, max_blocks_per_seq, seq_lens, batch, max_seq_len,
+    return decode_any(cfg, cache, false, {0, 0}, q, block_table, max_blocks_per_seq, seq_lens, batch, max_seq_len,
                       num_splits, out, workspace, workspace_bytes, stream);
 }
 
@@ -466,8 +634,38 @@ kvattn_status kvattn_decode_fp8(const kvattn_config* cfg, const kvattn_cache_fp8
 {
     if (!cache) return KVATTN_ERR_INVALID_ARG;
     const kvattn_cache c{cache->pool, cache->pool, cache->num_blocks, cache->block_size};
-    return decode_any(cfg, &c, true, q, block_table, max_blocks_per_seq, seq_lens, batch, max_seq_len, num_splits,
-                      out, workspace, workspace_bytes, stream);
+    return decode_any(cfg, &c, true, {0, 0}, q, block_table, max_blocks_per_seq, seq_lens, batch, max_seq_len,
+                      num_splits, out, workspace, workspace_bytes, stream);
+}
+
+size_t kvattn_decode_window_workspace_size(const kvattn_config* cfg, int32_t batch, int32_t max_seq_len,
+                                           int32_t window, int32_t num_sinks, int32_t num_splits)
+{
+    if (window < 1 || num_sinks < 0 || max_seq_len < 0) return 0;
+    return kvattn_decode_workspace_size(cfg, batch, window_span(max_seq_len, {window, num_sinks}), num_splits);
+}
+
+kvattn_status kvattn_decode_window(const kvattn_config* cfg, const kvattn_cache* cache, const void* q,
+                                   const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                   int32_t batch, int32_t max_seq_len, int32_t window, int32_t num_sinks,
+                                   int32_t num_splits, void* out, void* workspace, size_t workspace_bytes,
+                                   void* stream)
+{
+    if (window < 1 || num_sinks < 0) return KVATTN_ERR_INVALID_ARG;
+    return decode_any(cfg, cache, false, {window, num_sinks}, q, block_table, max_blocks_per_seq, seq_lens, batch,
+                      max_seq_len, num_splits, out, workspace, workspace_bytes, stream);
+}
+
+kvattn_status kvattn_decode_window_fp8(const kvattn_config* cfg, const kvattn_cache_fp8* cache, const void* q,
+                                       const int32_t* block_table, int32_t max_blocks_per_seq,
+                                       const int32_t* seq_lens, int32_t batch, int32_t max_seq_len, int32_t window,
+                                       int32_t num_sinks, int32_t num_splits, void* out, void* workspace,
+                                       size_t workspace_bytes, void* stream)
+{
+    if (!cache || window < 1 || num_sinks < 0) return KVATTN_ERR_INVALID_ARG;
+    const kvattn_cache c{cache->pool, cache->pool, cache->num_blocks, cache->block_size};
+    return decode_any(cfg, &c, true, {window, num_sinks}, q, block_table, max_blocks_per_seq, seq_lens, batch,
+                      max_seq_len, num_splits, out, workspace, workspace_bytes, stream);
 }
 
 kvattn_status kvattn_rope_append_fp8(const kvattn_config* cfg, const kvattn_cache_fp8* cache, void* q,
@@ -604,6 +802,103 @@ kvattn_status kvattn_prefill_chunk_fp8(const kvattn_config* cfg, const kvattn_ca
     a.status = device_status_ptr();
     if (!a.status) return KVATTN_ERR_CUDA;
     return launch_prefill_fp8(a, cache->pool, L, workspace, static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+
+// Checks shared by the two windowed prefills, and their kernel arguments.
+// Nothing to do (*todo false) is KVATTN_OK.
+kvattn_status prefill_window_args(const kvattn_config* cfg, const kvattn_cache* cache, const void* q,
+                                  const int32_t* cu_q_lens, const int32_t* prefix_lens, const int32_t* block_table,
+                                  int32_t max_blocks_per_seq, int32_t num_chunks, int32_t max_q_len, int32_t total_q,
+                                  int32_t window, int32_t num_sinks, void* out, PrefillArgs& a, bool* todo)
+{
+    *todo = false;
+    if (!config_ok(cfg) || num_chunks < 0 || max_q_len < 0 || total_q < 0 || window < 1 || num_sinks < 0)
+        return KVATTN_ERR_INVALID_ARG;
+    const kvattn_status st = config_supported(cfg);
+    if (st != KVATTN_OK) return st;
+    if (cfg->dtype != KVATTN_BF16) return KVATTN_ERR_UNSUPPORTED;
+    if (!cache_ok(cache, max_blocks_per_seq)) return KVATTN_ERR_INVALID_ARG;
+    if (cache->block_size % 16 != 0) return KVATTN_ERR_UNSUPPORTED;
+    if (num_chunks == 0 || total_q == 0 || max_q_len == 0) return KVATTN_OK;
+    if (!q || !cu_q_lens || !prefix_lens || !block_table || !out) return KVATTN_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15u) return KVATTN_ERR_INVALID_ARG;
+    std::memset(&a, 0, sizeof(a));
+    a.q = q;
+    a.k_pool = cache->k_pool;
+    a.v_pool = cache->v_pool;
+    a.cu_q_lens = cu_q_lens;
+    a.prefix_lens = prefix_lens;
+    a.block_table = block_table;
+    a.out = out;
+    a.num_blocks = cache->num_blocks;
+    a.block_size = cache->block_size;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_chunks = num_chunks;
+    a.max_q_len = max_q_len;
+    a.total_q = total_q;
+    a.hq = cfg->num_q_heads;
+    a.hkv = cfg->num_kv_heads;
+    a.d = cfg->head_dim;
+    a.scale_log2 = scale_of(cfg) * 1.4426950408889634f;
+    a.window = std::min(window, kMaxWindowKeys);
+    a.sinks = std::min(num_sinks, kMaxWindowKeys);
+    *todo = true;
+    return KVATTN_OK;
+}
+
+}  // namespace
+
+kvattn_status kvattn_prefill_window(const kvattn_config* cfg, const kvattn_cache* cache, const void* q,
+                                    const int32_t* cu_q_lens, const int32_t* prefix_lens, const int32_t* block_table,
+                                    int32_t max_blocks_per_seq, int32_t num_chunks, int32_t max_q_len,
+                                    int32_t total_q, int32_t window, int32_t num_sinks, void* out, void* stream)
+{
+    PrefillArgs a;
+    bool todo;
+    const kvattn_status st = prefill_window_args(cfg, cache, q, cu_q_lens, prefix_lens, block_table,
+                                                 max_blocks_per_seq, num_chunks, max_q_len, total_q, window, num_sinks,
+                                                 out, a, &todo);
+    if (!todo) return st;
+    a.status = device_status_ptr();
+    if (!a.status) return KVATTN_ERR_CUDA;
+    return launch_prefill_window(a, static_cast<cudaStream_t>(stream));
+}
+
+size_t kvattn_prefill_window_fp8_workspace_size(const kvattn_config* cfg, int32_t block_size,
+                                                int32_t max_blocks_per_seq, int32_t num_chunks, int32_t max_q_len,
+                                                int32_t window, int32_t num_sinks)
+{
+    if (!config_ok(cfg) || config_supported(cfg) != KVATTN_OK) return 0;
+    if (cfg->dtype != KVATTN_BF16 || cfg->head_dim != 128) return 0;
+    return fp8_window_layout(cfg->num_kv_heads, block_size, max_blocks_per_seq, num_chunks, max_q_len, window,
+                             num_sinks).bytes;
+}
+
+kvattn_status kvattn_prefill_window_fp8(const kvattn_config* cfg, const kvattn_cache_fp8* cache, const void* q,
+                                        const int32_t* cu_q_lens, const int32_t* prefix_lens,
+                                        const int32_t* block_table, int32_t max_blocks_per_seq, int32_t num_chunks,
+                                        int32_t max_q_len, int32_t total_q, int32_t window, int32_t num_sinks,
+                                        void* out, void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (!cache) return KVATTN_ERR_INVALID_ARG;
+    const kvattn_cache c{cache->pool, cache->pool, cache->num_blocks, cache->block_size};
+    PrefillArgs a;
+    bool todo;
+    const kvattn_status st = prefill_window_args(cfg, &c, q, cu_q_lens, prefix_lens, block_table, max_blocks_per_seq,
+                                                 num_chunks, max_q_len, total_q, window, num_sinks, out, a, &todo);
+    if (st != KVATTN_OK) return st;
+    if (cfg->head_dim != 128) return KVATTN_ERR_UNSUPPORTED;
+    if (!todo) return st;
+    if (!workspace) return KVATTN_ERR_INVALID_ARG;
+    const Fp8WindowLayout L = fp8_window_layout(cfg->num_kv_heads, cache->block_size, max_blocks_per_seq, num_chunks,
+                                                max_q_len, window, num_sinks);
+    if (L.bytes == 0) return KVATTN_ERR_INVALID_ARG;
+    if (workspace_bytes < L.bytes) return KVATTN_ERR_WORKSPACE_TOO_SMALL;
+    a.status = device_status_ptr();
+    if (!a.status) return KVATTN_ERR_CUDA;
+    return launch_prefill_window_fp8(a, cache->pool, L, workspace, static_cast<cudaStream_t>(stream));
 }
 
 kvattn_status kvattn_selftest_wait_timeout(int32_t limit_us, void* stream)

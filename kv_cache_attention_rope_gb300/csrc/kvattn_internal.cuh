@@ -95,6 +95,37 @@ struct RopeArgs {
 kvattn_status launch_rope_append(const RopeArgs& a, cudaStream_t s);
 kvattn_status launch_rope_append_fp8(const RopeArgs& a, cudaStream_t s);  // a.fp8 set
 
+// V rows of an fp8 append into a.k_pool's pages (rope_append.cu; K and q are the caller's).
+kvattn_status launch_append_v_fp8(const RopeArgs& a, cudaStream_t s);
+
+struct RotaryArgs {
+    const void* q;
+    const void* k;
+    const void* v;
+    int64_t q_stride, k_stride, v_stride;  // bytes from one token's row to the next
+    void* q_out;                           // rotated q rows (== q: in place)
+    int64_t q_out_stride;                  // bytes
+    int32_t fp8;                           // k_pool is an fp8 page pool (v_pool unused, v not stored)
+    void* k_pool;
+    void* v_pool;
+    const int32_t* positions;
+    const int32_t* seq_ids;
+    const int32_t* block_table;
+    int64_t num_blocks;
+    int32_t block_size;
+    int32_t num_seqs;
+    int32_t max_blocks;
+    int32_t num_tokens;
+    int32_t hq, hkv, d;
+    int32_t dtype;
+    int32_t half;   // pairs of the halves (else adjacent pairs)
+    int32_t rot;    // rotated dims: a multiple of 16
+    float amplitude;
+    int* status;
+    uint64_t turns[64];  // speed of each pair, 2^-64 turns per position
+};
+kvattn_status launch_rotary_append(const RotaryArgs& a, cudaStream_t s);
+
 // fp8 cache page: the 16 tokens of one (block, KV head, 16-token group) at
 // D = 128, laid out for the decode kernel (one bulk copy per page, every
 // fragment load conflict-free):
@@ -143,8 +174,10 @@ struct DecodeArgs {
     int32_t dtype;
     float scale_log2;  // softmax scale * log2(e)
     int* status;
+    int32_t window, sinks;  // launch_decode_window only
 };
 kvattn_status launch_decode(const DecodeArgs& a, cudaStream_t s);
+kvattn_status launch_decode_window(const DecodeArgs& a, cudaStream_t s);
 
 // Largest decode batch (the kernels keep a per-sequence prefix sum in shared memory).
 constexpr int32_t kMaxDecodeBatch = 8192;
@@ -189,8 +222,11 @@ struct PrefillArgs {
     int32_t hq, hkv, d;
     float scale_log2;
     int* status;
+    int32_t window, sinks;  // launch_prefill_window only
 };
 kvattn_status launch_prefill(const PrefillArgs& a, cudaStream_t s);
+kvattn_status launch_prefill_window(const PrefillArgs& a, cudaStream_t s);
+constexpr int32_t kMaxWindowKeys = 1 << 30;  // keys of a sequence, window and sinks of a windowed prefill
 
 // Workspace of the fp8 prefill: the chunks' blocks expanded to bf16 (nb
 // blocks, K and V), their block table, owners and first blocks.  bytes == 0
@@ -205,6 +241,20 @@ Fp8PrefillLayout fp8_prefill_layout(int32_t hkv, int32_t block_size, int32_t max
 // over the bf16 copy (pa's pools and table are replaced).
 kvattn_status launch_prefill_fp8(const PrefillArgs& pa, const void* pool, const Fp8PrefillLayout& L,
                                  void* workspace, cudaStream_t s);
+
+// Workspace of the windowed fp8 prefill: each chunk's seen blocks (at most
+// `per_chunk`) expanded to bf16, and their block table.  bytes == 0 for invalid
+// arguments.
+struct Fp8WindowLayout {
+    int64_t per_chunk;
+    size_t off_table, off_k, off_v, bytes;
+};
+Fp8WindowLayout fp8_window_layout(int32_t hkv, int32_t block_size, int32_t max_blocks, int32_t num_chunks,
+                                  int32_t max_q_len, int32_t window, int32_t sinks);
+// Expands the pages that the chunks see into the workspace, then runs
+// launch_prefill_window over the bf16 copy (pa's pools and table are replaced).
+kvattn_status launch_prefill_window_fp8(const PrefillArgs& pa, const void* pool, const Fp8WindowLayout& L,
+                                        void* workspace, cudaStream_t s);
 
 // ---------------------------------------------------------------- device side
 

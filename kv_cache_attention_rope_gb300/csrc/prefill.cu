@@ -163,6 +163,12 @@ __device__ __forceinline__ bool elect_one()
     return pred != 0;
 }
 
+// Bits 0 .. n-1 (all for n >= 64, none for n <= 0).
+__device__ __forceinline__ uint64_t low_bits(int n)
+{
+    return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull;
+}
+
 // One work item: query rows [256 qt, 256 qt + 256) of chunk c, query head j,
 // as tiles A (first 128 rows) and B (next 128) against the same K/V stream.
 struct Item {
@@ -172,23 +178,57 @@ struct Item {
     int row0;         // first q row (token index)
     int pos0;         // absolute position of row 0
     int n_kv;         // 128-key tiles (0: nothing to do)
+    int pages, sink_pages, gap;  // windowed attention: see item_pages
 };
+
+// Windowed attention: row p sees keys j <= p with j > p - window or j < sinks.
+// The pages of an item are its sink_pages first ones and those from the page
+// of its first row's first window key on, `gap` pages apart.  Its tiles are cut
+// from that list, so a tile may hold pages of both parts, and key j of the
+// second part is column j - 16 gap of it.  In these columns the row at position
+// p sits at p' = p - 16 gap and sees the columns v <= p' with v > p' - window
+// or v < sinks: with gap > 0 every column of the first part is below the
+// first row's window, and every column of the second is a key past the sinks.
+__device__ __forceinline__ void item_pages(const PrefillArgs& a, int pos0, int rows, Item& it)
+{
+    const int all = (pos0 + rows - 1) / kPage + 1;
+    it.sink_pages = a.sinks > 0 ? min(all, (a.sinks - 1) / kPage + 1) : 0;
+    it.gap = max(0, max(0, pos0 - a.window + 1) / kPage - it.sink_pages);
+    it.pages = all - it.gap;
+    it.n_kv = (it.pages + kBN / kPage - 1) / (kBN / kPage);
+}
+
+// Most keys of a sequence: its table row's, and for the window's column
+// arithmetic in 32 bits (window and sinks are at most this too) 2^30.
+template <bool kWin>
+__device__ __forceinline__ int64_t key_limit(const PrefillArgs& a)
+{
+    const int64_t n = (int64_t)a.max_blocks * a.block_size;
+    return kWin ? min(n, (int64_t)kMaxWindowKeys) : n;
+}
 
 // Tiles of the (chunk, 256-row block) pair: the key range row 255 (or the
 // last row) sees; 0 when the block is past the chunk's end or the chunk's
 // metadata is out of range (recorded by make_item).
+template <bool kWin>
 __device__ __forceinline__ int pair_tiles(const PrefillArgs& a, int n_qt, int pair)
 {
     const int c = pair / n_qt, qt = pair % n_qt;
     const int q0 = a.cu_q_lens[c], qlen = a.cu_q_lens[c + 1] - q0, P = a.prefix_lens[c];
     if (qt * 2 * kBM >= qlen) return 0;
     if (qlen < 0 || P < 0 || qlen > a.max_q_len || q0 < 0 || q0 + qlen > a.total_q ||
-        (int64_t)(P + qlen) > (int64_t)a.max_blocks * a.block_size)
+        (int64_t)P + qlen > key_limit<kWin>(a))
         return 0;
     const int rows = min(2 * kBM, qlen - qt * 2 * kBM);
+    if constexpr (kWin) {
+        Item it;
+        item_pages(a, P + qt * 2 * kBM, rows, it);
+        return it.n_kv;
+    }
     return (P + qt * 2 * kBM + rows - 1) / kBN + 1;
 }
 
+template <bool kWin>
 __device__ __forceinline__ Item make_item(const PrefillArgs& a, int n_qt, int pair, int j, bool report)
 {
     Item it;
@@ -202,14 +242,15 @@ __device__ __forceinline__ Item make_item(const PrefillArgs& a, int n_qt, int pa
     it.rows = it.row0 = it.pos0 = 0;
     if (qt * 2 * kBM >= qlen) return it;  // nothing to do
     if (qlen < 0 || P < 0 || qlen > a.max_q_len || q0 < 0 || q0 + qlen > a.total_q ||
-        (int64_t)it.seq_len > (int64_t)a.max_blocks * a.block_size) {
+        (int64_t)P + qlen > key_limit<kWin>(a)) {
         if (report) record_error(a.status, KVATTN_ERR_BAD_INDEX);
         return it;
     }
     it.rows = min(2 * kBM, qlen - qt * 2 * kBM);
     it.row0 = q0 + qt * 2 * kBM;
     it.pos0 = P + qt * 2 * kBM;
-    it.n_kv = (it.pos0 + it.rows - 1) / kBN + 1;
+    if constexpr (kWin) item_pages(a, it.pos0, it.rows, it);
+    else it.n_kv = (it.pos0 + it.rows - 1) / kBN + 1;
     return it;
 }
 
@@ -222,7 +263,7 @@ __device__ __forceinline__ Item make_item(const PrefillArgs& a, int n_qt, int pa
 // ones without a global counter.  Pipeline state (stages, phases) runs on
 // across items, so the next item's Q, K, V and first S overlap the current
 // item's last tiles and epilogue.
-template <int kHD>
+template <int kHD, bool kWin>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ Maps maps, const int n_qt)
 {
@@ -256,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n_pairs = a.num_chunks * n_qt;
     const bool sorted = n_pairs <= kMaxPairs;
     if (sorted) {
-        for (int i = threadIdx.x; i < n_pairs; i += kThreads) plen[i] = pair_tiles(a, n_qt, i);
+        for (int i = threadIdx.x; i < n_pairs; i += kThreads) plen[i] = pair_tiles<kWin>(a, n_qt, i);
     }
     if (threadIdx.x == 0) {
         mbar_init(B.q_full, 1);
@@ -304,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto item_at = [&](int i, bool report) -> Item {
         const int pr = i / a.hq;
-        return make_item(a, n_qt, sorted ? order[pr] : pr, i % a.hq, report);
+        return make_item<kWin>(a, n_qt, sorted ? order[pr] : pr, i % a.hq, report);
     };
 
     if (warp == 0) {
@@ -340,9 +381,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++ii;
             const int32_t* trow = a.block_table + (int64_t)it.c * a.max_blocks;
             // lane p < 8 loads the block id of page p of tile t (keys 128t + 16p ..)
+            auto page_key = [&](int t) -> int {
+                const int p = t * (kBN / kPage) + lane;
+                return (kWin && p >= it.sink_pages ? p + it.gap : p) * kPage;
+            };
+            auto has_page = [&](int t) -> bool {
+                if constexpr (kWin) return lane < kBN / kPage && t * (kBN / kPage) + lane < it.pages;
+                return lane < kBN / kPage && t * kBN + lane * kPage < it.seq_len;
+            };
             auto fetch = [&](int t) -> int32_t {
-                const int key0 = t * kBN + lane * kPage;
-                return (lane < kBN / kPage && t < it.n_kv && key0 < it.seq_len) ? trow[key0 / a.block_size] : -1;
+                return (t < it.n_kv && has_page(t)) ? trow[page_key(t) / a.block_size] : -1;
             };
             int32_t blk_next = fetch(0);
             for (int t = 0; t < it.n_kv; ++t, ++g) {
@@ -350,8 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 blk_next = fetch(t + 1);  // in flight while this tile is issued
                 int y = 0;
                 bool have = false;
-                const int key0 = t * kBN + lane * kPage;
-                if (lane < kBN / kPage && key0 < it.seq_len) {
+                const int key0 = page_key(t);
+                if (has_page(t)) {
                     if (blk < 0 || blk >= a.num_blocks) {
                         record_error(a.status, KVATTN_ERR_BAD_INDEX);
                     } else {
@@ -527,12 +575,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int x = 0; x < 2; ++x) {
                     const uint32_t tS = tmem + lane_base + x * 128 + hf * 64;
                     const uint32_t tO = tmem + lane_base + 256 + x * 128 + hf * (kHD / 2);
-                    const int pos_r = it.pos0 + x * kBM + r;  // absolute position of this row
-                    const int pos_first = it.pos0 + x * kBM;  // ... of the tile's first row
+                    const int col0 = kWin ? it.gap * kPage : 0;      // see item_pages
+                    const int pos_r = it.pos0 + x * kBM + r - col0;  // absolute position of this row (kWin: its column)
+                    const int pos_first = it.pos0 + x * kBM - col0;  // ... of the tile's first row
                     // keys past the end of the sequence: V rows must be zero (stale
                     // cache slots may hold anything, and 0 * NaN is NaN).  Done in
                     // tile A's phase; PV_B(t) is issued after PV_A(t).
-                    const bool zero_v = x == 0 && (t + 1) * kBN > it.seq_len;
+                    // A window's other rows that no row of the item sees (past its
+                    // last row, or before its first row's window and past the
+                    // sinks) likewise.
+                    const int v_end = kWin ? it.pos0 + it.rows - col0 : it.seq_len;  // columns from here on
+                    const int v_low = kWin ? it.pos0 - a.window - col0 : -1;        // columns sinks .. v_low
+                    const bool zero_v = x == 0 && ((t + 1) * kBN > v_end ||
+                                                   (kWin && t * kBN <= v_low && (t + 1) * kBN > a.sinks));
                     bool good = warp_wait(&B.s_full[x], g & 1, abort_flag, a.status);
                     if (good && zero_v)
                         good = warp_wait(&B.v_full[g % kVStages], (g / kVStages) & 1, abort_flag, a.status);
@@ -545,7 +600,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_ld_wait();
                         // causal mask: keys past this row's position (only tiles
                         // that reach beyond the tile's first row can have any)
-                        if (t * kBN + kBN - 1 > pos_first) {
+                        if constexpr (kWin) {
+                            const int c = t * kBN + hf * 64;  // this half's first column
+                            const int last = pos_first + kBM - 1;
+                            if (c + 63 > pos_first || (c <= last - a.window && c + 63 >= a.sinks)) {
+                                // bit e: column c + e is seen
+                                uint64_t m = low_bits(pos_r - c + 1) & (~low_bits(pos_r - a.window - c + 1) | low_bits(a.sinks - c));
+#pragma unroll
+                                for (int e = 0; e < 64; ++e)
+                                    if (!((e < 32 ? (uint32_t)m : (uint32_t)(m >> 32)) & (1u << (e & 31))))
+                                        sv[e] = __float_as_uint(-INFINITY);
+                            }
+                        } else if (t * kBN + kBN - 1 > pos_first) {
                             const int lim = pos_r - t * kBN - hf * 64;  // last visible column of this half
 #pragma unroll
                             for (int e = 0; e < 64; ++e)
@@ -614,7 +680,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     if (zero_v) {
-                        if (t * kBN + r >= it.seq_len) {
+                        const int v = t * kBN + r;
+                        if (v >= v_end || (kWin && v <= v_low && v >= a.sinks)) {
                             // key r's row of the V stage: this half zeroes its kHD bytes
                             unsigned char* vrow = smem + kOffV + (g % kVStages) * kTileBytes + (r >> 3) * kGroup +
                                                   (r & 7) * 128 + hf * (kHD == 128 ? 1024 : 64);
@@ -840,7 +907,7 @@ bool pool_maps(const void* k_pool, const void* v_pool, int64_t rows, bool row_bo
 
 namespace {
 
-template <int kHD>
+template <int kHD, bool kWin>
 kvattn_status launch_prefill_d(const PrefillArgs& a, cudaStream_t s)
 {
     if ((int64_t)a.num_blocks * a.hkv * a.block_size >= ((int64_t)1 << 31)) return KVATTN_ERR_UNSUPPORTED;
@@ -848,13 +915,13 @@ kvattn_status launch_prefill_d(const PrefillArgs& a, cudaStream_t s)
     if (!make_maps<kHD>(a, maps)) return KVATTN_ERR_CUDA;
     constexpr int kSmem = Geo<kHD>::kSmemBytes;
     static SmemLimit limit;
-    if (limit.ensure(reinterpret_cast<const void*>(prefill_kernel<kHD>), kSmem) != cudaSuccess) return KVATTN_ERR_CUDA;
+    if (limit.ensure(reinterpret_cast<const void*>(prefill_kernel<kHD, kWin>), kSmem) != cudaSuccess) return KVATTN_ERR_CUDA;
     const int n_qt = (a.max_q_len + 2 * kBM - 1) / (2 * kBM);
     const int64_t items = (int64_t)a.num_chunks * n_qt * a.hq;
     if (items <= 0) return KVATTN_OK;
     if (items > 0x7fffffff) return KVATTN_ERR_UNSUPPORTED;
     const int64_t grid = std::min<int64_t>(items, num_sms());  // persistent: one CTA per SM
-    return cuda_status(launch_pdl(prefill_kernel<kHD>, dim3((unsigned)grid), dim3(kThreads), kSmem, s, a, maps, n_qt));
+    return cuda_status(launch_pdl(prefill_kernel<kHD, kWin>, dim3((unsigned)grid), dim3(kThreads), kSmem, s, a, maps, n_qt));
 }
 
 }  // namespace
@@ -862,8 +929,16 @@ kvattn_status launch_prefill_d(const PrefillArgs& a, cudaStream_t s)
 kvattn_status launch_prefill(const PrefillArgs& a, cudaStream_t s)
 {
     if (a.hq % a.hkv) return KVATTN_ERR_UNSUPPORTED;
-    if (a.d == 128) return launch_prefill_d<128>(a, s);
-    if (a.d == 64) return launch_prefill_d<64>(a, s);
+    if (a.d == 128) return launch_prefill_d<128, false>(a, s);
+    if (a.d == 64) return launch_prefill_d<64, false>(a, s);
+    return KVATTN_ERR_UNSUPPORTED;
+}
+
+kvattn_status launch_prefill_window(const PrefillArgs& a, cudaStream_t s)
+{
+    if (a.hq % a.hkv) return KVATTN_ERR_UNSUPPORTED;
+    if (a.d == 128) return launch_prefill_d<128, true>(a, s);
+    if (a.d == 64) return launch_prefill_d<64, true>(a, s);
     return KVATTN_ERR_UNSUPPORTED;
 }
 

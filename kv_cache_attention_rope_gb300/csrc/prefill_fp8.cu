@@ -54,6 +54,7 @@ struct Fp8PrefillArgs {
     __nv_bfloat16* k_copy;     // [nb][hkv][block_size][128]
     __nv_bfloat16* v_copy;
     int* status;
+    int32_t window, sinks, per_chunk;  // windowed form: copy block c * per_chunk + i is chunk c's i-th seen block
 };
 
 // Blocks chunk c's keys occupy; 0 for a chunk the prefill kernel rejects or
@@ -140,6 +141,25 @@ __device__ __forceinline__ void expand4(uint32_t w, float s, uint32_t& o0, uint3
 
 constexpr int kExpandWarps = 8;
 
+// Windowed form: the logical block of chunk c's i-th seen block and the range
+// of its keys that no row sees, or false when the chunk sees fewer blocks.  The
+// rows at prefix .. prefix + qlen - 1 see the keys from low = prefix - window
+// + 1 on and the first `sinks`.
+__device__ __forceinline__ bool seen_block(const Fp8PrefillArgs& a, int c, int i, int& j, int& low, int& total)
+{
+    const int all = chunk_blocks(a, c);
+    const int P = a.prefix_lens[c];
+    total = P + a.cu_q_lens[c + 1] - a.cu_q_lens[c];
+    if (all == 0 || total > kMaxWindowKeys) return false;
+    low = max(0, P - a.window + 1);
+    const int lead = a.sinks > 0 ? min(all, (a.sinks - 1) / a.block_size + 1) : 0;
+    j = i < lead ? i : i + max(0, low / a.block_size - lead);
+    return j < all;
+}
+
+// kWin: the copy's block table is written here, by the lane that has a block's
+// first page, and pages without a seen key are not converted.
+template <bool kWin>
 __global__ void __launch_bounds__(kExpandWarps * 32) prefill_fp8_expand(const Fp8PrefillArgs a)
 {
     pdl_wait();
@@ -147,7 +167,7 @@ __global__ void __launch_bounds__(kExpandWarps * 32) prefill_fp8_expand(const Fp
     const int lane = threadIdx.x & 31;
     unsigned char* pbuf = bufs + (threadIdx.x >> 5) * 2 * kF8Page;
     const int ppb = a.block_size / 16;  // pages per block and head
-    const int64_t used = min(a.first[a.num_chunks], a.nb);
+    const int64_t used = kWin ? a.nb : min(a.first[a.num_chunks], a.nb);
     const int64_t pages = used * a.hkv * ppb;
     const int64_t nwarps = (int64_t)gridDim.x * kExpandWarps;
     const int64_t wid = (int64_t)blockIdx.x * kExpandWarps + (threadIdx.x >> 5);
@@ -160,10 +180,24 @@ __global__ void __launch_bounds__(kExpandWarps * 32) prefill_fp8_expand(const Fp
         if (g < end) {
             const int64_t b = g / (a.hkv * ppb);
             const int rem = (int)(g - b * a.hkv * ppb), h = rem / ppb, p = rem - h * ppb;
-            const int c = a.owner[b];
-            const int j = (int)(b - a.first[c]);
-            const int total = a.prefix_lens[c] + a.cu_q_lens[c + 1] - a.cu_q_lens[c];
-            if (j * a.block_size + p * 16 < total) {
+            int c, j, total;
+            bool wanted;
+            if constexpr (kWin) {
+                c = (int)(b / a.per_chunk);
+                int low;
+                wanted = seen_block(a, c, (int)(b - (int64_t)c * a.per_chunk), j, low, total);
+                if (wanted && rem == 0) a.ctable[(int64_t)c * a.max_blocks + j] = (int32_t)b;
+                if (wanted) {
+                    const int key0 = j * a.block_size + p * 16;
+                    wanted = key0 < total && (key0 < a.sinks || key0 + 15 >= low);
+                }
+            } else {
+                c = a.owner[b];
+                j = (int)(b - a.first[c]);
+                total = a.prefix_lens[c] + a.cu_q_lens[c + 1] - a.cu_q_lens[c];
+                wanted = j * a.block_size + p * 16 < total;
+            }
+            if (wanted) {
                 const int32_t blk = a.block_table[(int64_t)c * a.max_blocks + j];
                 if (blk < 0 || blk >= a.num_blocks)
                     record_error(a.status, KVATTN_ERR_BAD_INDEX);
@@ -247,6 +281,40 @@ __global__ void __launch_bounds__(kExpandWarps * 32) prefill_fp8_expand(const Fp
     }
 }
 
+constexpr int kExpandSmem = kExpandWarps * 2 * kF8Page;
+
+// One wave of resident CTAs (each warp walks a contiguous range of pages).
+template <bool kWin>
+cudaError_t expand_grid(int* grid)
+{
+    static SmemLimit limit;
+    cudaError_t e = limit.ensure(reinterpret_cast<const void*>(prefill_fp8_expand<kWin>), kExpandSmem);
+    if (e != cudaSuccess) return e;
+    int per_sm = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, prefill_fp8_expand<kWin>, kExpandWarps * 32, kExpandSmem);
+    *grid = num_sms() * std::max(1, per_sm);
+    return e;
+}
+
+Fp8PrefillArgs common_args(const PrefillArgs& pa, const void* pool)
+{
+    Fp8PrefillArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.pool = static_cast<const unsigned char*>(pool);
+    a.num_blocks = pa.num_blocks;
+    a.block_table = pa.block_table;
+    a.cu_q_lens = pa.cu_q_lens;
+    a.prefix_lens = pa.prefix_lens;
+    a.num_chunks = pa.num_chunks;
+    a.max_blocks = pa.max_blocks;
+    a.max_q_len = pa.max_q_len;
+    a.total_q = pa.total_q;
+    a.block_size = pa.block_size;
+    a.hkv = pa.hkv;
+    a.status = pa.status;
+    return a;
+}
+
 constexpr size_t kAlign = 1024;
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
@@ -287,36 +355,19 @@ kvattn_status launch_prefill_fp8(const PrefillArgs& pa, const void* pool, const 
     if ((int64_t)pa.num_chunks * ((pa.max_q_len + 255) / 256) * pa.hq > 0x7fffffff) return KVATTN_ERR_UNSUPPORTED;
     unsigned char* ws = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(workspace) + kAlign - 1) / kAlign * kAlign);
-    Fp8PrefillArgs a;
-    std::memset(&a, 0, sizeof(a));
-    a.pool = static_cast<const unsigned char*>(pool);
-    a.num_blocks = pa.num_blocks;
-    a.block_table = pa.block_table;
-    a.cu_q_lens = pa.cu_q_lens;
-    a.prefix_lens = pa.prefix_lens;
-    a.num_chunks = pa.num_chunks;
-    a.max_blocks = pa.max_blocks;
-    a.max_q_len = pa.max_q_len;
-    a.total_q = pa.total_q;
-    a.block_size = pa.block_size;
-    a.hkv = pa.hkv;
+    Fp8PrefillArgs a = common_args(pa, pool);
     a.nb = L.nb;
     a.first = reinterpret_cast<int64_t*>(ws + L.off_first);
     a.owner = reinterpret_cast<int32_t*>(ws + L.off_owner);
     a.ctable = reinterpret_cast<int32_t*>(ws + L.off_table);
     a.k_copy = reinterpret_cast<__nv_bfloat16*>(ws + L.off_k);
     a.v_copy = reinterpret_cast<__nv_bfloat16*>(ws + L.off_v);
-    a.status = pa.status;
-    constexpr int kExpandSmem = kExpandWarps * 2 * kF8Page;
-    static SmemLimit limit;
-    cudaError_t e = limit.ensure(reinterpret_cast<const void*>(prefill_fp8_expand), kExpandSmem);
-    if (e != cudaSuccess) return cuda_status(e);
-    int per_sm = 0;  // one wave of resident CTAs (each warp walks a contiguous range of pages)
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, prefill_fp8_expand, kExpandWarps * 32, kExpandSmem);
+    int grid = 0;
+    cudaError_t e = expand_grid<false>(&grid);
     if (e != cudaSuccess) return cuda_status(e);
     e = launch_pdl(prefill_fp8_plan, dim3(1), dim3(1024), 0, s, a);
     if (e != cudaSuccess) return cuda_status(e);
-    e = launch_pdl(prefill_fp8_expand, dim3(num_sms() * std::max(1, per_sm)), dim3(kExpandWarps * 32), kExpandSmem, s, a);
+    e = launch_pdl(prefill_fp8_expand<false>, dim3(grid), dim3(kExpandWarps * 32), kExpandSmem, s, a);
     if (e != cudaSuccess) return cuda_status(e);
     PrefillArgs b = pa;
     b.k_pool = a.k_copy;
@@ -324,6 +375,61 @@ kvattn_status launch_prefill_fp8(const PrefillArgs& pa, const void* pool, const 
     b.block_table = a.ctable;
     b.num_blocks = L.nb;
     return launch_prefill(b, s);
+}
+
+Fp8WindowLayout fp8_window_layout(int32_t hkv, int32_t block_size, int32_t max_blocks, int32_t num_chunks,
+                                  int32_t max_q_len, int32_t window, int32_t sinks)
+{
+    Fp8WindowLayout L;
+    std::memset(&L, 0, sizeof(L));
+    if (hkv <= 0 || block_size <= 0 || block_size % 16 || max_blocks <= 0 || num_chunks < 0 || max_q_len < 0 ||
+        window < 1 || sinks < 0)
+        return L;
+    // the sinks' blocks, and those that a run of window - 1 + max_q_len keys can touch
+    const int64_t run = (int64_t)window - 1 + max_q_len;
+    const int64_t seen = ((int64_t)sinks + block_size - 1) / block_size + (run + block_size - 2) / block_size + 1;
+    L.per_chunk = std::min<int64_t>(max_blocks, seen);
+    size_t off = 0;
+    L.off_table = off;
+    off = align_up(off + (size_t)num_chunks * (size_t)max_blocks * 4);
+    const size_t copy = (size_t)num_chunks * (size_t)L.per_chunk * hkv * block_size * kF8D * 2;
+    L.off_k = off;
+    off = align_up(off + copy);
+    L.off_v = off;
+    off = align_up(off + copy);
+    L.bytes = off + kAlign;  // slack: the base is aligned up to 1 KB
+    return L;
+}
+
+kvattn_status launch_prefill_window_fp8(const PrefillArgs& pa, const void* pool, const Fp8WindowLayout& L,
+                                        void* workspace, cudaStream_t s)
+{
+    if (pa.num_chunks == 0 || pa.total_q == 0 || pa.max_q_len == 0) return KVATTN_OK;
+    // launch_prefill_window's own refusals, checked before anything is launched
+    const int64_t nb = L.per_chunk * pa.num_chunks;
+    if (nb > INT32_MAX / pa.hkv / pa.block_size) return KVATTN_ERR_UNSUPPORTED;
+    if ((int64_t)pa.num_chunks * ((pa.max_q_len + 255) / 256) * pa.hq > 0x7fffffff) return KVATTN_ERR_UNSUPPORTED;
+    unsigned char* ws = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(workspace) + kAlign - 1) / kAlign * kAlign);
+    Fp8PrefillArgs a = common_args(pa, pool);
+    a.window = pa.window;
+    a.sinks = pa.sinks;
+    a.per_chunk = (int32_t)L.per_chunk;
+    a.nb = nb;
+    a.ctable = reinterpret_cast<int32_t*>(ws + L.off_table);
+    a.k_copy = reinterpret_cast<__nv_bfloat16*>(ws + L.off_k);
+    a.v_copy = reinterpret_cast<__nv_bfloat16*>(ws + L.off_v);
+    int grid = 0;
+    cudaError_t e = expand_grid<true>(&grid);
+    if (e == cudaSuccess)
+        e = launch_pdl(prefill_fp8_expand<true>, dim3(grid), dim3(kExpandWarps * 32), kExpandSmem, s, a);
+    if (e != cudaSuccess) return cuda_status(e);
+    PrefillArgs b = pa;
+    b.k_pool = a.k_copy;
+    b.v_pool = a.v_copy;
+    b.block_table = a.ctable;
+    b.num_blocks = nb;
+    return launch_prefill_window(b, s);
 }
 
 }  // namespace kvattn

@@ -877,6 +877,12 @@ kvattn_status launch_rope_append(const RopeArgs& a, cudaStream_t s)
     return KVATTN_ERR_UNSUPPORTED;
 }
 
+kvattn_status launch_append_v_fp8(const RopeArgs& a, cudaStream_t s)
+{
+    return cuda_status(launch_pdl(append_v_fp8_kernel, dim3((unsigned)((a.num_tokens + kVWin - 1) / kVWin), (unsigned)a.hkv),
+                                  dim3(32), 0, s, a));
+}
+
 kvattn_status launch_rope_append_fp8(const RopeArgs& a, cudaStream_t s)
 {
     // the ring kernel only: a token whose bf16 q, k, v do not fit two stages is refused
@@ -885,8 +891,7 @@ kvattn_status launch_rope_append_fp8(const RopeArgs& a, cudaStream_t s)
     if (a.dtype == KVATTN_BF16 && a.d == 128) launched = launch_pipe<true, 128, true>(a, s, err);
     if (!launched) return KVATTN_ERR_UNSUPPORTED;
     if (err != cudaSuccess) return KVATTN_ERR_CUDA;
-    return cuda_status(launch_pdl(append_v_fp8_kernel, dim3((unsigned)((a.num_tokens + kVWin - 1) / kVWin), (unsigned)a.hkv),
-                                  dim3(32), 0, s, a));
+    return launch_append_v_fp8(a, s);
 }
 
 }  // namespace kvattn
