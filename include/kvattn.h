@@ -430,6 +430,8 @@ kvattn_status kvattn_decode_static_scratch(const kvattn_config* cfg, const kvatt
  * blocks that are read, hold has no effect (NaN and infinities too).
  *   window      >= 1; INT32_MAX sees the whole cache
  *   num_sinks   >= 0
+ *   num_splits  0: the library's choice, one launch when the keys are few;
+ *               otherwise as kvattn_decode's
  *   workspace   >= kvattn_decode_window_workspace_size(...) bytes, as
  *               kvattn_decode's; calls that may overlap on the GPU (two
  *               streams, two captured graphs) need one each

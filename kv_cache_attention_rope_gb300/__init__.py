@@ -490,41 +490,97 @@ def make_rotary(layout: str = "adjacent", rotary_dim: int = 0, scaling: str = "n
     return Rotary(ROPE_LAYOUT[layout], rotary_dim, ROPE_SCALING[scaling], factor, original_len, low, high, amplitude)
 
 
-def _same_device(*tensors) -> None:
-    """Every tensor on the current CUDA device: kernels are launched there."""
-    current = _torch().cuda.current_device()
-    for t in tensors:
-        if t.is_cuda and t.get_device() != current:
-            raise ValueError(f"tensor on {t.device}, but cuda:{current} is the current device")
+# These calls may be a few microseconds of GPU work each, so their marshalling is kept short: one pass over each
+# tensor (type, device, contiguity), pointers as plain integers, the stream's handle without a Stream object.
+
+def _here(stream):
+    """Current CUDA device and the raw handle of the stream to use on it."""
+    torch = _torch()
+    device = torch.cuda.current_device()
+    if stream is None:
+        return device, torch._C._cuda_getCurrentRawStream(device)
+    if stream.device.index != device:
+        raise ValueError(f"stream of {stream.device}, but cuda:{device} is the current device")
+    return device, stream.cuda_stream
+
+
+def _refuse(t, name: str, dtype, device: int):
+    """Raises what is wrong with a tensor that _ptr or _token_rows would not take."""
+    _dev(t, name, dtype)
+    raise ValueError(f"{name} lives on {t.device}, but cuda:{device} is the current device")
+
+
+def _ptr(t, name: str, dtype, device: int) -> int:
+    if t.dtype is dtype and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, dtype, device)
+
+
+def _token_rows(t, name: str, heads: int, head_dim: int, dtype, device: int):
+    """_rows, and the device: pointer and row stride of a [T, heads, D] or [T, heads*D] view."""
+    if t.dtype is dtype and t.get_device() == device and t.dim() == 3:
+        T, h, d = t.shape
+        s, sh, sd = t.stride()
+        if h == heads and d == head_dim and sd == 1 and (sh == d or h == 1):
+            return t.data_ptr(), s if T > 1 else h * d
+    p, s = _rows(t, name, heads, head_dim, dtype)
+    if t.get_device() != device:
+        _refuse(t.reshape(-1), name, dtype, device)
+    return p.value, s
 
 
 def _shape(t, name: str, *shape) -> None:
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
-def _check_cache(cfg: Config, cache, kind) -> None:
+def _check_cache(cfg: Config, cache, kind, device: int):
+    """The cache's descriptor, once it fits the config; returns it and the element type of the queries."""
     if type(cache) is not kind:
         raise TypeError(f"cache must be a {kind.__name__}")
     if cache.num_kv_heads != cfg.num_kv_heads or cache.head_dim != cfg.head_dim:
         raise ValueError("cache heads / head_dim do not match the config")
-    if kind is Cache and dtype_code(cache.k_pool) != cfg.dtype:
-        raise TypeError("cache element type does not match the config")
-
-
-def _dtype(cfg: Config):
     torch = _torch()
-    return torch.bfloat16 if cfg.dtype == BF16 else torch.float32
+    dt = torch.bfloat16 if cfg.dtype == BF16 else torch.float32
+    pool = cache.pool if kind is CacheFP8 else cache.k_pool
+    if kind is Cache and pool.dtype is not dt:
+        raise TypeError("cache element type does not match the config")
+    if pool.get_device() != device:
+        raise ValueError(f"cache lives on {pool.device}, but cuda:{device} is the current device")
+    return ctypes.byref(cache.desc), dt
+
+
+def _table(block_table, rows: int, device: int):
+    if block_table.dim() != 2 or block_table.shape[0] < rows:
+        raise ValueError(f"block_table must have a row for each of the {rows} sequences")
+    return _ptr(block_table, "block_table", _torch().int32, device), block_table.shape[1]
+
+
+def _out(out, q, dtype, device: int):
+    if out is None:
+        out = _torch().empty_like(q)
+    elif out.shape != q.shape:
+        raise ValueError(f"out must be {list(q.shape)}, got {list(out.shape)}")
+    return out, _ptr(out, "out", dtype, device)
+
+
+def _scratch(workspace, size, q, device: int):
+    """Pointer and bytes of the workspace; `size` (a function) says how much to allocate when there is none."""
+    torch = _torch()
+    if workspace is None:
+        workspace = torch.empty(max(size(), 256), dtype=torch.uint8, device=q.device)
+    return _ptr(workspace, "workspace", workspace.dtype, device), workspace.nbytes
 
 
 def _rotary_append(fn, what, kind, cfg, rotary, cache, q, k, v, positions, seq_ids, block_table, stream, q_out):
-    torch = _torch()
-    _check_cache(cfg, cache, kind)
-    T, dt = q.shape[0], _dtype(cfg)
+    device, s = _here(stream)
+    desc, dt = _check_cache(cfg, cache, kind, device)
+    int32 = _torch().int32
     hq, hkv, d = cfg.num_q_heads, cfg.num_kv_heads, cfg.head_dim
-    qp, qs = _rows(q, "q", hq, d, dt)
-    kp, ks = _rows(k, "k", hkv, d, dt)
-    vp, vs = _rows(v, "v", hkv, d, dt)
+    T = q.shape[0]
+    qp, qs = _token_rows(q, "q", hq, d, dt, device)
+    kp, ks = _token_rows(k, "k", hkv, d, dt, device)
+    vp, vs = _token_rows(v, "v", hkv, d, dt, device)
     if k.shape[0] != T or v.shape[0] != T:
         raise ValueError("q, k and v differ in tokens")
     _shape(positions, "positions", T)
@@ -532,12 +588,11 @@ def _rotary_append(fn, what, kind, cfg, rotary, cache, q, k, v, positions, seq_i
     qo = None
     if q_out is not None:
         _shape(q_out, "q_out", T, hq, d)
-        qo = _dev(q_out, "q_out", dt)
-    _same_device(q, k, v, positions, block_table)
-    check(fn(ctypes.byref(cfg), ctypes.byref(rotary), ctypes.byref(cache.desc), qp, qs, kp, ks, vp, vs, qo,
-             _dev(positions, "positions", torch.int32), _dev(seq_ids, "seq_ids", torch.int32),
-             _dev(block_table, "block_table", torch.int32), block_table.shape[0], block_table.shape[1], T,
-             _stream(stream)), what)
+        qo = _ptr(q_out, "q_out", dt, device)
+    table, width = _table(block_table, 0, device)
+    check(fn(ctypes.byref(cfg), ctypes.byref(rotary), desc, qp, qs, kp, ks, vp, vs, qo,
+             _ptr(positions, "positions", int32, device), _ptr(seq_ids, "seq_ids", int32, device), table,
+             block_table.shape[0], width, T, s), what)
 
 
 def rotary_append(cfg: Config, rotary: Rotary, cache: Cache, q, k, v, positions, seq_ids, block_table, stream=None,
@@ -564,26 +619,18 @@ def decode_window_workspace_size(cfg: Config, batch: int, max_seq_len: int, wind
 
 def _decode_window(fn, what, kind, cfg, cache, q, block_table, seq_lens, max_seq_len, window, num_sinks, out,
                    workspace, num_splits, stream):
-    torch = _torch()
-    _check_cache(cfg, cache, kind)
-    B, dt = q.shape[0], _dtype(cfg)
+    device, s = _here(stream)
+    desc, dt = _check_cache(cfg, cache, kind, device)
+    B = q.shape[0]
     _shape(q, "q", B, cfg.num_q_heads, cfg.head_dim)
     _shape(seq_lens, "seq_lens", B)
-    if block_table.dim() != 2 or block_table.shape[0] < B:
-        raise ValueError(f"block_table must have a row for each of the {B} sequences")
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        _shape(out, "out", *q.shape)
-    if workspace is None:
-        n = decode_window_workspace_size(cfg, B, max_seq_len, window, num_sinks, num_splits)
-        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
-    _same_device(q, block_table, seq_lens, out, workspace)
-    check(fn(ctypes.byref(cfg), ctypes.byref(cache.desc), _dev(q, "q", dt),
-             _dev(block_table, "block_table", torch.int32), block_table.shape[1],
-             _dev(seq_lens, "seq_lens", torch.int32), B, max_seq_len, window, num_sinks, num_splits,
-             _dev(out, "out", dt), _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-             _stream(stream)), what)
+    table, width = _table(block_table, B, device)
+    out, op = _out(out, q, dt, device)
+    wp, nbytes = _scratch(workspace, lambda: decode_window_workspace_size(cfg, B, max_seq_len, window, num_sinks,
+                                                                          num_splits), q, device)
+    check(fn(ctypes.byref(cfg), desc, _ptr(q, "q", dt, device), table, width,
+             _ptr(seq_lens, "seq_lens", _torch().int32, device), B, max_seq_len, window, num_sinks, num_splits, op, wp,
+             nbytes, s), what)
     return out
 
 
@@ -602,31 +649,27 @@ def decode_window_fp8(cfg: Config, cache: CacheFP8, q, block_table, seq_lens, ma
                           block_table, seq_lens, max_seq_len, window, num_sinks, out, workspace, num_splits, stream)
 
 
-def _prefill_window_args(kind, cfg, cache, q, cu_q_lens, prefix_lens, block_table, out):
+def _prefill_window_args(kind, cfg, cache, q, cu_q_lens, prefix_lens, block_table, device):
     torch = _torch()
-    _check_cache(cfg, cache, kind)
+    desc, _ = _check_cache(cfg, cache, kind, device)
     n = prefix_lens.shape[0]
     _shape(q, "q", q.shape[0], cfg.num_q_heads, cfg.head_dim)
+    _shape(prefix_lens, "prefix_lens", n)
     _shape(cu_q_lens, "cu_q_lens", n + 1)
-    if block_table.dim() != 2 or block_table.shape[0] < n:
-        raise ValueError(f"block_table must have a row for each of the {n} chunks")
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        _shape(out, "out", *q.shape)
-    _same_device(q, cu_q_lens, prefix_lens, block_table, out)
-    return out, n, (_dev(q, "q", torch.bfloat16), _dev(cu_q_lens, "cu_q_lens", torch.int32),
-                    _dev(prefix_lens, "prefix_lens", torch.int32), _dev(block_table, "block_table", torch.int32),
-                    block_table.shape[1], n)
+    table, width = _table(block_table, n, device)
+    return n, (ctypes.byref(cfg), desc, _ptr(q, "q", torch.bfloat16, device),
+               _ptr(cu_q_lens, "cu_q_lens", torch.int32, device), _ptr(prefix_lens, "prefix_lens", torch.int32, device),
+               table, width, n)
 
 
 def prefill_window(cfg: Config, cache: Cache, q, cu_q_lens, prefix_lens, block_table, max_q_len: int, window: int,
                    num_sinks: int = 0, out=None, stream=None):
     """kvattn_prefill_window: causal attention of query chunks, each row over its last `window` keys and the first
     num_sinks."""
-    out, _, args = _prefill_window_args(Cache, cfg, cache, q, cu_q_lens, prefix_lens, block_table, out)
-    check(lib.kvattn_prefill_window(ctypes.byref(cfg), ctypes.byref(cache.desc), *args, max_q_len, q.shape[0], window,
-                                    num_sinks, _dev(out, "out", q.dtype), _stream(stream)), "kvattn_prefill_window")
+    device, s = _here(stream)
+    _, args = _prefill_window_args(Cache, cfg, cache, q, cu_q_lens, prefix_lens, block_table, device)
+    out, op = _out(out, q, q.dtype, device)
+    check(lib.kvattn_prefill_window(*args, max_q_len, q.shape[0], window, num_sinks, op, s), "kvattn_prefill_window")
     return out
 
 
@@ -640,16 +683,12 @@ def prefill_window_fp8_workspace_size(cfg: Config, block_size: int, max_blocks_p
 def prefill_window_fp8(cfg: Config, cache: CacheFP8, q, cu_q_lens, prefix_lens, block_table, max_q_len: int,
                        window: int, num_sinks: int = 0, out=None, workspace=None, stream=None):
     """kvattn_prefill_window_fp8: prefill_window over an fp8 cache (bf16 q and output)."""
-    torch = _torch()
-    out, n, args = _prefill_window_args(CacheFP8, cfg, cache, q, cu_q_lens, prefix_lens, block_table, out)
-    if workspace is None:
-        size = prefill_window_fp8_workspace_size(cfg, cache.block_size, block_table.shape[1], n, max_q_len, window,
-                                                 num_sinks)
-        workspace = torch.empty(max(size, 256), dtype=torch.uint8, device=q.device)
-    _same_device(workspace)
-    check(lib.kvattn_prefill_window_fp8(ctypes.byref(cfg), ctypes.byref(cache.desc), *args, max_q_len, q.shape[0],
-                                        window, num_sinks, _dev(out, "out", q.dtype), _dev(workspace, "workspace"),
-                                        workspace.numel() * workspace.element_size(), _stream(stream)),
+    device, s = _here(stream)
+    n, args = _prefill_window_args(CacheFP8, cfg, cache, q, cu_q_lens, prefix_lens, block_table, device)
+    out, op = _out(out, q, q.dtype, device)
+    wp, nbytes = _scratch(workspace, lambda: prefill_window_fp8_workspace_size(
+        cfg, cache.block_size, block_table.shape[1], n, max_q_len, window, num_sinks), q, device)
+    check(lib.kvattn_prefill_window_fp8(*args, max_q_len, q.shape[0], window, num_sinks, op, wp, nbytes, s),
           "kvattn_prefill_window_fp8")
     return out
 

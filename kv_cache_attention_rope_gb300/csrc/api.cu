@@ -88,6 +88,25 @@ cudaError_t SmemLimit::ensure(const void* func, int bytes)
     return e;
 }
 
+cudaError_t Residency::query(const void* func, int threads, int bytes, int* per_sm)
+{
+    const int dev = current_device();
+    if (dev < 0) return cudaErrorInvalidDevice;
+    cudaError_t e = limit_.ensure(func, bytes);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> g(mu_);
+    if (per_sm_[dev] == 0 || threads_[dev] != threads || bytes_[dev] != bytes) {
+        int n = 0;
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, func, threads, bytes);
+        if (e != cudaSuccess) return e;
+        threads_[dev] = threads;
+        bytes_[dev] = bytes;
+        per_sm_[dev] = std::max(1, n);
+    }
+    *per_sm = per_sm_[dev];
+    return cudaSuccess;
+}
+
 namespace {
 
 bool config_ok(const kvattn_config* c)
@@ -612,7 +631,8 @@ kvattn_status decode_any(const kvattn_config* cfg, const kvattn_cache* cache, bo
     if (!a.status) return KVATTN_ERR_CUDA;
     a.window = win.window;
     a.sinks = win.sinks;
-    return win.window ? launch_decode_window(a, static_cast<cudaStream_t>(stream))
+    const int32_t max_tiles = num_splits ? 0 : (int32_t)(((int64_t)window_span(max_seq_len, win) + 15) / 16);
+    return win.window ? launch_decode_window(a, max_tiles, static_cast<cudaStream_t>(stream))
                       : launch_decode(a, static_cast<cudaStream_t>(stream));
 }
 

@@ -1,0 +1,653 @@
+// Windowed decode attention in one launch, for calls whose keys are few: a
+// thread-block cluster per (sequence, KV head).
+//
+// What it computes: kvattn_decode_window's out[b][j], an online softmax over
+// the seen 16-token tiles of each (sequence, KV head), as decode_kernel.cuh.
+//
+// How: with a window the keys of a segment are bounded, so the segments of a
+// call are of much the same length and need neither a balanced stream nor a
+// second kernel that merges its pieces.  What such a call waits for is
+// latency: every step below is one that a short chain of dependent loads asks
+// for.  The warps of a cluster take the segment's tiles in turn.  A warp loads
+// its tile straight from global memory into MMA fragments (no shared memory,
+// no barrier): the dims of a dot product may be taken in any order, so a lane
+// loads whole 16-byte chunks and the query's fragments follow the same order,
+// and the dims of the output are named so that each lane's chunks of V hold
+// the rows it owns.  S^T = K Q^T and O^T += V^T P^T have the 16 tokens and the
+// dims on the M axis and up to 8 query heads on N; P goes from the C fragment
+// of one to the B fragment of the other by movmatrix.  A warp keeps its own
+// running maximum and sum; the warps of a CTA merge through shared memory and
+// the CTAs of a cluster through distributed shared memory.
+#include <cooperative_groups.h>
+
+#include "decode_kernel.cuh"
+
+namespace kvattn {
+namespace {
+
+namespace cg = cooperative_groups;
+
+enum DirectKind { kBf16Cache, kFp8Cache, kF32Cache };
+
+// One warp's share of a segment: its running maxima and sums (log2 units) and
+// its unnormalised output, kept for query heads 2 q4 and 2 q4 + 1.
+template <int kD>
+struct WarpState {
+    float o[kD / 16][4];
+    float m[2], l[2];
+    float vref, vinv;  // fp8: the V scale that o is in units of
+    __device__ __forceinline__ void init()
+    {
+#pragma unroll
+        for (int e = 0; e < kD / 16; ++e) o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
+        vref = vinv = 0.f;
+    }
+    // Probabilities of this lane's tokens r0, r1 (scores x: (r0, head 0),
+    // (r0, 1), (r1, 0), (r1, 1), V scales sv0, sv1).  The maxima are raised
+    // when a score exceeds them by more than 2^8, and the V scale when a
+    // token's is over 16 times it; the warp agrees on them only then.
+    template <bool kScaled>
+    __device__ __forceinline__ void weigh(const float (&x)[4], float sv0, float sv1, float (&p)[4])
+    {
+        float l0 = fmaxf(x[0], x[2]), l1 = fmaxf(x[1], x[3]), lv = kScaled ? fmaxf(sv0, sv1) : 0.f;
+        const bool raise = l0 > m[0] + 8.f || l1 > m[1] + 8.f || (kScaled && lv > vref * 16.f);
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+            for (int s = 4; s < 32; s <<= 1) {
+                l0 = fmaxf(l0, __shfl_xor_sync(0xffffffffu, l0, s));
+                l1 = fmaxf(l1, __shfl_xor_sync(0xffffffffu, l1, s));
+                if (kScaled) lv = fmaxf(lv, __shfl_xor_sync(0xffffffffu, lv, s));
+            }
+            float f0 = 1.f, f1 = 1.f;
+            if (l0 > m[0] + 8.f) {
+                f0 = m[0] == -INFINITY ? 0.f : fast_exp2(m[0] - l0);
+                l[0] *= f0;
+                m[0] = l0;
+            }
+            if (l1 > m[1] + 8.f) {
+                f1 = m[1] == -INFINITY ? 0.f : fast_exp2(m[1] - l1);
+                l[1] *= f1;
+                m[1] = l1;
+            }
+            if (kScaled && lv > vref * 16.f) {
+                if (vref > 0.f) {
+                    f0 *= vref / lv;
+                    f1 *= vref / lv;
+                }
+                vref = lv;
+                vinv = 1.f / lv;
+            }
+#pragma unroll
+            for (int e = 0; e < kD / 16; ++e) {
+                o[e][0] *= f0;
+                o[e][1] *= f1;
+                o[e][2] *= f0;
+                o[e][3] *= f1;
+            }
+        }
+        // a head whose scores are all -inf so far has no weight yet
+        const float m0 = m[0] == -INFINITY ? 0.f : m[0], m1 = m[1] == -INFINITY ? 0.f : m[1];
+        p[0] = fast_exp2(x[0] - m0);
+        p[1] = fast_exp2(x[1] - m1);
+        p[2] = fast_exp2(x[2] - m0);
+        p[3] = fast_exp2(x[3] - m1);
+        l[0] += p[0] + p[2];
+        l[1] += p[1] + p[3];
+    }
+};
+
+__device__ __forceinline__ uint4 ldg16(const void* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+__device__ __forceinline__ uint32_t ldg4(const void* p) { return __ldg(reinterpret_cast<const uint32_t*>(p)); }
+
+// ---- bf16 cache.  K: lane (g4, q4) holds rows (tokens) g4 and g4 + 8, 16-byte
+// chunks q4 + 4i of each; chunk i is the lane's share of MMA k-steps 2i and
+// 2i + 1.  V: rows 2 q4, 2 q4 + 1, 2 q4 + 8, 2 q4 + 9, chunks g4 (+ 8 at D =
+// 128); two rows' words interleave into pairs of tokens of one dim.
+template <int kD>
+struct Bf16Tile {
+    static constexpr int kC = kD / 32;   // K chunks per row and lane
+    static constexpr int kVC = kD / 64;  // V chunks per row and lane
+    uint4 k[2][kC];
+    __device__ __forceinline__ void load_k(const char* kp, uint32_t seen, int g4, int q4)
+    {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const bool in = seen >> (g4 + 8 * r) & 1u;
+#pragma unroll
+            for (int i = 0; i < kC; ++i)
+                k[r][i] = in ? ldg16(kp + (g4 + 8 * r) * (kD * 2) + (q4 + 4 * i) * 16) : make_uint4(0, 0, 0, 0);
+        }
+    }
+    static __device__ __forceinline__ void load_v(uint4 (&v)[4][kVC], const char* vp, uint32_t seen, int g4, int q4)
+    {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = 2 * q4 + (r & 1) + 8 * (r >> 1);
+            const bool in = seen >> row & 1u;
+#pragma unroll
+            for (int i = 0; i < kVC; ++i)
+                v[r][i] = in ? ldg16(vp + row * (kD * 2) + (g4 + 8 * i) * 16) : make_uint4(0, 0, 0, 0);
+        }
+    }
+    __device__ __forceinline__ void scores(float (&s)[4], const uint32_t (&q)[kD / 16][2]) const
+    {
+        float u[4] = {0.f, 0.f, 0.f, 0.f};  // two chains of dependent MMAs
+#pragma unroll
+        for (int i = 0; i < kC; ++i) {
+            mma_bf16_16816(s, k[0][i].x, k[1][i].x, k[0][i].y, k[1][i].y, q[2 * i][0], q[2 * i][1]);
+            mma_bf16_16816(u, k[0][i].z, k[1][i].z, k[0][i].w, k[1][i].w, q[2 * i + 1][0], q[2 * i + 1][1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] += u[i];
+    }
+    // O^T rows g4 and g4 + 8 of fragment e are dims dim_of(e, 0) and dim_of(e, 1)
+    static __device__ __forceinline__ int dim_of(int e, int half, int g4)
+    {
+        return kD == 128 ? 64 * half + 8 * g4 + e : 8 * g4 + 4 * half + e;
+    }
+    static __device__ __forceinline__ void add(const uint4 (&v)[4][kVC], float (&o)[kD / 16][4], uint32_t b0, uint32_t b1)
+    {
+        uint32_t w[4][kVC * 4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int i = 0; i < kVC; ++i) {
+                w[r][4 * i] = v[r][i].x;
+                w[r][4 * i + 1] = v[r][i].y;
+                w[r][4 * i + 2] = v[r][i].z;
+                w[r][4 * i + 3] = v[r][i].w;
+            }
+        // pair of dim d (0 .. 8 kVC - 1 of this lane) of rows r, r + 1
+        auto pair = [&](int r, int d) { return __byte_perm(w[r][d / 2], w[r + 1][d / 2], d & 1 ? 0x7632 : 0x5410); };
+#pragma unroll
+        for (int e = 0; e < kD / 16; ++e) {
+            const int d0 = e, d1 = kD == 128 ? e + 8 : e + 4;
+            mma_bf16_16816(o[e], pair(0, d0), pair(0, d1), pair(2, d0), pair(2, d1), b0, b1);
+        }
+    }
+};
+
+// ---- fp8 pages (layout: kF8Page), f16 operands.  K: rows rk0, rk1 = rk0 + 2,
+// chunks q4 and q4 + 4, each the lane's share of four k-steps.  V is stored
+// transposed: one word is tokens 4 q4 .. 4 q4 + 3 of a dim, whose order the
+// rows rk0, rk1 follow.
+struct Fp8Tile {
+    uint4 k[2][2];
+    uint32_t v[16];
+    float ks[2], vs[2];
+    __device__ __forceinline__ void load_k(const char* pg, int rk0, int q4)
+    {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = rk0 + 2 * r;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) k[r][i] = ldg16(pg + row * 128 + (((q4 + 4 * i) ^ f8_swz(row)) << 4));
+            ks[r] = __uint_as_float(ldg4(pg + kF8KsOff + 4 * row));
+        }
+    }
+    __device__ __forceinline__ void load_v(const char* pg, int rk0, int g4, int q4)
+    {
+#pragma unroll
+        for (int m = 0; m < 16; ++m) v[m] = ldg4(pg + kF8VOff + 16 * (8 * m + g4) + 4 * q4);
+        vs[0] = __uint_as_float(ldg4(pg + kF8VsOff + 4 * rk0));
+        vs[1] = __uint_as_float(ldg4(pg + kF8VsOff + 4 * rk0 + 8));
+    }
+    __device__ __forceinline__ void scores(float (&s)[4], const uint32_t (&q)[8][2]) const
+    {
+        float u[4] = {0.f, 0.f, 0.f, 0.f};  // two chains of dependent MMAs
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t a[4] = {k[0][i].x, k[0][i].y, k[0][i].z, k[0][i].w};
+            const uint32_t b[4] = {k[1][i].x, k[1][i].y, k[1][i].z, k[1][i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                mma_f16_16816(i ? u : s, e4m3x2_to_f16x2(a[j]), e4m3x2_to_f16x2(b[j]), e4m3x2_to_f16x2(a[j] >> 16),
+                              e4m3x2_to_f16x2(b[j] >> 16), q[4 * i + j][0], q[4 * i + j][1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] += u[i];
+    }
+    static __device__ __forceinline__ int dim_of(int e, int half, int g4) { return 16 * e + 8 * half + g4; }
+    __device__ __forceinline__ void add(float (&o)[8][4], uint32_t b0, uint32_t b1, uint32_t vmask) const
+    {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t x = v[2 * e] & vmask, y = v[2 * e + 1] & vmask;
+            mma_f16_16816(o[e], e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(y), e4m3x2_to_f16x2(x >> 16),
+                          e4m3x2_to_f16x2(y >> 16), b0, b1);
+        }
+    }
+};
+
+// Resident warps per SM that the register budgets leave room for.  Measured
+// (32 / 8 heads, 32 sequences, window 4096; 16, 12 and 8 warps): a bf16 tile
+// at D = 128 wants 200 registers, 100.7, 91.9 and 88.5 us (the first with
+// spills); an fp8 page 168, 70.1, 55.0 and 64.9 us.
+constexpr int warps_per_sm(int kind, int d, int g)
+{
+    return kind == kF32Cache ? (d * g > 64 ? 8 : 16) : kind == kFp8Cache ? 12 : d == 64 ? 16 : 8;
+}
+
+// Shared floats of a CTA: every warp's output and (max, sum) of each head, and
+// the CTA's merge of them (read by the other CTAs of the cluster).
+__host__ __device__ constexpr int direct_floats(int warps, int heads, int d) { return (warps + 1) * heads * (d + 2); }
+
+template <int kKind, int kD, int kG>
+__global__ void __launch_bounds__(warps_per_sm(kKind, kD, kG) * 32, 1)
+    decode_direct_kernel(const __grid_constant__ DecodeArgs a, const int cluster)
+{
+    pdl_wait();
+    extern __shared__ float part[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
+    const int g4 = lane >> 2, q4 = lane & 3;
+    const int rank = blockIdx.x % cluster, seg = blockIdx.x / cluster;
+    const int b = seg / a.hkv, h = seg - b * a.hkv;
+    const int G = a.hq / a.hkv;
+    const int64_t q0 = ((int64_t)b * a.hq + h * G) * kD;  // first element of the group's queries and outputs
+    const int L = a.seq_lens[b];
+
+    // per-head rows of the warps' (and, last, the CTA's) outputs and (max, sum)
+    auto row_of = [&](int w, int g) { return part + (w * G + g) * kD; };
+    float* ml = part + (warps + 1) * G * kD;
+    auto ml_of = [&](int w, int g) { return ml + 2 * (w * G + g); };
+
+    Piece pc;
+    pc.len = 0;
+    Window win{0, 0, 0, 0};
+    if (len_ok(L, a)) {
+        win = window_of(L, a);
+        pc.len = L;
+        pc.sink_tiles = win.sink_tiles;
+        pc.gap = win.gap;
+        pc.low = win.low;
+    } else if (rank == 0 && h == 0 && tid == 0) {
+        record_error(a.status, KVATTN_ERR_BAD_INDEX);
+    }
+    auto first_token = [&](int t) { return (t >= pc.sink_tiles ? t + pc.gap : t) * kTile; };
+    const int n = cluster * warps, first = rank * warps + warp;  // this warp: tiles first, first + n, ...
+    const int mine = first < win.tiles ? (win.tiles - 1 - first) / n + 1 : 0;
+    const int32_t* trow = a.block_table + (int64_t)b * a.max_blocks;
+    // row in the pool of this lane's tile of a batch of 32 (-1: none)
+    auto lookup = [&](int base) -> int64_t {
+        if (base + lane >= mine) return -1;
+        const int tok = first_token(first + (base + lane) * n);
+        const int32_t id = trow[tok / a.block_size];
+        if (id < 0 || id >= a.num_blocks) {
+            record_error(a.status, KVATTN_ERR_BAD_INDEX);
+            return -1;
+        }
+        return ((int64_t)id * a.hkv + h) * a.block_size + tok % a.block_size;
+    };
+    // keys of the j-th tile of this warp that are seen (0 when its block id is bad)
+    auto seen_of = [&](int j, int64_t row) -> uint32_t {
+        return row < 0 ? 0u : seen_bits(first_token(first + j * n), pc, a);
+    };
+    int64_t rows = lookup(0);
+
+    if constexpr (kKind != kF32Cache) {
+        // the group's queries as B fragments: head g4, the dims in the order of K's chunks
+        uint32_t q[kD / 16][2];
+#pragma unroll
+        for (int i = 0; i < kD / 16; ++i) q[i][0] = q[i][1] = 0u;
+        if (g4 < G) {
+            const __nv_bfloat16* qh = reinterpret_cast<const __nv_bfloat16*>(a.q) + q0 + g4 * kD;
+            if constexpr (kKind == kBf16Cache) {
+#pragma unroll
+                for (int i = 0; i < kD / 32; ++i) {
+                    const uint4 w = ldg16(qh + 8 * (q4 + 4 * i));
+                    q[2 * i][0] = w.x;
+                    q[2 * i][1] = w.y;
+                    q[2 * i + 1][0] = w.z;
+                    q[2 * i + 1][1] = w.w;
+                }
+            } else {  // scaled by 2^-4 into f16's range (the scores are scaled back)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 w = ldg16(qh + 16 * (q4 + 4 * (i >> 1)) + 8 * (i & 1));
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        q[2 * i + (j >> 1)][j & 1] = pack_f16_rn(bf16lo(u[j]) * 0.0625f, bf16hi(u[j]) * 0.0625f);
+                }
+            }
+        }
+        WarpState<kD> st;
+        st.init();
+        const float sl2 = a.scale_log2 * (kKind == kFp8Cache ? 16.f : 1.f);
+        if constexpr (kKind == kBf16Cache) {
+            Bf16Tile<kD> t;
+            const char *kp = (const char*)a.k_pool, *vp = (const char*)a.v_pool;
+            uint4 v[2][4][kD / 64];
+            int64_t row = __shfl_sync(0xffffffffu, rows, 0);
+            uint32_t seen = mine ? seen_of(0, row) : 0u;
+            if (mine) {
+                t.load_k(kp + row * (kD * 2), seen, g4, q4);
+                t.load_v(v[0], vp + row * (kD * 2), seen, g4, q4);
+            }
+            auto step = [&](int j, const uint4 (&vnow)[4][kD / 64], uint4 (&vnext)[4][kD / 64]) {
+                float s[4] = {0.f, 0.f, 0.f, 0.f};
+                t.scores(s, q);
+                // the next tile flies during this tile's softmax and P.V
+                const uint32_t now = seen;
+                if (j + 1 < mine) {
+                    if (((j + 1) & 31) == 0) rows = lookup(j + 1);
+                    row = __shfl_sync(0xffffffffu, rows, (j + 1) & 31);
+                    seen = seen_of(j + 1, row);
+                    t.load_k(kp + row * (kD * 2), seen, g4, q4);
+                    t.load_v(vnext, vp + row * (kD * 2), seen, g4, q4);
+                }
+                const float x[4] = {now >> g4 & 1u ? s[0] * sl2 : -INFINITY, now >> g4 & 1u ? s[1] * sl2 : -INFINITY,
+                                    now >> (g4 + 8) & 1u ? s[2] * sl2 : -INFINITY,
+                                    now >> (g4 + 8) & 1u ? s[3] * sl2 : -INFINITY};
+                float p[4];
+                st.template weigh<false>(x, 0.f, 0.f, p);
+                t.add(vnow, st.o, movmatrix_trans(pack_bf16_rn(p[0], p[1])), movmatrix_trans(pack_bf16_rn(p[2], p[3])));
+            };
+            for (int j = 0; j < mine; j += 2) {
+                step(j, v[0], v[1]);
+                if (j + 1 < mine) step(j + 1, v[1], v[0]);
+            }
+            st.vref = 1.f;
+        } else {
+            const int rk0 = (g4 >> 1) * 4 + (g4 & 1), rk1 = rk0 + 2;
+            const char* pool = (const char*)a.k_pool;
+            Fp8Tile t[2];
+            auto fetch = [&](Fp8Tile& d, int64_t row) {
+                if (row < 0) row = 0;  // a bad block: nothing of it is seen
+                const char* pg = pool + row / kTile * kF8Page;
+                d.load_k(pg, rk0, q4);
+                d.load_v(pg, rk0, g4, q4);
+            };
+            int64_t row = __shfl_sync(0xffffffffu, rows, 0);
+            uint32_t seen = mine ? seen_of(0, row) : 0u;
+            if (mine) fetch(t[0], row);
+            auto step = [&](int j, Fp8Tile& d, Fp8Tile& next) {
+                const uint32_t now = seen;
+                if (j + 1 < mine) {  // the next page flies while this one is computed
+                    if (((j + 1) & 31) == 0) rows = lookup(j + 1);
+                    row = __shfl_sync(0xffffffffu, rows, (j + 1) & 31);
+                    seen = seen_of(j + 1, row);
+                    fetch(next, row);
+                }
+                float s[4] = {0.f, 0.f, 0.f, 0.f};
+                d.scores(s, q);
+                const float k0 = d.ks[0] * sl2, k1 = d.ks[1] * sl2;
+                const bool in0 = now >> rk0 & 1u, in1 = now >> rk1 & 1u;
+                const float x[4] = {in0 ? s[0] * k0 : -INFINITY, in0 ? s[1] * k0 : -INFINITY,
+                                    in1 ? s[2] * k1 : -INFINITY, in1 ? s[3] * k1 : -INFINITY};
+                const float sv0 = in0 ? d.vs[0] : 0.f, sv1 = in1 ? d.vs[1] : 0.f;
+                uint32_t vmask = 0xffffffffu;  // the bytes of this lane's words whose tokens are seen
+                if (now != (1u << kTile) - 1u) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (!(now >> (4 * q4 + i) & 1u)) vmask &= ~(0xffu << (8 * i));
+                }
+                float p[4];
+                st.template weigh<true>(x, sv0, sv1, p);
+                const float c0 = sv0 * st.vinv, c1 = sv1 * st.vinv;
+                d.add(st.o, movmatrix_trans(pack_f16_rn(p[0] * c0, p[1] * c0)),
+                      movmatrix_trans(pack_f16_rn(p[2] * c1, p[3] * c1)), vmask);
+            };
+            for (int j = 0; j < mine; j += 2) {
+                step(j, t[0], t[1]);
+                if (j + 1 < mine) step(j + 1, t[1], t[0]);
+            }
+        }
+#pragma unroll
+        for (int s = 4; s < 32; s <<= 1) {
+            st.l[0] += __shfl_xor_sync(0xffffffffu, st.l[0], s);
+            st.l[1] += __shfl_xor_sync(0xffffffffu, st.l[1], s);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int g = 2 * q4 + e;
+            if (g < G) {
+                float* r = row_of(warp, g);
+#pragma unroll
+                for (int i = 0; i < kD / 16; ++i)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        int d;
+                        if constexpr (kKind == kBf16Cache) d = Bf16Tile<kD>::dim_of(i, half, g4);
+                        else d = Fp8Tile::dim_of(i, half, g4);
+                        r[d] = st.o[i][2 * half + e] * st.vref;
+                    }
+                if (g4 == 0) {
+                    ml_of(warp, g)[0] = st.m[e];
+                    ml_of(warp, g)[1] = st.l[e];
+                }
+            }
+        }
+    } else {
+        // ---- fp32 cache, CUDA cores.  Scores: lane (g4, q4) holds tokens g4 and
+        // g4 + 8, 16-byte chunks q4 + 4i; a quad's partial sums meet by shuffle.
+        // P.V: a lane owns 4 dims of every (D = 128) or every other (D = 64)
+        // token; the probabilities go through the warp's slot of shared memory.
+        constexpr int kC = kD / 16;        // chunks per row and lane
+        constexpr int kRep = 128 / kD;     // lanes that share a dim slice
+        constexpr int kVR = kTile / kRep;  // tokens per lane
+        const int dl = lane % (kD / 4), tr = lane / (kD / 4);
+        const float* qs = reinterpret_cast<const float*>(a.q) + q0;
+        float* pb = row_of(warp, 0);  // [token][kG], before the warp's output takes its place
+        float o[kG][4], m[kG], l[kG];
+#pragma unroll
+        for (int g = 0; g < kG; ++g) {
+            o[g][0] = o[g][1] = o[g][2] = o[g][3] = 0.f;
+            m[g] = -INFINITY;
+            l[g] = 0.f;
+        }
+        const uint4 none = make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < mine; ++j) {
+            if (j > 0 && (j & 31) == 0) rows = lookup(j);
+            const int64_t row = __shfl_sync(0xffffffffu, rows, j & 31);
+            const uint32_t seen = seen_of(j, row);
+            const char* kp = (const char*)a.k_pool + row * (kD * 4);
+            const char* vp = (const char*)a.v_pool + row * (kD * 4);
+            uint4 k[2][kC], v[kVR];
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int i = 0; i < kC; ++i)
+                    k[r][i] = seen >> (g4 + 8 * r) & 1u ? ldg16(kp + (g4 + 8 * r) * (kD * 4) + (q4 + 4 * i) * 16) : none;
+#pragma unroll
+            for (int t = 0; t < kVR; ++t)
+                v[t] = seen >> (t * kRep + tr) & 1u ? ldg16(vp + (t * kRep + tr) * (kD * 4) + dl * 16) : none;
+            float x[2][kG];
+#pragma unroll
+            for (int g = 0; g < kG; ++g) {
+                float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                for (int i = 0; i < kC; ++i) {
+                    const float4 w = __ldg(reinterpret_cast<const float4*>(qs + g * kD) + q4 + 4 * i);
+                    const float* k0 = reinterpret_cast<const float*>(&k[0][i]);
+                    const float* k1 = reinterpret_cast<const float*>(&k[1][i]);
+                    s0 = fmaf(w.x, k0[0], fmaf(w.y, k0[1], fmaf(w.z, k0[2], fmaf(w.w, k0[3], s0))));
+                    s1 = fmaf(w.x, k1[0], fmaf(w.y, k1[1], fmaf(w.z, k1[2], fmaf(w.w, k1[3], s1))));
+                }
+                s0 += __shfl_xor_sync(0xffffffffu, s0, 1);
+                s1 += __shfl_xor_sync(0xffffffffu, s1, 1);
+                s0 += __shfl_xor_sync(0xffffffffu, s0, 2);
+                s1 += __shfl_xor_sync(0xffffffffu, s1, 2);
+                x[0][g] = seen >> g4 & 1u ? s0 * a.scale_log2 : -INFINITY;
+                x[1][g] = seen >> (g4 + 8) & 1u ? s1 * a.scale_log2 : -INFINITY;
+            }
+#pragma unroll
+            for (int g = 0; g < kG; ++g) {
+                float t = fmaxf(x[0][g], x[1][g]);
+#pragma unroll
+                for (int s = 4; s < 32; s <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, s));
+                t = fmaxf(t, m[g]);
+                const float f = m[g] == -INFINITY ? 0.f : exp2f(m[g] - t);
+                m[g] = t;
+                const float base = t == -INFINITY ? 0.f : t;
+                x[0][g] = exp2f(x[0][g] - base);
+                x[1][g] = exp2f(x[1][g] - base);
+                l[g] = l[g] * f + (x[0][g] + x[1][g]);
+                o[g][0] *= f;
+                o[g][1] *= f;
+                o[g][2] *= f;
+                o[g][3] *= f;
+                if (q4 == 0) {
+                    pb[g4 * kG + g] = x[0][g];
+                    pb[(g4 + 8) * kG + g] = x[1][g];
+                }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int t = 0; t < kVR; ++t) {
+                const float* vv = reinterpret_cast<const float*>(&v[t]);
+#pragma unroll
+                for (int g = 0; g < kG; ++g) {
+                    const float p = pb[(t * kRep + tr) * kG + g];
+                    o[g][0] = fmaf(p, vv[0], o[g][0]);
+                    o[g][1] = fmaf(p, vv[1], o[g][1]);
+                    o[g][2] = fmaf(p, vv[2], o[g][2]);
+                    o[g][3] = fmaf(p, vv[3], o[g][3]);
+                }
+            }
+            __syncwarp();
+        }
+#pragma unroll
+        for (int g = 0; g < kG; ++g) {
+#pragma unroll
+            for (int s = 4; s < 32; s <<= 1) l[g] += __shfl_xor_sync(0xffffffffu, l[g], s);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (kRep == 2) o[g][i] += __shfl_xor_sync(0xffffffffu, o[g][i], 16);
+            if (tr == 0) *reinterpret_cast<float4*>(row_of(warp, g) + 4 * dl) = make_float4(o[g][0], o[g][1], o[g][2], o[g][3]);
+            if (lane == 0) {
+                ml_of(warp, g)[0] = m[g];
+                ml_of(warp, g)[1] = l[g];
+            }
+        }
+    }
+    __syncthreads();
+
+    // ---- the warps' states, then the CTAs'
+    auto store = [&](int e, float num, float den) {
+        const float o = den > 0.f ? num / den : 0.f;
+        if constexpr (kKind == kF32Cache) reinterpret_cast<float*>(a.out)[q0 + e] = o;
+        else reinterpret_cast<__nv_bfloat16*>(a.out)[q0 + e] = __float2bfloat16_rn(o);
+    };
+    for (int e = tid; e < G * kD; e += blockDim.x) {
+        const int g = e / kD, d = e - g * kD;
+        float M = -INFINITY, num = 0.f, den = 0.f;
+#pragma unroll 4
+        for (int w = 0; w < warps; ++w) M = fmaxf(M, ml_of(w, g)[0]);
+        if (M != -INFINITY) {
+#pragma unroll 4
+            for (int w = 0; w < warps; ++w) {
+                const float f = exp2f(ml_of(w, g)[0] - M);  // a warp without a key: 0
+                num += f * row_of(w, g)[d];
+                den += f * ml_of(w, g)[1];
+            }
+        }
+        if (cluster == 1) {
+            store(e, num, den);
+        } else {
+            row_of(warps, g)[d] = num;
+            if (d == 0) {
+                ml_of(warps, g)[0] = M;
+                ml_of(warps, g)[1] = den;
+            }
+        }
+    }
+    if (cluster > 1) {
+        cg::cluster_group cl = cg::this_cluster();
+        cl.sync();
+        for (int e = rank * blockDim.x + tid; e < G * kD; e += n * 32) {
+            const int g = e / kD, d = e - g * kD;
+            float M = -INFINITY, num = 0.f, den = 0.f;
+            for (int r = 0; r < cluster; ++r) M = fmaxf(M, cl.map_shared_rank(ml_of(warps, g), r)[0]);
+            if (M != -INFINITY) {
+                for (int r = 0; r < cluster; ++r) {
+                    const float* o = cl.map_shared_rank(row_of(warps, g), r);
+                    const float* s = cl.map_shared_rank(ml_of(warps, g), r);
+                    const float f = exp2f(s[0] - M);
+                    num += f * o[d];
+                    den += f * s[1];
+                }
+            }
+            store(e, num, den);
+        }
+        cl.sync();  // the others' shared memory stays until it has been read
+    }
+}
+
+template <int kKind, int kD, int kG>
+kvattn_status run_direct(const DecodeArgs& a, int warps, int cluster, cudaStream_t s)
+{
+    auto kern = decode_direct_kernel<kKind, kD, kG>;
+    const int bytes = direct_floats(warps, a.hq / a.hkv, kD) * 4;
+    static SmemLimit limit;
+    if (limit.ensure(reinterpret_cast<const void*>(kern), bytes) != cudaSuccess) return KVATTN_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.batch * a.hkv * cluster));
+    cfg.blockDim = dim3(warps * 32);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kern, a, cluster));
+}
+
+kvattn_status direct_dispatch(const DecodeArgs& a, int warps, int cluster, cudaStream_t s)
+{
+    if (a.fp8) return run_direct<kFp8Cache, 128, 8>(a, warps, cluster, s);
+    if (a.dtype == KVATTN_BF16)
+        return a.d == 128 ? run_direct<kBf16Cache, 128, 8>(a, warps, cluster, s)
+                          : run_direct<kBf16Cache, 64, 8>(a, warps, cluster, s);
+    switch (a.hq / a.hkv) {
+#define KVATTN_DIRECT_F32(GG)                                                    \
+    case GG:                                                                     \
+        return a.d == 128 ? run_direct<kF32Cache, 128, GG>(a, warps, cluster, s) \
+                          : run_direct<kF32Cache, 64, GG>(a, warps, cluster, s);
+        KVATTN_DIRECT_F32(1)
+        KVATTN_DIRECT_F32(2)
+        KVATTN_DIRECT_F32(4)
+        KVATTN_DIRECT_F32(8)
+#undef KVATTN_DIRECT_F32
+    }
+    return KVATTN_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+bool launch_decode_direct(const DecodeArgs& a, int32_t max_tiles, cudaStream_t s, kvattn_status* st)
+{
+    const int kind = a.fp8 ? kFp8Cache : a.dtype == KVATTN_BF16 ? kBf16Cache : kF32Cache;
+    const int G = a.hq / a.hkv;
+    const int64_t segs = (int64_t)a.batch * a.hkv, tiles = segs * max_tiles;
+    // Where the balanced stream of decode_kernel.cuh is faster: long calls of
+    // many keys.  Measured (us, this and the stream; thousands of tiles): bf16
+    // D = 128 17 27 / 32, 66 88 / 90, 264 343 / 324; fp8 17 14.5 / 25.8, 66
+    // 55 / 59, 264 200 / 195; fp32 groups of 4 4.2 13.4 / 20.6, 16 49 / 48,
+    // 66 171 / 160; bf16 D = 64 264 165 / 307 and fp32 without groups 264
+    // 574 / 608, so these always come here.
+    int64_t most = INT64_MAX;
+    if (kind == kF32Cache) most = G == 1 ? most : 16384;
+    else if (a.d == 128) most = 65536;
+    if (tiles > most || segs * 8 > INT32_MAX) return false;
+    // One wave of warps: the most warps per CTA that let every segment be
+    // resident (a quarter of the SM's when not even that does), at most 8;
+    // then CTAs per segment; but no warp without a tile.
+    const int cap = warps_per_sm(kind, a.d, G);
+    const int64_t sms = num_sms();
+    int warps = 8;
+    while (warps > cap / 4 && sms * (cap / warps) < segs) --warps;
+    int cluster = 1;
+    while (cluster < 8 && warps == 8 && sms * (cap / 8) >= 2 * cluster * segs && 16 * cluster <= max_tiles) cluster *= 2;
+    warps = std::min(warps, max_tiles);
+    *st = direct_dispatch(a, warps, cluster, s);
+    return true;
+}
+
+}  // namespace kvattn

@@ -1086,12 +1086,10 @@ kvattn_status run(const DecodeArgs& a, cudaStream_t s)
     const SharedLayout SL = shared_layout<kBF16, kD, kGT, kFP8>(stages, a.batch);
     const int smem_bytes = SL.bytes + 1024;
     auto kern = decode_split_kernel<kBF16, kD, kGT, kMma, kRowBoxes, kFP8, kWin>;
-    static SmemLimit limit;
-    if (limit.ensure(reinterpret_cast<const void*>(kern), smem_bytes) != cudaSuccess) return KVATTN_ERR_CUDA;
+    static Residency residency;
     int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, smem_bytes) != cudaSuccess)
+    if (residency.query(reinterpret_cast<const void*>(kern), kThreads, smem_bytes, &per_sm) != cudaSuccess)
         return KVATTN_ERR_CUDA;
-    per_sm = std::max(1, per_sm);
     const int grid = num_sms() * per_sm;
     cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kThreads), smem_bytes, s, a, maps, stages);
     if (e != cudaSuccess) return KVATTN_ERR_CUDA;

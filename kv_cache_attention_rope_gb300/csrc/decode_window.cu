@@ -1,10 +1,17 @@
 // Windowed decode attention: one query per sequence over the last `window`
-// tokens of its cache and the first `sinks` ones, with the split-KV kernels of
-// decode_kernel.cuh over the tiles that hold them.
+// tokens of its cache and the first `sinks` ones.  Calls of few keys take one
+// launch (decode_direct.cu); the others, and those with a given number of
+// splits, the split-KV kernels of decode_kernel.cuh over the tiles that hold
+// seen keys.
 #include "decode_kernel.cuh"
 
 namespace kvattn {
 
-kvattn_status launch_decode_window(const DecodeArgs& a, cudaStream_t s) { return dispatch<true>(a, s); }
+kvattn_status launch_decode_window(const DecodeArgs& a, int32_t max_tiles, cudaStream_t s)
+{
+    kvattn_status st;
+    if (max_tiles > 0 && launch_decode_direct(a, max_tiles, s, &st)) return st;
+    return dispatch<true>(a, s);
+}
 
 }  // namespace kvattn

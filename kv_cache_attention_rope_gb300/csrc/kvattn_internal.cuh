@@ -65,6 +65,20 @@ private:
     int set_[64] = {};
 };
 
+// A kernel's resident CTAs per SM on the current device at a block size and a
+// dynamic shared-memory size, its limit raised first.  The answer is a pure
+// function of these; the last one of each device is kept (asking the runtime
+// costs about as much host time as a launch).
+class Residency {
+public:
+    cudaError_t query(const void* func, int threads, int bytes, int* per_sm);
+
+private:
+    SmemLimit limit_;
+    std::mutex mu_;
+    int threads_[64] = {}, bytes_[64] = {}, per_sm_[64] = {};
+};
+
 struct RopeArgs {
     void* q;
     const void* k;
@@ -177,7 +191,10 @@ struct DecodeArgs {
     int32_t window, sinks;  // launch_decode_window only
 };
 kvattn_status launch_decode(const DecodeArgs& a, cudaStream_t s);
-kvattn_status launch_decode_window(const DecodeArgs& a, cudaStream_t s);
+// max_tiles: most 16-token tiles that a query sees, or 0 to cut the segments as a.splits says.
+kvattn_status launch_decode_window(const DecodeArgs& a, int32_t max_tiles, cudaStream_t s);
+// The one-launch form, where it is the faster one (else false, nothing launched).
+bool launch_decode_direct(const DecodeArgs& a, int32_t max_tiles, cudaStream_t s, kvattn_status* st);
 
 // Largest decode batch (the kernels keep a per-sequence prefix sum in shared memory).
 constexpr int32_t kMaxDecodeBatch = 8192;

@@ -287,12 +287,11 @@ constexpr int kExpandSmem = kExpandWarps * 2 * kF8Page;
 template <bool kWin>
 cudaError_t expand_grid(int* grid)
 {
-    static SmemLimit limit;
-    cudaError_t e = limit.ensure(reinterpret_cast<const void*>(prefill_fp8_expand<kWin>), kExpandSmem);
-    if (e != cudaSuccess) return e;
+    static Residency residency;
     int per_sm = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, prefill_fp8_expand<kWin>, kExpandWarps * 32, kExpandSmem);
-    *grid = num_sms() * std::max(1, per_sm);
+    const cudaError_t e = residency.query(reinterpret_cast<const void*>(prefill_fp8_expand<kWin>), kExpandWarps * 32,
+                                          kExpandSmem, &per_sm);
+    *grid = num_sms() * per_sm;
     return e;
 }
 

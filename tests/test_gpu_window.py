@@ -42,15 +42,27 @@ def _decode(kv, dtype, hq, hkv, d, lens, window, sinks, block=16, splits=0, seed
                                           (ALL, 0), (5, 600), (1, ALL)])
 @pytest.mark.parametrize("dtype,hq,hkv,d", [("bf16", 32, 8, 128), ("bf16", 8, 8, 128), ("f32", 12, 12, 64),
                                             ("fp8", 16, 4, 128)])
-def test_decode_masks(kvattn_lib, dtype, hq, hkv, d, window, sinks):
-    _decode(kvattn_lib, dtype, hq, hkv, d, LENS, window, sinks, seed=window % 97 + sinks % 89)
+@pytest.mark.parametrize("splits", [0, 3])
+def test_decode_masks(kvattn_lib, dtype, hq, hkv, d, window, sinks, splits):
+    """In one launch (splits 0: these are few keys) and over the balanced stream."""
+    _decode(kvattn_lib, dtype, hq, hkv, d, LENS, window, sinks, splits=splits, seed=window % 97 + sinks % 89)
 
 
 @pytest.mark.parametrize("dtype,hq,hkv,d,block", [("bf16", 64, 8, 128, 16), ("bf16", 8, 1, 128, 48), ("bf16", 4, 2, 64, 32),
                                                   ("bf16", 16, 2, 64, 16), ("bf16", 8, 4, 128, 16), ("f32", 32, 4, 128, 16),
                                                   ("f32", 8, 2, 64, 64), ("fp8", 8, 1, 128, 32), ("fp8", 64, 8, 128, 16)])
-def test_decode_heads_and_blocks(kvattn_lib, dtype, hq, hkv, d, block):
-    _decode(kvattn_lib, dtype, hq, hkv, d, LENS, 75, 5, block=block, seed=hq)
+@pytest.mark.parametrize("splits", [0, 2])
+def test_decode_heads_and_blocks(kvattn_lib, dtype, hq, hkv, d, block, splits):
+    _decode(kvattn_lib, dtype, hq, hkv, d, LENS, 75, 5, block=block, splits=splits, seed=hq)
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,d", [("bf16", 8, 1, 128), ("bf16", 4, 4, 64), ("fp8", 4, 1, 128), ("f32", 1, 1, 128),
+                                            ("f32", 2, 1, 64), ("f32", 4, 1, 64), ("f32", 8, 1, 128), ("f32", 2, 1, 128)])
+@pytest.mark.parametrize("lens,window", [([9000], 6000), ([1, 4000, 0, 2500, 16], 3000), ([300] * 40, 250),
+                                         ([35, 0, 20] * 120, 34)])
+def test_decode_clusters(kvattn_lib, dtype, hq, hkv, d, lens, window):
+    """From several thread blocks per segment, and several rounds of 32 tiles per warp, to several segments a block."""
+    _decode(kvattn_lib, dtype, hq, hkv, d, lens, window, 20, seed=len(lens))
 
 
 @pytest.mark.parametrize("splits", [1, 2, 5, 40])
@@ -59,10 +71,11 @@ def test_decode_splits(kvattn_lib, dtype, splits):
     _decode(kvattn_lib, dtype, 8, 2, 128, [3000, 0, 2200, 17, 801], 700, 33, splits=splits, seed=splits)
 
 
-@pytest.mark.parametrize("dtype,hq,hkv,d", [("f32", 12, 12, 64), ("bf16", 8, 2, 128)])
-def test_decode_contiguous_cache(kvattn_lib, dtype, hq, hkv, d):
+@pytest.mark.parametrize("dtype,hq,hkv,d", [("f32", 12, 12, 64), ("bf16", 8, 2, 128), ("bf16", 8, 8, 64)])
+@pytest.mark.parametrize("splits", [0, 2])
+def test_decode_contiguous_cache(kvattn_lib, dtype, hq, hkv, d, splits):
     """One row per sequence, of a length that is no multiple of 16."""
-    _decode(kvattn_lib, dtype, hq, hkv, d, [1, 777, 400, 775], 130, 3, block=777, seed=5)
+    _decode(kvattn_lib, dtype, hq, hkv, d, [1, 777, 400, 775], 130, 3, block=777, splits=splits, seed=5)
 
 
 def test_decode_one_and_many_sequences(kvattn_lib):
