@@ -89,8 +89,8 @@ struct Geo {
 };
 
 struct Maps {
-    CUtensorMap q;  // 3-D: (D, Hq, total_q), box (64, 1, 128)
-    CUtensorMap o;  // 3-D: (D, Hq, total_q), box (32, 1, 32), 64-byte swizzle (output stores)
+    CUtensorMap q;  // 3-D: (D, Hq, total_q), box (64, 1, 128) (kWin: (64, G, 128 / G))
+    CUtensorMap o;  // 3-D: (D, Hq, total_q), box (32, 1, 32) ((32, G, 32 / G)), 64-byte swizzle (output stores)
     CUtensorMap k;  // 4-D: (64 columns, 8 rows, 2 panels, rows / 8), box (64, 8, 2, 2)
     CUtensorMap v;
 };
@@ -169,12 +169,18 @@ __device__ __forceinline__ uint64_t low_bits(int n)
     return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull;
 }
 
+// kWin: row r of an item is query head r % G of its token r / G, the G heads of
+// a KV head's group together.  A windowed item reads window - 1 + its tokens
+// keys, so 256 rows of one head at a window of 1024 take 10 tiles for 8 tiles'
+// worth of seen keys; 64 tokens of 4 heads take 8.6, and the two row tiles see
+// nearly the same columns.
+//
 // One work item: query rows [256 qt, 256 qt + 256) of chunk c, query head j,
 // as tiles A (first 128 rows) and B (next 128) against the same K/V stream.
 struct Item {
-    int c, j, h;      // chunk, query head, KV head
+    int c, j, h;      // chunk, (first) query head, KV head
     int seq_len;      // prefix + chunk length
-    int rows;         // valid rows of the 256
+    int rows;         // valid rows of the 256 (kWin: tokens of the 256 / heads of a group)
     int row0;         // first q row (token index)
     int pos0;         // absolute position of row 0
     int n_kv;         // 128-key tiles (0: nothing to do)
@@ -210,22 +216,28 @@ __device__ __forceinline__ int64_t key_limit(const PrefillArgs& a)
 // Tiles of the (chunk, 256-row block) pair: the key range row 255 (or the
 // last row) sees; 0 when the block is past the chunk's end or the chunk's
 // metadata is out of range (recorded by make_item).
+// Query rows of an item: 256 rows of one head, or (kWin) as many tokens as
+// make 256 rows with the heads of a group.
+template <bool kWin>
+__device__ __forceinline__ int item_rows(const PrefillArgs& a) { return kWin ? 2 * kBM / (a.hq / a.hkv) : 2 * kBM; }
+
 template <bool kWin>
 __device__ __forceinline__ int pair_tiles(const PrefillArgs& a, int n_qt, int pair)
 {
     const int c = pair / n_qt, qt = pair % n_qt;
     const int q0 = a.cu_q_lens[c], qlen = a.cu_q_lens[c + 1] - q0, P = a.prefix_lens[c];
-    if (qt * 2 * kBM >= qlen) return 0;
+    const int step = item_rows<kWin>(a);
+    if (qt * step >= qlen) return 0;
     if (qlen < 0 || P < 0 || qlen > a.max_q_len || q0 < 0 || q0 + qlen > a.total_q ||
         (int64_t)P + qlen > key_limit<kWin>(a))
         return 0;
-    const int rows = min(2 * kBM, qlen - qt * 2 * kBM);
+    const int rows = min(step, qlen - qt * step);
     if constexpr (kWin) {
         Item it;
-        item_pages(a, P + qt * 2 * kBM, rows, it);
+        item_pages(a, P + qt * step, rows, it);
         return it.n_kv;
     }
-    return (P + qt * 2 * kBM + rows - 1) / kBN + 1;
+    return (P + qt * step + rows - 1) / kBN + 1;
 }
 
 template <bool kWin>
@@ -234,21 +246,22 @@ __device__ __forceinline__ Item make_item(const PrefillArgs& a, int n_qt, int pa
     Item it;
     it.c = pair / n_qt;
     const int qt = pair % n_qt;
-    it.j = j;
-    it.h = j / (a.hq / a.hkv);
+    it.j = kWin ? j * (a.hq / a.hkv) : j;
+    it.h = kWin ? j : j / (a.hq / a.hkv);
     const int q0 = a.cu_q_lens[it.c], qlen = a.cu_q_lens[it.c + 1] - q0, P = a.prefix_lens[it.c];
     it.seq_len = P + qlen;
     it.n_kv = 0;
     it.rows = it.row0 = it.pos0 = 0;
-    if (qt * 2 * kBM >= qlen) return it;  // nothing to do
+    const int step = item_rows<kWin>(a);
+    if (qt * step >= qlen) return it;  // nothing to do
     if (qlen < 0 || P < 0 || qlen > a.max_q_len || q0 < 0 || q0 + qlen > a.total_q ||
         (int64_t)P + qlen > key_limit<kWin>(a)) {
         if (report) record_error(a.status, KVATTN_ERR_BAD_INDEX);
         return it;
     }
-    it.rows = min(2 * kBM, qlen - qt * 2 * kBM);
-    it.row0 = q0 + qt * 2 * kBM;
-    it.pos0 = P + qt * 2 * kBM;
+    it.rows = min(step, qlen - qt * step);
+    it.row0 = q0 + qt * step;
+    it.pos0 = P + qt * step;
     if constexpr (kWin) item_pages(a, it.pos0, it.rows, it);
     else it.n_kv = (it.pos0 + it.rows - 1) / kBN + 1;
     return it;
@@ -336,7 +349,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;  // S_A at +0, S_B at +128, O_A at +256, O_B at +384
-    const int n_items = n_pairs * a.hq;
+    const int lg = kWin ? __ffs(a.hq / a.hkv) - 1 : 0;  // row r of a tile: token r >> lg
+    const int per_pair = kWin ? a.hkv : a.hq;
+    const int n_items = n_pairs * per_pair;
     const int G = gridDim.x, k_cta = blockIdx.x;
     // i-th item of this CTA's sequence (-1 past the end)
     auto item_index = [&](int r) -> int {
@@ -344,8 +359,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         return i < n_items ? i : -1;
     };
     auto item_at = [&](int i, bool report) -> Item {
-        const int pr = i / a.hq;
-        return make_item<kWin>(a, n_qt, sorted ? order[pr] : pr, i % a.hq, report);
+        const int pr = i / per_pair;
+        return make_item<kWin>(a, n_qt, sorted ? order[pr] : pr, i % per_pair, report);
     };
 
     if (warp == 0) {
@@ -373,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int x = 0; x < 2; ++x)
                         for (int p = 0; p < GE::kPanels; ++p)
                             tma_load_3d(smem + kOffQ + x * kTileBytes + p * kPanel, &maps.q, 64 * p, it.j,
-                                        it.row0 + x * kBM, B.q_full, pol_q);
+                                        it.row0 + x * (kBM >> lg), B.q_full, pol_q);
                 }
             }
             go = __shfl_sync(0xffffffffu, go, 0);
@@ -576,8 +591,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t tS = tmem + lane_base + x * 128 + hf * 64;
                     const uint32_t tO = tmem + lane_base + 256 + x * 128 + hf * (kHD / 2);
                     const int col0 = kWin ? it.gap * kPage : 0;      // see item_pages
-                    const int pos_r = it.pos0 + x * kBM + r - col0;  // absolute position of this row (kWin: its column)
-                    const int pos_first = it.pos0 + x * kBM - col0;  // ... of the tile's first row
+                    const int pos_first = it.pos0 + x * (kBM >> lg) - col0;  // absolute position of the tile's first row (kWin: its column)
+                    const int pos_r = pos_first + (r >> lg);                 // ... of this row
                     // keys past the end of the sequence: V rows must be zero (stale
                     // cache slots may hold anything, and 0 * NaN is NaN).  Done in
                     // tile A's phase; PV_B(t) is issued after PV_A(t).
@@ -602,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // that reach beyond the tile's first row can have any)
                         if constexpr (kWin) {
                             const int c = t * kBN + hf * 64;  // this half's first column
-                            const int last = pos_first + kBM - 1;
+                            const int last = pos_first + (kBM >> lg) - 1;
                             if (c + 63 > pos_first || (c <= last - a.window && c + 63 >= a.sinks)) {
                                 // bit e: column c + e is seen
                                 uint64_t m = low_bits(pos_r - c + 1) & (~low_bits(pos_r - a.window - c + 1) | low_bits(a.sinks - c));
@@ -716,13 +731,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int x = 0; x < 2; ++x) {
                 const float l = lsum[x] + lx[((1 - hf) * 2 + x) * 128 + r];
                 const float inv = l > 0.f ? 1.f / l : 0.f;
-                const int row = x * kBM + r;  // row of the 256
+                const int row = (x * kBM + r) >> lg;  // token of the item
                 const uint32_t tO = tmem + lane_base + 256 + x * 128 + hf * (kHD / 2);
                 // this warp's 32 rows all belong to the item: TMA store of a
                 // 32-row x 32-column box per chunk from a 64-byte-swizzled
                 // staging tile (rows past the item's end belong to other
                 // chunks and are never written: plain stores there)
-                const bool full = x * kBM + quarter * 32 + 32 <= it.rows;
+                const int row32 = (x * kBM + quarter * 32) >> lg;  // this warp's first
+                const bool full = row32 + (32 >> lg) <= it.rows;
 #pragma unroll
                 for (int q = 0; q < kHD / 64; ++q) {
                     uint32_t v[32];
@@ -743,12 +759,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         fence_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            tma_store_3d(&maps.o, hf * (kHD / 2) + q * 32, it.j, it.row0 + x * kBM + quarter * 32, stage);
+                            tma_store_3d(&maps.o, hf * (kHD / 2) + q * 32, it.j, it.row0 + row32, stage);
                             bulk_commit_group();
                         }
                     } else if (row < it.rows) {
                         __nv_bfloat16* orow = reinterpret_cast<__nv_bfloat16*>(a.out) +
-                                              ((int64_t)(it.row0 + row) * a.hq + it.j) * kHD + hf * (kHD / 2) + q * 32;
+                                              ((int64_t)(it.row0 + row) * a.hq + it.j + (r & ((1 << lg) - 1))) * kHD +
+                                              hf * (kHD / 2) + q * 32;
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
                             *reinterpret_cast<uint4*>(orow + 8 * c) =
@@ -792,7 +809,7 @@ EncodeTiled encoder()
 }
 
 template <int kHD>
-bool make_maps(const PrefillArgs& a, Maps& m)
+bool make_maps(const PrefillArgs& a, int heads, Maps& m)  // heads: query heads that a row tile holds
 {
     EncodeTiled enc = encoder();
     if (!enc) return false;
@@ -801,12 +818,12 @@ bool make_maps(const PrefillArgs& a, Maps& m)
     {
         const cuuint64_t dims[3] = {(cuuint64_t)kHD, (cuuint64_t)a.hq, (cuuint64_t)a.total_q};
         const cuuint64_t strides[2] = {(cuuint64_t)kHD * 2, (cuuint64_t)a.hq * kHD * 2};
-        const cuuint32_t box[3] = {64, 1, (cuuint32_t)kBM};
+        const cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)(kBM / heads)};
         if (enc(&m.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), dims, strides, box, estr,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return false;
-        const cuuint32_t obox[3] = {32, 1, 32};
+        const cuuint32_t obox[3] = {32, (cuuint32_t)heads, (cuuint32_t)(32 / heads)};
         if (enc(&m.o, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.out, dims, strides, obox, estr,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -912,12 +929,14 @@ kvattn_status launch_prefill_d(const PrefillArgs& a, cudaStream_t s)
 {
     if ((int64_t)a.num_blocks * a.hkv * a.block_size >= ((int64_t)1 << 31)) return KVATTN_ERR_UNSUPPORTED;
     Maps maps;
-    if (!make_maps<kHD>(a, maps)) return KVATTN_ERR_CUDA;
+    const int heads = kWin ? a.hq / a.hkv : 1;
+    if (!make_maps<kHD>(a, heads, maps)) return KVATTN_ERR_CUDA;
     constexpr int kSmem = Geo<kHD>::kSmemBytes;
     static SmemLimit limit;
     if (limit.ensure(reinterpret_cast<const void*>(prefill_kernel<kHD, kWin>), kSmem) != cudaSuccess) return KVATTN_ERR_CUDA;
-    const int n_qt = (a.max_q_len + 2 * kBM - 1) / (2 * kBM);
-    const int64_t items = (int64_t)a.num_chunks * n_qt * a.hq;
+    const int rows = 2 * kBM / heads;
+    const int n_qt = (int)(((int64_t)a.max_q_len + rows - 1) / rows);
+    const int64_t items = (int64_t)a.num_chunks * n_qt * (a.hq / heads);
     if (items <= 0) return KVATTN_OK;
     if (items > 0x7fffffff) return KVATTN_ERR_UNSUPPORTED;
     const int64_t grid = std::min<int64_t>(items, num_sms());  // persistent: one CTA per SM
