@@ -89,8 +89,8 @@ struct Geo {
 };
 
 struct Maps {
-    CUtensorMap q;  // 3-D: (D, Hq, total_q), box (64, 1, 128) (kWin: (64, G, 128 / G))
-    CUtensorMap o;  // 3-D: (D, Hq, total_q), box (32, 1, 32) ((32, G, 32 / G)), 64-byte swizzle (output stores)
+    CUtensorMap q;  // 3-D: (D, Hq, total_q), box (64, 1, 128)
+    CUtensorMap o;  // 3-D: (D, Hq, total_q), box (32, 1, 32), 64-byte swizzle (output stores)
     CUtensorMap k;  // 4-D: (64 columns, 8 rows, 2 panels, rows / 8), box (64, 8, 2, 2)
     CUtensorMap v;
 };
@@ -163,107 +163,53 @@ __device__ __forceinline__ bool elect_one()
     return pred != 0;
 }
 
-// Bits 0 .. n-1 (all for n >= 64, none for n <= 0).
-__device__ __forceinline__ uint64_t low_bits(int n)
-{
-    return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull;
-}
-
-// kWin: row r of an item is query head r % G of its token r / G, the G heads of
-// a KV head's group together.  A windowed item reads window - 1 + its tokens
-// keys, so 256 rows of one head at a window of 1024 take 10 tiles for 8 tiles'
-// worth of seen keys; 64 tokens of 4 heads take 8.6, and the two row tiles see
-// nearly the same columns.
-//
 // One work item: query rows [256 qt, 256 qt + 256) of chunk c, query head j,
 // as tiles A (first 128 rows) and B (next 128) against the same K/V stream.
 struct Item {
-    int c, j, h;      // chunk, (first) query head, KV head
+    int c, j, h;      // chunk, query head, KV head
     int seq_len;      // prefix + chunk length
-    int rows;         // valid rows of the 256 (kWin: tokens of the 256 / heads of a group)
+    int rows;         // valid rows of the 256
     int row0;         // first q row (token index)
     int pos0;         // absolute position of row 0
     int n_kv;         // 128-key tiles (0: nothing to do)
-    int pages, sink_pages, gap;  // windowed attention: see item_pages
 };
-
-// Windowed attention: row p sees keys j <= p with j > p - window or j < sinks.
-// The pages of an item are its sink_pages first ones and those from the page
-// of its first row's first window key on, `gap` pages apart.  Its tiles are cut
-// from that list, so a tile may hold pages of both parts, and key j of the
-// second part is column j - 16 gap of it.  In these columns the row at position
-// p sits at p' = p - 16 gap and sees the columns v <= p' with v > p' - window
-// or v < sinks: with gap > 0 every column of the first part is below the
-// first row's window, and every column of the second is a key past the sinks.
-__device__ __forceinline__ void item_pages(const PrefillArgs& a, int pos0, int rows, Item& it)
-{
-    const int all = (pos0 + rows - 1) / kPage + 1;
-    it.sink_pages = a.sinks > 0 ? min(all, (a.sinks - 1) / kPage + 1) : 0;
-    it.gap = max(0, max(0, pos0 - a.window + 1) / kPage - it.sink_pages);
-    it.pages = all - it.gap;
-    it.n_kv = (it.pages + kBN / kPage - 1) / (kBN / kPage);
-}
-
-// Most keys of a sequence: its table row's, and for the window's column
-// arithmetic in 32 bits (window and sinks are at most this too) 2^30.
-template <bool kWin>
-__device__ __forceinline__ int64_t key_limit(const PrefillArgs& a)
-{
-    const int64_t n = (int64_t)a.max_blocks * a.block_size;
-    return kWin ? min(n, (int64_t)kMaxWindowKeys) : n;
-}
 
 // Tiles of the (chunk, 256-row block) pair: the key range row 255 (or the
 // last row) sees; 0 when the block is past the chunk's end or the chunk's
 // metadata is out of range (recorded by make_item).
-// Query rows of an item: 256 rows of one head, or (kWin) as many tokens as
-// make 256 rows with the heads of a group.
-template <bool kWin>
-__device__ __forceinline__ int item_rows(const PrefillArgs& a) { return kWin ? 2 * kBM / (a.hq / a.hkv) : 2 * kBM; }
-
-template <bool kWin>
 __device__ __forceinline__ int pair_tiles(const PrefillArgs& a, int n_qt, int pair)
 {
     const int c = pair / n_qt, qt = pair % n_qt;
     const int q0 = a.cu_q_lens[c], qlen = a.cu_q_lens[c + 1] - q0, P = a.prefix_lens[c];
-    const int step = item_rows<kWin>(a);
-    if (qt * step >= qlen) return 0;
+    if (qt * 2 * kBM >= qlen) return 0;
     if (qlen < 0 || P < 0 || qlen > a.max_q_len || q0 < 0 || q0 + qlen > a.total_q ||
-        (int64_t)P + qlen > key_limit<kWin>(a))
+        (int64_t)(P + qlen) > (int64_t)a.max_blocks * a.block_size)
         return 0;
-    const int rows = min(step, qlen - qt * step);
-    if constexpr (kWin) {
-        Item it;
-        item_pages(a, P + qt * step, rows, it);
-        return it.n_kv;
-    }
-    return (P + qt * step + rows - 1) / kBN + 1;
+    const int rows = min(2 * kBM, qlen - qt * 2 * kBM);
+    return (P + qt * 2 * kBM + rows - 1) / kBN + 1;
 }
 
-template <bool kWin>
 __device__ __forceinline__ Item make_item(const PrefillArgs& a, int n_qt, int pair, int j, bool report)
 {
     Item it;
     it.c = pair / n_qt;
     const int qt = pair % n_qt;
-    it.j = kWin ? j * (a.hq / a.hkv) : j;
-    it.h = kWin ? j : j / (a.hq / a.hkv);
+    it.j = j;
+    it.h = j / (a.hq / a.hkv);
     const int q0 = a.cu_q_lens[it.c], qlen = a.cu_q_lens[it.c + 1] - q0, P = a.prefix_lens[it.c];
     it.seq_len = P + qlen;
     it.n_kv = 0;
     it.rows = it.row0 = it.pos0 = 0;
-    const int step = item_rows<kWin>(a);
-    if (qt * step >= qlen) return it;  // nothing to do
+    if (qt * 2 * kBM >= qlen) return it;  // nothing to do
     if (qlen < 0 || P < 0 || qlen > a.max_q_len || q0 < 0 || q0 + qlen > a.total_q ||
-        (int64_t)P + qlen > key_limit<kWin>(a)) {
+        (int64_t)it.seq_len > (int64_t)a.max_blocks * a.block_size) {
         if (report) record_error(a.status, KVATTN_ERR_BAD_INDEX);
         return it;
     }
-    it.rows = min(step, qlen - qt * step);
-    it.row0 = q0 + qt * step;
-    it.pos0 = P + qt * step;
-    if constexpr (kWin) item_pages(a, it.pos0, it.rows, it);
-    else it.n_kv = (it.pos0 + it.rows - 1) / kBN + 1;
+    it.rows = min(2 * kBM, qlen - qt * 2 * kBM);
+    it.row0 = q0 + qt * 2 * kBM;
+    it.pos0 = P + qt * 2 * kBM;
+    it.n_kv = (it.pos0 + it.rows - 1) / kBN + 1;
     return it;
 }
 
@@ -276,7 +222,7 @@ __device__ __forceinline__ Item make_item(const PrefillArgs& a, int n_qt, int pa
 // ones without a global counter.  Pipeline state (stages, phases) runs on
 // across items, so the next item's Q, K, V and first S overlap the current
 // item's last tiles and epilogue.
-template <int kHD, bool kWin>
+template <int kHD>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ Maps maps, const int n_qt)
 {
@@ -310,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n_pairs = a.num_chunks * n_qt;
     const bool sorted = n_pairs <= kMaxPairs;
     if (sorted) {
-        for (int i = threadIdx.x; i < n_pairs; i += kThreads) plen[i] = pair_tiles<kWin>(a, n_qt, i);
+        for (int i = threadIdx.x; i < n_pairs; i += kThreads) plen[i] = pair_tiles(a, n_qt, i);
     }
     if (threadIdx.x == 0) {
         mbar_init(B.q_full, 1);
@@ -349,9 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;  // S_A at +0, S_B at +128, O_A at +256, O_B at +384
-    const int lg = kWin ? __ffs(a.hq / a.hkv) - 1 : 0;  // row r of a tile: token r >> lg
-    const int per_pair = kWin ? a.hkv : a.hq;
-    const int n_items = n_pairs * per_pair;
+    const int n_items = n_pairs * a.hq;
     const int G = gridDim.x, k_cta = blockIdx.x;
     // i-th item of this CTA's sequence (-1 past the end)
     auto item_index = [&](int r) -> int {
@@ -359,8 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         return i < n_items ? i : -1;
     };
     auto item_at = [&](int i, bool report) -> Item {
-        const int pr = i / per_pair;
-        return make_item<kWin>(a, n_qt, sorted ? order[pr] : pr, i % per_pair, report);
+        const int pr = i / a.hq;
+        return make_item(a, n_qt, sorted ? order[pr] : pr, i % a.hq, report);
     };
 
     if (warp == 0) {
@@ -388,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int x = 0; x < 2; ++x)
                         for (int p = 0; p < GE::kPanels; ++p)
                             tma_load_3d(smem + kOffQ + x * kTileBytes + p * kPanel, &maps.q, 64 * p, it.j,
-                                        it.row0 + x * (kBM >> lg), B.q_full, pol_q);
+                                        it.row0 + x * kBM, B.q_full, pol_q);
                 }
             }
             go = __shfl_sync(0xffffffffu, go, 0);
@@ -396,16 +340,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++ii;
             const int32_t* trow = a.block_table + (int64_t)it.c * a.max_blocks;
             // lane p < 8 loads the block id of page p of tile t (keys 128t + 16p ..)
-            auto page_key = [&](int t) -> int {
-                const int p = t * (kBN / kPage) + lane;
-                return (kWin && p >= it.sink_pages ? p + it.gap : p) * kPage;
-            };
-            auto has_page = [&](int t) -> bool {
-                if constexpr (kWin) return lane < kBN / kPage && t * (kBN / kPage) + lane < it.pages;
-                return lane < kBN / kPage && t * kBN + lane * kPage < it.seq_len;
-            };
             auto fetch = [&](int t) -> int32_t {
-                return (t < it.n_kv && has_page(t)) ? trow[page_key(t) / a.block_size] : -1;
+                const int key0 = t * kBN + lane * kPage;
+                return (lane < kBN / kPage && t < it.n_kv && key0 < it.seq_len) ? trow[key0 / a.block_size] : -1;
             };
             int32_t blk_next = fetch(0);
             for (int t = 0; t < it.n_kv; ++t, ++g) {
@@ -413,8 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 blk_next = fetch(t + 1);  // in flight while this tile is issued
                 int y = 0;
                 bool have = false;
-                const int key0 = page_key(t);
-                if (has_page(t)) {
+                const int key0 = t * kBN + lane * kPage;
+                if (lane < kBN / kPage && key0 < it.seq_len) {
                     if (blk < 0 || blk >= a.num_blocks) {
                         record_error(a.status, KVATTN_ERR_BAD_INDEX);
                     } else {
@@ -590,19 +527,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int x = 0; x < 2; ++x) {
                     const uint32_t tS = tmem + lane_base + x * 128 + hf * 64;
                     const uint32_t tO = tmem + lane_base + 256 + x * 128 + hf * (kHD / 2);
-                    const int col0 = kWin ? it.gap * kPage : 0;      // see item_pages
-                    const int pos_first = it.pos0 + x * (kBM >> lg) - col0;  // absolute position of the tile's first row (kWin: its column)
-                    const int pos_r = pos_first + (r >> lg);                 // ... of this row
+                    const int pos_r = it.pos0 + x * kBM + r;  // absolute position of this row
+                    const int pos_first = it.pos0 + x * kBM;  // ... of the tile's first row
                     // keys past the end of the sequence: V rows must be zero (stale
                     // cache slots may hold anything, and 0 * NaN is NaN).  Done in
                     // tile A's phase; PV_B(t) is issued after PV_A(t).
-                    // A window's other rows that no row of the item sees (past its
-                    // last row, or before its first row's window and past the
-                    // sinks) likewise.
-                    const int v_end = kWin ? it.pos0 + it.rows - col0 : it.seq_len;  // columns from here on
-                    const int v_low = kWin ? it.pos0 - a.window - col0 : -1;        // columns sinks .. v_low
-                    const bool zero_v = x == 0 && ((t + 1) * kBN > v_end ||
-                                                   (kWin && t * kBN <= v_low && (t + 1) * kBN > a.sinks));
+                    const bool zero_v = x == 0 && (t + 1) * kBN > it.seq_len;
                     bool good = warp_wait(&B.s_full[x], g & 1, abort_flag, a.status);
                     if (good && zero_v)
                         good = warp_wait(&B.v_full[g % kVStages], (g / kVStages) & 1, abort_flag, a.status);
@@ -615,18 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_ld_wait();
                         // causal mask: keys past this row's position (only tiles
                         // that reach beyond the tile's first row can have any)
-                        if constexpr (kWin) {
-                            const int c = t * kBN + hf * 64;  // this half's first column
-                            const int last = pos_first + (kBM >> lg) - 1;
-                            if (c + 63 > pos_first || (c <= last - a.window && c + 63 >= a.sinks)) {
-                                // bit e: column c + e is seen
-                                uint64_t m = low_bits(pos_r - c + 1) & (~low_bits(pos_r - a.window - c + 1) | low_bits(a.sinks - c));
-#pragma unroll
-                                for (int e = 0; e < 64; ++e)
-                                    if (!((e < 32 ? (uint32_t)m : (uint32_t)(m >> 32)) & (1u << (e & 31))))
-                                        sv[e] = __float_as_uint(-INFINITY);
-                            }
-                        } else if (t * kBN + kBN - 1 > pos_first) {
+                        if (t * kBN + kBN - 1 > pos_first) {
                             const int lim = pos_r - t * kBN - hf * 64;  // last visible column of this half
 #pragma unroll
                             for (int e = 0; e < 64; ++e)
@@ -695,8 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     if (zero_v) {
-                        const int v = t * kBN + r;
-                        if (v >= v_end || (kWin && v <= v_low && v >= a.sinks)) {
+                        if (t * kBN + r >= it.seq_len) {
                             // key r's row of the V stage: this half zeroes its kHD bytes
                             unsigned char* vrow = smem + kOffV + (g % kVStages) * kTileBytes + (r >> 3) * kGroup +
                                                   (r & 7) * 128 + hf * (kHD == 128 ? 1024 : 64);
@@ -731,14 +649,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int x = 0; x < 2; ++x) {
                 const float l = lsum[x] + lx[((1 - hf) * 2 + x) * 128 + r];
                 const float inv = l > 0.f ? 1.f / l : 0.f;
-                const int row = (x * kBM + r) >> lg;  // token of the item
+                const int row = x * kBM + r;  // row of the 256
                 const uint32_t tO = tmem + lane_base + 256 + x * 128 + hf * (kHD / 2);
                 // this warp's 32 rows all belong to the item: TMA store of a
                 // 32-row x 32-column box per chunk from a 64-byte-swizzled
                 // staging tile (rows past the item's end belong to other
                 // chunks and are never written: plain stores there)
-                const int row32 = (x * kBM + quarter * 32) >> lg;  // this warp's first
-                const bool full = row32 + (32 >> lg) <= it.rows;
+                const bool full = x * kBM + quarter * 32 + 32 <= it.rows;
 #pragma unroll
                 for (int q = 0; q < kHD / 64; ++q) {
                     uint32_t v[32];
@@ -759,13 +676,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         fence_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            tma_store_3d(&maps.o, hf * (kHD / 2) + q * 32, it.j, it.row0 + row32, stage);
+                            tma_store_3d(&maps.o, hf * (kHD / 2) + q * 32, it.j, it.row0 + x * kBM + quarter * 32, stage);
                             bulk_commit_group();
                         }
                     } else if (row < it.rows) {
                         __nv_bfloat16* orow = reinterpret_cast<__nv_bfloat16*>(a.out) +
-                                              ((int64_t)(it.row0 + row) * a.hq + it.j + (r & ((1 << lg) - 1))) * kHD +
-                                              hf * (kHD / 2) + q * 32;
+                                              ((int64_t)(it.row0 + row) * a.hq + it.j) * kHD + hf * (kHD / 2) + q * 32;
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
                             *reinterpret_cast<uint4*>(orow + 8 * c) =
@@ -809,7 +725,7 @@ EncodeTiled encoder()
 }
 
 template <int kHD>
-bool make_maps(const PrefillArgs& a, int heads, Maps& m)  // heads: query heads that a row tile holds
+bool make_maps(const PrefillArgs& a, Maps& m)
 {
     EncodeTiled enc = encoder();
     if (!enc) return false;
@@ -818,12 +734,12 @@ bool make_maps(const PrefillArgs& a, int heads, Maps& m)  // heads: query heads 
     {
         const cuuint64_t dims[3] = {(cuuint64_t)kHD, (cuuint64_t)a.hq, (cuuint64_t)a.total_q};
         const cuuint64_t strides[2] = {(cuuint64_t)kHD * 2, (cuuint64_t)a.hq * kHD * 2};
-        const cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)(kBM / heads)};
+        const cuuint32_t box[3] = {64, 1, (cuuint32_t)kBM};
         if (enc(&m.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), dims, strides, box, estr,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return false;
-        const cuuint32_t obox[3] = {32, (cuuint32_t)heads, (cuuint32_t)(32 / heads)};
+        const cuuint32_t obox[3] = {32, 1, 32};
         if (enc(&m.o, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.out, dims, strides, obox, estr,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -924,23 +840,21 @@ bool pool_maps(const void* k_pool, const void* v_pool, int64_t rows, bool row_bo
 
 namespace {
 
-template <int kHD, bool kWin>
+template <int kHD>
 kvattn_status launch_prefill_d(const PrefillArgs& a, cudaStream_t s)
 {
     if ((int64_t)a.num_blocks * a.hkv * a.block_size >= ((int64_t)1 << 31)) return KVATTN_ERR_UNSUPPORTED;
     Maps maps;
-    const int heads = kWin ? a.hq / a.hkv : 1;
-    if (!make_maps<kHD>(a, heads, maps)) return KVATTN_ERR_CUDA;
+    if (!make_maps<kHD>(a, maps)) return KVATTN_ERR_CUDA;
     constexpr int kSmem = Geo<kHD>::kSmemBytes;
     static SmemLimit limit;
-    if (limit.ensure(reinterpret_cast<const void*>(prefill_kernel<kHD, kWin>), kSmem) != cudaSuccess) return KVATTN_ERR_CUDA;
-    const int rows = 2 * kBM / heads;
-    const int n_qt = (int)(((int64_t)a.max_q_len + rows - 1) / rows);
-    const int64_t items = (int64_t)a.num_chunks * n_qt * (a.hq / heads);
+    if (limit.ensure(reinterpret_cast<const void*>(prefill_kernel<kHD>), kSmem) != cudaSuccess) return KVATTN_ERR_CUDA;
+    const int n_qt = (a.max_q_len + 2 * kBM - 1) / (2 * kBM);
+    const int64_t items = (int64_t)a.num_chunks * n_qt * a.hq;
     if (items <= 0) return KVATTN_OK;
     if (items > 0x7fffffff) return KVATTN_ERR_UNSUPPORTED;
     const int64_t grid = std::min<int64_t>(items, num_sms());  // persistent: one CTA per SM
-    return cuda_status(launch_pdl(prefill_kernel<kHD, kWin>, dim3((unsigned)grid), dim3(kThreads), kSmem, s, a, maps, n_qt));
+    return cuda_status(launch_pdl(prefill_kernel<kHD>, dim3((unsigned)grid), dim3(kThreads), kSmem, s, a, maps, n_qt));
 }
 
 }  // namespace
@@ -948,16 +862,8 @@ kvattn_status launch_prefill_d(const PrefillArgs& a, cudaStream_t s)
 kvattn_status launch_prefill(const PrefillArgs& a, cudaStream_t s)
 {
     if (a.hq % a.hkv) return KVATTN_ERR_UNSUPPORTED;
-    if (a.d == 128) return launch_prefill_d<128, false>(a, s);
-    if (a.d == 64) return launch_prefill_d<64, false>(a, s);
-    return KVATTN_ERR_UNSUPPORTED;
-}
-
-kvattn_status launch_prefill_window(const PrefillArgs& a, cudaStream_t s)
-{
-    if (a.hq % a.hkv) return KVATTN_ERR_UNSUPPORTED;
-    if (a.d == 128) return launch_prefill_d<128, true>(a, s);
-    if (a.d == 64) return launch_prefill_d<64, true>(a, s);
+    if (a.d == 128) return launch_prefill_d<128>(a, s);
+    if (a.d == 64) return launch_prefill_d<64>(a, s);
     return KVATTN_ERR_UNSUPPORTED;
 }
 
