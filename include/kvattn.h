@@ -538,8 +538,10 @@ kvattn_status kvattn_prefill_chunk_fp8(const kvattn_config* cfg, const kvattn_ca
  *               one is a BAD_INDEX)
  * The other arguments, results and errors as kvattn_prefill_chunk.
  *
- * kvattn_prefill_window_fp8: the same over a kvattn_cache_fp8, attending over
- * the values of kvattn_prefill_chunk_fp8 (head_dim 128).  The pages that a
+ * kvattn_prefill_window_fp8: the same over a kvattn_cache_fp8 (head_dim 128).
+ * K is code * scale rounded to bf16 (q's type), V is code * scale rounded to
+ * f16 over a power of two that is common to the chunk and KV head (within 2^-11
+ * relative, or 2^-40 of the largest seen V of the head).  The pages that a
  * chunk sees are expanded into `workspace`, at least
  * kvattn_prefill_window_fp8_workspace_size(...) bytes (any alignment, any
  * contents, free again once the stream has passed the call), which bounds them

@@ -239,7 +239,9 @@ struct PrefillArgs {
     int32_t hq, hkv, d;
     float scale_log2;
     int* status;
-    int32_t window, sinks;  // launch_prefill_window only
+    // launch_prefill_window only.  v_scale: null, or V is f16 and out its result times v_scale[chunk][KV head]
+    int32_t window, sinks;
+    const float* v_scale;
 };
 kvattn_status launch_prefill(const PrefillArgs& a, cudaStream_t s);
 kvattn_status launch_prefill_window(const PrefillArgs& a, cudaStream_t s);
@@ -260,11 +262,12 @@ kvattn_status launch_prefill_fp8(const PrefillArgs& pa, const void* pool, const 
                                  void* workspace, cudaStream_t s);
 
 // Workspace of the windowed fp8 prefill: each chunk's seen blocks (at most
-// `per_chunk`) expanded to bf16, and their block table.  bytes == 0 for invalid
+// `per_chunk`) expanded to 16 bits, their block table, and the power of two that
+// each (chunk, KV head)'s V was divided by.  bytes == 0 for invalid
 // arguments.
 struct Fp8WindowLayout {
     int64_t per_chunk;
-    size_t off_table, off_k, off_v, bytes;
+    size_t off_vscale, off_table, off_k, off_v, bytes;
 };
 Fp8WindowLayout fp8_window_layout(int32_t hkv, int32_t block_size, int32_t max_blocks, int32_t num_chunks,
                                   int32_t max_q_len, int32_t window, int32_t sinks);

@@ -92,6 +92,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int m, int n, bool b_mn_ma
     return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(m >> 4) << 24);
 }
+// ... with f16 A and B.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n, bool b_mn_major)
+{
+    return idesc_bf16_f32(m, n, b_mn_major) & ~((7u << 7) | (7u << 10));
+}
 
 // Shared-memory matrix descriptor, 128-byte swizzle: start address, leading
 // and stride byte offsets (all >> 4), descriptor version 1 (bit 46), layout

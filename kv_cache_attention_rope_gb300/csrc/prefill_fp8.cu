@@ -54,7 +54,9 @@ struct Fp8PrefillArgs {
     __nv_bfloat16* k_copy;     // [nb][hkv][block_size][128]
     __nv_bfloat16* v_copy;
     int* status;
-    int32_t window, sinks, per_chunk;  // windowed form: copy block c * per_chunk + i is chunk c's i-th seen block
+    // windowed form: copy block c * per_chunk + i is chunk c's i-th seen block; V is copied in f16, divided by v_scale
+    int32_t window, sinks, per_chunk;
+    float* v_scale;            // [num_chunks][hkv], powers of two
 };
 
 // Blocks chunk c's keys occupy; 0 for a chunk the prefill kernel rejects or
@@ -141,25 +143,89 @@ __device__ __forceinline__ void expand4(uint32_t w, float s, uint32_t& o0, uint3
 
 constexpr int kExpandWarps = 8;
 
-// Windowed form: the logical block of chunk c's i-th seen block and the range
-// of its keys that no row sees, or false when the chunk sees fewer blocks.  The
-// rows at prefix .. prefix + qlen - 1 see the keys from low = prefix - window
-// + 1 on and the first `sinks`.
-__device__ __forceinline__ bool seen_block(const Fp8PrefillArgs& a, int c, int i, int& j, int& low, int& total)
+// A warp's copy of a page into shared memory (16-byte asynchronous copies, one
+// commit group).
+__device__ __forceinline__ void fetch_page(unsigned char* buf, const unsigned char* src, int lane)
 {
-    const int all = chunk_blocks(a, c);
-    const int P = a.prefix_lens[c];
-    total = P + a.cu_q_lens[c + 1] - a.cu_q_lens[c];
-    if (all == 0 || total > kMaxWindowKeys) return false;
-    low = max(0, P - a.window + 1);
-    const int lead = a.sinks > 0 ? min(all, (a.sinks - 1) / a.block_size + 1) : 0;
-    j = i < lead ? i : i + max(0, low / a.block_size - lead);
-    return j < all;
+    const uint32_t dst = smem_addr(buf);
+    for (int c = lane; c < kF8Page / 16; c += 32)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16 * c), "l"(src + 16 * c) : "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
-// kWin: the copy's block table is written here, by the lane that has a block's
-// first page, and pages without a seen key are not converted.
-template <bool kWin>
+// A warp's conversion of the page at src (shared memory) to token-major rows:
+// K to bf16, V to bf16 or (kF16V) to f16 times vmul.
+template <bool kF16V>
+__device__ __forceinline__ void convert_page(const unsigned char* src, __nv_bfloat16* kd, __nv_bfloat16* vd, float vmul,
+                                             int lane)
+{
+    const float* scales = reinterpret_cast<const float*>(src + kF8KsOff);
+    // K: lane takes chunk cc (16 dims) of tokens r = lane / 8 + 4 t
+    const int cc = lane & 7;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const int r = (lane >> 3) + 4 * t;
+        const uint4 kw = *reinterpret_cast<const uint4*>(src + r * 128 + 16 * (cc ^ f8_swz(r)));
+        const float ks = scales[r];
+        uint4 o0, o1;
+        expand4(kw.x, ks, o0.x, o0.y);
+        expand4(kw.y, ks, o0.z, o0.w);
+        expand4(kw.z, ks, o1.x, o1.y);
+        expand4(kw.w, ks, o1.z, o1.w);
+        *reinterpret_cast<uint4*>(kd + r * kF8D + 16 * cc) = o0;
+        *reinterpret_cast<uint4*>(kd + r * kF8D + 16 * cc + 8) = o1;
+    }
+    // V: lane takes dims 8 gv .. 8 gv + 7 of tokens 8 hv .. 8 hv + 7
+    const int gv = lane >> 1, hv = lane & 1;
+    uint2 vw[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        vw[k] = *reinterpret_cast<const uint2*>(src + kF8VOff + 16 * (8 * gv + k) + 8 * hv);
+    const float4 vs0 = *reinterpret_cast<const float4*>(src + kF8VsOff + 32 * hv);
+    const float4 vs1 = *reinterpret_cast<const float4*>(src + kF8VsOff + 32 * hv + 16);
+    float vs[8] = {vs0.x, vs0.y, vs0.z, vs0.w, vs1.x, vs1.y, vs1.z, vs1.w};
+    if constexpr (kF16V) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) vs[k] *= vmul;
+    }
+#pragma unroll
+    for (int tt = 0; tt < 8; ++tt) {
+        // token 8 hv + tt: byte tt % 4 of the low (tt < 4) or high word of each dim
+        const uint32_t sel = (uint32_t)(tt & 3) | ((uint32_t)(4 + (tt & 3)) << 4);
+        uint32_t o[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const uint32_t x = tt < 4 ? vw[2 * m].x : vw[2 * m].y;
+            const uint32_t y = tt < 4 ? vw[2 * m + 1].x : vw[2 * m + 1].y;
+            const float2 f = f16x2_to_float2(e4m3x2_to_f16x2(__byte_perm(x, y, sel)));
+            o[m] = kF16V ? pack_f16_rn(f.x * vs[tt], f.y * vs[tt]) : bf16x2_rn(f.x * vs[tt], f.y * vs[tt]);
+        }
+        *reinterpret_cast<uint4*>(vd + (8 * hv + tt) * kF8D + 8 * gv) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+// Windowed form: what chunk c sees.  The rows at prefix .. prefix + qlen - 1 see
+// the keys from `low` = prefix - window + 1 on and the first `sinks`: its first
+// `lead` blocks and those `gap` further on, n in all.
+struct SeenBlocks {
+    int n, lead, gap, low, total;
+    __device__ __forceinline__ int block(int i) const { return i < lead ? i : i + gap; }
+    __device__ __forceinline__ bool key(int k, int sinks) const { return k < total && (k < sinks || k >= low); }
+};
+__device__ __forceinline__ SeenBlocks seen_blocks(const Fp8PrefillArgs& a, int c)
+{
+    SeenBlocks s{0, 0, 0, 0, 0};
+    const int all = chunk_blocks(a, c);
+    const int P = a.prefix_lens[c];
+    s.total = P + a.cu_q_lens[c + 1] - a.cu_q_lens[c];
+    if (all == 0 || s.total > kMaxWindowKeys) return s;
+    s.low = max(0, P - a.window + 1);
+    s.lead = a.sinks > 0 ? min(all, (a.sinks - 1) / a.block_size + 1) : 0;
+    s.gap = max(0, s.low / a.block_size - s.lead);
+    s.n = all - s.gap;
+    return s;
+}
+
 __global__ void __launch_bounds__(kExpandWarps * 32) prefill_fp8_expand(const Fp8PrefillArgs a)
 {
     pdl_wait();
@@ -167,7 +233,7 @@ __global__ void __launch_bounds__(kExpandWarps * 32) prefill_fp8_expand(const Fp
     const int lane = threadIdx.x & 31;
     unsigned char* pbuf = bufs + (threadIdx.x >> 5) * 2 * kF8Page;
     const int ppb = a.block_size / 16;  // pages per block and head
-    const int64_t used = kWin ? a.nb : min(a.first[a.num_chunks], a.nb);
+    const int64_t used = min(a.first[a.num_chunks], a.nb);
     const int64_t pages = used * a.hkv * ppb;
     const int64_t nwarps = (int64_t)gridDim.x * kExpandWarps;
     const int64_t wid = (int64_t)blockIdx.x * kExpandWarps + (threadIdx.x >> 5);
@@ -180,24 +246,10 @@ __global__ void __launch_bounds__(kExpandWarps * 32) prefill_fp8_expand(const Fp
         if (g < end) {
             const int64_t b = g / (a.hkv * ppb);
             const int rem = (int)(g - b * a.hkv * ppb), h = rem / ppb, p = rem - h * ppb;
-            int c, j, total;
-            bool wanted;
-            if constexpr (kWin) {
-                c = (int)(b / a.per_chunk);
-                int low;
-                wanted = seen_block(a, c, (int)(b - (int64_t)c * a.per_chunk), j, low, total);
-                if (wanted && rem == 0) a.ctable[(int64_t)c * a.max_blocks + j] = (int32_t)b;
-                if (wanted) {
-                    const int key0 = j * a.block_size + p * 16;
-                    wanted = key0 < total && (key0 < a.sinks || key0 + 15 >= low);
-                }
-            } else {
-                c = a.owner[b];
-                j = (int)(b - a.first[c]);
-                total = a.prefix_lens[c] + a.cu_q_lens[c + 1] - a.cu_q_lens[c];
-                wanted = j * a.block_size + p * 16 < total;
-            }
-            if (wanted) {
+            const int c = a.owner[b];
+            const int j = (int)(b - a.first[c]);
+            const int total = a.prefix_lens[c] + a.cu_q_lens[c + 1] - a.cu_q_lens[c];
+            if (j * a.block_size + p * 16 < total) {
                 const int32_t blk = a.block_table[(int64_t)c * a.max_blocks + j];
                 if (blk < 0 || blk >= a.num_blocks)
                     record_error(a.status, KVATTN_ERR_BAD_INDEX);
@@ -210,13 +262,10 @@ __global__ void __launch_bounds__(kExpandWarps * 32) prefill_fp8_expand(const Fp
         // asynchronous copies, the next one while the current one converts
         unsigned todo = __ballot_sync(0xffffffffu, my_src != nullptr);
         auto fetch = [&](int i, int bsel) {
-            const unsigned char* src = reinterpret_cast<const unsigned char*>(
-                __shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(my_src), i));
-            const uint32_t dst = smem_addr(pbuf + bsel * kF8Page);
-            for (int c = lane; c < kF8Page / 16; c += 32)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16 * c), "l"(src + 16 * c)
-                             : "memory");
-            asm volatile("cp.async.commit_group;" ::: "memory");
+            fetch_page(pbuf + bsel * kF8Page,
+                       reinterpret_cast<const unsigned char*>(
+                           __shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(my_src), i)),
+                       lane);
         };
         int bsel = 0;
         if (todo) fetch(__ffs(todo) - 1, 0);
@@ -234,48 +283,109 @@ __global__ void __launch_bounds__(kExpandWarps * 32) prefill_fp8_expand(const Fp
             // copy page g0 + i = rows 16 p .. 16 p + 15 of copy block b, head h:
             // [b][h][block_size][128] has them at ((b * hkv + h) * ppb + p) * 16 rows
             const int64_t row0 = (g0 + i) * 16;
-            __nv_bfloat16* kd = a.k_copy + row0 * kF8D;
-            __nv_bfloat16* vd = a.v_copy + row0 * kF8D;
-            const float* scales = reinterpret_cast<const float*>(src + kF8KsOff);
-            // K: lane takes chunk cc (16 dims) of tokens r = lane / 8 + 4 t
-            const int cc = lane & 7;
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int r = (lane >> 3) + 4 * t;
-                const uint4 kw = *reinterpret_cast<const uint4*>(src + r * 128 + 16 * (cc ^ f8_swz(r)));
-                const float ks = scales[r];
-                uint4 o0, o1;
-                expand4(kw.x, ks, o0.x, o0.y);
-                expand4(kw.y, ks, o0.z, o0.w);
-                expand4(kw.z, ks, o1.x, o1.y);
-                expand4(kw.w, ks, o1.z, o1.w);
-                *reinterpret_cast<uint4*>(kd + r * kF8D + 16 * cc) = o0;
-                *reinterpret_cast<uint4*>(kd + r * kF8D + 16 * cc + 8) = o1;
-            }
-            // V: lane takes dims 8 gv .. 8 gv + 7 of tokens 8 hv .. 8 hv + 7
-            const int gv = lane >> 1, hv = lane & 1;
-            uint2 vw[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                vw[k] = *reinterpret_cast<const uint2*>(src + kF8VOff + 16 * (8 * gv + k) + 8 * hv);
-            const float4 vs0 = *reinterpret_cast<const float4*>(src + kF8VsOff + 32 * hv);
-            const float4 vs1 = *reinterpret_cast<const float4*>(src + kF8VsOff + 32 * hv + 16);
-            const float vs[8] = {vs0.x, vs0.y, vs0.z, vs0.w, vs1.x, vs1.y, vs1.z, vs1.w};
-#pragma unroll
-            for (int tt = 0; tt < 8; ++tt) {
-                // token 8 hv + tt: byte tt % 4 of the low (tt < 4) or high word of each dim
-                const uint32_t sel = (uint32_t)(tt & 3) | ((uint32_t)(4 + (tt & 3)) << 4);
-                uint32_t o[4];
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const uint32_t x = tt < 4 ? vw[2 * m].x : vw[2 * m].y;
-                    const uint32_t y = tt < 4 ? vw[2 * m + 1].x : vw[2 * m + 1].y;
-                    const float2 f = f16x2_to_float2(e4m3x2_to_f16x2(__byte_perm(x, y, sel)));
-                    o[m] = bf16x2_rn(f.x * vs[tt], f.y * vs[tt]);
-                }
-                *reinterpret_cast<uint4*>(vd + (8 * hv + tt) * kF8D + 8 * gv) = make_uint4(o[0], o[1], o[2], o[3]);
-            }
+            convert_page<false>(src, a.k_copy + row0 * kF8D, a.v_copy + row0 * kF8D, 1.f, lane);
             __syncwarp();  // buffer bsel is refilled two pages later
+            bsel ^= 1;
+        }
+    }
+}
+
+// Windowed form: `slices` CTAs per (chunk, KV head), each converting a share of
+// the pages that the chunk sees.  V is copied in f16, whose 11 bits hold code *
+// scale eight times more exactly than bf16's 8; it is divided by the power of
+// two that brings the largest seen V value of the chunk and head to 2^14 ..
+// 2^15, and f16 covers 29 binades below that at full precision.  (P, which the
+// MMA takes in V's type, gains as much.)  Every CTA finds that power itself from
+// the scales, 64 of a page's 4224 bytes: a kernel of its own for it took 5 us of
+// a call's 89.  The copy's block table is written here too.
+__global__ void __launch_bounds__(kExpandWarps * 32) prefill_fp8_expand_window(const Fp8PrefillArgs a, const int slices)
+{
+    pdl_wait();
+    extern __shared__ __align__(16) unsigned char bufs[];  // [kExpandWarps][2][kF8Page]
+    __shared__ float wmax[kExpandWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    unsigned char* pbuf = bufs + warp * 2 * kF8Page;
+    const int pair = blockIdx.x / slices, slice = blockIdx.x - pair * slices;
+    const int c = pair / a.hkv, h = pair - c * a.hkv, ppb = a.block_size / 16;
+    const SeenBlocks s = seen_blocks(a, c);
+    const int pages = s.n * ppb;
+    const int32_t* trow = a.block_table + (int64_t)c * a.max_blocks;
+    auto block_id = [&](int j, bool report) -> int {
+        const int32_t blk = trow[j];
+        if (blk >= 0 && blk < a.num_blocks) return blk;
+        if (report) record_error(a.status, KVATTN_ERR_BAD_INDEX);
+        return -1;
+    };
+    auto page_of = [&](int blk, int p) -> const unsigned char* {
+        return a.pool + (((int64_t)blk * a.hkv + h) * ppb + p) * kF8Page;
+    };
+    // this warp's pages: first, first + stride, ...; lane i looks up the i-th of a batch of 32
+    const int first = slice * kExpandWarps + warp, stride = slices * kExpandWarps;
+    const unsigned char* my_src = nullptr;
+    auto lookup = [&](int base) {
+        const int g = first + (base + lane) * stride;
+        my_src = nullptr;
+        if (g < pages) {
+            const int j = s.block(g / ppb), p = g % ppb, key0 = j * a.block_size + p * 16;
+            if (h == 0 && p == 0) a.ctable[(int64_t)c * a.max_blocks + j] = (int32_t)((int64_t)c * a.per_chunk + g / ppb);
+            if (key0 < s.total && (key0 < a.sinks || key0 + 15 >= s.low)) {
+                const int blk = block_id(j, true);
+                if (blk >= 0) my_src = page_of(blk, p);
+            }
+        }
+    };
+    lookup(0);
+    unsigned todo = __ballot_sync(0xffffffffu, my_src != nullptr);
+    auto fetch = [&](int i, int bsel) {
+        fetch_page(pbuf + bsel * kF8Page,
+                   reinterpret_cast<const unsigned char*>(
+                       __shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(my_src), i)),
+                   lane);
+    };
+    if (todo) fetch(__ffs(todo) - 1, 0);  // the first page flies while the largest V is found
+    float m = 0.f;
+    for (int e = tid; e < pages * 4; e += kExpandWarps * 32) {  // 4 tokens each
+        const int j = s.block((e >> 2) / ppb), p = (e >> 2) % ppb;
+        const int key0 = j * a.block_size + p * 16 + (e & 3) * 4;
+        const int blk = block_id(j, false);
+        if (blk < 0) continue;
+        const float4 v = *reinterpret_cast<const float4*>(page_of(blk, p) + kF8VsOff + (e & 3) * 16);
+        const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (s.key(key0 + i, a.sinks)) m = fmaxf(m, f[i]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) wmax[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kExpandWarps; ++i) m = fmaxf(m, wmax[i]);
+    // |code * scale| <= 448 scale < 2^(e + 10), scale's exponent being e
+    const int ex = m > 0.f && m < INFINITY ? min(122, max(-100, ilogbf(m) - 5)) : 0;
+    if (slice == 0 && tid == 0) a.v_scale[pair] = ldexpf(1.f, ex);
+    const float vmul = ldexpf(1.f, -ex);
+    int bsel = 0;
+    for (int base = 0; first + base * stride < pages; base += 32) {
+        if (base > 0) {
+            lookup(base);
+            todo = __ballot_sync(0xffffffffu, my_src != nullptr);
+            if (todo) fetch(__ffs(todo) - 1, bsel);
+        }
+        while (todo) {
+            const int i = __ffs(todo) - 1;
+            todo &= todo - 1;
+            if (todo) {
+                fetch(__ffs(todo) - 1, bsel ^ 1);
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+            } else {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+            }
+            __syncwarp();  // every lane's copies of page i have landed
+            const int g = first + (base + i) * stride;
+            const int64_t row0 = ((((int64_t)c * a.per_chunk + g / ppb) * a.hkv + h) * ppb + g % ppb) * 16;
+            convert_page<true>(pbuf + bsel * kF8Page, a.k_copy + row0 * kF8D, a.v_copy + row0 * kF8D, vmul, lane);
+            __syncwarp();  // the buffer is refilled two pages later
             bsel ^= 1;
         }
     }
@@ -283,15 +393,12 @@ __global__ void __launch_bounds__(kExpandWarps * 32) prefill_fp8_expand(const Fp
 
 constexpr int kExpandSmem = kExpandWarps * 2 * kF8Page;
 
-// One wave of resident CTAs (each warp walks a contiguous range of pages).
-template <bool kWin>
-cudaError_t expand_grid(int* grid)
+// Resident CTAs of an expansion kernel on the whole GPU.
+cudaError_t expand_wave(Residency& residency, const void* kern, int* ctas)
 {
-    static Residency residency;
     int per_sm = 0;
-    const cudaError_t e = residency.query(reinterpret_cast<const void*>(prefill_fp8_expand<kWin>), kExpandWarps * 32,
-                                          kExpandSmem, &per_sm);
-    *grid = num_sms() * per_sm;
+    const cudaError_t e = residency.query(kern, kExpandWarps * 32, kExpandSmem, &per_sm);
+    *ctas = num_sms() * per_sm;
     return e;
 }
 
@@ -361,12 +468,13 @@ kvattn_status launch_prefill_fp8(const PrefillArgs& pa, const void* pool, const 
     a.ctable = reinterpret_cast<int32_t*>(ws + L.off_table);
     a.k_copy = reinterpret_cast<__nv_bfloat16*>(ws + L.off_k);
     a.v_copy = reinterpret_cast<__nv_bfloat16*>(ws + L.off_v);
-    int grid = 0;
-    cudaError_t e = expand_grid<false>(&grid);
+    static Residency residency;
+    int grid = 0;  // one wave (each warp walks a contiguous range of pages)
+    cudaError_t e = expand_wave(residency, reinterpret_cast<const void*>(prefill_fp8_expand), &grid);
     if (e != cudaSuccess) return cuda_status(e);
     e = launch_pdl(prefill_fp8_plan, dim3(1), dim3(1024), 0, s, a);
     if (e != cudaSuccess) return cuda_status(e);
-    e = launch_pdl(prefill_fp8_expand<false>, dim3(grid), dim3(kExpandWarps * 32), kExpandSmem, s, a);
+    e = launch_pdl(prefill_fp8_expand, dim3(grid), dim3(kExpandWarps * 32), kExpandSmem, s, a);
     if (e != cudaSuccess) return cuda_status(e);
     PrefillArgs b = pa;
     b.k_pool = a.k_copy;
@@ -389,6 +497,8 @@ Fp8WindowLayout fp8_window_layout(int32_t hkv, int32_t block_size, int32_t max_b
     const int64_t seen = ((int64_t)sinks + block_size - 1) / block_size + (run + block_size - 2) / block_size + 1;
     L.per_chunk = std::min<int64_t>(max_blocks, seen);
     size_t off = 0;
+    L.off_vscale = off;
+    off = align_up(off + (size_t)num_chunks * hkv * 4);
     L.off_table = off;
     off = align_up(off + (size_t)num_chunks * (size_t)max_blocks * 4);
     const size_t copy = (size_t)num_chunks * (size_t)L.per_chunk * hkv * block_size * kF8D * 2;
@@ -419,16 +529,27 @@ kvattn_status launch_prefill_window_fp8(const PrefillArgs& pa, const void* pool,
     a.ctable = reinterpret_cast<int32_t*>(ws + L.off_table);
     a.k_copy = reinterpret_cast<__nv_bfloat16*>(ws + L.off_k);
     a.v_copy = reinterpret_cast<__nv_bfloat16*>(ws + L.off_v);
-    int grid = 0;
-    cudaError_t e = expand_grid<true>(&grid);
-    if (e == cudaSuccess)
-        e = launch_pdl(prefill_fp8_expand<true>, dim3(grid), dim3(kExpandWarps * 32), kExpandSmem, s, a);
+    a.v_scale = reinterpret_cast<float*>(ws + L.off_vscale);
+    static Residency residency;
+    int wave = 0;
+    cudaError_t e = expand_wave(residency, reinterpret_cast<const void*>(prefill_fp8_expand_window), &wave);
+    if (e != cudaSuccess) return cuda_status(e);
+    // one wave of CTAs, but no warp without a page; two waves, which balance the
+    // SMs better, while a warp keeps two pages (16 chunks of 512 queries, window
+    // 4096: 378 against 392 us with one wave; 8 with 1024: 84 against 82)
+    const int64_t pairs = (int64_t)pa.num_chunks * pa.hkv, pages = L.per_chunk * (pa.block_size / 16);
+    const int64_t one = std::min(wave / pairs, (pages + kExpandWarps - 1) / kExpandWarps);
+    const int64_t two = std::min(2 * wave / pairs, pages / (2 * kExpandWarps));
+    const int64_t slices = std::max<int64_t>(1, std::max(one, two));
+    e = launch_pdl(prefill_fp8_expand_window, dim3((unsigned)(pairs * slices)), dim3(kExpandWarps * 32), kExpandSmem, s, a,
+                   (int)slices);
     if (e != cudaSuccess) return cuda_status(e);
     PrefillArgs b = pa;
     b.k_pool = a.k_copy;
     b.v_pool = a.v_copy;
     b.block_table = a.ctable;
     b.num_blocks = nb;
+    b.v_scale = a.v_scale;
     return launch_prefill_window(b, s);
 }
 

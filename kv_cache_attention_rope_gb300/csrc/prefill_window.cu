@@ -221,7 +221,9 @@ __device__ __forceinline__ bool has_unseen(const PrefillArgs& a, const Unseen& u
 // KV heads innermost.  CTA k takes, in round r, item r G + k for even r and
 // r G + G - 1 - k for odd r (G CTAs).  Pipeline state (stages, phases) runs on
 // across items.
-template <int kHD>
+// kF16V: V (and so P, which the MMA takes in V's type) in f16, scaled per
+// (chunk, KV head): out is multiplied by a.v_scale.
+template <int kHD, bool kF16V>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_window_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ Maps maps, const int n_qt)
 {
@@ -426,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // k-step only adds (byte offset >> 4) to the start-address field, which
             // cannot carry out of it (shared-memory offsets stay below 256 KB).
             constexpr uint32_t idesc_s = idesc_bf16_f32(kBM, kBN, false);
-            constexpr uint32_t idesc_o = idesc_bf16_f32(kBM, kHD, true);
+            constexpr uint32_t idesc_o = kF16V ? idesc_f16_f32(kBM, kHD, true) : idesc_bf16_f32(kBM, kHD, true);
             const uint32_t sbase = smem_addr(smem);
             const uint64_t dQ = umma_desc_sw128(sbase + kOffQ, 16, 1024);      // Q_x: + x * kTileBytes
             const uint64_t dK = umma_desc_sw128(sbase + kOffK, 16, kGroup);    // K stage s: + s * kTileBytes
@@ -659,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint64_t xx =
                         ffma2(pk(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), scale2, msub2);
                     const uint64_t pp = pk(fast_exp2(pk_lo(xx)), fast_exp2(pk_hi(xx)));
-                    pw[e] = pack_bf16_rn(pk_lo(pp), pk_hi(pp));
+                    pw[e] = kF16V ? pack_f16_rn(pk_lo(pp), pk_hi(pp)) : pack_bf16_rn(pk_lo(pp), pk_hi(pp));
                     sum2[e & 1] = fadd2(sum2[e & 1], pp);
                 }
                 tmem_st32(tmem + lane_base + x * 128 + hf * 32, pw);
@@ -708,12 +710,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!warp_wait(&B.l_full[ii & 1], (ii >> 1) & 1, abort_flag, a.status)) break;
             const float* lx = xchg + 512 + (ii & 1) * 512;
             const float l[2] = {lx[r] + lx[256 + r], lx[128 + r] + lx[384 + r]};
+            const float vmul = kF16V ? a.v_scale[(int64_t)w.p.c * a.hkv + w.h] : 1.f;
 #pragma unroll 1
             for (int x = 0; x < 2; ++x) {
                 if (!(ok = warp_wait(&B.o_done[x], ii & 1, abort_flag, a.status))) break;
                 tc_fence_after();
                 const float lr = x ? l[1] : l[0];
-                const float inv = lr > 0.f ? 1.f / lr : 0.f;
+                const float inv = (lr > 0.f ? 1.f / lr : 0.f) * vmul;
                 const int row = (x * kBM + r) >> lg;  // token of the item
                 const uint32_t tO = tmem + lane_base + 256 + x * 128;
                 // this warp's 32 rows all belong to the item: TMA store of a 32-row
@@ -825,7 +828,7 @@ bool make_maps(const PrefillArgs& a, Maps& m)
            encode(&m.v, a.v_pool, 2, pdims, pstrides, pbox, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int kHD>
+template <int kHD, bool kF16V>
 kvattn_status launch(const PrefillArgs& a, cudaStream_t s)
 {
     if ((int64_t)a.num_blocks * a.hkv * a.block_size >= ((int64_t)1 << 31)) return KVATTN_ERR_UNSUPPORTED;
@@ -839,10 +842,10 @@ kvattn_status launch(const PrefillArgs& a, cudaStream_t s)
     constexpr int kSmem = Geo<kHD>::kSmemBytes;
     static_assert(kSmem <= 232448, "shared memory of a block");
     static SmemLimit limit;
-    if (limit.ensure(reinterpret_cast<const void*>(prefill_window_kernel<kHD>), kSmem) != cudaSuccess)
+    if (limit.ensure(reinterpret_cast<const void*>(prefill_window_kernel<kHD, kF16V>), kSmem) != cudaSuccess)
         return KVATTN_ERR_CUDA;
     const int64_t grid = std::min<int64_t>(items, num_sms());  // persistent: one CTA per SM
-    return cuda_status(launch_pdl(prefill_window_kernel<kHD>, dim3((unsigned)grid), dim3(kThreads), kSmem, s, a, maps,
+    return cuda_status(launch_pdl(prefill_window_kernel<kHD, kF16V>, dim3((unsigned)grid), dim3(kThreads), kSmem, s, a, maps,
                                   (int)n_qt));
 }
 
@@ -850,7 +853,8 @@ kvattn_status launch(const PrefillArgs& a, cudaStream_t s)
 
 kvattn_status launch_prefill_window(const PrefillArgs& a, cudaStream_t s)
 {
-    return a.d == 128 ? launch<128>(a, s) : a.d == 64 ? launch<64>(a, s) : KVATTN_ERR_UNSUPPORTED;
+    if (a.v_scale) return a.d == 128 ? launch<128, true>(a, s) : KVATTN_ERR_UNSUPPORTED;
+    return a.d == 128 ? launch<128, false>(a, s) : a.d == 64 ? launch<64, false>(a, s) : KVATTN_ERR_UNSUPPORTED;
 }
 
 }  // namespace kvattn

@@ -122,10 +122,8 @@ def _chunk_case(kv, dtype, hq, hkv, d, chunks, window, sinks, block=16, seed=0, 
     masks = [seen(range(p, p + n), p + n, window, sinks) for p, n in chunks]
     wanted = [m.any(0) if len(m) else np.zeros(L, bool) for m, L in zip(masks, lens)]
     c = WindowCache(kv, dtype, hkv, d, lens, wanted, block=block, seed=seed)
-    if dtype == "fp8":  # the prefill's values: code * scale rounded to fp32 and then to bf16
-        for rows in (c.k, c.v):
-            for i, x in enumerate(rows):
-                rows[i] = torch.from_numpy(x).float().to(torch.bfloat16).double().numpy()
+    if dtype == "fp8":  # the prefill's K: code * scale rounded to fp32 and then to bf16
+        c.k = [torch.from_numpy(x).float().to(torch.bfloat16).double().numpy() for x in c.k]
     cu = np.concatenate([[0], np.cumsum([n for _, n in chunks])]).astype(np.int32)
     q = _q(np.random.default_rng(seed + 1), (int(cu[-1]) + spare_rows, hq, d), dtype)
     cfg = kv.make_config(hq, hkv, d, kv.BF16)
@@ -165,6 +163,31 @@ def test_prefill_masks_fp8(kvattn_lib, window, sinks):
                                                   ("bf16", 4, 4, 128, 1040), ("fp8", 16, 4, 128, 16)])
 def test_prefill_heads_and_blocks(kvattn_lib, dtype, hq, hkv, d, block):
     _prefill(kvattn_lib, dtype, hq, hkv, d, [(700, 290), (0, 77), (64, 1)], 150, 5, step=11, block=block, seed=hq)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -30, 2.0 ** 20])
+def test_prefill_fp8_v_of_any_size(kvattn_lib, scale):
+    """V far outside f16's range, its size differing by head and token."""
+    kv = kvattn_lib
+    lens, window, sinks = [300, 70], 120, 4
+    chunks = [(100, 200), (0, 70)]
+    masks = [seen(range(p, p + n), p + n, window, sinks) for p, n in chunks]
+    c = WindowCache(kv, "fp8", 2, 128, lens, [m.any(0) for m in masks], seed=3)
+    pool = c.cache.pool
+    scales = pool[..., 4160:].contiguous().view(torch.float32)                       # [blocks, heads, 1, 16]
+    times = scale * 2.0 ** torch.tensor([0.0, 7.0], device="cuda")[:, None, None]    # by head ...
+    times = times * 2.0 ** -(torch.arange(16, device="cuda") % 4).float()            # ... and by token
+    pool[..., 4160:] = (scales * times).view(torch.uint8)
+    c.k = [torch.from_numpy(x).float().to(torch.bfloat16).double().numpy() for x in c.k]
+    c.v = [x * times[:, 0].double().cpu().numpy().T[np.arange(len(x)) % 16][:, :, None] for x in c.v]
+    q = _q(np.random.default_rng(1), (270, 8, 128), "bf16")
+    cfg = kv.make_config(8, 2, 128, kv.BF16)
+    out = kv.prefill_window_fp8(cfg, c.cache, q.cuda(), torch.tensor([0, 200, 270], dtype=torch.int32).cuda(),
+                                torch.tensor([100, 0], dtype=torch.int32).cuda(), c.d_table, 200, window, sinks)
+    assert kv.get_device_status() == 0
+    for i, (a, b) in enumerate([(0, 200), (200, 270)]):
+        want, mag = attend(q[a:b].double().numpy(), c.k[i], c.v[i], masks[i])
+        check_attention(f64(out)[a:b], want, mag, "fp8", f"chunk {i}")
 
 
 def test_prefill_more_items_than_processors(kvattn_lib):
