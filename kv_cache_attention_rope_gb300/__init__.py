@@ -149,6 +149,12 @@ def _load():
 
 lib = _load()
 
+try:
+    from . import _marshal
+except ImportError as e:
+    raise ImportError(f"kvattn's extension module is not built ({e}): run "
+                      "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+
 
 def check(code: int, what: str) -> None:
     if code != 0:
@@ -490,13 +496,22 @@ def make_rotary(layout: str = "adjacent", rotary_dim: int = 0, scaling: str = "n
     return Rotary(ROPE_LAYOUT[layout], rotary_dim, ROPE_SCALING[scaling], factor, original_len, low, high, amplitude)
 
 
-# These calls may be a few microseconds of GPU work each, so their marshalling is kept short: one pass over each
-# tensor (type, device, contiguity), pointers as plain integers, the stream's handle without a Stream object.
+# These calls may be a few microseconds of GPU work each, so their marshalling is kept short.  With every buffer given
+# and the current stream, _marshal (csrc/marshal.cpp) checks the tensors and makes the call; it returns None when
+# something is not as it should be, and the functions here then say what, or do the general case.
+
+_marshal_ready = False
+
 
 def _here(stream):
     """Current CUDA device and the raw handle of the stream to use on it."""
+    global _marshal_ready
     torch = _torch()
     device = torch.cuda.current_device()
+    if not _marshal_ready:
+        _marshal.setup(torch.bfloat16, torch.float32, torch.int32, torch._C._cuda_getDevice,
+                       torch._C._cuda_getCurrentRawStream)
+        _marshal_ready = True
     if stream is None:
         return device, torch._C._cuda_getCurrentRawStream(device)
     if stream.device.index != device:
@@ -599,6 +614,10 @@ def rotary_append(cfg: Config, rotary: Rotary, cache: Cache, q, k, v, positions,
                   q_out=None) -> None:
     """kvattn_rotary_append: rotate q in place (or into q_out), write rotated k and raw v into the cache, in the
     rotary form of make_rotary.  q, k, v as for rope_append (dense, or views of a fused QKV output)."""
+    if stream is None:
+        st = _marshal.rotary_append(False, cfg, rotary, cache, q, k, v, positions, seq_ids, block_table, q_out)
+        if st is not None:
+            return check(st, "kvattn_rotary_append")
     _rotary_append(lib.kvattn_rotary_append, "kvattn_rotary_append", Cache, cfg, rotary, cache, q, k, v, positions,
                    seq_ids, block_table, stream, q_out)
 
@@ -606,6 +625,10 @@ def rotary_append(cfg: Config, rotary: Rotary, cache: Cache, q, k, v, positions,
 def rotary_append_fp8(cfg: Config, rotary: Rotary, cache: CacheFP8, q, k, v, positions, seq_ids, block_table,
                       stream=None, q_out=None) -> None:
     """kvattn_rotary_append_fp8: rotary_append into an fp8 cache (bf16 q, k, v)."""
+    if stream is None:
+        st = _marshal.rotary_append(True, cfg, rotary, cache, q, k, v, positions, seq_ids, block_table, q_out)
+        if st is not None:
+            return check(st, "kvattn_rotary_append_fp8")
     _rotary_append(lib.kvattn_rotary_append_fp8, "kvattn_rotary_append_fp8", CacheFP8, cfg, rotary, cache, q, k, v,
                    positions, seq_ids, block_table, stream, q_out)
 
@@ -638,6 +661,12 @@ def decode_window(cfg: Config, cache: Cache, q, block_table, seq_lens, max_seq_l
                   num_sinks: int = 0, out=None, workspace=None, num_splits: int = 0, stream=None):
     """kvattn_decode_window: one query token per sequence against the last `window` cached tokens and the first
     num_sinks.  Table entries of blocks that hold neither may be anything (-1 once they were freed)."""
+    if stream is None and out is not None and workspace is not None:
+        st = _marshal.decode_window(False, cfg, cache, q, block_table, seq_lens, max_seq_len, window, num_sinks,
+                                    num_splits, out, workspace)
+        if st is not None:
+            check(st, "kvattn_decode_window")
+            return out
     return _decode_window(lib.kvattn_decode_window, "kvattn_decode_window", Cache, cfg, cache, q, block_table,
                           seq_lens, max_seq_len, window, num_sinks, out, workspace, num_splits, stream)
 
@@ -645,6 +674,12 @@ def decode_window(cfg: Config, cache: Cache, q, block_table, seq_lens, max_seq_l
 def decode_window_fp8(cfg: Config, cache: CacheFP8, q, block_table, seq_lens, max_seq_len: int, window: int,
                       num_sinks: int = 0, out=None, workspace=None, num_splits: int = 0, stream=None):
     """kvattn_decode_window_fp8: decode_window over an fp8 cache (bf16 q and output)."""
+    if stream is None and out is not None and workspace is not None:
+        st = _marshal.decode_window(True, cfg, cache, q, block_table, seq_lens, max_seq_len, window, num_sinks,
+                                    num_splits, out, workspace)
+        if st is not None:
+            check(st, "kvattn_decode_window_fp8")
+            return out
     return _decode_window(lib.kvattn_decode_window_fp8, "kvattn_decode_window_fp8", CacheFP8, cfg, cache, q,
                           block_table, seq_lens, max_seq_len, window, num_sinks, out, workspace, num_splits, stream)
 
@@ -666,6 +701,12 @@ def prefill_window(cfg: Config, cache: Cache, q, cu_q_lens, prefix_lens, block_t
                    num_sinks: int = 0, out=None, stream=None):
     """kvattn_prefill_window: causal attention of query chunks, each row over its last `window` keys and the first
     num_sinks."""
+    if stream is None and out is not None:
+        st = _marshal.prefill_window(False, cfg, cache, q, cu_q_lens, prefix_lens, block_table, max_q_len, window,
+                                     num_sinks, out, None)
+        if st is not None:
+            check(st, "kvattn_prefill_window")
+            return out
     device, s = _here(stream)
     _, args = _prefill_window_args(Cache, cfg, cache, q, cu_q_lens, prefix_lens, block_table, device)
     out, op = _out(out, q, q.dtype, device)
@@ -683,6 +724,12 @@ def prefill_window_fp8_workspace_size(cfg: Config, block_size: int, max_blocks_p
 def prefill_window_fp8(cfg: Config, cache: CacheFP8, q, cu_q_lens, prefix_lens, block_table, max_q_len: int,
                        window: int, num_sinks: int = 0, out=None, workspace=None, stream=None):
     """kvattn_prefill_window_fp8: prefill_window over an fp8 cache (bf16 q and output)."""
+    if stream is None and out is not None and workspace is not None:
+        st = _marshal.prefill_window(True, cfg, cache, q, cu_q_lens, prefix_lens, block_table, max_q_len, window,
+                                     num_sinks, out, workspace)
+        if st is not None:
+            check(st, "kvattn_prefill_window_fp8")
+            return out
     device, s = _here(stream)
     n, args = _prefill_window_args(CacheFP8, cfg, cache, q, cu_q_lens, prefix_lens, block_table, device)
     out, op = _out(out, q, q.dtype, device)

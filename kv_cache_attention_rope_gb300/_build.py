@@ -11,6 +11,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkvattn.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")  # Python extension module, linked against LIB beside it
 SOURCES = ["api.cu", "rope_append.cu", "rotary.cu", "decode.cu", "decode_window.cu", "decode_direct.cu", "decode_static.cu", "prefill.cu", "prefill_window.cu", "prefill_fp8.cu", "blocks.cu", "allocator.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -72,6 +73,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stderr}")
         os.replace(tmp, LIB)
+    src = os.path.join(CSRC, "marshal.cpp")
+    if force or _stale(MARSHAL, [src, *headers, __file__]):
+        import sysconfig
+
+        tmp = MARSHAL + f".tmp{os.getpid()}"
+        r = subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
+                            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(ROOT, "include"), src, "-o", tmp,
+                            "-L", PKG, "-l:libkvattn.so", "-Wl,-rpath,$ORIGIN"], capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on marshal.cpp:\n{r.stderr}")
+        os.replace(tmp, MARSHAL)
     with open(stamp, "w") as f:
         f.write(arch)
     return LIB

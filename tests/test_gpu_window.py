@@ -340,3 +340,57 @@ def test_captured_calls(kvattn_lib, dtype):
     assert kv.get_device_status() == 0
     assert torch.equal(got[0], a) and torch.equal(got[1], b)
     assert torch.isfinite(a).all() and a.abs().sum() > 0 and b.abs().sum() > 0
+
+
+def test_python_refusals(kvattn_lib):
+    """Arguments that are not what the call takes raise, whichever way they were marshalled, and write nothing."""
+    kv = kvattn_lib
+    c = WindowCache(kv, "bf16", 2, 128, [40], [np.ones(40, bool)], seed=1)
+    c8 = WindowCache(kv, "fp8", 2, 128, [40], [np.ones(40, bool)], seed=1)
+    cfg = kv.make_config(8, 2, 128, kv.BF16)
+    q = _q(np.random.default_rng(0), (1, 8, 128), "bf16").cuda()
+    n = torch.tensor([40], dtype=torch.int32).cuda()
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    out = torch.full_like(q, 5.0)
+    kv.decode_window(cfg, c.cache, q, c.d_table, n, 40, 16, 2, workspace=ws)
+    good = dict(cfg=cfg, cache=c.cache, q=q, block_table=c.d_table, seq_lens=n, max_seq_len=40, window=16, num_sinks=2,
+                out=out, workspace=ws)
+    for bad, error in ((dict(q=q.float()), TypeError), (dict(q=q.cpu()), ValueError), (dict(q=q[:, :4]), ValueError),
+                       (dict(q=q.transpose(1, 2)), ValueError), (dict(seq_lens=n.long()), TypeError),
+                       (dict(seq_lens=torch.cat([n, n])), ValueError), (dict(block_table=c.d_table[:0]), ValueError),
+                       (dict(block_table=c.d_table.cpu()), ValueError), (dict(out=out[:, :4]), ValueError),
+                       (dict(out=out.float()), TypeError), (dict(cache=c8.cache), TypeError),
+                       (dict(cfg=kv.make_config(8, 4, 128, kv.BF16)), ValueError),
+                       (dict(cfg=kv.make_config(8, 2, 128, kv.F32)), TypeError), (dict(window=0), kv.KvattnError),
+                       (dict(num_sinks=-1), kv.KvattnError), (dict(workspace=ws[:16], num_splits=4), kv.KvattnError)):
+        with pytest.raises(error):
+            kv.decode_window(**{**good, **bad})
+    qc = q.expand(3, 8, 128).contiguous()
+    outc = torch.full_like(qc, 5.0)
+    cu = torch.tensor([0, 3], dtype=torch.int32).cuda()
+    pre = dict(cfg=cfg, cache=c.cache, q=qc, cu_q_lens=cu, prefix_lens=n - 3, block_table=c.d_table, max_q_len=3, window=16,
+               num_sinks=2, out=outc)
+    for bad, error in ((dict(q=qc.float()), TypeError), (dict(cu_q_lens=cu[:1]), ValueError),
+                       (dict(prefix_lens=(n - 3).long()), TypeError), (dict(out=outc[:2]), ValueError),
+                       (dict(block_table=c.d_table[:0]), ValueError), (dict(window=-3), kv.KvattnError)):
+        with pytest.raises(error):
+            kv.prefill_window(**{**pre, **bad})
+    with pytest.raises(kv.KvattnError):
+        kv.prefill_window_fp8(**{**pre, "cache": c8.cache}, workspace=ws[:64])
+    k = _q(np.random.default_rng(1), (3, 2, 128), "bf16").cuda()
+    ints = torch.tensor([1, 2, 3], dtype=torch.int32).cuda()
+    app = dict(cfg=cfg, rotary=kv.make_rotary("half"), cache=c.cache, q=qc, k=k, v=k, positions=ints, seq_ids=ints * 0,
+               block_table=c.d_table, q_out=outc)
+    before = c.cache.k_pool.clone()
+    for bad, error in ((dict(q=qc[:2]), ValueError), (dict(k=k.float()), TypeError), (dict(v=k[:, :1]), ValueError),
+                       (dict(positions=ints[:2]), ValueError), (dict(seq_ids=ints.long()), TypeError),
+                       (dict(q_out=outc[:2]), ValueError), (dict(q=qc.cpu()), ValueError), (dict(cache=c8.cache), TypeError),
+                       (dict(rotary=kv.make_rotary("half", 24)), kv.KvattnError)):
+        with pytest.raises(error):
+            kv.rotary_append(**{**app, **bad})
+    torch.cuda.synchronize()
+    assert torch.all(out == 5.0) and torch.all(outc == 5.0)
+    assert torch.equal(torch.nan_to_num(c.cache.k_pool), torch.nan_to_num(before))
+    assert kv.get_device_status() == 0
+    kv.decode_window(**good)
+    assert torch.all(out != 5.0)
