@@ -13,10 +13,9 @@
 //
 // How: the op moves 2 (Hq + 2 Hkv) D elements per token and computes little,
 // so it is bound by HBM.  A unit is two 16-byte vectors of one head whose
-// elements pair up with each other (half) or inside themselves (adjacent):
-// units u < R / (2 kEPV) turn with pairs kEPV u .. kEPV u + kEPV - 1 in either
-// layout, the others are copied.  A thread keeps one unit index and walks the
-// heads, so it reads its kEPV twiddles once per token.
+// elements pair up with each other (half layout), or two vectors that hold their
+// pairs (adjacent); vectors past R are copied.  A thread keeps one unit index and
+// walks the heads, so it reads its twiddles once per token.
 //
 // Rounding.  The speed of a pair is a 64-bit fixed-point count of turns per
 // position, so position * speed mod 2^64 is the angle's fraction of a turn
@@ -49,54 +48,70 @@ __device__ __forceinline__ float2 twiddle(uint64_t u)
     }
 }
 
-// Two vectors of a rotated unit in place: c2[i], s2[i] hold the twiddles of
-// pairs 2i and 2i + 1 of the unit, packed.
-template <bool kBF16, bool kHalf>
-__device__ __forceinline__ void turn(uint4& va, uint4& vb, const uint64_t* c2, const uint64_t* s2)
+// Packed twiddles: c[i], s[i] are the cosines and sines of pairs 2i and 2i + 1.
+template <int kN>
+struct Twiddles {
+    uint64_t c[kN / 2], s[kN / 2];
+    __device__ __forceinline__ void load(const float2* tw)  // kN pairs
+    {
+#pragma unroll
+        for (int i = 0; i < kN / 2; ++i) {
+            const float4 w = *reinterpret_cast<const float4*>(tw + 2 * i);
+            c[i] = pk(w.x, w.z);
+            s[i] = pk(w.y, w.w);
+        }
+    }
+};
+__device__ __forceinline__ void turn2(uint64_t x0, uint64_t x1, uint64_t c, uint64_t s, uint64_t& y0, uint64_t& y1)
+{
+    y0 = ffma2(x1, s ^ 0x8000000080000000ull, fmul2(x0, c));
+    y1 = ffma2(x1, c, fmul2(x0, s));
+}
+
+// Half layout: element e of va pairs with element e of vb.
+template <bool kBF16>
+__device__ __forceinline__ void turn_half(uint4& va, uint4& vb, const uint64_t* c, const uint64_t* s)
 {
     uint32_t* a = reinterpret_cast<uint32_t*>(&va);
     uint32_t* b = reinterpret_cast<uint32_t*>(&vb);
-    const uint64_t neg = 0x8000000080000000ull;
+    uint64_t y0, y1;
     if constexpr (kBF16) {
-        if constexpr (kHalf) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint64_t x0 = pk(bf16lo(a[i]), bf16hi(a[i])), x1 = pk(bf16lo(b[i]), bf16hi(b[i]));
-                const uint64_t y0 = ffma2(x1, s2[i] ^ neg, fmul2(x0, c2[i]));
-                const uint64_t y1 = ffma2(x1, c2[i], fmul2(x0, s2[i]));
-                a[i] = pack_bf16_rn(pk_lo(y0), pk_hi(y0));
-                b[i] = pack_bf16_rn(pk_lo(y1), pk_hi(y1));
-            }
-        } else {
-            // words 2i, 2i + 1 of the unit are its pairs 2i, 2i + 1
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t& w0 = i < 2 ? a[2 * i] : b[2 * i - 4];
-                uint32_t& w1 = i < 2 ? a[2 * i + 1] : b[2 * i - 3];
-                const uint64_t x0 = pk(bf16lo(w0), bf16lo(w1)), x1 = pk(bf16hi(w0), bf16hi(w1));
-                const uint64_t y0 = ffma2(x1, s2[i] ^ neg, fmul2(x0, c2[i]));
-                const uint64_t y1 = ffma2(x1, c2[i], fmul2(x0, s2[i]));
-                w0 = pack_bf16_rn(pk_lo(y0), pk_lo(y1));
-                w1 = pack_bf16_rn(pk_hi(y0), pk_hi(y1));
-            }
+        for (int i = 0; i < 4; ++i) {
+            turn2(pk(bf16lo(a[i]), bf16hi(a[i])), pk(bf16lo(b[i]), bf16hi(b[i])), c[i], s[i], y0, y1);
+            a[i] = pack_bf16_rn(pk_lo(y0), pk_hi(y0));
+            b[i] = pack_bf16_rn(pk_lo(y1), pk_hi(y1));
         }
     } else {
-        float* fa = reinterpret_cast<float*>(&va);
-        float* fb = reinterpret_cast<float*>(&vb);
+        uint64_t* a2 = reinterpret_cast<uint64_t*>(&va);
+        uint64_t* b2 = reinterpret_cast<uint64_t*>(&vb);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {  // pairs 2i, 2i + 1 of the unit
-            float& p0 = kHalf ? fa[2 * i] : (i ? fb[0] : fa[0]);
-            float& p1 = kHalf ? fb[2 * i] : (i ? fb[1] : fa[1]);
-            float& q0 = kHalf ? fa[2 * i + 1] : (i ? fb[2] : fa[2]);
-            float& q1 = kHalf ? fb[2 * i + 1] : (i ? fb[3] : fa[3]);
-            const uint64_t x0 = pk(p0, q0), x1 = pk(p1, q1);
-            const uint64_t y0 = ffma2(x1, s2[i] ^ neg, fmul2(x0, c2[i]));
-            const uint64_t y1 = ffma2(x1, c2[i], fmul2(x0, s2[i]));
-            p0 = pk_lo(y0);
-            q0 = pk_hi(y0);
-            p1 = pk_lo(y1);
-            q1 = pk_hi(y1);
+        for (int i = 0; i < 2; ++i) {
+            turn2(a2[i], b2[i], c[i], s[i], y0, y1);
+            a2[i] = y0;
+            b2[i] = y1;
         }
+    }
+}
+
+// Adjacent layout: the pairs of one vector.
+template <bool kBF16>
+__device__ __forceinline__ void turn_adjacent(uint4& v, const uint64_t* c, const uint64_t* s)
+{
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+    uint64_t y0, y1;
+    if constexpr (kBF16) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            turn2(pk(bf16lo(w[2 * i]), bf16lo(w[2 * i + 1])), pk(bf16hi(w[2 * i]), bf16hi(w[2 * i + 1])), c[i], s[i], y0, y1);
+            w[2 * i] = pack_bf16_rn(pk_lo(y0), pk_lo(y1));
+            w[2 * i + 1] = pack_bf16_rn(pk_hi(y0), pk_hi(y1));
+        }
+    } else {
+        float* f = reinterpret_cast<float*>(&v);
+        turn2(pk(f[0], f[2]), pk(f[1], f[3]), c[0], s[0], y0, y1);
+        v = make_uint4(__float_as_uint(pk_lo(y0)), __float_as_uint(pk_lo(y1)), __float_as_uint(pk_hi(y0)),
+                       __float_as_uint(pk_hi(y1)));
     }
 }
 
@@ -122,25 +137,36 @@ __device__ __forceinline__ uint2 codes8(const uint4& v, float inv)
     return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-// One token per CTA.
-template <bool kBF16, int kD, bool kHalf, bool kFP8>
-__global__ void __launch_bounds__(kThreads) rotary_append_kernel(const __grid_constant__ RotaryArgs a)
+// kTPT threads per token.  Residency: 8 CTAs per SM (7 where the half layout
+// keeps twice the twiddles) at a few spilled bytes beat 5 without: 8320 tokens of
+// 32 / 8 heads at D = 128, half 34.8 against 42.9 us, adjacent 32.8 against 37.5.
+template <bool kBF16, int kD, bool kHalf, bool kFP8, int kTPT>
+__global__ void __launch_bounds__(kThreads, (kHalf ? 7 : 8)) rotary_append_kernel(const __grid_constant__ RotaryArgs a)
 {
     pdl_wait();
     constexpr int kE = kBF16 ? 2 : 4;
     constexpr int kEPV = 16 / kE;              // elements per 16-byte vector
     constexpr int kU = kD / (2 * kEPV);        // units per head
-    constexpr int kGroups = kThreads / kU;     // heads in flight
+    constexpr int kGroups = kTPT / kU;         // heads in flight
     constexpr int kVPH = kD / kEPV;            // vectors per head
     static_assert(!kFP8 || (kBF16 && kD == 128), "fp8 pages hold D = 128 rows quantised from bf16");
-    __shared__ __align__(16) float2 tw[kD / 2];
+    constexpr int kFlightV = kTPT == kThreads ? 1 : 2;
+    static_assert(kGroups >= 1, "a token's threads hold whole heads");
+    __shared__ __align__(16) float2 tws[kThreads / kTPT][kD / 2];
 
-    const int t = blockIdx.x, tid = threadIdx.x;
+    static_assert(kTPT == 32 || kTPT == kThreads, "a token's threads are a warp or the CTA");
+    const int tid = kTPT == kThreads ? (int)threadIdx.x : (int)threadIdx.x % kTPT;  // thread of the token
+    const int t = kTPT == kThreads ? blockIdx.x : blockIdx.x * (kThreads / kTPT) + threadIdx.x / kTPT;
+    if (kTPT != kThreads && t >= a.num_tokens) return;
+    float2* tw = tws[kTPT == kThreads ? 0 : threadIdx.x / kTPT];
     const int u = tid % kU, hg = tid / kU;
-    const bool rot = u < a.rot / (2 * kEPV);
-    // element offsets of the unit's two vectors in a head
-    const int ea = kHalf && rot ? u * kEPV : 2 * u * kEPV;
-    const int eb = kHalf && rot ? a.rot / 2 + u * kEPV : 2 * u * kEPV + kEPV;
+    // element offsets of the unit's two vectors in a head, and whether they turn:
+    // neighbouring units hold neighbouring vectors, so a warp's accesses are whole lines
+    const int nu = a.rot / (2 * kEPV);  // units that turn (half layout)
+    const bool rot_a = kHalf ? u < nu : u * kEPV < a.rot;
+    const bool rot_b = kHalf ? u < nu : (u + kU) * kEPV < a.rot;
+    const int ea = kHalf && !rot_a ? a.rot + (u - nu) * kEPV : u * kEPV;
+    const int eb = !kHalf ? (u + kU) * kEPV : rot_a ? a.rot / 2 + u * kEPV : a.rot + (u - nu + kU - nu) * kEPV;
     const int heads = a.hq + a.hkv;            // q heads, then k heads
     const char* qrow = (const char*)a.q + t * a.q_stride;
     const char* krow = (const char*)a.k + t * a.k_stride;
@@ -152,11 +178,15 @@ __global__ void __launch_bounds__(kThreads) rotary_append_kernel(const __grid_co
         x = *reinterpret_cast<const uint4*>(row + ea * kE);
         y = *reinterpret_cast<const uint4*>(row + eb * kE);
     };
-    uint4 xa[kFlight], xb[kFlight], xv = make_uint4(0, 0, 0, 0);
+    uint4 xa[kFlight], xb[kFlight], xv[kFlightV];
+#pragma unroll
+    for (int i = 0; i < kFlightV; ++i) xv[i] = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < kFlight; ++i)
         if (hg + i * kGroups < heads) load(hg + i * kGroups, xa[i], xb[i]);
-    if (tid < nvec) xv = *reinterpret_cast<const uint4*>(vrow + tid * 16);
+#pragma unroll
+    for (int i = 0; i < kFlightV; ++i)
+        if (tid + i * kTPT < nvec) xv[i] = *reinterpret_cast<const uint4*>(vrow + (tid + i * kTPT) * 16);
 
     const int pos = a.positions[t], seq = a.seq_ids[t];
     bool ok = pos >= 0 && seq >= 0 && seq < a.num_seqs && pos / a.block_size < a.max_blocks;
@@ -170,23 +200,27 @@ __global__ void __launch_bounds__(kThreads) rotary_append_kernel(const __grid_co
         return;
     }
     const int off = pos % a.block_size;
-    if (tid < a.rot / 2) {
-        const float2 w = twiddle((uint64_t)(uint32_t)pos * a.turns[tid]);
-        tw[tid] = make_float2(w.x * a.amplitude, w.y * a.amplitude);
-    }
-    __syncthreads();
-    uint64_t c2[kEPV / 2], s2[kEPV / 2];
 #pragma unroll
-    for (int i = 0; i < kEPV / 2; ++i) {
-        if (rot) {
-            const float4 w = *reinterpret_cast<const float4*>(&tw[u * kEPV + 2 * i]);
-            c2[i] = pk(w.x, w.z);
-            s2[i] = pk(w.y, w.w);
+    for (int i0 = 0; i0 < kD / 2; i0 += kTPT) {
+        const int i = i0 + tid;
+        if (i < a.rot / 2) {
+            const float2 w = twiddle((uint64_t)(uint32_t)pos * a.turns[i]);
+            tw[i] = make_float2(w.x * a.amplitude, w.y * a.amplitude);
         }
     }
+    if constexpr (kTPT == 32) __syncwarp();
+    else __syncthreads();
+    Twiddles<kHalf ? kEPV : kEPV / 2> ta, tb;  // (half: tb unused)
+    if (rot_a) ta.load(&tw[kHalf ? u * kEPV : u * kEPV / 2]);
+    if (!kHalf && rot_b) tb.load(&tw[(u + kU) * kEPV / 2]);
 
     auto finish = [&](int hh, uint4 x, uint4 y) {
-        if (rot) turn<kBF16, kHalf>(x, y, c2, s2);
+        if constexpr (kHalf) {
+            if (rot_a) turn_half<kBF16>(x, y, ta.c, ta.s);
+        } else {
+            if (rot_a) turn_adjacent<kBF16>(x, ta.c, ta.s);
+            if (rot_b) turn_adjacent<kBF16>(y, tb.c, tb.s);
+        }
         if (hh < a.hq) {
             char* row = (char*)a.q_out + t * a.q_out_stride + hh * (kD * kE);
             *reinterpret_cast<uint4*>(row + ea * kE) = x;
@@ -228,18 +262,33 @@ __global__ void __launch_bounds__(kThreads) rotary_append_kernel(const __grid_co
         for (int i = 0; i < kFlight; ++i)
             if (h0 + i * kGroups < heads) finish(h0 + i * kGroups, xa[i], xb[i]);
     }
-    if (tid < nvec) put_v(tid, xv);
-    for (int j = tid + kThreads; j < nvec; j += kThreads) put_v(j, *reinterpret_cast<const uint4*>(vrow + j * 16));
+#pragma unroll
+    for (int i = 0; i < kFlightV; ++i)
+        if (tid + i * kTPT < nvec) put_v(tid + i * kTPT, xv[i]);
+    for (int j = tid + kFlightV * kTPT; j < nvec; j += kTPT)
+        put_v(j, *reinterpret_cast<const uint4*>(vrow + j * 16));
+}
+
+template <bool kBF16, int kD, bool kHalf, bool kFP8>
+kvattn_status launch(const RotaryArgs& a, cudaStream_t s)
+{
+    auto run = [&](auto kern, int tpt) {
+        const int per = kThreads / tpt;
+        return cuda_status(launch_pdl(kern, dim3((a.num_tokens + per - 1) / per), dim3(kThreads), 0, s, a));
+    };
+    // A CTA per token, or a warp when the token is small and there are enough of
+    // them for every SM's warps (8320 tokens, CTA and warp: 32 / 8 heads of 128
+    // 34.8 and 40.1 us; 16 / 8 of 128 32.1 and 27.8; 12 / 12 of 64 17.4 and 12.1;
+    // 64 tokens of those 2.4 and 3.0).
+    const int units = (a.hq + a.hkv) * (kD / (kBF16 ? 16 : 8));
+    return units <= 192 && a.num_tokens >= 2048 ? run(rotary_append_kernel<kBF16, kD, kHalf, kFP8, 32>, 32)
+                                                : run(rotary_append_kernel<kBF16, kD, kHalf, kFP8, 128>, 128);
 }
 
 template <bool kBF16, int kD, bool kFP8>
-kvattn_status launch(const RotaryArgs& a, cudaStream_t s)
+kvattn_status launch_layout(const RotaryArgs& a, cudaStream_t s)
 {
-    const cudaError_t e = a.half ? launch_pdl(rotary_append_kernel<kBF16, kD, true, kFP8>, dim3(a.num_tokens),
-                                              dim3(kThreads), 0, s, a)
-                                 : launch_pdl(rotary_append_kernel<kBF16, kD, false, kFP8>, dim3(a.num_tokens),
-                                              dim3(kThreads), 0, s, a);
-    return cuda_status(e);
+    return a.half ? launch<kBF16, kD, true, kFP8>(a, s) : launch<kBF16, kD, false, kFP8>(a, s);
 }
 
 }  // namespace
@@ -248,11 +297,11 @@ kvattn_status launch_rotary_append(const RotaryArgs& a, cudaStream_t s)
 {
     if (a.fp8) {
         if (a.dtype != KVATTN_BF16 || a.d != 128) return KVATTN_ERR_UNSUPPORTED;
-        return launch<true, 128, true>(a, s);
+        return launch_layout<true, 128, true>(a, s);
     }
     const bool bf16 = a.dtype == KVATTN_BF16;
-    if (a.d == 128) return bf16 ? launch<true, 128, false>(a, s) : launch<false, 128, false>(a, s);
-    if (a.d == 64) return bf16 ? launch<true, 64, false>(a, s) : launch<false, 64, false>(a, s);
+    if (a.d == 128) return bf16 ? launch_layout<true, 128, false>(a, s) : launch_layout<false, 128, false>(a, s);
+    if (a.d == 64) return bf16 ? launch_layout<true, 64, false>(a, s) : launch_layout<false, 64, false>(a, s);
     return KVATTN_ERR_UNSUPPORTED;
 }
 
