@@ -394,3 +394,136 @@ def test_python_refusals(kvattn_lib):
     assert kv.get_device_status() == 0
     kv.decode_window(**good)
     assert torch.all(out != 5.0)
+
+
+def test_prefill_many_chunks(kvattn_lib):
+    """More (chunk, token block) pairs than are ranked in shared memory: 700 chunks of 0 to 3 rows and a long one."""
+    g = np.random.default_rng(31)
+    chunks = [(int(g.integers(0, 90)), int(g.integers(0, 4))) for _ in range(699)] + [(40, 300)]
+    _prefill(kvattn_lib, "bf16", 2, 1, 128, chunks, 33, 2, step=29, seed=7, spare_rows=2)
+
+
+def test_prefill_bad_chunks(kvattn_lib):
+    """Chunks whose metadata is out of range are skipped and recorded; the others are as without them."""
+    kv = kvattn_lib
+    chunks = [(100, 30), (50, 40), (0, 20)]
+    lens = [p + n for p, n in chunks]
+    masks = [seen(range(p, p + n), p + n, 64, 3) for p, n in chunks]
+    c = WindowCache(kv, "bf16", 2, 128, lens, [m.any(0) for m in masks], seed=2)
+    q = _q(np.random.default_rng(3), (90, 8, 128), "bf16")
+    cfg = kv.make_config(8, 2, 128, kv.BF16)
+    cu = torch.tensor([0, 30, 70, 90], dtype=torch.int32).cuda()
+    for prefix, max_q in (([100, -1, 0], 40), ([100, 10 ** 6, 0], 40), ([100, 50, 0], 39)):
+        out = torch.full((90, 8, 128), 9.0, dtype=torch.bfloat16, device="cuda")
+        kv.prefill_window(cfg, c.cache, q.cuda(), cu, torch.tensor(prefix, dtype=torch.int32).cuda(), c.d_table, max_q, 64,
+                          3, out=out)
+        assert kv.get_device_status() == kv.STATUS_CODE["KVATTN_ERR_BAD_INDEX"]
+        got = f64(out)
+        assert np.all(got[30:70] == 9.0)
+        for i, (a, b) in ((0, (0, 30)), (2, (70, 90))):
+            want, mag = attend(q[a:b].double().numpy(), c.k[i], c.v[i], masks[i])
+            check_attention(got[a:b], want, mag, "bf16", f"chunk {i}")
+
+
+def test_streams(kvattn_lib):
+    """The stream argument, and the current stream, with buffers of another one."""
+    kv = kvattn_lib
+    c = WindowCache(kv, "bf16", 2, 128, [500], [np.ones(500, bool)], seed=4)
+    cfg = kv.make_config(8, 2, 128, kv.BF16)
+    q = _q(np.random.default_rng(5), (1, 8, 128), "bf16").cuda()
+    qc = q.expand(7, 8, 128).contiguous()
+    n = torch.tensor([500], dtype=torch.int32).cuda()
+    cu = torch.tensor([0, 7], dtype=torch.int32).cuda()
+    want = kv.decode_window(cfg, c.cache, q, c.d_table, n, 500, 99, 4)
+    want_c = kv.prefill_window(cfg, c.cache, qc, cu, n - 7, c.d_table, 7, 99, 4)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    a = kv.decode_window(cfg, c.cache, q, c.d_table, n, 500, 99, 4, stream=side)
+    b = kv.prefill_window(cfg, c.cache, qc, cu, n - 7, c.d_table, 7, 99, 4, stream=side)
+    with torch.cuda.stream(side):
+        a2 = kv.decode_window(cfg, c.cache, q, c.d_table, n, 500, 99, 4, out=torch.empty_like(q),
+                              workspace=torch.empty(1 << 20, dtype=torch.uint8, device="cuda"))
+    side.synchronize()
+    assert torch.equal(a, want) and torch.equal(a2, want) and torch.equal(b, want_c)
+
+
+@pytest.mark.parametrize("dtype,hkv,d", [("bf16", 8, 128), ("bf16", 8, 64), ("f32", 4, 128)])
+def test_far_into_a_large_pool(kvattn_lib, dtype, hkv, d):
+    """Blocks whose element offsets pass 2^31 (bytes 2^32), written by the append and read by both attentions."""
+    kv = kvattn_lib
+    t = TORCH_DT[dtype]
+    per = hkv * 16 * d
+    blocks = (2 ** 31 + 2 ** 28) // per
+    hq = 4 * hkv
+    cfg = kv.make_config(hq, hkv, d, kv.F32 if dtype == "f32" else kv.BF16)
+    cache = kv.Cache(*(torch.empty((blocks, hkv, 16, d), dtype=t, device="cuda") for _ in range(2)))
+    L = 50
+    table = torch.tensor([[0, blocks - 1, blocks - 3, 2 ** 31 // per + 1]], dtype=torch.int32).cuda()
+    for b in table[0].tolist():
+        cache.k_pool[b] = cache.v_pool[b] = float("nan")
+    g = np.random.default_rng(6)
+    qkv = torch.from_numpy(g.standard_normal((L, (hq + 2 * hkv) * d))).to(t).cuda()
+    q, k, v = kv.split_qkv(qkv, hq, hkv, d)
+    rot = torch.empty((L, hq, d), dtype=t, device="cuda")
+    pos = torch.arange(L, dtype=torch.int32).cuda()
+    kv.rotary_append(cfg, kv.make_rotary("half"), cache, q, k, v, pos, pos * 0, table, q_out=rot)
+    from _window_support import rotate, speeds
+    keys, _ = rotate(f64(k), np.arange(L), speeds(10000.0, d), d, "half", 1.0)
+    keys = torch.from_numpy(keys).to(t).double().numpy()
+    stored = f64(cache.k_pool[table[0].long()[pos.long() // 16], :, pos.long() % 16])
+    assert np.abs(stored - keys).max() <= 2.0 ** (-6 if dtype == "bf16" else -20)   # a step of values below 8
+    mask = seen(range(L), L, 20, 5)
+    n = torch.tensor([L], dtype=torch.int32).cuda()
+    out = kv.decode_window(cfg, cache, rot[-1:].contiguous(), table, n, L, 20, 5)
+    want, mag = attend(f64(rot[-1:]), stored, f64(v), mask[-1:])
+    check_attention(f64(out), want, mag, dtype, "decode")
+    flat = kv.decode_window(cfg, cache, rot[-1:].contiguous(), table, n, L, 20, 5, num_splits=2)
+    check_attention(f64(flat), want, mag, dtype, "decode, split")
+    if dtype == "bf16" and blocks * hkv * 16 < 2 ** 31:
+        out = kv.prefill_window(cfg, cache, rot, torch.tensor([0, L], dtype=torch.int32).cuda(), n * 0, table, L, 20, 5)
+        want, mag = attend(f64(rot), stored, f64(v), mask)
+        check_attention(f64(out), want, mag, dtype, "prefill")
+    assert kv.get_device_status() == 0
+
+
+def test_first_call_in_a_capture(kvattn_lib):
+    """A process whose first calls are captured: what they set up (attributes, tensor maps) is no stream work."""
+    import subprocess
+    import sys
+
+    code = """
+import sys
+sys.path[:0] = [%r, %r]
+import numpy as np, torch, kv_cache_attention_rope_gb300 as kv
+cfg = kv.make_config(8, 2, 128, kv.BF16)
+cache = kv.Cache(*(torch.randn((4, 2, 16, 128), device='cuda').to(torch.bfloat16) for _ in range(2)))
+q = torch.randn((3, 8, 128), device='cuda').to(torch.bfloat16)
+k = torch.randn((3, 2, 128), device='cuda').to(torch.bfloat16)
+table = torch.arange(4, dtype=torch.int32, device='cuda')[None]
+pos = torch.tensor([20, 21, 22], dtype=torch.int32, device='cuda')
+ids, n = pos * 0, torch.tensor([23], dtype=torch.int32, device='cuda')
+cu, prefix = torch.tensor([0, 3], dtype=torch.int32, device='cuda'), torch.tensor([20], dtype=torch.int32, device='cuda')
+rot, a, b = torch.empty_like(q), torch.zeros_like(q[:1]), torch.zeros_like(q)
+ws = torch.empty(1 << 20, dtype=torch.uint8, device='cuda')
+def calls():
+    kv.rotary_append(cfg, kv.make_rotary('half'), cache, q, k, k, pos, ids, table, q_out=rot)
+    kv.decode_window(cfg, cache, rot[2:], table, n, 64, 16, 2, out=a, workspace=ws)
+    kv.decode_window(cfg, cache, rot[2:], table, n, 64, 16, 2, out=a, workspace=ws, num_splits=2)
+    kv.prefill_window(cfg, cache, rot, cu, prefix, table, 3, 16, 2, out=b)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    calls()
+graph.replay()
+torch.cuda.synchronize()
+got = a.clone(), b.clone()
+calls()
+torch.cuda.synchronize()
+assert kv.get_device_status() == 0 and torch.equal(got[0], a) and torch.equal(got[1], b) and a.abs().sum() > 0
+print('captured')
+"""
+    import os
+
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", code % (os.path.dirname(here), here)], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr
