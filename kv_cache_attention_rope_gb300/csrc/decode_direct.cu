@@ -221,13 +221,16 @@ struct Fp8Tile {
     }
 };
 
-// Resident warps per SM that the register budgets leave room for.  Measured
-// (32 / 8 heads, 32 sequences, window 4096; 16, 12 and 8 warps): a bf16 tile
-// at D = 128 wants 200 registers, 100.7, 91.9 and 88.5 us (the first with
-// spills); an fp8 page 168, 70.1, 55.0 and 64.9 us.
+// Resident warps per SM that the register budgets leave room for.  Measured: a
+// bf16 tile at D = 128, with the next one on its way, wants 200 registers (32 / 8
+// heads, 32 sequences, window 4096: 88.5 us with 8 warps, 91.9 with 12, 100.7
+// with 16, which spill); an fp8 page whose K and V are fetched again as soon as
+// they are used 127 (64 / 8 heads, 64 sequences, window 1024: 33.2 us with 16
+// warps, 36.6 with 12; two pages in 168 registers and 12 warps 33.9, three in
+// 237 and 8 warps 36.5).
 constexpr int warps_per_sm(int kind, int d, int g)
 {
-    return kind == kF32Cache ? (d * g > 64 ? 8 : 16) : kind == kFp8Cache ? 12 : d == 64 ? 16 : 8;
+    return kind == kF32Cache ? (d * g > 64 ? 8 : 16) : kind == kFp8Cache || d == 64 ? 16 : 8;
 }
 
 // Shared floats of a CTA: every warp's output and (max, sum) of each head, and
@@ -353,31 +356,32 @@ __global__ void __launch_bounds__(warps_per_sm(kKind, kD, kG) * 32, 1)
         } else {
             const int rk0 = (g4 >> 1) * 4 + (g4 & 1), rk1 = rk0 + 2;
             const char* pool = (const char*)a.k_pool;
-            Fp8Tile t[2];
-            auto fetch = [&](Fp8Tile& d, int64_t row) {
-                if (row < 0) row = 0;  // a bad block: nothing of it is seen
-                const char* pg = pool + row / kTile * kF8Page;
-                d.load_k(pg, rk0, q4);
-                d.load_v(pg, rk0, g4, q4);
-            };
+            Fp8Tile t;
+            // (of a bad block nothing is seen)
+            auto page = [&](int64_t row) { return pool + (row < 0 ? 0 : row) / kTile * kF8Page; };
             int64_t row = __shfl_sync(0xffffffffu, rows, 0);
             uint32_t seen = mine ? seen_of(0, row) : 0u;
-            if (mine) fetch(t[0], row);
-            auto step = [&](int j, Fp8Tile& d, Fp8Tile& next) {
+            const char* pg = page(row);
+            if (mine) {
+                t.load_k(pg, rk0, q4);
+                t.load_v(pg, rk0, g4, q4);
+            }
+            for (int j = 0; j < mine; ++j) {
+                float s[4] = {0.f, 0.f, 0.f, 0.f};
+                t.scores(s, q);
+                const float k0 = t.ks[0] * sl2, k1 = t.ks[1] * sl2;
                 const uint32_t now = seen;
-                if (j + 1 < mine) {  // the next page flies while this one is computed
+                if (j + 1 < mine) {  // the next page's K flies from here, its V from the end of this turn
                     if (((j + 1) & 31) == 0) rows = lookup(j + 1);
                     row = __shfl_sync(0xffffffffu, rows, (j + 1) & 31);
                     seen = seen_of(j + 1, row);
-                    fetch(next, row);
+                    pg = page(row);
+                    t.load_k(pg, rk0, q4);
                 }
-                float s[4] = {0.f, 0.f, 0.f, 0.f};
-                d.scores(s, q);
-                const float k0 = d.ks[0] * sl2, k1 = d.ks[1] * sl2;
                 const bool in0 = now >> rk0 & 1u, in1 = now >> rk1 & 1u;
                 const float x[4] = {in0 ? s[0] * k0 : -INFINITY, in0 ? s[1] * k0 : -INFINITY,
                                     in1 ? s[2] * k1 : -INFINITY, in1 ? s[3] * k1 : -INFINITY};
-                const float sv0 = in0 ? d.vs[0] : 0.f, sv1 = in1 ? d.vs[1] : 0.f;
+                const float sv0 = in0 ? t.vs[0] : 0.f, sv1 = in1 ? t.vs[1] : 0.f;
                 uint32_t vmask = 0xffffffffu;  // the bytes of this lane's words whose tokens are seen
                 if (now != (1u << kTile) - 1u) {
 #pragma unroll
@@ -387,12 +391,9 @@ __global__ void __launch_bounds__(warps_per_sm(kKind, kD, kG) * 32, 1)
                 float p[4];
                 st.template weigh<true>(x, sv0, sv1, p);
                 const float c0 = sv0 * st.vinv, c1 = sv1 * st.vinv;
-                d.add(st.o, movmatrix_trans(pack_f16_rn(p[0] * c0, p[1] * c0)),
+                t.add(st.o, movmatrix_trans(pack_f16_rn(p[0] * c0, p[1] * c0)),
                       movmatrix_trans(pack_f16_rn(p[2] * c1, p[3] * c1)), vmask);
-            };
-            for (int j = 0; j < mine; j += 2) {
-                step(j, t[0], t[1]);
-                if (j + 1 < mine) step(j + 1, t[1], t[0]);
+                if (j + 1 < mine) t.load_v(pg, rk0, g4, q4);
             }
         }
 #pragma unroll
@@ -628,8 +629,8 @@ bool launch_decode_direct(const DecodeArgs& a, int32_t max_tiles, cudaStream_t s
     const int64_t segs = (int64_t)a.batch * a.hkv, tiles = segs * max_tiles;
     // Where the balanced stream of decode_kernel.cuh is faster: long calls of
     // many keys.  Measured (us, this and the stream; thousands of tiles): bf16
-    // D = 128 17 27 / 32, 66 88 / 90, 264 343 / 324; fp8 17 14.5 / 25.8, 66
-    // 55 / 59, 264 200 / 195; fp32 groups of 4 4.2 13.4 / 20.6, 16 49 / 48,
+    // D = 128 17 27 / 32, 66 88 / 90, 264 343 / 324; fp8 17 14.5 / 26.3, 33
+    // 31.4 / 37.9, 264 200 / 195; fp32 groups of 4 4.2 13.4 / 20.6, 16 49 / 48,
     // 66 171 / 160; bf16 D = 64 264 165 / 307 and fp32 without groups 264
     // 574 / 608, so these always come here.
     int64_t most = INT64_MAX;
