@@ -25,11 +25,11 @@
 // row's window, and every column of the second is a key past the sinks.
 //
 // Roles (four warpgroups):
-//  - warp 0: TMA copies of Q tiles and of 128-key K and V tiles, one 4 KB box
-//    per page, straight from the block table; warp 1: the MMAs, in the order
-//    PV_A(t) S_A(t+1) PV_B(t) S_B(t+1), through the items without a gap (tile
-//    t+1 of an item's last is the next item's first); warps 2 and 3: zeros in V
-//    rows that no row sees;
+//  - warp 0: TMA copies of Q tiles and of 128-key K tiles, warp 2 of V tiles,
+//    one 4 KB box per page, straight from the block table; warp 1: the MMAs, in
+//    the order PV_A(t) S_A(t+1) PV_B(t) S_B(t+1), through the items without a
+//    gap (tile t+1 of an item's last is the next item's first); warp 3: zeros in
+//    V rows that no row sees;
 //  - warps 4-7 and 8-11: the softmax of columns 0-63 and 64-127 of whichever
 //    tile is due; P (bf16) overwrites the first half of S in TMEM;
 //  - warps 12-15: O / row sums -> bf16 rows of out, while the others are at
@@ -52,7 +52,8 @@ constexpr int kPage = 16;      // tokens per TMA copy of one block
 constexpr int kThreads = 512;
 constexpr int kStages = 2;     // of K and of V
 constexpr int kPanel = kBM * 128;  // 16 KB: 128 rows x 64 columns (one 128-byte swizzle panel of Q)
-constexpr int kMaxPairs = 512;     // more (chunk, token block) pairs than this: read from global memory, unsorted
+constexpr int kMaxPairs = 512;     // more (chunk, token block) pairs than this are taken unsorted
+constexpr int kMaxChunks = 4 * kMaxPairs - 1;  // of a launch: their pair counts fit where the sorted pairs go
 // Registers per thread of the warpgroups (the block starts with 128 each:
 // 96 + 2 x 168 + 80 = 4 x 128).
 constexpr int kRegsIssue = 96, kRegsSoftmax = 168, kRegsOutput = 80;
@@ -71,15 +72,14 @@ struct Geo {
     static constexpr int kOffV = kOffK + kStages * kTileBytes;
     static constexpr int kOffBar = kOffV + kStages * kTileBytes;
     static constexpr int kOffX = kOffBar + 256;        // fp32: row maxima [2][2][128], row sums of two items [2][2][2][128]
-    static constexpr int kOffPairs = kOffX + 6144;     // sorted pairs
-    static constexpr int kOffStage = (kOffPairs + kMaxPairs * 16 + 1023) / 1024 * 1024;  // two 2 KB boxes per output warp
-    static constexpr int kSmemBytes = kOffStage + 4 * 4096 + 1024;  // + slack to align the base to 1 KB
+    static constexpr int kOffPairs = kOffX + 6144;     // sorted pairs (or `before`)
+    static constexpr int kOffScratch = kOffPairs + kMaxPairs * 16;  // tiles per pair
+    static constexpr int kSmemBytes = kOffScratch + kMaxPairs * 4 + 1024;  // + slack to align the base to 1 KB
     static_assert(kD == 64 || kD == 128, "head dim");
 };
 
 struct Maps {
     CUtensorMap q;  // 3-D: (D, Hq, total_q), box (64, G, 128 / G)
-    CUtensorMap o;  // 3-D: (D, Hq, total_q), box (32, G, 32 / G), 64-byte swizzle (output stores)
     CUtensorMap k;  // 4-D: (64 columns, 8 rows, 2 panels, rows / 8), box (64, 8, 2, 2); D = 64: 2-D, box (64, 16)
     CUtensorMap v;
 };
@@ -98,16 +98,18 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 256, "the barriers fit before the exchange area");
 
+// The flag is looked at only where the wait does not succeed at once: a role
+// that finds its barriers complete runs on after an abort.
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status)
 {
+    if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
     if (*abort_flag) return false;
     if (mbar_wait(bar, parity, status)) return true;
     *abort_flag = 1;
     return false;
 }
 
-// Whole-warp wait: every lane waits, the warp agrees (tcgen05.ld/st that
-// follow are warp-collective, so a partial warp must never reach them).
+// Whole-warp wait: every lane waits, the warp agrees.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status)
 {
     const bool ok = wait_or_abort(bar, parity, abort_flag, status);
@@ -130,18 +132,18 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return r;
 }
 
-// Named barrier `id` over `nthreads` threads that also returns the AND of
-// every participant's `v`.
-__device__ __forceinline__ bool bar_and(int id, int nthreads, bool v)
+// Named barrier `id` over `nthreads` threads.
+__device__ __forceinline__ void bar_sync(int id, int nthreads)
 {
-    uint32_t res;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.and.pred p, %2, %3, q;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(res)
-        : "r"((uint32_t)v), "r"(id), "r"(nthreads)
-        : "memory");
-    return res != 0;
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
+// 32 bytes (a sector) to p, aligned to 32.
+__device__ __forceinline__ void store_256(void* p, const uint32_t* v)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 
 // One lane of the (converged) warp is elected.
@@ -161,29 +163,54 @@ __device__ __forceinline__ uint32_t low_bits(int n)
 }
 
 // A token block of a chunk: rows (tokens) row0 .. row0 + rows - 1 of q, at
-// positions pos0 ..; rows == 0: nothing to do.
+// positions pos0 ...
 struct Pair {
     int row0, pos0, rows, c;
 };
 
-// Pair i: chunk i / n_qt, token block i % n_qt.  Metadata out of range gives
-// no rows (recorded when `report`).
-__device__ __forceinline__ Pair make_pair(const PrefillArgs& a, int n_qt, int step, int i, bool report)
+// Tokens of chunk c; metadata out of range gives none (recorded when `report`).
+__device__ __forceinline__ int chunk_rows(const PrefillArgs& a, int c, bool report)
 {
-    Pair p{0, 0, 0, i / n_qt};
-    const int first = (i - p.c * n_qt) * step;
-    const int q0 = a.cu_q_lens[p.c], qlen = a.cu_q_lens[p.c + 1] - q0, P = a.prefix_lens[p.c];
+    const int q0 = a.cu_q_lens[c], qlen = a.cu_q_lens[c + 1] - q0, P = a.prefix_lens[c];
     if (qlen < 0 || P < 0 || qlen > a.max_q_len || q0 < 0 || (int64_t)q0 + qlen > a.total_q ||
         (int64_t)P + qlen > min((int64_t)a.max_blocks * a.block_size, (int64_t)kMaxWindowKeys)) {
-        if (report && first == 0) record_error(a.status, KVATTN_ERR_BAD_INDEX);
-        return p;
+        if (report) record_error(a.status, KVATTN_ERR_BAD_INDEX);
+        return 0;
     }
-    if (first >= qlen) return p;
-    p.rows = min(step, qlen - first);
-    p.row0 = q0 + first;
-    p.pos0 = P + first;
-    return p;
+    return qlen;
 }
+
+// Pair i of a call: before[c] pairs belong to the chunks before chunk c.
+__device__ __forceinline__ Pair make_pair(const PrefillArgs& a, const int* before, int step, int i)
+{
+    int c = 0;  // the last chunk with before[c] <= i: the one pair i is in
+    for (int n = a.num_chunks; n > 1;) {
+        const int half = n >> 1;
+        if (before[c + half] <= i) c += half;
+        n -= half;
+    }
+    const int first = (i - before[c]) * step;
+    const int q0 = a.cu_q_lens[c];
+    return {q0 + first, a.prefix_lens[c] + first, min(step, a.cu_q_lens[c + 1] - q0 - first), c};
+}
+
+// i / d for 0 <= i < 2^30: with 2^s >= d, m = ceil(2^(30+s) / d) is above
+// 2^(30+s) / d by less than 2^s / d, so i m / 2^(30+s) is above i / d by less
+// than 1 / d.
+struct Divisor {
+    uint32_t m, shift;
+    explicit Divisor(int d)
+    {
+        int s = 0;
+        while ((1 << s) < d) ++s;
+        m = (uint32_t)((((uint64_t)1 << (30 + s)) + d - 1) / d);
+        shift = 30 + s;
+    }
+    __device__ __forceinline__ int quot(int i) const { return (int)(((uint64_t)(uint32_t)i * m) >> shift); }
+};
+struct Divisors {
+    Divisor hkv, block_pages;  // KV heads; 16-token pages of a block
+};
 
 // The pages of a pair (see the top of the file) and its tiles.
 struct Pages {
@@ -191,8 +218,7 @@ struct Pages {
 };
 __device__ __forceinline__ Pages pages_of(const PrefillArgs& a, const Pair& p)
 {
-    Pages g{0, 0, 0, 0};
-    if (p.rows == 0) return g;
+    Pages g;
     const int all = (p.pos0 + p.rows - 1) / kPage + 1;
     g.sink = a.sinks > 0 ? min(all, (a.sinks - 1) / kPage + 1) : 0;
     g.gap = max(0, max(0, p.pos0 - a.window + 1) / kPage - g.sink);
@@ -216,16 +242,17 @@ __device__ __forceinline__ bool has_unseen(const PrefillArgs& a, const Unseen& u
     return (t + 1) * kBN > u.end || (t * kBN <= u.low && (t + 1) * kBN > a.sinks);
 }
 
-// Persistent CTAs.  Items are (pair, KV head) with pairs in descending order
-// of tiles (every CTA ranks them identically in shared memory; ties by index),
-// KV heads innermost.  CTA k takes, in round r, item r G + k for even r and
-// r G + G - 1 - k for odd r (G CTAs).  Pipeline state (stages, phases) runs on
-// across items.
+// Persistent CTAs.  Items are (pair, KV head), KV heads innermost, with up to
+// kMaxPairs pairs in descending order of tiles (every CTA ranks them identically
+// in shared memory; ties by index) and more in the order of their chunks.
+// CTA k takes, in round r, item r G + k for even r and r G + G - 1 - k for odd r
+// (G CTAs).  Pipeline state (stages, phases) runs on across items.
 // kF16V: V (and so P, which the MMA takes in V's type) in f16, scaled per
 // (chunk, KV head): out is multiplied by a.v_scale.
 template <int kHD, bool kF16V>
 __global__ void __launch_bounds__(kThreads, 1)
-    prefill_window_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ Maps maps, const int n_qt)
+    prefill_window_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ Maps maps,
+                          const __grid_constant__ Divisors div)
 {
     pdl_wait();
     using GE = Geo<kHD>;
@@ -236,21 +263,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     Bars& B = *reinterpret_cast<Bars*>(smem + GE::kOffBar);
     volatile int* abort_flag = &B.abort_flag;
     Pair* sorted_pairs = reinterpret_cast<Pair*>(smem + GE::kOffPairs);
-    int* plen = reinterpret_cast<int*>(smem + GE::kOffStage);  // tiles per pair, before the staging boxes are used
+    int* before = reinterpret_cast<int*>(smem + GE::kOffPairs);
+    int* scratch = reinterpret_cast<int*>(smem + GE::kOffScratch);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int lg = __ffs(a.hq / a.hkv) - 1;  // row r of a tile: token r >> lg, head r & (G - 1)
     const int step = 2 * kBM >> lg;          // tokens of an item
-    const int n_pairs = a.num_chunks * n_qt;
-    const bool sorted = n_pairs <= kMaxPairs;
-    Pair mine{0, 0, 0, 0};
-    int my_tiles = 0;
-    static_assert(kMaxPairs <= kThreads, "a thread ranks one pair");
-    if (sorted && (int)threadIdx.x < n_pairs) {
-        mine = make_pair(a, n_qt, step, threadIdx.x, blockIdx.x == 0);
-        my_tiles = pages_of(a, mine).tiles;
-        plen[threadIdx.x] = my_tiles;
+    // before[c]: a thread counts up to four neighbouring chunks, then a scan
+    const int per = (a.num_chunks + kThreads - 1) / kThreads;
+    int counts[4], sum = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int c = (int)threadIdx.x * per + j;
+        counts[j] = sum;
+        if (j < per && c < a.num_chunks) sum += (chunk_rows(a, c, blockIdx.x == 0) + step - 1) / step;
     }
+    int upto = sum;  // of the warp's lanes up to this one
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int s = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += s;
+    }
+    if (lane == 31) scratch[warp] = upto;
     if (threadIdx.x == 0) {
         for (int x = 0; x < 2; ++x) {
             mbar_init(&B.q_full[x], 1);
@@ -274,56 +308,74 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == 1) tmem_alloc(&B.tmem, 512);
     __syncthreads();
-    if (sorted && (int)threadIdx.x < n_pairs) {  // rank = pairs with more tiles, or as many and a smaller index
-        int rank = 0;
-        for (int q = 0; q < n_pairs; ++q) {
-            const int lq = plen[q];
-            rank += (lq > my_tiles) || (lq == my_tiles && q < (int)threadIdx.x);
+    int n_pairs = 0, base = upto - sum;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) {
+        if (i == warp) base += n_pairs;
+        n_pairs += scratch[i];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int c = (int)threadIdx.x * per + j;
+        if (j < per && c < a.num_chunks) before[c] = base + counts[j];
+    }
+    __syncthreads();
+    const bool sorted = n_pairs <= kMaxPairs;
+    static_assert(kMaxPairs <= kThreads, "a thread ranks one pair");
+    if (sorted) {
+        Pair mine{0, 0, 0, 0};
+        int my_tiles = 0;
+        if ((int)threadIdx.x < n_pairs) {
+            mine = make_pair(a, before, step, threadIdx.x);
+            my_tiles = pages_of(a, mine).tiles;
+            scratch[threadIdx.x] = my_tiles;
         }
-        sorted_pairs[rank] = mine;
+        __syncthreads();
+        if ((int)threadIdx.x < n_pairs) {  // rank = pairs with more tiles, or as many and a smaller index
+            int rank = 0;
+            for (int q = 0; q < n_pairs; ++q) {
+                const int lq = scratch[q];
+                rank += (lq > my_tiles) || (lq == my_tiles && q < (int)threadIdx.x);
+            }
+            sorted_pairs[rank] = mine;
+        }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = B.tmem;  // S_A at +0, S_B at +128, O_A at +256, O_B at +384
     const int n_items = n_pairs * a.hkv;
-    // Walks this CTA's items with work.
+    // Walks this CTA's items.
     struct Walk {
         int round = 0;
         int h;
         Pair p;
         Pages g;
     };
-    auto next_item = [&](Walk& w, bool report) -> bool {
-        for (;; ++w.round) {
-            const int i = w.round * (int)gridDim.x + ((w.round & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
-            if (i >= n_items) return false;
-            const int pr = i / a.hkv;
-            w.h = i - pr * a.hkv;
-            w.p = sorted ? sorted_pairs[pr] : make_pair(a, n_qt, step, pr, report);
-            if (w.p.rows == 0) continue;
-            w.g = pages_of(a, w.p);
-            ++w.round;
-            return true;
-        }
+    auto next_item = [&](Walk& w) -> bool {
+        const int i = w.round * (int)gridDim.x + ((w.round & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
+        if (i >= n_items) return false;
+        const int pr = div.hkv.quot(i);
+        w.h = i - pr * a.hkv;
+        w.p = sorted ? sorted_pairs[pr] : make_pair(a, before, step, pr);
+        w.g = pages_of(a, w.p);
+        ++w.round;
+        return true;
     };
 
     if (warp < 4) {
         setmaxnreg_dec<kRegsIssue>();
-        if (warp == 0) {
-            // ============================= TMA producer =============================
+        if (warp == 0 || warp == 2) {
+            // ====================== TMA producers: K and Q, V ======================
+            // Warp 0 copies K tiles and Q, warp 2 V tiles: neither waits behind the
+            // other's buffers.
             const uint64_t pol_q = l2_evict_first_policy();
             const uint64_t pol_kv = l2_evict_normal_policy();
+            const bool is_k = warp == 0;
             if (lane == 0) {
-                tma_prefetch_map(&maps.q);
-                tma_prefetch_map(&maps.k);
-                tma_prefetch_map(&maps.v);
+                if (is_k) tma_prefetch_map(&maps.q);
+                tma_prefetch_map(is_k ? &maps.k : &maps.v);
             }
-            int g = 0, ii = 0;            // tiles and items started so far (this CTA)
-            int kg = 0, qg = 0;           // K and Q tiles (A then B, item by item) armed
-            // bit s of stage s's V: armed; its last copies complete on v_raw (else on
-            // v_full), in a phase of this parity; parity of its tiles that did so far
-            uint32_t v_armed = 0, v_raw = 0, v_parity = 0, fixes = 0;
             bool go = true;
             // lane 0 waits for `empty` (unless the buffer is new) and arms `full`
             auto arm = [&](uint64_t* full, uint64_t* empty, bool fresh, uint32_t parity, uint32_t bytes) -> bool {
@@ -333,56 +385,66 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 return go = __shfl_sync(0xffffffffu, go, 0);
             };
-            // lane p < 8: page p of tile t
-            auto page_key = [&](const Walk& w, int t) -> int {
+            // Lane p < 8 copies page p of a tile.  Its block's id, from the table a
+            // tile ahead: nothing of the load's result is looked at until then (lanes
+            // without a page read their row's first entry).
+            auto has_page = [&](const Pages& pg, int t) -> bool {
+                return lane < kBN / kPage && t * (kBN / kPage) + lane < pg.n;
+            };
+            auto page = [&](const Pages& pg, int t) -> int {
                 const int p = t * (kBN / kPage) + lane;
-                return (p >= w.g.sink ? p + w.g.gap : p) * kPage;
+                return p >= pg.sink ? p + pg.gap : p;
             };
-            auto has_page = [&](const Walk& w, int t) -> bool {
-                return lane < kBN / kPage && t * (kBN / kPage) + lane < w.g.n;
+            auto block_id = [&](const Walk& w, int t) -> int32_t {
+                const int col = has_page(w.g, t) ? div.block_pages.quot(page(w.g, t)) : 0;
+                return a.block_table[(int64_t)w.p.c * a.max_blocks + col];
             };
-            auto fetch = [&](const Walk& w, int t) -> int32_t {
-                return has_page(w, t) ? a.block_table[(int64_t)w.p.c * a.max_blocks + page_key(w, t) / a.block_size] : -1;
+            // The pool row of this lane's page, or -1.
+            auto page_row = [&](const Walk& w, int t, int32_t blk) -> int {
+                if (!has_page(w.g, t)) return -1;
+                if (blk < 0 || blk >= a.num_blocks) {
+                    if (is_k) record_error(a.status, KVATTN_ERR_BAD_INDEX);
+                    return -1;
+                }
+                const int pg = page(w.g, t), in = pg * kPage - div.block_pages.quot(pg) * a.block_size;
+                return (int)(((int64_t)blk * a.hkv + w.h) * a.block_size) + in;
             };
+            auto copy = [&](const CUtensorMap* m, unsigned char* tile, int row, uint64_t* full) {
+                if (row < 0) return;
+                if constexpr (kHD == 128)
+                    tma_load_4d(tile + lane * kPageBytes, m, 0, 0, 0, row >> 3, full, pol_kv);
+                else
+                    tma_load_2d(tile + lane * kPageBytes, m, 0, row, full, pol_kv);
+            };
+            int g = 0, ii = 0;     // tiles and items started so far (this CTA)
+            int kg = 0, qg = 0;    // K and Q tiles (A then B, item by item) armed
+            // bit s of stage s's V: armed; its last copies complete on v_raw (else on
+            // v_full), in a phase of this parity; parity of its tiles that did so far
+            uint32_t v_armed = 0, v_raw = 0, v_parity = 0, fixes = 0;
             Walk w, ahead;  // this item and the next
-            bool more = next_item(ahead, lane == 0);
-            int32_t blk_next = more ? fetch(ahead, 0) : -1;
+            bool more = next_item(ahead);
+            int32_t blk_next = more ? block_id(ahead, 0) : 0;
             while (go && more) {
                 w = ahead;
-                more = next_item(ahead, lane == 0);
-                const Unseen un = unseen_of(a, w.p, w.g);
                 for (int t = 0; t < w.g.tiles; ++t, ++g) {
-                    const int32_t blk = blk_next;
-                    // block ids of the next tile in flight while this one is issued
-                    blk_next = t + 1 < w.g.tiles ? fetch(w, t + 1) : more ? fetch(ahead, 0) : -1;
-                    int y = 0;
-                    bool have = has_page(w, t);
-                    if (have) {
-                        if (blk < 0 || blk >= a.num_blocks) {
-                            record_error(a.status, KVATTN_ERR_BAD_INDEX);
-                            have = false;
-                        } else {
-                            y = (int)(((int64_t)blk * a.hkv + w.h) * a.block_size + page_key(w, t) % a.block_size);
-                        }
-                    }
-                    const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, have)) * (uint32_t)kPageBytes;
+                    const int row = page_row(w, t, blk_next);
+                    const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, row >= 0)) * (uint32_t)kPageBytes;
                     const int s = g % kStages;
                     const uint32_t parity = ((g / kStages) - 1) & 1;
-                    // K stage: free once S_A and S_B of tile g - kStages are done
-                    if (!arm(&B.k_full[s], &B.k_empty[s], g < kStages, parity, bytes)) break;
-                    if (have) {
-                        if constexpr (kHD == 128)
-                            tma_load_4d(smem + kOffK + s * kTileBytes + lane * kPageBytes, &maps.k, 0, 0, 0, y >> 3,
-                                        &B.k_full[s], pol_kv);
-                        else
-                            tma_load_2d(smem + kOffK + s * kTileBytes + lane * kPageBytes, &maps.k, 0, y, &B.k_full[s],
-                                        pol_kv);
+                    if (is_k) {
+                        // K stage: free once S_A and S_B of tile g - kStages are done
+                        if (!arm(&B.k_full[s], &B.k_empty[s], g < kStages, parity, bytes)) break;
+                        copy(&maps.k, smem + kOffK + s * kTileBytes, row, &B.k_full[s]);
+                        kg = g + 1;
                     }
-                    kg = g + 1;
-                    if (t == 0) {
+                    if (t == 0) more = next_item(ahead);
+                    const bool last = t + 1 == w.g.tiles;
+                    blk_next = block_id(last ? ahead : w, last ? 0 : t + 1);
+                    if (is_k) {
+                        if (t > 0) continue;
                         // Q_x: free once every S_x MMA of the previous item is done (its
                         // K stage is free sooner, so K goes first)
-                        for (int x = 0; go && x < 2; ++x) {
+                        for (int x = 0; x < 2; ++x) {
                             if (!arm(&B.q_full[x], &B.q_empty[x], ii == 0, (ii - 1) & 1, kTileBytes)) break;
                             if (lane < GE::kPanels)
                                 tma_load_3d(smem + kOffQ + x * kTileBytes + lane * kPanel, &maps.q, 64 * lane, w.h << lg,
@@ -391,24 +453,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         if (!go) break;
                         ++ii;
+                    } else {
+                        // V stage: free once PV_A and PV_B of tile g - kStages are done
+                        const bool fix = has_unseen(a, unseen_of(a, w.p, w.g), t);
+                        uint64_t* full = fix ? &B.v_raw[s] : &B.v_full[s];
+                        if (!arm(full, &B.v_empty[s], g < kStages, parity, bytes)) break;
+                        copy(&maps.v, smem + kOffV + s * kTileBytes, row, full);
+                        const uint32_t phase = fix ? fixes >> s & 1u : (g / kStages) & 1u;
+                        const uint32_t bit = 1u << s;
+                        v_armed |= bit;
+                        v_raw = fix ? v_raw | bit : v_raw & ~bit;
+                        v_parity = phase ? v_parity | bit : v_parity & ~bit;
+                        if (fix) fixes ^= bit;
                     }
-                    // V stage: free once PV_A and PV_B of tile g - kStages are done
-                    const bool fix = has_unseen(a, un, t);
-                    uint64_t* full = fix ? &B.v_raw[s] : &B.v_full[s];
-                    if (!arm(full, &B.v_empty[s], g < kStages, parity, bytes)) break;
-                    if (have) {
-                        if constexpr (kHD == 128)
-                            tma_load_4d(smem + kOffV + s * kTileBytes + lane * kPageBytes, &maps.v, 0, 0, 0, y >> 3, full,
-                                        pol_kv);
-                        else
-                            tma_load_2d(smem + kOffV + s * kTileBytes + lane * kPageBytes, &maps.v, 0, y, full, pol_kv);
-                    }
-                    const uint32_t phase = fix ? fixes >> s & 1u : (g / kStages) & 1u;
-                    const uint32_t bit = 1u << s;
-                    v_armed |= bit;
-                    v_raw = fix ? v_raw | bit : v_raw & ~bit;
-                    v_parity = phase ? v_parity | bit : v_parity & ~bit;
-                    if (fix) fixes ^= bit;
                 }
             }
             // After an abort, let every armed copy land before the CTA can exit.
@@ -469,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // overwrites S_x's columns after PV_x(t) has read P_x(t) from them
             // (tensor operations of one thread run in issue order).
             Walk w;
-            int n_kv = next_item(w, false) ? w.g.tiles : 0;
+            int n_kv = next_item(w) ? w.g.tiles : 0;
             int g = 0, item = 0;
             bool ok = n_kv > 0;
             if (ok && (ok = wait(&B.q_full[0], 0) && wait(&B.k_full[0], 0))) {
@@ -505,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!ok) break;
                 // the item's last tile, and the next item's first S
-                const int n_next = next_item(w, false) ? w.g.tiles : 0;
+                const int n_next = next_item(w) ? w.g.tiles : 0;
                 const int g1 = g + 1;
                 if (!(ok = wait(&B.v_full[g % kStages], (g / kStages) & 1) && wait(&B.p_full[0], g & 1))) break;
                 if (n_kv == 1 && item > 0 && !(ok = wait(&B.o_free[0], op))) break;
@@ -540,32 +597,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ============================ stale V rows =============================
             // V rows that no row of the item sees must be zero for the MMA: they
             // may hold anything, and 0 * NaN is NaN.
-            // The copies of such a tile complete on v_raw, and these warps complete
+            // The copies of such a tile complete on v_raw, and this warp completes
             // v_full.
-            const int th = (warp - 2) * 32 + lane;
             int g = 0;
             uint32_t fixes = 0;  // bit s: parity of stage s's tiles seen here so far
             bool ok = true;
             Walk w;
-            while (ok && next_item(w, false)) {
+            while (ok && next_item(w)) {
                 const Unseen un = unseen_of(a, w.p, w.g);
                 for (int t = 0; t < w.g.tiles; ++t, ++g) {
                     if (!has_unseen(a, un, t)) continue;
                     const int s = g % kStages;
-                    ok = warp_wait(&B.v_raw[s], fixes >> s & 1u, abort_flag, a.status);
+                    if (!(ok = warp_wait(&B.v_raw[s], fixes >> s & 1u, abort_flag, a.status))) break;
                     fixes ^= 1u << s;
-                    if (ok) {  // two threads a row, 16-byte chunks of both panels in turn
-                        for (int r = th >> 1; r < kBN; r += 32) {
-                            const int v = t * kBN + r;
-                            if (v < un.end && (v > un.low || v < a.sinks)) continue;
-                            unsigned char* row = smem + kOffV + s * kTileBytes + (r >> 3) * kGroup + (r & 7) * 128;
-                            for (int ch = th & 1; ch < kHD / 8; ch += 2)
-                                *reinterpret_cast<uint4*>(row + (ch >> 3) * 1024 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    unsigned char* tile = smem + kOffV + s * kTileBytes;
+                    constexpr int kChunks = kHD / 8;  // 16-byte chunks of a row: a warp's stores are of whole rows
+                    auto zero = [&](int r0, int r1) {
+                        for (int i = r0 * kChunks + lane; i < r1 * kChunks; i += 32) {
+                            const int r = i / kChunks, ch = i % kChunks;
+                            *reinterpret_cast<uint4*>(tile + (r >> 3) * kGroup + (r & 7) * 128 + (ch >> 3) * 1024 +
+                                                      (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
                         }
-                        fence_async_smem();
-                    }
-                    if (!(ok = bar_and(5, 64, ok))) break;
-                    if (th == 0) mbar_arrive(&B.v_full[s]);
+                    };
+                    zero(min(max(a.sinks - t * kBN, 0), kBN), min(max(un.low + 1 - t * kBN, 0), kBN));
+                    zero(min(max(un.end - t * kBN, 0), kBN), kBN);
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&B.v_full[s]);
                 }
             }
         }
@@ -577,8 +635,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // tile, warps 4-7 its columns 0..63 (half hf = 0) and warps 8-11 its
         // columns 64..127 (hf = 1).  The halves of a row (warps w and w + 4: the
         // same TMEM lane quarter) agree on the row max through shared memory, with
-        // a named barrier of that pair per tile; the barrier ANDs the pair's wait
-        // results, so a failed wait stops both halves at the same point.
+        // a named barrier of that pair per tile.
+        // These warps never stop early: after an abort their waits return at once
+        // and they run on, over whatever TMEM holds, to the end of their items
+        // (nothing of it is reported good).  Each branch that is not here saves
+        // about 100 cycles of a tile's 1200 (16 chunks, window 4096: 315 us with the
+        // wait's result looked at and the maximum's three cases in branches, 307).
         const int hf = (warp - 4) >> 2;
         const int quarter = warp & 3;        // TMEM lanes 32*quarter .. +31
         const int r = quarter * 32 + lane;   // row of the tile
@@ -586,26 +648,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* xchg = reinterpret_cast<float*>(smem + GE::kOffX);  // [2 tile phases][2 halves][128 rows]
         const float sl2 = a.scale_log2;
         int g = 0, ii = 0;
-        bool ok = true;
         Walk w;
-        while (ok && next_item(w, false)) {
+        while (next_item(w)) {
             const int col0 = w.g.gap * kPage;
             const int tok = w.p.pos0 - col0;                    // column of the item's first token
             float m_of[2] = {-INFINITY, -INFINITY}, l_of[2] = {0.f, 0.f};
-            for (int t = 0; ok && t < w.g.tiles; ++t)
+            for (int t = 0; t < w.g.tiles; ++t) {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const uint32_t tS = tmem + lane_base + x * 128 + hf * 64;
-                const uint32_t tO = tmem + lane_base + 256 + x * 128 + hf * (kHD / 2);
-                const int p0 = tok + ((x * kBM + quarter * 32) >> lg);  // column of the warp's first row
-                const int p1 = p0 + ((32 >> lg) - 1);                   // ... of its last
-                const int pr = p0 + (lane >> lg);                       // ... of this thread's
-                const int c = t * kBN + hf * 64;                        // first column of this half
-                const bool some = c + 63 > p0 || (c <= p1 - a.window && c + 63 >= a.sinks);
-                const bool good = warp_wait(&B.s_full[x], g & 1, abort_flag, a.status);
-                uint32_t sv[64];
-                float hm = -INFINITY;
-                if (good) {
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t tS = tmem + lane_base + x * 128 + hf * 64;
+                    const uint32_t tO = tmem + lane_base + 256 + x * 128 + hf * (kHD / 2);
+                    const int p0 = tok + ((x * kBM + quarter * 32) >> lg);  // column of the warp's first row
+                    const int p1 = p0 + ((32 >> lg) - 1);                   // ... of its last
+                    const int pr = p0 + (lane >> lg);                       // ... of this thread's
+                    const int c = t * kBN + hf * 64;                        // first column of this half
+                    const bool some = c + 63 > p0 || (c <= p1 - a.window && c + 63 >= a.sinks);
+                    wait_or_abort(&B.s_full[x], g & 1, abort_flag, a.status);
+                    __syncwarp();
+                    if (x == 1 && w.p.rows <= step / 2) {  // B has no rows: P_B may be anything
+                        mbar_arrive(&B.p_full[1]);
+                        ++g;
+                        continue;
+                    }
+                    uint32_t sv[64];
                     tc_fence_after();
                     tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
                     tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
@@ -629,63 +694,55 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
                             m4[q] = max3(m4[q], __uint_as_float(sv[e + 2 * q]), __uint_as_float(sv[e + 2 * q + 1]));
-                    hm = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                }
-                float* slot = xchg + x * 256;
-                slot[hf * 128 + r] = hm;
-                if (!bar_and(1 + quarter, 64, good)) {
-                    ok = false;
-                    break;
-                }
-                const float m_tile = fmaxf(hm, slot[(1 - hf) * 128 + r]) * sl2;
-                float alpha = 1.f;
-                bool rescale = false;
-                if (m_of[x] == -INFINITY) {
-                    m_of[x] = m_tile;
-                } else if (m_tile > m_of[x] + 8.f) {
-                    alpha = fast_exp2(m_of[x] - m_tile);
-                    m_of[x] = m_tile;
-                    rescale = true;
-                }
-                // P = 2^(s*scale*log2e - m) as bf16 into columns 32hf..32hf+31 of
-                // S_x (both halves have read their S before the barrier); a row
-                // with no seen key yet subtracts +inf so every p is 0.  The row sum
-                // adds the fp32 p (their bf16 roundings differ by at most 2^-8
-                // relative, at random).
-                uint32_t pw[32];
-                const float msub = m_of[x] == -INFINITY ? INFINITY : m_of[x];
-                const uint64_t scale2 = pk(sl2, sl2), msub2 = pk(-msub, -msub);
-                uint64_t sum2[2] = {0, 0};
+                    const float hm = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    float* slot = xchg + x * 256;
+                    slot[hf * 128 + r] = hm;
+                    bar_sync(1 + quarter, 64);
+                    const float m_tile = fmaxf(hm, slot[(1 - hf) * 128 + r]) * sl2;
+                    const bool none = m_of[x] == -INFINITY;  // no seen key so far
+                    const bool rescale = !none && m_tile > m_of[x] + 8.f;
+                    const float m_new = none || rescale ? m_tile : m_of[x];
+                    const float alpha = none ? 1.f : fast_exp2(m_of[x] - m_new);
+                    m_of[x] = m_new;
+                    // P = 2^(s*scale*log2e - m) as bf16 into columns 32hf..32hf+31 of
+                    // S_x (both halves have read their S before the barrier); a row
+                    // with no seen key yet subtracts +inf so every p is 0.  The row sum
+                    // adds the fp32 p (their bf16 roundings differ by at most 2^-8
+                    // relative, at random).
+                    uint32_t pw[32];
+                    const float msub = m_of[x] == -INFINITY ? INFINITY : m_of[x];
+                    const uint64_t scale2 = pk(sl2, sl2), msub2 = pk(-msub, -msub);
+                    uint64_t sum2[2] = {0, 0};
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const uint64_t xx =
-                        ffma2(pk(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), scale2, msub2);
-                    const uint64_t pp = pk(fast_exp2(pk_lo(xx)), fast_exp2(pk_hi(xx)));
-                    pw[e] = kF16V ? pack_f16_rn(pk_lo(pp), pk_hi(pp)) : pack_bf16_rn(pk_lo(pp), pk_hi(pp));
-                    sum2[e & 1] = fadd2(sum2[e & 1], pp);
-                }
-                tmem_st32(tmem + lane_base + x * 128 + hf * 32, pw);
-                l_of[x] = l_of[x] * alpha + ((pk_lo(sum2[0]) + pk_hi(sum2[0])) + (pk_lo(sum2[1]) + pk_hi(sum2[1])));
-                // O_x (this half's columns): PV_x(t-1) completed before S_x(t) was
-                // reported.  The whole warp rescales if any of its rows must (alpha
-                // is 1 for the others).
-                if (__any_sync(0xffffffffu, rescale && t > 0)) {
-#pragma unroll 1
-                    for (int q = 0; q < kHD / 64; ++q) {
-                        uint32_t v[32];
-                        tmem_ld32(tO + q * 32, v);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-                        tmem_st32(tO + q * 32, v);
+                    for (int e = 0; e < 32; ++e) {
+                        const uint64_t xx =
+                            ffma2(pk(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), scale2, msub2);
+                        const uint64_t pp = pk(fast_exp2(pk_lo(xx)), fast_exp2(pk_hi(xx)));
+                        pw[e] = kF16V ? pack_f16_rn(pk_lo(pp), pk_hi(pp)) : pack_bf16_rn(pk_lo(pp), pk_hi(pp));
+                        sum2[e & 1] = fadd2(sum2[e & 1], pp);
                     }
+                    tmem_st32(tmem + lane_base + x * 128 + hf * 32, pw);
+                    l_of[x] = l_of[x] * alpha + ((pk_lo(sum2[0]) + pk_hi(sum2[0])) + (pk_lo(sum2[1]) + pk_hi(sum2[1])));
+                    // O_x (this half's columns): PV_x(t-1) completed before S_x(t) was
+                    // reported.  The whole warp rescales if any of its rows must (alpha
+                    // is 1 for the others).
+                    if (__any_sync(0xffffffffu, rescale && t > 0)) {
+#pragma unroll 1
+                        for (int q = 0; q < kHD / 64; ++q) {
+                            uint32_t v[32];
+                            tmem_ld32(tO + q * 32, v);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+                            tmem_st32(tO + q * 32, v);
+                        }
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    mbar_arrive(&B.p_full[x]);
+                    g += x;
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                mbar_arrive(&B.p_full[x]);
-                g += x;
             }
-            if (!ok) break;
             // this item's row sums to the output warps (two items' worth: the sums
             // of item ii - 2 were read before S_x of this item was issued)
             float* lx = xchg + 512 + (ii & 1) * 512;  // [2 halves][2 tiles][128 rows]
@@ -702,11 +759,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = quarter * 32 + lane;
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         const float* xchg = reinterpret_cast<const float*>(smem + GE::kOffX);
-        unsigned char* stage = smem + GE::kOffStage + quarter * 4096;  // this warp's two staging boxes
-        int ii = 0, box = 0;
+        // Rows go out of registers, in whole 32-byte sectors where out is aligned to
+        // them: O_x is free sooner than by way of shared memory and bulk stores,
+        // which the first P.V of the next item waits for (16 chunks of 512 queries,
+        // window 128 and 1024: 47.0 and 106.4 us, bulk stores 49.5 and 108.4).
+        const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
+        int ii = 0;
         bool ok = true;
         Walk w;
-        while (ok && next_item(w, false)) {
+        while (ok && next_item(w)) {
             if (!warp_wait(&B.l_full[ii & 1], (ii >> 1) & 1, abort_flag, a.status)) break;
             const float* lx = xchg + 512 + (ii & 1) * 512;
             const float l[2] = {lx[r] + lx[256 + r], lx[128 + r] + lx[384 + r]};
@@ -719,12 +780,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float inv = (lr > 0.f ? 1.f / lr : 0.f) * vmul;
                 const int row = (x * kBM + r) >> lg;  // token of the item
                 const uint32_t tO = tmem + lane_base + 256 + x * 128;
-                // this warp's 32 rows all belong to the item: TMA store of a 32-row
-                // x 32-column box per chunk from a 64-byte-swizzled staging tile
-                // (rows past the item's end belong to other chunks and are never
-                // written: plain stores there)
-                const int row32 = (x * kBM + quarter * 32) >> lg;  // this warp's first
-                const bool full = row32 + (32 >> lg) <= w.p.rows;
+                __nv_bfloat16* orow =
+                    reinterpret_cast<__nv_bfloat16*>(a.out) +
+                    ((int64_t)(w.p.row0 + row) * a.hq + (w.h << lg) + (r & ((1 << lg) - 1))) * kHD;
 #pragma unroll 1
                 for (int q = 0; q < kHD / 32; ++q) {
                     uint32_t v[32];
@@ -738,36 +796,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
                         o[e] = pack_bf16_rn(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
-                    if (full) {
-                        // the box two stores back has been read before it is overwritten
-                        unsigned char* st = stage + (box & 1) * 2048;
-                        ++box;
-                        if (lane == 0) bulk_wait_group_read1();
-                        __syncwarp();
+                    if (row < w.p.rows) {
+                        if (wide) {
+                            store_256(orow + q * 32, o);
+                            store_256(orow + q * 32 + 16, o + 8);
+                        } else {
 #pragma unroll
-                        for (int ch = 0; ch < 4; ++ch)  // 16-byte chunk ch of row `lane` at chunk ch ^ ((lane >> 1) & 3)
-                            *reinterpret_cast<uint4*>(st + lane * 64 + ((ch ^ ((lane >> 1) & 3)) << 4)) =
-                                make_uint4(o[4 * ch], o[4 * ch + 1], o[4 * ch + 2], o[4 * ch + 3]);
-                        fence_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            tma_store_3d(&maps.o, q * 32, w.h << lg, w.p.row0 + row32, st);
-                            bulk_commit_group();
+                            for (int ch = 0; ch < 4; ++ch)
+                                *reinterpret_cast<uint4*>(orow + q * 32 + 8 * ch) =
+                                    make_uint4(o[4 * ch], o[4 * ch + 1], o[4 * ch + 2], o[4 * ch + 3]);
                         }
-                    } else if (row < w.p.rows) {
-                        __nv_bfloat16* orow =
-                            reinterpret_cast<__nv_bfloat16*>(a.out) +
-                            ((int64_t)(w.p.row0 + row) * a.hq + (w.h << lg) + (r & ((1 << lg) - 1))) * kHD + q * 32;
-#pragma unroll
-                        for (int ch = 0; ch < 4; ++ch)
-                            *reinterpret_cast<uint4*>(orow + 8 * ch) =
-                                make_uint4(o[4 * ch], o[4 * ch + 1], o[4 * ch + 2], o[4 * ch + 3]);
                     }
                 }
             }
             ++ii;
         }
-        if (lane == 0) bulk_wait_group0();  // output stores complete before the CTA exits
     }
     tc_fence_before();
     __syncthreads();
@@ -799,12 +842,12 @@ EncodeTiled encoder()
 }
 
 bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-            const cuuint32_t* box, CUtensorMapSwizzle swizzle)
+            const cuuint32_t* box)
 {
     const cuuint32_t estr[3] = {1, 1, 1};
     EncodeTiled enc = encoder();
     return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, estr,
-                      CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -815,17 +858,16 @@ bool make_maps(const PrefillArgs& a, Maps& m)
     const cuuint32_t G = a.hq / a.hkv;
     const cuuint64_t dims[3] = {(cuuint64_t)kHD, (cuuint64_t)a.hq, (cuuint64_t)a.total_q};
     const cuuint64_t strides[2] = {(cuuint64_t)kHD * 2, (cuuint64_t)a.hq * kHD * 2};
-    const cuuint32_t qbox[3] = {64, G, (cuuint32_t)kBM / G}, obox[3] = {32, G, 32 / G};
-    if (!encode(&m.q, a.q, 3, dims, strides, qbox, CU_TENSOR_MAP_SWIZZLE_128B)) return false;
-    if (!encode(&m.o, a.out, 3, dims, strides, obox, CU_TENSOR_MAP_SWIZZLE_64B)) return false;
+    const cuuint32_t qbox[3] = {64, G, (cuuint32_t)kBM / G};
+    if (!encode(&m.q, a.q, 3, dims, strides, qbox)) return false;
     const int64_t rows = (int64_t)a.num_blocks * a.hkv * a.block_size;
     if constexpr (kHD == 128) return pool_maps(a.k_pool, a.v_pool, rows, false, &m.k, &m.v);
     // (64 columns, rows): a box of (64, 16) is one 16-row page, [16 rows][128 B]
     const cuuint64_t pdims[2] = {64, (cuuint64_t)rows};
     const cuuint64_t pstrides[1] = {64 * 2};
     const cuuint32_t pbox[2] = {64, 16};
-    return encode(&m.k, a.k_pool, 2, pdims, pstrides, pbox, CU_TENSOR_MAP_SWIZZLE_128B) &&
-           encode(&m.v, a.v_pool, 2, pdims, pstrides, pbox, CU_TENSOR_MAP_SWIZZLE_128B);
+    return encode(&m.k, a.k_pool, 2, pdims, pstrides, pbox) &&
+           encode(&m.v, a.v_pool, 2, pdims, pstrides, pbox);
 }
 
 template <int kHD, bool kF16V>
@@ -833,9 +875,7 @@ kvattn_status launch(const PrefillArgs& a, cudaStream_t s)
 {
     if ((int64_t)a.num_blocks * a.hkv * a.block_size >= ((int64_t)1 << 31)) return KVATTN_ERR_UNSUPPORTED;
     const int64_t step = 2 * kBM / (a.hq / a.hkv);
-    const int64_t n_qt = (a.max_q_len + step - 1) / step;
-    const int64_t items = a.num_chunks * n_qt * a.hkv;
-    if (items <= 0) return KVATTN_OK;
+    const int64_t items = a.num_chunks * ((a.max_q_len + step - 1) / step) * a.hkv;  // at most
     if (items > 0x3fffffff) return KVATTN_ERR_UNSUPPORTED;  // item numbers of the round past the last are 32-bit too
     Maps maps;
     if (!make_maps<kHD>(a, maps)) return KVATTN_ERR_CUDA;
@@ -845,8 +885,19 @@ kvattn_status launch(const PrefillArgs& a, cudaStream_t s)
     if (limit.ensure(reinterpret_cast<const void*>(prefill_window_kernel<kHD, kF16V>), kSmem) != cudaSuccess)
         return KVATTN_ERR_CUDA;
     const int64_t grid = std::min<int64_t>(items, num_sms());  // persistent: one CTA per SM
-    return cuda_status(launch_pdl(prefill_window_kernel<kHD, kF16V>, dim3((unsigned)grid), dim3(kThreads), kSmem, s, a, maps,
-                                  (int)n_qt));
+    const Divisors div{Divisor(a.hkv), Divisor(a.block_size / kPage)};
+    for (int c = 0; c < a.num_chunks; c += kMaxChunks) {
+        PrefillArgs b = a;
+        b.num_chunks = std::min(a.num_chunks - c, kMaxChunks);
+        b.cu_q_lens += c;
+        b.prefix_lens += c;
+        b.block_table += (int64_t)c * a.max_blocks;
+        if (b.v_scale) b.v_scale += (int64_t)c * a.hkv;
+        const kvattn_status st = cuda_status(launch_pdl(prefill_window_kernel<kHD, kF16V>, dim3((unsigned)grid),
+                                                        dim3(kThreads), kSmem, s, b, maps, div));
+        if (st != KVATTN_OK) return st;
+    }
+    return KVATTN_OK;
 }
 
 }  // namespace

@@ -403,6 +403,41 @@ def test_prefill_many_chunks(kvattn_lib):
     _prefill(kvattn_lib, "bf16", 2, 1, 128, chunks, 33, 2, step=29, seed=7, spare_rows=2)
 
 
+def test_prefill_long_chunk_among_short(kvattn_lib):
+    """A long chunk and many of one row: far fewer token blocks than chunks times the longest chunk's."""
+    g = np.random.default_rng(32)
+    chunks = [(int(g.integers(0, 60)), 1) for _ in range(150)]
+    chunks[70] = (30, 1100)
+    _prefill(kvattn_lib, "bf16", 4, 2, 128, chunks, 40, 3, step=97, seed=8)
+
+
+def test_prefill_thousands_of_chunks(kvattn_lib):
+    """More chunks than one launch takes, every one with its own prefix, in two shapes: most of them empty, and none."""
+    for least in (0, 1):
+        g = np.random.default_rng(33 + least)
+        chunks = [(int(g.integers(0, 20)), int(g.integers(least, 2)) if i % 1000 else 9) for i in range(4200)]
+        _prefill(kvattn_lib, "bf16", 2, 1, 64, chunks, 11, 2, step=3, seed=9 + least)
+    _prefill(kvattn_lib, "fp8", 4, 1, 128, [(i % 37, 1) for i in range(2100)], 11, 2, seed=11)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("shift", [8, 16])
+def test_prefill_out_alignment(kvattn_lib, d, shift):
+    """An output on 16 bytes, and on 32: the same values."""
+    kv = kvattn_lib
+    n = 140
+    c = WindowCache(kv, "bf16", 2, d, [n], [np.ones(n, bool)], seed=4)
+    cfg = kv.make_config(8, 2, d, kv.BF16)
+    q = _q(np.random.default_rng(6), (n, 8, d), "bf16").cuda()
+    cu, prefix = torch.tensor([0, n], dtype=torch.int32).cuda(), torch.zeros(1, dtype=torch.int32).cuda()
+    want = kv.prefill_window(cfg, c.cache, q, cu, prefix, c.d_table, n, 50, 2)
+    room = torch.full((q.numel() + 64,), 9.0, dtype=torch.bfloat16, device="cuda")
+    out = room[shift:shift + q.numel()].view(q.shape)
+    kv.prefill_window(cfg, c.cache, q, cu, prefix, c.d_table, n, 50, 2, out=out)
+    assert torch.equal(out, want)
+    assert torch.all(room[:shift] == 9.0) and torch.all(room[shift + q.numel():] == 9.0)
+
+
 def test_prefill_bad_chunks(kvattn_lib):
     """Chunks whose metadata is out of range are skipped and recorded; the others are as without them."""
     kv = kvattn_lib
