@@ -10,10 +10,11 @@
 // latency: every step below is one that a short chain of dependent loads asks
 // for.  The warps of a cluster take the segment's tiles in turn.  A warp loads
 // its tile straight from global memory into MMA fragments (no shared memory,
-// no barrier): the dims of a dot product may be taken in any order, so a lane
-// loads whole 16-byte chunks and the query's fragments follow the same order,
-// and the dims of the output are named so that each lane's chunks of V hold
-// the rows it owns.  S^T = K Q^T and O^T += V^T P^T have the 16 tokens and the
+// no barrier; fp8 pages, which take longer to convert than to arrive, by way of
+// two buffers of the warp's own): the dims of a dot product may be taken in any
+// order, so a lane loads whole 16-byte chunks and the query's fragments follow
+// the same order, and the dims of the output are named so that each lane's chunks
+// of V hold the rows it owns.  S^T = K Q^T and O^T += V^T P^T have the 16 tokens and the
 // dims on the M axis and up to 8 query heads on N; P goes from the C fragment
 // of one to the B fragment of the other by movmatrix.  A warp keeps its own
 // running maximum and sum; the warps of a CTA merge through shared memory and
@@ -98,8 +99,11 @@ struct WarpState {
     }
 };
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ uint4 ldg16(const void* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
-__device__ __forceinline__ uint32_t ldg4(const void* p) { return __ldg(reinterpret_cast<const uint32_t*>(p)); }
 
 // ---- bf16 cache.  K: lane (g4, q4) holds rows (tokens) g4 and g4 + 8, 16-byte
 // chunks q4 + 4i of each; chunk i is the lane's share of MMA k-steps 2i and
@@ -177,22 +181,20 @@ struct Fp8Tile {
     uint4 k[2][2];
     uint32_t v[16];
     float ks[2], vs[2];
-    __device__ __forceinline__ void load_k(const char* pg, int rk0, int q4)
+    __device__ __forceinline__ void load(const unsigned char* pg, int rk0, int g4, int q4)
     {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int row = rk0 + 2 * r;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) k[r][i] = ldg16(pg + row * 128 + (((q4 + 4 * i) ^ f8_swz(row)) << 4));
-            ks[r] = __uint_as_float(ldg4(pg + kF8KsOff + 4 * row));
+            for (int i = 0; i < 2; ++i)
+                k[r][i] = *reinterpret_cast<const uint4*>(pg + row * 128 + (((q4 + 4 * i) ^ f8_swz(row)) << 4));
+            ks[r] = *reinterpret_cast<const float*>(pg + kF8KsOff + 4 * row);
+            vs[r] = *reinterpret_cast<const float*>(pg + kF8VsOff + 4 * row);
         }
-    }
-    __device__ __forceinline__ void load_v(const char* pg, int rk0, int g4, int q4)
-    {
 #pragma unroll
-        for (int m = 0; m < 16; ++m) v[m] = ldg4(pg + kF8VOff + 16 * (8 * m + g4) + 4 * q4);
-        vs[0] = __uint_as_float(ldg4(pg + kF8VsOff + 4 * rk0));
-        vs[1] = __uint_as_float(ldg4(pg + kF8VsOff + 4 * rk0 + 8));
+        for (int m = 0; m < 16; ++m)
+            v[m] = *reinterpret_cast<const uint32_t*>(pg + kF8VOff + 16 * (8 * m + g4) + 4 * q4);
     }
     __device__ __forceinline__ void scores(float (&s)[4], const uint32_t (&q)[8][2]) const
     {
@@ -224,25 +226,36 @@ struct Fp8Tile {
 // Resident warps per SM that the register budgets leave room for.  Measured: a
 // bf16 tile at D = 128, with the next one on its way, wants 200 registers (32 / 8
 // heads, 32 sequences, window 4096: 88.5 us with 8 warps, 91.9 with 12, 100.7
-// with 16, which spill); an fp8 page whose K and V are fetched again as soon as
-// they are used 127 (64 / 8 heads, 64 sequences, window 1024: 33.2 us with 16
-// warps, 36.6 with 12; two pages in 168 registers and 12 warps 33.9, three in
-// 237 and 8 warps 36.5).
+// with 16, which spill); an fp8 page that is converted while the warp's next two
+// are under way 128 (64 / 8 heads, 64 sequences, window 1024: 29.4 us with 16
+// warps, 29.6 with 20, 36 with 24, which spill; straight from global memory into
+// registers 33.1, two pages ahead so 33.9, with three more 36.5; the scores of the
+// next page before this one's P.V 30.6).
 constexpr int warps_per_sm(int kind, int d, int g)
 {
     return kind == kF32Cache ? (d * g > 64 ? 8 : 16) : kind == kFp8Cache || d == 64 ? 16 : 8;
 }
 
-// Shared floats of a CTA: every warp's output and (max, sum) of each head, and
-// the CTA's merge of them (read by the other CTAs of the cluster).
-__host__ __device__ constexpr int direct_floats(int warps, int heads, int d) { return (warps + 1) * heads * (d + 2); }
+constexpr int kRing = 2;  // fp8: pages of a warp in shared memory
+// Floats of a warp's output of each head (fp8: they take the place of its pages).
+__host__ __device__ constexpr int warp_floats(int kind, int heads, int d)
+{
+    return kind == kFp8Cache ? kRing * kF8Page / 4 : heads * d;
+}
+// Shared floats of a CTA: every warp's output, the CTA's merge of them (read by
+// the other CTAs of the cluster), and the (max, sum) of each of these heads.
+__host__ __device__ constexpr int direct_floats(int kind, int warps, int heads, int d)
+{
+    return warps * warp_floats(kind, heads, d) + heads * d + (warps + 1) * heads * 2;
+}
+static_assert(warp_floats(kFp8Cache, 8, 128) >= 8 * 128, "a warp's outputs fit where its pages were");
 
 template <int kKind, int kD, int kG>
 __global__ void __launch_bounds__(warps_per_sm(kKind, kD, kG) * 32, 1)
     decode_direct_kernel(const __grid_constant__ DecodeArgs a, const int cluster)
 {
     pdl_wait();
-    extern __shared__ float part[];
+    extern __shared__ __align__(128) float part[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
     const int g4 = lane >> 2, q4 = lane & 3;
     const int rank = blockIdx.x % cluster, seg = blockIdx.x / cluster;
@@ -252,8 +265,9 @@ __global__ void __launch_bounds__(warps_per_sm(kKind, kD, kG) * 32, 1)
     const int L = a.seq_lens[b];
 
     // per-head rows of the warps' (and, last, the CTA's) outputs and (max, sum)
-    auto row_of = [&](int w, int g) { return part + (w * G + g) * kD; };
-    float* ml = part + (warps + 1) * G * kD;
+    const int wf = warp_floats(kKind, G, kD);
+    auto row_of = [&](int w, int g) { return part + w * wf + g * kD; };
+    float* ml = part + warps * wf + G * kD;
     auto ml_of = [&](int w, int g) { return ml + 2 * (w * G + g); };
 
     Piece pc;
@@ -355,29 +369,41 @@ __global__ void __launch_bounds__(warps_per_sm(kKind, kD, kG) * 32, 1)
             st.vref = 1.f;
         } else {
             const int rk0 = (g4 >> 1) * 4 + (g4 & 1), rk1 = rk0 + 2;
-            const char* pool = (const char*)a.k_pool;
-            Fp8Tile t;
-            // (of a bad block nothing is seen)
-            auto page = [&](int64_t row) { return pool + (row < 0 ? 0 : row) / kTile * kF8Page; };
-            int64_t row = __shfl_sync(0xffffffffu, rows, 0);
-            uint32_t seen = mine ? seen_of(0, row) : 0u;
-            const char* pg = page(row);
-            if (mine) {
-                t.load_k(pg, rk0, q4);
-                t.load_v(pg, rk0, g4, q4);
-            }
+            const unsigned char* pool = (const unsigned char*)a.k_pool;
+            unsigned char* ring = reinterpret_cast<unsigned char*>(row_of(warp, 0));
+            uint32_t seen[kRing];  // of the pages under way, the next one first
+            // page j on its way to its slot (one group of copies, empty past the last page)
+            auto fetch = [&](int j) -> uint32_t {
+                uint32_t bits = 0;
+                if (j < mine) {
+                    if (j > 0 && (j & 31) == 0) rows = lookup(j);
+                    const int64_t row = __shfl_sync(0xffffffffu, rows, j & 31);
+                    bits = seen_of(j, row);
+                    // (of a bad block nothing is seen)
+                    const unsigned char* src = pool + (row < 0 ? 0 : row) / kTile * kF8Page + 16 * lane;
+                    const uint32_t dst = smem_addr(ring + j % kRing * kF8Page + 16 * lane);
+#pragma unroll
+                    for (int c = 0; c < kF8Page / 512; ++c) cp_async16(dst + 512 * c, src + 512 * c);
+                    if (lane < kF8Page % 512 / 16) cp_async16(dst + kF8Page / 512 * 512, src + kF8Page / 512 * 512);
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                return bits;
+            };
+#pragma unroll
+            for (int i = 0; i < kRing; ++i) seen[i] = fetch(i);
             for (int j = 0; j < mine; ++j) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+                __syncwarp();  // every lane's copies of page j are there
+                Fp8Tile t;
+                t.load(ring + j % kRing * kF8Page, rk0, g4, q4);
+                const uint32_t now = seen[0];
+#pragma unroll
+                for (int i = 0; i + 1 < kRing; ++i) seen[i] = seen[i + 1];
+                __syncwarp();  // and every lane has read it
+                seen[kRing - 1] = fetch(j + kRing);
                 float s[4] = {0.f, 0.f, 0.f, 0.f};
                 t.scores(s, q);
                 const float k0 = t.ks[0] * sl2, k1 = t.ks[1] * sl2;
-                const uint32_t now = seen;
-                if (j + 1 < mine) {  // the next page's K flies from here, its V from the end of this turn
-                    if (((j + 1) & 31) == 0) rows = lookup(j + 1);
-                    row = __shfl_sync(0xffffffffu, rows, (j + 1) & 31);
-                    seen = seen_of(j + 1, row);
-                    pg = page(row);
-                    t.load_k(pg, rk0, q4);
-                }
                 const bool in0 = now >> rk0 & 1u, in1 = now >> rk1 & 1u;
                 const float x[4] = {in0 ? s[0] * k0 : -INFINITY, in0 ? s[1] * k0 : -INFINITY,
                                     in1 ? s[2] * k1 : -INFINITY, in1 ? s[3] * k1 : -INFINITY};
@@ -393,8 +419,9 @@ __global__ void __launch_bounds__(warps_per_sm(kKind, kD, kG) * 32, 1)
                 const float c0 = sv0 * st.vinv, c1 = sv1 * st.vinv;
                 t.add(st.o, movmatrix_trans(pack_f16_rn(p[0] * c0, p[1] * c0)),
                       movmatrix_trans(pack_f16_rn(p[2] * c1, p[3] * c1)), vmask);
-                if (j + 1 < mine) t.load_v(pg, rk0, g4, q4);
             }
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncwarp();  // the outputs take the pages' place
         }
 #pragma unroll
         for (int s = 4; s < 32; s <<= 1) {
@@ -581,7 +608,7 @@ template <int kKind, int kD, int kG>
 kvattn_status run_direct(const DecodeArgs& a, int warps, int cluster, cudaStream_t s)
 {
     auto kern = decode_direct_kernel<kKind, kD, kG>;
-    const int bytes = direct_floats(warps, a.hq / a.hkv, kD) * 4;
+    const int bytes = direct_floats(kKind, warps, a.hq / a.hkv, kD) * 4;
     static SmemLimit limit;
     if (limit.ensure(reinterpret_cast<const void*>(kern), bytes) != cudaSuccess) return KVATTN_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
@@ -629,12 +656,16 @@ bool launch_decode_direct(const DecodeArgs& a, int32_t max_tiles, cudaStream_t s
     const int64_t segs = (int64_t)a.batch * a.hkv, tiles = segs * max_tiles;
     // Where the balanced stream of decode_kernel.cuh is faster: long calls of
     // many keys.  Measured (us, this and the stream; thousands of tiles): bf16
-    // D = 128 17 27 / 32, 66 88 / 90, 264 343 / 324; fp8 17 14.5 / 26.3, 33
-    // 31.4 / 37.9, 264 200 / 195; fp32 groups of 4 4.2 13.4 / 20.6, 16 49 / 48,
-    // 66 171 / 160; bf16 D = 64 264 165 / 307 and fp32 without groups 264
-    // 574 / 608, so these always come here.
+    // D = 128 17 27 / 32, 66 88 / 90, 264 343 / 324; fp32 groups of 4 4.2 13.4 /
+    // 20.6, 16 49 / 48, 66 171 / 160; bf16 D = 64 264 165 / 307 and fp32 without
+    // groups 264 574 / 608, so these always come here.  fp8 pages stream as fast
+    // from here (17 13.9 / 26.0, 66 47 / 59, 264 172 / 195, 526 330 / 364) and
+    // lose only where a long sequence among short ones keeps its few warps busy
+    // (64 sequences of 1 to 32768 tokens, windows of 8192 and 16384: 162 / 179 and
+    // 304 / 286).
     int64_t most = INT64_MAX;
     if (kind == kF32Cache) most = G == 1 ? most : 16384;
+    else if (kind == kFp8Cache) most = max_tiles <= 512 + 2 ? most : 65536;  // (a window of 8192 and a few sinks)
     else if (a.d == 128) most = 65536;
     if (tiles > most || segs * 8 > INT32_MAX) return false;
     // One wave of warps: the most warps per CTA that let every segment be
