@@ -239,9 +239,10 @@ struct PrefillArgs {
     int32_t hq, hkv, d;
     float scale_log2;
     int* status;
-    // launch_prefill_window only.  v_scale: null, or V is f16 and out its result times v_scale[chunk][KV head]
+    // launch_prefill_window only.  kv_scale: null, or K and V are f16, the scores theirs times kv_scale[chunk][KV head].x
+    // and out its result times .y
     int32_t window, sinks;
-    const float* v_scale;
+    const float2* kv_scale;
 };
 kvattn_status launch_prefill(const PrefillArgs& a, cudaStream_t s);
 kvattn_status launch_prefill_window(const PrefillArgs& a, cudaStream_t s);
@@ -267,7 +268,7 @@ kvattn_status launch_prefill_fp8(const PrefillArgs& pa, const void* pool, const 
 // arguments.
 struct Fp8WindowLayout {
     int64_t per_chunk;
-    size_t off_vscale, off_table, off_k, off_v, bytes;
+    size_t off_scale, off_table, off_k, off_v, bytes;
 };
 Fp8WindowLayout fp8_window_layout(int32_t hkv, int32_t block_size, int32_t max_blocks, int32_t num_chunks,
                                   int32_t max_q_len, int32_t window, int32_t sinks);

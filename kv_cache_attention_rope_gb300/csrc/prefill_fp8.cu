@@ -54,9 +54,9 @@ struct Fp8PrefillArgs {
     __nv_bfloat16* k_copy;     // [nb][hkv][block_size][128]
     __nv_bfloat16* v_copy;
     int* status;
-    // windowed form: copy block c * per_chunk + i is chunk c's i-th seen block; V is copied in f16, divided by v_scale
+    // windowed form: copy block c * per_chunk + i is chunk c's i-th seen block; K and V are copied in f16, divided by kv_scale
     int32_t window, sinks, per_chunk;
-    float* v_scale;            // [num_chunks][hkv], powers of two
+    float2* kv_scale;          // [num_chunks][hkv], powers of two
 };
 
 // Blocks chunk c's keys occupy; 0 for a chunk the prefill kernel rejects or
@@ -132,13 +132,21 @@ __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi)
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Four e4m3 codes (bytes of w) times s -> two bf16 pairs
+// Two values in f16 (kF16) or bf16.
+template <bool kF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    return kF16 ? pack_f16_rn(lo, hi) : bf16x2_rn(lo, hi);
+}
+
+// Four e4m3 codes (bytes of w) times s -> two pairs
+template <bool kF16>
 __device__ __forceinline__ void expand4(uint32_t w, float s, uint32_t& o0, uint32_t& o1)
 {
     const float2 a = f16x2_to_float2(e4m3x2_to_f16x2(w));
     const float2 b = f16x2_to_float2(e4m3x2_to_f16x2(w >> 16));
-    o0 = bf16x2_rn(a.x * s, a.y * s);
-    o1 = bf16x2_rn(b.x * s, b.y * s);
+    o0 = pack2<kF16>(a.x * s, a.y * s);
+    o1 = pack2<kF16>(b.x * s, b.y * s);
 }
 
 constexpr int kExpandWarps = 8;
@@ -154,10 +162,10 @@ __device__ __forceinline__ void fetch_page(unsigned char* buf, const unsigned ch
 }
 
 // A warp's conversion of the page at src (shared memory) to token-major rows:
-// K to bf16, V to bf16 or (kF16V) to f16 times vmul.
-template <bool kF16V>
-__device__ __forceinline__ void convert_page(const unsigned char* src, __nv_bfloat16* kd, __nv_bfloat16* vd, float vmul,
-                                             int lane)
+// to bf16, or (kF16) to f16 times kmul and vmul.
+template <bool kF16>
+__device__ __forceinline__ void convert_page(const unsigned char* src, __nv_bfloat16* kd, __nv_bfloat16* vd, float kmul,
+                                             float vmul, int lane)
 {
     const float* scales = reinterpret_cast<const float*>(src + kF8KsOff);
     // K: lane takes chunk cc (16 dims) of tokens r = lane / 8 + 4 t
@@ -166,12 +174,12 @@ __device__ __forceinline__ void convert_page(const unsigned char* src, __nv_bflo
     for (int t = 0; t < 4; ++t) {
         const int r = (lane >> 3) + 4 * t;
         const uint4 kw = *reinterpret_cast<const uint4*>(src + r * 128 + 16 * (cc ^ f8_swz(r)));
-        const float ks = scales[r];
+        const float ks = kF16 ? scales[r] * kmul : scales[r];
         uint4 o0, o1;
-        expand4(kw.x, ks, o0.x, o0.y);
-        expand4(kw.y, ks, o0.z, o0.w);
-        expand4(kw.z, ks, o1.x, o1.y);
-        expand4(kw.w, ks, o1.z, o1.w);
+        expand4<kF16>(kw.x, ks, o0.x, o0.y);
+        expand4<kF16>(kw.y, ks, o0.z, o0.w);
+        expand4<kF16>(kw.z, ks, o1.x, o1.y);
+        expand4<kF16>(kw.w, ks, o1.z, o1.w);
         *reinterpret_cast<uint4*>(kd + r * kF8D + 16 * cc) = o0;
         *reinterpret_cast<uint4*>(kd + r * kF8D + 16 * cc + 8) = o1;
     }
@@ -184,7 +192,7 @@ __device__ __forceinline__ void convert_page(const unsigned char* src, __nv_bflo
     const float4 vs0 = *reinterpret_cast<const float4*>(src + kF8VsOff + 32 * hv);
     const float4 vs1 = *reinterpret_cast<const float4*>(src + kF8VsOff + 32 * hv + 16);
     float vs[8] = {vs0.x, vs0.y, vs0.z, vs0.w, vs1.x, vs1.y, vs1.z, vs1.w};
-    if constexpr (kF16V) {
+    if constexpr (kF16) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) vs[k] *= vmul;
     }
@@ -198,7 +206,7 @@ __device__ __forceinline__ void convert_page(const unsigned char* src, __nv_bflo
             const uint32_t x = tt < 4 ? vw[2 * m].x : vw[2 * m].y;
             const uint32_t y = tt < 4 ? vw[2 * m + 1].x : vw[2 * m + 1].y;
             const float2 f = f16x2_to_float2(e4m3x2_to_f16x2(__byte_perm(x, y, sel)));
-            o[m] = kF16V ? pack_f16_rn(f.x * vs[tt], f.y * vs[tt]) : bf16x2_rn(f.x * vs[tt], f.y * vs[tt]);
+            o[m] = pack2<kF16>(f.x * vs[tt], f.y * vs[tt]);
         }
         *reinterpret_cast<uint4*>(vd + (8 * hv + tt) * kF8D + 8 * gv) = make_uint4(o[0], o[1], o[2], o[3]);
     }
@@ -283,7 +291,7 @@ __global__ void __launch_bounds__(kExpandWarps * 32) prefill_fp8_expand(const Fp
             // copy page g0 + i = rows 16 p .. 16 p + 15 of copy block b, head h:
             // [b][h][block_size][128] has them at ((b * hkv + h) * ppb + p) * 16 rows
             const int64_t row0 = (g0 + i) * 16;
-            convert_page<false>(src, a.k_copy + row0 * kF8D, a.v_copy + row0 * kF8D, 1.f, lane);
+            convert_page<false>(src, a.k_copy + row0 * kF8D, a.v_copy + row0 * kF8D, 1.f, 1.f, lane);
             __syncwarp();  // buffer bsel is refilled two pages later
             bsel ^= 1;
         }
@@ -291,18 +299,19 @@ __global__ void __launch_bounds__(kExpandWarps * 32) prefill_fp8_expand(const Fp
 }
 
 // Windowed form: `slices` CTAs per (chunk, KV head), each converting a share of
-// the pages that the chunk sees.  V is copied in f16, whose 11 bits hold code *
-// scale eight times more exactly than bf16's 8; it is divided by the power of
-// two that brings the largest seen V value of the chunk and head to 2^14 ..
-// 2^15, and f16 covers 29 binades below that at full precision.  (P, which the
-// MMA takes in V's type, gains as much.)  Every CTA finds that power itself from
-// the scales, 64 of a page's 4224 bytes: a kernel of its own for it took 5 us of
-// a call's 89.  The copy's block table is written here too.
+// the pages that the chunk sees.  K and V are copied in f16, whose 11 bits hold
+// code * scale eight times more exactly than bf16's 8; each is divided by the
+// power of two that brings its largest seen value of the chunk and head to 2^14
+// .. 2^15, and f16 covers 29 binades below that at full precision.  (q and P,
+// which the MMAs take in K's and V's type, lose nothing and gain as much.)
+// Every CTA finds the powers itself from the scales, 128 of a page's 4224 bytes:
+// a kernel of its own for V's took 5 us of a call's 89.  The copy's block table
+// is written here too.
 __global__ void __launch_bounds__(kExpandWarps * 32) prefill_fp8_expand_window(const Fp8PrefillArgs a, const int slices)
 {
     pdl_wait();
     extern __shared__ __align__(16) unsigned char bufs[];  // [kExpandWarps][2][kF8Page]
-    __shared__ float wmax[kExpandWarps];
+    __shared__ float2 wmax[kExpandWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     unsigned char* pbuf = bufs + warp * 2 * kF8Page;
     const int pair = blockIdx.x / slices, slice = blockIdx.x - pair * slices;
@@ -342,29 +351,33 @@ __global__ void __launch_bounds__(kExpandWarps * 32) prefill_fp8_expand_window(c
                        __shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(my_src), i)),
                    lane);
     };
-    if (todo) fetch(__ffs(todo) - 1, 0);  // the first page flies while the largest V is found
-    float m = 0.f;
+    if (todo) fetch(__ffs(todo) - 1, 0);  // the first page flies while the largest K and V are found
+    float2 m = make_float2(0.f, 0.f);
     for (int e = tid; e < pages * 4; e += kExpandWarps * 32) {  // 4 tokens each
         const int j = s.block((e >> 2) / ppb), p = (e >> 2) % ppb;
         const int key0 = j * a.block_size + p * 16 + (e & 3) * 4;
         const int blk = block_id(j, false);
         if (blk < 0) continue;
-        const float4 v = *reinterpret_cast<const float4*>(page_of(blk, p) + kF8VsOff + (e & 3) * 16);
-        const float f[4] = {v.x, v.y, v.z, v.w};
+        const unsigned char* sc = page_of(blk, p) + (e & 3) * 16;
+        const float4 k = *reinterpret_cast<const float4*>(sc + kF8KsOff);
+        const float4 v = *reinterpret_cast<const float4*>(sc + kF8VsOff);
+        const float kf[4] = {k.x, k.y, k.z, k.w}, vf[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (s.key(key0 + i, a.sinks)) m = fmaxf(m, f[i]);
+            if (s.key(key0 + i, a.sinks)) m = make_float2(fmaxf(m.x, kf[i]), fmaxf(m.y, vf[i]));
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 16; o > 0; o >>= 1)
+        m = make_float2(fmaxf(m.x, __shfl_xor_sync(0xffffffffu, m.x, o)), fmaxf(m.y, __shfl_xor_sync(0xffffffffu, m.y, o)));
     if (lane == 0) wmax[warp] = m;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kExpandWarps; ++i) m = fmaxf(m, wmax[i]);
+    for (int i = 0; i < kExpandWarps; ++i) m = make_float2(fmaxf(m.x, wmax[i].x), fmaxf(m.y, wmax[i].y));
     // |code * scale| <= 448 scale < 2^(e + 10), scale's exponent being e
-    const int ex = m > 0.f && m < INFINITY ? min(122, max(-100, ilogbf(m) - 5)) : 0;
-    if (slice == 0 && tid == 0) a.v_scale[pair] = ldexpf(1.f, ex);
-    const float vmul = ldexpf(1.f, -ex);
+    auto power = [](float x) { return x > 0.f && x < INFINITY ? min(122, max(-100, ilogbf(x) - 5)) : 0; };
+    const int ke = power(m.x), ve = power(m.y);
+    if (slice == 0 && tid == 0) a.kv_scale[pair] = make_float2(ldexpf(1.f, ke), ldexpf(1.f, ve));
+    const float2 mul = make_float2(ldexpf(1.f, -ke), ldexpf(1.f, -ve));
     int bsel = 0;
     for (int base = 0; first + base * stride < pages; base += 32) {
         if (base > 0) {
@@ -384,7 +397,7 @@ __global__ void __launch_bounds__(kExpandWarps * 32) prefill_fp8_expand_window(c
             __syncwarp();  // every lane's copies of page i have landed
             const int g = first + (base + i) * stride;
             const int64_t row0 = ((((int64_t)c * a.per_chunk + g / ppb) * a.hkv + h) * ppb + g % ppb) * 16;
-            convert_page<true>(pbuf + bsel * kF8Page, a.k_copy + row0 * kF8D, a.v_copy + row0 * kF8D, vmul, lane);
+            convert_page<true>(pbuf + bsel * kF8Page, a.k_copy + row0 * kF8D, a.v_copy + row0 * kF8D, mul.x, mul.y, lane);
             __syncwarp();  // the buffer is refilled two pages later
             bsel ^= 1;
         }
@@ -497,8 +510,8 @@ Fp8WindowLayout fp8_window_layout(int32_t hkv, int32_t block_size, int32_t max_b
     const int64_t seen = ((int64_t)sinks + block_size - 1) / block_size + (run + block_size - 2) / block_size + 1;
     L.per_chunk = std::min<int64_t>(max_blocks, seen);
     size_t off = 0;
-    L.off_vscale = off;
-    off = align_up(off + (size_t)num_chunks * hkv * 4);
+    L.off_scale = off;
+    off = align_up(off + (size_t)num_chunks * hkv * 8);
     L.off_table = off;
     off = align_up(off + (size_t)num_chunks * (size_t)max_blocks * 4);
     const size_t copy = (size_t)num_chunks * (size_t)L.per_chunk * hkv * block_size * kF8D * 2;
@@ -529,7 +542,7 @@ kvattn_status launch_prefill_window_fp8(const PrefillArgs& pa, const void* pool,
     a.ctable = reinterpret_cast<int32_t*>(ws + L.off_table);
     a.k_copy = reinterpret_cast<__nv_bfloat16*>(ws + L.off_k);
     a.v_copy = reinterpret_cast<__nv_bfloat16*>(ws + L.off_v);
-    a.v_scale = reinterpret_cast<float*>(ws + L.off_vscale);
+    a.kv_scale = reinterpret_cast<float2*>(ws + L.off_scale);
     static Residency residency;
     int wave = 0;
     cudaError_t e = expand_wave(residency, reinterpret_cast<const void*>(prefill_fp8_expand_window), &wave);
@@ -549,7 +562,7 @@ kvattn_status launch_prefill_window_fp8(const PrefillArgs& pa, const void* pool,
     b.v_pool = a.v_copy;
     b.block_table = a.ctable;
     b.num_blocks = nb;
-    b.v_scale = a.v_scale;
+    b.kv_scale = a.kv_scale;
     return launch_prefill_window(b, s);
 }
 

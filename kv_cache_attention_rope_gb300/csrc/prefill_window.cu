@@ -87,6 +87,7 @@ struct Maps {
 // Barriers, in shared memory.
 struct Bars {
     uint64_t q_full[2], q_empty[2];  // of Q_x: loaded; every S_x MMA of the item is done
+    uint64_t q_f16[2];               // kF16: converted
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
     uint64_t v_raw[kStages];         // V loaded, with rows to zero before it counts as v_full
     uint64_t s_full[2], p_full[2];
@@ -247,9 +248,11 @@ __device__ __forceinline__ bool has_unseen(const PrefillArgs& a, const Unseen& u
 // in shared memory; ties by index) and more in the order of their chunks.
 // CTA k takes, in round r, item r G + k for even r and r G + G - 1 - k for odd r
 // (G CTAs).  Pipeline state (stages, phases) runs on across items.
-// kF16V: V (and so P, which the MMA takes in V's type) in f16, scaled per
-// (chunk, KV head): out is multiplied by a.v_scale.
-template <int kHD, bool kF16V>
+// kF16: K and V (and so q and P, which the MMAs take in their types) in f16,
+// scaled per (chunk, KV head) as a.kv_scale says.  q arrives in bf16, and the
+// output warps, which have time, convert it in place to q / 16 (f16's 11 bits
+// hold bf16's 8; from 2^20 on it is infinite, and under 2^-10 it loses bits).
+template <int kHD, bool kF16>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_window_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ Maps maps,
                           const __grid_constant__ Divisors div)
@@ -289,6 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = 0; x < 2; ++x) {
             mbar_init(&B.q_full[x], 1);
             mbar_init(&B.q_empty[x], 1);
+            mbar_init(&B.q_f16[x], 128);
             mbar_init(&B.s_full[x], 1);
             mbar_init(&B.p_full[x], 256);
             mbar_init(&B.o_done[x], 1);
@@ -484,8 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // elected lane issues.  Operand descriptors are built once: a stage or
             // k-step only adds (byte offset >> 4) to the start-address field, which
             // cannot carry out of it (shared-memory offsets stay below 256 KB).
-            constexpr uint32_t idesc_s = idesc_bf16_f32(kBM, kBN, false);
-            constexpr uint32_t idesc_o = kF16V ? idesc_f16_f32(kBM, kHD, true) : idesc_bf16_f32(kBM, kHD, true);
+            constexpr uint32_t idesc_s = kF16 ? idesc_f16_f32(kBM, kBN, false) : idesc_bf16_f32(kBM, kBN, false);
+            constexpr uint32_t idesc_o = kF16 ? idesc_f16_f32(kBM, kHD, true) : idesc_bf16_f32(kBM, kHD, true);
             const uint32_t sbase = smem_addr(smem);
             const uint64_t dQ = umma_desc_sw128(sbase + kOffQ, 16, 1024);      // Q_x: + x * kTileBytes
             const uint64_t dK = umma_desc_sw128(sbase + kOffK, 16, kGroup);    // K stage s: + s * kTileBytes
@@ -529,11 +533,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             int n_kv = next_item(w) ? w.g.tiles : 0;
             int g = 0, item = 0;
             bool ok = n_kv > 0;
-            if (ok && (ok = wait(&B.q_full[0], 0) && wait(&B.k_full[0], 0))) {
+            uint64_t* q_ready = kF16 ? B.q_f16 : B.q_full;
+            if (ok && (ok = wait(&q_ready[0], 0) && wait(&B.k_full[0], 0))) {
                 tc_fence_after();
                 issue_s(0, 0);
                 if (n_kv == 1) commit(&B.q_empty[0]);
-                if ((ok = wait(&B.q_full[1], 0))) {
+                if ((ok = wait(&q_ready[1], 0))) {
                     tc_fence_after();
                     issue_s(1, 0);
                     commit(&B.k_empty[0]);
@@ -569,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 issue_pv(0, g, n_kv == 1, true);
                 if (n_next > 0) {
-                    if (!(ok = wait(&B.q_full[0], (item + 1) & 1) && wait(&B.k_full[g1 % kStages], (g1 / kStages) & 1)))
+                    if (!(ok = wait(&q_ready[0], (item + 1) & 1) && wait(&B.k_full[g1 % kStages], (g1 / kStages) & 1)))
                         break;
                     tc_fence_after();
                     issue_s(0, g1);
@@ -580,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 issue_pv(1, g, n_kv == 1, true);
                 if (n_next > 0) {
-                    if (!(ok = wait(&B.q_full[1], (item + 1) & 1))) break;
+                    if (!(ok = wait(&q_ready[1], (item + 1) & 1))) break;
                     tc_fence_after();
                     issue_s(1, g1);
                     commit(&B.k_empty[g1 % kStages]);
@@ -646,10 +651,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = quarter * 32 + lane;   // row of the tile
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         float* xchg = reinterpret_cast<float*>(smem + GE::kOffX);  // [2 tile phases][2 halves][128 rows]
-        const float sl2 = a.scale_log2;
         int g = 0, ii = 0;
         Walk w;
         while (next_item(w)) {
+            // (f16: q was divided by 16)
+            const float sl2 = kF16 ? a.kv_scale[(int64_t)w.p.c * a.hkv + w.h].x * 16.f * a.scale_log2 : a.scale_log2;
             const int col0 = w.g.gap * kPage;
             const int tok = w.p.pos0 - col0;                    // column of the item's first token
             float m_of[2] = {-INFINITY, -INFINITY}, l_of[2] = {0.f, 0.f};
@@ -718,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint64_t xx =
                             ffma2(pk(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), scale2, msub2);
                         const uint64_t pp = pk(fast_exp2(pk_lo(xx)), fast_exp2(pk_hi(xx)));
-                        pw[e] = kF16V ? pack_f16_rn(pk_lo(pp), pk_hi(pp)) : pack_bf16_rn(pk_lo(pp), pk_hi(pp));
+                        pw[e] = kF16 ? pack_f16_rn(pk_lo(pp), pk_hi(pp)) : pack_bf16_rn(pk_lo(pp), pk_hi(pp));
                         sum2[e & 1] = fadd2(sum2[e & 1], pp);
                     }
                     tmem_st32(tmem + lane_base + x * 128 + hf * 32, pw);
@@ -766,12 +772,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
         int ii = 0;
         bool ok = true;
-        Walk w;
-        while (ok && next_item(w)) {
-            if (!warp_wait(&B.l_full[ii & 1], (ii >> 1) & 1, abort_flag, a.status)) break;
+        auto convert_q = [&](uint32_t parity) {
+#pragma unroll 1
+            for (int x = 0; ok && x < 2; ++x) {
+                if (!(ok = warp_wait(&B.q_full[x], parity, abort_flag, a.status))) break;
+                uint4* q = reinterpret_cast<uint4*>(smem + kOffQ + x * kTileBytes);
+#pragma unroll 4
+                for (int i = r; i < kTileBytes / 16; i += 128) {
+                    const uint4 v = q[i];
+                    auto half2 = [](uint32_t u) { return pack_f16_rn(bf16lo(u) * 0.0625f, bf16hi(u) * 0.0625f); };
+                    q[i] = make_uint4(half2(v.x), half2(v.y), half2(v.z), half2(v.w));
+                }
+                fence_async_smem();
+                mbar_arrive(&B.q_f16[x]);
+            }
+        };
+        Walk w, ahead;
+        bool more = next_item(ahead);
+        if (kF16 && more) convert_q(0);
+        while (ok && more) {
+            w = ahead;
+            more = next_item(ahead);
+            // (the next item's Q comes once this one's scores are done, before its
+            // sums and outputs are)
+            if (kF16 && more) convert_q((ii + 1) & 1);
+            if (!ok || !warp_wait(&B.l_full[ii & 1], (ii >> 1) & 1, abort_flag, a.status)) break;
             const float* lx = xchg + 512 + (ii & 1) * 512;
             const float l[2] = {lx[r] + lx[256 + r], lx[128 + r] + lx[384 + r]};
-            const float vmul = kF16V ? a.v_scale[(int64_t)w.p.c * a.hkv + w.h] : 1.f;
+            const float vmul = kF16 ? a.kv_scale[(int64_t)w.p.c * a.hkv + w.h].y : 1.f;
 #pragma unroll 1
             for (int x = 0; x < 2; ++x) {
                 if (!(ok = warp_wait(&B.o_done[x], ii & 1, abort_flag, a.status))) break;
@@ -870,7 +898,7 @@ bool make_maps(const PrefillArgs& a, Maps& m)
            encode(&m.v, a.v_pool, 2, pdims, pstrides, pbox);
 }
 
-template <int kHD, bool kF16V>
+template <int kHD, bool kF16>
 kvattn_status launch(const PrefillArgs& a, cudaStream_t s)
 {
     if ((int64_t)a.num_blocks * a.hkv * a.block_size >= ((int64_t)1 << 31)) return KVATTN_ERR_UNSUPPORTED;
@@ -882,7 +910,7 @@ kvattn_status launch(const PrefillArgs& a, cudaStream_t s)
     constexpr int kSmem = Geo<kHD>::kSmemBytes;
     static_assert(kSmem <= 232448, "shared memory of a block");
     static SmemLimit limit;
-    if (limit.ensure(reinterpret_cast<const void*>(prefill_window_kernel<kHD, kF16V>), kSmem) != cudaSuccess)
+    if (limit.ensure(reinterpret_cast<const void*>(prefill_window_kernel<kHD, kF16>), kSmem) != cudaSuccess)
         return KVATTN_ERR_CUDA;
     const int64_t grid = std::min<int64_t>(items, num_sms());  // persistent: one CTA per SM
     const Divisors div{Divisor(a.hkv), Divisor(a.block_size / kPage)};
@@ -892,8 +920,8 @@ kvattn_status launch(const PrefillArgs& a, cudaStream_t s)
         b.cu_q_lens += c;
         b.prefix_lens += c;
         b.block_table += (int64_t)c * a.max_blocks;
-        if (b.v_scale) b.v_scale += (int64_t)c * a.hkv;
-        const kvattn_status st = cuda_status(launch_pdl(prefill_window_kernel<kHD, kF16V>, dim3((unsigned)grid),
+        if (b.kv_scale) b.kv_scale += (int64_t)c * a.hkv;
+        const kvattn_status st = cuda_status(launch_pdl(prefill_window_kernel<kHD, kF16>, dim3((unsigned)grid),
                                                         dim3(kThreads), kSmem, s, b, maps, div));
         if (st != KVATTN_OK) return st;
     }
@@ -904,7 +932,7 @@ kvattn_status launch(const PrefillArgs& a, cudaStream_t s)
 
 kvattn_status launch_prefill_window(const PrefillArgs& a, cudaStream_t s)
 {
-    if (a.v_scale) return a.d == 128 ? launch<128, true>(a, s) : KVATTN_ERR_UNSUPPORTED;
+    if (a.kv_scale) return a.d == 128 ? launch<128, true>(a, s) : KVATTN_ERR_UNSUPPORTED;
     return a.d == 128 ? launch<128, false>(a, s) : a.d == 64 ? launch<64, false>(a, s) : KVATTN_ERR_UNSUPPORTED;
 }
 

@@ -77,9 +77,11 @@ def check_attention(got, want, mag, dtype, what):
     """|got - want| within the roundings.  bf16: each weight is rounded to bf16 before P.V (half a step, 2^-8 relative,
     of each w |v|) and the output once (2^-8 |out|); the fp32 score sums (128 products of up to ~16 in all: 128 *
     2^-24 * 16 = 2^-13 absolute, so 2^-12 relative on a weight after its normalisation) and exp2 add less than 2^-11.
-    fp8: the weights are rounded to f16 (2^-11), as is V in a prefill.  f32: the scores' and the output's alone."""
+    fp8: the weights are rounded to f16 (2^-11), as are V and K in a prefill: 2^-11 for V, and for K errors of up to
+    2^-11 |q k| in each of 128 products, independent, so 2^-11 / sqrt(3) of sqrt(sum (q k)^2 / 128), which is about 1: six
+    standard deviations are 2^-9.2 of a score, and of a weight.  f32: the scores' and the output's alone."""
     assert np.all(np.isfinite(got)), f"{what}: not finite"
-    weight = {"bf16": 2.0 ** -8, "fp8": 2.0 ** -10, "f32": 0.0}[dtype] + 2.0 ** -11
+    weight = {"bf16": 2.0 ** -8, "fp8": 2.0 ** -10 + 2.0 ** -9, "f32": 0.0}[dtype] + 2.0 ** -11
     bound = weight * mag + HALF_STEP["f32" if dtype == "f32" else "bf16"] * (np.abs(want) + weight * mag) + 1e-30
     over = np.abs(got - want) - bound
     assert np.all(over <= 0), f"{what}: {over.max():.3e} past the bound"

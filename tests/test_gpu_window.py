@@ -122,8 +122,6 @@ def _chunk_case(kv, dtype, hq, hkv, d, chunks, window, sinks, block=16, seed=0, 
     masks = [seen(range(p, p + n), p + n, window, sinks) for p, n in chunks]
     wanted = [m.any(0) if len(m) else np.zeros(L, bool) for m, L in zip(masks, lens)]
     c = WindowCache(kv, dtype, hkv, d, lens, wanted, block=block, seed=seed)
-    if dtype == "fp8":  # the prefill's K: code * scale rounded to fp32 and then to bf16
-        c.k = [torch.from_numpy(x).float().to(torch.bfloat16).double().numpy() for x in c.k]
     cu = np.concatenate([[0], np.cumsum([n for _, n in chunks])]).astype(np.int32)
     q = _q(np.random.default_rng(seed + 1), (int(cu[-1]) + spare_rows, hq, d), dtype)
     cfg = kv.make_config(hq, hkv, d, kv.BF16)
