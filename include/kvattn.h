@@ -215,8 +215,10 @@ kvattn_status kvattn_rope_append_strided(const kvattn_config* cfg, const kvattn_
  * Errors: INVALID_ARG (null pointer, unknown layout or scaling, rope_base < 1,
  * factor < 1, low < 0, high <= low, original_len <= 0, negative amplitude, a
  * value that is not finite; the arguments of kvattn_rope_append_strided),
- * UNSUPPORTED (rotary_dim), CUDA; device: BAD_INDEX (that token is skipped).
- * num_tokens == 0 launches nothing.
+ * UNSUPPORTED (rotary_dim, more than 2^20 heads), CUDA; device: BAD_INDEX (that
+ * token is skipped).  num_tokens == 0 launches nothing.  The tokens of a call go
+ * to slots of their own: of two that name the same (sequence, position) the slot
+ * gets some elements of each.
  *
  * kvattn_rotary_append_fp8: the same into a kvattn_cache_fp8 (cfg->dtype
  * KVATTN_BF16, head_dim 128): q as above, and each rotated k row (its bf16
@@ -438,7 +440,9 @@ kvattn_status kvattn_decode_static_scratch(const kvattn_config* cfg, const kvatt
  * The other arguments, results and errors as kvattn_decode.
  *
  * kvattn_decode_window_fp8: the same over a kvattn_cache_fp8, as
- * kvattn_decode_fp8 (same workspace size).
+ * kvattn_decode_fp8 (same workspace size): q is taken in f16 over 16, exactly
+ * for magnitudes from 2^-10 to under 2^20 (smaller ones to within 2^-21; larger
+ * ones overflow).
  */
 size_t kvattn_decode_window_workspace_size(const kvattn_config* cfg, int32_t batch, int32_t max_seq_len,
                                            int32_t window, int32_t num_sinks, int32_t num_splits);
@@ -539,14 +543,14 @@ kvattn_status kvattn_prefill_chunk_fp8(const kvattn_config* cfg, const kvattn_ca
  * The other arguments, results and errors as kvattn_prefill_chunk.
  *
  * kvattn_prefill_window_fp8: the same over a kvattn_cache_fp8 (head_dim 128).
- * K is code * scale rounded to bf16 (q's type), V is code * scale rounded to
- * f16 over a power of two that is common to the chunk and KV head (within 2^-11
- * relative, or 2^-40 of the largest seen V of the head).  The pages that a
- * chunk sees are expanded into `workspace`, at least
- * kvattn_prefill_window_fp8_workspace_size(...) bytes (any alignment, any
- * contents, free again once the stream has passed the call), which bounds them
- * by max_q_len, window and num_sinks (0 for invalid arguments).  Errors in
- * addition: WORKSPACE_TOO_SMALL.
+ * K and V are code * scale rounded to f16 over a power of two each that is
+ * common to the chunk and KV head (within 2^-11 relative, or 2^-40 of the
+ * largest seen K or V of the head), and q is taken in f16 as by
+ * kvattn_decode_window_fp8.  The pages that a chunk sees are expanded into
+ * `workspace`, at least kvattn_prefill_window_fp8_workspace_size(...) bytes (any
+ * alignment, any contents, free again once the stream has passed the call),
+ * which bounds them by max_q_len, window and num_sinks (0 for invalid
+ * arguments).  Errors in addition: WORKSPACE_TOO_SMALL.
  */
 kvattn_status kvattn_prefill_window(const kvattn_config* cfg, const kvattn_cache* cache, const void* q,
                                     const int32_t* cu_q_lens, const int32_t* prefix_lens, const int32_t* block_table,

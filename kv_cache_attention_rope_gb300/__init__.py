@@ -571,19 +571,26 @@ def _table(block_table, rows: int, device: int):
     return _ptr(block_table, "block_table", _torch().int32, device), block_table.shape[1]
 
 
-def _out(out, q, dtype, device: int):
+def _empty(shape, dtype, like, stream):
+    """A dense tensor for the call's stream: allocated there, so that work of another stream neither still uses its
+    memory nor gets it before the call is through with it."""
+    torch = _torch()
+    with torch.cuda.stream(stream):  # (None: the current one)
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _out(out, q, dtype, device: int, stream):
     if out is None:
-        out = _torch().empty_like(q)
+        out = _empty(q.shape, q.dtype, q, stream)
     elif out.shape != q.shape:
         raise ValueError(f"out must be {list(q.shape)}, got {list(out.shape)}")
     return out, _ptr(out, "out", dtype, device)
 
 
-def _scratch(workspace, size, q, device: int):
+def _scratch(workspace, size, q, device: int, stream):
     """Pointer and bytes of the workspace; `size` (a function) says how much to allocate when there is none."""
-    torch = _torch()
     if workspace is None:
-        workspace = torch.empty(max(size(), 256), dtype=torch.uint8, device=q.device)
+        workspace = _empty((max(size(), 256),), _torch().uint8, q, stream)
     return _ptr(workspace, "workspace", workspace.dtype, device), workspace.nbytes
 
 
@@ -648,9 +655,9 @@ def _decode_window(fn, what, kind, cfg, cache, q, block_table, seq_lens, max_seq
     _shape(q, "q", B, cfg.num_q_heads, cfg.head_dim)
     _shape(seq_lens, "seq_lens", B)
     table, width = _table(block_table, B, device)
-    out, op = _out(out, q, dt, device)
+    out, op = _out(out, q, dt, device, stream)
     wp, nbytes = _scratch(workspace, lambda: decode_window_workspace_size(cfg, B, max_seq_len, window, num_sinks,
-                                                                          num_splits), q, device)
+                                                                          num_splits), q, device, stream)
     check(fn(ctypes.byref(cfg), desc, _ptr(q, "q", dt, device), table, width,
              _ptr(seq_lens, "seq_lens", _torch().int32, device), B, max_seq_len, window, num_sinks, num_splits, op, wp,
              nbytes, s), what)
@@ -709,7 +716,7 @@ def prefill_window(cfg: Config, cache: Cache, q, cu_q_lens, prefix_lens, block_t
             return out
     device, s = _here(stream)
     _, args = _prefill_window_args(Cache, cfg, cache, q, cu_q_lens, prefix_lens, block_table, device)
-    out, op = _out(out, q, q.dtype, device)
+    out, op = _out(out, q, q.dtype, device, stream)
     check(lib.kvattn_prefill_window(*args, max_q_len, q.shape[0], window, num_sinks, op, s), "kvattn_prefill_window")
     return out
 
@@ -732,9 +739,9 @@ def prefill_window_fp8(cfg: Config, cache: CacheFP8, q, cu_q_lens, prefix_lens, 
             return out
     device, s = _here(stream)
     n, args = _prefill_window_args(CacheFP8, cfg, cache, q, cu_q_lens, prefix_lens, block_table, device)
-    out, op = _out(out, q, q.dtype, device)
+    out, op = _out(out, q, q.dtype, device, stream)
     wp, nbytes = _scratch(workspace, lambda: prefill_window_fp8_workspace_size(
-        cfg, cache.block_size, block_table.shape[1], n, max_q_len, window, num_sinks), q, device)
+        cfg, cache.block_size, block_table.shape[1], n, max_q_len, window, num_sinks), q, device, stream)
     check(lib.kvattn_prefill_window_fp8(*args, max_q_len, q.shape[0], window, num_sinks, op, wp, nbytes, s),
           "kvattn_prefill_window_fp8")
     return out

@@ -163,9 +163,9 @@ def test_prefill_heads_and_blocks(kvattn_lib, dtype, hq, hkv, d, block):
     _prefill(kvattn_lib, dtype, hq, hkv, d, [(700, 290), (0, 77), (64, 1)], 150, 5, step=11, block=block, seed=hq)
 
 
-@pytest.mark.parametrize("scale", [2.0 ** -30, 2.0 ** 20])
-def test_prefill_fp8_v_of_any_size(kvattn_lib, scale):
-    """V far outside f16's range, its size differing by head and token."""
+@pytest.mark.parametrize("scale,k_scale", [(2.0 ** -30, 1.0), (2.0 ** 20, 2.0 ** 7), (1.0, 2.0 ** -14)])
+def test_prefill_fp8_k_and_v_of_any_size(kvattn_lib, scale, k_scale):
+    """K and V far outside f16's range, V's size differing by head and token, q as small or large as K is large or small."""
     kv = kvattn_lib
     lens, window, sinks = [300, 70], 120, 4
     chunks = [(100, 200), (0, 70)]
@@ -176,9 +176,10 @@ def test_prefill_fp8_v_of_any_size(kvattn_lib, scale):
     times = scale * 2.0 ** torch.tensor([0.0, 7.0], device="cuda")[:, None, None]    # by head ...
     times = times * 2.0 ** -(torch.arange(16, device="cuda") % 4).float()            # ... and by token
     pool[..., 4160:] = (scales * times).view(torch.uint8)
-    c.k = [torch.from_numpy(x).float().to(torch.bfloat16).double().numpy() for x in c.k]
+    pool[..., 4096:4160] = (pool[..., 4096:4160].contiguous().view(torch.float32) * k_scale).view(torch.uint8)
+    c.k = [x * k_scale for x in c.k]
     c.v = [x * times[:, 0].double().cpu().numpy().T[np.arange(len(x)) % 16][:, :, None] for x in c.v]
-    q = _q(np.random.default_rng(1), (270, 8, 128), "bf16")
+    q = _q(np.random.default_rng(1), (270, 8, 128), "bf16") / k_scale
     cfg = kv.make_config(8, 2, 128, kv.BF16)
     out = kv.prefill_window_fp8(cfg, c.cache, q.cuda(), torch.tensor([0, 200, 270], dtype=torch.int32).cuda(),
                                 torch.tensor([100, 0], dtype=torch.int32).cuda(), c.d_table, 200, window, sinks)
@@ -478,6 +479,28 @@ def test_streams(kvattn_lib):
                               workspace=torch.empty(1 << 20, dtype=torch.uint8, device="cuda"))
     side.synchronize()
     assert torch.equal(a, want) and torch.equal(a2, want) and torch.equal(b, want_c)
+
+
+def test_stream_allocations(kvattn_lib):
+    """What a call on a side stream allocates for itself is not given to the current stream while the call waits."""
+    kv = kvattn_lib
+    c = WindowCache(kv, "fp8", 2, 128, [500], [np.ones(500, bool)], seed=4)
+    cfg = kv.make_config(8, 2, 128, kv.BF16)
+    q = _q(np.random.default_rng(5), (60, 8, 128), "bf16").cuda()
+    cu, prefix = torch.tensor([0, 60], dtype=torch.int32).cuda(), torch.tensor([440], dtype=torch.int32).cuda()
+    call = lambda stream: kv.prefill_window_fp8(cfg, c.cache, q, cu, prefix, c.d_table, 60, 99, 4, stream=stream)
+    want = call(None)
+    size = kv.prefill_window_fp8_workspace_size(cfg, 16, c.d_table.shape[1], 1, 60, 99, 4)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+    got = call(side)
+    for n in (size, q.numel() * 2):
+        torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
 
 
 @pytest.mark.parametrize("dtype,hkv,d", [("bf16", 8, 128), ("bf16", 8, 64), ("f32", 4, 128)])

@@ -49,6 +49,7 @@ def test_rotary_refusals(kv, fp8):
         assert _rotary(kv, form=f, fp8=fp8) == uns
     assert _rotary(kv, cfg=kv.make_config(8, 2, 128, kv.BF16, rope_base=0.5), fp8=fp8) == bad
     assert _rotary(kv, cfg=kv.make_config(8, 2, 96, kv.BF16), fp8=fp8) == uns
+    assert _rotary(kv, cfg=kv.make_config(2 ** 21, 2 ** 18, 128, kv.BF16), fp8=fp8) == uns
     assert _rotary(kv, T=-1, fp8=fp8) == bad
     assert _rotary(kv, nseq=0, fp8=fp8) == bad
     assert _rotary(kv, maxb=0, fp8=fp8) == bad
