@@ -525,7 +525,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (elect_one()) tc_commit(b);
                 __syncwarp();
             };
-            auto wait = [&](uint64_t* b, uint32_t parity) { return warp_wait(b, parity, abort_flag, a.status); };
+            auto wait = [&](uint64_t* b, uint32_t parity) {
+                if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
+                return warp_wait(b, parity, abort_flag, a.status);
+            };
             // Order per tile t: PV_A(t) S_A(t+1) PV_B(t) S_B(t+1); S_x(t+1)
             // overwrites S_x's columns after PV_x(t) has read P_x(t) from them
             // (tensor operations of one thread run in issue order).
@@ -643,9 +646,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // a named barrier of that pair per tile.
         // These warps never stop early: after an abort their waits return at once
         // and they run on, over whatever TMEM holds, to the end of their items
-        // (nothing of it is reported good).  Each branch that is not here saves
-        // about 100 cycles of a tile's 1200 (16 chunks, window 4096: 315 us with the
-        // wait's result looked at and the maximum's three cases in branches, 307).
+        // (nothing of it is reported good).  What a tile costs is its instructions'
+        // way to the warps as much as their number: each branch that is not here
+        // saves about 100 cycles of 1200 (16 chunks, window 4096: 315 us with the
+        // wait's result looked at and the maximum's three cases in branches, 307),
+        // and one body for A and B, whose states change places after each, stays in
+        // the instruction cache where two do not (windows of 128 and 1024: 41.9 and
+        // 103 us, two bodies 47.7 and 107).
         const int hf = (warp - 4) >> 2;
         const int quarter = warp & 3;        // TMEM lanes 32*quarter .. +31
         const int r = quarter * 32 + lane;   // row of the tile
@@ -658,102 +665,110 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float sl2 = kF16 ? a.kv_scale[(int64_t)w.p.c * a.hkv + w.h].x * 16.f * a.scale_log2 : a.scale_log2;
             const int col0 = w.g.gap * kPage;
             const int tok = w.p.pos0 - col0;                    // column of the item's first token
-            float m_of[2] = {-INFINITY, -INFINITY}, l_of[2] = {0.f, 0.f};
-            for (int t = 0; t < w.g.tiles; ++t) {
+            float m_now = -INFINITY, l_now = 0.f, m_other = -INFINITY, l_other = 0.f;  // of A and B in turn
+            auto swap = [&] {
+                const float m = m_now, l = l_now;
+                m_now = m_other;
+                l_now = l_other;
+                m_other = m;
+                l_other = l;
+            };
+#pragma unroll 1
+            for (int st = 0; st < 2 * w.g.tiles; ++st) {
+                const int t = st >> 1, x = st & 1;
+                const uint32_t tS = tmem + lane_base + x * 128 + hf * 64;
+                const uint32_t tO = tmem + lane_base + 256 + x * 128 + hf * (kHD / 2);
+                const int p0 = tok + ((x * kBM + quarter * 32) >> lg);  // column of the warp's first row
+                const int p1 = p0 + ((32 >> lg) - 1);                   // ... of its last
+                const int pr = p0 + (lane >> lg);                       // ... of this thread's
+                const int c = t * kBN + hf * 64;                        // first column of this half
+                const bool some = c + 63 > p0 || (c <= p1 - a.window && c + 63 >= a.sinks);
+                wait_or_abort(&B.s_full[x], g & 1, abort_flag, a.status);
+                __syncwarp();
+                if (x == 1 && w.p.rows <= step / 2) {  // B has no rows: P_B may be anything
+                    mbar_arrive(&B.p_full[1]);
+                    ++g;
+                    swap();
+                    continue;
+                }
+                uint32_t sv[64];
+                tc_fence_after();
+                tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+                tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+                tmem_ld_wait();
+                if (some) {  // bit e: column c + e is seen
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const uint32_t tS = tmem + lane_base + x * 128 + hf * 64;
-                    const uint32_t tO = tmem + lane_base + 256 + x * 128 + hf * (kHD / 2);
-                    const int p0 = tok + ((x * kBM + quarter * 32) >> lg);  // column of the warp's first row
-                    const int p1 = p0 + ((32 >> lg) - 1);                   // ... of its last
-                    const int pr = p0 + (lane >> lg);                       // ... of this thread's
-                    const int c = t * kBN + hf * 64;                        // first column of this half
-                    const bool some = c + 63 > p0 || (c <= p1 - a.window && c + 63 >= a.sinks);
-                    wait_or_abort(&B.s_full[x], g & 1, abort_flag, a.status);
-                    __syncwarp();
-                    if (x == 1 && w.p.rows <= step / 2) {  // B has no rows: P_B may be anything
-                        mbar_arrive(&B.p_full[1]);
-                        ++g;
-                        continue;
+                    for (int q = 0; q < 2; ++q) {
+                        const int cq = c + 32 * q;
+                        const uint32_t m = low_bits(pr - cq + 1) & (~low_bits(pr - a.window - cq + 1) | low_bits(a.sinks - cq));
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!(m & (1u << e))) sv[32 * q + e] = __float_as_uint(-INFINITY);
                     }
-                    uint32_t sv[64];
-                    tc_fence_after();
-                    tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-                    tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
-                    tmem_ld_wait();
-                    if (some) {  // bit e: column c + e is seen
+                }
+                float m4[4];
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            const int cq = c + 32 * q;
-                            const uint32_t m = low_bits(pr - cq + 1) & (~low_bits(pr - a.window - cq + 1) | low_bits(a.sinks - cq));
+                for (int q = 0; q < 4; ++q)
+                    m4[q] = fmaxf(__uint_as_float(sv[2 * q]), __uint_as_float(sv[2 * q + 1]));
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!(m & (1u << e))) sv[32 * q + e] = __float_as_uint(-INFINITY);
-                        }
-                    }
-                    float m4[4];
+                for (int e = 8; e < 64; e += 8)
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        m4[q] = fmaxf(__uint_as_float(sv[2 * q]), __uint_as_float(sv[2 * q + 1]));
+                        m4[q] = max3(m4[q], __uint_as_float(sv[e + 2 * q]), __uint_as_float(sv[e + 2 * q + 1]));
+                const float hm = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                float* slot = xchg + x * 256;
+                slot[hf * 128 + r] = hm;
+                bar_sync(1 + quarter, 64);
+                const float m_tile = fmaxf(hm, slot[(1 - hf) * 128 + r]) * sl2;
+                const bool none = m_now == -INFINITY;  // no seen key so far
+                const bool rescale = !none && m_tile > m_now + 8.f;
+                const float m_new = none || rescale ? m_tile : m_now;
+                const float alpha = none ? 1.f : fast_exp2(m_now - m_new);
+                m_now = m_new;
+                // P = 2^(s*scale*log2e - m) as bf16 into columns 32hf..32hf+31 of
+                // S_x (both halves have read their S before the barrier); a row
+                // with no seen key yet subtracts +inf so every p is 0.  The row sum
+                // adds the fp32 p (their bf16 roundings differ by at most 2^-8
+                // relative, at random).
+                uint32_t pw[32];
+                const float msub = m_now == -INFINITY ? INFINITY : m_now;
+                const uint64_t scale2 = pk(sl2, sl2), msub2 = pk(-msub, -msub);
+                uint64_t sum2[2] = {0, 0};
 #pragma unroll
-                    for (int e = 8; e < 64; e += 8)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            m4[q] = max3(m4[q], __uint_as_float(sv[e + 2 * q]), __uint_as_float(sv[e + 2 * q + 1]));
-                    const float hm = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                    float* slot = xchg + x * 256;
-                    slot[hf * 128 + r] = hm;
-                    bar_sync(1 + quarter, 64);
-                    const float m_tile = fmaxf(hm, slot[(1 - hf) * 128 + r]) * sl2;
-                    const bool none = m_of[x] == -INFINITY;  // no seen key so far
-                    const bool rescale = !none && m_tile > m_of[x] + 8.f;
-                    const float m_new = none || rescale ? m_tile : m_of[x];
-                    const float alpha = none ? 1.f : fast_exp2(m_of[x] - m_new);
-                    m_of[x] = m_new;
-                    // P = 2^(s*scale*log2e - m) as bf16 into columns 32hf..32hf+31 of
-                    // S_x (both halves have read their S before the barrier); a row
-                    // with no seen key yet subtracts +inf so every p is 0.  The row sum
-                    // adds the fp32 p (their bf16 roundings differ by at most 2^-8
-                    // relative, at random).
-                    uint32_t pw[32];
-                    const float msub = m_of[x] == -INFINITY ? INFINITY : m_of[x];
-                    const uint64_t scale2 = pk(sl2, sl2), msub2 = pk(-msub, -msub);
-                    uint64_t sum2[2] = {0, 0};
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const uint64_t xx =
-                            ffma2(pk(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), scale2, msub2);
-                        const uint64_t pp = pk(fast_exp2(pk_lo(xx)), fast_exp2(pk_hi(xx)));
-                        pw[e] = kF16 ? pack_f16_rn(pk_lo(pp), pk_hi(pp)) : pack_bf16_rn(pk_lo(pp), pk_hi(pp));
-                        sum2[e & 1] = fadd2(sum2[e & 1], pp);
-                    }
-                    tmem_st32(tmem + lane_base + x * 128 + hf * 32, pw);
-                    l_of[x] = l_of[x] * alpha + ((pk_lo(sum2[0]) + pk_hi(sum2[0])) + (pk_lo(sum2[1]) + pk_hi(sum2[1])));
-                    // O_x (this half's columns): PV_x(t-1) completed before S_x(t) was
-                    // reported.  The whole warp rescales if any of its rows must (alpha
-                    // is 1 for the others).
-                    if (__any_sync(0xffffffffu, rescale && t > 0)) {
-#pragma unroll 1
-                        for (int q = 0; q < kHD / 64; ++q) {
-                            uint32_t v[32];
-                            tmem_ld32(tO + q * 32, v);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-                            tmem_st32(tO + q * 32, v);
-                        }
-                    }
-                    tmem_st_wait();
-                    tc_fence_before();
-                    mbar_arrive(&B.p_full[x]);
-                    g += x;
+                for (int e = 0; e < 32; ++e) {
+                    const uint64_t xx =
+                        ffma2(pk(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), scale2, msub2);
+                    const uint64_t pp = pk(fast_exp2(pk_lo(xx)), fast_exp2(pk_hi(xx)));
+                    pw[e] = kF16 ? pack_f16_rn(pk_lo(pp), pk_hi(pp)) : pack_bf16_rn(pk_lo(pp), pk_hi(pp));
+                    sum2[e & 1] = fadd2(sum2[e & 1], pp);
                 }
+                tmem_st32(tmem + lane_base + x * 128 + hf * 32, pw);
+                l_now = l_now * alpha + ((pk_lo(sum2[0]) + pk_hi(sum2[0])) + (pk_lo(sum2[1]) + pk_hi(sum2[1])));
+                // O_x (this half's columns): PV_x(t-1) completed before S_x(t) was
+                // reported.  The whole warp rescales if any of its rows must (alpha
+                // is 1 for the others).
+                if (__any_sync(0xffffffffu, rescale && t > 0)) {
+#pragma unroll 1
+                    for (int q = 0; q < kHD / 64; ++q) {
+                        uint32_t v[32];
+                        tmem_ld32(tO + q * 32, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+                        tmem_st32(tO + q * 32, v);
+                    }
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&B.p_full[x]);
+                g += x;
+                swap();
             }
             // this item's row sums to the output warps (two items' worth: the sums
             // of item ii - 2 were read before S_x of this item was issued)
             float* lx = xchg + 512 + (ii & 1) * 512;  // [2 halves][2 tiles][128 rows]
-            lx[(hf * 2 + 0) * 128 + r] = l_of[0];
-            lx[(hf * 2 + 1) * 128 + r] = l_of[1];
+            lx[(hf * 2 + 0) * 128 + r] = l_now;
+            lx[(hf * 2 + 1) * 128 + r] = l_other;
             mbar_arrive(&B.l_full[ii & 1]);
             ++ii;
         }
