@@ -223,7 +223,7 @@ struct Fp8Tile {
     }
 };
 
-// Resident warps per SM that the register budgets leave room for.  Measured: a
+// Resident warps per SM that the registers leave room for.  Measured: a
 // bf16 tile at D = 128, with the next one on its way, wants 200 registers (32 / 8
 // heads, 32 sequences, window 4096: 88.5 us with 8 warps, 91.9 with 12, 100.7
 // with 16, which spill); an fp8 page that is converted while the warp's next two
