@@ -325,21 +325,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     const bool sorted = n_pairs <= kMaxPairs;
-    static_assert(kMaxPairs <= kThreads, "a thread ranks one pair");
+    static_assert(kMaxPairs == kThreads, "a thread ranks one pair");
     if (sorted) {
+        // rank = pairs with more tiles, or as many and a smaller index: with larger keys
         Pair mine{0, 0, 0, 0};
-        int my_tiles = 0;
+        int key = -1;
         if ((int)threadIdx.x < n_pairs) {
             mine = make_pair(a, before, step, threadIdx.x);
-            my_tiles = pages_of(a, mine).tiles;
-            scratch[threadIdx.x] = my_tiles;
+            key = min(pages_of(a, mine).tiles, 1 << 20) * kMaxPairs + (kMaxPairs - 1 - (int)threadIdx.x);
         }
+        scratch[threadIdx.x] = key;
         __syncthreads();
-        if ((int)threadIdx.x < n_pairs) {  // rank = pairs with more tiles, or as many and a smaller index
+        if ((int)threadIdx.x < n_pairs) {
             int rank = 0;
-            for (int q = 0; q < n_pairs; ++q) {
-                const int lq = scratch[q];
-                rank += (lq > my_tiles) || (lq == my_tiles && q < (int)threadIdx.x);
+#pragma unroll 4
+            for (int q = 0; q < (n_pairs + 3) / 4; ++q) {
+                const int4 o = reinterpret_cast<const int4*>(scratch)[q];
+                rank += (o.x > key) + (o.y > key) + (o.z > key) + (o.w > key);
             }
             sorted_pairs[rank] = mine;
         }
