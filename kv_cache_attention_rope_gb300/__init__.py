@@ -509,8 +509,7 @@ def _here(stream):
     torch = _torch()
     device = torch.cuda.current_device()
     if not _marshal_ready:
-        _marshal.setup(torch.bfloat16, torch.float32, torch.int32, torch._C._cuda_getDevice,
-                       torch._C._cuda_getCurrentRawStream)
+        _marshal.setup(torch._C._to_dlpack, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
         _marshal_ready = True
     if stream is None:
         return device, torch._C._cuda_getCurrentRawStream(device)
