@@ -262,6 +262,9 @@ __global__ void __launch_bounds__(warps_per_sm(kKind, kD, kG) * 32, 1)
     const int b = seg / a.hkv, h = seg - b * a.hkv;
     const int G = a.hq / a.hkv;
     const int64_t q0 = ((int64_t)b * a.hq + h * G) * kD;  // first element of the group's queries and outputs
+    const int32_t* trow = a.block_table + (int64_t)b * a.max_blocks;
+    const bool contiguous = a.max_blocks == 1;  // its only block is looked up beside the length
+    const int32_t block0 = contiguous ? trow[0] : -1;
     const int L = a.seq_lens[b];
 
     // per-head rows of the warps' (and, last, the CTA's) outputs and (max, sum)
@@ -285,12 +288,11 @@ __global__ void __launch_bounds__(warps_per_sm(kKind, kD, kG) * 32, 1)
     auto first_token = [&](int t) { return (t >= pc.sink_tiles ? t + pc.gap : t) * kTile; };
     const int n = cluster * warps, first = rank * warps + warp;  // this warp: tiles first, first + n, ...
     const int mine = first < win.tiles ? (win.tiles - 1 - first) / n + 1 : 0;
-    const int32_t* trow = a.block_table + (int64_t)b * a.max_blocks;
     // row in the pool of this lane's tile of a batch of 32 (-1: none)
     auto lookup = [&](int base) -> int64_t {
         if (base + lane >= mine) return -1;
         const int tok = first_token(first + (base + lane) * n);
-        const int32_t id = trow[tok / a.block_size];
+        const int32_t id = contiguous ? block0 : trow[tok / a.block_size];
         if (id < 0 || id >= a.num_blocks) {
             record_error(a.status, KVATTN_ERR_BAD_INDEX);
             return -1;
@@ -670,13 +672,16 @@ bool launch_decode_direct(const DecodeArgs& a, int32_t max_tiles, cudaStream_t s
     if (tiles > most || segs * 8 > INT32_MAX) return false;
     // One wave of warps: the most warps per CTA that let every segment be
     // resident (a quarter of the SM's when not even that does), at most 8;
-    // then CTAs per segment; but no warp without a tile.
+    // then CTAs per segment; but no warp without a tile, and no second CTA for
+    // fewer than 4 tiles per warp, which cost less than the cluster's launch and
+    // merge (1 sequence, 32 / 8 heads of bf16: 18 tiles 5.1 us in one CTA and 5.7
+    // in two; 34 tiles 6.6 in two and 5.9 in four).
     const int cap = warps_per_sm(kind, a.d, G);
     const int64_t sms = num_sms();
     int warps = 8;
     while (warps > cap / 4 && sms * (cap / warps) < segs) --warps;
     int cluster = 1;
-    while (cluster < 8 && warps == 8 && sms * (cap / 8) >= 2 * cluster * segs && 16 * cluster <= max_tiles) cluster *= 2;
+    while (max_tiles >= 32 && cluster < 8 && warps == 8 && sms * (cap / 8) >= 2 * cluster * segs && 16 * cluster <= max_tiles) cluster *= 2;
     warps = std::min(warps, max_tiles);
     *st = direct_dispatch(a, warps, cluster, s);
     return true;
