@@ -555,51 +555,90 @@ __global__ void __launch_bounds__(warps_per_sm(kKind, kD, kG) * 32, 1)
     }
     __syncthreads();
 
-    // ---- the warps' states, then the CTAs'
-    auto store = [&](int e, float num, float den) {
-        const float o = den > 0.f ? num / den : 0.f;
-        if constexpr (kKind == kF32Cache) reinterpret_cast<float*>(a.out)[q0 + e] = o;
-        else reinterpret_cast<__nv_bfloat16*>(a.out)[q0 + e] = __float2bfloat16_rn(o);
+    // ---- the warps' states, then the CTAs', kV dims a thread: four, or one where
+    // that leaves most threads idle (12 heads of 64 without groups, fp32, 8
+    // sequences, window 256: 4.3 us, with four 4.45)
+    constexpr int kV = kKind == kF32Cache && kG * kD <= 128 ? 1 : 4;
+    struct Dims {
+        float v[kV];
     };
-    for (int e = tid; e < G * kD; e += blockDim.x) {
-        const int g = e / kD, d = e - g * kD;
-        float M = -INFINITY, num = 0.f, den = 0.f;
-#pragma unroll 4
-        for (int w = 0; w < warps; ++w) M = fmaxf(M, ml_of(w, g)[0]);
-        if (M != -INFINITY) {
-#pragma unroll 4
-            for (int w = 0; w < warps; ++w) {
-                const float f = exp2f(ml_of(w, g)[0] - M);  // a warp without a key: 0
-                num += f * row_of(w, g)[d];
-                den += f * ml_of(w, g)[1];
+    auto read = [](const float* p) {
+        Dims o;
+        if constexpr (kV == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(p);
+            o.v[0] = x.x;
+            o.v[1] = x.y;
+            o.v[2] = x.z;
+            o.v[3] = x.w;
+        } else {
+            o.v[0] = *p;
+        }
+        return o;
+    };
+    auto write = [](float* p, const Dims& o) {
+        if constexpr (kV == 4) *reinterpret_cast<float4*>(p) = make_float4(o.v[0], o.v[1], o.v[2], o.v[3]);
+        else *p = o.v[0];
+    };
+    auto store = [&](int e, Dims num, float den) {
+        const float inv = den > 0.f ? 1.f / den : 0.f;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) num.v[i] *= inv;
+        if constexpr (kKind == kF32Cache)
+            write(reinterpret_cast<float*>(a.out) + q0 + e, num);
+        else
+            *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + q0 + e) =
+                make_uint2(pack_bf16_rn(num.v[0], num.v[1]), pack_bf16_rn(num.v[2], num.v[3]));
+    };
+    // The merge of `n` states (at most 8, their loads under way together): outputs
+    // at row(i), (max, sum) at stat(i).
+    auto merge = [&](int n, auto row, auto stat, Dims& num, float& M, float& den) {
+        float2 s[8];
+        Dims o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            s[i] = make_float2(-INFINITY, 0.f);
+            if (i < n) {
+                s[i] = *reinterpret_cast<const float2*>(stat(i));
+                o[i] = read(row(i));
             }
         }
+        M = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) M = fmaxf(M, s[i].x);
+#pragma unroll
+        for (int k = 0; k < kV; ++k) num.v[k] = 0.f;
+        den = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i < n && s[i].x != -INFINITY) {  // a state without a key has no weight
+                const float f = exp2f(s[i].x - M);
+#pragma unroll
+                for (int k = 0; k < kV; ++k) num.v[k] += f * o[i].v[k];
+                den += f * s[i].y;
+            }
+        }
+    };
+    for (int e = kV * tid; e < G * kD; e += kV * blockDim.x) {
+        const int g = e / kD, d = e - g * kD;
+        Dims num;
+        float M, den;
+        merge(warps, [&](int w) { return row_of(w, g) + d; }, [&](int w) { return ml_of(w, g); }, num, M, den);
         if (cluster == 1) {
             store(e, num, den);
         } else {
-            row_of(warps, g)[d] = num;
-            if (d == 0) {
-                ml_of(warps, g)[0] = M;
-                ml_of(warps, g)[1] = den;
-            }
+            write(row_of(warps, g) + d, num);
+            if (d == 0) *reinterpret_cast<float2*>(ml_of(warps, g)) = make_float2(M, den);
         }
     }
     if (cluster > 1) {
         cg::cluster_group cl = cg::this_cluster();
         cl.sync();
-        for (int e = rank * blockDim.x + tid; e < G * kD; e += n * 32) {
+        for (int e = kV * (rank * blockDim.x + tid); e < G * kD; e += kV * n * 32) {
             const int g = e / kD, d = e - g * kD;
-            float M = -INFINITY, num = 0.f, den = 0.f;
-            for (int r = 0; r < cluster; ++r) M = fmaxf(M, cl.map_shared_rank(ml_of(warps, g), r)[0]);
-            if (M != -INFINITY) {
-                for (int r = 0; r < cluster; ++r) {
-                    const float* o = cl.map_shared_rank(row_of(warps, g), r);
-                    const float* s = cl.map_shared_rank(ml_of(warps, g), r);
-                    const float f = exp2f(s[0] - M);
-                    num += f * o[d];
-                    den += f * s[1];
-                }
-            }
+            Dims num;
+            float M, den;
+            merge(cluster, [&](int r) { return cl.map_shared_rank(row_of(warps, g) + d, r); },
+                  [&](int r) { return cl.map_shared_rank(ml_of(warps, g), r); }, num, M, den);
             store(e, num, den);
         }
         cl.sync();  // the others' shared memory stays until it has been read
@@ -674,8 +713,8 @@ bool launch_decode_direct(const DecodeArgs& a, int32_t max_tiles, cudaStream_t s
     // resident (a quarter of the SM's when not even that does), at most 8;
     // then CTAs per segment; but no warp without a tile, and no second CTA for
     // fewer than 4 tiles per warp, which cost less than the cluster's launch and
-    // merge (1 sequence, 32 / 8 heads of bf16: 18 tiles 5.1 us in one CTA and 5.7
-    // in two; 34 tiles 6.6 in two and 5.9 in four).
+    // merge (18 tiles: 8 sequences of 12 fp32 heads of 64 4.4 us in one CTA and
+    // 5.25 in two, 1 of 32 / 8 fp8 heads 5.1 and 5.3, of bf16 4.9 and 4.95).
     const int cap = warps_per_sm(kind, a.d, G);
     const int64_t sms = num_sms();
     int warps = 8;
