@@ -549,7 +549,7 @@ kvattn_status launch_prefill_window_fp8(const PrefillArgs& pa, const void* pool,
     if (e != cudaSuccess) return cuda_status(e);
     // one wave of CTAs, but no warp without a page; two waves, which balance the
     // SMs better, while a warp keeps two pages (16 chunks of 512 queries, window
-    // 4096: 378 against 392 us with one wave; 8 with 1024: 84 against 82)
+    // 4096: 365 against 378 us with one wave)
     const int64_t pairs = (int64_t)pa.num_chunks * pa.hkv, pages = L.per_chunk * (pa.block_size / 16);
     const int64_t one = std::min(wave / pairs, (pages + kExpandWarps - 1) / kExpandWarps);
     const int64_t two = std::min(2 * wave / pairs, pages / (2 * kExpandWarps));
