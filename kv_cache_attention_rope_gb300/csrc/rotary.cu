@@ -137,11 +137,12 @@ __device__ __forceinline__ uint2 codes8(const uint4& v, float inv)
     return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-// kTPT threads per token.  Residency: 8 CTAs per SM (7 where the half layout
+// kTPT threads per token (kSplit: and 2^parts_log2 CTAs, each with a share of its
+// heads).  Residency: 8 CTAs per SM (7 where the half layout
 // keeps twice the twiddles) at a few spilled bytes beat 5 without: 8320 tokens of
 // 32 / 8 heads at D = 128, half 34.8 against 42.9 us, adjacent 32.8 against 37.5.
-template <bool kBF16, int kD, bool kHalf, bool kFP8, int kTPT>
-__global__ void __launch_bounds__(kThreads, (kHalf ? 7 : 8)) rotary_append_kernel(const __grid_constant__ RotaryArgs a)
+template <bool kBF16, int kD, bool kHalf, bool kFP8, int kTPT, bool kSplit>
+__global__ void __launch_bounds__(kThreads, (kHalf ? 7 : 8)) rotary_append_kernel(const __grid_constant__ RotaryArgs a, const int parts_log2)
 {
     pdl_wait();
     constexpr int kE = kBF16 ? 2 : 4;
@@ -156,10 +157,14 @@ __global__ void __launch_bounds__(kThreads, (kHalf ? 7 : 8)) rotary_append_kerne
 
     static_assert(kTPT == 32 || kTPT == kThreads, "a token's threads are a warp or the CTA");
     const int tid = kTPT == kThreads ? (int)threadIdx.x : (int)threadIdx.x % kTPT;  // thread of the token
-    const int t = kTPT == kThreads ? blockIdx.x : blockIdx.x * (kThreads / kTPT) + threadIdx.x / kTPT;
+    static_assert(!kSplit || kTPT == kThreads, "parts are CTAs");
+    const int lp = kSplit ? parts_log2 : 0, part = kSplit ? blockIdx.x & ((1 << lp) - 1) : 0;
+    const int t = kTPT == kThreads ? blockIdx.x >> lp : blockIdx.x * (kThreads / kTPT) + threadIdx.x / kTPT;
     if (kTPT != kThreads && t >= a.num_tokens) return;
     float2* tw = tws[kTPT == kThreads ? 0 : threadIdx.x / kTPT];
-    const int u = tid % kU, hg = tid / kU;
+    const int u = tid % kU, hg = tid / kU + part * kGroups;  // unit, first head
+    const int hs = kGroups << lp;                            // heads between a thread's
+    const int vg = tid + part * kTPT, vs = kTPT << lp;       // V vectors: first, step
     // element offsets of the unit's two vectors in a head, and whether they turn:
     // neighbouring units hold neighbouring vectors, so a warp's accesses are whole lines
     const int nu = a.rot / (2 * kEPV);  // units that turn (half layout)
@@ -183,10 +188,10 @@ __global__ void __launch_bounds__(kThreads, (kHalf ? 7 : 8)) rotary_append_kerne
     for (int i = 0; i < kFlightV; ++i) xv[i] = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < kFlight; ++i)
-        if (hg + i * kGroups < heads) load(hg + i * kGroups, xa[i], xb[i]);
+        if (hg + i * hs < heads) load(hg + i * hs, xa[i], xb[i]);
 #pragma unroll
     for (int i = 0; i < kFlightV; ++i)
-        if (tid + i * kTPT < nvec) xv[i] = *reinterpret_cast<const uint4*>(vrow + (tid + i * kTPT) * 16);
+        if (vg + i * vs < nvec) xv[i] = *reinterpret_cast<const uint4*>(vrow + (vg + i * vs) * 16);
 
     const int pos = a.positions[t], seq = a.seq_ids[t];
     bool ok = pos >= 0 && seq >= 0 && seq < a.num_seqs && pos / a.block_size < a.max_blocks;
@@ -252,37 +257,48 @@ __global__ void __launch_bounds__(kThreads, (kHalf ? 7 : 8)) rotary_append_kerne
         char* row = (char*)a.v_pool + ((blk * a.hkv + j / kVPH) * a.block_size + off) * (int64_t)(kD * kE);
         *reinterpret_cast<uint4*>(row + (j % kVPH) * 16) = x;
     };
-    for (int h0 = hg; h0 < heads; h0 += kFlight * kGroups) {
+    for (int h0 = hg; h0 < heads; h0 += kFlight * hs) {
         if (h0 != hg) {
 #pragma unroll
             for (int i = 0; i < kFlight; ++i)
-                if (h0 + i * kGroups < heads) load(h0 + i * kGroups, xa[i], xb[i]);
+                if (h0 + i * hs < heads) load(h0 + i * hs, xa[i], xb[i]);
         }
 #pragma unroll
         for (int i = 0; i < kFlight; ++i)
-            if (h0 + i * kGroups < heads) finish(h0 + i * kGroups, xa[i], xb[i]);
+            if (h0 + i * hs < heads) finish(h0 + i * hs, xa[i], xb[i]);
     }
 #pragma unroll
     for (int i = 0; i < kFlightV; ++i)
-        if (tid + i * kTPT < nvec) put_v(tid + i * kTPT, xv[i]);
-    for (int j = tid + kFlightV * kTPT; j < nvec; j += kTPT)
+        if (vg + i * vs < nvec) put_v(vg + i * vs, xv[i]);
+    for (int j = vg + kFlightV * vs; j < nvec; j += vs)
         put_v(j, *reinterpret_cast<const uint4*>(vrow + j * 16));
 }
 
 template <bool kBF16, int kD, bool kHalf, bool kFP8>
 kvattn_status launch(const RotaryArgs& a, cudaStream_t s)
 {
-    auto run = [&](auto kern, int tpt) {
+    auto run = [&](auto kern, int tpt, int parts_log2) {
         const int per = kThreads / tpt;
-        return cuda_status(launch_pdl(kern, dim3((a.num_tokens + per - 1) / per), dim3(kThreads), 0, s, a));
+        return cuda_status(launch_pdl(kern, dim3(((a.num_tokens + per - 1) / per) << parts_log2), dim3(kThreads), 0, s, a,
+                                      parts_log2));
     };
     // A CTA per token, or a warp when the token is small and there are enough of
     // them for every SM's warps (8320 tokens, CTA and warp: 32 / 8 heads of 128
     // 34.8 and 40.1 us; 16 / 8 of 128 32.1 and 27.8; 12 / 12 of 64 17.4 and 12.1;
     // 64 tokens of those 2.4 and 3.0).
     const int units = (a.hq + a.hkv) * (kD / (kBF16 ? 16 : 8));
-    return units <= 192 && a.num_tokens >= 2048 ? run(rotary_append_kernel<kBF16, kD, kHalf, kFP8, 32>, 32)
-                                                : run(rotary_append_kernel<kBF16, kD, kHalf, kFP8, 128>, 128);
+    if (units <= 192 && a.num_tokens >= 2048) return run(rotary_append_kernel<kBF16, kD, kHalf, kFP8, 32, false>, 32, 0);
+    // Two or four CTAs for a large token: as many as one wave of CTAs has room for
+    // (fp32, 32 / 32 heads of 128, 8 and 300 tokens: 5.2 -> 2.5 and 5.9 -> 4.8 us),
+    // or two beyond a wave, for a fuller last one (1319 and 4300: 28 -> 24.4 and 75
+    // -> 70).  With 600 tokens, half a wave, two cost 9.0 against 7.8; smaller tokens
+    // lose to the second look-up and twiddles (bf16, 32 / 8, 300: 3.0 -> 3.4).
+    const int64_t wave = (int64_t)num_sms() * (kHalf ? 7 : 8);
+    int parts = 0;
+    while (parts < 2 && units >> (parts + 1) >= 256 && ((int64_t)a.num_tokens << (parts + 1)) <= wave) ++parts;
+    if (units >= 1024 && a.num_tokens > wave && a.num_tokens <= INT32_MAX / 2) parts = 1;
+    return parts ? run(rotary_append_kernel<kBF16, kD, kHalf, kFP8, 128, true>, 128, parts)
+                 : run(rotary_append_kernel<kBF16, kD, kHalf, kFP8, 128, false>, 128, 0);
 }
 
 template <bool kBF16, int kD, bool kFP8>

@@ -99,6 +99,28 @@ def test_in_place_dense_and_block_sizes(kvattn_lib, block):
     _close(cache.k_pool.double().cpu().numpy()[c.at], want[:, 16:], size[:, 16:], "bf16", "k")
 
 
+@pytest.mark.parametrize("dtype,hq,hkv,tokens,layout,rot", [
+    ("f32", 32, 32, 5, "half", 0), ("f32", 32, 32, 300, "adjacent", 64), ("f32", 32, 32, 700, "half", 16),
+    ("f32", 32, 32, 1300, "half", 0), ("bf16", 128, 16, 7, "adjacent", 0), ("bf16", 64, 64, 1301, "half", 96),
+    ("f32", 32, 8, 40, "half", 0)])
+def test_large_tokens(kvattn_lib, dtype, hq, hkv, tokens, layout, rot):
+    """Tokens of many heads, few and many of them: a token's heads may be several thread blocks' work.  In place."""
+    kv = kvattn_lib
+    c = Case(dtype, hq, hkv, 128, [range(50, 50 + tokens - tokens // 2), range(tokens // 2)], seed=tokens)
+    cfg = kv.make_config(hq, hkv, 128, kv.BF16 if dtype == "bf16" else kv.F32)
+    cache = kv.Cache(*(p.cuda() for p in c.pools))
+    kv.rotary_append(cfg, kv.make_rotary(layout, rot), cache, *c.split(kv), *c.ints)
+    assert kv.get_device_status() == 0
+    R = rot or 128
+    want, size = rotate(c.x64[:, :hq + hkv], c.pos, speeds(10000.0, R), R, layout, 1.0)
+    got = c.qkv.double().cpu().numpy().reshape(c.x64.shape)
+    _close(got[:, :hq], want[:, :hq], size[:, :hq], dtype, "q")
+    assert np.array_equal(got[:, hq:], c.x64[:, hq:]), "k or v of the projection output was written"
+    got_k, got_v = (p.double().cpu().numpy() for p in (cache.k_pool, cache.v_pool))
+    _close(got_k[c.at], want[:, hq:], size[:, hq:], dtype, "k")
+    assert np.array_equal(got_v[c.at], c.x64[:, hq + hkv:])
+
+
 def test_adjacent_whole_head_is_rope_append(kvattn_lib):
     """The form rope_append has: its correctly rounded values, up to the fp32 rotation's error."""
     kv = kvattn_lib
@@ -162,25 +184,26 @@ def test_few_tokens(kvattn_lib, tokens):
         assert torch.equal(cache.k_pool.cpu(), c.pools[0])
 
 
-@pytest.mark.parametrize("layout,rot", [("half", 0), ("half", 64), ("adjacent", 0), ("adjacent", 32)])
-def test_fp8_rows(kvattn_lib, layout, rot):
+@pytest.mark.parametrize("layout,rot,hq,hkv", [("half", 0, 32, 8), ("half", 64, 32, 8), ("adjacent", 0, 32, 8),
+                                               ("adjacent", 32, 32, 8), ("half", 0, 128, 16), ("adjacent", 96, 64, 16)])
+def test_fp8_rows(kvattn_lib, layout, rot, hq, hkv):
     """Codes and scales of each row are the quantisation of a bf16 row within the rotation's bound: V's bit for bit,
     K's values within half an e4m3 step (2^-4 relative, 2^-10 of the scale's 448 below the normals) of it."""
     kv = kvattn_lib
-    c = Case("bf16", 32, 8, 128, [range(3, 40), [77], range(160, 176)], block=32, seed=4)
-    cfg = kv.make_config(32, 8, 128, kv.BF16)
-    cache = kv.CacheFP8(torch.zeros((c.nb, 8, 2, 4224), dtype=torch.uint8, device="cuda"), 32)
-    q_out = torch.empty((len(c.pos), 32, 128), dtype=torch.bfloat16, device="cuda")
+    c = Case("bf16", hq, hkv, 128, [range(3, 40), [77], range(160, 176)], block=32, seed=4)
+    cfg = kv.make_config(hq, hkv, 128, kv.BF16)
+    cache = kv.CacheFP8(torch.zeros((c.nb, hkv, 2, 4224), dtype=torch.uint8, device="cuda"), 32)
+    q_out = torch.empty((len(c.pos), hq, 128), dtype=torch.bfloat16, device="cuda")
     kv.rotary_append_fp8(cfg, kv.make_rotary(layout, rot), cache, *c.split(kv), *c.ints, q_out=q_out)
     assert kv.get_device_status() == 0
     R = rot or 128
-    want, size = rotate(c.x64[:, :40], c.pos, speeds(10000.0, R), R, layout, 1.0)
-    _close(q_out.double().cpu().numpy(), want[:, :32], size[:, :32], "bf16", "q")
+    want, size = rotate(c.x64[:, :hq + hkv], c.pos, speeds(10000.0, R), R, layout, 1.0)
+    _close(q_out.double().cpu().numpy(), want[:, :hq], size[:, :hq], "bf16", "q")
     ck, sk, cv, sv = unpack_rows(cache.pool.cpu().numpy(), c.at[0], c.at[2])
-    codes, scales = fp8.quantize_rows(c.x64[:, 40:])
+    codes, scales = fp8.quantize_rows(c.x64[:, hq + hkv:])
     assert np.array_equal(sv, scales)
     assert np.array_equal(fp8.e4m3_decode(cv), fp8.e4m3_decode(codes))
-    wk, wsize = want[:, 32:], size[:, 32:]
+    wk, wsize = want[:, hq:], size[:, hq:]
     row = 2.0 ** -8 * (np.abs(wk) + 2.0 ** -21 * wsize) + 2.0 ** -21 * wsize       # the stored bf16 row
     amax = np.abs(wk).max(-1)
     # the scale: amax is of the bf16 row; amax / 448 is rounded to fp32
