@@ -33,7 +33,7 @@
 //  - warps 4-7 and 8-11: the softmax of columns 0-63 and 64-127 of whichever
 //    tile is due; P (bf16) overwrites the first half of S in TMEM;
 //  - warps 12-15: O / row sums -> bf16 rows of out, while the others are at
-//    the next item.
+//    the next item (and, over an fp8 cache's copy, q -> f16 as it arrives).
 // TMEM: S_A, S_B, O_A, O_B, 128 columns each.  Every wait on a barrier is
 // bounded (1 s): a timeout records KVATTN_ERR_TIMEOUT, the roles stop waiting,
 // drain their copies and MMAs, free TMEM and return.
