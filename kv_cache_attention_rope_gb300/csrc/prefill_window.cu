@@ -100,7 +100,8 @@ struct Bars {
 static_assert(sizeof(Bars) <= 256, "the barriers fit before the exchange area");
 
 // The flag is looked at only where the wait does not succeed at once: a role
-// that finds its barriers complete runs on after an abort.
+// that finds its barriers complete runs on after an abort (a try in vain comes
+// back within a microsecond on this GPU).
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status)
 {
     if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
