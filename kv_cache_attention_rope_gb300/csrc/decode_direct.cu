@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(warps_per_sm(kKind, kD, kG) * 32, 1)
         else *p = o.v[0];
     };
     auto store = [&](int e, Dims num, float den) {
-        const float inv = den > 0.f ? 1.f / den : 0.f;
+        const float inv = den == 0.f ? 0.f : 1.f / den;
 #pragma unroll
         for (int i = 0; i < kV; ++i) num.v[i] *= inv;
         if constexpr (kKind == kF32Cache)
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(warps_per_sm(kKind, kD, kG) * 32, 1)
         den = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (i < n && s[i].x != -INFINITY) {  // a state without a key has no weight
+            if (i < n && s[i].y != 0.f) {  // a state without a key has no weight (one whose scores are NaN has a sum of NaN)
                 const float f = exp2f(s[i].x - M);
 #pragma unroll
                 for (int k = 0; k < kV; ++k) num.v[k] += f * o[i].v[k];

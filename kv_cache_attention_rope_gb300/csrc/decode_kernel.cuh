@@ -503,17 +503,17 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_sp
                 float Mx = -INFINITY;
 #pragma unroll
                 for (int w = 0; w < kConsumerWarps; ++w) Mx = fmaxf(Mx, merge[(w * kMG + g) * (kD + 2) + kD]);
+                // a state without a key has a sum of 0; one whose scores are NaN
+                // has a sum of NaN, which is not 0, and hands it on
                 float num = 0.f, den = 0.f;
-                if (Mx != -INFINITY) {
 #pragma unroll
-                    for (int w = 0; w < kConsumerWarps; ++w) {
-                        const float* mr = merge + (size_t)(w * kMG + g) * (kD + 2);
-                        const float f = (mr[kD] == -INFINITY) ? 0.f : exp2f(mr[kD] - Mx);
-                        num += f * mr[d];
-                        den += f * mr[kD + 1];
-                    }
+                for (int w = 0; w < kConsumerWarps; ++w) {
+                    const float* mr = merge + (size_t)(w * kMG + g) * (kD + 2);
+                    const float f = mr[kD + 1] == 0.f ? 0.f : exp2f(mr[kD] - Mx);
+                    num += f * mr[d];
+                    den += f * mr[kD + 1];
                 }
-                const float o = den > 0.f ? num / den : 0.f;
+                const float o = den == 0.f ? 0.f : num / den;
                 const int64_t qrow = (int64_t)pc.b * hq + qh0 + h0 + g;
                 if (direct) {
                     if constexpr (kBF16)
@@ -1038,17 +1038,15 @@ __global__ void __launch_bounds__(128) decode_combine_kernel(const __grid_consta
 #pragma unroll
     for (int i = 0; i < kDL; ++i) acc[i] = 0.f;
     float den = 0.f;
-    if (M != -INFINITY) {
-        for (int c = 0; c < ns; ++c) {
-            const float mc = ml[2 * c], lc = ml[2 * c + 1];
-            const float w = (mc == -INFINITY) ? 0.f : lc * exp2f(mc - M);
-            den += w;
-            const float* o = a.part_o + ((int64_t)wid * a.splits + c) * kD;
+    for (int c = 0; c < ns; ++c) {  // (a piece's sum is 0 without a key, NaN with NaN scores)
+        const float mc = ml[2 * c], lc = ml[2 * c + 1];
+        const float w = lc == 0.f ? 0.f : lc * exp2f(mc - M);
+        den += w;
+        const float* o = a.part_o + ((int64_t)wid * a.splits + c) * kD;
 #pragma unroll
-            for (int i = 0; i < kDL; ++i) acc[i] += w * o[lane * kDL + i];
-        }
+        for (int i = 0; i < kDL; ++i) acc[i] += w * o[lane * kDL + i];
     }
-    const float inv = den > 0.f ? 1.f / den : 0.f;
+    const float inv = den == 0.f ? 0.f : 1.f / den;
 #pragma unroll
     for (int i = 0; i < kDL; ++i) {
         const int64_t e = (int64_t)wid * kD + lane * kDL + i;
