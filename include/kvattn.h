@@ -323,7 +323,10 @@ kvattn_status kvattn_copy_blocks_layered(const kvattn_config* cfg, void* base, i
  * kvattn_decode_fp8: as kvattn_decode, with K and V the dequantised values
  * code * scale; bf16 q and output, head_dim 128, group size 4 or 8,
  * block_size a multiple of 16 (else UNSUPPORTED / INVALID_ARG).  Workspace:
- * kvattn_decode_workspace_size with the same arguments.
+ * kvattn_decode_workspace_size with the same arguments.  A key's weight times its
+ * V scale is rounded to f16: within 2^-11 relative, or 2^-25 of the largest V
+ * scale of the sequence's KV head, whatever that key's weight (a row of zeros is
+ * stored with the scale 1); kvattn_decode_window_fp8 does not lose to such keys.
  */
 kvattn_status kvattn_rope_append_fp8(const kvattn_config* cfg, const kvattn_cache_fp8* cache, void* q,
                                      const void* k, const void* v, const int32_t* positions, const int32_t* seq_ids,
@@ -442,7 +445,9 @@ kvattn_status kvattn_decode_static_scratch(const kvattn_config* cfg, const kvatt
  * kvattn_decode_window_fp8: the same over a kvattn_cache_fp8, as
  * kvattn_decode_fp8 (same workspace size): q is taken in f16 over 16, exactly
  * for magnitudes from 2^-10 to under 2^20 (smaller ones to within 2^-21; larger
- * ones overflow).
+ * ones overflow).  A key's weight times its V scale is rounded to f16: within
+ * 2^-11 relative, or 2^-25 of the largest such product of the query head (rows of
+ * zeros, which are stored with the scale 1, do not count).
  */
 size_t kvattn_decode_window_workspace_size(const kvattn_config* cfg, int32_t batch, int32_t max_seq_len,
                                            int32_t window, int32_t num_sinks, int32_t num_splits);

@@ -19,6 +19,8 @@
 // of one to the B fragment of the other by movmatrix.  A warp keeps its own
 // running maximum and sum; the warps of a CTA merge through shared memory and
 // the CTAs of a cluster through distributed shared memory.
+#include <type_traits>
+
 #include <cooperative_groups.h>
 
 #include "decode_kernel.cuh"
@@ -30,36 +32,28 @@ namespace cg = cooperative_groups;
 
 enum DirectKind { kBf16Cache, kFp8Cache, kF32Cache };
 
-// One warp's share of a segment: its running maxima and sums (log2 units) and
-// its unnormalised output, kept for query heads 2 q4 and 2 q4 + 1.
-template <int kD>
-struct WarpState {
-    float o[kD / 16][4];
+// One warp's share of a segment over a bf16 cache: its running maxima and sums
+// (log2 units) of query heads 2 q4 and 2 q4 + 1, and how they weigh a tile's
+// scores (fp8 pages: Fp8Softmax).
+struct Softmax {
     float m[2], l[2];
-    float vref, vinv;  // fp8: the V scale that o is in units of
     __device__ __forceinline__ void init()
     {
-#pragma unroll
-        for (int e = 0; e < kD / 16; ++e) o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.f;
         m[0] = m[1] = -INFINITY;
         l[0] = l[1] = 0.f;
-        vref = vinv = 0.f;
     }
     // Probabilities of this lane's tokens r0, r1 (scores x: (r0, head 0),
-    // (r0, 1), (r1, 0), (r1, 1), V scales sv0, sv1).  The maxima are raised
-    // when a score exceeds them by more than 2^8, and the V scale when a
-    // token's is over 16 times it; the warp agrees on them only then.
-    template <bool kScaled>
-    __device__ __forceinline__ void weigh(const float (&x)[4], float sv0, float sv1, float (&p)[4])
+    // (r0, 1), (r1, 0), (r1, 1)).  The maxima are raised, and o rescaled, when a
+    // score exceeds them by more than 2^8; the warp agrees on them only then.
+    template <int kN>
+    __device__ __forceinline__ void step(const float (&x)[4], float (&o)[kN][4], float (&p)[4])
     {
-        float l0 = fmaxf(x[0], x[2]), l1 = fmaxf(x[1], x[3]), lv = kScaled ? fmaxf(sv0, sv1) : 0.f;
-        const bool raise = l0 > m[0] + 8.f || l1 > m[1] + 8.f || (kScaled && lv > vref * 16.f);
-        if (__any_sync(0xffffffffu, raise)) {
+        float l0 = fmaxf(x[0], x[2]), l1 = fmaxf(x[1], x[3]);
+        if (__any_sync(0xffffffffu, l0 > m[0] + 8.f || l1 > m[1] + 8.f)) {
 #pragma unroll
             for (int s = 4; s < 32; s <<= 1) {
                 l0 = fmaxf(l0, __shfl_xor_sync(0xffffffffu, l0, s));
                 l1 = fmaxf(l1, __shfl_xor_sync(0xffffffffu, l1, s));
-                if (kScaled) lv = fmaxf(lv, __shfl_xor_sync(0xffffffffu, lv, s));
             }
             float f0 = 1.f, f1 = 1.f;
             if (l0 > m[0] + 8.f) {
@@ -72,16 +66,8 @@ struct WarpState {
                 l[1] *= f1;
                 m[1] = l1;
             }
-            if (kScaled && lv > vref * 16.f) {
-                if (vref > 0.f) {
-                    f0 *= vref / lv;
-                    f1 *= vref / lv;
-                }
-                vref = lv;
-                vinv = 1.f / lv;
-            }
 #pragma unroll
-            for (int e = 0; e < kD / 16; ++e) {
+            for (int e = 0; e < kN; ++e) {
                 o[e][0] *= f0;
                 o[e][1] *= f1;
                 o[e][2] *= f0;
@@ -332,8 +318,11 @@ __global__ void __launch_bounds__(warps_per_sm(kKind, kD, kG) * 32, 1)
                 }
             }
         }
-        WarpState<kD> st;
+        std::conditional_t<kKind == kFp8Cache, Fp8Softmax, Softmax> st;
         st.init();
+        float o[kD / 16][4];  // unnormalised output
+#pragma unroll
+        for (int e = 0; e < kD / 16; ++e) o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.f;
         const float sl2 = a.scale_log2 * (kKind == kFp8Cache ? 16.f : 1.f);
         if constexpr (kKind == kBf16Cache) {
             Bf16Tile<kD> t;
@@ -361,14 +350,13 @@ __global__ void __launch_bounds__(warps_per_sm(kKind, kD, kG) * 32, 1)
                                     now >> (g4 + 8) & 1u ? s[2] * sl2 : -INFINITY,
                                     now >> (g4 + 8) & 1u ? s[3] * sl2 : -INFINITY};
                 float p[4];
-                st.template weigh<false>(x, 0.f, 0.f, p);
-                t.add(vnow, st.o, movmatrix_trans(pack_bf16_rn(p[0], p[1])), movmatrix_trans(pack_bf16_rn(p[2], p[3])));
+                st.step(x, o, p);
+                t.add(vnow, o, movmatrix_trans(pack_bf16_rn(p[0], p[1])), movmatrix_trans(pack_bf16_rn(p[2], p[3])));
             };
             for (int j = 0; j < mine; j += 2) {
                 step(j, v[0], v[1]);
                 if (j + 1 < mine) step(j + 1, v[1], v[0]);
             }
-            st.vref = 1.f;
         } else {
             const int rk0 = (g4 >> 1) * 4 + (g4 & 1), rk1 = rk0 + 2;
             const unsigned char* pool = (const unsigned char*)a.k_pool;
@@ -416,11 +404,9 @@ __global__ void __launch_bounds__(warps_per_sm(kKind, kD, kG) * 32, 1)
                     for (int i = 0; i < 4; ++i)
                         if (!(now >> (4 * q4 + i) & 1u)) vmask &= ~(0xffu << (8 * i));
                 }
-                float p[4];
-                st.template weigh<true>(x, sv0, sv1, p);
-                const float c0 = sv0 * st.vinv, c1 = sv1 * st.vinv;
-                t.add(st.o, movmatrix_trans(pack_f16_rn(p[0] * c0, p[1] * c0)),
-                      movmatrix_trans(pack_f16_rn(p[2] * c1, p[3] * c1)), vmask);
+                float w[4];
+                st.step(x, sv0, sv1, lane, [&](int i) { return t.v[i] & vmask; }, o, w);
+                t.add(o, movmatrix_trans(pack_f16_rn(w[0], w[1])), movmatrix_trans(pack_f16_rn(w[2], w[3])), vmask);
             }
             asm volatile("cp.async.wait_group 0;" ::: "memory");
             __syncwarp();  // the outputs take the pages' place
@@ -442,7 +428,8 @@ __global__ void __launch_bounds__(warps_per_sm(kKind, kD, kG) * 32, 1)
                         int d;
                         if constexpr (kKind == kBf16Cache) d = Bf16Tile<kD>::dim_of(i, half, g4);
                         else d = Fp8Tile::dim_of(i, half, g4);
-                        r[d] = st.o[i][2 * half + e] * st.vref;
+                        if constexpr (kKind == kFp8Cache) r[d] = o[i][2 * half + e] * st.ref[e];
+                        else r[d] = o[i][2 * half + e];
                     }
                 if (g4 == 0) {
                     ml_of(warp, g)[0] = st.m[e];

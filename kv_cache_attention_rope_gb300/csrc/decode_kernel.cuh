@@ -215,6 +215,106 @@ __device__ __forceinline__ uint32_t seen_bits(int tok0, const Piece& pc, const D
 }
 
 // Walks the pieces of this CTA.  Producer and consumers run identical copies.
+// Softmax state of a warp over fp8 pages, windowed form: of query heads 2 q4 and
+// 2 q4 + 1 the running maximum (log2 units), the sum, and the reference that the
+// output o is in units of.  P goes into the MMA in f16 as weight * V scale /
+// reference.  The reference follows that product, not the scale, so that a token
+// of large V and no weight leaves the others their bits, and a row of zeros, which
+// is stored with the scale 1, does not count.  f16 rounds each product within
+// 2^-11 relative, or 2^-25 of the head's largest.
+struct Fp8Softmax {
+    static constexpr float kLeast = 0x1p-100f;  // of a reference: its inverse is finite
+    float m[2], l[2], ref[2], rinv[2];
+    float scale16;  // 16 times the smaller reference
+    __device__ __forceinline__ void init()
+    {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            m[e] = -INFINITY;
+            l[e] = ref[e] = rinv[e] = 0.f;
+        }
+        scale16 = 0.f;
+    }
+    // One tile: scores x of this lane's tokens rk0 and rk1 ((rk0, head 0), (rk0,
+    // 1), (rk1, 0), (rk1, 1)), their V scales sv0 and sv1 (0: not seen), word(i)
+    // the lane's i-th word of V codes (tokens 4 q4 .. 4 q4 + 3).  Gives the
+    // products w for P.V and rescales o.  The maximum is raised when a score
+    // exceeds it by more than 2^8.  A V scale over 16 times a reference has the
+    // products looked at, and the reference raised to one that is; so w stays
+    // within 2^12.  The warp agrees on these only then.
+    template <int kN, typename Word>
+    __device__ __forceinline__ void step(const float (&x)[4], float sv0, float sv1, int lane, Word word, float (&o)[kN][4],
+                                         float (&w)[4])
+    {
+        float l0 = fmaxf(x[0], x[2]), l1 = fmaxf(x[1], x[3]);
+        const bool raise = l0 > m[0] + 8.f || l1 > m[1] + 8.f || fmaxf(sv0, sv1) > scale16;
+        float p[4];
+        auto weigh = [&] {
+            // a head whose scores are all -inf so far has no weight yet
+            const float m0 = m[0] == -INFINITY ? 0.f : m[0], m1 = m[1] == -INFINITY ? 0.f : m[1];
+            p[0] = fast_exp2(x[0] - m0);
+            p[1] = fast_exp2(x[1] - m1);
+            p[2] = fast_exp2(x[2] - m0);
+            p[3] = fast_exp2(x[3] - m1);
+        };
+        if (__any_sync(0xffffffffu, raise)) {
+            if (__any_sync(0xffffffffu, sv0 == 1.f || sv1 == 1.f)) {  // rows of zeros?
+                uint32_t any = 0;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) any |= word(i) & 0x7f7f7f7fu;
+#pragma unroll
+                for (int s = 4; s < 32; s <<= 1) any |= __shfl_xor_sync(0xffffffffu, any, s);
+                const int g4 = lane >> 2;  // rk0 = 4 (g4 / 2) + g4 % 2, rk1 = rk0 + 2
+                any = __shfl_sync(0xffffffffu, any, g4 >> 1) >> (8 * (g4 & 1));
+                if (sv0 == 1.f && (any & 0xffu) == 0u) sv0 = 0.f;
+                if (sv1 == 1.f && (any & 0xff0000u) == 0u) sv1 = 0.f;
+            }
+#pragma unroll
+            for (int s = 4; s < 32; s <<= 1) {
+                l0 = fmaxf(l0, __shfl_xor_sync(0xffffffffu, l0, s));
+                l1 = fmaxf(l1, __shfl_xor_sync(0xffffffffu, l1, s));
+            }
+            const float top[2] = {l0, l1};
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (top[e] > m[e] + 8.f) {  // (-inf: nothing before)
+                    const float f = m[e] == -INFINITY ? 0.f : fast_exp2(m[e] - top[e]);
+                    l[e] *= f;
+                    ref[e] *= f;
+                    m[e] = top[e];
+                }
+            weigh();
+            float most[2] = {fmaxf(p[0] * sv0, p[2] * sv1), fmaxf(p[1] * sv0, p[3] * sv1)};
+            float f[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int s = 4; s < 32; s <<= 1) most[e] = fmaxf(most[e], __shfl_xor_sync(0xffffffffu, most[e], s));
+                const float r = fmaxf(most[e] > ref[e] * 16.f ? most[e] : ref[e], kLeast);
+                f[e] = ref[e] / r;
+                ref[e] = r;
+                rinv[e] = 1.f / r;
+            }
+            scale16 = 16.f * fminf(ref[0], ref[1]);
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                o[i][0] *= f[0];
+                o[i][1] *= f[1];
+                o[i][2] *= f[0];
+                o[i][3] *= f[1];
+            }
+        } else {
+            weigh();
+        }
+        l[0] += p[0] + p[2];
+        l[1] += p[1] + p[3];
+        w[0] = p[0] * sv0 * rinv[0];
+        w[1] = p[1] * sv0 * rinv[1];
+        w[2] = p[2] * sv1 * rinv[0];
+        w[3] = p[3] * sv1 * rinv[1];
+    }
+};
+
 template <bool kWin>
 struct PieceIter {
     const int* P;  // P[b]: first stream tile of sequence b (P[batch] = total)
@@ -546,7 +646,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_sp
             // lane's four tokens of one dim, the A operand of O^T += V^T P^T.
             // Q is scaled by 2^-4 into f16 range, the K scales multiply S per
             // token.  P carries each token's V scale over a lazy reference
-            // vref (rescaled like the running max).
+            // (rescaled like the running max): the largest scale so far, or in
+            // the windowed form the largest product with a weight (Fp8Softmax).
             const int g4 = lane >> 2, q4 = lane & 3;
             const int rk0 = (g4 >> 1) * 4 + (g4 & 1), rk1 = rk0 + 2;  // K rows (tokens) of this lane
             uint32_t qb[kD / 16][2];  // B fragment: head g4, dims 16kk + 4q4 .. 16kk + 4q4 + 3
@@ -568,6 +669,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_sp
             for (int m = 0; m < kD / 16; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
             float m_run[2] = {-INFINITY, -INFINITY}, lrun[2] = {0.f, 0.f};  // heads 2q4, 2q4 + 1
             float vref = 0.f, vinv = 0.f;
+            Fp8Softmax win;  // windowed form: in the place of these four
+            win.init();
             const float sl2 = a.scale_log2 * 16.f;  // undoes the 2^-4 on Q
             for (int li = 0; li < ntiles; ++li) {
                 const uint32_t p = pos + li;
@@ -616,54 +719,65 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_sp
                     for (int j = 0; j < 4; ++j)
                         if (!sees(4 * q4 + j)) vmask &= ~(0xffu << (8 * j));
                 }
-                // lazy references: the max of each head (raised when a tile
-                // exceeds it by more than 2^8) and the V scale (when a tile's
-                // is over 16x it); the tile's maxima over its 16 tokens are
-                // only formed when some lane's own values call for a raise
-                float l0 = fmaxf(x[0], x[2]), l1 = fmaxf(x[1], x[3]), lv = fmaxf(sv0, sv1);
-                const bool raise = l0 > m_run[0] + 8.f || l1 > m_run[1] + 8.f || lv > vref * 16.f;
-                if (__any_sync(0xffffffffu, raise)) {
+                float w[4];  // weight * V scale over a reference
+                if constexpr (kWin) {
+                    win.step(x, sv0, sv1, lane, [&](int i) {
+                        return *reinterpret_cast<const uint32_t*>(pg + kF8VOff + g4 * 16 + 4 * q4 + i * 128) & vmask;
+                    }, o, w);
+                } else {
+                    // lazy references: the max of each head (raised when a tile
+                    // exceeds it by more than 2^8) and the V scale (when a tile's
+                    // is over 16x it); the tile's maxima over its 16 tokens are
+                    // only formed when some lane's own values call for a raise
+                    float l0 = fmaxf(x[0], x[2]), l1 = fmaxf(x[1], x[3]), lv = fmaxf(sv0, sv1);
+                    const bool raise = l0 > m_run[0] + 8.f || l1 > m_run[1] + 8.f || lv > vref * 16.f;
+                    if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-                    for (int sh = 4; sh < 32; sh <<= 1) {
-                        l0 = fmaxf(l0, __shfl_xor_sync(0xffffffffu, l0, sh));
-                        l1 = fmaxf(l1, __shfl_xor_sync(0xffffffffu, l1, sh));
-                        lv = fmaxf(lv, __shfl_xor_sync(0xffffffffu, lv, sh));
-                    }
-                    float f0 = 1.f, f1 = 1.f;
-                    if (l0 > m_run[0] + 8.f) {
-                        f0 = m_run[0] == -INFINITY ? 0.f : fast_exp2(m_run[0] - l0);
-                        lrun[0] *= f0;
-                        m_run[0] = l0;
-                    }
-                    if (l1 > m_run[1] + 8.f) {
-                        f1 = m_run[1] == -INFINITY ? 0.f : fast_exp2(m_run[1] - l1);
-                        lrun[1] *= f1;
-                        m_run[1] = l1;
-                    }
-                    if (lv > vref * 16.f) {
-                        if (vref > 0.f) {
-                            f0 *= vref / lv;
-                            f1 *= vref / lv;
+                        for (int sh = 4; sh < 32; sh <<= 1) {
+                            l0 = fmaxf(l0, __shfl_xor_sync(0xffffffffu, l0, sh));
+                            l1 = fmaxf(l1, __shfl_xor_sync(0xffffffffu, l1, sh));
+                            lv = fmaxf(lv, __shfl_xor_sync(0xffffffffu, lv, sh));
                         }
-                        vref = lv;
-                        vinv = 1.f / lv;
-                    }
+                        float f0 = 1.f, f1 = 1.f;
+                        if (l0 > m_run[0] + 8.f) {
+                            f0 = m_run[0] == -INFINITY ? 0.f : fast_exp2(m_run[0] - l0);
+                            lrun[0] *= f0;
+                            m_run[0] = l0;
+                        }
+                        if (l1 > m_run[1] + 8.f) {
+                            f1 = m_run[1] == -INFINITY ? 0.f : fast_exp2(m_run[1] - l1);
+                            lrun[1] *= f1;
+                            m_run[1] = l1;
+                        }
+                        if (lv > vref * 16.f) {
+                            if (vref > 0.f) {
+                                f0 *= vref / lv;
+                                f1 *= vref / lv;
+                            }
+                            vref = lv;
+                            vinv = 1.f / lv;
+                        }
 #pragma unroll
-                    for (int m = 0; m < kD / 16; ++m) {
-                        o[m][0] *= f0;
-                        o[m][1] *= f1;
-                        o[m][2] *= f0;
-                        o[m][3] *= f1;
+                        for (int m = 0; m < kD / 16; ++m) {
+                            o[m][0] *= f0;
+                            o[m][1] *= f1;
+                            o[m][2] *= f0;
+                            o[m][3] *= f1;
+                        }
                     }
+                    const float p0 = fast_exp2(x[0] - m_run[0]), p1 = fast_exp2(x[1] - m_run[1]);
+                    const float p2 = fast_exp2(x[2] - m_run[0]), p3 = fast_exp2(x[3] - m_run[1]);
+                    lrun[0] += p0 + p2;
+                    lrun[1] += p1 + p3;
+                    const float c0 = sv0 * vinv, c1 = sv1 * vinv;
+                    w[0] = p0 * c0;
+                    w[1] = p1 * c0;
+                    w[2] = p2 * c1;
+                    w[3] = p3 * c1;
                 }
-                const float p0 = fast_exp2(x[0] - m_run[0]), p1 = fast_exp2(x[1] - m_run[1]);
-                const float p2 = fast_exp2(x[2] - m_run[0]), p3 = fast_exp2(x[3] - m_run[1]);
-                lrun[0] += p0 + p2;
-                lrun[1] += p1 + p3;
-                const float c0 = sv0 * vinv, c1 = sv1 * vinv;
                 // P^T B fragment: head g4, tokens 4q4, 4q4+1 (pb0) and 4q4+2, 4q4+3 (pb1)
-                const uint32_t pb0 = movmatrix_trans(pack_f16_rn(p0 * c0, p1 * c0));
-                const uint32_t pb1 = movmatrix_trans(pack_f16_rn(p2 * c1, p3 * c1));
+                const uint32_t pb0 = movmatrix_trans(pack_f16_rn(w[0], w[1]));
+                const uint32_t pb1 = movmatrix_trans(pack_f16_rn(w[2], w[3]));
                 // V^T words: dims 16m + g4 and 16m + 8 + g4, tokens 4q4 .. 4q4+3
                 // (stale tokens zeroed: 0 * NaN)
                 const unsigned char* vt = pg + kF8VOff + g4 * 16 + 4 * q4;
@@ -678,6 +792,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_sp
                 if (lane == 0) mbar_arrive(&empty[stage]);
             }
             pos += ntiles;
+            if constexpr (kWin) {
+                m_run[0] = win.m[0];
+                m_run[1] = win.m[1];
+                lrun[0] = win.l[0];
+                lrun[1] = win.l[1];
+            }
+            const float unit[2] = {kWin ? win.ref[0] : vref, kWin ? win.ref[1] : vref};  // of o
 #pragma unroll
             for (int sh = 4; sh < 32; sh <<= 1) {
                 lrun[0] += __shfl_xor_sync(0xffffffffu, lrun[0], sh);
@@ -693,8 +814,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_sp
                         float* mr = mw + (hd - h0) * (kD + 2);
 #pragma unroll
                         for (int m = 0; m < kD / 16; ++m) {
-                            mr[16 * m + g4] = o[m][e] * vref;
-                            mr[16 * m + 8 + g4] = o[m][2 + e] * vref;
+                            mr[16 * m + g4] = o[m][e] * unit[e];
+                            mr[16 * m + 8 + g4] = o[m][2 + e] * unit[e];
                         }
                         if (g4 == 0) {
                             mr[kD] = m_run[e];

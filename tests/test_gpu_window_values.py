@@ -106,3 +106,64 @@ def test_decode_of_the_whole_cache_seen_nan(kvattn_lib, dtype, splits):
     for r, L in enumerate(lens):
         want, mag = attend(q[r:r + 1].double().numpy(), c.k[r], c.v[r], wanted[r][None])
         _check_with_nan(got[r:r + 1], want, mag, dtype, f"length {L}")
+
+
+def _v_size(c, r, times, zero=()):
+    """Multiplies the V rows of sequence r of an fp8 cache by times[token] (powers of two: exact), and makes the rows
+    `zero` zeros as they are stored: codes of 0 and the scale 1."""
+    pool = c.cache.pool
+    for token in np.nonzero(c.table[r, np.arange(len(times)) // c.cache.block_size] >= 0)[0]:
+        b, s = _at(c, r, int(token))
+        page = pool[b, :, s // 16]
+        at = 4160 + 4 * (s % 16)
+        scale = page[:, at:at + 4].contiguous().view(torch.float32)
+        if token in zero:
+            page[:, 2048 + s % 16:4096:16] = 0
+            scale = torch.ones_like(scale)
+        else:
+            scale = scale * float(times[token])
+        page[:, at:at + 4] = scale.view(torch.uint8)
+    c.v[r] = c.v[r] * np.asarray(times)[:, None, None]
+    c.v[r][list(zero)] = 0.0
+
+
+@pytest.mark.parametrize("case", ["zero rows", "no weight", "by token", "tiny"])
+@pytest.mark.parametrize("splits", [0, 3])
+def test_decode_fp8_v_of_any_size(kvattn_lib, case, splits):
+    """V rows of very different sizes: rows of zeros (stored with the scale 1) among small ones, a row 2^30 times the
+    others whose weight is 2^-150, sizes from 1 to 2^-23 by token, all of 2^-90."""
+    kv = kvattn_lib
+    lens, window, sinks, hkv, g = [1024, 17, 300, 1], 800, 2, 2, 4
+    wanted = [seen([L - 1], L, window, sinks)[0] for L in lens]
+    c = WindowCache(kv, "fp8", hkv, 128, lens, wanted, seed=6)
+    q = _q(7, (len(lens), hkv, 1, 128)).expand(len(lens), hkv, g, 128).reshape(len(lens), hkv * g, 128).contiguous()
+    for r, L in enumerate(lens):
+        t, zero = np.ones(L), ()
+        if case == "zero rows":
+            t *= 2.0 ** -20
+            zero = sorted({0, L - 1, max(0, L - 6)})
+        elif case == "by token":
+            t = 2.0 ** -(np.arange(L) % 24).astype(np.float64)
+        elif case == "tiny":
+            t *= 2.0 ** -90
+        elif L > 100:  # the key of the lowest score of each head, which 2^6 times as long weighs under 2^-150
+            for h in range(hkv):
+                s = np.where(wanted[r], c.k[r][:, h] @ q[r, h * g].double().numpy() / np.sqrt(128.0), 0.0)
+                low = int(s.argmin())
+                assert s[low] * 2.0 ** 6 < -150 * np.log(2.0)
+                b, at = _at(c, r, low)
+                page = c.cache.pool[b, h, at // 16]
+                for off, times in ((4096, 2.0 ** 6), (4160, 2.0 ** 30)):
+                    w = page[off + 4 * (at % 16):off + 4 * (at % 16) + 4]
+                    w.copy_((w.clone().view(torch.float32) * times).view(torch.uint8))
+                c.k[r][low, h] *= 2.0 ** 6
+                c.v[r][low, h] *= 2.0 ** 30
+        _v_size(c, r, t, zero)
+    out = kv.decode_window_fp8(kv.make_config(hkv * g, hkv, 128, kv.BF16), c.cache, q.cuda(), c.d_table,
+                               torch.tensor(lens, dtype=torch.int32).cuda(), max(lens), window, sinks, num_splits=splits)
+    assert kv.get_device_status() == 0
+    for r, L in enumerate(lens):
+        want, mag = attend(q[r:r + 1].double().numpy(), c.k[r], c.v[r], wanted[r][None])
+        # the roundings of check_attention; a product of a weight and a V scale loses at most 2^-25 of the largest
+        # besides, and of 800 keys those together are far below the 2^-10 of sum w |v| that the bound has to spare
+        check_attention(f64(out)[r:r + 1], want, mag, "fp8", f"{case}, length {L}")
