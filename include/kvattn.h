@@ -549,7 +549,7 @@ kvattn_status kvattn_prefill_chunk_fp8(const kvattn_config* cfg, const kvattn_ca
  *
  * kvattn_prefill_window_fp8: the same over a kvattn_cache_fp8 (head_dim 128).
  * K and V are code * scale rounded to f16 over a power of two each that is
- * common to the chunk and KV head (within 2^-11 relative, or 2^-40 of the
+ * common to the chunk and KV head (within 2^-11 relative, or 2^-38 of the
  * largest seen K or V of the head), and q is taken in f16 as by
  * kvattn_decode_window_fp8.  The pages that a chunk sees are expanded into
  * `workspace`, at least kvattn_prefill_window_fp8_workspace_size(...) bytes (any

@@ -298,12 +298,30 @@ __global__ void __launch_bounds__(kExpandWarps * 32) prefill_fp8_expand(const Fp
     }
 }
 
+// Whether row r of a page holds zeros (which are stored with the scale 1).
+__device__ __forceinline__ bool zero_k(const unsigned char* page, int r)
+{
+    uint32_t any = 0;
+    for (int i = 0; i < 8 && !any; ++i) {
+        const uint4 w = *reinterpret_cast<const uint4*>(page + r * 128 + 16 * i);
+        any = (w.x | w.y | w.z | w.w) & 0x7f7f7f7fu;
+    }
+    return !any;
+}
+__device__ __forceinline__ bool zero_v(const unsigned char* page, int r)
+{
+    uint32_t any = 0;
+    for (int d = 0; d < kF8D && !any; ++d) any = page[kF8VOff + 16 * d + r] & 0x7fu;
+    return !any;
+}
+
 // Windowed form: `slices` CTAs per (chunk, KV head), each converting a share of
 // the pages that the chunk sees.  K and V are copied in f16, whose 11 bits hold
 // code * scale eight times more exactly than bf16's 8; each is divided by the
-// power of two that brings its largest seen value of the chunk and head to 2^14
-// .. 2^15, and f16 covers 29 binades below that at full precision.  (q and P,
-// which the MMAs take in K's and V's type, lose nothing and gain as much.)
+// power of two that brings 448 times the largest scale of a seen row of the chunk
+// and head (rows of zeros aside) to 2^13.8 .. 2^14.8, and f16 covers 27 binades
+// below that at full precision.  (q and P, which the MMAs take in K's and V's type,
+// lose nothing and gain as much.)
 // Every CTA finds the powers itself from the scales, 128 of a page's 4224 bytes:
 // a kernel of its own for V's took 5 us of a call's 89.  The copy's block table
 // is written here too.
@@ -364,7 +382,11 @@ __global__ void __launch_bounds__(kExpandWarps * 32) prefill_fp8_expand_window(c
         const float kf[4] = {k.x, k.y, k.z, k.w}, vf[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (s.key(key0 + i, a.sinks)) m = make_float2(fmaxf(m.x, kf[i]), fmaxf(m.y, vf[i]));
+            if (s.key(key0 + i, a.sinks)) {
+                const int r = (e & 3) * 4 + i;
+                if (!(kf[i] == 1.f && zero_k(page_of(blk, p), r))) m.x = fmaxf(m.x, kf[i]);
+                if (!(vf[i] == 1.f && zero_v(page_of(blk, p), r))) m.y = fmaxf(m.y, vf[i]);
+            }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)

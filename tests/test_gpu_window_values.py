@@ -167,3 +167,29 @@ def test_decode_fp8_v_of_any_size(kvattn_lib, case, splits):
         # the roundings of check_attention; a product of a weight and a V scale loses at most 2^-25 of the largest
         # besides, and of 800 keys those together are far below the 2^-10 of sum w |v| that the bound has to spare
         check_attention(f64(out)[r:r + 1], want, mag, "fp8", f"{case}, length {L}")
+
+
+@pytest.mark.parametrize("size", [2.0 ** -30, 1.0, 2.0 ** 30])
+def test_prefill_fp8_rows_of_zeros(kvattn_lib, size):
+    """V rows of zeros, stored with the scale 1, among rows far smaller and larger than 1; K rows of zeros too."""
+    kv = kvattn_lib
+    chunks, window, sinks, zero = [(100, 200), (0, 70)], 120, 4, [0, 3, 40, 60, 101, 299]
+    masks = [seen(range(p, p + n), p + n, window, sinks) for p, n in chunks]
+    c = WindowCache(kv, "fp8", 2, 128, [300, 70], [m.any(0) for m in masks], seed=3)
+    for r, m in enumerate(masks):
+        mine = [t for t in zero if t < m.shape[1]]
+        _v_size(c, r, np.full(m.shape[1], size), mine)
+        for token in mine:
+            if m.any(0)[token]:
+                b, s = _at(c, r, token)
+                c.cache.pool[b, :, s // 16, 128 * (s % 16):128 * (s % 16) + 128] = 0
+                c.cache.pool[b, :, s // 16, 4096 + 4 * (s % 16):4100 + 4 * (s % 16)] = torch.ones(1).view(torch.uint8).cuda()
+                c.k[r][token] = 0.0
+    q = _q(1, (270, 8, 128))
+    out = kv.prefill_window_fp8(kv.make_config(8, 2, 128, kv.BF16), c.cache, q.cuda(),
+                                torch.tensor([0, 200, 270], dtype=torch.int32).cuda(),
+                                torch.tensor([100, 0], dtype=torch.int32).cuda(), c.d_table, 200, window, sinks)
+    assert kv.get_device_status() == 0
+    for i, (a, b) in enumerate([(0, 200), (200, 270)]):
+        want, mag = attend(q[a:b].double().numpy(), c.k[i], c.v[i], masks[i])
+        check_attention(f64(out)[a:b], want, mag, "fp8", f"chunk {i}")
