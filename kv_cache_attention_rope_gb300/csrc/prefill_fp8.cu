@@ -319,9 +319,9 @@ __device__ __forceinline__ bool zero_v(const unsigned char* page, int r)
 // the pages that the chunk sees.  K and V are copied in f16, whose 11 bits hold
 // code * scale eight times more exactly than bf16's 8; each is divided by the
 // power of two that brings 448 times the largest scale of a seen row of the chunk
-// and head (rows of zeros aside) to 2^13.8 .. 2^14.8, and f16 covers 27 binades
-// below that at full precision.  (q and P, which the MMAs take in K's and V's type,
-// lose nothing and gain as much.)
+// and head (rows of zeros and of infinities aside) to 2^13.8 .. 2^14.8, and f16
+// covers 27 binades below that at full precision.  (q and P, which the MMAs take in
+// K's and V's type, lose nothing and gain as much.)
 // Every CTA finds the powers itself from the scales, 128 of a page's 4224 bytes:
 // a kernel of its own for V's took 5 us of a call's 89.  The copy's block table
 // is written here too.
@@ -384,8 +384,8 @@ __global__ void __launch_bounds__(kExpandWarps * 32) prefill_fp8_expand_window(c
         for (int i = 0; i < 4; ++i)
             if (s.key(key0 + i, a.sinks)) {
                 const int r = (e & 3) * 4 + i;
-                if (!(kf[i] == 1.f && zero_k(page_of(blk, p), r))) m.x = fmaxf(m.x, kf[i]);
-                if (!(vf[i] == 1.f && zero_v(page_of(blk, p), r))) m.y = fmaxf(m.y, vf[i]);
+                if (kf[i] < INFINITY && !(kf[i] == 1.f && zero_k(page_of(blk, p), r))) m.x = fmaxf(m.x, kf[i]);
+                if (vf[i] < INFINITY && !(vf[i] == 1.f && zero_v(page_of(blk, p), r))) m.y = fmaxf(m.y, vf[i]);
             }
     }
 #pragma unroll
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kExpandWarps * 32) prefill_fp8_expand_window(c
 #pragma unroll
     for (int i = 0; i < kExpandWarps; ++i) m = make_float2(fmaxf(m.x, wmax[i].x), fmaxf(m.y, wmax[i].y));
     // |code * scale| <= 448 scale < 2^(e + 10), scale's exponent being e
-    auto power = [](float x) { return x > 0.f && x < INFINITY ? min(122, max(-100, ilogbf(x) - 5)) : 0; };
+    auto power = [](float x) { return x > 0.f ? min(122, max(-100, ilogbf(x) - 5)) : 0; };
     const int ke = power(m.x), ve = power(m.y);
     if (slice == 0 && tid == 0) a.kv_scale[pair] = make_float2(ldexpf(1.f, ke), ldexpf(1.f, ve));
     const float2 mul = make_float2(ldexpf(1.f, -ke), ldexpf(1.f, -ve));

@@ -193,3 +193,23 @@ def test_prefill_fp8_rows_of_zeros(kvattn_lib, size):
     for i, (a, b) in enumerate([(0, 200), (200, 270)]):
         want, mag = attend(q[a:b].double().numpy(), c.k[i], c.v[i], masks[i])
         check_attention(f64(out)[a:b], want, mag, "fp8", f"chunk {i}")
+
+
+def test_prefill_fp8_infinite_key_of_a_later_row(kvattn_lib):
+    """An infinite key (its scale) that only the chunk's last row sees: the other rows keep the precision of their small
+    keys."""
+    kv = kvattn_lib
+    n, window, sinks, small = 150, 60, 2, 2.0 ** -17
+    mask = seen(range(n), n, window, sinks)
+    c = WindowCache(kv, "fp8", 2, 128, [n], [mask.any(0)], seed=9)
+    ks = c.cache.pool[..., 4096:4160].contiguous().view(torch.float32) * small
+    b, s = _at(c, 0, n - 1)
+    ks[b, :, s // 16, s % 16] = float("inf")
+    c.cache.pool[..., 4096:4160] = ks.view(torch.uint8)
+    q = _q(2, (n, 8, 128)) / small
+    out = kv.prefill_window_fp8(kv.make_config(8, 2, 128, kv.BF16), c.cache, q.cuda(),
+                                torch.tensor([0, n], dtype=torch.int32).cuda(), torch.zeros(1, dtype=torch.int32).cuda(),
+                                c.d_table, n, window, sinks)
+    assert kv.get_device_status() == 0
+    want, mag = attend(q[:-1].double().numpy(), c.k[0] * small, c.v[0], mask[:-1])
+    check_attention(f64(out)[:-1], want, mag, "fp8", "rows before")
