@@ -247,6 +247,13 @@ struct PrefillArgs {
 kvattn_status launch_prefill(const PrefillArgs& a, cudaStream_t s);
 kvattn_status launch_prefill_window(const PrefillArgs& a, cudaStream_t s);
 constexpr int32_t kMaxWindowKeys = 1 << 30;  // keys of a sequence, window and sinks of a windowed prefill
+// Whether a windowed prefill's work items (one KV head, 256 rows of its group of
+// query heads) can be numbered: numbers of the round past the last are 32-bit too.
+inline bool window_items_ok(const PrefillArgs& a)
+{
+    const int64_t step = 256 / (a.hq / a.hkv);
+    return a.num_chunks * ((a.max_q_len + step - 1) / step) <= 0x3fffffff / a.hkv;
+}
 
 // Workspace of the fp8 prefill: the chunks' blocks expanded to bf16 (nb
 // blocks, K and V), their block table, owners and first blocks.  bytes == 0

@@ -552,8 +552,7 @@ kvattn_status launch_prefill_window_fp8(const PrefillArgs& pa, const void* pool,
     // launch_prefill_window's own refusals, checked before anything is launched
     const int64_t nb = L.per_chunk * pa.num_chunks;
     if (nb > INT32_MAX / pa.hkv / pa.block_size) return KVATTN_ERR_UNSUPPORTED;
-    const int64_t rows = 256 / (pa.hq / pa.hkv);  // tokens of an item
-    if (pa.num_chunks * ((pa.max_q_len + rows - 1) / rows) * pa.hkv > 0x7fffffff) return KVATTN_ERR_UNSUPPORTED;
+    if (!window_items_ok(pa)) return KVATTN_ERR_UNSUPPORTED;
     unsigned char* ws = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(workspace) + kAlign - 1) / kAlign * kAlign);
     Fp8PrefillArgs a = common_args(pa, pool);

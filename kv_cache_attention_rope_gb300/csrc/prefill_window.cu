@@ -921,8 +921,8 @@ kvattn_status launch(const PrefillArgs& a, cudaStream_t s)
 {
     if ((int64_t)a.num_blocks * a.hkv * a.block_size >= ((int64_t)1 << 31)) return KVATTN_ERR_UNSUPPORTED;
     const int64_t step = 2 * kBM / (a.hq / a.hkv);
+    if (!window_items_ok(a)) return KVATTN_ERR_UNSUPPORTED;
     const int64_t items = a.num_chunks * ((a.max_q_len + step - 1) / step) * a.hkv;  // at most
-    if (items > 0x3fffffff) return KVATTN_ERR_UNSUPPORTED;  // item numbers of the round past the last are 32-bit too
     Maps maps;
     if (!make_maps<kHD>(a, maps)) return KVATTN_ERR_CUDA;
     constexpr int kSmem = Geo<kHD>::kSmemBytes;

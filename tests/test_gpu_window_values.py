@@ -213,3 +213,26 @@ def test_prefill_fp8_infinite_key_of_a_later_row(kvattn_lib):
     assert kv.get_device_status() == 0
     want, mag = attend(q[:-1].double().numpy(), c.k[0] * small, c.v[0], mask[:-1])
     check_attention(f64(out)[:-1], want, mag, "fp8", "rows before")
+
+
+def test_prefill_fp8_refusal_launches_nothing(kvattn_lib):
+    """More work items than can be numbered, by a max_q_len far past the chunk's: refused before the workspace is
+    touched, in the plain form as well."""
+    kv = kvattn_lib
+    hq, hkv, n, window, sinks, most = 128, 32, 20, 16, 2, 2 ** 31 - 1
+    c = WindowCache(kv, "fp8", hkv, 128, [n], [np.ones(n, bool)], seed=1)
+    cfg = kv.make_config(hq, hkv, 128, kv.BF16)
+    q = _q(2, (n, hq, 128)).cuda()
+    cu, prefix = torch.tensor([0, n], dtype=torch.int32).cuda(), torch.zeros(1, dtype=torch.int32).cuda()
+    ws = torch.full((kv.prefill_window_fp8_workspace_size(cfg, 16, c.d_table.shape[1], 1, most, window, sinks),), 77,
+                    dtype=torch.uint8, device="cuda")
+    out = torch.full_like(q, 9.0)
+    with pytest.raises(kv.KvattnError, match="UNSUPPORTED"):
+        kv.prefill_window_fp8(cfg, c.cache, q, cu, prefix, c.d_table, most, window, sinks, out=out, workspace=ws)
+    c16 = WindowCache(kv, "bf16", hkv, 128, [n], [np.ones(n, bool)], seed=1)
+    with pytest.raises(kv.KvattnError, match="UNSUPPORTED"):
+        kv.prefill_window(cfg, c16.cache, q, cu, prefix, c16.d_table, most, window, sinks, out=out)
+    torch.cuda.synchronize()
+    assert torch.all(ws == 77) and torch.all(out == 9.0) and kv.get_device_status() == 0
+    kv.prefill_window_fp8(cfg, c.cache, q, cu, prefix, c.d_table, n, window, sinks, out=out, workspace=ws)
+    assert kv.get_device_status() == 0 and torch.all(out != 9.0) and not torch.all(ws == 77)
