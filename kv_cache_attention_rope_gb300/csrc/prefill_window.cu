@@ -35,8 +35,9 @@
 //  - warps 12-15: O / row sums -> bf16 rows of out, while the others are at
 //    the next item (and, over an fp8 cache's copy, q -> f16 as it arrives).
 // TMEM: S_A, S_B, O_A, O_B, 128 columns each.  Every wait on a barrier is
-// bounded (1 s): a timeout records KVATTN_ERR_TIMEOUT, the roles stop waiting,
-// drain their copies and MMAs, free TMEM and return.
+// bounded (1 s, and more where many tiles go by meanwhile): a timeout records
+// KVATTN_ERR_TIMEOUT, the roles stop waiting, drain their copies and MMAs, free TMEM
+// and return.
 #include <algorithm>
 #include <cstring>
 #include <mutex>
@@ -109,6 +110,23 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, vo
     if (mbar_wait(bar, parity, status)) return true;
     *abort_flag = 1;
     return false;
+}
+
+// Whole-warp wait of the roles that do not take part in every tile: for as long as
+// the `tiles` that go by meanwhile may take besides (1.3 to 3.5 us each), and not
+// past an abort.
+constexpr uint64_t kTileLimitNs = 8000;
+__device__ __forceinline__ bool long_wait(uint64_t* bar, uint32_t parity, int tiles, volatile int* abort_flag, int* status)
+{
+    const uint64_t limit = kWaitLimitNs + (uint64_t)tiles * kTileLimitNs, t0 = global_timer_ns();
+    bool ok = false;
+    while (!(ok = mbar_try_wait(bar, parity)) && !*abort_flag) {
+        if (global_timer_ns() - t0 > limit) {
+            record_error(status, KVATTN_ERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
 }
 
 // Whole-warp wait: every lane waits, the warp agrees.
@@ -610,16 +628,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             // may hold anything, and 0 * NaN is NaN.
             // The copies of such a tile complete on v_raw, and this warp completes
             // v_full.
-            int g = 0;
-            uint32_t fixes = 0;  // bit s: parity of stage s's tiles seen here so far
+            int g = 0, since = 0;  // tiles; tiles since the last wait
+            uint32_t fixes = 0;    // bit s: parity of stage s's tiles seen here so far
             bool ok = true;
             Walk w;
             while (ok && next_item(w)) {
                 const Unseen un = unseen_of(a, w.p, w.g);
                 for (int t = 0; t < w.g.tiles; ++t, ++g) {
+                    ++since;
                     if (!has_unseen(a, un, t)) continue;
                     const int s = g % kStages;
-                    if (!(ok = warp_wait(&B.v_raw[s], fixes >> s & 1u, abort_flag, a.status))) break;
+                    if (!(ok = long_wait(&B.v_raw[s], fixes >> s & 1u, since, abort_flag, a.status))) break;
+                    since = 0;
                     fixes ^= 1u << s;
                     unsigned char* tile = smem + kOffV + s * kTileBytes;
                     constexpr int kChunks = kHD / 8;  // 16-byte chunks of a row: a warp's stores are of whole rows
@@ -790,10 +810,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
         int ii = 0;
         bool ok = true;
-        auto convert_q = [&](uint32_t parity) {
+        auto convert_q = [&](uint32_t parity, int tiles) {
 #pragma unroll 1
             for (int x = 0; ok && x < 2; ++x) {
-                if (!(ok = warp_wait(&B.q_full[x], parity, abort_flag, a.status))) break;
+                if (!(ok = long_wait(&B.q_full[x], parity, tiles, abort_flag, a.status))) break;
                 uint4* q = reinterpret_cast<uint4*>(smem + kOffQ + x * kTileBytes);
 #pragma unroll 4
                 for (int i = r; i < kTileBytes / 16; i += 128) {
@@ -807,14 +827,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         Walk w, ahead;
         bool more = next_item(ahead);
-        if (kF16 && more) convert_q(0);
+        if (kF16 && more) convert_q(0, 0);
         while (ok && more) {
             w = ahead;
             more = next_item(ahead);
             // (the next item's Q comes once this one's scores are done, before its
             // sums and outputs are)
-            if (kF16 && more) convert_q((ii + 1) & 1);
-            if (!ok || !warp_wait(&B.l_full[ii & 1], (ii >> 1) & 1, abort_flag, a.status)) break;
+            if (kF16 && more) convert_q((ii + 1) & 1, w.g.tiles);
+            if (!ok || !long_wait(&B.l_full[ii & 1], (ii >> 1) & 1, w.g.tiles, abort_flag, a.status)) break;
             const float* lx = xchg + 512 + (ii & 1) * 512;
             const float l[2] = {lx[r] + lx[256 + r], lx[128 + r] + lx[384 + r]};
             const float vmul = kF16 ? a.kv_scale[(int64_t)w.p.c * a.hkv + w.h].y : 1.f;

@@ -236,3 +236,22 @@ def test_prefill_fp8_refusal_launches_nothing(kvattn_lib):
     assert torch.all(ws == 77) and torch.all(out == 9.0) and kv.get_device_status() == 0
     kv.prefill_window_fp8(cfg, c.cache, q, cu, prefix, c.d_table, n, window, sinks, out=out, workspace=ws)
     assert kv.get_device_status() == 0 and torch.all(out != 9.0) and not torch.all(ws == 77)
+
+
+def test_prefill_longer_than_a_wait(kvattn_lib):
+    """1.7 s of items without a row to zero (they end where a tile does), then one that has some: the role that zeroes
+    them waits from the start to the end.  Keys of zeros and V of a power of two per dim make every sum exact."""
+    kv = kvattn_lib
+    keys, rows, block, d, heads = 2 ** 20, 190 * 256, 4096, 64, 128
+    cfg = kv.make_config(heads, heads, d, kv.BF16)
+    v = (2.0 ** (torch.arange(d) % 5)).to(torch.bfloat16)
+    cache = kv.Cache(torch.zeros((2, heads, block, d), dtype=torch.bfloat16, device="cuda"),
+                     v.expand(2, heads, block, d).contiguous().cuda())
+    table = (torch.arange(keys // block, dtype=torch.int32) % 2).expand(2, -1).contiguous().cuda()
+    q = torch.ones((rows + 1, heads, d), dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor([0, rows, rows + 1], dtype=torch.int32).cuda()
+    prefix = torch.tensor([keys - rows, 0], dtype=torch.int32).cuda()
+    out = torch.zeros_like(q)
+    kv.prefill_window(cfg, cache, q, cu, prefix, table, rows, 2 ** 31 - 1, out=out)
+    assert kv.get_device_status() == 0
+    assert torch.all(out == v.cuda())
