@@ -543,8 +543,11 @@ kvattn_status kvattn_prefill_chunk_fp8(const kvattn_config* cfg, const kvattn_ca
  * table entries, and the slots that no row of the chunk sees, may be anything.
  * V elements that some row of a chunk sees must be finite (a row's weight of a
  * key it does not see is 0, and 0 times an infinity is not).
- *   window      >= 1, num_sinks >= 0; sequences of up to 2^30 keys (a longer
- *               one is a BAD_INDEX)
+ *   window      >= 1, num_sinks >= 0; sequences of up to 2^30 keys, of which a
+ *               row sees up to 2^20 (a chunk past either is a BAD_INDEX).  The
+ *               tensor cores' sums drop what lies 2^-25 below them, so n seen keys
+ *               whose V agree in sign lose up to n 2^-26 of the output: 2^-9 at
+ *               131072, less than an output's rounding, 2^-6 at 2^20
  * The other arguments, results and errors as kvattn_prefill_chunk.
  *
  * kvattn_prefill_window_fp8: the same over a kvattn_cache_fp8 (head_dim 128).

@@ -247,6 +247,10 @@ struct PrefillArgs {
 kvattn_status launch_prefill(const PrefillArgs& a, cudaStream_t s);
 kvattn_status launch_prefill_window(const PrefillArgs& a, cudaStream_t s);
 constexpr int32_t kMaxWindowKeys = 1 << 30;  // keys of a sequence, window and sinks of a windowed prefill
+// Keys that a row of it sees.  The tensor cores drop what of a product lies below
+// 2^-25 of the sum that it is added to (2^28 keys of equal weight and V = 1 add up
+// to 2^26), so n keys lose up to n 2^-26 of their sum.
+constexpr int32_t kMaxSeenKeys = 1 << 20;
 // Whether a windowed prefill's work items (one KV head, 256 rows of its group of
 // query heads) can be numbered: numbers of the round past the last are 32-bit too.
 inline bool window_items_ok(const PrefillArgs& a)
@@ -285,6 +289,14 @@ kvattn_status launch_prefill_window_fp8(const PrefillArgs& pa, const void* pool,
                                         void* workspace, cudaStream_t s);
 
 // ---------------------------------------------------------------- device side
+
+// Whether a windowed prefill takes a chunk of qlen > 0 queries after a prefix of P
+// >= 0 keys: the last row sees the most.
+__device__ __forceinline__ bool window_keys_ok(int P, int qlen, int window, int sinks)
+{
+    const int64_t total = (int64_t)P + qlen, low = total > window ? total - window : 0;
+    return total <= kMaxWindowKeys && total - low + (low < sinks ? low : sinks) <= kMaxSeenKeys;
+}
 
 // Waits for the grid launched before this one on the stream (see launch_pdl).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

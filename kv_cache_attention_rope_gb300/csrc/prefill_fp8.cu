@@ -226,7 +226,7 @@ __device__ __forceinline__ SeenBlocks seen_blocks(const Fp8PrefillArgs& a, int c
     const int all = chunk_blocks(a, c);
     const int P = a.prefix_lens[c];
     s.total = P + a.cu_q_lens[c + 1] - a.cu_q_lens[c];
-    if (all == 0 || s.total > kMaxWindowKeys) return s;
+    if (all == 0 || !window_keys_ok(P, s.total - P, a.window, a.sinks)) return s;
     s.low = max(0, P - a.window + 1);
     s.lead = a.sinks > 0 ? min(all, (a.sinks - 1) / a.block_size + 1) : 0;
     s.gap = max(0, s.low / a.block_size - s.lead);

@@ -193,7 +193,8 @@ __device__ __forceinline__ int chunk_rows(const PrefillArgs& a, int c, bool repo
 {
     const int q0 = a.cu_q_lens[c], qlen = a.cu_q_lens[c + 1] - q0, P = a.prefix_lens[c];
     if (qlen < 0 || P < 0 || qlen > a.max_q_len || q0 < 0 || (int64_t)q0 + qlen > a.total_q ||
-        (int64_t)P + qlen > min((int64_t)a.max_blocks * a.block_size, (int64_t)kMaxWindowKeys)) {
+        (int64_t)P + qlen > (int64_t)a.max_blocks * a.block_size ||
+        (qlen > 0 && !window_keys_ok(P, qlen, a.window, a.sinks))) {
         if (report) record_error(a.status, KVATTN_ERR_BAD_INDEX);
         return 0;
     }

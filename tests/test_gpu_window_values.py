@@ -255,3 +255,46 @@ def test_prefill_longer_than_a_wait(kvattn_lib):
     kv.prefill_window(cfg, cache, q, cu, prefix, table, rows, 2 ** 31 - 1, out=out)
     assert kv.get_device_status() == 0
     assert torch.all(out == v.cuda())
+
+
+def test_prefill_of_a_very_long_sequence(kvattn_lib):
+    """One row over 2^28 keys: refused where it sees more than 2^20 of them (the tensor cores' sums of equal V stop growing
+    at 2^26), answered where it sees 2^20, and a chunk without rows is no error.  Keys of zeros and V of a power of two
+    per dim make every sum exact."""
+    kv = kvattn_lib
+    keys, block, d = 2 ** 28, 4096, 64
+    cfg = kv.make_config(1, 1, d, kv.BF16)
+    v = (2.0 ** (torch.arange(d) % 5)).to(torch.bfloat16)
+    cache = kv.Cache(torch.zeros((2, 1, block, d), dtype=torch.bfloat16, device="cuda"),
+                     v.expand(2, 1, block, d).contiguous().cuda())
+    table = (torch.arange(keys // block, dtype=torch.int32) % 2)[None].cuda()
+    q = _q(1, (1, 1, d)).cuda()
+    cu, prefix = torch.tensor([0, 1], dtype=torch.int32).cuda(), torch.tensor([keys - 1], dtype=torch.int32).cuda()
+    bad = kv.STATUS_CODE["KVATTN_ERR_BAD_INDEX"]
+    for window, sinks, status in ((2 ** 31 - 1, 0, bad), (2 ** 20 + 1, 0, bad), (2 ** 20, 4, bad), (1, 2 ** 20, bad),
+                                  (2 ** 20, 0, 0), (2 ** 20 - 4, 4, 0), (1, 2 ** 20 - 1, 0)):
+        out = torch.zeros_like(q)
+        kv.prefill_window(cfg, cache, q, cu, prefix, table, 1, window, sinks, out=out)
+        assert kv.get_device_status() == status, (window, sinks)
+        assert torch.equal(out[0, 0].cpu(), torch.zeros_like(v) if status else v), (window, sinks)
+    kv.prefill_window(cfg, cache, q, cu * 0, prefix, table, 1, 2 ** 31 - 1, out=out)
+    assert kv.get_device_status() == 0
+
+
+def test_prefill_fp8_of_a_very_long_sequence(kvattn_lib):
+    """The same limit over an fp8 cache."""
+    kv = kvattn_lib
+    keys, block = 2 ** 20 + 16, 4096
+    pool = torch.zeros((1, 1, block // 16, 4224), dtype=torch.uint8, device="cuda")
+    pool[..., 2048:4096] = 0x38                                      # V = 1
+    pool[..., 4096:] = torch.ones(32).view(torch.uint8).cuda()
+    cfg = kv.make_config(4, 1, 128, kv.BF16)
+    table = torch.zeros((1, -(-keys // block)), dtype=torch.int32, device="cuda")
+    q = _q(1, (1, 4, 128)).cuda()
+    cu = torch.tensor([0, 1], dtype=torch.int32).cuda()
+    for prefix, status in ((2 ** 20, kv.STATUS_CODE["KVATTN_ERR_BAD_INDEX"]), (2 ** 20 - 1, 0)):
+        out = torch.zeros_like(q)
+        kv.prefill_window_fp8(cfg, kv.CacheFP8(pool, block), q, cu, torch.tensor([prefix], dtype=torch.int32).cuda(), table,
+                              1, 2 ** 31 - 1, out=out)
+        assert kv.get_device_status() == status
+        assert torch.all(out == (0.0 if status else 1.0))
