@@ -206,7 +206,7 @@ kvattn_status kvattn_rope_append_strided(const kvattn_config* cfg, const kvattn_
  *                           b^(-2i/R) / (2 pi): pairs of more than `high` turns
  *                           over the original context keep their speed, pairs
  *                           of fewer than `low` turns slow by s
- * computed in double.  The products and sums of a rotation are fp32 and a
+ * rounded to 2^-64 turns.  The products and sums of a rotation are fp32 and a
  * stored element is rounded once: within half an ulp of its type plus
  * 2^-21 a (|x0| + |x1|) of exact at any position.
  *

@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <limits>
 #include <mutex>
 
 #include "kvattn_internal.cuh"
@@ -191,34 +192,48 @@ bool rotary_ok(const kvattn_config* c, const kvattn_rotary* r)
 
 // Speed of pair i < rot / 2 in 2^-64 turns per position (kvattn_rotary_append
 // in kvattn.h states the formulas; with base and factor at least 1 it is below
-// 1 / (2 pi) turns).  A model's layers share one form: the last one computed by
-// this host thread is kept.
+// 1 / (2 pi) turns).  At position 2^31 an error of 2^-53 in a speed near 1 would be
+// 2^-22 radians, hence the wider type, which takes longer (128 bits in software on
+// Arm).  The layers of a model share one form or a few: the last ones computed by
+// this host thread are kept.
 void rotary_turns(const kvattn_config* c, const kvattn_rotary* r, int rot, uint64_t* turns)
 {
-    static thread_local kvattn_rotary last;
-    static thread_local float last_base = 0.f;
-    static thread_local int last_rot = 0;
-    static thread_local uint64_t kept[64];
-    if (last_rot != rot || last_base != c->rope_base || std::memcmp(&last, r, sizeof(last)) != 0) {
-        const double two_pi = 6.283185307179586476925286766559, s = r->factor;
-        double base = c->rope_base;
-        if (r->scaling == KVATTN_ROPE_BASE) base *= std::pow(s, (double)rot / (double)(rot - 2));
-        for (int i = 0; i < rot / 2; ++i) {
-            double f = std::pow(base, -2.0 * (double)i / (double)rot) / two_pi;
-            if (r->scaling == KVATTN_ROPE_LINEAR) {
-                f /= s;
-            } else if (r->scaling == KVATTN_ROPE_PARTS) {
-                const double g = ((double)r->original_len * f - r->low) / ((double)r->high - r->low);
-                const double share = std::min(1.0, std::max(0.0, g));
-                f = f * (share + (1.0 - share) / s);
-            }
-            kept[i] = (uint64_t)std::llrint(std::ldexp(f, 64));
+    using real = long double;
+    static_assert(std::numeric_limits<real>::digits >= 64, "the host's long double holds a speed to 2^-64");
+    struct Form {
+        kvattn_rotary r;
+        float base;
+        int rot;  // 0: none
+        uint64_t turns[64];
+    };
+    constexpr int kForms = 4;
+    static thread_local Form kept[kForms];
+    static thread_local int oldest = 0;
+    for (const Form& k : kept)
+        if (k.rot == rot && k.base == c->rope_base && std::memcmp(&k.r, r, sizeof(k.r)) == 0) {
+            std::memcpy(turns, k.turns, sizeof(k.turns));
+            return;
         }
-        last = *r;
-        last_base = c->rope_base;
-        last_rot = rot;
+    Form& k = kept[oldest];
+    oldest = (oldest + 1) % kForms;
+    const real two_pi = 6.28318530717958647692528676655900577L, s = r->factor;
+    real base = c->rope_base;
+    if (r->scaling == KVATTN_ROPE_BASE) base *= std::pow(s, (real)rot / (real)(rot - 2));
+    for (int i = 0; i < rot / 2; ++i) {
+        real f = std::pow(base, (real)(-2 * i) / (real)rot) / two_pi;
+        if (r->scaling == KVATTN_ROPE_LINEAR) {
+            f /= s;
+        } else if (r->scaling == KVATTN_ROPE_PARTS) {
+            const real g = ((real)r->original_len * f - r->low) / ((real)r->high - r->low);
+            const real share = std::min<real>(1, std::max<real>(0, g));
+            f = f * (share + (1 - share) / s);
+        }
+        k.turns[i] = (uint64_t)std::llrint(std::ldexp(f, 64));
     }
-    std::memcpy(turns, kept, sizeof(kept));
+    k.r = *r;
+    k.base = c->rope_base;
+    k.rot = rot;
+    std::memcpy(turns, k.turns, sizeof(k.turns));
 }
 
 // One CTA waits on an mbarrier that nothing will complete, through the same
