@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 import os
 
 from . import _build
@@ -489,11 +490,19 @@ def prefill_chunk_fp8(cfg: Config, cache: CacheFP8, q, cu_q_lens, prefix_lens, b
 
 # ------------------------------------------------------------------ rotary forms, sliding windows
 
+def _int32(value, name: str) -> int:
+    """The value of an int32 argument (ctypes would keep the low 32 bits of a larger one)."""
+    value = operator.index(value)
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise ValueError(f"{name} must fit 32 bits, got {value}")
+    return value
+
+
 def make_rotary(layout: str = "adjacent", rotary_dim: int = 0, scaling: str = "none", factor: float = 1.0,
                 original_len: float = 0.0, low: float = 1.0, high: float = 32.0, amplitude: float = 1.0) -> Rotary:
     """The rotary form of kvattn_rotary_append: pairs "adjacent" or "half", rotary_dim rotated dims (0: the whole
     head), speeds "none", "linear", "base" or "parts" scaled by factor, amplitude on the rotated dims."""
-    return Rotary(ROPE_LAYOUT[layout], rotary_dim, ROPE_SCALING[scaling], factor, original_len, low, high, amplitude)
+    return Rotary(ROPE_LAYOUT[layout], _int32(rotary_dim, "rotary_dim"), ROPE_SCALING[scaling], factor, original_len, low, high, amplitude)
 
 
 # These calls may be a few microseconds of GPU work each, so their marshalling is kept short.  With every buffer given
@@ -642,8 +651,9 @@ def rotary_append_fp8(cfg: Config, rotary: Rotary, cache: CacheFP8, q, k, v, pos
 def decode_window_workspace_size(cfg: Config, batch: int, max_seq_len: int, window: int, num_sinks: int = 0,
                                  num_splits: int = 0) -> int:
     """kvattn_decode_window_workspace_size (0 for invalid arguments)."""
-    return int(lib.kvattn_decode_window_workspace_size(ctypes.byref(cfg), batch, max_seq_len, window, num_sinks,
-                                                       num_splits))
+    return int(lib.kvattn_decode_window_workspace_size(
+        ctypes.byref(cfg), _int32(batch, "batch"), _int32(max_seq_len, "max_seq_len"), _int32(window, "window"),
+        _int32(num_sinks, "num_sinks"), _int32(num_splits, "num_splits")))
 
 
 def _decode_window(fn, what, kind, cfg, cache, q, block_table, seq_lens, max_seq_len, window, num_sinks, out,
@@ -658,8 +668,9 @@ def _decode_window(fn, what, kind, cfg, cache, q, block_table, seq_lens, max_seq
     wp, nbytes = _scratch(workspace, lambda: decode_window_workspace_size(cfg, B, max_seq_len, window, num_sinks,
                                                                           num_splits), q, device, stream)
     check(fn(ctypes.byref(cfg), desc, _ptr(q, "q", dt, device), table, width,
-             _ptr(seq_lens, "seq_lens", _torch().int32, device), B, max_seq_len, window, num_sinks, num_splits, op, wp,
-             nbytes, s), what)
+             _ptr(seq_lens, "seq_lens", _torch().int32, device), B, _int32(max_seq_len, "max_seq_len"),
+             _int32(window, "window"), _int32(num_sinks, "num_sinks"), _int32(num_splits, "num_splits"), op, wp, nbytes,
+             s), what)
     return out
 
 
@@ -690,7 +701,7 @@ def decode_window_fp8(cfg: Config, cache: CacheFP8, q, block_table, seq_lens, ma
                           block_table, seq_lens, max_seq_len, window, num_sinks, out, workspace, num_splits, stream)
 
 
-def _prefill_window_args(kind, cfg, cache, q, cu_q_lens, prefix_lens, block_table, device):
+def _prefill_window_args(kind, cfg, cache, q, cu_q_lens, prefix_lens, block_table, max_q_len, window, num_sinks, device):
     torch = _torch()
     desc, _ = _check_cache(cfg, cache, kind, device)
     n = prefix_lens.shape[0]
@@ -700,7 +711,8 @@ def _prefill_window_args(kind, cfg, cache, q, cu_q_lens, prefix_lens, block_tabl
     table, width = _table(block_table, n, device)
     return n, (ctypes.byref(cfg), desc, _ptr(q, "q", torch.bfloat16, device),
                _ptr(cu_q_lens, "cu_q_lens", torch.int32, device), _ptr(prefix_lens, "prefix_lens", torch.int32, device),
-               table, width, n)
+               table, width, n, _int32(max_q_len, "max_q_len"), q.shape[0], _int32(window, "window"),
+               _int32(num_sinks, "num_sinks"))
 
 
 def prefill_window(cfg: Config, cache: Cache, q, cu_q_lens, prefix_lens, block_table, max_q_len: int, window: int,
@@ -714,17 +726,20 @@ def prefill_window(cfg: Config, cache: Cache, q, cu_q_lens, prefix_lens, block_t
             check(st, "kvattn_prefill_window")
             return out
     device, s = _here(stream)
-    _, args = _prefill_window_args(Cache, cfg, cache, q, cu_q_lens, prefix_lens, block_table, device)
+    _, args = _prefill_window_args(Cache, cfg, cache, q, cu_q_lens, prefix_lens, block_table, max_q_len, window,
+                                   num_sinks, device)
     out, op = _out(out, q, q.dtype, device, stream)
-    check(lib.kvattn_prefill_window(*args, max_q_len, q.shape[0], window, num_sinks, op, s), "kvattn_prefill_window")
+    check(lib.kvattn_prefill_window(*args, op, s), "kvattn_prefill_window")
     return out
 
 
 def prefill_window_fp8_workspace_size(cfg: Config, block_size: int, max_blocks_per_seq: int, num_chunks: int,
                                       max_q_len: int, window: int, num_sinks: int = 0) -> int:
     """kvattn_prefill_window_fp8_workspace_size (0 for invalid arguments)."""
-    return int(lib.kvattn_prefill_window_fp8_workspace_size(ctypes.byref(cfg), block_size, max_blocks_per_seq,
-                                                            num_chunks, max_q_len, window, num_sinks))
+    return int(lib.kvattn_prefill_window_fp8_workspace_size(
+        ctypes.byref(cfg), _int32(block_size, "block_size"), _int32(max_blocks_per_seq, "max_blocks_per_seq"),
+        _int32(num_chunks, "num_chunks"), _int32(max_q_len, "max_q_len"), _int32(window, "window"),
+        _int32(num_sinks, "num_sinks")))
 
 
 def prefill_window_fp8(cfg: Config, cache: CacheFP8, q, cu_q_lens, prefix_lens, block_table, max_q_len: int,
@@ -737,12 +752,12 @@ def prefill_window_fp8(cfg: Config, cache: CacheFP8, q, cu_q_lens, prefix_lens, 
             check(st, "kvattn_prefill_window_fp8")
             return out
     device, s = _here(stream)
-    n, args = _prefill_window_args(CacheFP8, cfg, cache, q, cu_q_lens, prefix_lens, block_table, device)
+    n, args = _prefill_window_args(CacheFP8, cfg, cache, q, cu_q_lens, prefix_lens, block_table, max_q_len, window,
+                                   num_sinks, device)
     out, op = _out(out, q, q.dtype, device, stream)
     wp, nbytes = _scratch(workspace, lambda: prefill_window_fp8_workspace_size(
         cfg, cache.block_size, block_table.shape[1], n, max_q_len, window, num_sinks), q, device, stream)
-    check(lib.kvattn_prefill_window_fp8(*args, max_q_len, q.shape[0], window, num_sinks, op, wp, nbytes, s),
-          "kvattn_prefill_window_fp8")
+    check(lib.kvattn_prefill_window_fp8(*args, op, wp, nbytes, s), "kvattn_prefill_window_fp8")
     return out
 
 

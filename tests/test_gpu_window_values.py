@@ -298,3 +298,34 @@ def test_prefill_fp8_of_a_very_long_sequence(kvattn_lib):
                               1, 2 ** 31 - 1, out=out)
         assert kv.get_device_status() == status
         assert torch.all(out == (0.0 if status else 1.0))
+
+
+def test_python_integers_past_32_bits(kvattn_lib):
+    """An integer that does not fit raises; its low 32 bits are not taken for it."""
+    kv = kvattn_lib
+    c = WindowCache(kv, "bf16", 2, 128, [40], [np.ones(40, bool)], seed=1)
+    c8 = WindowCache(kv, "fp8", 2, 128, [40], [np.ones(40, bool)], seed=1)
+    cfg = kv.make_config(8, 2, 128, kv.BF16)
+    q = _q(0, (1, 8, 128)).cuda()
+    n = torch.tensor([40], dtype=torch.int32).cuda()
+    cu, prefix = torch.tensor([0, 1], dtype=torch.int32).cuda(), n - 1
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    out = torch.full_like(q, 5.0)
+    for given in (dict(out=out, workspace=ws), dict(out=out), {}):
+        for cache, dec, pre in ((c.cache, kv.decode_window, kv.prefill_window),
+                                (c8.cache, kv.decode_window_fp8, kv.prefill_window_fp8)):
+            more = {k: v for k, v in given.items() if k == "out" or pre is kv.prefill_window_fp8}
+            for wrong in (2 ** 32 + 16, 2 ** 31, -2 ** 32 + 16):
+                for name in ("max_seq_len", "window", "num_sinks", "num_splits"):
+                    with pytest.raises(ValueError, match=name):
+                        dec(cfg, cache, q, c.d_table, n, **{**dict(max_seq_len=40, window=16, num_sinks=2), name: wrong}, **given)
+                for name in ("max_q_len", "window", "num_sinks"):
+                    with pytest.raises(ValueError, match=name):
+                        pre(cfg, cache, q, cu, prefix, c.d_table, **{**dict(max_q_len=1, window=16, num_sinks=2), name: wrong},
+                            **more)
+            with pytest.raises(TypeError):
+                dec(cfg, cache, q, c.d_table, n, 40, 16.0, **given)
+    torch.cuda.synchronize()
+    assert torch.all(out == 5.0)
+    a = kv.decode_window(cfg, c.cache, q, c.d_table, n, np.int64(40), np.int32(16), 2)
+    assert torch.equal(a, kv.decode_window(cfg, c.cache, q, c.d_table, n, 40, 16, 2, out=out, workspace=ws))
