@@ -150,11 +150,17 @@ def _load():
 
 lib = _load()
 
+
+
+class _General:
+    """In the place of the extension module where there is none: every call is marshalled the general way."""
+    setup = decode_window = prefill_window = rotary_append = staticmethod(lambda *args: None)
+
+
 try:
     from . import _marshal
-except ImportError as e:
-    raise ImportError(f"kvattn's extension module is not built ({e}): run "
-                      "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+except ImportError:  # not built (no Python headers), or for another Python
+    _marshal = _General
 
 
 def check(code: int, what: str) -> None:
@@ -509,19 +515,22 @@ def make_rotary(layout: str = "adjacent", rotary_dim: int = 0, scaling: str = "n
 # and the current stream, _marshal (csrc/marshal.cpp) checks the tensors and makes the call; it returns None when
 # something is not as it should be, and the functions here then say what, or do the general case.
 
-_marshal_ready = False
+_raw_stream = None  # device index -> raw handle of the current stream
 
 
 def _here(stream):
     """Current CUDA device and the raw handle of the stream to use on it."""
-    global _marshal_ready
+    global _raw_stream
     torch = _torch()
     device = torch.cuda.current_device()
-    if not _marshal_ready:
-        _marshal.setup(torch._C._to_dlpack, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
-        _marshal_ready = True
+    if _raw_stream is None:
+        # (the torch._C names are the short way to what the public functions say)
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _marshal.setup(torch.utils.dlpack.to_dlpack, getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+                       _raw_stream)
     if stream is None:
-        return device, torch._C._cuda_getCurrentRawStream(device)
+        return device, _raw_stream(device)
     if stream.device.index != device:
         raise ValueError(f"stream of {stream.device}, but cuda:{device} is the current device")
     return device, stream.cuda_stream

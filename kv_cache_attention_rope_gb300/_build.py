@@ -5,13 +5,15 @@ import concurrent.futures
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkvattn.so")
-MARSHAL = os.path.join(PKG, "_marshal.so")  # Python extension module, linked against LIB beside it
+# Python extension module, linked against LIB beside it; the name says which Python it was built for
+MARSHAL = os.path.join(PKG, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["api.cu", "rope_append.cu", "rotary.cu", "decode.cu", "decode_window.cu", "decode_direct.cu", "decode_static.cu", "prefill.cu", "prefill_window.cu", "prefill_fp8.cu", "blocks.cu", "allocator.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -33,6 +35,24 @@ def _stale(obj: str, deps: list[str]) -> bool:
         return True
     t = os.path.getmtime(obj)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _build_marshal(force: bool, headers: list[str]) -> None:
+    """The extension module that shortens some calls' marshalling.  The package does without it, so a Python without its
+    headers is no error."""
+    src, include = os.path.join(CSRC, "marshal.cpp"), sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")) or not (force or _stale(MARSHAL, [src, *headers, __file__])):
+        return
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    r = subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", "-I", include,
+                        "-I", os.path.join(ROOT, "include"), src, "-o", tmp, "-L", PKG, "-l:libkvattn.so",
+                        "-Wl,-rpath,$ORIGIN"], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on marshal.cpp:\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+    untagged = os.path.join(PKG, "_marshal.so")  # an earlier build's, of whatever Python
+    if os.path.exists(untagged):
+        os.remove(untagged)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -73,17 +93,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stderr}")
         os.replace(tmp, LIB)
-    src = os.path.join(CSRC, "marshal.cpp")
-    if force or _stale(MARSHAL, [src, *headers, __file__]):
-        import sysconfig
-
-        tmp = MARSHAL + f".tmp{os.getpid()}"
-        r = subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
-                            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(ROOT, "include"), src, "-o", tmp,
-                            "-L", PKG, "-l:libkvattn.so", "-Wl,-rpath,$ORIGIN"], capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"g++ failed on marshal.cpp:\n{r.stderr}")
-        os.replace(tmp, MARSHAL)
+    _build_marshal(force, headers)
     with open(stamp, "w") as f:
         f.write(arch)
     return LIB

@@ -329,3 +329,38 @@ def test_python_integers_past_32_bits(kvattn_lib):
     assert torch.all(out == 5.0)
     a = kv.decode_window(cfg, c.cache, q, c.d_table, n, np.int64(40), np.int32(16), 2)
     assert torch.equal(a, kv.decode_window(cfg, c.cache, q, c.d_table, n, 40, 16, 2, out=out, workspace=ws))
+
+
+def test_calls_without_the_extension_module(kvattn_lib, monkeypatch):
+    """The general way of marshalling gives what the extension module's gives."""
+    kv = kvattn_lib
+    c = WindowCache(kv, "bf16", 2, 128, [40], [np.ones(40, bool)], seed=1)
+    c8 = WindowCache(kv, "fp8", 2, 128, [40], [np.ones(40, bool)], seed=1)
+    cfg, form = kv.make_config(8, 2, 128, kv.BF16), kv.make_rotary("half")
+    q, k = _q(0, (1, 8, 128)).cuda(), _q(1, (1, 2, 128)).cuda()
+    n = torch.tensor([40], dtype=torch.int32).cuda()
+    cu = torch.tensor([0, 1], dtype=torch.int32).cuda()
+
+    def calls():
+        out = []
+        for cache, app, dec, pre, ws in (
+                (c.cache, kv.rotary_append, kv.decode_window, kv.prefill_window, {}),
+                (c8.cache, kv.rotary_append_fp8, kv.decode_window_fp8, kv.prefill_window_fp8,
+                 dict(workspace=torch.empty(1 << 20, dtype=torch.uint8, device="cuda")))):
+            r, a, b = (torch.zeros_like(q) for _ in range(3))
+            app(cfg, form, cache, q, k, k, n - 1, n * 0, c.d_table if cache is c.cache else c8.d_table, q_out=r)
+            table = c.d_table if cache is c.cache else c8.d_table
+            dec(cfg, cache, r, table, n, 40, 16, 2, out=a, workspace=torch.empty(1 << 20, dtype=torch.uint8, device="cuda"))
+            pre(cfg, cache, r, cu, n - 1, table, 1, 16, 2, out=b, **ws)
+            out += [r, a, b]
+        return out
+
+    calls()
+    fast = calls()
+    monkeypatch.setattr(kv, "_marshal", kv._General)
+    slow = calls()
+    monkeypatch.setattr(kv, "_raw_stream", None)          # as in a process that never had it
+    slow += calls()
+    assert kv.get_device_status() == 0
+    for x, y in zip(fast + fast, slow):
+        assert torch.equal(x, y) and x.abs().sum() > 0

@@ -29,3 +29,39 @@ def test_sizes_past_32_bits(kv):
             kv.make_rotary("half", wrong)
     with pytest.raises(TypeError):
         kv.make_rotary("half", 64.0)
+
+
+def test_package_without_the_extension_module():
+    """Where the extension module is not built, or is another Python's, the package is all there."""
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import sys
+sys.modules['kv_cache_attention_rope_gb300._marshal'] = None     # importing it raises ImportError
+import kv_cache_attention_rope_gb300 as kv
+assert kv._marshal.decode_window(1, 2) is None
+cfg = kv.make_config(8, 2, 128, kv.BF16)
+assert kv.version() > 0 and kv.decode_window_workspace_size(cfg, 4, 1000, 100) > 0
+alloc = kv.BlockAllocator(4)
+assert len(alloc.alloc(3)) == 3
+print('whole')
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "whole" in r.stdout, r.stderr
+
+
+def test_extension_module_is_built_for_one_python(kv, tmp_path, monkeypatch):
+    """Its file name has the Python's tag, and without Python's headers the build goes without it."""
+    import importlib.machinery
+    import os
+    import sysconfig
+
+    build = kv._build
+    assert any("cpython" in s and build.MARSHAL.endswith("_marshal" + s) for s in importlib.machinery.EXTENSION_SUFFIXES)
+    monkeypatch.setattr(build, "MARSHAL", str(tmp_path / os.path.basename(build.MARSHAL)))
+    monkeypatch.setattr(sysconfig, "get_paths", lambda: {"include": str(tmp_path)})
+    build._build_marshal(True, [])
+    assert not os.listdir(tmp_path)
