@@ -19,6 +19,7 @@
 // of one to the B fragment of the other by movmatrix.  A warp keeps its own
 // running maximum and sum; the warps of a CTA merge through shared memory and
 // the CTAs of a cluster through distributed shared memory.
+#include <mutex>
 #include <type_traits>
 
 #include <cooperative_groups.h>
@@ -632,6 +633,39 @@ __global__ void __launch_bounds__(warps_per_sm(kKind, kD, kG) * 32, 1)
     }
 }
 
+// How many clusters of a size are resident at once, per device (a pure function of
+// the kernel, its block and its shared memory; asking the runtime takes longer than a
+// launch).  Clusters do not cross the GPU's groups of SMs, so these are fewer than the
+// SMs' CTAs over the size: of 8 CTAs at one per SM 15, where 152 / 8 is 19.
+class ClusterResidency {
+public:
+    template <typename Kernel>
+    int query(Kernel kern, const cudaLaunchConfig_t& cfg, int log2_size)
+    {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+        std::lock_guard<std::mutex> g(mu_);
+        Entry& e = kept_[dev][log2_size];
+        if (e.bytes != (int)cfg.dynamicSmemBytes) {
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+                (void)cudaGetLastError();
+                return 0;
+            }
+            e.bytes = (int)cfg.dynamicSmemBytes;
+            e.clusters = n;
+        }
+        return e.clusters;
+    }
+
+private:
+    struct Entry {
+        int bytes, clusters;
+    };
+    std::mutex mu_;
+    Entry kept_[64][4] = {};
+};
+
 template <int kKind, int kD, int kG>
 kvattn_status run_direct(const DecodeArgs& a, int warps, int cluster, cudaStream_t s)
 {
@@ -640,7 +674,6 @@ kvattn_status run_direct(const DecodeArgs& a, int warps, int cluster, cudaStream
     static SmemLimit limit;
     if (limit.ensure(reinterpret_cast<const void*>(kern), bytes) != cudaSuccess) return KVATTN_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.batch * a.hkv * cluster));
     cfg.blockDim = dim3(warps * 32);
     cfg.dynamicSmemBytes = bytes;
     cfg.stream = s;
@@ -648,9 +681,18 @@ kvattn_status run_direct(const DecodeArgs& a, int warps, int cluster, cudaStream
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
+    // half the CTAs per segment rather than a second wave of clusters (bf16 D = 128,
+    // 16 segments of 32768 keys: in clusters of 8 98.9 us, of 4 88.7)
+    static ClusterResidency resident;
+    for (; cluster > 1; cluster /= 2) {
+        attr[1].val.clusterDim.x = cluster;
+        cfg.gridDim = dim3((unsigned)(a.batch * a.hkv * cluster));
+        cfg.numAttrs = 2;
+        if (resident.query(kern, cfg, cluster == 8 ? 3 : cluster == 4 ? 2 : 1) >= a.batch * a.hkv) break;
+    }
+    cfg.gridDim = dim3((unsigned)(a.batch * a.hkv * cluster));
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cuda_status(cudaLaunchKernelEx(&cfg, kern, a, cluster));
 }
@@ -698,7 +740,8 @@ bool launch_decode_direct(const DecodeArgs& a, int32_t max_tiles, cudaStream_t s
     if (tiles > most || segs * 8 > INT32_MAX) return false;
     // One wave of warps: the most warps per CTA that let every segment be
     // resident (a quarter of the SM's when not even that does), at most 8;
-    // then CTAs per segment; but no warp without a tile, and no second CTA for
+    // then CTAs per segment, a cluster as large as lets them be resident (run_direct
+    // has the last word); but no warp without a tile, and no second CTA for
     // fewer than 4 tiles per warp, which cost less than the cluster's launch and
     // merge (18 tiles: 8 sequences of 12 fp32 heads of 64 4.4 us in one CTA and
     // 5.25 in two, 1 of 32 / 8 fp8 heads 5.1 and 5.3, of bf16 4.9 and 4.95).

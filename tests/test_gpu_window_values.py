@@ -364,3 +364,36 @@ def test_calls_without_the_extension_module(kvattn_lib, monkeypatch):
     assert kv.get_device_status() == 0
     for x, y in zip(fast + fast, slow):
         assert torch.equal(x, y) and x.abs().sum() > 0
+
+
+def _decode_us(kv, dtype, hq, batch, keys, calls=20):
+    """us of a decode_window call among others: sequences of one length, a cache larger than L2."""
+    cfg = kv.make_config(hq, 1, 128, kv.F32 if dtype == "f32" else kv.BF16)
+    t = TORCH_DT["f32" if dtype == "f32" else "bf16"]
+    block = 256
+    cache = kv.Cache(*(torch.zeros((batch * keys // block, 1, block, 128), dtype=t, device="cuda") for _ in range(2)))
+    table = torch.arange(batch * keys // block, dtype=torch.int32, device="cuda").view(batch, -1)
+    lens = torch.full((batch,), keys, dtype=torch.int32, device="cuda")
+    q = torch.ones((batch, hq, 128), dtype=t, device="cuda")
+    out = torch.empty_like(q)
+    ws = torch.empty(max(256, kv.decode_window_workspace_size(cfg, batch, keys, keys)), dtype=torch.uint8, device="cuda")
+    times = []
+    for _ in range(5):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(calls):
+            kv.decode_window(cfg, cache, q, table, lens, keys, keys, out=out, workspace=ws)
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b) * 1e3 / calls)
+    assert kv.get_device_status() == 0
+    return min(times)
+
+
+@pytest.mark.parametrize("dtype,hq,few,more,keys", [("bf16", 4, 16, 20, 16384), ("bf16", 4, 16, 20, 32768),
+                                                    ("f32", 1, 16, 20, 16384), ("bf16", 4, 38, 44, 16384)])
+def test_fewer_sequences_take_no_longer(kvattn_lib, dtype, hq, few, more, keys):
+    """A count of segments whose clusters are not resident at once, and a larger one whose smaller clusters are."""
+    a, b = _decode_us(kvattn_lib, dtype, hq, few, keys), _decode_us(kvattn_lib, dtype, hq, more, keys)
+    print(f"{few}: {a:.1f} us, {more}: {b:.1f} us")
+    assert a <= 1.04 * b, (a, b)
