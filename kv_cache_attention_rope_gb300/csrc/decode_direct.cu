@@ -666,13 +666,17 @@ private:
     Entry kept_[64][4] = {};
 };
 
+// False, with nothing launched, where the balanced stream is the faster one.
 template <int kKind, int kD, int kG>
-kvattn_status run_direct(const DecodeArgs& a, int warps, int cluster, cudaStream_t s)
+bool run_direct(const DecodeArgs& a, int max_tiles, int warps, int cluster, cudaStream_t s, kvattn_status* st)
 {
     auto kern = decode_direct_kernel<kKind, kD, kG>;
-    const int bytes = direct_floats(kKind, warps, a.hq / a.hkv, kD) * 4;
+    const int G = a.hq / a.hkv, bytes = direct_floats(kKind, warps, G, kD) * 4;
     static SmemLimit limit;
-    if (limit.ensure(reinterpret_cast<const void*>(kern), bytes) != cudaSuccess) return KVATTN_ERR_CUDA;
+    if (limit.ensure(reinterpret_cast<const void*>(kern), bytes) != cudaSuccess) {
+        *st = KVATTN_ERR_CUDA;
+        return true;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(warps * 32);
     cfg.dynamicSmemBytes = bytes;
@@ -692,29 +696,45 @@ kvattn_status run_direct(const DecodeArgs& a, int warps, int cluster, cudaStream
         cfg.numAttrs = 2;
         if (resident.query(kern, cfg, cluster == 8 ? 3 : cluster == 4 ? 2 : 1) >= a.batch * a.hkv) break;
     }
+    // Clusters that leave warps' places empty, with many bytes a warp: the stream,
+    // which cuts segments anywhere, fills them once there are 16 segments (at most
+    // 16 pieces each).  Measured (us, this and the stream): bf16 D = 128 without
+    // groups, 38 segments of 16384 keys 88.7 / 68.3, groups of 4, 16 of 32768 88.7 /
+    // 78.5; fp32 groups of 4, 16 of 16384 84.6 / 68.3, 38 of 4096 53.9 / 45.7.  With
+    // fewer segments it loses (bf16, 8 of 32768 51.8 / 78.5, 15 62.1 / 78.5), with
+    // half the bf16 keys it gains little or loses (groups of 4, 16 of 16384 51.8 /
+    // 49.8, repeated calls 41.1 / 46.6), and it always does with fp8 pages and bf16 D
+    // = 64 (16 of 32768 66.2 / 86.7 and 47.7 / 72.3).
+    if constexpr (kKind == kF32Cache || (kKind == kBf16Cache && kD == 128)) {
+        const int64_t segs = (int64_t)a.batch * a.hkv, places = (int64_t)num_sms() * warps_per_sm(kKind, kD, G);
+        const int64_t per_warp = (int64_t)max_tiles * 2 * kTile * kD * (kKind == kF32Cache ? 4 : 2) / (cluster * warps);
+        const int64_t many = (kKind == kF32Cache ? 256 : 512) << 10;
+        if (segs >= 16 && segs * cluster * warps * 10 < places * 7 && per_warp >= many) return false;
+    }
     cfg.gridDim = dim3((unsigned)(a.batch * a.hkv * cluster));
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, kern, a, cluster));
+    *st = cuda_status(cudaLaunchKernelEx(&cfg, kern, a, cluster));
+    return true;
 }
 
-kvattn_status direct_dispatch(const DecodeArgs& a, int warps, int cluster, cudaStream_t s)
+bool direct_dispatch(const DecodeArgs& a, int max_tiles, int warps, int cluster, cudaStream_t s, kvattn_status* st)
 {
-    if (a.fp8) return run_direct<kFp8Cache, 128, 8>(a, warps, cluster, s);
+    if (a.fp8) return run_direct<kFp8Cache, 128, 8>(a, max_tiles, warps, cluster, s, st);
     if (a.dtype == KVATTN_BF16)
-        return a.d == 128 ? run_direct<kBf16Cache, 128, 8>(a, warps, cluster, s)
-                          : run_direct<kBf16Cache, 64, 8>(a, warps, cluster, s);
+        return a.d == 128 ? run_direct<kBf16Cache, 128, 8>(a, max_tiles, warps, cluster, s, st)
+                          : run_direct<kBf16Cache, 64, 8>(a, max_tiles, warps, cluster, s, st);
     switch (a.hq / a.hkv) {
-#define KVATTN_DIRECT_F32(GG)                                                    \
-    case GG:                                                                     \
-        return a.d == 128 ? run_direct<kF32Cache, 128, GG>(a, warps, cluster, s) \
-                          : run_direct<kF32Cache, 64, GG>(a, warps, cluster, s);
+#define KVATTN_DIRECT_F32(GG)                                                                   \
+    case GG:                                                                                    \
+        return a.d == 128 ? run_direct<kF32Cache, 128, GG>(a, max_tiles, warps, cluster, s, st) \
+                          : run_direct<kF32Cache, 64, GG>(a, max_tiles, warps, cluster, s, st);
         KVATTN_DIRECT_F32(1)
         KVATTN_DIRECT_F32(2)
         KVATTN_DIRECT_F32(4)
         KVATTN_DIRECT_F32(8)
 #undef KVATTN_DIRECT_F32
     }
-    return KVATTN_ERR_UNSUPPORTED;
+    return false;
 }
 
 }  // namespace
@@ -728,11 +748,11 @@ bool launch_decode_direct(const DecodeArgs& a, int32_t max_tiles, cudaStream_t s
     // many keys.  Measured (us, this and the stream; thousands of tiles): bf16
     // D = 128 17 27 / 32, 66 88 / 90, 264 343 / 324; fp32 groups of 4 4.2 13.4 /
     // 20.6, 16 49 / 48, 66 171 / 160; bf16 D = 64 264 165 / 307 and fp32 without
-    // groups 264 574 / 608, so these always come here.  fp8 pages stream as fast
-    // from here (17 13.9 / 26.0, 66 47 / 59, 264 172 / 195, 526 330 / 364) and
-    // lose only where a long sequence among short ones keeps its few warps busy
-    // (64 sequences of 1 to 32768 tokens, windows of 8192 and 16384: 162 / 179 and
-    // 304 / 286).
+    // groups 264 574 / 608, so these come here at any length (run_direct refuses the
+    // rest).  fp8 pages stream as fast from here (17 13.9 / 26.0, 66 47 / 59, 264 172
+    // / 195, 526 330 / 364) and lose only where a long sequence among short ones keeps
+    // its few warps busy (64 sequences of 1 to 32768 tokens, windows of 8192 and
+    // 16384: 162 / 179 and 304 / 286).
     int64_t most = INT64_MAX;
     if (kind == kF32Cache) most = G == 1 ? most : 16384;
     else if (kind == kFp8Cache) most = max_tiles <= 512 + 2 ? most : 65536;  // (a window of 8192 and a few sinks)
@@ -752,8 +772,7 @@ bool launch_decode_direct(const DecodeArgs& a, int32_t max_tiles, cudaStream_t s
     int cluster = 1;
     while (max_tiles >= 32 && cluster < 8 && warps == 8 && sms * (cap / 8) >= 2 * cluster * segs && 16 * cluster <= max_tiles) cluster *= 2;
     warps = std::min(warps, max_tiles);
-    *st = direct_dispatch(a, warps, cluster, s);
-    return true;
+    return direct_dispatch(a, max_tiles, warps, cluster, s, st);
 }
 
 }  // namespace kvattn

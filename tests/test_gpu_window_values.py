@@ -366,7 +366,7 @@ def test_calls_without_the_extension_module(kvattn_lib, monkeypatch):
         assert torch.equal(x, y) and x.abs().sum() > 0
 
 
-def _decode_us(kv, dtype, hq, batch, keys, calls=20):
+def _decode_us(kv, dtype, hq, batch, keys, calls=20, splits=0):
     """us of a decode_window call among others: sequences of one length, a cache larger than L2."""
     cfg = kv.make_config(hq, 1, 128, kv.F32 if dtype == "f32" else kv.BF16)
     t = TORCH_DT["f32" if dtype == "f32" else "bf16"]
@@ -376,13 +376,14 @@ def _decode_us(kv, dtype, hq, batch, keys, calls=20):
     lens = torch.full((batch,), keys, dtype=torch.int32, device="cuda")
     q = torch.ones((batch, hq, 128), dtype=t, device="cuda")
     out = torch.empty_like(q)
-    ws = torch.empty(max(256, kv.decode_window_workspace_size(cfg, batch, keys, keys)), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(max(256, kv.decode_window_workspace_size(cfg, batch, keys, keys, 0, splits)), dtype=torch.uint8,
+                     device="cuda")
     times = []
     for _ in range(5):
         a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
         a.record()
         for _ in range(calls):
-            kv.decode_window(cfg, cache, q, table, lens, keys, keys, out=out, workspace=ws)
+            kv.decode_window(cfg, cache, q, table, lens, keys, keys, out=out, workspace=ws, num_splits=splits)
         b.record()
         torch.cuda.synchronize()
         times.append(a.elapsed_time(b) * 1e3 / calls)
@@ -397,3 +398,12 @@ def test_fewer_sequences_take_no_longer(kvattn_lib, dtype, hq, few, more, keys):
     a, b = _decode_us(kvattn_lib, dtype, hq, few, keys), _decode_us(kvattn_lib, dtype, hq, more, keys)
     print(f"{few}: {a:.1f} us, {more}: {b:.1f} us")
     assert a <= 1.04 * b, (a, b)
+
+
+@pytest.mark.parametrize("dtype,hq,batch,keys", [("bf16", 1, 38, 16384), ("bf16", 4, 16, 32768), ("f32", 4, 16, 16384),
+                                                 ("f32", 1, 16, 32768), ("bf16", 4, 8, 32768), ("bf16", 1, 1, 131072)])
+def test_choice_of_the_decode_form(kvattn_lib, dtype, hq, batch, keys):
+    """The library's own choice is no slower than the balanced stream with as many pieces as it would take (16)."""
+    a, b = _decode_us(kvattn_lib, dtype, hq, batch, keys), _decode_us(kvattn_lib, dtype, hq, batch, keys, splits=16)
+    print(f"{a:.1f} us, stream {b:.1f} us")
+    assert a <= 1.06 * b, (a, b)
