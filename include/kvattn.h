@@ -215,10 +215,10 @@ kvattn_status kvattn_rope_append_strided(const kvattn_config* cfg, const kvattn_
  * Errors: INVALID_ARG (null pointer, unknown layout or scaling, rope_base < 1,
  * factor < 1, low < 0, high <= low, original_len <= 0, negative amplitude, a
  * value that is not finite; the arguments of kvattn_rope_append_strided),
- * UNSUPPORTED (rotary_dim, more than 2^20 heads), CUDA; device: BAD_INDEX (that
- * token is skipped).  num_tokens == 0 launches nothing.  The tokens of a call go
- * to slots of their own: of two that name the same (sequence, position) the slot
- * gets some elements of each.
+ * UNSUPPORTED (rotary_dim, more than 2^20 heads; fp8: more than 65535 KV heads),
+ * CUDA; device: BAD_INDEX (that token is skipped).  num_tokens == 0 launches
+ * nothing.  The tokens of a call go to slots of their own: of two that name the
+ * same (sequence, position) the slot gets some elements of each.
  *
  * kvattn_rotary_append_fp8: the same into a kvattn_cache_fp8 (cfg->dtype
  * KVATTN_BF16, head_dim 128): q as above, and each rotated k row (its bf16

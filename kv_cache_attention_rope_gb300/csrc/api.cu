@@ -363,6 +363,7 @@ kvattn_status kvattn_rope_append_strided(const kvattn_config* cfg, const kvattn_
 namespace {
 
 constexpr int32_t kMaxRotaryHeads = 1 << 20;  // the kernel counts a token's bytes in 32 bits
+constexpr int32_t kMaxFp8KvHeads = 65535;     // the kernel of an fp8 cache's V has them in its grid's second dimension
 
 kvattn_status rotary_append_any(const kvattn_config* cfg, const kvattn_rotary* rotary, const kvattn_cache* cache,
                                 bool fp8, void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
@@ -376,7 +377,7 @@ kvattn_status rotary_append_any(const kvattn_config* cfg, const kvattn_rotary* r
     if (fp8 && (cfg->dtype != KVATTN_BF16 || cfg->head_dim != 128)) return KVATTN_ERR_UNSUPPORTED;
     const int rot = rotary->rotary_dim ? rotary->rotary_dim : cfg->head_dim;
     if (rot > cfg->head_dim || rot % 16 != 0) return KVATTN_ERR_UNSUPPORTED;
-    if (cfg->num_q_heads > kMaxRotaryHeads) return KVATTN_ERR_UNSUPPORTED;
+    if (cfg->num_q_heads > kMaxRotaryHeads || (fp8 && cfg->num_kv_heads > kMaxFp8KvHeads)) return KVATTN_ERR_UNSUPPORTED;
     if (!cache_ok(cache, max_blocks_per_seq) || (fp8 && cache->block_size % 16 != 0)) return KVATTN_ERR_INVALID_ARG;
     const int64_t e = cfg->dtype == KVATTN_BF16 ? 2 : 4;
     const int64_t qrow = (int64_t)cfg->num_q_heads * cfg->head_dim;

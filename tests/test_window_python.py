@@ -65,3 +65,22 @@ def test_extension_module_is_built_for_one_python(kv, tmp_path, monkeypatch):
     monkeypatch.setattr(sysconfig, "get_paths", lambda: {"include": str(tmp_path)})
     build._build_marshal(True, [])
     assert not os.listdir(tmp_path)
+
+
+def test_rotary_fp8_refuses_more_kv_heads_than_its_grid_holds(kv):
+    """Before anything is launched: K and q would have been stored, and V not."""
+    import ctypes
+
+    fake = ctypes.c_void_p(0x7F0000001000)
+
+    def call(hkv, fp8):
+        cfg, form = kv.make_config(hkv, hkv, 128, kv.BF16), kv.make_rotary("half")
+        cache = kv.CacheFP8Desc(fake, 8, 16) if fp8 else kv.CacheDesc(fake, fake, 8, 16)
+        row = 128 * hkv
+        fn = kv.lib.kvattn_rotary_append_fp8 if fp8 else kv.lib.kvattn_rotary_append
+        return fn(ctypes.byref(cfg), ctypes.byref(form), ctypes.byref(cache), fake, row, fake, row, fake, row, None, fake, fake,
+                  fake, 1, 1, 0, None)
+
+    ok, uns = kv.STATUS_CODE["KVATTN_OK"], kv.STATUS_CODE["KVATTN_ERR_UNSUPPORTED"]
+    assert call(65535, True) == ok and call(65536, True) == uns
+    assert call(2 ** 20, False) == ok and call(2 ** 20 + 1, False) == uns
