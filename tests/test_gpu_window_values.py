@@ -407,3 +407,50 @@ def test_choice_of_the_decode_form(kvattn_lib, dtype, hq, batch, keys):
     a, b = _decode_us(kvattn_lib, dtype, hq, batch, keys), _decode_us(kvattn_lib, dtype, hq, batch, keys, splits=16)
     print(f"{a:.1f} us, stream {b:.1f} us")
     assert a <= 1.06 * b, (a, b)
+
+
+def test_first_cluster_in_a_capture(kvattn_lib):
+    """A process whose first call of long windows, which takes several thread blocks a segment, is captured: what is asked
+    of the runtime for it is no stream work, and its answer is the one outside a capture."""
+    import os
+    import subprocess
+    import sys
+
+    code = """
+import sys
+sys.path[:0] = [%r]
+import torch, kv_cache_attention_rope_gb300 as kv
+L, block = 16384, 256
+table = torch.arange(L // block, dtype=torch.int32, device='cuda')[None]
+n = torch.tensor([L], dtype=torch.int32, device='cuda')
+ws = torch.empty(1 << 24, dtype=torch.uint8, device='cuda')
+todo = []
+for dtype, d in ((torch.bfloat16, 128), (torch.bfloat16, 64), (torch.float32, 128)):
+    cfg = kv.make_config(4, 1, d, kv.BF16 if dtype is torch.bfloat16 else kv.F32)
+    cache = kv.Cache(*(torch.randn((L // block, 1, block, d), device='cuda').to(dtype) for _ in range(2)))
+    q = torch.randn((1, 4, d), device='cuda').to(dtype)
+    todo.append((kv.decode_window, cfg, cache, q, torch.zeros_like(q)))
+pool = torch.randint(0, 64, (L // block, 1, block // 16, 4224), dtype=torch.uint8, device='cuda')
+pool[..., 4096:] = torch.ones(32).view(torch.uint8).cuda()
+q = torch.randn((1, 4, 128), device='cuda').to(torch.bfloat16)
+todo.append((kv.decode_window_fp8, kv.make_config(4, 1, 128, kv.BF16), kv.CacheFP8(pool, block), q, torch.zeros_like(q)))
+def calls():
+    for f, cfg, cache, q, out in todo:
+        f(cfg, cache, q, table, n, L, L, out=out, workspace=ws)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    calls()
+graph.replay()
+torch.cuda.synchronize()
+got = [t[-1].clone() for t in todo]
+calls()
+torch.cuda.synchronize()
+assert kv.get_device_status() == 0
+for t, x in zip(todo, got):
+    assert torch.equal(t[-1], x) and torch.isfinite(x).all() and x.abs().sum() > 0   # (the same sums in the same order)
+print('captured')
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code % root], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr
