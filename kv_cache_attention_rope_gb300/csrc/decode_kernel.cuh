@@ -765,8 +765,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_sp
                             o[m][3] *= f1;
                         }
                     }
-                    const float p0 = fast_exp2(x[0] - m_run[0]), p1 = fast_exp2(x[1] - m_run[1]);
-                    const float p2 = fast_exp2(x[2] - m_run[0]), p3 = fast_exp2(x[3] - m_run[1]);
+                    // (scores that are all -inf so far have no weight)
+                    const float m0 = m_run[0] == -INFINITY ? 0.f : m_run[0], m1 = m_run[1] == -INFINITY ? 0.f : m_run[1];
+                    const float p0 = fast_exp2(x[0] - m0), p1 = fast_exp2(x[1] - m1);
+                    const float p2 = fast_exp2(x[2] - m0), p3 = fast_exp2(x[3] - m1);
                     lrun[0] += p0 + p2;
                     lrun[1] += p1 + p3;
                     const float c0 = sv0 * vinv, c1 = sv1 * vinv;
@@ -912,8 +914,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_sp
                         o[nd][1] *= alpha;
                     }
                 }
-                const float p0 = fast_exp2(x[0] - m_run), p1 = fast_exp2(x[1] - m_run);
-                const float p2 = fast_exp2(x[2] - m_run), p3 = fast_exp2(x[3] - m_run);
+                // (scores that are all -inf so far have no weight)
+                const float m0 = m_run == -INFINITY ? 0.f : m_run;
+                const float p0 = fast_exp2(x[0] - m0), p1 = fast_exp2(x[1] - m0);
+                const float p2 = fast_exp2(x[2] - m0), p3 = fast_exp2(x[3] - m0);
                 lrun += (p0 + p1) + (p2 + p3);
                 const uint32_t pa0 = pack_bf16_rn(p0, p1), pa2 = pack_bf16_rn(p2, p3);
 #pragma unroll

@@ -454,3 +454,39 @@ print('captured')
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code % root], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "captured" in r.stdout, r.stderr
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,d", [("bf16", 8, 2, 128), ("bf16", 8, 2, 64), ("bf16", 2, 2, 128), ("f32", 8, 2, 128),
+                                            ("fp8", 8, 2, 128)])
+def test_seen_scores_of_minus_infinity(kvattn_lib, dtype, hq, hkv, d):
+    """Keys whose score is -infinity (the newest one alone in its tile at 17, 33 and 4001 keys, and the first tile) weigh
+    nothing, in every form of the decode and in the prefill."""
+    kv = kvattn_lib
+    lens = [17, 33, 40, 4001, 600]
+    wanted = [np.ones(L, bool) for L in lens]
+    c = WindowCache(kv, dtype, hkv, d, lens, wanted, seed=2)
+    q = _q(3, (len(lens), hq, d), dtype).abs()
+    low = [(0, 16), (1, 32), (2, 5), (3, 4000), *((4, t) for t in range(16))]
+    for r, token in low:
+        b, s = _at(c, r, token)
+        if dtype == "fp8":  # codes of -1 with an infinite scale
+            page = c.cache.pool[b, :, s // 16]
+            page[:, 128 * (s % 16):128 * (s % 16) + 128] = 0xB8
+            page[:, 4096 + 4 * (s % 16):4100 + 4 * (s % 16)] = torch.tensor([float("inf")]).view(torch.uint8).cuda()
+        else:
+            c.cache.k_pool[b, :, s, 0] = -float("inf")
+        c.k[r][token, :, 0] = -np.inf
+    cfg = kv.make_config(hq, hkv, d, kv.F32 if dtype == "f32" else kv.BF16)
+    n = torch.tensor(lens, dtype=torch.int32).cuda()
+    dec, win = (kv.decode_fp8, kv.decode_window_fp8) if dtype == "fp8" else (kv.decode, kv.decode_window)
+    qd = q.cuda()
+    got = {f"splits {s}": dec(cfg, c.cache, qd, c.d_table, n, max(lens), num_splits=s) for s in (0, 1, 3)}
+    got |= {f"window, splits {s}": win(cfg, c.cache, qd, c.d_table, n, max(lens), 5000, num_splits=s) for s in (0, 1, 3)}
+    if dtype != "f32":
+        pre = kv.prefill_window_fp8 if dtype == "fp8" else kv.prefill_window
+        got["prefill"] = pre(cfg, c.cache, qd, torch.arange(len(lens) + 1, dtype=torch.int32).cuda(), n - 1, c.d_table, 1, 5000)
+    assert kv.get_device_status() == 0
+    for r, L in enumerate(lens):
+        want, mag = attend(q[r:r + 1].double().numpy(), c.k[r], c.v[r], wanted[r][None])
+        for what, out in got.items():
+            check_attention(f64(out)[r:r + 1], want, mag, dtype, f"{what}, length {L}")
