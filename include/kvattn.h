@@ -205,7 +205,11 @@ kvattn_status kvattn_rope_append_strided(const kvattn_config* cfg, const kvattn_
  *                           (high - low) held to [0, 1], t = original_len
  *                           b^(-2i/R) / (2 pi): pairs of more than `high` turns
  *                           over the original context keep their speed, pairs
- *                           of fewer than `low` turns slow by s
+ *                           of fewer than `low` turns slow by s.  (Linear in
+ *                           turns.  Some implementations with low 1 and high 32
+ *                           are linear in i between two rounded dims instead:
+ *                           halfway their g is 0.5, this one's 0.15.  A model
+ *                           trained with those speeds is not served by this.)
  * rounded to 2^-64 turns.  The products and sums of a rotation are fp32 and a
  * stored element is rounded once: within half an ulp of its type plus
  * 2^-21 a (|x0| + |x1|) of exact at any position.

@@ -507,7 +507,9 @@ def _int32(value, name: str) -> int:
 def make_rotary(layout: str = "adjacent", rotary_dim: int = 0, scaling: str = "none", factor: float = 1.0,
                 original_len: float = 0.0, low: float = 1.0, high: float = 32.0, amplitude: float = 1.0) -> Rotary:
     """The rotary form of kvattn_rotary_append: pairs "adjacent" or "half", rotary_dim rotated dims (0: the whole
-    head), speeds "none", "linear", "base" or "parts" scaled by factor, amplitude on the rotated dims."""
+    head), speeds "none", "linear", "base" or "parts" scaled by factor, amplitude on the rotated dims.  "parts" goes
+    from scaled to unscaled speeds linearly in a pair's turns over original_len, from `low` to `high` of them; a model
+    whose ramp is linear in the pair's index has other speeds."""
     return Rotary(ROPE_LAYOUT[layout], _int32(rotary_dim, "rotary_dim"), ROPE_SCALING[scaling], factor, original_len, low, high, amplitude)
 
 
