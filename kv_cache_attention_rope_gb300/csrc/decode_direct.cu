@@ -352,6 +352,8 @@ __global__ void __launch_bounds__(warps_per_sm(kKind, kD, kG) * 32, 1)
                                     now >> (g4 + 8) & 1u ? s[3] * sl2 : -INFINITY};
                 float p[4];
                 st.step(x, o, p);
+                // P in bf16, the type of V that the MMA takes it with: off by at most
+                // 2^-8 relative, at random; the sum adds the fp32 p
                 t.add(vnow, o, movmatrix_trans(pack_bf16_rn(p[0], p[1])), movmatrix_trans(pack_bf16_rn(p[2], p[3])));
             };
             for (int j = 0; j < mine; j += 2) {
@@ -634,9 +636,10 @@ __global__ void __launch_bounds__(warps_per_sm(kKind, kD, kG) * 32, 1)
 }
 
 // How many clusters of a size are resident at once, per device (a pure function of
-// the kernel, its block and its shared memory; asking the runtime takes longer than a
-// launch).  Clusters do not cross the GPU's groups of SMs, so these are fewer than the
-// SMs' CTAs over the size: of 8 CTAs at one per SM 15, where 152 / 8 is 19.
+// the kernel, its block, which is of 8 warps wherever clusters are, and its shared
+// memory; asking the runtime takes longer than a launch).  Clusters do not cross the
+// GPU's groups of SMs, so these are fewer than the SMs' CTAs over the size: of 8 CTAs
+// at one per SM 15, where 152 / 8 is 19.
 class ClusterResidency {
 public:
     template <typename Kernel>

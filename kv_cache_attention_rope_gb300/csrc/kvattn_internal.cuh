@@ -274,8 +274,8 @@ kvattn_status launch_prefill_fp8(const PrefillArgs& pa, const void* pool, const 
                                  void* workspace, cudaStream_t s);
 
 // Workspace of the windowed fp8 prefill: each chunk's seen blocks (at most
-// `per_chunk`) expanded to 16 bits, their block table, and the power of two that
-// each (chunk, KV head)'s V was divided by.  bytes == 0 for invalid
+// `per_chunk`) expanded to f16, their block table, and the two powers of two that
+// each (chunk, KV head)'s K and V were divided by.  bytes == 0 for invalid
 // arguments.
 struct Fp8WindowLayout {
     int64_t per_chunk;
@@ -284,7 +284,7 @@ struct Fp8WindowLayout {
 Fp8WindowLayout fp8_window_layout(int32_t hkv, int32_t block_size, int32_t max_blocks, int32_t num_chunks,
                                   int32_t max_q_len, int32_t window, int32_t sinks);
 // Expands the pages that the chunks see into the workspace, then runs
-// launch_prefill_window over the bf16 copy (pa's pools and table are replaced).
+// launch_prefill_window over the f16 copy (pa's pools and table are replaced).
 kvattn_status launch_prefill_window_fp8(const PrefillArgs& pa, const void* pool, const Fp8WindowLayout& L,
                                         void* workspace, cudaStream_t s);
 

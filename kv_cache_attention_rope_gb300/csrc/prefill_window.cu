@@ -31,7 +31,8 @@
 //    gap (tile t+1 of an item's last is the next item's first); warp 3: zeros in
 //    V rows that no row sees;
 //  - warps 4-7 and 8-11: the softmax of columns 0-63 and 64-127 of whichever
-//    tile is due; P (bf16) overwrites the first half of S in TMEM;
+//    tile is due; P, in V's type (bf16, or f16 over an fp8 cache's copy),
+//    overwrites the first half of S in TMEM;
 //  - warps 12-15: O / row sums -> bf16 rows of out, while the others are at
 //    the next item (and, over an fp8 cache's copy, q -> f16 as it arrives).
 // TMEM: S_A, S_B, O_A, O_B, 128 columns each.  Every wait on a barrier is
@@ -749,11 +750,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float m_new = none || rescale ? m_tile : m_now;
                 const float alpha = none ? 1.f : fast_exp2(m_now - m_new);
                 m_now = m_new;
-                // P = 2^(s*scale*log2e - m) as bf16 into columns 32hf..32hf+31 of
-                // S_x (both halves have read their S before the barrier); a row
-                // with no seen key yet subtracts +inf so every p is 0.  The row sum
-                // adds the fp32 p (their bf16 roundings differ by at most 2^-8
-                // relative, at random).
+                // P = 2^(s*scale*log2e - m), in the type of V that the MMA takes it
+                // with, into columns 32hf..32hf+31 of S_x (both halves have read
+                // their S before the barrier); a row with no seen key yet subtracts
+                // +inf so every p is 0.  The row sum adds the fp32 p, whose rounding
+                // to bf16 (f16) is off by at most 2^-8 (2^-11) relative, at random.
                 uint32_t pw[32];
                 const float msub = m_now == -INFINITY ? INFINITY : m_now;
                 const uint64_t scale2 = pk(sl2, sl2), msub2 = pk(-msub, -msub);
