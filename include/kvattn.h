@@ -436,7 +436,9 @@ kvattn_status kvattn_decode_static_scratch(const kvattn_config* cfg, const kvatt
  * Only blocks that hold a key the token sees are read: the other entries of a
  * block-table row may be anything (-1 for blocks given back to the allocator
  * when they slid out of the window), and what their slots, or unseen slots of
- * blocks that are read, hold has no effect (NaN and infinities too).
+ * blocks that are read, hold has no effect (NaN and infinities too).  What it
+ * sees counts: a NaN score makes its query head's output NaN, one of -infinity
+ * weighs nothing.
  *   window      >= 1; INT32_MAX sees the whole cache
  *   num_sinks   >= 0
  *   num_splits  0: the library's choice, one launch when the keys are few;
