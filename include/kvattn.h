@@ -258,6 +258,57 @@ kvattn_status kvattn_rotary_append_fp8(const kvattn_config* cfg, const kvattn_ro
                                        int32_t num_seqs, int32_t max_blocks_per_seq, int32_t num_tokens, void* stream);
 
 /*
+ * kvattn_rotary_append_axes -- kvattn_rotary_append with positions on several
+ * axes (images and video: time, height, width) and cache slots of their own.
+ *
+ * [RoPE page], section 4 (pair i turns by m theta_i), with m the position of the
+ * token on the axis that pair i belongs to:
+ *     KVATTN_AXES_SECTIONS  the first sections[0] pairs on axis 0, the next
+ *                           sections[1] on axis 1, ...
+ *     KVATTN_AXES_CYCLIC    pair i on axis a = i % num_axes if i / num_axes <
+ *                           sections[a], else on axis 0
+ * and the speeds f_i, the pairing and the amplitude kvattn_rotary's.  [Engine
+ * page], section 3.2 has the cache index equal to the position; here it is
+ * slots[t], since the tokens of an image have positions alike, and a sequence
+ * whose tokens were moved together (kvattn_compact_tokens) goes on at slots
+ * below its positions.  The attention calls go by slots: causal order is that of
+ * the slots, and seq_lens counts them.
+ *
+ *   positions   device, [num_axes][num_tokens] int32, >= 0
+ *   slots       device, [num_tokens] int32, >= 0: the cache index
+ * num_axes 1 .. 4; sections[a] >= 0 for a < num_axes, together rotary_dim / 2
+ * pairs (and in turn KVATTN_AXES_CYCLIC: axis a > 0 has the sections[a] pairs
+ * a, a + num_axes, ... below rotary_dim / 2).  Every axis alike (text) is
+ * kvattn_rotary_append at that position.  The other arguments, results and errors as
+ * kvattn_rotary_append; INVALID_ARG besides for axes that are none of these;
+ * device: BAD_INDEX also for a negative position (that token is skipped).
+ *
+ * kvattn_rotary_append_axes_fp8: the same into a kvattn_cache_fp8, as
+ * kvattn_rotary_append_fp8.
+ */
+typedef enum { KVATTN_AXES_SECTIONS = 0, KVATTN_AXES_CYCLIC = 1 } kvattn_axes_order;
+
+typedef struct {
+    int32_t num_axes;      /* 1 .. 4 */
+    int32_t order;         /* kvattn_axes_order */
+    int32_t sections[4];   /* pairs of each axis */
+} kvattn_rope_axes;
+
+kvattn_status kvattn_rotary_append_axes(const kvattn_config* cfg, const kvattn_rotary* rotary,
+                                        const kvattn_rope_axes* axes, const kvattn_cache* cache, void* q,
+                                        int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                        int64_t v_stride, void* q_out, const int32_t* positions, const int32_t* slots,
+                                        const int32_t* seq_ids, const int32_t* block_table, int32_t num_seqs,
+                                        int32_t max_blocks_per_seq, int32_t num_tokens, void* stream);
+kvattn_status kvattn_rotary_append_axes_fp8(const kvattn_config* cfg, const kvattn_rotary* rotary,
+                                            const kvattn_rope_axes* axes, const kvattn_cache_fp8* cache, void* q,
+                                            int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                            int64_t v_stride, void* q_out, const int32_t* positions,
+                                            const int32_t* slots, const int32_t* seq_ids, const int32_t* block_table,
+                                            int32_t num_seqs, int32_t max_blocks_per_seq, int32_t num_tokens,
+                                            void* stream);
+
+/*
  * Multi-layer cache: one device allocation holding every layer's K area and V
  * area, so that one block id (one block-table entry, one allocator) names the
  * same block in all of them.
@@ -305,6 +356,53 @@ kvattn_status kvattn_copy_blocks(const kvattn_config* cfg, const kvattn_cache* c
 kvattn_status kvattn_copy_blocks_layered(const kvattn_config* cfg, void* base, int32_t num_layers,
                                          int64_t num_blocks, int32_t block_size, const int32_t* src_ids,
                                          const int32_t* dst_ids, int32_t n, void* stream);
+/* The same in a kvattn_cache_fp8 (head_dim 128): codes and scales. */
+kvattn_status kvattn_copy_blocks_fp8(const kvattn_config* cfg, const kvattn_cache_fp8* cache, const int32_t* src_ids,
+                                     const int32_t* dst_ids, int32_t n, void* stream);
+
+/*
+ * kvattn_compact_tokens -- a sequence's kept tokens move together in its cache:
+ * token starts[s] + j of sequence s (block-table row s) becomes a bit copy of its
+ * token keep[cu_keep[s] + j], j = 0 .. cu_keep[s+1] - cu_keep[s] - 1, in K and V
+ * and every head (kvattn_compact_tokens_layered: and every layer of a multi-layer
+ * cache), in place.
+ *
+ * [Nano-vLLM], section 05 (blocks are allocated and released whole, tokens live in
+ * their slots): drafted tokens that a check rejects, or tokens evicted from a long
+ * context, leave holes in the middle that no release of blocks fills.  Afterwards
+ * the sequence has starts[s] + (kept) tokens, kvattn_table_shrink releases the
+ * blocks behind them, and kvattn_rotary_append_axes appends at slots that are no
+ * longer the positions (moved keys keep the rotation of theirs).
+ *
+ *   starts      device, [num_seqs] int32, first place of the kept tokens
+ *   cu_keep     device, [num_seqs + 1] int32, non-decreasing, cu_keep[0] = 0
+ *   keep        device, [total_keep] int32: per sequence ascending positions from
+ *               starts[s] on
+ * Tokens before starts[s] and behind the last kept one's place stay as they were.
+ * The blocks that places lie in must belong to one sequence of the call only
+ * (copy shared ones first, kvattn_table_prepare_append); the blocks that hold neither a
+ * place nor a kept position are not looked at.
+ * Errors: INVALID_ARG (null pointer, negative count, bad cache), UNSUPPORTED,
+ * CUDA; device: BAD_INDEX (a place or kept position outside the table or pool
+ * stays as it was; a list that does not ascend leaves the sequence's tokens
+ * from starts[s] on unspecified; a list outside `keep` counts as empty).
+ * num_seqs == 0 or total_keep == 0 launches nothing.
+ *
+ * kvattn_compact_tokens_fp8: the same in a kvattn_cache_fp8 (head_dim 128).
+ */
+kvattn_status kvattn_compact_tokens(const kvattn_config* cfg, const kvattn_cache* cache, const int32_t* starts,
+                                    const int32_t* cu_keep, const int32_t* keep, int32_t total_keep,
+                                    const int32_t* block_table, int32_t num_seqs, int32_t max_blocks_per_seq,
+                                    void* stream);
+kvattn_status kvattn_compact_tokens_layered(const kvattn_config* cfg, void* base, int32_t num_layers,
+                                            int64_t num_blocks, int32_t block_size, const int32_t* starts,
+                                            const int32_t* cu_keep, const int32_t* keep, int32_t total_keep,
+                                            const int32_t* block_table, int32_t num_seqs, int32_t max_blocks_per_seq,
+                                            void* stream);
+kvattn_status kvattn_compact_tokens_fp8(const kvattn_config* cfg, const kvattn_cache_fp8* cache, const int32_t* starts,
+                                        const int32_t* cu_keep, const int32_t* keep, int32_t total_keep,
+                                        const int32_t* block_table, int32_t num_seqs, int32_t max_blocks_per_seq,
+                                        void* stream);
 
 /*
  * FP8 KV cache: kvattn_rope_append into a kvattn_cache_fp8, and kvattn_decode
@@ -467,6 +565,52 @@ kvattn_status kvattn_decode_window_fp8(const kvattn_config* cfg, const kvattn_ca
                                        const int32_t* seq_lens, int32_t batch, int32_t max_seq_len, int32_t window,
                                        int32_t num_sinks, int32_t num_splits, void* out, void* workspace,
                                        size_t workspace_bytes, void* stream);
+
+/*
+ * kvattn_decode_shared -- kvattn_decode for a batch in which groups of sequences
+ * begin with the same tokens (samples of one prompt, chats under one system
+ * prompt): what a group has in common is read once for all of its queries.
+ *
+ * [Nano-vLLM], section 05 (sequences with a common prefix share its blocks), and
+ * [Engine page], section 3.4: the softmax over the common keys and the one over a
+ * sequence's own are merged by their running maxima and sums, so the result is
+ * kvattn_decode's,
+ *     out[b][j] = sum_{i < seq_lens[b]} softmax_i(q[b][j] . K_b[i][j/G] * scale) * V_b[i][j/G].
+ *
+ *   cu_groups   device, [num_groups + 1] int32, cu_groups[0] = 0, non-decreasing,
+ *               cu_groups[num_groups] <= batch: group g is the sequences
+ *               cu_groups[g] .. cu_groups[g+1] - 1; the others are in none
+ *   shared_lens device, [num_groups] int32: the first shared_lens[g] tokens have the
+ *               same K and V in every row of group g, as kvattn_table_fork leaves
+ *               them.  They may be read through the row of any sequence of the group
+ *               that has all of them; a shorter one takes no part (and one of length 0
+ *               needs no blocks)
+ *   num_groups  0 .. batch; max_shared_len: host upper bound of shared_lens
+ *   workspace   >= kvattn_decode_shared_workspace_size(...) bytes, any contents,
+ *               256-byte aligned; calls that may overlap on the GPU need one each
+ * Every dtype, head layout and block size of kvattn_decode.  Prefixes are read
+ * once in bf16 caches whose block_size is a multiple of 16; other calls, and those too short to gain, read
+ * each sequence by itself.  What a sequence sees counts as in kvattn_decode_window: a NaN score makes
+ * its query head's output NaN.
+ * The other arguments, results and errors as kvattn_decode.  Groups that are none
+ * of these, or a shared length above max_shared_len, share nothing: the results
+ * are right all the same, and a call that reads prefixes once records BAD_INDEX.
+ *
+ * kvattn_decode_shared_fp8: the same over a kvattn_cache_fp8, as kvattn_decode_window_fp8.
+ */
+size_t kvattn_decode_shared_workspace_size(const kvattn_config* cfg, int32_t batch, int32_t max_seq_len,
+                                           int32_t num_groups, int32_t max_shared_len);
+kvattn_status kvattn_decode_shared(const kvattn_config* cfg, const kvattn_cache* cache, const void* q,
+                                   const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                   int32_t batch, int32_t max_seq_len, const int32_t* cu_groups,
+                                   const int32_t* shared_lens, int32_t num_groups, int32_t max_shared_len, void* out,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+kvattn_status kvattn_decode_shared_fp8(const kvattn_config* cfg, const kvattn_cache_fp8* cache, const void* q,
+                                       const int32_t* block_table, int32_t max_blocks_per_seq,
+                                       const int32_t* seq_lens, int32_t batch, int32_t max_seq_len,
+                                       const int32_t* cu_groups, const int32_t* shared_lens, int32_t num_groups,
+                                       int32_t max_shared_len, void* out, void* workspace, size_t workspace_bytes,
+                                       void* stream);
 
 /*
  * kvattn_prefill_chunk -- causal attention of chunks of new query tokens
@@ -643,6 +787,15 @@ kvattn_status kvattn_table_grow(kvattn_allocator* a, int32_t* table_row, int32_t
 /* Frees the blocks covering a sequence of len tokens and sets those entries to -1. */
 kvattn_status kvattn_table_release(kvattn_allocator* a, int32_t* table_row, int32_t max_blocks,
                                    int32_t block_size, int32_t len);
+
+/*
+ * Shortens a sequence of cur_len tokens to its first new_len: frees the blocks that
+ * cover only later ones and sets those entries to -1 (kvattn_compact_tokens left
+ * the kept tokens at the front).  All or nothing; INVALID_ARG if new_len > cur_len,
+ * the row is too narrow, or such a block is not allocated.
+ */
+kvattn_status kvattn_table_shrink(kvattn_allocator* a, int32_t* table_row, int32_t max_blocks,
+                                  int32_t block_size, int32_t cur_len, int32_t new_len);
 
 /*
  * Prefix sharing ([Nano-vLLM], section 05: reference-counted blocks shared by

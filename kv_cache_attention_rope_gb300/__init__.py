@@ -46,6 +46,10 @@ EXPORTED = [
     "kvattn_rotary_append", "kvattn_rotary_append_fp8",
     "kvattn_decode_window_workspace_size", "kvattn_decode_window", "kvattn_decode_window_fp8",
     "kvattn_prefill_window", "kvattn_prefill_window_fp8_workspace_size", "kvattn_prefill_window_fp8",
+    "kvattn_rotary_append_axes", "kvattn_rotary_append_axes_fp8",
+    "kvattn_decode_shared_workspace_size", "kvattn_decode_shared", "kvattn_decode_shared_fp8",
+    "kvattn_copy_blocks_fp8", "kvattn_compact_tokens", "kvattn_compact_tokens_layered", "kvattn_compact_tokens_fp8",
+    "kvattn_table_shrink",
 ]
 
 
@@ -77,7 +81,12 @@ class Rotary(ctypes.Structure):
                 ("high", ctypes.c_float), ("amplitude", ctypes.c_float)]
 
 
+class RopeAxes(ctypes.Structure):
+    _fields_ = [("num_axes", ctypes.c_int32), ("order", ctypes.c_int32), ("sections", ctypes.c_int32 * 4)]
+
+
 ROPE_LAYOUT = {"adjacent": 0, "half": 1}
+AXES_ORDER = {"sections": 0, "cyclic": 1}
 ROPE_SCALING = {"none": 0, "linear": 1, "base": 2, "parts": 3}
 
 FP8_PAGE_BYTES = 4224  # one (block, KV head, 16 tokens) page at head_dim 128
@@ -127,6 +136,20 @@ def _load():
         "kvattn_prefill_window_fp8_workspace_size": ([cfgp, i32, i32, i32, i32, i32, i32], sz),
         "kvattn_prefill_window_fp8": ([cfgp, ctypes.POINTER(CacheFP8Desc), p, p, p, p, i32, i32, i32, i32, i32, i32,
                                        p, p, sz, p], ctypes.c_int),
+        "kvattn_rotary_append_axes": ([cfgp, ctypes.POINTER(Rotary), ctypes.POINTER(RopeAxes), cachep, p, i64, p, i64, p,
+                                       i64, p, p, p, p, p, i32, i32, i32, p], ctypes.c_int),
+        "kvattn_rotary_append_axes_fp8": ([cfgp, ctypes.POINTER(Rotary), ctypes.POINTER(RopeAxes),
+                                           ctypes.POINTER(CacheFP8Desc), p, i64, p, i64, p, i64, p, p, p, p, p, i32, i32,
+                                           i32, p], ctypes.c_int),
+        "kvattn_decode_shared_workspace_size": ([cfgp, i32, i32, i32, i32], sz),
+        "kvattn_decode_shared": ([cfgp, cachep, p, p, i32, p, i32, i32, p, p, i32, i32, p, p, sz, p], ctypes.c_int),
+        "kvattn_decode_shared_fp8": ([cfgp, ctypes.POINTER(CacheFP8Desc), p, p, i32, p, i32, i32, p, p, i32, i32, p, p,
+                                      sz, p], ctypes.c_int),
+        "kvattn_copy_blocks_fp8": ([cfgp, ctypes.POINTER(CacheFP8Desc), p, p, i32, p], ctypes.c_int),
+        "kvattn_compact_tokens": ([cfgp, cachep, p, p, p, i32, p, i32, i32, p], ctypes.c_int),
+        "kvattn_compact_tokens_layered": ([cfgp, p, i32, i64, i32, p, p, p, i32, p, i32, i32, p], ctypes.c_int),
+        "kvattn_compact_tokens_fp8": ([cfgp, ctypes.POINTER(CacheFP8Desc), p, p, p, i32, p, i32, i32, p], ctypes.c_int),
+        "kvattn_table_shrink": ([p, p, i32, i32, i32, i32], ctypes.c_int),
         "kvattn_get_device_status": ([p, ctypes.POINTER(i32)], ctypes.c_int),
         "kvattn_selftest_wait_timeout": ([i32, p], ctypes.c_int),
         "kvattn_allocator_create": ([i64, ctypes.POINTER(p)], ctypes.c_int),
@@ -155,6 +178,7 @@ lib = _load()
 class _General:
     """In the place of the extension module where there is none: every call is marshalled the general way."""
     setup = decode_window = prefill_window = rotary_append = staticmethod(lambda *args: None)
+    decode_shared = rotary_append_axes = compact_tokens = copy_blocks_fp8 = setup
 
 
 try:
@@ -331,11 +355,16 @@ class LayeredCache:
 
 
 def copy_blocks(cfg: Config, cache, src_ids, dst_ids, stream=None) -> None:
-    """kvattn_copy_blocks (a Cache) or kvattn_copy_blocks_layered (a LayeredCache):
+    """kvattn_copy_blocks (a Cache), kvattn_copy_blocks_layered (a LayeredCache) or kvattn_copy_blocks_fp8 (a CacheFP8):
     block dst_ids[i] := block src_ids[i] in every K and V region.  The ids are
     int32 device tensors, or sequences that are uploaded first."""
     torch = _torch()
-    dev = cache.pool.device if isinstance(cache, LayeredCache) else cache.k_pool.device
+    fp8 = isinstance(cache, CacheFP8)
+    if fp8 and stream is None:
+        st = _marshal.copy_blocks_fp8(cfg, cache, src_ids, dst_ids)
+        if st is not None:
+            return check(st, "kvattn_copy_blocks_fp8")
+    dev = cache.pool.device if fp8 or isinstance(cache, LayeredCache) else cache.k_pool.device
     src = src_ids if isinstance(src_ids, torch.Tensor) else torch.tensor(list(src_ids), dtype=torch.int32, device=dev)
     dst = dst_ids if isinstance(dst_ids, torch.Tensor) else torch.tensor(list(dst_ids), dtype=torch.int32, device=dev)
     if src.numel() != dst.numel():
@@ -344,7 +373,12 @@ def copy_blocks(cfg: Config, cache, src_ids, dst_ids, stream=None) -> None:
     if n == 0:
         return
     sp, dp = _dev(src, "src_ids", torch.int32), _dev(dst, "dst_ids", torch.int32)
-    if isinstance(cache, LayeredCache):
+    if fp8:
+        device, s = _here(stream)
+        desc, _ = _check_cache(cfg, cache, CacheFP8, device)
+        check(lib.kvattn_copy_blocks_fp8(ctypes.byref(cfg), desc, _ptr(src, "src_ids", torch.int32, device),
+                                         _ptr(dst, "dst_ids", torch.int32, device), n, s), "kvattn_copy_blocks_fp8")
+    elif isinstance(cache, LayeredCache):
         check(lib.kvattn_copy_blocks_layered(ctypes.byref(cfg), ctypes.c_void_p(cache.pool.data_ptr()),
                                              cache.num_layers, cache.num_blocks, cache.block_size, sp, dp, n,
                                              _stream(stream)), "kvattn_copy_blocks_layered")
@@ -772,6 +806,155 @@ def prefill_window_fp8(cfg: Config, cache: CacheFP8, q, cu_q_lens, prefix_lens, 
     return out
 
 
+# ------------------------------------------------------------------ shared prefixes, compaction, several axes
+
+def decode_shared_workspace_size(cfg: Config, batch: int, max_seq_len: int, num_groups: int, max_shared_len: int) -> int:
+    """kvattn_decode_shared_workspace_size (0 for invalid arguments)."""
+    return int(lib.kvattn_decode_shared_workspace_size(
+        ctypes.byref(cfg), _int32(batch, "batch"), _int32(max_seq_len, "max_seq_len"), _int32(num_groups, "num_groups"),
+        _int32(max_shared_len, "max_shared_len")))
+
+
+def _decode_shared(fn, what, kind, cfg, cache, q, block_table, seq_lens, max_seq_len, cu_groups, shared_lens,
+                   max_shared_len, out, workspace, stream):
+    device, s = _here(stream)
+    int32 = _torch().int32
+    desc, dt = _check_cache(cfg, cache, kind, device)
+    B, n = q.shape[0], shared_lens.shape[0]
+    _shape(q, "q", B, cfg.num_q_heads, cfg.head_dim)
+    _shape(seq_lens, "seq_lens", B)
+    _shape(shared_lens, "shared_lens", n)
+    _shape(cu_groups, "cu_groups", n + 1)
+    table, width = _table(block_table, B, device)
+    out, op = _out(out, q, dt, device, stream)
+    wp, nbytes = _scratch(workspace, lambda: decode_shared_workspace_size(cfg, B, max_seq_len, n, max_shared_len), q,
+                          device, stream)
+    check(fn(ctypes.byref(cfg), desc, _ptr(q, "q", dt, device), table, width, _ptr(seq_lens, "seq_lens", int32, device),
+             B, _int32(max_seq_len, "max_seq_len"), _ptr(cu_groups, "cu_groups", int32, device),
+             _ptr(shared_lens, "shared_lens", int32, device), n, _int32(max_shared_len, "max_shared_len"), op, wp, nbytes,
+             s), what)
+    return out
+
+
+def decode_shared(cfg: Config, cache: Cache, q, block_table, seq_lens, max_seq_len: int, cu_groups, shared_lens,
+                  max_shared_len: int, out=None, workspace=None, stream=None):
+    """kvattn_decode_shared: one query token per sequence against its whole cache, the first shared_lens[g] tokens that
+    the sequences cu_groups[g] .. cu_groups[g + 1] - 1 have in common (as BlockAllocator.fork leaves them) read once."""
+    if stream is None and out is not None and workspace is not None:
+        st = _marshal.decode_shared(False, cfg, cache, q, block_table, seq_lens, max_seq_len, cu_groups, shared_lens,
+                                    max_shared_len, out, workspace)
+        if st is not None:
+            check(st, "kvattn_decode_shared")
+            return out
+    return _decode_shared(lib.kvattn_decode_shared, "kvattn_decode_shared", Cache, cfg, cache, q, block_table, seq_lens,
+                          max_seq_len, cu_groups, shared_lens, max_shared_len, out, workspace, stream)
+
+
+def decode_shared_fp8(cfg: Config, cache: CacheFP8, q, block_table, seq_lens, max_seq_len: int, cu_groups, shared_lens,
+                      max_shared_len: int, out=None, workspace=None, stream=None):
+    """kvattn_decode_shared_fp8: decode_shared over an fp8 cache (bf16 q and output)."""
+    if stream is None and out is not None and workspace is not None:
+        st = _marshal.decode_shared(True, cfg, cache, q, block_table, seq_lens, max_seq_len, cu_groups, shared_lens,
+                                    max_shared_len, out, workspace)
+        if st is not None:
+            check(st, "kvattn_decode_shared_fp8")
+            return out
+    return _decode_shared(lib.kvattn_decode_shared_fp8, "kvattn_decode_shared_fp8", CacheFP8, cfg, cache, q, block_table,
+                          seq_lens, max_seq_len, cu_groups, shared_lens, max_shared_len, out, workspace, stream)
+
+
+def compact_tokens(cfg: Config, cache, block_table, starts, cu_keep, keep, stream=None) -> None:
+    """kvattn_compact_tokens (a Cache), _layered (a LayeredCache) or _fp8 (a CacheFP8): token starts[s] + j of sequence s
+    becomes its token keep[cu_keep[s] + j] (ascending positions), in place.  BlockAllocator.shrink then frees the blocks
+    behind."""
+    if stream is None:
+        st = _marshal.compact_tokens({Cache: 0, CacheFP8: 1, LayeredCache: 2}.get(type(cache), -1), cfg, cache,
+                                     block_table, starts, cu_keep, keep)
+        if st is not None:
+            return check(st, "kvattn_compact_tokens")
+    device, s = _here(stream)
+    int32 = _torch().int32
+    n = starts.shape[0]
+    _shape(starts, "starts", n)
+    _shape(cu_keep, "cu_keep", n + 1)
+    _shape(keep, "keep", keep.shape[0])
+    table, width = _table(block_table, n, device)
+    lists = (_ptr(starts, "starts", int32, device), _ptr(cu_keep, "cu_keep", int32, device),
+             _ptr(keep, "keep", int32, device), keep.shape[0], table, n, width, s)
+    if isinstance(cache, LayeredCache):
+        pool = cache.pool
+        if cache.cfg.num_kv_heads != cfg.num_kv_heads or cache.cfg.head_dim != cfg.head_dim:
+            raise ValueError("cache heads / head_dim do not match the config")
+        pp = _ptr(pool, "pool", _torch().bfloat16 if cfg.dtype == BF16 else _torch().float32, device)
+        check(lib.kvattn_compact_tokens_layered(ctypes.byref(cfg), pp, cache.num_layers, cache.num_blocks,
+                                                cache.block_size, *lists), "kvattn_compact_tokens_layered")
+    elif isinstance(cache, CacheFP8):
+        desc, _ = _check_cache(cfg, cache, CacheFP8, device)
+        check(lib.kvattn_compact_tokens_fp8(ctypes.byref(cfg), desc, *lists), "kvattn_compact_tokens_fp8")
+    else:
+        desc, _ = _check_cache(cfg, cache, Cache, device)
+        check(lib.kvattn_compact_tokens(ctypes.byref(cfg), desc, *lists), "kvattn_compact_tokens")
+
+
+def make_axes(sections, order: str = "sections") -> RopeAxes:
+    """Pairs of each axis of positions (1 to 4 axes): "sections" one axis after the other, "cyclic" in turn, as
+    kvattn_rotary_append_axes says."""
+    sections = [_int32(s, "sections") for s in sections]
+    if not 1 <= len(sections) <= 4:
+        raise ValueError("1 to 4 axes")
+    return RopeAxes(len(sections), AXES_ORDER[order], (ctypes.c_int32 * 4)(*sections))
+
+
+def _rotary_append_axes(fn, what, kind, cfg, rotary, axes, cache, q, k, v, positions, slots, seq_ids, block_table, stream,
+                        q_out):
+    device, s = _here(stream)
+    desc, dt = _check_cache(cfg, cache, kind, device)
+    int32 = _torch().int32
+    hq, hkv, d = cfg.num_q_heads, cfg.num_kv_heads, cfg.head_dim
+    T = q.shape[0]
+    qp, qs = _token_rows(q, "q", hq, d, dt, device)
+    kp, ks = _token_rows(k, "k", hkv, d, dt, device)
+    vp, vs = _token_rows(v, "v", hkv, d, dt, device)
+    if k.shape[0] != T or v.shape[0] != T:
+        raise ValueError("q, k and v differ in tokens")
+    _shape(positions, "positions", axes.num_axes, T)
+    _shape(slots, "slots", T)
+    _shape(seq_ids, "seq_ids", T)
+    qo = None
+    if q_out is not None:
+        _shape(q_out, "q_out", T, hq, d)
+        qo = _ptr(q_out, "q_out", dt, device)
+    table, width = _table(block_table, 0, device)
+    check(fn(ctypes.byref(cfg), ctypes.byref(rotary), ctypes.byref(axes), desc, qp, qs, kp, ks, vp, vs, qo,
+             _ptr(positions, "positions", int32, device), _ptr(slots, "slots", int32, device),
+             _ptr(seq_ids, "seq_ids", int32, device), table, block_table.shape[0], width, T, s), what)
+
+
+def rotary_append_axes(cfg: Config, rotary: Rotary, axes: RopeAxes, cache: Cache, q, k, v, positions, slots, seq_ids,
+                       block_table, stream=None, q_out=None) -> None:
+    """kvattn_rotary_append_axes: rotary_append with positions [num_axes, T] on the axes of make_axes, and k and v written
+    at the cache indexes slots [T]."""
+    if stream is None:
+        st = _marshal.rotary_append_axes(False, cfg, rotary, cache, q, k, v, positions, seq_ids, block_table, q_out, axes,
+                                         slots)
+        if st is not None:
+            return check(st, "kvattn_rotary_append_axes")
+    _rotary_append_axes(lib.kvattn_rotary_append_axes, "kvattn_rotary_append_axes", Cache, cfg, rotary, axes, cache, q, k,
+                        v, positions, slots, seq_ids, block_table, stream, q_out)
+
+
+def rotary_append_axes_fp8(cfg: Config, rotary: Rotary, axes: RopeAxes, cache: CacheFP8, q, k, v, positions, slots,
+                           seq_ids, block_table, stream=None, q_out=None) -> None:
+    """kvattn_rotary_append_axes_fp8: rotary_append_axes into an fp8 cache (bf16 q, k, v)."""
+    if stream is None:
+        st = _marshal.rotary_append_axes(True, cfg, rotary, cache, q, k, v, positions, seq_ids, block_table, q_out, axes,
+                                         slots)
+        if st is not None:
+            return check(st, "kvattn_rotary_append_axes_fp8")
+    _rotary_append_axes(lib.kvattn_rotary_append_axes_fp8, "kvattn_rotary_append_axes_fp8", CacheFP8, cfg, rotary, axes,
+                        cache, q, k, v, positions, slots, seq_ids, block_table, stream, q_out)
+
+
 def get_device_status(stream=None) -> int:
     """Waits for the stream and returns (and clears) the device status word."""
     v = ctypes.c_int32(0)
@@ -865,6 +1048,13 @@ class BlockAllocator:
                                               int(block_size), int(cur_len), int(new_len), ctypes.byref(src),
                                               ctypes.byref(dst)), "kvattn_table_prepare_append")
         return None if src.value < 0 else (src.value, dst.value)
+
+    def shrink(self, table_row, block_size: int, cur_len: int, new_len: int) -> None:
+        """Frees the blocks that cover only tokens from new_len on (in place)."""
+        if table_row.dtype.name != "int32" or not table_row.flags.c_contiguous:
+            raise TypeError("table_row must be a contiguous int32 numpy array")
+        check(lib.kvattn_table_shrink(self._h, table_row.ctypes.data_as(ctypes.c_void_p), table_row.size,
+                                      int(block_size), int(cur_len), int(new_len)), "kvattn_table_shrink")
 
     def release(self, table_row, block_size: int, length: int) -> None:
         if table_row.dtype.name != "int32" or not table_row.flags.c_contiguous:

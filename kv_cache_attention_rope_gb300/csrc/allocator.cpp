@@ -180,6 +180,19 @@ kvattn_status kvattn_table_release(kvattn_allocator* a, int32_t* table_row, int3
     return KVATTN_OK;
 }
 
+kvattn_status kvattn_table_shrink(kvattn_allocator* a, int32_t* table_row, int32_t max_blocks,
+                                  int32_t block_size, int32_t cur_len, int32_t new_len)
+{
+    if (!a || !table_row || max_blocks <= 0 || block_size <= 0 || new_len < 0 || new_len > cur_len)
+        return KVATTN_ERR_INVALID_ARG;
+    const int32_t have = blocks_for(cur_len, block_size), need = blocks_for(new_len, block_size);
+    if (have > max_blocks) return KVATTN_ERR_INVALID_ARG;
+    const kvattn_status s = kvattn_free_blocks(a, table_row + need, have - need);
+    if (s != KVATTN_OK) return s;
+    for (int32_t i = need; i < have; ++i) table_row[i] = -1;
+    return KVATTN_OK;
+}
+
 kvattn_status kvattn_table_fork(kvattn_allocator* a, const int32_t* src_row, int32_t* dst_row,
                                 int32_t max_blocks, int32_t block_size, int32_t len)
 {

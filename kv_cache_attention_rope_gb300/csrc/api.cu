@@ -365,8 +365,35 @@ namespace {
 constexpr int32_t kMaxRotaryHeads = 1 << 20;  // the kernel counts a token's bytes in 32 bits
 constexpr int32_t kMaxFp8KvHeads = 65535;     // the kernel of an fp8 cache's V has them in its grid's second dimension
 
-kvattn_status rotary_append_any(const kvattn_config* cfg, const kvattn_rotary* rotary, const kvattn_cache* cache,
-                                bool fp8, void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+// The axis of each of `pairs` pairs; false for axes that kvattn.h does not allow.
+bool axes_of_pairs(const kvattn_rope_axes* x, int pairs, uint8_t* axis)
+{
+    if (x->num_axes < 1 || x->num_axes > kMaxAxes) return false;
+    if (x->order != KVATTN_AXES_SECTIONS && x->order != KVATTN_AXES_CYCLIC) return false;
+    int64_t all = 0;
+    for (int a = 0; a < x->num_axes; ++a) {
+        if (x->sections[a] < 0 || x->sections[a] > pairs) return false;
+        all += x->sections[a];
+    }
+    if (all != pairs) return false;
+    int n = 0;
+    if (x->order == KVATTN_AXES_SECTIONS) {
+        for (int a = 0; a < x->num_axes; ++a)
+            for (int j = 0; j < x->sections[a]; ++j) axis[n++] = (uint8_t)a;
+        return true;
+    }
+    for (int a = 1; a < x->num_axes; ++a)  // its last pair is there
+        if (x->sections[a] > 0 && a + (x->sections[a] - 1) * x->num_axes >= pairs) return false;
+    for (; n < pairs; ++n) {
+        const int a = n % x->num_axes;
+        axis[n] = (uint8_t)(n / x->num_axes < x->sections[a] ? a : 0);
+    }
+    return true;
+}
+
+// axes null: `positions` are the slots too.
+kvattn_status rotary_append_any(const kvattn_config* cfg, const kvattn_rotary* rotary, const kvattn_rope_axes* axes,
+                                const int32_t* slots, const kvattn_cache* cache, bool fp8, void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                                 int64_t v_stride, void* q_out, const int32_t* positions, const int32_t* seq_ids,
                                 const int32_t* block_table, int32_t num_seqs, int32_t max_blocks_per_seq,
                                 int32_t num_tokens, void* stream)
@@ -377,6 +404,8 @@ kvattn_status rotary_append_any(const kvattn_config* cfg, const kvattn_rotary* r
     if (fp8 && (cfg->dtype != KVATTN_BF16 || cfg->head_dim != 128)) return KVATTN_ERR_UNSUPPORTED;
     const int rot = rotary->rotary_dim ? rotary->rotary_dim : cfg->head_dim;
     if (rot > cfg->head_dim || rot % 16 != 0) return KVATTN_ERR_UNSUPPORTED;
+    uint8_t axis[64] = {};
+    if (axes && !axes_of_pairs(axes, rot / 2, axis)) return KVATTN_ERR_INVALID_ARG;
     if (cfg->num_q_heads > kMaxRotaryHeads || (fp8 && cfg->num_kv_heads > kMaxFp8KvHeads)) return KVATTN_ERR_UNSUPPORTED;
     if (!cache_ok(cache, max_blocks_per_seq) || (fp8 && cache->block_size % 16 != 0)) return KVATTN_ERR_INVALID_ARG;
     const int64_t e = cfg->dtype == KVATTN_BF16 ? 2 : 4;
@@ -388,7 +417,7 @@ kvattn_status rotary_append_any(const kvattn_config* cfg, const kvattn_rotary* r
         return KVATTN_ERR_INVALID_ARG;
     if (((q_stride | k_stride | v_stride) * e) & 15) return KVATTN_ERR_INVALID_ARG;
     if (num_tokens == 0) return KVATTN_OK;
-    if (!q || !k || !v || !positions || !seq_ids || !block_table) return KVATTN_ERR_INVALID_ARG;
+    if (!q || !k || !v || !positions || !seq_ids || !block_table || (axes && !slots)) return KVATTN_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
          reinterpret_cast<uintptr_t>(q_out)) & 15u)
         return KVATTN_ERR_INVALID_ARG;
@@ -423,7 +452,13 @@ kvattn_status rotary_append_any(const kvattn_config* cfg, const kvattn_rotary* r
     a.status = device_status_ptr();
     if (!a.status) return KVATTN_ERR_CUDA;
     rotary_turns(cfg, rotary, rot, a.turns);
-    const kvattn_status kst = launch_rotary_append(a, static_cast<cudaStream_t>(stream));
+    if (axes) {
+        a.slots = slots;
+        a.num_axes = axes->num_axes;
+        std::memcpy(a.axis, axis, sizeof(axis));
+    }
+    const kvattn_status kst = axes ? launch_rotary_append_axes(a, static_cast<cudaStream_t>(stream))
+                                   : launch_rotary_append(a, static_cast<cudaStream_t>(stream));
     if (kst != KVATTN_OK || !fp8) return kst;
     RopeArgs r;  // the V pages
     std::memset(&r, 0, sizeof(r));
@@ -431,7 +466,9 @@ kvattn_status rotary_append_any(const kvattn_config* cfg, const kvattn_rotary* r
     r.v_stride = a.v_stride;
     r.k_pool = cache->k_pool;
     r.fp8 = 1;
-    r.positions = positions;
+    r.positions = axes ? slots : positions;
+    r.axes = axes ? positions : nullptr;
+    r.num_axes = axes ? axes->num_axes : 0;
     r.seq_ids = seq_ids;
     r.block_table = block_table;
     r.num_blocks = cache->num_blocks;
@@ -451,7 +488,7 @@ kvattn_status kvattn_rotary_append(const kvattn_config* cfg, const kvattn_rotary
                                    const int32_t* block_table, int32_t num_seqs, int32_t max_blocks_per_seq,
                                    int32_t num_tokens, void* stream)
 {
-    return rotary_append_any(cfg, rotary, cache, false, q, q_stride, k, k_stride, v, v_stride, q_out, positions,
+    return rotary_append_any(cfg, rotary, nullptr, nullptr, cache, false, q, q_stride, k, k_stride, v, v_stride, q_out, positions,
                              seq_ids, block_table, num_seqs, max_blocks_per_seq, num_tokens, stream);
 }
 
@@ -463,8 +500,34 @@ kvattn_status kvattn_rotary_append_fp8(const kvattn_config* cfg, const kvattn_ro
 {
     if (!cache) return KVATTN_ERR_INVALID_ARG;
     const kvattn_cache c{cache->pool, cache->pool, cache->num_blocks, cache->block_size};
-    return rotary_append_any(cfg, rotary, &c, true, q, q_stride, k, k_stride, v, v_stride, q_out, positions, seq_ids,
+    return rotary_append_any(cfg, rotary, nullptr, nullptr, &c, true, q, q_stride, k, k_stride, v, v_stride, q_out, positions, seq_ids,
                              block_table, num_seqs, max_blocks_per_seq, num_tokens, stream);
+}
+
+kvattn_status kvattn_rotary_append_axes(const kvattn_config* cfg, const kvattn_rotary* rotary,
+                                        const kvattn_rope_axes* axes, const kvattn_cache* cache, void* q,
+                                        int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                        int64_t v_stride, void* q_out, const int32_t* positions, const int32_t* slots,
+                                        const int32_t* seq_ids, const int32_t* block_table, int32_t num_seqs,
+                                        int32_t max_blocks_per_seq, int32_t num_tokens, void* stream)
+{
+    if (!axes) return KVATTN_ERR_INVALID_ARG;
+    return rotary_append_any(cfg, rotary, axes, slots, cache, false, q, q_stride, k, k_stride, v, v_stride, q_out,
+                             positions, seq_ids, block_table, num_seqs, max_blocks_per_seq, num_tokens, stream);
+}
+
+kvattn_status kvattn_rotary_append_axes_fp8(const kvattn_config* cfg, const kvattn_rotary* rotary,
+                                            const kvattn_rope_axes* axes, const kvattn_cache_fp8* cache, void* q,
+                                            int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                            int64_t v_stride, void* q_out, const int32_t* positions,
+                                            const int32_t* slots, const int32_t* seq_ids, const int32_t* block_table,
+                                            int32_t num_seqs, int32_t max_blocks_per_seq, int32_t num_tokens,
+                                            void* stream)
+{
+    if (!axes || !cache) return KVATTN_ERR_INVALID_ARG;
+    const kvattn_cache c{cache->pool, cache->pool, cache->num_blocks, cache->block_size};
+    return rotary_append_any(cfg, rotary, axes, slots, &c, true, q, q_stride, k, k_stride, v, v_stride, q_out, positions,
+                             seq_ids, block_table, num_seqs, max_blocks_per_seq, num_tokens, stream);
 }
 
 namespace {
@@ -507,9 +570,15 @@ kvattn_status kvattn_layer_cache(const kvattn_config* cfg, void* base, int32_t n
 
 namespace {
 
-kvattn_status copy_blocks(const kvattn_config* cfg, char* k_base, char* v_base, int64_t layer_stride,
-                          int32_t layers, int64_t num_blocks, int32_t block_size, const int32_t* src_ids,
-                          const int32_t* dst_ids, int32_t n, void* stream)
+// block_bytes: of a region (kvattn_cache: of K or V; kvattn_cache_fp8: its pages)
+int64_t region_block_bytes(const kvattn_config* cfg, bool fp8, int32_t block_size)
+{
+    if (fp8) return (int64_t)cfg->num_kv_heads * (block_size / 16) * kF8Page;
+    return (int64_t)cfg->num_kv_heads * block_size * cfg->head_dim * (cfg->dtype == KVATTN_BF16 ? 2 : 4);
+}
+
+kvattn_status copy_blocks(char* k_base, char* v_base, int64_t layer_stride, int32_t regions, int64_t block_bytes,
+                          int64_t num_blocks, const int32_t* src_ids, const int32_t* dst_ids, int32_t n, void* stream)
 {
     if (n < 0) return KVATTN_ERR_INVALID_ARG;
     if (n == 0) return KVATTN_OK;
@@ -519,8 +588,8 @@ kvattn_status copy_blocks(const kvattn_config* cfg, char* k_base, char* v_base, 
     a.k_base = k_base;
     a.v_base = v_base;
     a.layer_stride = layer_stride;
-    a.layers = layers;
-    a.block_bytes = (int64_t)cfg->num_kv_heads * block_size * cfg->head_dim * (cfg->dtype == KVATTN_BF16 ? 2 : 4);
+    a.regions = regions;
+    a.block_bytes = block_bytes;
     a.num_blocks = num_blocks;
     a.src = src_ids;
     a.dst = dst_ids;
@@ -528,6 +597,46 @@ kvattn_status copy_blocks(const kvattn_config* cfg, char* k_base, char* v_base, 
     a.status = device_status_ptr();
     if (!a.status) return KVATTN_ERR_CUDA;
     return launch_copy_blocks(a, static_cast<cudaStream_t>(stream));
+}
+
+// A kvattn_cache_fp8 and the config that it needs.
+kvattn_status fp8_cache_check(const kvattn_config* cfg, const kvattn_cache* c, int32_t max_blocks_per_seq)
+{
+    if (!config_ok(cfg) || !cache_ok(c, max_blocks_per_seq) || c->block_size % 16 != 0) return KVATTN_ERR_INVALID_ARG;
+    const kvattn_status st = config_supported(cfg);
+    if (st != KVATTN_OK) return st;
+    return cfg->dtype != KVATTN_BF16 || cfg->head_dim != 128 ? KVATTN_ERR_UNSUPPORTED : KVATTN_OK;
+}
+
+kvattn_status compact_tokens(const kvattn_config* cfg, char* k_base, char* v_base, int64_t layer_stride, int32_t layers,
+                             bool fp8, int64_t num_blocks, int32_t block_size, const int32_t* starts,
+                             const int32_t* cu_keep, const int32_t* keep, int32_t total_keep,
+                             const int32_t* block_table, int32_t num_seqs, int32_t max_blocks_per_seq, void* stream)
+{
+    if (num_seqs < 0 || total_keep < 0) return KVATTN_ERR_INVALID_ARG;
+    if (num_seqs == 0 || total_keep == 0) return KVATTN_OK;
+    if (!starts || !cu_keep || !keep || !block_table) return KVATTN_ERR_INVALID_ARG;
+    CompactArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.k_base = k_base;
+    a.v_base = v_base;
+    a.layer_stride = layer_stride;
+    a.layers = layers;
+    a.fp8 = fp8 ? 1 : 0;
+    a.hkv = cfg->num_kv_heads;
+    a.row_bytes = cfg->head_dim * (cfg->dtype == KVATTN_BF16 ? 2 : 4);
+    a.num_blocks = num_blocks;
+    a.block_size = block_size;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_seqs = num_seqs;
+    a.total_keep = total_keep;
+    a.starts = starts;
+    a.cu = cu_keep;
+    a.keep = keep;
+    a.block_table = block_table;
+    a.status = device_status_ptr();
+    if (!a.status) return KVATTN_ERR_CUDA;
+    return launch_compact(a, static_cast<cudaStream_t>(stream));
 }
 
 }  // namespace
@@ -538,8 +647,20 @@ kvattn_status kvattn_copy_blocks(const kvattn_config* cfg, const kvattn_cache* c
     if (!config_ok(cfg) || !cache_ok(cache, 1)) return KVATTN_ERR_INVALID_ARG;
     const kvattn_status st = config_supported(cfg);
     if (st != KVATTN_OK) return st;
-    return copy_blocks(cfg, static_cast<char*>(cache->k_pool), static_cast<char*>(cache->v_pool), 0, 1,
-                       cache->num_blocks, cache->block_size, src_ids, dst_ids, n, stream);
+    return copy_blocks(static_cast<char*>(cache->k_pool), static_cast<char*>(cache->v_pool), 0, 2,
+                       region_block_bytes(cfg, false, cache->block_size), cache->num_blocks, src_ids, dst_ids, n, stream);
+}
+
+kvattn_status kvattn_copy_blocks_fp8(const kvattn_config* cfg, const kvattn_cache_fp8* cache, const int32_t* src_ids,
+                                     const int32_t* dst_ids, int32_t n, void* stream)
+{
+    if (!cache) return KVATTN_ERR_INVALID_ARG;
+    const kvattn_cache c{cache->pool, cache->pool, cache->num_blocks, cache->block_size};
+    const kvattn_status st = fp8_cache_check(cfg, &c, 1);
+    if (st != KVATTN_OK) return st;
+    char* pool = static_cast<char*>(cache->pool);
+    return copy_blocks(pool, pool, 0, 1, region_block_bytes(cfg, true, cache->block_size), cache->num_blocks, src_ids,
+                       dst_ids, n, stream);
 }
 
 kvattn_status kvattn_copy_blocks_layered(const kvattn_config* cfg, void* base, int32_t num_layers,
@@ -551,8 +672,53 @@ kvattn_status kvattn_copy_blocks_layered(const kvattn_config* cfg, void* base, i
     if (st != KVATTN_OK) return st;
     if (num_blocks > INT32_MAX) return KVATTN_ERR_INVALID_ARG;
     const int64_t region = static_cast<char*>(first.v_pool) - static_cast<char*>(first.k_pool);
-    return copy_blocks(cfg, static_cast<char*>(first.k_pool), static_cast<char*>(first.v_pool), 2 * region,
-                       num_layers, num_blocks, block_size, src_ids, dst_ids, n, stream);
+    if (num_layers > INT32_MAX / 2) return KVATTN_ERR_UNSUPPORTED;
+    return copy_blocks(static_cast<char*>(first.k_pool), static_cast<char*>(first.v_pool), 2 * region, 2 * num_layers,
+                       region_block_bytes(cfg, false, block_size), num_blocks, src_ids, dst_ids, n, stream);
+}
+
+kvattn_status kvattn_compact_tokens(const kvattn_config* cfg, const kvattn_cache* cache, const int32_t* starts,
+                                    const int32_t* cu_keep, const int32_t* keep, int32_t total_keep,
+                                    const int32_t* block_table, int32_t num_seqs, int32_t max_blocks_per_seq,
+                                    void* stream)
+{
+    if (!config_ok(cfg) || !cache_ok(cache, max_blocks_per_seq)) return KVATTN_ERR_INVALID_ARG;
+    const kvattn_status st = config_supported(cfg);
+    if (st != KVATTN_OK) return st;
+    return compact_tokens(cfg, static_cast<char*>(cache->k_pool), static_cast<char*>(cache->v_pool), 0, 1, false,
+                          cache->num_blocks, cache->block_size, starts, cu_keep, keep, total_keep, block_table, num_seqs,
+                          max_blocks_per_seq, stream);
+}
+
+kvattn_status kvattn_compact_tokens_layered(const kvattn_config* cfg, void* base, int32_t num_layers,
+                                            int64_t num_blocks, int32_t block_size, const int32_t* starts,
+                                            const int32_t* cu_keep, const int32_t* keep, int32_t total_keep,
+                                            const int32_t* block_table, int32_t num_seqs, int32_t max_blocks_per_seq,
+                                            void* stream)
+{
+    kvattn_cache first;
+    kvattn_status st = kvattn_layer_cache(cfg, base, num_layers, num_blocks, block_size, 0, &first);
+    if (st != KVATTN_OK) return st;
+    if (!cache_ok(&first, max_blocks_per_seq)) return KVATTN_ERR_INVALID_ARG;
+    if (num_layers > INT32_MAX / 2) return KVATTN_ERR_UNSUPPORTED;
+    char* k = static_cast<char*>(first.k_pool);
+    char* v = static_cast<char*>(first.v_pool);
+    return compact_tokens(cfg, k, v, 2 * (v - k), num_layers, false, num_blocks, block_size, starts, cu_keep, keep,
+                          total_keep, block_table, num_seqs, max_blocks_per_seq, stream);
+}
+
+kvattn_status kvattn_compact_tokens_fp8(const kvattn_config* cfg, const kvattn_cache_fp8* cache, const int32_t* starts,
+                                        const int32_t* cu_keep, const int32_t* keep, int32_t total_keep,
+                                        const int32_t* block_table, int32_t num_seqs, int32_t max_blocks_per_seq,
+                                        void* stream)
+{
+    if (!cache) return KVATTN_ERR_INVALID_ARG;
+    const kvattn_cache c{cache->pool, cache->pool, cache->num_blocks, cache->block_size};
+    const kvattn_status st = fp8_cache_check(cfg, &c, max_blocks_per_seq);
+    if (st != KVATTN_OK) return st;
+    char* pool = static_cast<char*>(cache->pool);
+    return compact_tokens(cfg, pool, pool, 0, 1, true, cache->num_blocks, cache->block_size, starts, cu_keep, keep,
+                          total_keep, block_table, num_seqs, max_blocks_per_seq, stream);
 }
 
 int32_t kvattn_decode_num_splits(const kvattn_config* cfg, int32_t batch, int32_t max_seq_len, int32_t num_splits)
@@ -705,6 +871,58 @@ kvattn_status kvattn_decode_window_fp8(const kvattn_config* cfg, const kvattn_ca
     const kvattn_cache c{cache->pool, cache->pool, cache->num_blocks, cache->block_size};
     return decode_any(cfg, &c, true, {window, num_sinks}, q, block_table, max_blocks_per_seq, seq_lens, batch,
                       max_seq_len, num_splits, out, workspace, workspace_bytes, stream);
+}
+
+namespace {
+
+bool groups_ok(int32_t batch, int32_t num_groups, int32_t max_shared_len)
+{
+    return num_groups >= 0 && num_groups <= batch && max_shared_len >= 0;
+}
+
+// Every sequence by itself.
+kvattn_status decode_shared_any(const kvattn_config* cfg, const kvattn_cache* cache, bool fp8, const void* q,
+                                const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                int32_t batch, int32_t max_seq_len, const int32_t* cu_groups,
+                                const int32_t* shared_lens, int32_t num_groups, int32_t max_shared_len, void* out,
+                                void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (batch >= 0 && !groups_ok(batch, num_groups, max_shared_len)) return KVATTN_ERR_INVALID_ARG;
+    if (num_groups > 0 && (!cu_groups || !shared_lens)) return KVATTN_ERR_INVALID_ARG;
+    return decode_any(cfg, cache, fp8, {INT32_MAX, 0}, q, block_table, max_blocks_per_seq, seq_lens, batch, max_seq_len, 0,
+                      out, workspace, workspace_bytes, stream);
+}
+
+}  // namespace
+
+size_t kvattn_decode_shared_workspace_size(const kvattn_config* cfg, int32_t batch, int32_t max_seq_len,
+                                           int32_t num_groups, int32_t max_shared_len)
+{
+    if (batch < 0 || max_seq_len < 0 || !groups_ok(batch, num_groups, max_shared_len)) return 0;
+    return kvattn_decode_window_workspace_size(cfg, batch, max_seq_len, INT32_MAX, 0, 0);
+}
+
+kvattn_status kvattn_decode_shared(const kvattn_config* cfg, const kvattn_cache* cache, const void* q,
+                                   const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                   int32_t batch, int32_t max_seq_len, const int32_t* cu_groups,
+                                   const int32_t* shared_lens, int32_t num_groups, int32_t max_shared_len, void* out,
+                                   void* workspace, size_t workspace_bytes, void* stream)
+{
+    return decode_shared_any(cfg, cache, false, q, block_table, max_blocks_per_seq, seq_lens, batch, max_seq_len, cu_groups,
+                             shared_lens, num_groups, max_shared_len, out, workspace, workspace_bytes, stream);
+}
+
+kvattn_status kvattn_decode_shared_fp8(const kvattn_config* cfg, const kvattn_cache_fp8* cache, const void* q,
+                                       const int32_t* block_table, int32_t max_blocks_per_seq,
+                                       const int32_t* seq_lens, int32_t batch, int32_t max_seq_len,
+                                       const int32_t* cu_groups, const int32_t* shared_lens, int32_t num_groups,
+                                       int32_t max_shared_len, void* out, void* workspace, size_t workspace_bytes,
+                                       void* stream)
+{
+    if (!cache) return KVATTN_ERR_INVALID_ARG;
+    const kvattn_cache c{cache->pool, cache->pool, cache->num_blocks, cache->block_size};
+    return decode_shared_any(cfg, &c, true, q, block_table, max_blocks_per_seq, seq_lens, batch, max_seq_len, cu_groups,
+                             shared_lens, num_groups, max_shared_len, out, workspace, workspace_bytes, stream);
 }
 
 kvattn_status kvattn_rope_append_fp8(const kvattn_config* cfg, const kvattn_cache_fp8* cache, void* q,

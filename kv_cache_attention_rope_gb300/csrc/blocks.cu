@@ -1,16 +1,18 @@
-// Copy-on-write of shared cache blocks.
+// Copies of whole cache blocks (copy on write of shared ones).
 //
 // "Nano-vLLM Part 2" page, section 05: the block manager keeps reference
 // counts so that sequences with a common prefix share its blocks, and one
 // block id names the same block in every layer's K and V area.  When a
 // sequence appends into a partially filled block that another sequence still
 // references, the block is first duplicated under a fresh id; this kernel
-// makes those duplicates, for every K and V region at once.
+// makes those duplicates, for every K and V region (an fp8 cache: its one
+// region of pages) at once.
 //
-// Plain 16-byte vector copies, grid-stride over (pair, region, vector): each
-// block-region is a contiguous Hkv x block_size x D run, so every warp reads
-// and writes 512 contiguous bytes.  A pair with an id outside the pool is
-// skipped and recorded as KVATTN_ERR_BAD_INDEX.
+// Bound by HBM: each block-region is one contiguous run (of Hkv x block_size x D
+// elements, or Hkv x block_size / 16 pages), read once and written once.  A
+// thread block copies chunks of a run, a chunk's vectors all under way before the first is
+// stored; ids are looked up once per chunk.  A pair with an id outside the pool
+// is skipped and recorded as KVATTN_ERR_BAD_INDEX.
 #include <algorithm>
 
 #include "kvattn_internal.cuh"
@@ -19,26 +21,37 @@ namespace kvattn {
 namespace {
 
 constexpr int kCopyThreads = 256;
+constexpr int kVecs = 4;  // 16-byte vectors of a thread in a chunk
 
-__global__ void __launch_bounds__(kCopyThreads) copy_blocks_kernel(const __grid_constant__ CopyArgs a)
+// Unit u: chunk u % chunks of region (u / chunks) % regions of pair u / (chunks regions).
+__global__ void __launch_bounds__(kCopyThreads) copy_blocks_kernel(const __grid_constant__ CopyArgs a, const int chunks,
+                                                                   const int chunk_vecs, const int64_t units)
 {
     pdl_wait();
-    const int64_t vpb = a.block_bytes / 16;             // vectors per block-region
-    const int64_t regions = 2 * (int64_t)a.layers;
-    const int64_t total = (int64_t)a.n * regions * vpb;
-    for (int64_t v = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x; v < total;
-         v += (int64_t)gridDim.x * kCopyThreads) {
-        const int64_t pair = v / (regions * vpb);
-        const int64_t rem = v - pair * regions * vpb;
-        const int64_t r = rem / vpb, off = rem - r * vpb;
+    const int vecs = (int)(a.block_bytes / 16);
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int64_t pr = u / chunks;
+        const int c = (int)(u - pr * chunks), pair = (int)(pr / a.regions), r = (int)(pr - (int64_t)pair * a.regions);
         const int32_t s = a.src[pair], d = a.dst[pair];
         if (s < 0 || s >= a.num_blocks || d < 0 || d >= a.num_blocks) {
-            if (r == 0 && off == 0) record_error(a.status, KVATTN_ERR_BAD_INDEX);
+            if (threadIdx.x == 0) record_error(a.status, KVATTN_ERR_BAD_INDEX);
             continue;
         }
         char* base = ((r & 1) ? a.v_base : a.k_base) + (r >> 1) * a.layer_stride;
-        const uint4 x = *reinterpret_cast<const uint4*>(base + (int64_t)s * a.block_bytes + off * 16);
-        *reinterpret_cast<uint4*>(base + (int64_t)d * a.block_bytes + off * 16) = x;
+        const uint4* from = reinterpret_cast<const uint4*>(base + (int64_t)s * a.block_bytes);
+        uint4* to = reinterpret_cast<uint4*>(base + (int64_t)d * a.block_bytes);
+        const int end = min(vecs, (c + 1) * chunk_vecs);
+        uint4 v[kVecs];
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int x = c * chunk_vecs + i * kCopyThreads + (int)threadIdx.x;
+            if (x < end) v[i] = from[x];
+        }
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int x = c * chunk_vecs + i * kCopyThreads + (int)threadIdx.x;
+            if (x < end) to[x] = v[i];
+        }
     }
 }
 
@@ -46,12 +59,12 @@ __global__ void __launch_bounds__(kCopyThreads) copy_blocks_kernel(const __grid_
 
 kvattn_status launch_copy_blocks(const CopyArgs& a, cudaStream_t s)
 {
-    const int64_t total = (int64_t)a.n * 2 * a.layers * (a.block_bytes / 16);
-    const int64_t want = (total + kCopyThreads - 1) / kCopyThreads;
-    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(want, (int64_t)num_sms() * 8));
-    const cudaError_t e0 = launch_pdl(copy_blocks_kernel, dim3(grid), dim3(kCopyThreads), 0, s, a);
-    if (e0 != cudaSuccess) return cuda_status(e0);
-    return cuda_status(cudaGetLastError());
+    if (a.block_bytes / 16 > INT32_MAX / 2) return KVATTN_ERR_UNSUPPORTED;
+    const int vecs = (int)(a.block_bytes / 16), most = kCopyThreads * kVecs;
+    const int chunks = (vecs + most - 1) / most, chunk_vecs = (vecs + chunks - 1) / chunks;
+    const int64_t units = (int64_t)a.n * a.regions * chunks;
+    const int grid = (int)std::min<int64_t>(units, (int64_t)num_sms() * 8);
+    return cuda_status(launch_pdl(copy_blocks_kernel, dim3(grid), dim3(kCopyThreads), 0, s, a, chunks, chunk_vecs, units));
 }
 
 }  // namespace kvattn

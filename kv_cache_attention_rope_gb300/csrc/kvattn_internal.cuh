@@ -105,6 +105,10 @@ struct RopeArgs {
     uint64_t turns[64];
     // cos/sin of k*pi/16, k = 0..4, as float-float pairs (c_hi, c_lo, s_hi, s_lo)
     float4 sector[5];
+    // launch_append_v_fp8 only: null, or [num_axes][num_tokens] positions (`positions` are slots then), of which a
+    // negative one makes the append reject the token
+    const int32_t* axes;
+    int32_t num_axes;
 };
 kvattn_status launch_rope_append(const RopeArgs& a, cudaStream_t s);
 kvattn_status launch_rope_append_fp8(const RopeArgs& a, cudaStream_t s);  // a.fp8 set
@@ -137,8 +141,14 @@ struct RotaryArgs {
     float amplitude;
     int* status;
     uint64_t turns[64];  // speed of each pair, 2^-64 turns per position
+    // launch_rotary_append_axes only: positions is [num_axes][num_tokens]
+    const int32_t* slots;
+    int32_t num_axes;
+    uint8_t axis[64];  // of each pair
 };
+constexpr int kMaxAxes = 4;
 kvattn_status launch_rotary_append(const RotaryArgs& a, cudaStream_t s);
+kvattn_status launch_rotary_append_axes(const RotaryArgs& a, cudaStream_t s);
 
 // fp8 cache page: the 16 tokens of one (block, KV head, 16-token group) at
 // D = 128, laid out for the decode kernel (one bulk copy per page, every
@@ -152,20 +162,40 @@ __host__ __device__ constexpr int f8_swz(int r) { return (r & 1) | ((r >> 1) & 6
 
 // Whole-block copies over every K/V region of a (multi-layer) cache: region
 // r = 2 * layer + (0: K, 1: V) starts at (r odd ? v_base : k_base) +
-// layer * layer_stride.
+// layer * layer_stride (an fp8 cache: one region, at k_base).
 struct CopyArgs {
     char* k_base;
     char* v_base;
     int64_t layer_stride;   // bytes; 0 for one layer
-    int64_t block_bytes;    // Hkv * block_size * D * element size (a multiple of 16)
+    int64_t block_bytes;    // of a region: Hkv * block_size * D * element size, or of pages (a multiple of 16)
     int64_t num_blocks;
     const int32_t* src;
     const int32_t* dst;
     int32_t n;
-    int32_t layers;
+    int32_t regions;
     int* status;
 };
 kvattn_status launch_copy_blocks(const CopyArgs& a, cudaStream_t s);
+
+// Token compaction: regions as for CopyArgs.
+struct CompactArgs {
+    char* k_base;
+    char* v_base;
+    int64_t layer_stride;   // bytes; 0 for one layer
+    int32_t layers;
+    int32_t fp8;            // k_base is an fp8 page pool (v_base unused, one layer)
+    int32_t hkv;
+    int32_t row_bytes;      // D * element size
+    int64_t num_blocks;
+    int32_t block_size, max_blocks, num_seqs;
+    int32_t total_keep;
+    const int32_t* starts;
+    const int32_t* cu;
+    const int32_t* keep;
+    const int32_t* block_table;
+    int* status;
+};
+kvattn_status launch_compact(const CompactArgs& a, cudaStream_t s);
 
 struct DecodeArgs {
     const void* q;

@@ -1,4 +1,5 @@
-// Argument marshalling of the rotary and windowed calls for Python.
+// Argument marshalling of the rotary, windowed, shared-prefix and compaction calls
+// for Python.
 //
 // These calls may be a few microseconds of GPU work, less than the interpreter
 // takes to check their tensors one attribute at a time and to hand them to
@@ -48,7 +49,7 @@ struct Type {
 };
 constexpr Type kAny{0, 0}, kInt32{0, 32}, kFloat32{2, 32}, kBfloat16{4, 16};
 
-constexpr int kMaxDims = 4;
+constexpr int kMaxDims = 6;
 
 struct View {
     void* ptr;
@@ -287,17 +288,20 @@ bool token_rows(PyObject* t, Type type, int64_t device, int64_t heads, int64_t d
 }
 
 // rotary_append(fp8, cfg, rotary, cache, q, k, v, positions, seq_ids, block_table, q_out or None)
-PyObject* rotary_append(PyObject*, PyObject* const* a, Py_ssize_t n)
+// rotary_append_axes(the same, axes, slots)
+PyObject* rotary_any(PyObject* const* a, Py_ssize_t n, bool with_axes)
 {
     int64_t device;
     void* stream;
-    if (n != 11 || !here(&device, &stream)) return irregular();
+    if (n != (with_axes ? 13 : 11) || !here(&device, &stream)) return irregular();
     const bool fp8 = a[0] == Py_True;
     const Struct<kvattn_config> cfg_s(a[1]);
     const Struct<kvattn_rotary> rot(a[2]);
     const kvattn_config* cfg = cfg_s.get();
     CacheArg cache;
-    View q, k, v, pos, ids, table, out;
+    View q, k, v, pos, ids, table, out, slots;
+    const Struct<kvattn_rope_axes> axes(with_axes ? a[11] : nullptr);
+    if (with_axes && (!axes.get() || !view(a[12], kInt32, device, false, &slots))) return irregular();
     if (!cfg || !rot.get() || !cache.get(a[3], fp8, cfg, device)) return irregular();
     const Type dt = type_of(cfg);
     if (!token_rows(a[4], dt, device, cfg->num_q_heads, cfg->head_dim, &q) ||
@@ -311,11 +315,17 @@ PyObject* rotary_append(PyObject*, PyObject* const* a, Py_ssize_t n)
     if (a[10] != Py_None && (!view(a[10], dt, device, false, &out) ||
                              !has_shape(out, 3, T, cfg->num_q_heads, cfg->head_dim)))
         return irregular();
-    if (k.dim[0] != T || v.dim[0] != T || !has_shape(pos, 1, T) || !has_shape(ids, 1, T) || table.ndim != 2 ||
+    const bool pos_ok = with_axes ? has_shape(pos, 2, axes.get()->num_axes, T) && has_shape(slots, 1, T) : has_shape(pos, 1, T);
+    if (k.dim[0] != T || v.dim[0] != T || !pos_ok || !has_shape(ids, 1, T) || table.ndim != 2 ||
         table.dim[0] > INT32_MAX || table.dim[1] > INT32_MAX || T > INT32_MAX)
         return irregular();
-    auto run = [&](auto fn, auto* desc) {
+    auto run = [&](auto fn, auto axes_fn, auto* desc) {
         return call([&] {
+            if (with_axes)
+                return axes_fn(cfg, rot.get(), axes.get(), desc, q.ptr, q.stride[0], k.ptr, k.stride[0], v.ptr,
+                               v.stride[0], out.ptr, (const int32_t*)pos.ptr, (const int32_t*)slots.ptr,
+                               (const int32_t*)ids.ptr, (const int32_t*)table.ptr, (int32_t)table.dim[0],
+                               (int32_t)table.dim[1], (int32_t)T, stream);
             return fn(cfg, rot.get(), desc, q.ptr, q.stride[0], k.ptr, k.stride[0], v.ptr, v.stride[0], out.ptr,
                       (const int32_t*)pos.ptr, (const int32_t*)ids.ptr, (const int32_t*)table.ptr, (int32_t)table.dim[0],
                       (int32_t)table.dim[1], (int32_t)T, stream);
@@ -323,15 +333,122 @@ PyObject* rotary_append(PyObject*, PyObject* const* a, Py_ssize_t n)
     };
     if (fp8) {
         const Struct<kvattn_cache_fp8> d(cache.desc);
-        return d.get() ? run(kvattn_rotary_append_fp8, d.get()) : irregular();
+        return d.get() ? run(kvattn_rotary_append_fp8, kvattn_rotary_append_axes_fp8, d.get()) : irregular();
     }
     const Struct<kvattn_cache> d(cache.desc);
-    return d.get() ? run(kvattn_rotary_append, d.get()) : irregular();
+    return d.get() ? run(kvattn_rotary_append, kvattn_rotary_append_axes, d.get()) : irregular();
+}
+PyObject* rotary_append(PyObject*, PyObject* const* a, Py_ssize_t n) { return rotary_any(a, n, false); }
+PyObject* rotary_append_axes(PyObject*, PyObject* const* a, Py_ssize_t n) { return rotary_any(a, n, true); }
+
+// decode_shared(fp8, cfg, cache, q, block_table, seq_lens, max_seq_len, cu_groups,
+//               shared_lens, max_shared_len, out, workspace)
+PyObject* decode_shared(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    int64_t device;
+    void* stream;
+    int32_t max_len, max_shared;
+    if (n != 12 || !here(&device, &stream)) return irregular();
+    const bool fp8 = a[0] == Py_True;
+    const Struct<kvattn_config> cfg_s(a[1]);
+    const kvattn_config* cfg = cfg_s.get();
+    CacheArg cache;
+    View q, table, lens, cu, shared, out, ws;
+    if (!cfg || !cache.get(a[2], fp8, cfg, device) || !view(a[3], type_of(cfg), device, false, &q) ||
+        !view(a[4], kInt32, device, false, &table) || !view(a[5], kInt32, device, false, &lens) ||
+        !as_i32(a[6], &max_len) || !view(a[7], kInt32, device, false, &cu) ||
+        !view(a[8], kInt32, device, false, &shared) || !as_i32(a[9], &max_shared) ||
+        !view(a[10], type_of(cfg), device, false, &out) || !view(a[11], kAny, device, false, &ws))
+        return irregular();
+    const int64_t B = q.dim[0], groups = shared.dim[0];
+    if (!has_shape(q, 3, B, cfg->num_q_heads, cfg->head_dim) || !has_shape(out, 3, B, cfg->num_q_heads, cfg->head_dim) ||
+        !has_shape(lens, 1, B) || !has_shape(shared, 1, groups) || !has_shape(cu, 1, groups + 1) || table.ndim != 2 ||
+        table.dim[0] < B || table.dim[1] > INT32_MAX || B > INT32_MAX || groups > INT32_MAX)
+        return irregular();
+    auto run = [&](auto fn, auto* desc) {
+        return call([&] {
+            return fn(cfg, desc, q.ptr, (const int32_t*)table.ptr, (int32_t)table.dim[1], (const int32_t*)lens.ptr,
+                      (int32_t)B, max_len, (const int32_t*)cu.ptr, (const int32_t*)shared.ptr, (int32_t)groups,
+                      max_shared, out.ptr, ws.ptr, (size_t)ws.nbytes, stream);
+        });
+    };
+    if (fp8) {
+        const Struct<kvattn_cache_fp8> d(cache.desc);
+        return d.get() ? run(kvattn_decode_shared_fp8, d.get()) : irregular();
+    }
+    const Struct<kvattn_cache> d(cache.desc);
+    return d.get() ? run(kvattn_decode_shared, d.get()) : irregular();
+}
+
+// copy_blocks_fp8(cfg, cache, src, dst)
+PyObject* copy_blocks_fp8(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    int64_t device;
+    void* stream;
+    if (n != 4 || !here(&device, &stream)) return irregular();
+    const Struct<kvattn_config> cfg_s(a[0]);
+    const kvattn_config* cfg = cfg_s.get();
+    CacheArg cache;
+    View src, dst;
+    if (!cfg || !cache.get(a[1], true, cfg, device) || !view(a[2], kInt32, device, false, &src) ||
+        !view(a[3], kInt32, device, false, &dst) || src.dim[0] > INT32_MAX || !has_shape(src, 1, src.dim[0]) ||
+        !has_shape(dst, 1, src.dim[0]))
+        return irregular();
+    const Struct<kvattn_cache_fp8> d(cache.desc);
+    if (!d.get()) return irregular();
+    return call([&] {
+        return kvattn_copy_blocks_fp8(cfg, d.get(), (const int32_t*)src.ptr, (const int32_t*)dst.ptr, (int32_t)src.dim[0],
+                                      stream);
+    });
+}
+
+// compact_tokens(0: Cache, 1: CacheFP8, 2: LayeredCache; cfg, cache, block_table, starts, cu_keep, keep)
+PyObject* compact_tokens(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    int64_t device;
+    void* stream;
+    int32_t kind;
+    if (n != 7 || !as_i32(a[0], &kind) || kind < 0 || !here(&device, &stream)) return irregular();
+    const Struct<kvattn_config> cfg_s(a[1]);
+    const kvattn_config* cfg = cfg_s.get();
+    View table, starts, cu, keep;
+    if (!cfg || !view(a[3], kInt32, device, false, &table) || !view(a[4], kInt32, device, false, &starts) ||
+        !view(a[5], kInt32, device, false, &cu) || !view(a[6], kInt32, device, false, &keep))
+        return irregular();
+    const int64_t S = starts.dim[0], K = keep.dim[0];
+    if (!has_shape(starts, 1, S) || !has_shape(cu, 1, S + 1) || !has_shape(keep, 1, K) || table.ndim != 2 ||
+        table.dim[0] < S || table.dim[1] > INT32_MAX || S > INT32_MAX || K > INT32_MAX)
+        return irregular();
+    auto run = [&](auto fn, auto... cache) {
+        return call([&] {
+            return fn(cfg, cache..., (const int32_t*)starts.ptr, (const int32_t*)cu.ptr, (const int32_t*)keep.ptr, (int32_t)K,
+                      (const int32_t*)table.ptr, (int32_t)S, (int32_t)table.dim[1], stream);
+        });
+    };
+    if (kind == 2) {
+        PyObject* pool = PyObject_GetAttr(a[2], s_pool);
+        View v;
+        const bool ok = pool && view(pool, type_of(cfg), device, false, &v) && v.ndim == 6 && v.dim[1] == 2 &&
+                        v.dim[3] == cfg->num_kv_heads && v.dim[5] == cfg->head_dim && v.dim[0] <= INT32_MAX &&
+                        v.dim[4] <= INT32_MAX;
+        Py_XDECREF(pool);
+        if (!ok) return irregular();
+        return run(kvattn_compact_tokens_layered, v.ptr, (int32_t)v.dim[0], v.dim[2], (int32_t)v.dim[4]);
+    }
+    CacheArg cache;
+    if (!cache.get(a[2], kind == 1, cfg, device)) return irregular();
+    if (kind == 1) {
+        const Struct<kvattn_cache_fp8> d(cache.desc);
+        return d.get() ? run(kvattn_compact_tokens_fp8, d.get()) : irregular();
+    }
+    const Struct<kvattn_cache> d(cache.desc);
+    return d.get() ? run(kvattn_compact_tokens, d.get()) : irregular();
 }
 
 #define KVATTN_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {KVATTN_METHOD(setup), KVATTN_METHOD(decode_window), KVATTN_METHOD(prefill_window),
-                         KVATTN_METHOD(rotary_append), {nullptr, nullptr, 0, nullptr}};
+                         KVATTN_METHOD(rotary_append), KVATTN_METHOD(rotary_append_axes), KVATTN_METHOD(decode_shared),
+                         KVATTN_METHOD(copy_blocks_fp8), KVATTN_METHOD(compact_tokens), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

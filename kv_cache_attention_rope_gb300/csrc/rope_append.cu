@@ -451,6 +451,8 @@ __device__ __forceinline__ long long page_id(const RopeArgs& a, int t, int& pos,
     if (pos < 0 || seq < 0 || seq >= a.num_seqs || pos / a.block_size >= a.max_blocks) return -1;
     blk = a.block_table[(int64_t)seq * a.max_blocks + pos / a.block_size];
     if (blk < 0 || blk >= a.num_blocks) return -1;  // recorded by the ring kernel
+    for (int x = 0; x < a.num_axes; ++x)
+        if (a.axes[(int64_t)x * a.num_tokens + t] < 0) return -1;
     return (long long)seq * (((long long)a.max_blocks * a.block_size) / 16) + pos / 16;
 }
 
