@@ -771,6 +771,38 @@ int32_t window_span(int32_t max_seq_len, DecodeWindow w)
     return (int32_t)std::min<int64_t>(max_seq_len, tiles * 16);
 }
 
+void decode_args(const kvattn_config* cfg, const kvattn_cache* cache, bool fp8, const void* q, const int32_t* block_table,
+                 int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t batch, int32_t max_seq_len, int32_t slots,
+                 void* out, void* workspace, DecodeArgs& a)
+{
+    std::memset(&a, 0, sizeof(a));
+    a.q = q;
+    a.k_pool = cache->k_pool;
+    a.v_pool = cache->v_pool;
+    a.block_table = block_table;
+    a.seq_lens = seq_lens;
+    a.out = out;
+    if (slots > 1) {
+        const WorkspaceLayout wl = workspace_layout(cfg, batch, slots);
+        char* w = static_cast<char*>(workspace);
+        a.nslots = reinterpret_cast<int32_t*>(w + wl.nslots_off);
+        a.part_o = reinterpret_cast<float*>(w + wl.o_off);
+        a.part_ml = reinterpret_cast<float*>(w + wl.ml_off);
+    }
+    a.num_blocks = cache->num_blocks;
+    a.block_size = cache->block_size;
+    a.max_blocks = max_blocks_per_seq;
+    a.batch = batch;
+    a.max_seq_len = max_seq_len;
+    a.splits = slots;
+    a.hq = cfg->num_q_heads;
+    a.hkv = cfg->num_kv_heads;
+    a.d = cfg->head_dim;
+    a.dtype = cfg->dtype;
+    a.scale_log2 = scale_of(cfg) * 1.4426950408889634f;
+    a.fp8 = fp8 ? 1 : 0;
+}
+
 kvattn_status decode_any(const kvattn_config* cfg, const kvattn_cache* cache, bool fp8, DecodeWindow win,
                          const void* q, const int32_t* block_table, int32_t max_blocks_per_seq,
                          const int32_t* seq_lens, int32_t batch, int32_t max_seq_len, int32_t num_splits, void* out,
@@ -787,31 +819,8 @@ kvattn_status decode_any(const kvattn_config* cfg, const kvattn_cache* cache, bo
         if (reinterpret_cast<uintptr_t>(workspace) & 255u) return KVATTN_ERR_INVALID_ARG;
     }
     DecodeArgs a;
-    std::memset(&a, 0, sizeof(a));
-    a.q = q;
-    a.k_pool = cache->k_pool;
-    a.v_pool = cache->v_pool;
-    a.block_table = block_table;
-    a.seq_lens = seq_lens;
-    a.out = out;
-    if (p.slots > 1) {
-        char* w = static_cast<char*>(workspace);
-        a.nslots = reinterpret_cast<int32_t*>(w + wl.nslots_off);
-        a.part_o = reinterpret_cast<float*>(w + wl.o_off);
-        a.part_ml = reinterpret_cast<float*>(w + wl.ml_off);
-    }
-    a.num_blocks = cache->num_blocks;
-    a.block_size = cache->block_size;
-    a.max_blocks = max_blocks_per_seq;
-    a.batch = batch;
-    a.max_seq_len = max_seq_len;
-    a.splits = p.slots;
-    a.hq = cfg->num_q_heads;
-    a.hkv = cfg->num_kv_heads;
-    a.d = cfg->head_dim;
-    a.dtype = cfg->dtype;
-    a.scale_log2 = scale_of(cfg) * 1.4426950408889634f;
-    a.fp8 = fp8 ? 1 : 0;
+    decode_args(cfg, cache, fp8, q, block_table, max_blocks_per_seq, seq_lens, batch, max_seq_len, p.slots, out, workspace,
+                a);
     a.status = device_status_ptr();
     if (!a.status) return KVATTN_ERR_CUDA;
     a.window = win.window;
@@ -880,7 +889,31 @@ bool groups_ok(int32_t batch, int32_t num_groups, int32_t max_shared_len)
     return num_groups >= 0 && num_groups <= batch && max_shared_len >= 0;
 }
 
-// Every sequence by itself.
+// Workspace of the form that reads prefixes once: kvattn_decode's for the
+// sequences' own keys, then the sequences' PrefixOf, then the prefix pieces' outputs
+// and (max, sum).  bytes == 0: this call cannot take that form.
+struct SharedLayout {
+    int32_t slots;
+    size_t prefix_off, o_off, ml_off, bytes;
+};
+SharedLayout shared_layout(const kvattn_config* cfg, int32_t batch, int32_t max_seq_len, int32_t num_groups,
+                           int32_t max_shared_len)
+{
+    SharedLayout l{};
+    if (cfg->dtype != KVATTN_BF16 || num_groups < 1 || num_groups > kMaxGroups || batch < 2 || max_shared_len < 16)
+        return l;
+    const int64_t pieces = prefix_pieces(cfg->num_q_heads, cfg->num_kv_heads, batch, num_groups, num_sms());
+    // (the stream's tiles are counted in 32 bits)
+    if (pieces > ((int64_t)1 << 30) / ((int64_t)max_shared_len / 128 + 1)) return l;
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    l.slots = decode_plan(batch, cfg->num_kv_heads, cfg->num_q_heads / cfg->num_kv_heads, max_seq_len, 0).slots;
+    l.prefix_off = up(workspace_layout(cfg, batch, l.slots).bytes);
+    l.o_off = l.prefix_off + up((size_t)batch * sizeof(PrefixOf));
+    l.ml_off = l.o_off + (size_t)pieces * kPrefixRows * cfg->head_dim * 4;
+    l.bytes = l.ml_off + (size_t)pieces * kPrefixRows * 2 * 4;
+    return l;
+}
+
 kvattn_status decode_shared_any(const kvattn_config* cfg, const kvattn_cache* cache, bool fp8, const void* q,
                                 const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* seq_lens,
                                 int32_t batch, int32_t max_seq_len, const int32_t* cu_groups,
@@ -889,8 +922,32 @@ kvattn_status decode_shared_any(const kvattn_config* cfg, const kvattn_cache* ca
 {
     if (batch >= 0 && !groups_ok(batch, num_groups, max_shared_len)) return KVATTN_ERR_INVALID_ARG;
     if (num_groups > 0 && (!cu_groups || !shared_lens)) return KVATTN_ERR_INVALID_ARG;
-    return decode_any(cfg, cache, fp8, {INT32_MAX, 0}, q, block_table, max_blocks_per_seq, seq_lens, batch, max_seq_len, 0,
-                      out, workspace, workspace_bytes, stream);
+    const kvattn_status st = decode_check(cfg, cache, fp8, q, block_table, max_blocks_per_seq, seq_lens, batch,
+                                          max_seq_len, 0, out);
+    if (st != KVATTN_OK || batch == 0) return st;
+    const SharedLayout l = shared_layout(cfg, batch, max_seq_len, num_groups, max_shared_len);
+    const bool once = l.bytes > 0 && !fp8 && cache->block_size % 16 == 0 &&
+                      cache->num_blocks * cfg->num_kv_heads < ((int64_t)1 << 31) / cache->block_size;
+    if (!once)  // every sequence by itself
+        return decode_any(cfg, cache, fp8, {INT32_MAX, 0}, q, block_table, max_blocks_per_seq, seq_lens, batch,
+                          max_seq_len, 0, out, workspace, workspace_bytes, stream);
+    if (!workspace || workspace_bytes < l.bytes) return KVATTN_ERR_WORKSPACE_TOO_SMALL;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return KVATTN_ERR_INVALID_ARG;
+    DecodeArgs a;
+    decode_args(cfg, cache, fp8, q, block_table, max_blocks_per_seq, seq_lens, batch, max_seq_len, l.slots, out, workspace,
+                a);
+    a.status = device_status_ptr();
+    if (!a.status) return KVATTN_ERR_CUDA;
+    char* w = static_cast<char*>(workspace);
+    a.prefix = reinterpret_cast<PrefixOf*>(w + l.prefix_off);
+    a.prefix_o = reinterpret_cast<float*>(w + l.o_off);
+    a.prefix_ml = reinterpret_cast<float*>(w + l.ml_off);
+    a.cu_groups = cu_groups;
+    a.shared_lens = shared_lens;
+    a.num_groups = num_groups;
+    a.max_shared = max_shared_len;
+    const kvattn_status pst = launch_decode_shared(a, static_cast<cudaStream_t>(stream));
+    return pst != KVATTN_OK ? pst : launch_decode_own(a, static_cast<cudaStream_t>(stream));
 }
 
 }  // namespace
@@ -899,7 +956,8 @@ size_t kvattn_decode_shared_workspace_size(const kvattn_config* cfg, int32_t bat
                                            int32_t num_groups, int32_t max_shared_len)
 {
     if (batch < 0 || max_seq_len < 0 || !groups_ok(batch, num_groups, max_shared_len)) return 0;
-    return kvattn_decode_window_workspace_size(cfg, batch, max_seq_len, INT32_MAX, 0, 0);
+    const size_t alone = kvattn_decode_window_workspace_size(cfg, batch, max_seq_len, INT32_MAX, 0, 0);
+    return alone == 0 ? 0 : std::max(alone, shared_layout(cfg, batch, max_seq_len, num_groups, max_shared_len).bytes);
 }
 
 kvattn_status kvattn_decode_shared(const kvattn_config* cfg, const kvattn_cache* cache, const void* q,

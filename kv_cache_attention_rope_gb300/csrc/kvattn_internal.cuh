@@ -197,6 +197,17 @@ struct CompactArgs {
 };
 kvattn_status launch_compact(const CompactArgs& a, cudaStream_t s);
 
+// What a sequence shares (launch_decode_shared): the first `tokens` of its keys (a
+// multiple of 16; 0: none), and where the partial results over them are.  The prefix
+// kernel's work is a stream of tiles, cut into equal ranges of `per` tiles; the tiles
+// of (sequence, KV head h) are first + h head_tiles .. + tiles - 1, piece c of the
+// stream's range c lies at (c + segment + h head_segments) kPrefixRows + row.
+struct PrefixOf {
+    int32_t tokens, first, tiles, head_tiles;
+    int32_t segment, head_segments, row, per;
+};
+constexpr int kPrefixRows = 256;
+
 struct DecodeArgs {
     const void* q;
     const void* k_pool;
@@ -219,12 +230,33 @@ struct DecodeArgs {
     float scale_log2;  // softmax scale * log2(e)
     int* status;
     int32_t window, sinks;  // launch_decode_window only
+    // launch_decode_shared and launch_decode_own only
+    PrefixOf* prefix;       // [batch]
+    float* prefix_o;        // [pieces][kPrefixRows][d], not divided by their sums
+    float* prefix_ml;       // [pieces][kPrefixRows][2] (max in log2 units, sum)
+    const int32_t* cu_groups;
+    const int32_t* shared_lens;
+    int32_t num_groups, max_shared;
 };
 kvattn_status launch_decode(const DecodeArgs& a, cudaStream_t s);
 // max_tiles: most 16-token tiles that a query sees, or 0 to cut the segments as a.splits says.
 kvattn_status launch_decode_window(const DecodeArgs& a, int32_t max_tiles, cudaStream_t s);
 // The one-launch form, where it is the faster one (else false, nothing launched).
 bool launch_decode_direct(const DecodeArgs& a, int32_t max_tiles, cudaStream_t s, kvattn_status* st);
+
+// Over the shared prefixes, into a.prefix, a.prefix_o and a.prefix_ml (decode_shared.cu), ...
+kvattn_status launch_decode_shared(const DecodeArgs& a, cudaStream_t s);
+// ... and then over each sequence's own keys, with the merge.
+kvattn_status launch_decode_own(const DecodeArgs& a, cudaStream_t s);
+// Most groups of a call that reads prefixes once (others read each sequence by itself).
+constexpr int32_t kMaxGroups = 512;
+// Partial results of the prefix kernel that a call may need: one per range, and one
+// more per (rows of a group, KV head).  Groups of fewer than two sequences share nothing.
+inline int64_t prefix_pieces(int32_t hq, int32_t hkv, int32_t batch, int32_t num_groups, int32_t ctas)
+{
+    const int64_t g = hq / hkv, groups = num_groups < batch / 2 ? num_groups : batch / 2;
+    return ctas + (batch * g / kPrefixRows + groups) * hkv;
+}
 
 // Largest decode batch (the kernels keep a per-sequence prefix sum in shared memory).
 constexpr int32_t kMaxDecodeBatch = 8192;
