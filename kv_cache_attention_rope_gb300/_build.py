@@ -14,7 +14,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkvattn.so")
 # Python extension module, linked against LIB beside it; the name says which Python it was built for
 MARSHAL = os.path.join(PKG, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
-SOURCES = ["api.cu", "rope_append.cu", "rotary.cu", "rotary_axes.cu", "decode.cu", "decode_window.cu", "decode_shared.cu", "decode_own.cu", "decode_direct.cu", "decode_static.cu", "prefill.cu", "prefill_window.cu", "prefill_fp8.cu", "blocks.cu", "compact.cu", "allocator.cpp"]
+SOURCES = ["api.cu", "rope_append.cu", "rotary.cu", "rotary_axes.cu", "decode.cu", "decode_window.cu", "decode_shared.cu", "decode_direct.cu", "decode_static.cu", "prefill.cu", "prefill_window.cu", "prefill_fp8.cu", "blocks.cu", "compact.cu", "allocator.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -889,28 +889,31 @@ bool groups_ok(int32_t batch, int32_t num_groups, int32_t max_shared_len)
     return num_groups >= 0 && num_groups <= batch && max_shared_len >= 0;
 }
 
-// Workspace of the form that reads prefixes once: kvattn_decode's for the
-// sequences' own keys, then the sequences' PrefixOf, then the prefix pieces' outputs
-// and (max, sum).  bytes == 0: this call cannot take that form.
+// Workspace of the form that reads prefixes once (SharedArgs), each part 256-byte
+// aligned.  bytes == 0: this call cannot take that form.
 struct SharedLayout {
-    int32_t slots;
-    size_t prefix_off, o_off, ml_off, bytes;
+    size_t o_off, ml_off, own_o_off, own_ml_off, bytes;
 };
 SharedLayout shared_layout(const kvattn_config* cfg, int32_t batch, int32_t max_seq_len, int32_t num_groups,
                            int32_t max_shared_len)
 {
     SharedLayout l{};
-    if (cfg->dtype != KVATTN_BF16 || num_groups < 1 || num_groups > kMaxGroups || batch < 2 || max_shared_len < 16)
+    if (cfg->dtype != KVATTN_BF16 || num_groups < 1 || num_groups > kMaxGroups || batch < 2 || batch > kMaxSharedBatch ||
+        max_shared_len < 16)
         return l;
-    const int64_t pieces = prefix_pieces(cfg->num_q_heads, cfg->num_kv_heads, batch, num_groups, num_sms());
-    // (the stream's tiles are counted in 32 bits)
-    if (pieces > ((int64_t)1 << 30) / ((int64_t)max_shared_len / 128 + 1)) return l;
+    const int32_t hkv = cfg->num_kv_heads, ctas = num_sms();
+    const int64_t pieces = shared_pieces(cfg->num_q_heads, hkv, batch, num_groups, ctas);
+    // (the streams' pages are counted in 32 bits)
+    const int64_t pages = pieces * ((int64_t)max_shared_len / 16 + 1) + (int64_t)batch * hkv * ((int64_t)max_seq_len / 16 + 1);
+    if (pages > (1 << 30)) return l;
+    const size_t rows = (size_t)pieces * kSharedRows;
+    const size_t own_rows = (size_t)own_pieces(hkv, batch, ctas) * (cfg->num_q_heads / hkv);
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    l.slots = decode_plan(batch, cfg->num_kv_heads, cfg->num_q_heads / cfg->num_kv_heads, max_seq_len, 0).slots;
-    l.prefix_off = up(workspace_layout(cfg, batch, l.slots).bytes);
-    l.o_off = l.prefix_off + up((size_t)batch * sizeof(PrefixOf));
-    l.ml_off = l.o_off + (size_t)pieces * kPrefixRows * cfg->head_dim * 4;
-    l.bytes = l.ml_off + (size_t)pieces * kPrefixRows * 2 * 4;
+    l.o_off = up((size_t)batch * sizeof(SharedOf));
+    l.ml_off = l.o_off + rows * cfg->head_dim * 4;
+    l.own_o_off = l.ml_off + rows * 2 * 4;
+    l.own_ml_off = l.own_o_off + up(own_rows * cfg->head_dim * 4);
+    l.bytes = l.own_ml_off + up(own_rows * 2 * 4);
     return l;
 }
 
@@ -933,21 +936,22 @@ kvattn_status decode_shared_any(const kvattn_config* cfg, const kvattn_cache* ca
                           max_seq_len, 0, out, workspace, workspace_bytes, stream);
     if (!workspace || workspace_bytes < l.bytes) return KVATTN_ERR_WORKSPACE_TOO_SMALL;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return KVATTN_ERR_INVALID_ARG;
-    DecodeArgs a;
-    decode_args(cfg, cache, fp8, q, block_table, max_blocks_per_seq, seq_lens, batch, max_seq_len, l.slots, out, workspace,
-                a);
-    a.status = device_status_ptr();
-    if (!a.status) return KVATTN_ERR_CUDA;
+    SharedArgs a;
+    std::memset(&a, 0, sizeof(a));
+    decode_args(cfg, cache, fp8, q, block_table, max_blocks_per_seq, seq_lens, batch, max_seq_len, 1, out, nullptr, a.d);
+    a.d.status = device_status_ptr();
+    if (!a.d.status) return KVATTN_ERR_CUDA;
     char* w = static_cast<char*>(workspace);
-    a.prefix = reinterpret_cast<PrefixOf*>(w + l.prefix_off);
-    a.prefix_o = reinterpret_cast<float*>(w + l.o_off);
-    a.prefix_ml = reinterpret_cast<float*>(w + l.ml_off);
+    a.of = reinterpret_cast<SharedOf*>(w);
+    a.o = reinterpret_cast<float*>(w + l.o_off);
+    a.ml = reinterpret_cast<float*>(w + l.ml_off);
+    a.own_o = reinterpret_cast<float*>(w + l.own_o_off);
+    a.own_ml = reinterpret_cast<float*>(w + l.own_ml_off);
     a.cu_groups = cu_groups;
     a.shared_lens = shared_lens;
     a.num_groups = num_groups;
     a.max_shared = max_shared_len;
-    const kvattn_status pst = launch_decode_shared(a, static_cast<cudaStream_t>(stream));
-    return pst != KVATTN_OK ? pst : launch_decode_own(a, static_cast<cudaStream_t>(stream));
+    return launch_decode_shared(a, static_cast<cudaStream_t>(stream));
 }
 
 }  // namespace

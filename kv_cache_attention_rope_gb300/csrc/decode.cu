@@ -28,6 +28,6 @@ DecodePlan decode_plan(int32_t batch, int32_t hkv, int32_t group, int32_t max_se
     return p;
 }
 
-kvattn_status launch_decode(const DecodeArgs& a, cudaStream_t s) { return dispatch<kWhole>(a, s); }
+kvattn_status launch_decode(const DecodeArgs& a, cudaStream_t s) { return dispatch<false>(a, s); }
 
 }  // namespace kvattn

@@ -160,56 +160,6 @@ struct Bf16Tile {
     }
 };
 
-// ---- fp8 pages (layout: kF8Page), f16 operands.  K: rows rk0, rk1 = rk0 + 2,
-// chunks q4 and q4 + 4, each the lane's share of four k-steps.  V is stored
-// transposed: one word is tokens 4 q4 .. 4 q4 + 3 of a dim, whose order the
-// rows rk0, rk1 follow.
-struct Fp8Tile {
-    uint4 k[2][2];
-    uint32_t v[16];
-    float ks[2], vs[2];
-    __device__ __forceinline__ void load(const unsigned char* pg, int rk0, int g4, int q4)
-    {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = rk0 + 2 * r;
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                k[r][i] = *reinterpret_cast<const uint4*>(pg + row * 128 + (((q4 + 4 * i) ^ f8_swz(row)) << 4));
-            ks[r] = *reinterpret_cast<const float*>(pg + kF8KsOff + 4 * row);
-            vs[r] = *reinterpret_cast<const float*>(pg + kF8VsOff + 4 * row);
-        }
-#pragma unroll
-        for (int m = 0; m < 16; ++m)
-            v[m] = *reinterpret_cast<const uint32_t*>(pg + kF8VOff + 16 * (8 * m + g4) + 4 * q4);
-    }
-    __device__ __forceinline__ void scores(float (&s)[4], const uint32_t (&q)[8][2]) const
-    {
-        float u[4] = {0.f, 0.f, 0.f, 0.f};  // two chains of dependent MMAs
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t a[4] = {k[0][i].x, k[0][i].y, k[0][i].z, k[0][i].w};
-            const uint32_t b[4] = {k[1][i].x, k[1][i].y, k[1][i].z, k[1][i].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                mma_f16_16816(i ? u : s, e4m3x2_to_f16x2(a[j]), e4m3x2_to_f16x2(b[j]), e4m3x2_to_f16x2(a[j] >> 16),
-                              e4m3x2_to_f16x2(b[j] >> 16), q[4 * i + j][0], q[4 * i + j][1]);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] += u[i];
-    }
-    static __device__ __forceinline__ int dim_of(int e, int half, int g4) { return 16 * e + 8 * half + g4; }
-    __device__ __forceinline__ void add(float (&o)[8][4], uint32_t b0, uint32_t b1, uint32_t vmask) const
-    {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint32_t x = v[2 * e] & vmask, y = v[2 * e + 1] & vmask;
-            mma_f16_16816(o[e], e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(y), e4m3x2_to_f16x2(x >> 16),
-                          e4m3x2_to_f16x2(y >> 16), b0, b1);
-        }
-    }
-};
-
 // Resident warps per SM that the registers leave room for.  Measured: a
 // bf16 tile at D = 128, with the next one on its way, wants 200 registers (32 / 8
 // heads, 32 sequences, window 4096: 88.5 us with 8 warps, 91.9 with 12, 100.7

@@ -1,6 +1,5 @@
-// Kernels of the split-KV decode attention (decode.cu), of its windowed form
-// (decode_window.cu) and of the part of a shared-prefix decode that is each
-// sequence's own (decode_own.cu) over a paged (or contiguous) KV cache.
+// Kernels of the split-KV decode attention (decode.cu) and of its windowed form
+// (decode_window.cu) over a paged (or contiguous) KV cache.
 //
 // What it computes: for every sequence b and query head j,
 //   out[b][j] = softmax_i(q[b][j] . K_b[i] * scale) V_b[i],  i < seq_lens[b]
@@ -40,15 +39,12 @@
 #include <cstring>
 #include <mutex>
 
-#include "kvattn_tc.cuh"
+#include "fp8_tile.cuh"
 
 namespace kvattn {
 namespace {
 
 constexpr int kTile = 16;  // tokens per tile
-// Which keys of a sequence a call is over: all, those of a window, or those behind
-// the prefix that it shares with others (the result is then always a partial one).
-enum Mode { kWhole, kWindow, kOwn };
 constexpr int kConsumerWarps = 4;
 constexpr int kThreads = (kConsumerWarps + 1) * 32;
 constexpr int kMinPer = 4;  // fewest tiles in a CTA's range (flat mode)
@@ -69,15 +65,6 @@ constexpr int ctas_per_sm() { return kFP8 ? 4 : 3; }
 struct PageMaps {
     CUtensorMap k, v;
 };
-
-// 2^x (ex2.approx.ftz: a few ulp, far below the bf16 rounding P goes through
-// on the tensor-core path); 2^-inf = 0.
-__device__ __forceinline__ float fast_exp2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // 16 bytes of cache elements -> f32x2 pairs (element 2i in the low half)
 template <bool kBF16>
@@ -219,107 +206,7 @@ __device__ __forceinline__ uint32_t seen_bits(int tok0, const Piece& pc, const D
 }
 
 // Walks the pieces of this CTA.  Producer and consumers run identical copies.
-// Softmax state of a warp over fp8 pages, windowed form: of query heads 2 q4 and
-// 2 q4 + 1 the running maximum (log2 units), the sum, and the reference that the
-// output o is in units of.  P goes into the MMA in f16 as weight * V scale /
-// reference.  The reference follows that product, not the scale, so that a token
-// of large V and no weight leaves the others their bits, and a row of zeros, which
-// is stored with the scale 1, does not count.  f16 rounds each product within
-// 2^-11 relative, or 2^-25 of the head's largest.
-struct Fp8Softmax {
-    static constexpr float kLeast = 0x1p-100f;  // of a reference: its inverse is finite
-    float m[2], l[2], ref[2], rinv[2];
-    float scale16;  // 16 times the smaller reference
-    __device__ __forceinline__ void init()
-    {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            m[e] = -INFINITY;
-            l[e] = ref[e] = rinv[e] = 0.f;
-        }
-        scale16 = 0.f;
-    }
-    // One tile: scores x of this lane's tokens rk0 and rk1 ((rk0, head 0), (rk0,
-    // 1), (rk1, 0), (rk1, 1)), their V scales sv0 and sv1 (0: not seen), word(i)
-    // the lane's i-th word of V codes (tokens 4 q4 .. 4 q4 + 3).  Gives the
-    // products w for P.V and rescales o.  The maximum is raised when a score
-    // exceeds it by more than 2^8.  A V scale over 16 times a reference has the
-    // products looked at, and the reference raised to one that is; so w stays
-    // within 2^12.  The warp agrees on these only then.
-    template <int kN, typename Word>
-    __device__ __forceinline__ void step(const float (&x)[4], float sv0, float sv1, int lane, Word word, float (&o)[kN][4],
-                                         float (&w)[4])
-    {
-        float l0 = fmaxf(x[0], x[2]), l1 = fmaxf(x[1], x[3]);
-        const bool raise = l0 > m[0] + 8.f || l1 > m[1] + 8.f || fmaxf(sv0, sv1) > scale16;
-        float p[4];
-        auto weigh = [&] {
-            // a head whose scores are all -inf so far has no weight yet
-            const float m0 = m[0] == -INFINITY ? 0.f : m[0], m1 = m[1] == -INFINITY ? 0.f : m[1];
-            p[0] = fast_exp2(x[0] - m0);
-            p[1] = fast_exp2(x[1] - m1);
-            p[2] = fast_exp2(x[2] - m0);
-            p[3] = fast_exp2(x[3] - m1);
-        };
-        if (__any_sync(0xffffffffu, raise)) {
-            if (__any_sync(0xffffffffu, sv0 == 1.f || sv1 == 1.f)) {  // rows of zeros?
-                uint32_t any = 0;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) any |= word(i) & 0x7f7f7f7fu;
-#pragma unroll
-                for (int s = 4; s < 32; s <<= 1) any |= __shfl_xor_sync(0xffffffffu, any, s);
-                const int g4 = lane >> 2;  // rk0 = 4 (g4 / 2) + g4 % 2, rk1 = rk0 + 2
-                any = __shfl_sync(0xffffffffu, any, g4 >> 1) >> (8 * (g4 & 1));
-                if (sv0 == 1.f && (any & 0xffu) == 0u) sv0 = 0.f;
-                if (sv1 == 1.f && (any & 0xff0000u) == 0u) sv1 = 0.f;
-            }
-#pragma unroll
-            for (int s = 4; s < 32; s <<= 1) {
-                l0 = fmaxf(l0, __shfl_xor_sync(0xffffffffu, l0, s));
-                l1 = fmaxf(l1, __shfl_xor_sync(0xffffffffu, l1, s));
-            }
-            const float top[2] = {l0, l1};
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                if (top[e] > m[e] + 8.f) {  // (-inf: nothing before)
-                    const float f = m[e] == -INFINITY ? 0.f : fast_exp2(m[e] - top[e]);
-                    l[e] *= f;
-                    ref[e] *= f;
-                    m[e] = top[e];
-                }
-            weigh();
-            float most[2] = {fmaxf(p[0] * sv0, p[2] * sv1), fmaxf(p[1] * sv0, p[3] * sv1)};
-            float f[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                for (int s = 4; s < 32; s <<= 1) most[e] = fmaxf(most[e], __shfl_xor_sync(0xffffffffu, most[e], s));
-                const float r = fmaxf(most[e] > ref[e] * 16.f ? most[e] : ref[e], kLeast);
-                f[e] = ref[e] / r;
-                ref[e] = r;
-                rinv[e] = 1.f / r;
-            }
-            scale16 = 16.f * fminf(ref[0], ref[1]);
-#pragma unroll
-            for (int i = 0; i < kN; ++i) {
-                o[i][0] *= f[0];
-                o[i][1] *= f[1];
-                o[i][2] *= f[0];
-                o[i][3] *= f[1];
-            }
-        } else {
-            weigh();
-        }
-        l[0] += p[0] + p[2];
-        l[1] += p[1] + p[3];
-        w[0] = p[0] * sv0 * rinv[0];
-        w[1] = p[1] * sv0 * rinv[1];
-        w[2] = p[2] * sv1 * rinv[0];
-        w[3] = p[3] * sv1 * rinv[1];
-    }
-};
-
-template <int kMode>
+template <bool kWin>
 struct PieceIter {
     const int* P;  // P[b]: first stream tile of sequence b (P[batch] = total)
     int batch, hh_count, per, r, r1, b, seg;
@@ -361,14 +248,11 @@ struct PieceIter {
             }
         }
         pc.len = a.seq_lens[pc.b];
-        if constexpr (kMode == kWindow) {
+        if constexpr (kWin) {
             const Window w = window_of(pc.len, a);
             pc.sink_tiles = w.sink_tiles;
             pc.gap = w.gap;
             pc.low = w.low;
-        } else if constexpr (kMode == kOwn) {
-            pc.sink_tiles = 0;
-            pc.gap = a.prefix[pc.b].tokens / kTile;
         }
         return true;
     }
@@ -379,14 +263,13 @@ __device__ __forceinline__ bool len_ok(int L, const DecodeArgs& a)
     return L >= 0 && L <= a.max_seq_len && (int64_t)L <= (int64_t)a.max_blocks * a.block_size;
 }
 
-template <bool kBF16, int kD, int kGT, bool kMma, bool kRowBoxes, bool kFP8, int kMode>
+template <bool kBF16, int kD, int kGT, bool kMma, bool kRowBoxes, bool kFP8, bool kWin>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_split_kernel(const __grid_constant__ DecodeArgs a,
                                                                 const __grid_constant__ PageMaps maps,
                                                                 const int stages)
 {
     pdl_wait();
     using T = Traits<kBF16, kD, kGT>;
-    constexpr bool kWin = kMode == kWindow;
     static_assert(!kMma || (kBF16 && kD == 128 && kGT <= 8), "tensor-core path: bf16, D = 128, <= 8 heads");
     static_assert(!kFP8 || (kMma && !kRowBoxes), "fp8 cache: tensor-core path on 16-row pages");
     constexpr int kStageB = stage_bytes<kBF16, kD, kGT, kFP8>();
@@ -411,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_sp
     for (int b = tid; b < a.batch; b += kThreads) {
         const int L = a.seq_lens[b];
         int nt = 0;
-        if (len_ok(L, a)) nt = kWin ? window_of(L, a).tiles : (L + kTile - 1) / kTile - (kMode == kOwn ? a.prefix[b].tokens / kTile : 0);
+        if (len_ok(L, a)) nt = kWin ? window_of(L, a).tiles : (L + kTile - 1) / kTile;
         else if (blockIdx.x == 0) record_error(a.status, KVATTN_ERR_BAD_INDEX);
         prefix[b + 1] = nt;
     }
@@ -451,26 +334,22 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_sp
 
     // token of a seen tile's first key
     auto first_token = [](const Piece& pc, int t) {
-        return (kMode != kWhole && t >= pc.sink_tiles ? t + pc.gap : t) * kTile;
+        return (kWin && t >= pc.sink_tiles ? t + pc.gap : t) * kTile;
     };
 
     // ---- sequences with no keys (or an invalid length): zero output
     for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
         if (prefix[b + 1] != prefix[b]) continue;
-        if constexpr (kMode == kOwn) {  // none of its own: no piece
-            for (int h = tid; h < HH; h += kThreads) a.nslots[(int64_t)b * HH + h] = 0;
-        } else {
-            for (int e = tid; e < a.hq * kD; e += kThreads) {
-                const int64_t o = (int64_t)b * a.hq * kD + e;
-                if constexpr (kBF16) reinterpret_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(0.f);
-                else reinterpret_cast<float*>(a.out)[o] = 0.f;
-            }
-            if (a.nslots)
-                for (int h = tid; h < HH; h += kThreads) a.nslots[(int64_t)b * HH + h] = 1;
+        for (int e = tid; e < a.hq * kD; e += kThreads) {
+            const int64_t o = (int64_t)b * a.hq * kD + e;
+            if constexpr (kBF16) reinterpret_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(0.f);
+            else reinterpret_cast<float*>(a.out)[o] = 0.f;
         }
+        if (a.nslots)
+            for (int h = tid; h < HH; h += kThreads) a.nslots[(int64_t)b * HH + h] = 1;
     }
 
-    PieceIter<kMode> iter;
+    PieceIter<kWin> iter;
     iter.P = prefix;
     iter.batch = a.batch;
     iter.hh_count = HH;
@@ -608,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_sp
         // slot): the piece's result goes to out, or to its partial slot.
         auto merge_pass = [&](int h0) {
             asm volatile("bar.sync 1, %0;" ::"n"(kConsumerWarps * 32) : "memory");
-            const bool direct = kMode != kOwn && pc.nslots == 1;
+            const bool direct = pc.nslots == 1;
             if (h0 == 0 && tid == 0 && pc.slot == 0 && a.nslots) a.nslots[(int64_t)pc.b * HH + pc.hh] = pc.nslots;
             for (int e = tid; e < kMG * kD; e += kConsumerWarps * 32) {
                 const int g = e / kD, d = e - g * kD;
@@ -681,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_sp
             for (int m = 0; m < kD / 16; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
             float m_run[2] = {-INFINITY, -INFINITY}, lrun[2] = {0.f, 0.f};  // heads 2q4, 2q4 + 1
             float vref = 0.f, vinv = 0.f;
-            Fp8Softmax win;  // windowed form and own keys: in the place of these four
+            Fp8Softmax win;  // windowed form: in the place of these four
             win.init();
             const float sl2 = a.scale_log2 * 16.f;  // undoes the 2^-4 on Q
             for (int li = 0; li < ntiles; ++li) {
@@ -732,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_sp
                         if (!sees(4 * q4 + j)) vmask &= ~(0xffu << (8 * j));
                 }
                 float w[4];  // weight * V scale over a reference
-                if constexpr (kMode != kWhole) {
+                if constexpr (kWin) {
                     win.step(x, sv0, sv1, lane, [&](int i) {
                         return *reinterpret_cast<const uint32_t*>(pg + kF8VOff + g4 * 16 + 4 * q4 + i * 128) & vmask;
                     }, o, w);
@@ -806,13 +685,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_sp
                 if (lane == 0) mbar_arrive(&empty[stage]);
             }
             pos += ntiles;
-            if constexpr (kMode != kWhole) {
+            if constexpr (kWin) {
                 m_run[0] = win.m[0];
                 m_run[1] = win.m[1];
                 lrun[0] = win.l[0];
                 lrun[1] = win.l[1];
             }
-            const float unit[2] = {kMode != kWhole ? win.ref[0] : vref, kMode != kWhole ? win.ref[1] : vref};  // of o
+            const float unit[2] = {kWin ? win.ref[0] : vref, kWin ? win.ref[1] : vref};  // of o
 #pragma unroll
             for (int sh = 4; sh < 32; sh <<= 1) {
                 lrun[0] += __shfl_xor_sync(0xffffffffu, lrun[0], sh);
@@ -1194,77 +1073,7 @@ __global__ void __launch_bounds__(128) decode_combine_kernel(const __grid_consta
     }
 }
 
-// Merges a row's partial results over the shared prefix (decode_shared.cu: sums
-// not divided yet) and over its own keys.  A warp per (sequence, query head): a
-// lane weighs a piece, then all lanes add up the pieces, kD / 32 dims each.
-template <int kD>
-__global__ void __launch_bounds__(128) decode_shared_combine_kernel(const __grid_constant__ DecodeArgs a, const int gt)
-{
-    pdl_wait();
-    const int wid = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (wid >= a.batch * a.hq) return;
-    const int b = wid / a.hq, qh = wid - b * a.hq;
-    const int G = a.hq / a.hkv, nsub = G / gt;
-    const PrefixOf p = a.prefix[b];
-    const int ns = a.nslots[(int64_t)b * a.hkv * nsub + (qh / G) * nsub + (qh % G) / gt];
-    int np = 0;
-    int64_t first = 0;  // row of the first prefix piece
-    if (p.tokens > 0) {
-        const int h = qh / G, t0 = p.first + h * p.head_tiles, c0 = t0 / p.per;
-        np = (t0 + p.tiles - 1) / p.per - c0 + 1;
-        first = (int64_t)(c0 + p.segment + h * p.head_segments) * kPrefixRows + p.row + qh % G;
-    }
-    const float* own_ml = a.part_ml + (int64_t)wid * a.splits * 2;
-    const float* own_o = a.part_o + (int64_t)wid * a.splits * kD;
-    constexpr int kDL = kD / 32;
-    float acc[kDL] = {}, den = 0.f, top = -INFINITY;
-    for (int c0 = 0; c0 < np + ns; c0 += 32) {
-        const int c = c0 + lane, n = min(32, np + ns - c0);
-        float2 ml = make_float2(-INFINITY, 0.f);
-        if (c < np) ml = *reinterpret_cast<const float2*>(a.prefix_ml + (first + (int64_t)c * kPrefixRows) * 2);
-        else if (c < np + ns) ml = *reinterpret_cast<const float2*>(own_ml + 2 * (c - np));
-        float M = ml.y == 0.f ? -INFINITY : ml.x;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        if (M > top) {
-            const float f = top == -INFINITY ? 0.f : exp2f(top - M);
-            den *= f;
-#pragma unroll
-            for (int i = 0; i < kDL; ++i) acc[i] *= f;
-            top = M;
-        }
-        // (a piece's sum is 0 without a key, NaN with NaN scores)
-        const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - top);
-        const float w = c < np ? f : f * ml.y;
-        float s = f * ml.y;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        den += s;
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const float wi = __shfl_sync(0xffffffffu, w, i);
-            const float* o = c0 + i < np ? a.prefix_o + (first + (int64_t)(c0 + i) * kPrefixRows) * kD
-                                         : own_o + (int64_t)(c0 + i - np) * kD;
-            if constexpr (kDL == 4) {
-                const float4 x = *reinterpret_cast<const float4*>(o + 4 * lane);
-                acc[0] += wi * x.x;
-                acc[1] += wi * x.y;
-                acc[2] += wi * x.z;
-                acc[3] += wi * x.w;
-            } else {
-                const float2 x = *reinterpret_cast<const float2*>(o + 2 * lane);
-                acc[0] += wi * x.x;
-                acc[1] += wi * x.y;
-            }
-        }
-    }
-    const float inv = den == 0.f ? 0.f : 1.f / den;
-    uint32_t* out = reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(a.out) + (int64_t)wid * kD + kDL * lane);
-#pragma unroll
-    for (int i = 0; i < kDL / 2; ++i) out[i] = pack_bf16_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-}
-
-template <bool kBF16, int kD, int kGT, bool kMma, bool kRowBoxes = false, bool kFP8 = false, int kMode = kWhole>
+template <bool kBF16, int kD, int kGT, bool kMma, bool kRowBoxes = false, bool kFP8 = false, bool kWin = false>
 kvattn_status run(const DecodeArgs& a, cudaStream_t s)
 {
     constexpr int kStageB = stage_bytes<kBF16, kD, kGT, kFP8>();
@@ -1290,7 +1099,7 @@ kvattn_status run(const DecodeArgs& a, cudaStream_t s)
     stages = std::max(kConsumerWarps, stages / kConsumerWarps * kConsumerWarps);
     const SharedLayout SL = shared_layout<kBF16, kD, kGT, kFP8>(stages, a.batch);
     const int smem_bytes = SL.bytes + 1024;
-    auto kern = decode_split_kernel<kBF16, kD, kGT, kMma, kRowBoxes, kFP8, kMode>;
+    auto kern = decode_split_kernel<kBF16, kD, kGT, kMma, kRowBoxes, kFP8, kWin>;
     static Residency residency;
     int per_sm = 0;
     if (residency.query(reinterpret_cast<const void*>(kern), kThreads, smem_bytes, &per_sm) != cudaSuccess)
@@ -1298,18 +1107,14 @@ kvattn_status run(const DecodeArgs& a, cudaStream_t s)
     const int grid = num_sms() * per_sm;
     cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kThreads), smem_bytes, s, a, maps, stages);
     if (e != cudaSuccess) return KVATTN_ERR_CUDA;
-    if constexpr (kMode == kOwn) {
-        static_assert(kBF16, "prefixes are shared over bf16 queries");
-        const int warps = a.batch * a.hq;
-        e = launch_pdl(decode_shared_combine_kernel<kD>, dim3((warps + 3) / 4), dim3(128), 0, s, a, kGT);
-    } else if (a.splits > 1) {
+    if (a.splits > 1) {
         const int warps = a.batch * a.hq;
         e = launch_pdl(decode_combine_kernel<kBF16, kD>, dim3((warps + 3) / 4), dim3(128), 0, s, a, kGT);
     }
     return cuda_status(e);
 }
 
-template <int kMode>
+template <bool kWin>
 kvattn_status dispatch(const DecodeArgs& a, cudaStream_t s)
 {
     const int G = a.hq / a.hkv;
@@ -1317,36 +1122,31 @@ kvattn_status dispatch(const DecodeArgs& a, cudaStream_t s)
     const int gt = G >= 4 ? 4 : G;
     if (a.fp8) {  // fp8 pages: the tensor-core path, every head of the group in one segment
         if (!(bf16 && a.d == 128 && (G == 4 || G == 8) && a.block_size % 16 == 0)) return KVATTN_ERR_UNSUPPORTED;
-        return G == 8 ? run<true, 128, 8, true, false, true, kMode>(a, s) : run<true, 128, 4, true, false, true, kMode>(a, s);
+        return G == 8 ? run<true, 128, 8, true, false, true, kWin>(a, s) : run<true, 128, 4, true, false, true, kWin>(a, s);
     }
     // bf16, D = 128, groups of 4 or 8 query heads per KV head: QK and PV on the
     // tensor cores with the group's heads as rows 0..G-1 of the MMA fragments,
     // so every page is read once per KV head (tensor-map row coordinates are
     // 32-bit)
     if (bf16 && a.d == 128 && (G == 4 || G == 8) && a.num_blocks * a.hkv * a.block_size < ((int64_t)1 << 31)) {
-        if constexpr (kMode == kOwn)  // (prefixes are shared in blocks of whole pages only)
-            return G == 8 ? run<true, 128, 8, true, false, false, kMode>(a, s) : run<true, 128, 4, true, false, false, kMode>(a, s);
-        else if (G == 8)
-            return a.block_size % 16 == 0 ? run<true, 128, 8, true, false, false, kMode>(a, s) : run<true, 128, 8, true, true, false, kMode>(a, s);
-        else return a.block_size % 16 == 0 ? run<true, 128, 4, true, false, false, kMode>(a, s) : run<true, 128, 4, true, true, false, kMode>(a, s);
+        if (G == 8)
+            return a.block_size % 16 == 0 ? run<true, 128, 8, true, false, false, kWin>(a, s) : run<true, 128, 8, true, true, false, kWin>(a, s);
+        return a.block_size % 16 == 0 ? run<true, 128, 4, true, false, false, kWin>(a, s) : run<true, 128, 4, true, true, false, kWin>(a, s);
     }
 #define KVATTN_DECODE_CASE(BF, DD, GG) \
-    if (bf16 == BF && a.d == DD && gt == GG) return run<BF, DD, GG, false, false, false, kMode>(a, s);
+    if (bf16 == BF && a.d == DD && gt == GG) return run<BF, DD, GG, false, false, false, kWin>(a, s);
     KVATTN_DECODE_CASE(true, 128, 1)
     KVATTN_DECODE_CASE(true, 128, 2)
     KVATTN_DECODE_CASE(true, 128, 4)
     KVATTN_DECODE_CASE(true, 64, 1)
     KVATTN_DECODE_CASE(true, 64, 2)
     KVATTN_DECODE_CASE(true, 64, 4)
-    if constexpr (kMode == kOwn) return KVATTN_ERR_UNSUPPORTED;  // fp32 caches have no shared form
-    else {
     KVATTN_DECODE_CASE(false, 128, 1)
     KVATTN_DECODE_CASE(false, 128, 2)
     KVATTN_DECODE_CASE(false, 128, 4)
     KVATTN_DECODE_CASE(false, 64, 1)
     KVATTN_DECODE_CASE(false, 64, 2)
     KVATTN_DECODE_CASE(false, 64, 4)
-    }
 #undef KVATTN_DECODE_CASE
     return KVATTN_ERR_UNSUPPORTED;
 }

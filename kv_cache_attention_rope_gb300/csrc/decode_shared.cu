@@ -1,39 +1,51 @@
-// Decode attention over the prefixes that groups of sequences share, on the
-// tcgen05 tensor cores: a prefix is read once for all the queries of its group.
+// Decode attention for a batch in which groups of sequences share their first
+// tokens: a prefix is read once for all the queries of its group.
 //
-// What it computes: for a group of sequences whose first S tokens are the same
-// (S rounded down to whole 16-token pages), and every query head j of every
-// sequence b of it, the partial softmax state
-//     m = max_{i < S} s_i,  l = sum_i 2^(s_i - m),  O = sum_i 2^(s_i - m) V[i],
+// What it computes: kvattn_decode's out[b][j], an online softmax over every key of
+// sequence b ("From-scratch AI inference engine" page, section 3.3: a query sees
+// all cached keys), as the merge of partial states
+//     m = max_i s_i,  l = sum_i 2^(s_i - m),  O = sum_i 2^(s_i - m) V[i],
 //     s_i = q[b][j] . K[i][j / G] * scale * log2(e)
-// in pieces over ranges of keys ("From-scratch AI inference engine" page, section
-// 3.4: states over parts of the keys merge by their maxima and sums;
-// "Nano-vLLM Part 2" page, section 05: sequences with a common prefix share its
-// blocks).  decode_own.cu then does each sequence's other keys and the merge.
+// over pieces of the prefix that b's group shares and of its own keys behind it
+// (section 3.4 of the same page: states over parts of the keys merge by their
+// maxima and sums; "Nano-vLLM Part 2" page, section 05: sequences with a common
+// prefix share its blocks).  Only whole 16-token pages of a prefix are shared, and a
+// sequence that is shorter takes no part, so no row has a mask of its own.
 //
-// What bounds it.  A KV head's queries are (sequences of the group) x G rows of one
-// matrix product, so the prefix's K and V are read once, 4 D e bytes a key and KV
-// head, for 4 D FLOPs a key and row: up to about 128 rows HBM has the longer
-// part, from 256 rows on the tensor cores and the softmax beside them.
+// What bounds it.  A KV head's queries over a prefix are (sequences of the group) x
+// G rows of one matrix product, so the prefix's K and V are read once, 4 D e bytes a
+// key and KV head, for 4 D FLOPs a key and row: up to about 128 rows HBM has the
+// longer part, from 256 rows on the tensor cores and the softmax beside them.  Own
+// keys have G rows and are HBM's.
 //
-// How.  Rows come in blocks of 256 / G sequences.  The (row block, KV head) segments'
-// tiles of 128 keys form one stream that is cut into equal ranges, one per SM
-// (persistent CTAs), segments being cut where ranges meet.  A piece of more than
-// 128 rows works on two row tiles A and B in turn over the same K and V tiles;
-// one of up to 128 rows has A and B over the even and the odd key tiles, with states of
-// their own that the output warps merge.  Either way the softmax of one runs beside the
-// products of the other.  A row sees every key of the prefix (shorter sequences
-// take no part), so only a prefix's last tile is masked, beyond its whole pages.
+// How.  One launch, a CTA per SM, some of them on prefixes and the others on own
+// keys, as many of each as make both end together; decode_shared_merge_kernel then
+// merges a row's pieces.
 //
-// Roles (four warpgroups): warp 0 copies K and Q tiles, warp 2 V tiles (a page a
-// lane, straight from the block table); warp 1 issues the MMAs in the order PV_A(t)
-// S_A(t+1) PV_B(t) S_B(t+1), from piece to piece without a gap; warps 4-11 the
-// softmax (columns 0-63 and 64-127), P overwriting the first half of S in
-// TMEM; warps 12-15 the outputs.  TMEM: S_A, S_B, O_A, O_B, 128 columns each.
+// Prefixes (prefix_cta): rows come in blocks of 256 / G sequences.  The pages of all
+// (row block, KV head) segments form one stream, cut into equal ranges, one per CTA,
+// segments being cut where ranges meet.  A piece is worked on in tiles of up to 8
+// pages on the tcgen05 tensor cores.  One of more than 128 rows has two row tiles by
+// turns over the same K and V tiles; any other has one.  Either way the steps (S, softmax,
+// P.V) alternate between two S buffers, so that the softmax of one runs beside the products
+// of the other; a piece of one row tile has one of the two O buffers, the next
+// piece the other.  Roles (four warpgroups): warp 0 copies K and Q tiles, warp 2 V
+// tiles (a page a lane, straight from the block table); warp 1 issues the MMAs, P.V
+// of a step and then S of the second one after it, from piece to piece without a gap;
+// warps 4-11 the softmax (columns 0-63 and 64-127), P overwriting the first half
+// of S in TMEM; warps 12-15 the outputs.  TMEM: S_0, S_1, O_0, O_1, 128 columns each.
+//
+// Own keys (own_warp): the pages of all (sequence, KV head) segments form a stream
+// too, cut into equal ranges, one per warp.  A warp brings its pages into a ring of its
+// own by TMA, multiplies them with mma.sync (the group's heads as rows 0..7 of the
+// fragments) and writes a state where a segment ends: no warp waits for another,
+// and nothing is paid per segment but its state.
+//
 // Every wait on a barrier is bounded: a timeout records KVATTN_ERR_TIMEOUT, the
 // roles stop waiting, drain their copies and MMAs, free TMEM and return.
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <cstring>
 
 #include "tc_roles.cuh"
@@ -48,38 +60,45 @@ constexpr int kPages = kBN / kPage;
 constexpr int kThreads = 512;
 constexpr int kStages = 2;     // of K, of V and of Q tiles
 constexpr int kPanel = kBM * 128;  // 16 KB: 128 rows x 64 columns (one 128-byte swizzle panel of Q)
-constexpr int kMinPer = 2;     // fewest tiles of a CTA's range
-static_assert(kPrefixRows == 2 * kBM, "a piece's rows");
-static_assert(kMaxGroups <= kThreads, "a thread per group");
+constexpr int kMinPer = 8;     // fewest shared pages of a CTA's range
+constexpr int kMinOwn = 2;     // fewest own pages of a warp's range
+constexpr int kPast = 4;       // pieces whose sums may be waiting for the output warps
+constexpr int kSeqs = kMaxSharedBatch / kThreads;  // sequences a thread plans
+static_assert(kSharedRows == 2 * kBM, "a prefix piece's rows");
+static_assert(kMaxGroups <= kThreads && kMaxSharedBatch % kThreads == 0, "a thread per group");
 // Registers per thread of the warpgroups (the block starts with 128 each:
 // 96 + 2 x 168 + 80 = 4 x 128).
 constexpr int kRegsIssue = 96, kRegsSoftmax = 168, kRegsOutput = 80;
 
-// Barriers, in shared memory.
+// Barriers of a CTA on prefixes.
 struct Bars {
     uint64_t q_full[kStages], q_empty[kStages];  // of a Q tile: loaded; every S MMA that reads it is done
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
     uint64_t s_full[2], p_full[2];
-    uint64_t o_done[2], o_free[2];   // the piece's last P.V into O_x has completed; O_x has been read
-    uint64_t l_full[2];              // maxima and row sums of the even and of the odd pieces
+    uint64_t o_done[2], o_free[2];   // the piece's last P.V into O_z has completed; O_z has been read
+    uint64_t l_full[kPast];          // maxima and row sums of a piece
     uint64_t drain;
     uint32_t tmem;
     int abort_flag;
 };
+static_assert(sizeof(Bars) <= 256, "the barriers fit before the exchange area");
 
-// The groups of the call, and the stream of their tiles (group g: tiles first[g] ..
-// first[g+1] - 1, segments segment[g] .., KV heads outermost, then row blocks).
-struct Groups {
+// The call's groups and sequences, and the streams of pages: group g's shared ones are
+// first[g] .. first[g+1] - 1 (its segments segment[g] ..: KV heads outermost, then
+// row blocks), sequence b's own Hkv own[b] .. Hkv own[b+1] - 1.
+struct Plan {
     int cu[kMaxGroups + 1];
     int tokens[kMaxGroups];   // shared, whole pages; 0: shares nothing
     int leader[kMaxGroups];   // a sequence of the group that has them
     int members[kMaxGroups];  // how many have them
     int first[kMaxGroups + 1], segment[kMaxGroups + 1];
-    int sums[2][kThreads / 32];
+    int own[kMaxSharedBatch + 1];
+    int sums[3][kThreads / 32];
 };
 
 template <int kD>
 struct Geo {
+    // prefixes
     static constexpr int kPanels = kD / 64;
     static constexpr int kTileBytes = kBM * kD * 2;    // a Q tile, a K stage or a V stage
     static constexpr int kGroup = 8 * kD * 2;          // one 8-key group of a stage (all panels)
@@ -88,13 +107,19 @@ struct Geo {
     static constexpr int kOffK = kStages * kTileBytes;
     static constexpr int kOffV = kOffK + kStages * kTileBytes;
     static constexpr int kOffBar = kOffV + kStages * kTileBytes;
-    // fp32: row maxima of a tile [2][2 halves][128]; of two pieces, row sums [2][2 halves][2][128] and maxima [2][2][128]
+    // fp32: row maxima of a tile [2][2 halves][128]; of kPast pieces, row sums [2 halves][2][128] and maxima [2][128]
     static constexpr int kOffX = kOffBar + 256;
-    static constexpr int kOffGroups = kOffX + 8192;
-    static constexpr int kSmemBytes = kOffGroups + (int)sizeof(Groups) + 1024;  // + slack to align the base to 1 KB
+    static constexpr int kPrefixEnd = kOffX + 2048 + kPast * 3072;
+    // own keys: every warp's ring, then its barriers
+    static constexpr int kOwnWarps = kD == 128 ? 12 : 16;
+    static constexpr int kOwnRing = kD == 128 ? 2 : 3;
+    static constexpr int kOffOwnBar = kOwnWarps * kOwnRing * 2 * kPageBytes;
+    static constexpr int kOwnEnd = kOffOwnBar + kOwnWarps * kOwnRing * 8;
+    static constexpr int kOffPlan = (kPrefixEnd > kOwnEnd ? kPrefixEnd : kOwnEnd);
+    static constexpr int kSmemBytes = kOffPlan + (int)sizeof(Plan) + 1024;  // + slack to align the base to 1 KB
     static_assert(kD == 64 || kD == 128, "head dim");
+    static_assert(kOwnWarps <= kMostOwnWarps && kOwnWarps <= kThreads / 32, "own warps");
 };
-static_assert(sizeof(Bars) <= 256, "the barriers fit before the exchange area");
 
 struct Maps {
     CUtensorMap q;  // 3-D: (D, Hq, batch), box (64, G, 128 / G)
@@ -102,135 +127,194 @@ struct Maps {
     CUtensorMap v;
 };
 
-// A piece: tiles t0 .. t1 - 1 of the `tokens` keys of the row `leader` of the table,
-// for KV head h and `rows` rows: head r % G of sequence b0 + r / G.
-struct Piece {
-    int b0, rows, h, t0, t1, tokens, leader, id;
-    __device__ __forceinline__ bool two() const { return rows > kBM; }
-    // A's and B's tiles: the x-th's t-th is key tile t0 + (two ? t : 2 t + x)
-    __device__ __forceinline__ int tiles(int x) const { return two() ? t1 - t0 : (t1 - t0 + 1 - x) >> 1; }
-};
-
-__device__ __forceinline__ bool len_ok(int L, const DecodeArgs& a)
+template <int kHD>
+__device__ __forceinline__ void copy_page(void* dst, const CUtensorMap* m, int row, uint64_t* full, uint64_t policy)
 {
-    return L >= 0 && L <= a.max_seq_len && (int64_t)L <= (int64_t)a.max_blocks * a.block_size;
+    if constexpr (kHD == 128) tma_load_4d(dst, m, 0, 0, 0, row >> 3, full, policy);
+    else tma_load_2d(dst, m, 0, row, full, policy);
 }
 
-// Fills G from the call's arguments; every CTA does.  Groups that are out of order
-// or out of range share nothing, nor does a group of which fewer than two sequences
-// have the prefix.
-__device__ __forceinline__ void plan_groups(const DecodeArgs& a, Groups& G, int lg)
+__device__ __forceinline__ int blocks_of(int seqs, int lg) { return ((seqs << lg) + kSharedRows - 1) / kSharedRows; }
+
+// The last group g of n with cu[g] <= b: the one b is in.
+__device__ __forceinline__ int group_of(const Plan& P, int n, int b)
+{
+    int g = 0;
+    for (int m = n; m > 1;) {
+        const int half = m >> 1;
+        if (P.cu[g + half] <= b) g += half;
+        m -= half;
+    }
+    return g;
+}
+
+// Fills the plan from the call's arguments (every CTA does).  Groups that are out of
+// order or out of range share nothing, nor does a group of which fewer than two
+// sequences have the prefix.
+__device__ __forceinline__ void make_plan(const SharedArgs& a, Plan& P, int lg)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.num_groups;
+    const int64_t room = (int64_t)a.d.max_blocks * a.d.block_size;
+    int len[kSeqs];
+#pragma unroll
+    for (int j = 0; j < kSeqs; ++j) {
+        const int b = j * kThreads + tid;
+        len[j] = b < a.d.batch ? a.d.seq_lens[b] : 0;
+    }
     bool ok = true;
     if (tid < n) {
         const int c0 = a.cu_groups[tid], c1 = a.cu_groups[tid + 1], s = a.shared_lens[tid];
-        ok = c0 >= 0 && c1 >= c0 && c1 <= a.batch && s >= 0 && s <= a.max_shared && (tid > 0 || c0 == 0) &&
-             (int64_t)s <= (int64_t)a.max_blocks * a.block_size;
-        G.cu[tid] = c0;
-        if (tid == n - 1) G.cu[n] = c1;
-        G.tokens[tid] = s & ~(kPage - 1);
-        G.leader[tid] = INT_MAX;
-        G.members[tid] = 0;
+        ok = c0 >= 0 && c1 >= c0 && c1 <= a.d.batch && s >= 0 && s <= a.max_shared && (tid > 0 || c0 == 0) && s <= room;
+        P.cu[tid] = c0;
+        if (tid == n - 1) P.cu[n] = c1;
+        P.tokens[tid] = s & ~(kPage - 1);
+        P.leader[tid] = INT_MAX;
+        P.members[tid] = 0;
+    }
+#pragma unroll
+    for (int j = 0; j < kSeqs; ++j) {
+        if (len[j] < 0 || len[j] > a.d.max_seq_len || len[j] > room) {
+            if (blockIdx.x == 0) record_error(a.d.status, KVATTN_ERR_BAD_INDEX);
+            len[j] = 0;
+        }
     }
     ok = __syncthreads_and(ok);
-    if (!ok && blockIdx.x == 0 && tid == 0) record_error(a.status, KVATTN_ERR_BAD_INDEX);
-    if (ok) {
-        for (int b = tid; b < G.cu[n]; b += kThreads) {
-            int g = 0;  // the last group with cu[g] <= b: the one b is in
-            for (int m = n; m > 1;) {
-                const int half = m >> 1;
-                if (G.cu[g + half] <= b) g += half;
-                m -= half;
-            }
-            const int L = a.seq_lens[b];
-            if (len_ok(L, a) && L >= G.tokens[g]) {
-                atomicMin(&G.leader[g], b);
-                atomicAdd(&G.members[g], 1);
-            }
-        }
-    }
-    __syncthreads();
-    int tiles = 0, segs = 0;
-    if (tid < n) {
-        if (!ok || G.members[tid] < 2) G.tokens[tid] = 0;
-        if (G.tokens[tid] > 0) {
-            const int seqs = G.cu[tid + 1] - G.cu[tid];
-            segs = (((seqs << lg) + kPrefixRows - 1) / kPrefixRows) * a.hkv;
-            tiles = segs * ((G.tokens[tid] + kBN - 1) / kBN);
-        }
-    }
-    int ti = tiles, si = segs;  // up to this lane's
+    if (!ok && blockIdx.x == 0 && tid == 0) record_error(a.d.status, KVATTN_ERR_BAD_INDEX);
+    int group[kSeqs];  // -1: none
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, ti, o), y = __shfl_up_sync(0xffffffffu, si, o);
-        if (lane >= o) {
-            ti += x;
-            si += y;
+    for (int j = 0; j < kSeqs; ++j) {
+        const int b = j * kThreads + tid;
+        group[j] = ok && b < P.cu[n] ? group_of(P, n, b) : -1;
+        if (group[j] >= 0 && P.tokens[group[j]] > 0 && len[j] >= P.tokens[group[j]]) {
+            atomicMin(&P.leader[group[j]], b);
+            atomicAdd(&P.members[group[j]], 1);
+        } else {
+            group[j] = -1;
         }
     }
-    if (lane == 31) {
-        G.sums[0][warp] = ti;
-        G.sums[1][warp] = si;
+    __syncthreads();
+    int v[3] = {0, 0, 0};  // pages of a group, its segments; own pages of this thread's next kSeqs sequences
+    if (tid < n) {
+        if (!ok || P.members[tid] < 2) P.tokens[tid] = 0;
+        if (P.tokens[tid] > 0) {
+            v[1] = blocks_of(P.cu[tid + 1] - P.cu[tid], lg) * a.d.hkv;
+            v[0] = v[1] * (P.tokens[tid] / kPage);
+        }
     }
     __syncthreads();
-    for (int w = 0; w < warp; ++w) {
-        ti += G.sums[0][w];
-        si += G.sums[1][w];
+    // own pages, for a moment in the places of the sums
+#pragma unroll
+    for (int j = 0; j < kSeqs; ++j) {
+        const int b = j * kThreads + tid;
+        if (b < a.d.batch) P.own[b + 1] = (len[j] + kPage - 1) / kPage - (group[j] >= 0 ? P.tokens[group[j]] / kPage : 0);
     }
+    __syncthreads();
+    int own[kSeqs];
+#pragma unroll
+    for (int j = 0; j < kSeqs; ++j) {
+        const int b = tid * kSeqs + j;
+        own[j] = v[2] += b < a.d.batch ? P.own[b + 1] : 0;
+    }
+    const int mine = v[2];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const int x = __shfl_up_sync(0xffffffffu, v[i], o);
+            if (lane >= o) v[i] += x;
+        }
+    if (lane == 31)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) P.sums[i][warp] = v[i];
+    __syncthreads();
+    for (int w = 0; w < warp; ++w)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) v[i] += P.sums[i][w];
     if (tid < n) {
-        G.first[tid + 1] = ti;
-        G.segment[tid + 1] = si;
+        P.first[tid + 1] = v[0];
+        P.segment[tid + 1] = v[1];
     }
-    if (tid == 0) G.first[0] = G.segment[0] = 0;
+#pragma unroll
+    for (int j = 0; j < kSeqs; ++j) {
+        const int b = tid * kSeqs + j;
+        if (b < a.d.batch) P.own[b + 1] = v[2] - mine + own[j];
+    }
+    if (tid == 0) P.first[0] = P.segment[0] = P.own[0] = 0;
     __syncthreads();
 }
 
-template <int kHD>
-__global__ void __launch_bounds__(kThreads, 1)
-    decode_prefix_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ Maps maps)
+// How many CTAs are on prefixes, and the pages of a CTA's and of an own warp's range.
+struct Ranges {
+    int ctas, per, own_per;
+};
+// Both kinds of CTA take about as long per page, and those on prefixes `more` pages'
+// time besides (tensor-core set-up, 256 rows of output): with t pages' time for all,
+// shared / (t - more) + own / t = ctas.
+__device__ __forceinline__ Ranges ranges_of(int shared, int own, int ctas, float more, int warps)
 {
-    pdl_wait();
+    Ranges r{0, 0, 0};
+    if (shared > 0) {
+        const float c = (float)ctas, p = (float)shared, o = (float)own, u = more * c + p + o;
+        const float t = (u + sqrtf(fmaxf(u * u - 4.f * c * more * o, 0.f))) / (2.f * c);
+        r.ctas = min((int)ceilf(p / fmaxf(t - more, 1.f)), (shared + kMinPer - 1) / kMinPer);
+        r.ctas = max(1, min(r.ctas, own > 0 ? ctas - 1 : ctas));
+        r.per = (shared + r.ctas - 1) / r.ctas;
+    }
+    if (own > 0) {
+        const int n = (ctas - r.ctas) * warps;
+        r.own_per = max((own + n - 1) / n, kMinOwn);
+    }
+    return r;
+}
+
+// ---------------------------------------------------------------- prefixes
+
+// A piece: pages p0 .. p1 - 1 of row `row` of the table for KV head h and `rows`
+// rows: head r % G of sequence b0 + r / G.  Its results go to rows `out` ...
+struct Piece {
+    int row, b0, rows, h, p0, p1, out;
+    __device__ __forceinline__ bool two() const { return rows > kBM; }
+    __device__ __forceinline__ int tiles() const { return (p1 - p0 + kPages - 1) / kPages; }
+    // Steps of S, softmax and P.V: step j is of key tile tile(j), and of the first or second
+    // row tile by turns if there are two.
+    __device__ __forceinline__ int steps() const { return two() ? 2 * tiles() : tiles(); }
+    __device__ __forceinline__ int tile(int j) const { return two() ? j >> 1 : j; }
+    __device__ __forceinline__ int pages(int t) const { return min(kPages, p1 - p0 - t * kPages); }
+};
+
+// Walks the pieces of a CTA's range.
+struct Walk {
+    int r, end, g;
+    __device__ __forceinline__ bool next(const SharedArgs& a, const Plan& P, int lg, Piece& p)
+    {
+        if (r >= end) return false;
+        while (P.first[g + 1] <= r) ++g;
+        const int pages = P.tokens[g] / kPage, seqs = P.cu[g + 1] - P.cu[g], blocks = blocks_of(seqs, lg);
+        const int off = r - P.first[g], seg = off / pages;
+        p.p0 = off - seg * pages;
+        p.p1 = min(pages, p.p0 + end - r);
+        p.h = seg / blocks;
+        const int rb = seg - p.h * blocks;
+        p.row = P.leader[g];
+        p.b0 = P.cu[g] + rb * (kSharedRows >> lg);
+        p.rows = min(kSharedRows, (seqs << lg) - rb * kSharedRows);
+        p.out = ((int)blockIdx.x + P.segment[g] + seg) * kSharedRows;
+        r += p.p1 - p.p0;
+        return true;
+    }
+};
+
+template <int kHD>
+__device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps, const Plan& P, const Walk walk0, int lg,
+                                           unsigned char* smem)
+{
     using GE = Geo<kHD>;
     constexpr int kTileBytes = GE::kTileBytes, kPageBytes = GE::kPageBytes, kGroup = GE::kGroup;
     constexpr int kOffQ = GE::kOffQ, kOffK = GE::kOffK, kOffV = GE::kOffV;
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     Bars& B = *reinterpret_cast<Bars*>(smem + GE::kOffBar);
-    Groups& G = *reinterpret_cast<Groups*>(smem + GE::kOffGroups);
     volatile int* abort_flag = &B.abort_flag;
-
+    int* const status = a.d.status;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int lg = __ffs(a.hq / a.hkv) - 1;  // row r of a piece: sequence r >> lg, head r & (G - 1)
-    plan_groups(a, G, lg);
-    const int total = G.first[a.num_groups];
-    const int per = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kMinPer);
-    // where the merge finds each sequence's partial results
-    for (int b = (int)blockIdx.x * kThreads + threadIdx.x; b < a.batch; b += (int)gridDim.x * kThreads) {
-        PrefixOf p{0, 0, 0, 0, 0, 0, 0, per};
-        int g = 0;
-        for (int m = a.num_groups; m > 1;) {
-            const int half = m >> 1;
-            if (G.cu[g + half] <= b) g += half;
-            m -= half;
-        }
-        const int L = a.seq_lens[b];
-        if (total > 0 && b < G.cu[a.num_groups] && G.tokens[g] > 0 && len_ok(L, a) && L >= G.tokens[g]) {
-            const int seqs = G.cu[g + 1] - G.cu[g], blocks = ((seqs << lg) + kPrefixRows - 1) / kPrefixRows;
-            const int r = (b - G.cu[g]) << lg, rb = r / kPrefixRows;
-            p.tokens = G.tokens[g];
-            p.tiles = (p.tokens + kBN - 1) / kBN;
-            p.first = G.first[g] + rb * p.tiles;
-            p.head_tiles = blocks * p.tiles;
-            p.segment = G.segment[g] + rb;
-            p.head_segments = blocks;
-            p.row = r - rb * kPrefixRows;
-        }
-        a.prefix[b] = p;
-    }
-    const int r_begin = min(total, (int)blockIdx.x * per), r_end = min(total, r_begin + per);
-    if (r_begin >= r_end) return;
-
     if (threadIdx.x == 0) {
         for (int x = 0; x < 2; ++x) {
             mbar_init(&B.q_full[x], 1);
@@ -243,8 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&B.p_full[x], 256);
             mbar_init(&B.o_done[x], 1);
             mbar_init(&B.o_free[x], 128);
-            mbar_init(&B.l_full[x], 256);
         }
+        for (int x = 0; x < kPast; ++x) mbar_init(&B.l_full[x], 256);
         mbar_init(&B.drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -253,31 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = B.tmem;  // S_A at +0, S_B at +128, O_A at +256, O_B at +384
-
-    // Walks this CTA's pieces.
-    struct Walk {
-        int r, g;
-    };
-    const Walk walk0{r_begin, 0};
-    auto next_piece = [&](Walk& w, Piece& p) -> bool {
-        if (w.r >= r_end) return false;
-        while (G.first[w.g + 1] <= w.r) ++w.g;
-        p.tokens = G.tokens[w.g];
-        p.leader = G.leader[w.g];
-        const int tiles = (p.tokens + kBN - 1) / kBN, seqs = G.cu[w.g + 1] - G.cu[w.g];
-        const int blocks = ((seqs << lg) + kPrefixRows - 1) / kPrefixRows;
-        const int off = w.r - G.first[w.g], seg = off / tiles;
-        p.t0 = off - seg * tiles;
-        p.t1 = min(tiles, p.t0 + r_end - w.r);
-        p.h = seg / blocks;
-        const int rb = seg - p.h * blocks;
-        p.b0 = G.cu[w.g] + rb * (kPrefixRows >> lg);
-        p.rows = min(kPrefixRows, (seqs << lg) - rb * kPrefixRows);
-        p.id = (int)blockIdx.x + G.segment[w.g] + seg;
-        w.r += p.t1 - p.t0;
-        return true;
-    };
+    const uint32_t tmem = B.tmem;  // S_0 at +0, S_1 at +128, O_0 at +256, O_1 at +384
 
     if (warp < 4) {
         setmaxnreg_dec<kRegsIssue>();
@@ -293,57 +353,55 @@ __global__ void __launch_bounds__(kThreads, 1)
             // lane 0 waits for `empty` (unless the buffer is new) and arms `full`
             auto arm = [&](uint64_t* full, uint64_t* empty, int use, uint32_t bytes) -> bool {
                 if (lane == 0) {
-                    go = use == 0 ? !*abort_flag : wait_or_abort(empty, (use - 1) & 1, abort_flag, a.status);
+                    go = use == 0 ? !*abort_flag : wait_or_abort(empty, (use - 1) & 1, abort_flag, status);
                     if (go) mbar_arrive_expect_tx(full, bytes);
                 }
                 return go = __shfl_sync(0xffffffffu, go, 0);
             };
-            // Lane p < 8 copies page p of a tile; its block's id comes from the table a
+            // Lane i < 8 copies page i of a tile; its block's id comes from the table a
             // tile ahead (lanes without a page read their row's first entry).
-            auto has_page = [&](const Piece& p, int t) { return lane < kPages && t * kBN + lane * kPage < p.tokens; };
             auto block_id = [&](const Piece& p, int t) -> int32_t {
-                const int col = has_page(p, t) ? (t * kBN + lane * kPage) / a.block_size : 0;
-                return a.block_table[(int64_t)p.leader * a.max_blocks + col];
+                const int col = lane < p.pages(t) ? (p.p0 + t * kPages + lane) * kPage / a.d.block_size : 0;
+                return a.d.block_table[(int64_t)p.row * a.d.max_blocks + col];
             };
-            auto page_row = [&](const Piece& p, int t, int32_t blk) -> int {
-                if (!has_page(p, t)) return -1;
-                if (blk < 0 || blk >= a.num_blocks) {
-                    if (is_k) record_error(a.status, KVATTN_ERR_BAD_INDEX);
+            auto pool_row = [&](const Piece& p, int t, int32_t blk) -> int {
+                if (lane >= p.pages(t)) return -1;
+                if (blk < 0 || blk >= a.d.num_blocks) {
+                    if (is_k) record_error(status, KVATTN_ERR_BAD_INDEX);
                     return -1;
                 }
-                return (int)(((int64_t)blk * a.hkv + p.h) * a.block_size) + (t * kBN + lane * kPage) % a.block_size;
+                return (int)(((int64_t)blk * a.d.hkv + p.h) * a.d.block_size) +
+                       (p.p0 + t * kPages + lane) * kPage % a.d.block_size;
             };
             int g = 0, qg = 0;  // K (or V) and Q tiles armed so far
             Walk w = walk0;
             Piece p, ahead;
-            bool more = next_piece(w, ahead);
-            int32_t blk_next = block_id(ahead, ahead.t0);
+            bool more = w.next(a, P, lg, ahead);
+            int32_t blk_next = block_id(ahead, 0);
             while (go && more) {
                 p = ahead;
-                for (int t = p.t0; t < p.t1; ++t) {
-                    const int row = page_row(p, t, blk_next);
+                const int n = p.tiles();
+                for (int t = 0; t < n; ++t) {
+                    const int row = pool_row(p, t, blk_next);
                     const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, row >= 0)) * (uint32_t)kPageBytes;
                     const int s = g % kStages;
-                    if (!arm(is_k ? &B.k_full[s] : &B.v_full[s], is_k ? &B.k_empty[s] : &B.v_empty[s], g / kStages, bytes)) break;
-                    if (row >= 0) {
-                        unsigned char* dst = smem + (is_k ? kOffK : kOffV) + s * kTileBytes + lane * kPageBytes;
-                        const CUtensorMap* m = is_k ? &maps.k : &maps.v;
-                        uint64_t* full = is_k ? &B.k_full[s] : &B.v_full[s];
-                        if constexpr (kHD == 128) tma_load_4d(dst, m, 0, 0, 0, row >> 3, full, pol);
-                        else tma_load_2d(dst, m, 0, row, full, pol);
-                    }
+                    uint64_t* full = is_k ? &B.k_full[s] : &B.v_full[s];
+                    if (!arm(full, is_k ? &B.k_empty[s] : &B.v_empty[s], g / kStages, bytes)) break;
+                    if (row >= 0)
+                        copy_page<kHD>(smem + (is_k ? kOffK : kOffV) + s * kTileBytes + lane * kPageBytes,
+                                       is_k ? &maps.k : &maps.v, row, full, pol);
                     ++g;
-                    const bool first = t == p.t0;
-                    if (t + 1 == p.t1) {
-                        more = next_piece(w, ahead);
-                        if (more) blk_next = block_id(ahead, ahead.t0);
+                    if (t + 1 == n) {
+                        more = w.next(a, P, lg, ahead);
+                        if (more) blk_next = block_id(ahead, 0);
                     } else {
                         blk_next = block_id(p, t + 1);
                     }
-                    if (is_k && first) {
-                        for (int x = 0; x < (p.two() ? 2 : 1); ++x) {
+                    if (is_k && t == 0) {
+                        const int tiles = p.two() ? 2 : 1;
+                        for (int x = 0; x < tiles; ++x) {
                             const int qs = qg % kStages;
-                            if (!arm(&B.q_full[qs], &B.q_empty[qs], qg / kStages, kTileBytes)) break;
+                            if (!arm(&B.q_full[qs], &B.q_empty[qs], qg / kStages, (uint32_t)kTileBytes)) break;
                             if (lane < GE::kPanels)
                                 tma_load_3d(smem + kOffQ + qs * kTileBytes + lane * kPanel, &maps.q, 64 * lane, p.h << lg,
                                             p.b0 + x * (kBM >> lg), &B.q_full[qs], pol);
@@ -357,8 +415,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0 && *abort_flag) {
                 for (int t = max(0, g - kStages); t < g; ++t)
-                    mbar_wait(is_k ? &B.k_full[t % kStages] : &B.v_full[t % kStages], (t / kStages) & 1, a.status);
-                for (int t = max(0, qg - kStages); t < qg; ++t) mbar_wait(&B.q_full[t % kStages], (t / kStages) & 1, a.status);
+                    mbar_wait(is_k ? &B.k_full[t % kStages] : &B.v_full[t % kStages], (t / kStages) & 1, status);
+                for (int t = max(0, qg - kStages); t < qg; ++t) mbar_wait(&B.q_full[t % kStages], (t / kStages) & 1, status);
             }
         } else if (warp == 1) {
             // ============================== MMA issuer ==============================
@@ -366,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // elected lane issues.  Operand descriptors are built once: a stage or
             // k-step only adds (byte offset >> 4) to the start-address field, which
             // cannot carry out of it (shared-memory offsets stay below 256 KB).
-            constexpr uint32_t idesc_s = idesc_bf16_f32(kBM, kBN, false);
+            constexpr uint32_t idesc_s = idesc_bf16_f32(kBM, 0, false);  // N: the tile's keys
             constexpr uint32_t idesc_o = idesc_bf16_f32(kBM, kHD, true);
             const uint32_t sbase = smem_addr(smem);
             const uint64_t dQ = umma_desc_sw128(sbase + kOffQ, 16, 1024);
@@ -375,16 +433,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint64_t kTileStep = kTileBytes >> 4;
             auto wait = [&](uint64_t* b, uint32_t parity) {
                 if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
-                return warp_wait(b, parity, abort_flag, a.status);
+                return warp_wait(b, parity, abort_flag, status);
             };
-            int kb = 0, vb = 0, qb = 0;      // K, V and Q tiles of the pieces before
-            uint32_t steps[2] = {0, 0};      // P_x that have been read so far
-            uint32_t pieces[2] = {0, 0};     // pieces with an O_x before this one
-            // S_x of the t-th tile of A or B.  The K stage is free after the last S that
-            // reads it, the Q tile after the piece's last.
-            auto do_s = [&](const Piece& p, int x, int t) -> bool {
-                const bool two = p.two();
-                const int kt = two ? t : 2 * t + x, k = kb + kt, q = qb + (two ? x : 0), n = p.t1 - p.t0;
+            // Steps through the pieces: the S and the P.V of each.
+            struct Steps {
+                Walk w;
+                Piece p;
+                bool more;
+                int j, n;    // of the piece p
+                int x;       // S_x is this step's, the next step's the other
+                int z;       // O_z is the piece's (two row tiles: O_0 and O_1)
+                int kv, q;   // K (or V) and Q tiles of the pieces before
+            };
+            auto start = [&](Steps& s) {
+                s.j = 0;
+                s.n = (s.more = s.w.next(a, P, lg, s.p)) ? s.p.steps() : 0;
+            };
+            auto advance = [&](Steps& s) {
+                s.x ^= 1;
+                if (++s.j < s.n) return;
+                if (!s.p.two()) s.z ^= 1;
+                s.kv += s.p.tiles();
+                s.q += s.p.two() ? 2 : 1;
+                start(s);
+            };
+            // The K stage is free after the last S that reads it, the Q tile after the
+            // piece's last.
+            auto do_s = [&](const Steps& s) -> bool {
+                const bool two = s.p.two();
+                const int y = s.j & 1, x = s.x, t = s.p.tile(s.j), k = s.kv + t, q = s.q + (two ? y : 0);
+                const uint32_t idesc = idesc_s | ((uint32_t)(s.p.pages(t) * kPage >> 3) << 17);
                 if (t == 0 && !wait(&B.q_full[q % kStages], (q / kStages) & 1)) return false;
                 if (!wait(&B.k_full[k % kStages], (k / kStages) & 1)) return false;
                 tc_fence_after();
@@ -394,76 +472,64 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < kHD / 16; ++i)  // k-step: 16 columns, 32 B inside the 128-byte atom
                         tc_mma_f16(d, qd + (uint64_t)(((i >> 2) * kPanel + (i & 3) * 32) >> 4),
-                                   kd + (uint64_t)(((i >> 2) * 1024 + (i & 3) * 32) >> 4), idesc_s, i > 0);
+                                   kd + (uint64_t)(((i >> 2) * 1024 + (i & 3) * 32) >> 4), idesc, i > 0);
                     tc_commit(&B.s_full[x]);
-                    if (!two || x == 1) tc_commit(&B.k_empty[k % kStages]);
-                    if (kt == n - 1) tc_commit(&B.q_empty[q % kStages]);
+                    if (!two || y == 1) tc_commit(&B.k_empty[k % kStages]);
+                    if (s.j + (two ? 2 : 1) >= s.n) tc_commit(&B.q_empty[q % kStages]);
                 }
                 __syncwarp();
                 return true;
             };
-            // O_x += P_x V, P_x in S_x's first 64 columns, over the tile's whole pages; a
-            // piece's first overwrites O_x (o_free: the piece before has been read)
-            auto do_pv = [&](const Piece& p, int x, int t) -> bool {
-                const bool two = p.two();
-                const int kt = two ? t : 2 * t + x, v = vb + kt;
-                if (!wait(&B.v_full[v % kStages], (v / kStages) & 1) || !wait(&B.p_full[x], steps[x] & 1)) return false;
-                ++steps[x];
-                if (t == 0) {
-                    if (pieces[x] > 0 && !wait(&B.o_free[x], (pieces[x] - 1) & 1)) return false;
-                    ++pieces[x];
+            // O_z += P_x V, P_x in S_x's first 64 columns, over the tile's pages; a piece's
+            // first overwrites O_z (o_free: the piece before on it has been read)
+            uint32_t seen = 0;    // bit x: parity of the P_x so far
+            uint32_t pieces = 0;  // bits z, 2 + z: parity of the pieces on O_z so far, whether there are any
+            auto do_pv = [&](const Steps& s) -> bool {
+                const bool two = s.p.two(), first = s.j < (two ? 2 : 1);
+                const int y = s.j & 1, x = s.x, z = two ? y : s.z, t = s.p.tile(s.j), v = s.kv + t;
+                if (!wait(&B.v_full[v % kStages], (v / kStages) & 1) || !wait(&B.p_full[x], seen >> x & 1u)) return false;
+                seen ^= 1u << x;
+                if (first) {
+                    if ((pieces >> (2 + z) & 1u) && !wait(&B.o_free[z], ~pieces >> z & 1u)) return false;
+                    pieces = (pieces ^ 1u << z) | 4u << z;
                 }
                 tc_fence_after();
                 if (elect_one()) {
                     const uint64_t vd = dV + (v % kStages) * kTileStep;
-                    const uint32_t d = tmem + 256 + x * 128, pa = tmem + x * 128;
-                    const int pages = min(kPages, (p.tokens - (p.t0 + kt) * kBN) / kPage);
+                    const uint32_t d = tmem + 256 + z * 128, pa = tmem + x * 128;
+                    const int pages = s.p.pages(t);
 #pragma unroll
                     for (int i = 0; i < kPages; ++i)  // k-step: 16 keys = two 8-key groups
                         if (i < pages)
-                            tc_mma_f16_ts(d, pa + i * 8, vd + (uint64_t)((i * 2 * kGroup) >> 4), idesc_o, (t > 0 || i > 0));
-                    if (!two || x == 1) tc_commit(&B.v_empty[v % kStages]);
-                    if (t + 1 == p.tiles(x)) tc_commit(&B.o_done[x]);
+                            tc_mma_f16_ts(d, pa + i * 8, vd + (uint64_t)((i * 2 * kGroup) >> 4), idesc_o, (!first || i > 0));
+                    if (!two || y == 1) tc_commit(&B.v_empty[v % kStages]);
+                    if (s.j + (two ? 2 : 1) >= s.n) tc_commit(&B.o_done[z]);
                 }
                 __syncwarp();
                 return true;
             };
-            // Order per t: PV_A(t) S_A(t+1) PV_B(t) S_B(t+1); S_x(t+1) overwrites S_x's
-            // columns after PV_x(t) has read P_x(t) from them (tensor operations of
-            // one thread run in issue order).
-            Walk w = walk0;
-            Piece p, next;
-            bool more = next_piece(w, p);
-            bool ok = do_s(p, 0, 0) && (p.tiles(1) == 0 || do_s(p, 1, 0));
-            while (ok && more) {
-                const int n0 = p.tiles(0), n1 = p.tiles(1);
-                for (int t = 0; ok && t + 1 < n0; ++t) {
-                    ok = do_pv(p, 0, t) && do_s(p, 0, t + 1) && do_pv(p, 1, t) && (t + 1 >= n1 || do_s(p, 1, t + 1));
+            // P.V of a step, then S of the second step after it, whichever piece that is
+            // of: it overwrites S_x's columns after P.V has read P_x from them (tensor
+            // operations of one thread run in issue order).
+            Steps fs{walk0, {}, false, 0, 0, 0, 0, 0, 0}, fo = fs;
+            start(fs);
+            start(fo);
+            bool ok = true;
+            for (int ahead = 0; ok && fo.more;) {
+                if (ahead < 2 && fs.more) {
+                    ok = do_s(fs);
+                    advance(fs);
+                    ++ahead;
+                } else {
+                    ok = do_pv(fo);
+                    advance(fo);
+                    --ahead;
                 }
-                if (!ok) break;
-                // the piece's last, and the next piece's first S
-                if (!(ok = do_pv(p, 0, n0 - 1))) break;
-                more = next_piece(w, next);
-                const int kb0 = kb, vb0 = vb, qb0 = qb;
-                const int kb1 = kb + p.t1 - p.t0, qb1 = qb + (p.two() ? 2 : 1);
-                if (more) {
-                    kb = kb1;
-                    qb = qb1;
-                    ok = do_s(next, 0, 0);
-                    kb = kb0;
-                    qb = qb0;
-                }
-                if (ok && n1 == n0) ok = do_pv(p, 1, n1 - 1);
-                kb = kb1;
-                qb = qb1;
-                vb = vb0 + p.t1 - p.t0;
-                if (ok && more && next.tiles(1) > 0) ok = do_s(next, 1, 0);
-                p = next;
             }
             // every MMA this warp issued has completed once `drain` flips
             if (elect_one()) tc_commit(&B.drain);
             __syncwarp();
-            mbar_wait(&B.drain, 0, a.status);
+            mbar_wait(&B.drain, 0, status);
         }
     } else if (warp < 12) {
         setmaxnreg_inc<kRegsSoftmax>();
@@ -473,32 +539,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         // 0) and warps 8-11 its columns 64..127 (hf = 1).  The halves of a row agree on
         // the row max through shared memory, with a named barrier of that pair of
         // warps per tile.  These warps never stop early: after an abort their waits return
-        // at once and they run on to the end (nothing of it is reported good).  One
-        // body for A and B, whose states change places after each.
+        // at once and they run on to the end (nothing of it is reported good).  The states
+        // of two row tiles change places after each step.
         const int hf = (warp - 4) >> 2;
         const int quarter = warp & 3;        // TMEM lanes 32*quarter .. +31
         const int r = quarter * 32 + lane;   // row of the tile
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         float* xchg = reinterpret_cast<float*>(smem + GE::kOffX);
-        const float sl2 = a.scale_log2;
+        const float sl2 = a.d.scale_log2;
         uint32_t steps = 0;  // bit x: parity of the S_x seen so far
-        int ii = 0;
+        int ii = 0, x = 0, z = 0, v = 0;  // v: V tiles of the pieces before
         Walk w = walk0;
         Piece p;
-        while (next_piece(w, p)) {
+        while (w.next(a, P, lg, p)) {
             const bool two = p.two();
-            const int n0 = p.tiles(0), n1 = p.tiles(1);
-            float m_now = -INFINITY, l_now = 0.f, m_other = -INFINITY, l_other = 0.f;  // of A and B in turn
+            const int n = p.steps();
+            float m_now = -INFINITY, l_now = 0.f, m_other = -INFINITY, l_other = 0.f;
 #pragma unroll 1
-            for (int st = 0; st < n0 + n1; ++st) {
-                const int t = st >> 1, x = st & 1;
+            for (int j = 0; j < n; ++j, x ^= 1) {
+                const int y = j & 1;
                 const uint32_t tS = tmem + lane_base + x * 128 + hf * 64;
-                const uint32_t tO = tmem + lane_base + 256 + x * 128 + hf * (kHD / 2);
-                const int keys = p.tokens - (p.t0 + (two ? t : st)) * kBN - hf * 64;  // of this half's columns
-                wait_or_abort(&B.s_full[x], steps >> x & 1u, abort_flag, a.status);
+                const uint32_t tO = tmem + lane_base + 256 + (two ? y : z) * 128 + hf * (kHD / 2);
+                const int keys = p.pages(p.tile(j)) * kPage - hf * 64;  // of this half's columns
+                wait_or_abort(&B.s_full[x], steps >> x & 1u, abort_flag, status);
                 __syncwarp();
                 steps ^= 1u << x;
-                if ((two ? x * kBM : 0) + quarter * 32 < p.rows) {  // (P of other rows may be anything)
+                const int rows = p.rows - (two ? y * kBM : 0);  // of the tile (P of others may be anything)
+                if (quarter * 32 < rows) {
                     uint32_t sv[64];
                     tc_fence_after();
                     tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
@@ -524,9 +591,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     bar_sync(1 + quarter, 64);
                     const float m_tile = fmaxf(hm, slot[(1 - hf) * 128 + r]) * sl2;
                     const bool none = m_now == -INFINITY;  // no score above -infinity so far
-                    const bool rescale = !none && m_tile > m_now + 8.f;
+                    const bool rescale = !none && m_tile > m_now + 8.f && r < rows;
                     const float m_new = none || rescale ? m_tile : m_now;
-                    const float alpha = none ? 1.f : fast_exp2(m_now - m_new);
+                    const float alpha = none || r >= rows ? 1.f : fast_exp2(m_now - m_new);
                     m_now = m_new;
                     // P = 2^(s*scale*log2e - m) in bf16, into columns 32hf..32hf+31 of S_x
                     // (both halves have read their S before the barrier); scores that are
@@ -546,49 +613,54 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tmem_st32(tmem + lane_base + x * 128 + hf * 32, pw);
                     l_now = l_now * alpha + ((pk_lo(sum2[0]) + pk_hi(sum2[0])) + (pk_lo(sum2[1]) + pk_hi(sum2[1])));
-                    // O_x (this half's columns): PV_x(t-1) completed before S_x(t) was
-                    // reported.  The whole warp rescales if any of its rows must (alpha
-                    // is 1 for the others).
-                    if (__any_sync(0xffffffffu, rescale && t > 0)) {
+                    // O (this half's columns): the P.V of two steps ago completed before this
+                    // S_x was reported; the last step's, if it was of this O too, before its V
+                    // stage was free.  The whole warp rescales if any of its rows must (alpha is 1
+                    // for the others).
+                    if (__any_sync(0xffffffffu, rescale && j > (two ? 1 : 0))) {
+                        if (!two) {
+                            const int u = v + j - 1;
+                            wait_or_abort(&B.v_empty[u % kStages], (u / kStages) & 1, abort_flag, status);
+                            __syncwarp();
+                            tc_fence_after();
+                        }
 #pragma unroll 1
                         for (int q = 0; q < kHD / 64; ++q) {
-                            uint32_t v[32];
-                            tmem_ld32(tO + q * 32, v);
+                            uint32_t o[32];
+                            tmem_ld32(tO + q * 32, o);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-                            tmem_st32(tO + q * 32, v);
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tmem_st32(tO + q * 32, o);
                         }
                     }
                     tmem_st_wait();
                     tc_fence_before();
                 }
                 mbar_arrive(&B.p_full[x]);
-                const float m = m_now, l = l_now;
-                m_now = m_other;
-                l_now = l_other;
-                m_other = m;
-                l_other = l;
+                if (two) {
+                    const float m = m_now, l = l_now;
+                    m_now = m_other;
+                    l_now = l_other;
+                    m_other = m;
+                    l_other = l;
+                }
             }
-            if ((n0 + n1) & 1) {  // A was last
-                const float m = m_now, l = l_now;
-                m_now = m_other;
-                l_now = l_other;
-                m_other = m;
-                l_other = l;
-            }
-            // this piece's maxima and sums to the output warps (two pieces' worth: those of
-            // piece ii - 2 were read before S_A of this piece was issued)
-            float* lx = xchg + 512 + (ii & 1) * 512;  // [2 halves][2 tiles][128 rows]
-            float* mx = xchg + 1536 + (ii & 1) * 256;
+            // This piece's maxima and sums to the output warps.  Those of piece ii - kPast
+            // have been read: this piece's last S came after the P.V of two steps before, of
+            // piece ii - 2 at least, whose first waited until the piece before it on its O, ii -
+            // 4 at least, had been read, which its sums are before.
+            float* lx = xchg + 512 + (ii % kPast) * 768;  // [2 halves][2 tiles][128 rows], then maxima [2][128]
             lx[(hf * 2 + 0) * 128 + r] = l_now;
             lx[(hf * 2 + 1) * 128 + r] = l_other;
             if (hf == 0) {
-                mx[r] = m_now;
-                mx[128 + r] = m_other;
+                lx[512 + r] = m_now;
+                lx[640 + r] = m_other;
             }
-            mbar_arrive(&B.l_full[ii & 1]);
+            mbar_arrive(&B.l_full[ii % kPast]);
             ++ii;
+            v += p.tiles();
+            if (!two) z ^= 1;
         }
     } else {
         setmaxnreg_dec<kRegsOutput>();
@@ -599,81 +671,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = quarter * 32 + lane;
         const uint32_t tO = tmem + ((uint32_t)(quarter * 32) << 16) + 256;
         const float* xchg = reinterpret_cast<const float*>(smem + GE::kOffX);
-        uint32_t done[2] = {0, 0};  // pieces with an O_x so far
-        int ii = 0;
+        uint32_t done = 0;  // bit z: parity of the pieces on O_z so far
+        int ii = 0, z0 = 0;
         Walk w = walk0;
         Piece p;
         bool ok = true;
-        while (ok && next_piece(w, p)) {
+        while (ok && w.next(a, P, lg, p)) {
             const bool two = p.two();
-            const int n1 = p.tiles(1);
-            if (!long_wait(&B.l_full[ii & 1], (ii >> 1) & 1, p.t1 - p.t0, abort_flag, a.status)) break;
-            const float* lx = xchg + 512 + (ii & 1) * 512;
-            const float* mx = xchg + 1536 + (ii & 1) * 256;
-            const float l0 = lx[r] + lx[256 + r], l1 = lx[128 + r] + lx[384 + r], m0 = mx[r], m1 = mx[128 + r];
+            if (!long_wait(&B.l_full[ii % kPast], (ii / kPast) & 1, p.tiles(), abort_flag, status)) break;
+            const float* lx = xchg + 512 + (ii % kPast) * 768;
+            const float l0 = lx[r] + lx[256 + r], l1 = lx[128 + r] + lx[384 + r], m0 = lx[512 + r], m1 = lx[640 + r];
             ++ii;
-            const int64_t row0 = (int64_t)p.id * kPrefixRows + r;
-            // 16 columns of O at a time into row `row`; merged: f0 O_A + f1 O_B
-            auto put = [&](int64_t row, bool write, float m, float l) {
-                if (write) *reinterpret_cast<float2*>(a.prefix_ml + row * 2) = make_float2(m, l);
-            };
-            if (two || n1 == 0) {
 #pragma unroll 1
-                for (int x = 0; x < (two ? 2 : 1); ++x) {
-                    if (!(ok = warp_wait(&B.o_done[x], done[x] & 1, abort_flag, a.status))) break;
-                    ++done[x];
-                    tc_fence_after();
-                    const bool write = x * kBM + r < p.rows;
-                    put(row0 + x * kBM, write, x ? m1 : m0, x ? l1 : l0);
-                    float* o = a.prefix_o + (row0 + x * kBM) * kHD;
-#pragma unroll 1
-                    for (int q = 0; q < kHD / 32; ++q) {
-                        uint32_t v[32];
-                        tmem_ld32(tO + x * 128 + q * 32, v);
-                        tmem_ld_wait();
-                        if (q + 1 == kHD / 32) {
-                            tc_fence_before();
-                            mbar_arrive(&B.o_free[x]);
-                        }
-                        if (write) {
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) store_256(o + q * 32 + 8 * c, v + 8 * c);
-                        }
-                    }
-                }
-            } else {
-                ok = warp_wait(&B.o_done[0], done[0] & 1, abort_flag, a.status) &&
-                     warp_wait(&B.o_done[1], done[1] & 1, abort_flag, a.status);
-                if (!ok) break;
-                ++done[0];
-                ++done[1];
+            for (int y = 0; y < (two ? 2 : 1); ++y) {
+                const int z = two ? y : z0;
+                if (!(ok = warp_wait(&B.o_done[z], done >> z & 1u, abort_flag, status))) break;
+                done ^= 1u << z;
                 tc_fence_after();
-                const bool write = r < p.rows;
-                // (a sum of 0: no score above -infinity, no weight)
-                const float m = fmaxf(l0 == 0.f ? -INFINITY : m0, l1 == 0.f ? -INFINITY : m1);
-                const float f0 = l0 == 0.f ? 0.f : fast_exp2(m0 - m), f1 = l1 == 0.f ? 0.f : fast_exp2(m1 - m);
-                put(row0, write, m, f0 * l0 + f1 * l1);
-                float* o = a.prefix_o + row0 * kHD;
+                const bool write = y * kBM + r < p.rows;
+                const int64_t row = (int64_t)p.out + y * kBM + r;
+                if (write) *reinterpret_cast<float2*>(a.ml + row * 2) = y ? make_float2(m1, l1) : make_float2(m0, l0);
+                float* o = a.o + row * kHD;
 #pragma unroll 1
-                for (int q = 0; q < kHD / 16; ++q) {
-                    uint32_t u[16], v[16];
-                    tmem_ld16(tO + q * 16, u);
-                    tmem_ld16(tO + 128 + q * 16, v);
+                for (int q = 0; q < kHD / 32; ++q) {
+                    uint32_t u[32];
+                    tmem_ld32(tO + z * 128 + q * 32, u);
                     tmem_ld_wait();
-                    if (q + 1 == kHD / 16) {
+                    if (q + 1 == kHD / 32) {
                         tc_fence_before();
-                        mbar_arrive(&B.o_free[0]);
-                        mbar_arrive(&B.o_free[1]);
+                        mbar_arrive(&B.o_free[z]);
                     }
                     if (write) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            u[e] = __float_as_uint(f0 * __uint_as_float(u[e]) + f1 * __uint_as_float(v[e]));
-                        store_256(o + q * 16, u);
-                        store_256(o + q * 16 + 8, u + 8);
+                        for (int c = 0; c < 4; ++c) store_256(o + q * 32 + 8 * c, u + 8 * c);
                     }
                 }
             }
+            if (!two) z0 ^= 1;
         }
     }
     tc_fence_before();
@@ -682,6 +716,312 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+}
+
+// ---------------------------------------------------------------- own keys
+
+// Range `c` of the own pages, begin .. end - 1, by this warp.
+template <int kHD>
+__device__ __forceinline__ void own_warp(const SharedArgs& a, const Maps& maps, const Plan& P, int c, int begin, int end,
+                                         int lg, unsigned char* ring, uint64_t* full)
+{
+    using GE = Geo<kHD>;
+    constexpr int kRing = GE::kOwnRing, kPageBytes = GE::kPageBytes;
+    constexpr int kGroup = 8 * kHD * 2;  // 8 rows of a page, all panels
+    const int lane = threadIdx.x & 31, g4 = lane >> 2, q4 = lane & 3;
+    const int mi = lane >> 3, rr = lane & 7;  // ldmatrix: matrix and row this lane addresses
+    const int G = 1 << lg, hkv = a.d.hkv, n = end - begin;
+    const uint64_t pol = l2_evict_first_policy();
+    // Lane i looks up page i of a batch of 32: its segment b Hkv + h, its row in the pool
+    // (-1: none), how many of its tokens are keys, and whether its segment ends.
+    struct Page {
+        int seg, row, info;
+    };
+    auto look_up = [&](int base) {
+        Page pg{0, -1, 0};
+        const int r = begin + base + lane;
+        if (r >= end) return pg;
+        int b = 0;  // the last sequence with Hkv own[b] <= r
+        for (int m = a.d.batch; m > 1;) {
+            const int half = m >> 1;
+            if (hkv * P.own[b + half] <= r) b += half;
+            m -= half;
+        }
+        const int pages = P.own[b + 1] - P.own[b], in = r - hkv * P.own[b], h = in / pages, len = a.d.seq_lens[b];
+        const int left = pages - (in - h * pages);  // pages up to the segment's end
+        const int tok = ((len + kPage - 1) / kPage - left) * kPage;
+        const int32_t blk = a.d.block_table[(int64_t)b * a.d.max_blocks + tok / a.d.block_size];
+        pg.seg = b * hkv + h;
+        pg.info = left == 1 || r + 1 == end ? 32 : 0;
+        if (blk < 0 || blk >= a.d.num_blocks) {
+            record_error(a.d.status, KVATTN_ERR_BAD_INDEX);
+        } else {
+            pg.row = (int)(((int64_t)blk * hkv + h) * a.d.block_size) + tok % a.d.block_size;
+            pg.info |= min(kPage, len - tok);
+        }
+        return pg;
+    };
+    Page now = look_up(0), next = look_up(32);  // batches j / 32 and the one after
+    int batch = 0;
+    auto get = [&](int Page::*f, int j) { return __shfl_sync(0xffffffffu, (j >> 5 == batch ? now : next).*f, j & 31); };
+    auto fetch = [&](int j) {  // page j on its way to its place in the ring
+        if (j >= n) return;
+        const int row = get(&Page::row, j);
+        if (lane == 0) {
+            uint64_t* bar = &full[j % kRing];
+            unsigned char* dst = ring + j % kRing * (2 * kPageBytes);
+            if (row >= 0) {
+                mbar_arrive_expect_tx(bar, 2 * kPageBytes);
+                copy_page<kHD>(dst, &maps.k, row, bar, pol);
+                copy_page<kHD>(dst + kPageBytes, &maps.v, row, bar, pol);
+            } else {
+                mbar_arrive(bar);
+            }
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < kRing; ++j) fetch(j);
+    // Q rows g4 (heads of the segment's group) as A fragments: columns 2 q4 .. and 8 + 2 q4
+    // .. of each k-step
+    uint32_t qa[kHD / 16][2], qn[kHD / 16][2];
+    auto load_q = [&](int seg, uint32_t (&q)[kHD / 16][2]) {
+        const uint32_t* row = reinterpret_cast<const uint32_t*>(reinterpret_cast<const __nv_bfloat16*>(a.d.q) +
+                                                                (((int64_t)seg << lg) + g4) * kHD);
+#pragma unroll
+        for (int i = 0; i < kHD / 16; ++i) {
+            q[i][0] = g4 < G ? __ldg(row + 8 * i + q4) : 0u;
+            q[i][1] = g4 < G ? __ldg(row + 8 * i + 4 + q4) : 0u;
+        }
+    };
+    load_q(get(&Page::seg, 0), qn);
+    float o[kHD / 8][2], m_run = -INFINITY, l_run = 0.f;
+    bool fresh = true;
+    for (int j = 0; j < n; ++j) {
+        if (j >> 5 != batch) {
+            ++batch;
+            now = next;
+            next = look_up((batch + 1) * 32);
+        }
+        const int seg = get(&Page::seg, j), info = get(&Page::info, j), keys = info & 31;
+        if (fresh) {
+#pragma unroll
+            for (int i = 0; i < kHD / 16; ++i) {
+                qa[i][0] = qn[i][0];
+                qa[i][1] = qn[i][1];
+            }
+#pragma unroll
+            for (int i = 0; i < kHD / 8; ++i) o[i][0] = o[i][1] = 0.f;
+            m_run = -INFINITY;
+            l_run = 0.f;
+        }
+        fresh = info & 32;
+        if (fresh && j + 1 < n) load_q(get(&Page::seg, j + 1), qn);  // (on its way during this page)
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[j % kRing], (j / kRing) & 1, a.d.status))) {
+            // nothing more is waited for but the copies under way
+            if (lane == 0)
+                for (int u = j + 1; u < min(n, j + kRing); ++u) mbar_wait(&full[u % kRing], (u / kRing) & 1, a.d.status);
+            __syncwarp();
+            return;
+        }
+        unsigned char* kst = ring + j % kRing * (2 * kPageBytes);
+        unsigned char* vst = kst + kPageBytes;
+        if (keys > 0) {
+            // V rows past the last key are stale: their p is 0, but 0 * NaN would be NaN
+            if (keys < kPage) {
+                constexpr int kChunks = kHD / 8;
+                for (int i = keys * kChunks + lane; i < kPage * kChunks; i += 32) {
+                    const int row = i / kChunks, ch = i % kChunks;
+                    *reinterpret_cast<uint4*>(vst + (row >> 3) * kGroup + (ch >> 3) * 1024 + (row & 7) * 128 + (ch & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                }
+                fence_async_smem();  // before the next copy into this place
+                __syncwarp();
+            }
+            // 16-byte chunk c of row r at chunk (c ^ r) of its 128 B (r = row mod 8)
+            const uint32_t kb = smem_addr(kst), vb = smem_addr(vst);
+            float s0[2] = {0.f, 0.f}, s1[2] = {0.f, 0.f};  // tokens 0-7, 8-15
+#pragma unroll
+            for (int i = 0; i < kHD / 16; ++i) {
+                // matrices (tokens 0-7, chunk 2i), (0-7, 2i+1), (8-15, 2i), (8-15, 2i+1)
+                const int ch = 2 * i + (mi & 1);
+                uint32_t b[4];
+                ldmatrix_x4(b, kb + (mi >> 1) * kGroup + (ch >> 3) * 1024 + rr * 128 + (((ch & 7) ^ rr) << 4));
+                mma_bf16_16816_top(s0, qa[i][0], qa[i][1], b[0], b[1]);
+                mma_bf16_16816_top(s1, qa[i][0], qa[i][1], b[2], b[3]);
+            }
+            // row g4: tokens 2q4, 2q4+1 (s0) and 8+2q4, 9+2q4 (s1), in log2 units
+            const float sl2 = a.d.scale_log2;
+            float x[4] = {s0[0] * sl2, s0[1] * sl2, s1[0] * sl2, s1[1] * sl2};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (2 * q4 + (e & 1) + 8 * (e >> 1) >= keys) x[e] = -INFINITY;
+            float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // the maximum is raised when a page's exceeds it by more than 2^8
+            if (top > m_run + 8.f) {
+                const float f = m_run == -INFINITY ? 0.f : fast_exp2(m_run - top);
+                m_run = top;
+                l_run *= f;
+#pragma unroll
+                for (int i = 0; i < kHD / 8; ++i) {
+                    o[i][0] *= f;
+                    o[i][1] *= f;
+                }
+            }
+            // (scores that are all -inf so far have no weight)
+            const float m0 = m_run == -INFINITY ? 0.f : m_run;
+            const float p0 = fast_exp2(x[0] - m0), p1 = fast_exp2(x[1] - m0);
+            const float p2 = fast_exp2(x[2] - m0), p3 = fast_exp2(x[3] - m0);
+            l_run += (p0 + p1) + (p2 + p3);
+            // P in bf16, the type of V that the MMA takes it with: off by at most 2^-8
+            // relative, at random; the sum adds the fp32 p
+            const uint32_t pa0 = pack_bf16_rn(p0, p1), pa2 = pack_bf16_rn(p2, p3);
+#pragma unroll
+            for (int i = 0; i < kHD / 16; ++i) {
+                // V^T: matrices (tokens 0-7, chunk 2i), (8-15, 2i), (0-7, 2i+1), (8-15, 2i+1)
+                const int ch = 2 * i + (mi >> 1);
+                uint32_t b[4];
+                ldmatrix_x4_trans(b, vb + (mi & 1) * kGroup + (ch >> 3) * 1024 + rr * 128 + (((ch & 7) ^ rr) << 4));
+                mma_bf16_16816_top(o[2 * i], pa0, pa2, b[0], b[1]);
+                mma_bf16_16816_top(o[2 * i + 1], pa0, pa2, b[2], b[3]);
+            }
+        }
+        __syncwarp();  // every lane has read the page
+        fetch(j + kRing);
+        if (fresh) {  // the segment's end, or the range's: its state
+            l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
+            l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
+            const int64_t row = (((int64_t)c + seg) << lg) + g4;
+            if (g4 < G) {
+                float* out = a.own_o + row * kHD + 2 * q4;
+#pragma unroll
+                for (int i = 0; i < kHD / 8; ++i) *reinterpret_cast<float2*>(out + 8 * i) = make_float2(o[i][0], o[i][1]);
+                if (q4 == 0) *reinterpret_cast<float2*>(a.own_ml + row * 2) = make_float2(m_run, l_run);
+            }
+        }
+    }
+}
+
+template <int kHD>
+__global__ void __launch_bounds__(kThreads, 1)
+    decode_shared_kernel(const __grid_constant__ SharedArgs a, const __grid_constant__ Maps maps)
+{
+    pdl_wait();
+    using GE = Geo<kHD>;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    Plan& P = *reinterpret_cast<Plan*>(smem + GE::kOffPlan);
+    const int lg = __ffs(a.d.hq / a.d.hkv) - 1;  // row r of a prefix piece: sequence r >> lg, head r & (G - 1)
+    make_plan(a, P, lg);
+    const int shared = P.first[a.num_groups], own = a.d.hkv * P.own[a.d.batch];
+    const Ranges ranges = ranges_of(shared, own, gridDim.x, 180000.f / (2 * GE::kPageBytes), GE::kOwnWarps);
+    // where the merge finds each sequence's partial results
+    for (int b = (int)blockIdx.x + (int)gridDim.x * threadIdx.x; b < a.d.batch; b += (int)gridDim.x * kThreads) {
+        SharedOf o{};
+        o.per = ranges.per;
+        o.own_per = ranges.own_per;
+        o.own_first = a.d.hkv * P.own[b];
+        o.own_pages = P.own[b + 1] - P.own[b];
+        if (shared > 0 && b < P.cu[a.num_groups]) {
+            const int g = group_of(P, a.num_groups, b), pages = P.tokens[g] / kPage, L = a.d.seq_lens[b];
+            if (pages > 0 && L >= P.tokens[g] && L <= a.d.max_seq_len && L <= (int64_t)a.d.max_blocks * a.d.block_size) {
+                const int r = (b - P.cu[g]) << lg, rb = r / kSharedRows;
+                o.pages = pages;
+                o.head_segments = blocks_of(P.cu[g + 1] - P.cu[g], lg);
+                o.first = P.first[g] + rb * pages;
+                o.head_pages = o.head_segments * pages;
+                o.segment = P.segment[g] + rb;
+                o.row = r - rb * kSharedRows;
+            }
+        }
+        a.of[b] = o;
+    }
+    if ((int)blockIdx.x < ranges.ctas) {
+        const int r = min(shared, (int)blockIdx.x * ranges.per), end = min(shared, r + ranges.per);
+        if (r < end) prefix_cta<kHD>(a, maps, P, Walk{r, end, 0}, lg, smem);
+    } else {
+        const int warp = threadIdx.x >> 5;
+        if (warp >= GE::kOwnWarps) return;
+        const int c = ((int)blockIdx.x - ranges.ctas) * GE::kOwnWarps + warp;
+        const int r = min(own, c * ranges.own_per), end = min(own, r + ranges.own_per);
+        if (r >= end) return;
+        uint64_t* full = reinterpret_cast<uint64_t*>(smem + GE::kOffOwnBar) + warp * GE::kOwnRing;
+        if ((threadIdx.x & 31) == 0) {
+            for (int s = 0; s < GE::kOwnRing; ++s) mbar_init(&full[s], 1);
+            fence_mbar_init();
+        }
+        __syncwarp();
+        own_warp<kHD>(a, maps, P, c, r, end, lg, smem + warp * GE::kOwnRing * 2 * GE::kPageBytes, full);
+    }
+}
+
+// Merges the pieces of a row: a warp per (sequence, query head), 8 pieces at a time
+// (a lane's loads of their outputs and the maxima and sums are under way together).
+template <int kHD>
+__global__ void __launch_bounds__(128) decode_shared_merge_kernel(const __grid_constant__ SharedArgs a)
+{
+    pdl_wait();
+    constexpr int kV = kHD / 32, kChunk = 8;
+    const int wid = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (wid >= a.d.batch * a.d.hq) return;
+    const int G = a.d.hq / a.d.hkv, b = wid / a.d.hq, qh = wid - b * a.d.hq, h = qh / G, g = qh - h * G;
+    const SharedOf s = a.of[b];
+    int np = 0, no = 0;
+    int64_t shared0 = 0, own0 = 0;  // rows of the first pieces
+    if (s.pages > 0) {
+        const int first = s.first + h * s.head_pages, c = first / s.per;
+        np = (first + s.pages - 1) / s.per - c + 1;
+        shared0 = (int64_t)(c + s.segment + h * s.head_segments) * kSharedRows + s.row + g;
+    }
+    if (s.own_pages > 0) {
+        const int first = s.own_first + h * s.own_pages, c = first / s.own_per;
+        no = (first + s.own_pages - 1) / s.own_per - c + 1;
+        own0 = (int64_t)(c + b * a.d.hkv + h) * G + g;
+    }
+    float acc[kV] = {}, den = 0.f, top = -INFINITY;
+    for (int c0 = 0; c0 < np + no; c0 += kChunk) {
+        auto row_of = [&](int c) { return c < np ? shared0 + (int64_t)c * kSharedRows : own0 + (int64_t)(c - np) * G; };
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (lane < kChunk && c0 + lane < np + no)
+            ml = *reinterpret_cast<const float2*>((c0 + lane < np ? a.ml : a.own_ml) + row_of(c0 + lane) * 2);
+        float o[kChunk][kV];
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+            if (c0 + i < np + no) {
+                const float* p = (c0 + i < np ? a.o : a.own_o) + row_of(c0 + i) * kHD + kV * lane;
+                if constexpr (kV == 4) *reinterpret_cast<float4*>(o[i]) = *reinterpret_cast<const float4*>(p);
+                else *reinterpret_cast<float2*>(o[i]) = *reinterpret_cast<const float2*>(p);
+            }
+        }
+        // (a piece's sum is 0 without a score above -infinity, NaN with NaN scores)
+        float m = ml.y == 0.f ? -INFINITY : ml.x;
+#pragma unroll
+        for (int x = 1; x < kChunk; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+        m = fmaxf(top, __shfl_sync(0xffffffffu, m, 0));
+        const float f0 = den == 0.f ? 0.f : exp2f(top - m), w = ml.y == 0.f ? 0.f : exp2f(ml.x - m);
+        top = m;
+        float sum = ml.y == 0.f ? 0.f : w * ml.y;
+#pragma unroll
+        for (int x = 1; x < kChunk; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        den = den * f0 + __shfl_sync(0xffffffffu, sum, 0);
+#pragma unroll
+        for (int k = 0; k < kV; ++k) acc[k] *= f0;
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+            if (wi != 0.f) {
+#pragma unroll
+                for (int k = 0; k < kV; ++k) acc[k] += wi * o[i][k];
+            }
+        }
+    }
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    uint32_t* out = reinterpret_cast<uint32_t*>(a.d.out) + ((int64_t)wid * kHD + kV * lane) / 2;
+    if constexpr (kV == 4)
+        *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16_rn(acc[0] * inv, acc[1] * inv), pack_bf16_rn(acc[2] * inv, acc[3] * inv));
+    else
+        *out = pack_bf16_rn(acc[0] * inv, acc[1] * inv);
 }
 
 template <int kHD>
@@ -703,22 +1043,25 @@ bool make_maps(const DecodeArgs& a, Maps& m)
 }
 
 template <int kHD>
-kvattn_status launch(const DecodeArgs& a, cudaStream_t s)
+kvattn_status launch(const SharedArgs& a, cudaStream_t s)
 {
     Maps maps;
-    if (!make_maps<kHD>(a, maps)) return KVATTN_ERR_CUDA;
+    if (!make_maps<kHD>(a.d, maps)) return KVATTN_ERR_CUDA;
     constexpr int kSmem = Geo<kHD>::kSmemBytes;
     static_assert(kSmem <= 232448, "shared memory of a block");
     static SmemLimit limit;
-    if (limit.ensure(reinterpret_cast<const void*>(decode_prefix_kernel<kHD>), kSmem) != cudaSuccess) return KVATTN_ERR_CUDA;
-    return cuda_status(launch_pdl(decode_prefix_kernel<kHD>, dim3((unsigned)num_sms()), dim3(kThreads), kSmem, s, a, maps));
+    if (limit.ensure(reinterpret_cast<const void*>(decode_shared_kernel<kHD>), kSmem) != cudaSuccess) return KVATTN_ERR_CUDA;
+    const cudaError_t e = launch_pdl(decode_shared_kernel<kHD>, dim3((unsigned)num_sms()), dim3(kThreads), kSmem, s, a, maps);
+    if (e != cudaSuccess) return KVATTN_ERR_CUDA;
+    const int rows = a.d.batch * a.d.hq;
+    return cuda_status(launch_pdl(decode_shared_merge_kernel<kHD>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s, a));
 }
 
 }  // namespace
 
-kvattn_status launch_decode_shared(const DecodeArgs& a, cudaStream_t s)
+kvattn_status launch_decode_shared(const SharedArgs& a, cudaStream_t s)
 {
-    return a.d == 128 ? launch<128>(a, s) : a.d == 64 ? launch<64>(a, s) : KVATTN_ERR_UNSUPPORTED;
+    return a.d.d == 128 ? launch<128>(a, s) : a.d.d == 64 ? launch<64>(a, s) : KVATTN_ERR_UNSUPPORTED;
 }
 
 }  // namespace kvattn

@@ -11,7 +11,7 @@ kvattn_status launch_decode_window(const DecodeArgs& a, int32_t max_tiles, cudaS
 {
     kvattn_status st;
     if (max_tiles > 0 && launch_decode_direct(a, max_tiles, s, &st)) return st;
-    return dispatch<kWindow>(a, s);
+    return dispatch<true>(a, s);
 }
 
 }  // namespace kvattn

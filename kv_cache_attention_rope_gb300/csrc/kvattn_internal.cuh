@@ -197,17 +197,6 @@ struct CompactArgs {
 };
 kvattn_status launch_compact(const CompactArgs& a, cudaStream_t s);
 
-// What a sequence shares (launch_decode_shared): the first `tokens` of its keys (a
-// multiple of 16; 0: none), and where the partial results over them are.  The prefix
-// kernel's work is a stream of tiles, cut into equal ranges of `per` tiles; the tiles
-// of (sequence, KV head h) are first + h head_tiles .. + tiles - 1, piece c of the
-// stream's range c lies at (c + segment + h head_segments) kPrefixRows + row.
-struct PrefixOf {
-    int32_t tokens, first, tiles, head_tiles;
-    int32_t segment, head_segments, row, per;
-};
-constexpr int kPrefixRows = 256;
-
 struct DecodeArgs {
     const void* q;
     const void* k_pool;
@@ -230,13 +219,6 @@ struct DecodeArgs {
     float scale_log2;  // softmax scale * log2(e)
     int* status;
     int32_t window, sinks;  // launch_decode_window only
-    // launch_decode_shared and launch_decode_own only
-    PrefixOf* prefix;       // [batch]
-    float* prefix_o;        // [pieces][kPrefixRows][d], not divided by their sums
-    float* prefix_ml;       // [pieces][kPrefixRows][2] (max in log2 units, sum)
-    const int32_t* cu_groups;
-    const int32_t* shared_lens;
-    int32_t num_groups, max_shared;
 };
 kvattn_status launch_decode(const DecodeArgs& a, cudaStream_t s);
 // max_tiles: most 16-token tiles that a query sees, or 0 to cut the segments as a.splits says.
@@ -244,18 +226,45 @@ kvattn_status launch_decode_window(const DecodeArgs& a, int32_t max_tiles, cudaS
 // The one-launch form, where it is the faster one (else false, nothing launched).
 bool launch_decode_direct(const DecodeArgs& a, int32_t max_tiles, cudaStream_t s, kvattn_status* st);
 
-// Over the shared prefixes, into a.prefix, a.prefix_o and a.prefix_ml (decode_shared.cu), ...
-kvattn_status launch_decode_shared(const DecodeArgs& a, cudaStream_t s);
-// ... and then over each sequence's own keys, with the merge.
-kvattn_status launch_decode_own(const DecodeArgs& a, cudaStream_t s);
-// Most groups of a call that reads prefixes once (others read each sequence by itself).
-constexpr int32_t kMaxGroups = 512;
-// Partial results of the prefix kernel that a call may need: one per range, and one
-// more per (rows of a group, KV head).  Groups of fewer than two sequences share nothing.
-inline int64_t prefix_pieces(int32_t hq, int32_t hkv, int32_t batch, int32_t num_groups, int32_t ctas)
+// Decode that reads shared prefixes once (decode_shared.cu).
+// Where a sequence's partial results are.  Shared 16-token pages form a stream that is
+// cut into ranges of `per` pages, one per CTA; own ones another, cut into ranges of own_per
+// pages, one per warp.  The pages of a (row block of a group, KV head) or (sequence, KV
+// head) are contiguous, and a piece is what of them lies in one range.  The shared pages of
+// (the sequence's row block, KV head h) are first + h head_pages .. + pages - 1 (pages 0:
+// it shares nothing), and the piece of range c is rows (c + segment + h head_segments)
+// kSharedRows + row .. of SharedArgs::o and ml.  The own pages are own_first + h own_pages
+// .. + own_pages - 1, and the piece of range c rows (c + b Hkv + h) G .. of own_o and own_ml.
+struct SharedOf {
+    int32_t first, pages, head_pages, segment;
+    int32_t head_segments, row, own_first, own_pages;
+    int32_t per, own_per, pad[2];
+};
+constexpr int kSharedRows = 256;    // of a prefix piece
+constexpr int kMostOwnWarps = 16;   // of a CTA
+struct SharedArgs {
+    DecodeArgs d;                   // (nslots, part_o, part_ml, splits unused)
+    const int32_t* cu_groups;
+    const int32_t* shared_lens;
+    int32_t num_groups, max_shared;
+    SharedOf* of;                   // [batch]
+    float *o, *ml;                  // prefix pieces: [rows][d], not divided by their sums; [rows][2] (max in log2 units, sum)
+    float *own_o, *own_ml;          // own pieces
+};
+kvattn_status launch_decode_shared(const SharedArgs& a, cudaStream_t s);
+// Most groups and sequences of a call that reads prefixes once (others read each
+// sequence by itself): the kernel keeps them in shared memory.
+constexpr int32_t kMaxGroups = 256, kMaxSharedBatch = 2048;
+// Pieces that a call may have: one per range, and one more per segment.  Groups of
+// fewer than two sequences share nothing.
+inline int64_t shared_pieces(int32_t hq, int32_t hkv, int32_t batch, int32_t num_groups, int32_t ctas)
 {
     const int64_t g = hq / hkv, groups = num_groups < batch / 2 ? num_groups : batch / 2;
-    return ctas + (batch * g / kPrefixRows + groups) * hkv;
+    return ctas + (batch * g / kSharedRows + groups) * hkv;
+}
+inline int64_t own_pieces(int32_t hkv, int32_t batch, int32_t ctas)
+{
+    return (int64_t)ctas * kMostOwnWarps + (int64_t)batch * hkv;
 }
 
 // Largest decode batch (the kernels keep a per-sequence prefix sum in shared memory).

@@ -5,6 +5,7 @@
 
 #include <mutex>
 
+#include "fast_exp2.cuh"
 #include "kvattn_tc.cuh"
 
 namespace kvattn {
@@ -44,15 +45,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 {
     const bool ok = wait_or_abort(bar, parity, abort_flag, status);
     return __all_sync(0xffffffffu, ok);
-}
-
-// 2^x (ex2.approx.ftz: a few ulp, far below the bf16 rounding that P goes
-// through); 2^-inf = 0.
-__device__ __forceinline__ float fast_exp2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c)
