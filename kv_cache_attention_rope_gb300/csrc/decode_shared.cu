@@ -36,10 +36,13 @@
 // of S in TMEM; warps 12-15 the outputs.  TMEM: S_0, S_1, O_0, O_1, 128 columns each.
 //
 // Own keys (own_warp): the pages of all (sequence, KV head) segments form a stream
-// too, cut into equal ranges, one per warp.  A warp brings its pages into a ring of its
-// own by TMA, multiplies them with mma.sync (the group's heads as rows 0..7 of the
-// fragments) and writes a state where a segment ends: no warp waits for another,
-// and nothing is paid per segment but its state.
+// too, cut into equal ranges, one per warp.  A warp loads its pages straight from
+// global memory into mma.sync fragments (bf16_tile.cuh), a page ahead, and writes a
+// state where a segment ends: no warp waits for another, and nothing is paid per
+// segment but its state.  That takes 230 registers, so eight warps of the CTA do it
+// and the others give theirs up.  (Twelve warps with rings in shared memory: a page took
+// 1500 cycles of work and 2000 to issue its cp.async copies, or as long for its two TMA
+// boxes; own parts of 64 sequences of up to 4096, 537 MB: 123 and 113 us.)
 //
 // Every wait on a barrier is bounded: a timeout records KVATTN_ERR_TIMEOUT, the
 // roles stop waiting, drain their copies and MMAs, free TMEM and return.
@@ -48,6 +51,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "bf16_tile.cuh"
 #include "tc_roles.cuh"
 
 namespace kvattn {
@@ -69,6 +73,8 @@ static_assert(kMaxGroups <= kThreads && kMaxSharedBatch % kThreads == 0, "a thre
 // Registers per thread of the warpgroups (the block starts with 128 each:
 // 96 + 2 x 168 + 80 = 4 x 128).
 constexpr int kRegsIssue = 96, kRegsSoftmax = 168, kRegsOutput = 80;
+constexpr int kRegsOwn = 232, kRegsIdle = 24;  // 2 x 232 + 2 x 24 = 4 x 128
+constexpr int kOwnWarps = 8;  // of a CTA on own keys: warps 4 .. 11
 
 // Barriers of a CTA on prefixes.
 struct Bars {
@@ -110,15 +116,9 @@ struct Geo {
     // fp32: row maxima of a tile [2][2 halves][128]; of kPast pieces, row sums [2 halves][2][128] and maxima [2][128]
     static constexpr int kOffX = kOffBar + 256;
     static constexpr int kPrefixEnd = kOffX + 2048 + kPast * 3072;
-    // own keys: every warp's ring, then its barriers
-    static constexpr int kOwnWarps = kD == 128 ? 12 : 16;
-    static constexpr int kOwnRing = kD == 128 ? 2 : 3;
-    static constexpr int kOffOwnBar = kOwnWarps * kOwnRing * 2 * kPageBytes;
-    static constexpr int kOwnEnd = kOffOwnBar + kOwnWarps * kOwnRing * 8;
-    static constexpr int kOffPlan = (kPrefixEnd > kOwnEnd ? kPrefixEnd : kOwnEnd);
+    static constexpr int kOffPlan = kPrefixEnd;
     static constexpr int kSmemBytes = kOffPlan + (int)sizeof(Plan) + 1024;  // + slack to align the base to 1 KB
     static_assert(kD == 64 || kD == 128, "head dim");
-    static_assert(kOwnWarps <= kMostOwnWarps && kOwnWarps <= kThreads / 32, "own warps");
 };
 
 struct Maps {
@@ -722,23 +722,17 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
 
 // Range `c` of the own pages, begin .. end - 1, by this warp.
 template <int kHD>
-__device__ __forceinline__ void own_warp(const SharedArgs& a, const Maps& maps, const Plan& P, int c, int begin, int end,
-                                         int lg, unsigned char* ring, uint64_t* full)
+__device__ __forceinline__ void own_warp(const SharedArgs& a, const Plan& P, int c, int begin, int end, int lg)
 {
-    using GE = Geo<kHD>;
-    constexpr int kRing = GE::kOwnRing, kPageBytes = GE::kPageBytes;
-    constexpr int kGroup = 8 * kHD * 2;  // 8 rows of a page, all panels
     const int lane = threadIdx.x & 31, g4 = lane >> 2, q4 = lane & 3;
-    const int mi = lane >> 3, rr = lane & 7;  // ldmatrix: matrix and row this lane addresses
     const int G = 1 << lg, hkv = a.d.hkv, n = end - begin;
-    const uint64_t pol = l2_evict_first_policy();
-    // Lane i looks up page i of a batch of 32: its segment b Hkv + h, its row in the pool
-    // (-1: none), how many of its tokens are keys, and whether its segment ends.
+    // Lane i looks up page i of a batch of 32: its segment b Hkv + h, its row in the pool,
+    // how many of its tokens are keys (0: its block is not there), and whether its segment ends.
     struct Page {
         int seg, row, info;
     };
     auto look_up = [&](int base) {
-        Page pg{0, -1, 0};
+        Page pg{0, 0, 0};
         const int r = begin + base + lane;
         if (r >= end) return pg;
         int b = 0;  // the last sequence with Hkv own[b] <= r
@@ -761,145 +755,95 @@ __device__ __forceinline__ void own_warp(const SharedArgs& a, const Maps& maps, 
         }
         return pg;
     };
-    Page now = look_up(0), next = look_up(32);  // batches j / 32 and the one after
-    int batch = 0;
-    auto get = [&](int Page::*f, int j) { return __shfl_sync(0xffffffffu, (j >> 5 == batch ? now : next).*f, j & 31); };
-    auto fetch = [&](int j) {  // page j on its way to its place in the ring
-        if (j >= n) return;
-        const int row = get(&Page::row, j);
-        if (lane == 0) {
-            uint64_t* bar = &full[j % kRing];
-            unsigned char* dst = ring + j % kRing * (2 * kPageBytes);
-            if (row >= 0) {
-                mbar_arrive_expect_tx(bar, 2 * kPageBytes);
-                copy_page<kHD>(dst, &maps.k, row, bar, pol);
-                copy_page<kHD>(dst + kPageBytes, &maps.v, row, bar, pol);
-            } else {
-                mbar_arrive(bar);
-            }
+    Page page = look_up(0);
+    // the group's queries as B fragments: head g4, the dims in the order of K's chunks
+    uint32_t q[kHD / 16][2], qn[kHD / 16][2];
+    auto load_q = [&](int seg) {
+        const __nv_bfloat16* qh = reinterpret_cast<const __nv_bfloat16*>(a.d.q) + (((int64_t)seg << lg) + g4) * kHD;
+#pragma unroll
+        for (int i = 0; i < kHD / 32; ++i) {
+            const uint4 w = g4 < G ? ldg16(qh + 8 * (q4 + 4 * i)) : make_uint4(0, 0, 0, 0);
+            qn[2 * i][0] = w.x;
+            qn[2 * i][1] = w.y;
+            qn[2 * i + 1][0] = w.z;
+            qn[2 * i + 1][1] = w.w;
         }
     };
-#pragma unroll
-    for (int j = 0; j < kRing; ++j) fetch(j);
-    // Q rows g4 (heads of the segment's group) as A fragments: columns 2 q4 .. and 8 + 2 q4
-    // .. of each k-step
-    uint32_t qa[kHD / 16][2], qn[kHD / 16][2];
-    auto load_q = [&](int seg, uint32_t (&q)[kHD / 16][2]) {
-        const uint32_t* row = reinterpret_cast<const uint32_t*>(reinterpret_cast<const __nv_bfloat16*>(a.d.q) +
-                                                                (((int64_t)seg << lg) + g4) * kHD);
-#pragma unroll
-        for (int i = 0; i < kHD / 16; ++i) {
-            q[i][0] = g4 < G ? __ldg(row + 8 * i + q4) : 0u;
-            q[i][1] = g4 < G ? __ldg(row + 8 * i + 4 + q4) : 0u;
-        }
+    const char *kp = (const char*)a.d.k_pool, *vp = (const char*)a.d.v_pool;
+    Bf16Tile<kHD> t;
+    uint4 v[2][4][kHD / 64];
+    int seg = __shfl_sync(0xffffffffu, page.seg, 0), info = __shfl_sync(0xffffffffu, page.info, 0);
+    auto seen_of = [](int info) { return (1u << (info & 31)) - 1u; };
+    auto load = [&](int j, uint4 (&vv)[4][kHD / 64]) {
+        const int64_t row = __shfl_sync(0xffffffffu, page.row, j & 31);
+        t.load_k(kp + row * (kHD * 2), seen_of(info), g4, q4);
+        t.load_v(vv, vp + row * (kHD * 2), seen_of(info), g4, q4);
     };
-    load_q(get(&Page::seg, 0), qn);
-    float o[kHD / 8][2], m_run = -INFINITY, l_run = 0.f;
+    load(0, v[0]);
+    load_q(seg);
+    Softmax st;
+    float o[kHD / 16][4];
     bool fresh = true;
-    for (int j = 0; j < n; ++j) {
-        if (j >> 5 != batch) {
-            ++batch;
-            now = next;
-            next = look_up((batch + 1) * 32);
-        }
-        const int seg = get(&Page::seg, j), info = get(&Page::info, j), keys = info & 31;
+    auto step = [&](int j, const uint4 (&vnow)[4][kHD / 64], uint4 (&vnext)[4][kHD / 64]) {
         if (fresh) {
 #pragma unroll
             for (int i = 0; i < kHD / 16; ++i) {
-                qa[i][0] = qn[i][0];
-                qa[i][1] = qn[i][1];
+                q[i][0] = qn[i][0];
+                q[i][1] = qn[i][1];
+                o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
             }
-#pragma unroll
-            for (int i = 0; i < kHD / 8; ++i) o[i][0] = o[i][1] = 0.f;
-            m_run = -INFINITY;
-            l_run = 0.f;
+            st.init();
         }
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        t.scores(s, q);
+        // the next page flies during this page's softmax and P.V, and so do the next
+        // segment's queries
+        const uint32_t now = seen_of(info);
+        const int seg_now = seg;
         fresh = info & 32;
-        if (fresh && j + 1 < n) load_q(get(&Page::seg, j + 1), qn);  // (on its way during this page)
-        if (!__all_sync(0xffffffffu, mbar_wait(&full[j % kRing], (j / kRing) & 1, a.d.status))) {
-            // nothing more is waited for but the copies under way
-            if (lane == 0)
-                for (int u = j + 1; u < min(n, j + kRing); ++u) mbar_wait(&full[u % kRing], (u / kRing) & 1, a.d.status);
-            __syncwarp();
-            return;
+        if (j + 1 < n) {
+            if (((j + 1) & 31) == 0) page = look_up(j + 1);
+            seg = __shfl_sync(0xffffffffu, page.seg, (j + 1) & 31);
+            info = __shfl_sync(0xffffffffu, page.info, (j + 1) & 31);
+            load(j + 1, vnext);
+            if (fresh) load_q(seg);
         }
-        unsigned char* kst = ring + j % kRing * (2 * kPageBytes);
-        unsigned char* vst = kst + kPageBytes;
-        if (keys > 0) {
-            // V rows past the last key are stale: their p is 0, but 0 * NaN would be NaN
-            if (keys < kPage) {
-                constexpr int kChunks = kHD / 8;
-                for (int i = keys * kChunks + lane; i < kPage * kChunks; i += 32) {
-                    const int row = i / kChunks, ch = i % kChunks;
-                    *reinterpret_cast<uint4*>(vst + (row >> 3) * kGroup + (ch >> 3) * 1024 + (row & 7) * 128 + (ch & 7) * 16) =
-                        make_uint4(0, 0, 0, 0);
-                }
-                fence_async_smem();  // before the next copy into this place
-                __syncwarp();
-            }
-            // 16-byte chunk c of row r at chunk (c ^ r) of its 128 B (r = row mod 8)
-            const uint32_t kb = smem_addr(kst), vb = smem_addr(vst);
-            float s0[2] = {0.f, 0.f}, s1[2] = {0.f, 0.f};  // tokens 0-7, 8-15
-#pragma unroll
-            for (int i = 0; i < kHD / 16; ++i) {
-                // matrices (tokens 0-7, chunk 2i), (0-7, 2i+1), (8-15, 2i), (8-15, 2i+1)
-                const int ch = 2 * i + (mi & 1);
-                uint32_t b[4];
-                ldmatrix_x4(b, kb + (mi >> 1) * kGroup + (ch >> 3) * 1024 + rr * 128 + (((ch & 7) ^ rr) << 4));
-                mma_bf16_16816_top(s0, qa[i][0], qa[i][1], b[0], b[1]);
-                mma_bf16_16816_top(s1, qa[i][0], qa[i][1], b[2], b[3]);
-            }
-            // row g4: tokens 2q4, 2q4+1 (s0) and 8+2q4, 9+2q4 (s1), in log2 units
-            const float sl2 = a.d.scale_log2;
-            float x[4] = {s0[0] * sl2, s0[1] * sl2, s1[0] * sl2, s1[1] * sl2};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (2 * q4 + (e & 1) + 8 * (e >> 1) >= keys) x[e] = -INFINITY;
-            float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // the maximum is raised when a page's exceeds it by more than 2^8
-            if (top > m_run + 8.f) {
-                const float f = m_run == -INFINITY ? 0.f : fast_exp2(m_run - top);
-                m_run = top;
-                l_run *= f;
-#pragma unroll
-                for (int i = 0; i < kHD / 8; ++i) {
-                    o[i][0] *= f;
-                    o[i][1] *= f;
-                }
-            }
-            // (scores that are all -inf so far have no weight)
-            const float m0 = m_run == -INFINITY ? 0.f : m_run;
-            const float p0 = fast_exp2(x[0] - m0), p1 = fast_exp2(x[1] - m0);
-            const float p2 = fast_exp2(x[2] - m0), p3 = fast_exp2(x[3] - m0);
-            l_run += (p0 + p1) + (p2 + p3);
-            // P in bf16, the type of V that the MMA takes it with: off by at most 2^-8
-            // relative, at random; the sum adds the fp32 p
-            const uint32_t pa0 = pack_bf16_rn(p0, p1), pa2 = pack_bf16_rn(p2, p3);
-#pragma unroll
-            for (int i = 0; i < kHD / 16; ++i) {
-                // V^T: matrices (tokens 0-7, chunk 2i), (8-15, 2i), (0-7, 2i+1), (8-15, 2i+1)
-                const int ch = 2 * i + (mi >> 1);
-                uint32_t b[4];
-                ldmatrix_x4_trans(b, vb + (mi & 1) * kGroup + (ch >> 3) * 1024 + rr * 128 + (((ch & 7) ^ rr) << 4));
-                mma_bf16_16816_top(o[2 * i], pa0, pa2, b[0], b[1]);
-                mma_bf16_16816_top(o[2 * i + 1], pa0, pa2, b[2], b[3]);
-            }
-        }
-        __syncwarp();  // every lane has read the page
-        fetch(j + kRing);
+        const float sl2 = a.d.scale_log2;
+        const float x[4] = {now >> g4 & 1u ? s[0] * sl2 : -INFINITY, now >> g4 & 1u ? s[1] * sl2 : -INFINITY,
+                            now >> (g4 + 8) & 1u ? s[2] * sl2 : -INFINITY,
+                            now >> (g4 + 8) & 1u ? s[3] * sl2 : -INFINITY};
+        float p[4];
+        st.step(x, o, p);
+        // P in bf16, the type of V that the MMA takes it with: off by at most 2^-8 relative,
+        // at random; the sum adds the fp32 p
+        t.add(vnow, o, movmatrix_trans(pack_bf16_rn(p[0], p[1])), movmatrix_trans(pack_bf16_rn(p[2], p[3])));
         if (fresh) {  // the segment's end, or the range's: its state
-            l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
-            l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
-            const int64_t row = (((int64_t)c + seg) << lg) + g4;
-            if (g4 < G) {
-                float* out = a.own_o + row * kHD + 2 * q4;
 #pragma unroll
-                for (int i = 0; i < kHD / 8; ++i) *reinterpret_cast<float2*>(out + 8 * i) = make_float2(o[i][0], o[i][1]);
-                if (q4 == 0) *reinterpret_cast<float2*>(a.own_ml + row * 2) = make_float2(m_run, l_run);
+            for (int i = 4; i < 32; i <<= 1) {
+                st.l[0] += __shfl_xor_sync(0xffffffffu, st.l[0], i);
+                st.l[1] += __shfl_xor_sync(0xffffffffu, st.l[1], i);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int g = 2 * q4 + e;
+                if (g >= G) continue;
+                const int64_t row = (((int64_t)c + seg_now) << lg) + g;
+                float* out = a.own_o + row * kHD;
+                // the lane's dims dim_of(i, half) are neighbours in i
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int i = 0; i < kHD / 16; i += 4)
+                        *reinterpret_cast<float4*>(out + Bf16Tile<kHD>::dim_of(i, half, g4)) =
+                            make_float4(o[i][2 * half + e], o[i + 1][2 * half + e], o[i + 2][2 * half + e],
+                                        o[i + 3][2 * half + e]);
+                if (g4 == 0) *reinterpret_cast<float2*>(a.own_ml + row * 2) = make_float2(st.m[e], st.l[e]);
             }
         }
+    };
+    for (int j = 0; j < n; j += 2) {
+        step(j, v[0], v[1]);
+        if (j + 1 < n) step(j + 1, v[1], v[0]);
     }
 }
 
@@ -915,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lg = __ffs(a.d.hq / a.d.hkv) - 1;  // row r of a prefix piece: sequence r >> lg, head r & (G - 1)
     make_plan(a, P, lg);
     const int shared = P.first[a.num_groups], own = a.d.hkv * P.own[a.d.batch];
-    const Ranges ranges = ranges_of(shared, own, gridDim.x, 180000.f / (2 * GE::kPageBytes), GE::kOwnWarps);
+    const Ranges ranges = ranges_of(shared, own, gridDim.x, 180000.f / (2 * GE::kPageBytes), kOwnWarps);
     // where the merge finds each sequence's partial results
     for (int b = (int)blockIdx.x + (int)gridDim.x * threadIdx.x; b < a.d.batch; b += (int)gridDim.x * kThreads) {
         SharedOf o{};
@@ -942,17 +886,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (r < end) prefix_cta<kHD>(a, maps, P, Walk{r, end, 0}, lg, smem);
     } else {
         const int warp = threadIdx.x >> 5;
-        if (warp >= GE::kOwnWarps) return;
-        const int c = ((int)blockIdx.x - ranges.ctas) * GE::kOwnWarps + warp;
-        const int r = min(own, c * ranges.own_per), end = min(own, r + ranges.own_per);
-        if (r >= end) return;
-        uint64_t* full = reinterpret_cast<uint64_t*>(smem + GE::kOffOwnBar) + warp * GE::kOwnRing;
-        if ((threadIdx.x & 31) == 0) {
-            for (int s = 0; s < GE::kOwnRing; ++s) mbar_init(&full[s], 1);
-            fence_mbar_init();
+        if (warp < 4 || warp >= 4 + kOwnWarps) {
+            setmaxnreg_dec<kRegsIdle>();
+            return;
         }
-        __syncwarp();
-        own_warp<kHD>(a, maps, P, c, r, end, lg, smem + warp * GE::kOwnRing * 2 * GE::kPageBytes, full);
+        setmaxnreg_inc<kRegsOwn>();
+        const int c = ((int)blockIdx.x - ranges.ctas) * kOwnWarps + warp - 4;
+        const int r = min(own, c * ranges.own_per), end = min(own, r + ranges.own_per);
+        if (r < end) own_warp<kHD>(a, P, c, r, end, lg);
     }
 }
 

@@ -241,7 +241,7 @@ struct SharedOf {
     int32_t per, own_per, pad[2];
 };
 constexpr int kSharedRows = 256;    // of a prefix piece
-constexpr int kMostOwnWarps = 16;   // of a CTA
+constexpr int kMostOwnWarps = 16;   // ranges of own pages per CTA, at most
 struct SharedArgs {
     DecodeArgs d;                   // (nslots, part_o, part_ml, splits unused)
     const int32_t* cu_groups;

@@ -96,6 +96,18 @@ def test_long_prefix(kvattn_lib, dtype, hq, hkv, d):
     _run(kvattn_lib, dtype, hq, hkv, d, [(9000, [9001, 9300, 9017])], seed=3)
 
 
+@pytest.mark.parametrize("dtype,hq,hkv,d", [("bf16", 16, 4, 128), ("bf16", 4, 4, 64), ("bf16", 8, 1, 64), ("fp8", 8, 1, 128),
+                                            ("bf16", 2, 1, 128)])
+@pytest.mark.parametrize("groups", [
+    [(300, [301, 5000, 310, 4396, 4397]), (0, [4500])],
+    [(5000, [5001, 5100, 9200, 0]), (64, [4160, 4161, 4159, 70])],
+    [(16, [5000, 17, 16])],
+])
+def test_long_own_parts(kvattn_lib, dtype, hq, hkv, d, groups):
+    """Sequences with many keys of their own, cut into many pieces, beside ones with few."""
+    _run(kvattn_lib, dtype, hq, hkv, d, groups, seed=hkv)
+
+
 @pytest.mark.parametrize("dtype,hq,hkv,d", [("bf16", 8, 2, 128), ("bf16", 4, 4, 64), ("fp8", 8, 2, 128), ("f32", 4, 2, 64)])
 def test_growing_scores(kvattn_lib, dtype, hq, hkv, d):
     """Keys that grow along the sequence: the maximum rises tile by tile, and lies in the prefix or in the own tokens."""
