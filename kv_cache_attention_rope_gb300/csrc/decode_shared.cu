@@ -64,8 +64,10 @@ constexpr int kPages = kBN / kPage;
 constexpr int kThreads = 512;
 constexpr int kStages = 2;     // of K, of V and of Q tiles
 constexpr int kPanel = kBM * 128;  // 16 KB: 128 rows x 64 columns (one 128-byte swizzle panel of Q)
+constexpr int kMinShared = 128;  // tokens of a prefix that is worth pieces of its own
 constexpr int kMinPer = 8;     // fewest shared pages of a CTA's range
 constexpr int kMinOwn = 2;     // fewest own pages of a warp's range
+constexpr float kSetUpBytes = 180000.f, kSegmentBytes = 80000.f, kOwnWeight = 1.0f;  // of K and V that take as long (ranges_of)
 constexpr int kPast = 4;       // pieces whose sums may be waiting for the output warps
 constexpr int kSeqs = kMaxSharedBatch / kThreads;  // sequences a thread plans
 static_assert(kSharedRows == 2 * kBM, "a prefix piece's rows");
@@ -148,73 +150,63 @@ __device__ __forceinline__ int group_of(const Plan& P, int n, int b)
     return g;
 }
 
-// Fills the plan from the call's arguments (every CTA does).  Groups that are out of
-// order or out of range share nothing, nor does a group of which fewer than two
-// sequences have the prefix.
-__device__ __forceinline__ void make_plan(const SharedArgs& a, Plan& P, int lg)
+// Fills the plan from the call's arguments (every CTA does), and `len` with the
+// sequences' lengths, 0 for one out of range.  Groups that are out of order or out of
+// range share nothing, nor does a prefix of fewer than kMinShared tokens, or of which
+// fewer than two sequences have it all.
+__device__ __forceinline__ void make_plan(const SharedArgs& a, Plan& P, int* len, int lg)
 {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.num_groups;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.num_groups, b0 = tid * kSeqs;
     const int64_t room = (int64_t)a.d.max_blocks * a.d.block_size;
-    int len[kSeqs];
+    int L[kSeqs];
 #pragma unroll
-    for (int j = 0; j < kSeqs; ++j) {
-        const int b = j * kThreads + tid;
-        len[j] = b < a.d.batch ? a.d.seq_lens[b] : 0;
-    }
+    for (int j = 0; j < kSeqs; ++j) L[j] = b0 + j < a.d.batch ? a.d.seq_lens[b0 + j] : 0;
     bool ok = true;
     if (tid < n) {
         const int c0 = a.cu_groups[tid], c1 = a.cu_groups[tid + 1], s = a.shared_lens[tid];
         ok = c0 >= 0 && c1 >= c0 && c1 <= a.d.batch && s >= 0 && s <= a.max_shared && (tid > 0 || c0 == 0) && s <= room;
         P.cu[tid] = c0;
         if (tid == n - 1) P.cu[n] = c1;
-        P.tokens[tid] = s & ~(kPage - 1);
+        P.tokens[tid] = s >= kMinShared ? s & ~(kPage - 1) : 0;
         P.leader[tid] = INT_MAX;
         P.members[tid] = 0;
     }
 #pragma unroll
     for (int j = 0; j < kSeqs; ++j) {
-        if (len[j] < 0 || len[j] > a.d.max_seq_len || len[j] > room) {
+        if (L[j] < 0 || L[j] > a.d.max_seq_len || L[j] > room) {
             if (blockIdx.x == 0) record_error(a.d.status, KVATTN_ERR_BAD_INDEX);
-            len[j] = 0;
+            L[j] = 0;
         }
+        if (b0 + j < a.d.batch) len[b0 + j] = L[j];
     }
     ok = __syncthreads_and(ok);
     if (!ok && blockIdx.x == 0 && tid == 0) record_error(a.d.status, KVATTN_ERR_BAD_INDEX);
-    int group[kSeqs];  // -1: none
+    int group[kSeqs];  // -1: none that it shares with
 #pragma unroll
     for (int j = 0; j < kSeqs; ++j) {
-        const int b = j * kThreads + tid;
-        group[j] = ok && b < P.cu[n] ? group_of(P, n, b) : -1;
-        if (group[j] >= 0 && P.tokens[group[j]] > 0 && len[j] >= P.tokens[group[j]]) {
-            atomicMin(&P.leader[group[j]], b);
-            atomicAdd(&P.members[group[j]], 1);
-        } else {
-            group[j] = -1;
+        group[j] = -1;
+        if (ok && b0 + j < P.cu[n]) {
+            const int g = group_of(P, n, b0 + j);
+            if (P.tokens[g] > 0 && L[j] >= P.tokens[g]) {
+                group[j] = g;
+                atomicMin(&P.leader[g], b0 + j);
+                atomicAdd(&P.members[g], 1);
+            }
         }
     }
     __syncthreads();
-    int v[3] = {0, 0, 0};  // pages of a group, its segments; own pages of this thread's next kSeqs sequences
+    auto shared = [&](int g) { return ok && P.members[g] >= 2 ? P.tokens[g] / kPage : 0; };  // pages
+    int v[3] = {0, 0, 0};  // pages of a group, its segments; own pages of this thread's sequences
+    int tokens = 0;
     if (tid < n) {
-        if (!ok || P.members[tid] < 2) P.tokens[tid] = 0;
-        if (P.tokens[tid] > 0) {
-            v[1] = blocks_of(P.cu[tid + 1] - P.cu[tid], lg) * a.d.hkv;
-            v[0] = v[1] * (P.tokens[tid] / kPage);
-        }
+        tokens = shared(tid) * kPage;
+        v[1] = tokens > 0 ? blocks_of(P.cu[tid + 1] - P.cu[tid], lg) * a.d.hkv : 0;
+        v[0] = v[1] * (tokens / kPage);
     }
-    __syncthreads();
-    // own pages, for a moment in the places of the sums
-#pragma unroll
-    for (int j = 0; j < kSeqs; ++j) {
-        const int b = j * kThreads + tid;
-        if (b < a.d.batch) P.own[b + 1] = (len[j] + kPage - 1) / kPage - (group[j] >= 0 ? P.tokens[group[j]] / kPage : 0);
-    }
-    __syncthreads();
     int own[kSeqs];
 #pragma unroll
-    for (int j = 0; j < kSeqs; ++j) {
-        const int b = tid * kSeqs + j;
-        own[j] = v[2] += b < a.d.batch ? P.own[b + 1] : 0;
-    }
+    for (int j = 0; j < kSeqs; ++j)
+        own[j] = v[2] += (L[j] + kPage - 1) / kPage - (group[j] >= 0 ? shared(group[j]) : 0);
     const int mine = v[2];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1)
@@ -227,18 +219,18 @@ __device__ __forceinline__ void make_plan(const SharedArgs& a, Plan& P, int lg)
 #pragma unroll
         for (int i = 0; i < 3; ++i) P.sums[i][warp] = v[i];
     __syncthreads();
-    for (int w = 0; w < warp; ++w)
 #pragma unroll
-        for (int i = 0; i < 3; ++i) v[i] += P.sums[i][w];
+    for (int w = 0; w < kThreads / 32; ++w)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) v[i] += w < warp ? P.sums[i][w] : 0;
     if (tid < n) {
         P.first[tid + 1] = v[0];
         P.segment[tid + 1] = v[1];
+        P.tokens[tid] = tokens;
     }
 #pragma unroll
-    for (int j = 0; j < kSeqs; ++j) {
-        const int b = tid * kSeqs + j;
-        if (b < a.d.batch) P.own[b + 1] = v[2] - mine + own[j];
-    }
+    for (int j = 0; j < kSeqs; ++j)
+        if (b0 + j < a.d.batch) P.own[b0 + j + 1] = v[2] - mine + own[j];
     if (tid == 0) P.first[0] = P.segment[0] = P.own[0] = 0;
     __syncthreads();
 }
@@ -247,16 +239,18 @@ __device__ __forceinline__ void make_plan(const SharedArgs& a, Plan& P, int lg)
 struct Ranges {
     int ctas, per, own_per;
 };
-// Both kinds of CTA take about as long per page, and those on prefixes `more` pages'
-// time besides (tensor-core set-up, 256 rows of output): with t pages' time for all,
-// shared / (t - more) + own / t = ctas.
-__device__ __forceinline__ Ranges ranges_of(int shared, int own, int ctas, float more, int warps)
+// In times of a shared page: an own page takes kOwnWeight, a prefix CTA `set_up` besides
+// its pages (tensor memory, the pipeline's filling) and `segment` for each of its
+// segments (256 rows of output); so with t for all,
+// (shared + segment segments) / (t - set_up) + kOwnWeight own / t = ctas.
+__device__ __forceinline__ Ranges ranges_of(int shared, int segments, int own, int ctas, float set_up, float segment,
+                                            int warps)
 {
     Ranges r{0, 0, 0};
     if (shared > 0) {
-        const float c = (float)ctas, p = (float)shared, o = (float)own, u = more * c + p + o;
-        const float t = (u + sqrtf(fmaxf(u * u - 4.f * c * more * o, 0.f))) / (2.f * c);
-        r.ctas = min((int)ceilf(p / fmaxf(t - more, 1.f)), (shared + kMinPer - 1) / kMinPer);
+        const float c = (float)ctas, p = (float)shared + segment * (float)segments, o = kOwnWeight * (float)own, u = set_up * c + p + o;
+        const float t = (u + sqrtf(fmaxf(u * u - 4.f * c * set_up * o, 0.f))) / (2.f * c);
+        r.ctas = min((int)ceilf(p / fmaxf(t - set_up, 1.f)), (shared + kMinPer - 1) / kMinPer);
         r.ctas = max(1, min(r.ctas, own > 0 ? ctas - 1 : ctas));
         r.per = (shared + r.ctas - 1) / r.ctas;
     }
@@ -334,6 +328,7 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
         fence_mbar_init();
     }
     if (warp == 1) tmem_alloc(&B.tmem, 512);
+    fence_async_smem();  // (the lengths were where copies go now)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -722,7 +717,7 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
 
 // Range `c` of the own pages, begin .. end - 1, by this warp.
 template <int kHD>
-__device__ __forceinline__ void own_warp(const SharedArgs& a, const Plan& P, int c, int begin, int end, int lg)
+__device__ __forceinline__ void own_warp(const SharedArgs& a, const Plan& P, const int* lens, int c, int begin, int end, int lg)
 {
     const int lane = threadIdx.x & 31, g4 = lane >> 2, q4 = lane & 3;
     const int G = 1 << lg, hkv = a.d.hkv, n = end - begin;
@@ -741,7 +736,7 @@ __device__ __forceinline__ void own_warp(const SharedArgs& a, const Plan& P, int
             if (hkv * P.own[b + half] <= r) b += half;
             m -= half;
         }
-        const int pages = P.own[b + 1] - P.own[b], in = r - hkv * P.own[b], h = in / pages, len = a.d.seq_lens[b];
+        const int pages = P.own[b + 1] - P.own[b], in = r - hkv * P.own[b], h = in / pages, len = lens[b];
         const int left = pages - (in - h * pages);  // pages up to the segment's end
         const int tok = ((len + kPage - 1) / kPage - left) * kPage;
         const int32_t blk = a.d.block_table[(int64_t)b * a.d.max_blocks + tok / a.d.block_size];
@@ -857,9 +852,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     Plan& P = *reinterpret_cast<Plan*>(smem + GE::kOffPlan);
     const int lg = __ffs(a.d.hq / a.d.hkv) - 1;  // row r of a prefix piece: sequence r >> lg, head r & (G - 1)
-    make_plan(a, P, lg);
+    int* len = reinterpret_cast<int*>(smem);  // (where Q will be)
+    make_plan(a, P, len, lg);
     const int shared = P.first[a.num_groups], own = a.d.hkv * P.own[a.d.batch];
-    const Ranges ranges = ranges_of(shared, own, gridDim.x, 180000.f / (2 * GE::kPageBytes), kOwnWarps);
+    const Ranges ranges = ranges_of(shared, P.segment[a.num_groups], own, gridDim.x, kSetUpBytes / (2 * GE::kPageBytes),
+                                    kSegmentBytes / (2 * GE::kPageBytes), kOwnWarps);
     // where the merge finds each sequence's partial results
     for (int b = (int)blockIdx.x + (int)gridDim.x * threadIdx.x; b < a.d.batch; b += (int)gridDim.x * kThreads) {
         SharedOf o{};
@@ -868,8 +865,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         o.own_first = a.d.hkv * P.own[b];
         o.own_pages = P.own[b + 1] - P.own[b];
         if (shared > 0 && b < P.cu[a.num_groups]) {
-            const int g = group_of(P, a.num_groups, b), pages = P.tokens[g] / kPage, L = a.d.seq_lens[b];
-            if (pages > 0 && L >= P.tokens[g] && L <= a.d.max_seq_len && L <= (int64_t)a.d.max_blocks * a.d.block_size) {
+            const int g = group_of(P, a.num_groups, b), pages = P.tokens[g] / kPage;
+            if (pages > 0 && len[b] >= P.tokens[g]) {
                 const int r = (b - P.cu[g]) << lg, rb = r / kSharedRows;
                 o.pages = pages;
                 o.head_segments = blocks_of(P.cu[g + 1] - P.cu[g], lg);
@@ -893,19 +890,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         setmaxnreg_inc<kRegsOwn>();
         const int c = ((int)blockIdx.x - ranges.ctas) * kOwnWarps + warp - 4;
         const int r = min(own, c * ranges.own_per), end = min(own, r + ranges.own_per);
-        if (r < end) own_warp<kHD>(a, P, c, r, end, lg);
+        if (r < end) own_warp<kHD>(a, P, len, c, r, end, lg);
     }
 }
 
-// Merges the pieces of a row: a warp per (sequence, query head), 8 pieces at a time
-// (a lane's loads of their outputs and the maxima and sums are under way together).
-template <int kHD>
+// Merges the pieces of a row (sequence, query head): kWarps warps a row, each the pieces
+// of every kWarps-th chunk of 4 (a lane's loads of their outputs and the maxima and sums are under
+// way together), then the warps' states.
+template <int kHD, int kWarps>
 __global__ void __launch_bounds__(128) decode_shared_merge_kernel(const __grid_constant__ SharedArgs a)
 {
     pdl_wait();
-    constexpr int kV = kHD / 32, kChunk = 8;
-    const int wid = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (wid >= a.d.batch * a.d.hq) return;
+    constexpr int kV = kHD / 32, kChunk = 4;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, share = warp % kWarps;
+    const int wid = blockIdx.x * (4 / kWarps) + warp / kWarps;
+    if (kWarps < 4 && wid >= a.d.batch * a.d.hq) return;
     const int G = a.d.hq / a.d.hkv, b = wid / a.d.hq, qh = wid - b * a.d.hq, h = qh / G, g = qh - h * G;
     const SharedOf s = a.of[b];
     int np = 0, no = 0;
@@ -921,7 +920,7 @@ __global__ void __launch_bounds__(128) decode_shared_merge_kernel(const __grid_c
         own0 = (int64_t)(c + b * a.d.hkv + h) * G + g;
     }
     float acc[kV] = {}, den = 0.f, top = -INFINITY;
-    for (int c0 = 0; c0 < np + no; c0 += kChunk) {
+    for (int c0 = share * kChunk; c0 < np + no; c0 += kWarps * kChunk) {
         auto row_of = [&](int c) { return c < np ? shared0 + (int64_t)c * kSharedRows : own0 + (int64_t)(c - np) * G; };
         float2 ml = make_float2(-INFINITY, 0.f);
         if (lane < kChunk && c0 + lane < np + no)
@@ -955,6 +954,31 @@ __global__ void __launch_bounds__(128) decode_shared_merge_kernel(const __grid_c
 #pragma unroll
                 for (int k = 0; k < kV; ++k) acc[k] += wi * o[i][k];
             }
+        }
+    }
+    if constexpr (kWarps > 1) {
+        __shared__ float part[kWarps][kHD], stat[kWarps][2];
+#pragma unroll
+        for (int k = 0; k < kV; ++k) part[warp][kV * lane + k] = acc[k];
+        if (lane == 0) {
+            stat[warp][0] = top;
+            stat[warp][1] = den;
+        }
+        __syncthreads();
+        if (warp > 0) return;
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, stat[w][1] == 0.f ? -INFINITY : stat[w][0]);
+        den = 0.f;
+#pragma unroll
+        for (int k = 0; k < kV; ++k) acc[k] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (stat[w][1] == 0.f) continue;
+            const float f = exp2f(stat[w][0] - m);
+            den += f * stat[w][1];
+#pragma unroll
+            for (int k = 0; k < kV; ++k) acc[k] += f * part[w][kV * lane + k];
         }
     }
     const float inv = den == 0.f ? 0.f : 1.f / den;
@@ -995,7 +1019,10 @@ kvattn_status launch(const SharedArgs& a, cudaStream_t s)
     const cudaError_t e = launch_pdl(decode_shared_kernel<kHD>, dim3((unsigned)num_sms()), dim3(kThreads), kSmem, s, a, maps);
     if (e != cudaSuccess) return KVATTN_ERR_CUDA;
     const int rows = a.d.batch * a.d.hq;
-    return cuda_status(launch_pdl(decode_shared_merge_kernel<kHD>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s, a));
+    // four warps a row where that leaves the GPU's warps room, for rows of many pieces
+    return cuda_status(rows <= 1024 ? launch_pdl(decode_shared_merge_kernel<kHD, 4>, dim3((unsigned)rows), dim3(128), 0, s, a)
+                                    : launch_pdl(decode_shared_merge_kernel<kHD, 1>, dim3((unsigned)((rows + 3) / 4)),
+                                                 dim3(128), 0, s, a));
 }
 
 }  // namespace
