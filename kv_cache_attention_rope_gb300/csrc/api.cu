@@ -929,7 +929,7 @@ kvattn_status decode_shared_any(const kvattn_config* cfg, const kvattn_cache* ca
                                           max_seq_len, 0, out);
     if (st != KVATTN_OK || batch == 0) return st;
     const SharedLayout l = shared_layout(cfg, batch, max_seq_len, num_groups, max_shared_len);
-    const bool once = l.bytes > 0 && !fp8 && cache->block_size % 16 == 0 &&
+    const bool once = l.bytes > 0 && cache->block_size % 16 == 0 &&
                       cache->num_blocks * cfg->num_kv_heads < ((int64_t)1 << 31) / cache->block_size;
     if (!once)  // every sequence by itself
         return decode_any(cfg, cache, fp8, {INT32_MAX, 0}, q, block_table, max_blocks_per_seq, seq_lens, batch,

@@ -44,6 +44,12 @@
 // 1500 cycles of work and 2000 to issue its cp.async copies, or as long for its two TMA
 // boxes; own parts of 64 sequences of up to 4096, 537 MB: 123 and 113 us.)
 //
+// fp8 pages.  On prefixes, warp 0 copies whole pages and the output warps, which have
+// time, make the operands of them: K's codes exactly in f16 (Q goes in f16 over 16), V's, in
+// the transposed order that the page has, exactly in bf16.  K's scales multiply the
+// scores' columns, V's the weights before they are rounded to bf16, whose range is the scales'
+// own.  Own keys go as in decode_direct.cu, pages through two buffers per warp.
+//
 // Every wait on a barrier is bounded: a timeout records KVATTN_ERR_TIMEOUT, the
 // roles stop waiting, drain their copies and MMAs, free TMEM and return.
 #include <algorithm>
@@ -52,6 +58,7 @@
 #include <cstring>
 
 #include "bf16_tile.cuh"
+#include "fp8_tile.cuh"
 #include "tc_roles.cuh"
 
 namespace kvattn {
@@ -69,6 +76,7 @@ constexpr int kMinPer = 8;     // fewest shared pages of a CTA's range
 constexpr int kMinOwn = 2;     // fewest own pages of a warp's range
 constexpr float kSetUpBytes = 180000.f, kSegmentBytes = 80000.f, kOwnWeight = 1.0f;  // of K and V that take as long (ranges_of)
 constexpr int kPast = 4;       // pieces whose sums may be waiting for the output warps
+constexpr int kRaw = 2;        // fp8: stages of pages
 constexpr int kSeqs = kMaxSharedBatch / kThreads;  // sequences a thread plans
 static_assert(kSharedRows == 2 * kBM, "a prefix piece's rows");
 static_assert(kMaxGroups <= kThreads && kMaxSharedBatch % kThreads == 0, "a thread per group");
@@ -76,7 +84,9 @@ static_assert(kMaxGroups <= kThreads && kMaxSharedBatch % kThreads == 0, "a thre
 // 96 + 2 x 168 + 80 = 4 x 128).
 constexpr int kRegsIssue = 96, kRegsSoftmax = 168, kRegsOutput = 80;
 constexpr int kRegsOwn = 232, kRegsIdle = 24;  // 2 x 232 + 2 x 24 = 4 x 128
-constexpr int kOwnWarps = 8;  // of a CTA on own keys: warps 4 .. 11
+// Warps of a CTA on own keys: 4 .. 11, or all of them (fp8).
+template <bool kF8>
+__host__ __device__ constexpr int own_warps() { return kF8 ? kThreads / 32 : 8; }
 
 // Barriers of a CTA on prefixes.
 struct Bars {
@@ -85,11 +95,13 @@ struct Bars {
     uint64_t s_full[2], p_full[2];
     uint64_t o_done[2], o_free[2];   // the piece's last P.V into O_z has completed; O_z has been read
     uint64_t l_full[kPast];          // maxima and row sums of a piece
+    // fp8: pages loaded, read; scales and Q converted (K and V: k_full[0], v_full[0] then)
+    uint64_t raw_full[kRaw], raw_empty[kRaw], scales[kPast], q_f16[kStages];
     uint64_t drain;
     uint32_t tmem;
     int abort_flag;
 };
-static_assert(sizeof(Bars) <= 256, "the barriers fit before the exchange area");
+static_assert(sizeof(Bars) <= 384, "the barriers fit before the exchange area");
 
 // The call's groups and sequences, and the streams of pages: group g's shared ones are
 // first[g] .. first[g+1] - 1 (its segments segment[g] ..: KV heads outermost, then
@@ -104,23 +116,28 @@ struct Plan {
     int sums[3][kThreads / 32];
 };
 
-template <int kD>
+template <int kD, bool kF8>
 struct Geo {
-    // prefixes
     static constexpr int kPanels = kD / 64;
     static constexpr int kTileBytes = kBM * kD * 2;    // a Q tile, a K stage or a V stage
     static constexpr int kGroup = 8 * kD * 2;          // one 8-key group of a stage (all panels)
     static constexpr int kPageBytes = kPage * kD * 2;  // one page of K or V
+    static constexpr int kCost = kF8 ? kF8Page : 2 * kPageBytes;  // bytes of a page of both
+    static constexpr int kRawBytes = kPages * kF8Page;
+    static constexpr int kKV = kF8 ? 1 : kStages;      // stages of K and of V
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = kStages * kTileBytes;
-    static constexpr int kOffV = kOffK + kStages * kTileBytes;
-    static constexpr int kOffBar = kOffV + kStages * kTileBytes;
+    static constexpr int kOffV = kOffK + kKV * kTileBytes;
+    static constexpr int kOffRaw = kOffV + kKV * kTileBytes;
+    static constexpr int kOffScales = kOffRaw + (kF8 ? kRaw * kRawBytes : 0);  // of kPast tiles: K's [128], V's [128]
+    static constexpr int kOffBar = kOffScales + (kF8 ? kPast * 1024 : 0);
     // fp32: row maxima of a tile [2][2 halves][128]; of kPast pieces, row sums [2 halves][2][128] and maxima [2][128]
-    static constexpr int kOffX = kOffBar + 256;
-    static constexpr int kPrefixEnd = kOffX + 2048 + kPast * 3072;
-    static constexpr int kOffPlan = kPrefixEnd;
+    static constexpr int kOffX = kOffBar + 384;
+    static constexpr int kOffPlan = kOffX + 2048 + kPast * 3072;
     static constexpr int kSmemBytes = kOffPlan + (int)sizeof(Plan) + 1024;  // + slack to align the base to 1 KB
+    static constexpr int kOffRing = 4 * kMaxSharedBatch;  // own keys, fp8: pages of the warps, behind the lengths
     static_assert(kD == 64 || kD == 128, "head dim");
+    static_assert(!kF8 || kOffRing + kThreads / 32 * 2 * kF8Page <= kOffBar, "the rings");
 };
 
 struct Maps {
@@ -298,12 +315,87 @@ struct Walk {
     }
 };
 
-template <int kHD>
+// fp8, by the 128 threads of the output warps (thread r).  Q tile `q` of the CTA, as
+// loaded: to f16 over 16, in place.
+__device__ __forceinline__ bool convert_q(Bars& B, unsigned char* tile, int q, int r, volatile int* abort_flag, int* status)
+{
+    if (!long_wait(&B.q_full[q % kStages], (q / kStages) & 1, 0, abort_flag, status)) return false;
+    uint4* p = reinterpret_cast<uint4*>(tile);
+#pragma unroll 4
+    for (int i = r; i < kBM * 128 * 2 / 16; i += 128) {
+        const uint4 v = p[i];
+        auto half2 = [](uint32_t u) { return pack_f16_rn(bf16lo(u) * 0.0625f, bf16hi(u) * 0.0625f); };
+        p[i] = make_uint4(half2(v.x), half2(v.y), half2(v.z), half2(v.w));
+    }
+    fence_async_smem();
+    mbar_arrive(&B.q_f16[q % kStages]);
+    return true;
+}
+
+// Tile g of the CTA, `pages` pages: K's codes to f16 and V's to bf16 (both exact), in
+// 64-column panels of 128 rows with 128-byte swizzle, K's rows the keys and V's the
+// dims; and the scales, K's times `mul`.
+__device__ __forceinline__ bool convert_tile(Bars& B, unsigned char* smem, float mul, int pages, int g, int r,
+                                             volatile int* abort_flag, int* status)
+{
+    using GE = Geo<128, true>;
+    const int s = g % kRaw;
+    if (!long_wait(&B.raw_full[s], (g / kRaw) & 1, 1, abort_flag, status)) return false;
+    const unsigned char* raw = smem + GE::kOffRaw + s * GE::kRawBytes;
+    float* sc = reinterpret_cast<float*>(smem + GE::kOffScales + (g % kPast) * 1024);
+    if (r < pages * kPage) {  // (the softmax has read the scales of kPast tiles ago: its P was for a P.V before this tile's S)
+        const unsigned char* pg = raw + (r >> 4) * kF8Page;
+        sc[r] = reinterpret_cast<const float*>(pg + kF8KsOff)[r & 15] * mul;
+        sc[128 + r] = reinterpret_cast<const float*>(pg + kF8VsOff)[r & 15];
+    }
+    mbar_arrive(&B.scales[g % kPast]);
+    // K: thread r has chunk place r % 8 of token r / 8 of each page
+    if (g > 0 && !long_wait(&B.k_empty[0], (g - 1) & 1, 1, abort_flag, status)) return false;
+    {
+        const int tok = r >> 3, c = (r & 7) ^ f8_swz(tok);
+        unsigned char* dst = smem + GE::kOffK + (c >> 2) * kPanel + tok * 128;
+        const int i0 = ((2 * (c & 3)) ^ (tok & 7)) << 4;
+#pragma unroll 2
+        for (int p = 0; p < pages; ++p) {
+            const uint4 w = *reinterpret_cast<const uint4*>(raw + p * kF8Page + 16 * r);
+            *reinterpret_cast<uint4*>(dst + p * (kPage * 128) + i0) = make_uint4(
+                e4m3x2_to_f16x2(w.x), e4m3x2_to_f16x2(w.x >> 16), e4m3x2_to_f16x2(w.y), e4m3x2_to_f16x2(w.y >> 16));
+            *reinterpret_cast<uint4*>(dst + p * (kPage * 128) + (i0 ^ 16)) = make_uint4(
+                e4m3x2_to_f16x2(w.z), e4m3x2_to_f16x2(w.z >> 16), e4m3x2_to_f16x2(w.w), e4m3x2_to_f16x2(w.w >> 16));
+        }
+    }
+    fence_async_smem();
+    mbar_arrive(&B.k_full[0]);
+    // V: thread r has dim r
+    if (g > 0 && !long_wait(&B.v_empty[0], (g - 1) & 1, 1, abort_flag, status)) return false;
+    {
+        auto bf16x2 = [](uint32_t two) {
+            const uint32_t h = e4m3x2_to_f16x2(two);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+            return pack_bf16_rn(f.x, f.y);
+        };
+        unsigned char* dst = smem + GE::kOffV + r * 128;
+#pragma unroll 2
+        for (int p = 0; p < pages; ++p) {
+            const uint4 w = *reinterpret_cast<const uint4*>(raw + p * kF8Page + kF8VOff + 16 * r);
+            unsigned char* at = dst + (p >> 2) * kPanel;
+            const int i0 = ((2 * (p & 3)) ^ (r & 7)) << 4;
+            *reinterpret_cast<uint4*>(at + i0) = make_uint4(bf16x2(w.x), bf16x2(w.x >> 16), bf16x2(w.y), bf16x2(w.y >> 16));
+            *reinterpret_cast<uint4*>(at + (i0 ^ 16)) = make_uint4(bf16x2(w.z), bf16x2(w.z >> 16), bf16x2(w.w), bf16x2(w.w >> 16));
+        }
+    }
+    fence_async_smem();
+    mbar_arrive(&B.v_full[0]);
+    mbar_arrive(&B.raw_empty[s]);
+    return true;
+}
+
+template <int kHD, bool kF8>
 __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps, const Plan& P, const Walk walk0, int lg,
                                            unsigned char* smem)
 {
-    using GE = Geo<kHD>;
-    constexpr int kTileBytes = GE::kTileBytes, kPageBytes = GE::kPageBytes, kGroup = GE::kGroup;
+    using GE = Geo<kHD, kF8>;
+    constexpr int kTileBytes = GE::kTileBytes, kPageBytes = GE::kPageBytes, kGroup = GE::kGroup, kKV = GE::kKV;
     constexpr int kOffQ = GE::kOffQ, kOffK = GE::kOffK, kOffV = GE::kOffV;
     Bars& B = *reinterpret_cast<Bars*>(smem + GE::kOffBar);
     volatile int* abort_flag = &B.abort_flag;
@@ -313,16 +405,24 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
         for (int x = 0; x < 2; ++x) {
             mbar_init(&B.q_full[x], 1);
             mbar_init(&B.q_empty[x], 1);
-            mbar_init(&B.k_full[x], 1);
+            mbar_init(&B.k_full[x], kF8 ? 128 : 1);
             mbar_init(&B.k_empty[x], 1);
-            mbar_init(&B.v_full[x], 1);
+            mbar_init(&B.v_full[x], kF8 ? 128 : 1);
             mbar_init(&B.v_empty[x], 1);
             mbar_init(&B.s_full[x], 1);
             mbar_init(&B.p_full[x], 256);
             mbar_init(&B.o_done[x], 1);
             mbar_init(&B.o_free[x], 128);
         }
-        for (int x = 0; x < kPast; ++x) mbar_init(&B.l_full[x], 256);
+        for (int x = 0; x < kPast; ++x) {
+            mbar_init(&B.l_full[x], 256);
+            mbar_init(&B.scales[x], 128);
+        }
+        for (int x = 0; x < kRaw; ++x) {
+            mbar_init(&B.raw_full[x], 1);
+            mbar_init(&B.raw_empty[x], 128);
+            mbar_init(&B.q_f16[x], 128);
+        }
         mbar_init(&B.drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -336,13 +436,13 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
 
     if (warp < 4) {
         setmaxnreg_dec<kRegsIssue>();
-        if (warp == 0 || warp == 2) {
+        if (warp == 0 || (warp == 2 && !kF8)) {
             // ====================== TMA producers: K and Q, V ======================
             const uint64_t pol = l2_evict_normal_policy();
             const bool is_k = warp == 0;
             if (lane == 0) {
                 if (is_k) tma_prefetch_map(&maps.q);
-                tma_prefetch_map(is_k ? &maps.k : &maps.v);
+                if (!kF8) tma_prefetch_map(is_k ? &maps.k : &maps.v);
             }
             bool go = true;
             // lane 0 waits for `empty` (unless the buffer is new) and arms `full`
@@ -378,11 +478,16 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
                 const int n = p.tiles();
                 for (int t = 0; t < n; ++t) {
                     const int row = pool_row(p, t, blk_next);
-                    const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, row >= 0)) * (uint32_t)kPageBytes;
+                    const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, row >= 0)) *
+                                           (uint32_t)(kF8 ? kF8Page : kPageBytes);
+                    static_assert(kRaw == kStages, "stages of pages as of tiles");
                     const int s = g % kStages;
-                    uint64_t* full = is_k ? &B.k_full[s] : &B.v_full[s];
-                    if (!arm(full, is_k ? &B.k_empty[s] : &B.v_empty[s], g / kStages, bytes)) break;
-                    if (row >= 0)
+                    uint64_t* full = kF8 ? &B.raw_full[s] : is_k ? &B.k_full[s] : &B.v_full[s];
+                    if (!arm(full, kF8 ? &B.raw_empty[s] : is_k ? &B.k_empty[s] : &B.v_empty[s], g / kStages, bytes)) break;
+                    if (kF8 && row >= 0)
+                        bulk_load(smem + GE::kOffRaw + s * GE::kRawBytes + lane * kF8Page,
+                                  (const char*)a.d.k_pool + (int64_t)(row / kPage) * kF8Page, kF8Page, full, pol);
+                    else if (row >= 0)
                         copy_page<kHD>(smem + (is_k ? kOffK : kOffV) + s * kTileBytes + lane * kPageBytes,
                                        is_k ? &maps.k : &maps.v, row, full, pol);
                     ++g;
@@ -410,7 +515,8 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
             __syncwarp();
             if (lane == 0 && *abort_flag) {
                 for (int t = max(0, g - kStages); t < g; ++t)
-                    mbar_wait(is_k ? &B.k_full[t % kStages] : &B.v_full[t % kStages], (t / kStages) & 1, status);
+                    mbar_wait(kF8 ? &B.raw_full[t % kStages] : is_k ? &B.k_full[t % kStages] : &B.v_full[t % kStages],
+                              (t / kStages) & 1, status);
                 for (int t = max(0, qg - kStages); t < qg; ++t) mbar_wait(&B.q_full[t % kStages], (t / kStages) & 1, status);
             }
         } else if (warp == 1) {
@@ -419,12 +525,14 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
             // elected lane issues.  Operand descriptors are built once: a stage or
             // k-step only adds (byte offset >> 4) to the start-address field, which
             // cannot carry out of it (shared-memory offsets stay below 256 KB).
-            constexpr uint32_t idesc_s = idesc_bf16_f32(kBM, 0, false);  // N: the tile's keys
-            constexpr uint32_t idesc_o = idesc_bf16_f32(kBM, kHD, true);
+            // (converted fp8 operands have 64-column panels of 128 rows, as Q; V's rows are dims)
+            constexpr uint32_t idesc_s = kF8 ? idesc_f16_f32(kBM, 0, false) : idesc_bf16_f32(kBM, 0, false);  // N: the tile's keys
+            constexpr uint32_t idesc_o = idesc_bf16_f32(kBM, kHD, !kF8);
             const uint32_t sbase = smem_addr(smem);
             const uint64_t dQ = umma_desc_sw128(sbase + kOffQ, 16, 1024);
-            const uint64_t dK = umma_desc_sw128(sbase + kOffK, 16, kGroup);
-            const uint64_t dV = umma_desc_sw128(sbase + kOffV, 1024, kGroup);
+            const uint64_t dK = umma_desc_sw128(sbase + kOffK, 16, kF8 ? 1024 : kGroup);
+            const uint64_t dV = kF8 ? umma_desc_sw128(sbase + kOffV, 16, 1024) : umma_desc_sw128(sbase + kOffV, 1024, kGroup);
+            uint64_t* const q_ready = kF8 ? B.q_f16 : B.q_full;
             constexpr uint64_t kTileStep = kTileBytes >> 4;
             auto wait = [&](uint64_t* b, uint32_t parity) {
                 if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
@@ -458,18 +566,18 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
                 const bool two = s.p.two();
                 const int y = s.j & 1, x = s.x, t = s.p.tile(s.j), k = s.kv + t, q = s.q + (two ? y : 0);
                 const uint32_t idesc = idesc_s | ((uint32_t)(s.p.pages(t) * kPage >> 3) << 17);
-                if (t == 0 && !wait(&B.q_full[q % kStages], (q / kStages) & 1)) return false;
-                if (!wait(&B.k_full[k % kStages], (k / kStages) & 1)) return false;
+                if (t == 0 && !wait(&q_ready[q % kStages], (q / kStages) & 1)) return false;
+                if (!wait(&B.k_full[k % kKV], (k / kKV) & 1)) return false;
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint64_t qd = dQ + (q % kStages) * kTileStep, kd = dK + (k % kStages) * kTileStep;
+                    const uint64_t qd = dQ + (q % kStages) * kTileStep, kd = dK + (k % kKV) * kTileStep;
                     const uint32_t d = tmem + x * 128;
 #pragma unroll
                     for (int i = 0; i < kHD / 16; ++i)  // k-step: 16 columns, 32 B inside the 128-byte atom
                         tc_mma_f16(d, qd + (uint64_t)(((i >> 2) * kPanel + (i & 3) * 32) >> 4),
-                                   kd + (uint64_t)(((i >> 2) * 1024 + (i & 3) * 32) >> 4), idesc, i > 0);
+                                   kd + (uint64_t)(((i >> 2) * (kF8 ? kPanel : 1024) + (i & 3) * 32) >> 4), idesc, i > 0);
                     tc_commit(&B.s_full[x]);
-                    if (!two || y == 1) tc_commit(&B.k_empty[k % kStages]);
+                    if (!two || y == 1) tc_commit(&B.k_empty[k % kKV]);
                     if (s.j + (two ? 2 : 1) >= s.n) tc_commit(&B.q_empty[q % kStages]);
                 }
                 __syncwarp();
@@ -482,7 +590,7 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
             auto do_pv = [&](const Steps& s) -> bool {
                 const bool two = s.p.two(), first = s.j < (two ? 2 : 1);
                 const int y = s.j & 1, x = s.x, z = two ? y : s.z, t = s.p.tile(s.j), v = s.kv + t;
-                if (!wait(&B.v_full[v % kStages], (v / kStages) & 1) || !wait(&B.p_full[x], seen >> x & 1u)) return false;
+                if (!wait(&B.v_full[v % kKV], (v / kKV) & 1) || !wait(&B.p_full[x], seen >> x & 1u)) return false;
                 seen ^= 1u << x;
                 if (first) {
                     if ((pieces >> (2 + z) & 1u) && !wait(&B.o_free[z], ~pieces >> z & 1u)) return false;
@@ -490,14 +598,16 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
                 }
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint64_t vd = dV + (v % kStages) * kTileStep;
+                    const uint64_t vd = dV + (v % kKV) * kTileStep;
                     const uint32_t d = tmem + 256 + z * 128, pa = tmem + x * 128;
                     const int pages = s.p.pages(t);
 #pragma unroll
                     for (int i = 0; i < kPages; ++i)  // k-step: 16 keys = two 8-key groups
                         if (i < pages)
-                            tc_mma_f16_ts(d, pa + i * 8, vd + (uint64_t)((i * 2 * kGroup) >> 4), idesc_o, (!first || i > 0));
-                    if (!two || y == 1) tc_commit(&B.v_empty[v % kStages]);
+                            tc_mma_f16_ts(d, pa + i * 8,
+                                          vd + (uint64_t)((kF8 ? (i >> 2) * kPanel + (i & 3) * 32 : i * 2 * kGroup) >> 4), idesc_o,
+                                          (!first || i > 0));
+                    if (!two || y == 1) tc_commit(&B.v_empty[v % kKV]);
                     if (s.j + (two ? 2 : 1) >= s.n) tc_commit(&B.o_done[z]);
                 }
                 __syncwarp();
@@ -541,7 +651,7 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
         const int r = quarter * 32 + lane;   // row of the tile
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         float* xchg = reinterpret_cast<float*>(smem + GE::kOffX);
-        const float sl2 = a.d.scale_log2;
+        const float sl2 = kF8 ? 1.f : a.d.scale_log2;  // (fp8: in K's scales)
         uint32_t steps = 0;  // bit x: parity of the S_x seen so far
         int ii = 0, x = 0, z = 0, v = 0;  // v: V tiles of the pieces before
         Walk w = walk0;
@@ -566,6 +676,21 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
                     tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
                     tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
                     tmem_ld_wait();
+                    [[maybe_unused]] const float4* vs = nullptr;  // V's scales of this half's columns
+                    if constexpr (kF8) {
+                        const int u = v + p.tile(j);
+                        const float4* ks = reinterpret_cast<const float4*>(smem + GE::kOffScales + (u % kPast) * 1024) + hf * 16;
+                        vs = ks + 32;
+                        wait_or_abort(&B.scales[u % kPast], (u / kPast) & 1, abort_flag, status);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float4 k = ks[e];
+                            sv[4 * e] = __float_as_uint(__uint_as_float(sv[4 * e]) * k.x);
+                            sv[4 * e + 1] = __float_as_uint(__uint_as_float(sv[4 * e + 1]) * k.y);
+                            sv[4 * e + 2] = __float_as_uint(__uint_as_float(sv[4 * e + 2]) * k.z);
+                            sv[4 * e + 3] = __float_as_uint(__uint_as_float(sv[4 * e + 3]) * k.w);
+                        }
+                    }
                     if (keys < 64) {
 #pragma unroll
                         for (int e = 0; e < 64; ++e)
@@ -603,7 +728,12 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
                         const uint64_t xx =
                             ffma2(pk(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), scale2, msub2);
                         const uint64_t pp = pk(fast_exp2(pk_lo(xx)), fast_exp2(pk_hi(xx)));
-                        pw[e] = pack_bf16_rn(pk_lo(pp), pk_hi(pp));
+                        if constexpr (kF8) {
+                            const float2 w = reinterpret_cast<const float2*>(vs)[e];
+                            pw[e] = pack_bf16_rn(pk_lo(pp) * w.x, pk_hi(pp) * w.y);
+                        } else {
+                            pw[e] = pack_bf16_rn(pk_lo(pp), pk_hi(pp));
+                        }
                         sum2[e & 1] = fadd2(sum2[e & 1], pp);
                     }
                     tmem_st32(tmem + lane_base + x * 128 + hf * 32, pw);
@@ -615,7 +745,7 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
                     if (__any_sync(0xffffffffu, rescale && j > (two ? 1 : 0))) {
                         if (!two) {
                             const int u = v + j - 1;
-                            wait_or_abort(&B.v_empty[u % kStages], (u / kStages) & 1, abort_flag, status);
+                            wait_or_abort(&B.v_empty[u % kKV], (u / kKV) & 1, abort_flag, status);
                             __syncwarp();
                             tc_fence_after();
                         }
@@ -669,10 +799,29 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
         uint32_t done = 0;  // bit z: parity of the pieces on O_z so far
         int ii = 0, z0 = 0;
         Walk w = walk0;
-        Piece p;
-        bool ok = true;
-        while (ok && w.next(a, P, lg, p)) {
+        Piece p, ahead;
+        bool ok = true, more = w.next(a, P, lg, ahead);
+        // fp8: before a piece's output comes the first tile of the next, whose S is
+        // issued before this one's last P.V is
+        [[maybe_unused]] int g = 0, qg = 0;  // tiles and Q tiles converted so far
+        auto convert = [&](const Piece& c, int t) {
+            if (!kF8) return true;
+            if (t == 0)
+                for (int x = 0; x < (c.two() ? 2 : 1); ++x, ++qg)
+                    if (!convert_q(B, smem + kOffQ + qg % kStages * kTileBytes, qg, r, abort_flag, status)) return false;
+            return convert_tile(B, smem, a.d.scale_log2 * 16.f, c.pages(t), g++, r, abort_flag, status);
+        };
+        ok = convert(ahead, 0);
+        while (ok && more) {
+            p = ahead;
             const bool two = p.two();
+            if constexpr (kF8) {
+                const int n = p.tiles();
+                for (int t = 1; ok && t < n; ++t) ok = convert(p, t);
+            }
+            more = w.next(a, P, lg, ahead);
+            if (ok && more) ok = convert(ahead, 0);
+            if (!ok) break;
             if (!long_wait(&B.l_full[ii % kPast], (ii / kPast) & 1, p.tiles(), abort_flag, status)) break;
             const float* lx = xchg + 512 + (ii % kPast) * 768;
             const float l0 = lx[r] + lx[256 + r], l1 = lx[128 + r] + lx[384 + r], m0 = lx[512 + r], m1 = lx[640 + r];
@@ -715,21 +864,16 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
 
 // ---------------------------------------------------------------- own keys
 
-// Range `c` of the own pages, begin .. end - 1, by this warp.
-template <int kHD>
-__device__ __forceinline__ void own_warp(const SharedArgs& a, const Plan& P, const int* lens, int c, int begin, int end, int lg)
-{
-    const int lane = threadIdx.x & 31, g4 = lane >> 2, q4 = lane & 3;
-    const int G = 1 << lg, hkv = a.d.hkv, n = end - begin;
-    // Lane i looks up page i of a batch of 32: its segment b Hkv + h, its row in the pool,
-    // how many of its tokens are keys (0: its block is not there), and whether its segment ends.
-    struct Page {
-        int seg, row, info;
-    };
-    auto look_up = [&](int base) {
-        Page pg{0, 0, 0};
-        const int r = begin + base + lane;
-        if (r >= end) return pg;
+// Lane i looks up page i of a batch of 32, from `first` on, of a range that ends at `end`:
+// its segment b Hkv + h, its row in the pool, how many of its tokens are keys (0: its
+// block is not there), and, as 32, whether its segment or the range ends.
+struct OwnPage {
+    int seg, row, info;
+    __device__ __forceinline__ OwnPage(const SharedArgs& a, const Plan& P, const int* lens, int first, int end)
+        : seg(0), row(0), info(0)
+    {
+        const int r = first + (threadIdx.x & 31), hkv = a.d.hkv;
+        if (r >= end) return;
         int b = 0;  // the last sequence with Hkv own[b] <= r
         for (int m = a.d.batch; m > 1;) {
             const int half = m >> 1;
@@ -740,17 +884,25 @@ __device__ __forceinline__ void own_warp(const SharedArgs& a, const Plan& P, con
         const int left = pages - (in - h * pages);  // pages up to the segment's end
         const int tok = ((len + kPage - 1) / kPage - left) * kPage;
         const int32_t blk = a.d.block_table[(int64_t)b * a.d.max_blocks + tok / a.d.block_size];
-        pg.seg = b * hkv + h;
-        pg.info = left == 1 || r + 1 == end ? 32 : 0;
+        seg = b * hkv + h;
+        info = left == 1 || r + 1 == end ? 32 : 0;
         if (blk < 0 || blk >= a.d.num_blocks) {
             record_error(a.d.status, KVATTN_ERR_BAD_INDEX);
         } else {
-            pg.row = (int)(((int64_t)blk * hkv + h) * a.d.block_size) + tok % a.d.block_size;
-            pg.info |= min(kPage, len - tok);
+            row = (int)(((int64_t)blk * hkv + h) * a.d.block_size) + tok % a.d.block_size;
+            info |= min(kPage, len - tok);
         }
-        return pg;
-    };
-    Page page = look_up(0);
+    }
+};
+__device__ __forceinline__ uint32_t seen_of(int info) { return (1u << (info & 31)) - 1u; }
+
+// Range `c` of the own pages, begin .. end - 1, by this warp.
+template <int kHD>
+__device__ __forceinline__ void own_warp(const SharedArgs& a, const Plan& P, const int* lens, int c, int begin, int end, int lg)
+{
+    const int lane = threadIdx.x & 31, g4 = lane >> 2, q4 = lane & 3;
+    const int G = 1 << lg, n = end - begin;
+    OwnPage page(a, P, lens, begin, end);
     // the group's queries as B fragments: head g4, the dims in the order of K's chunks
     uint32_t q[kHD / 16][2], qn[kHD / 16][2];
     auto load_q = [&](int seg) {
@@ -768,7 +920,6 @@ __device__ __forceinline__ void own_warp(const SharedArgs& a, const Plan& P, con
     Bf16Tile<kHD> t;
     uint4 v[2][4][kHD / 64];
     int seg = __shfl_sync(0xffffffffu, page.seg, 0), info = __shfl_sync(0xffffffffu, page.info, 0);
-    auto seen_of = [](int info) { return (1u << (info & 31)) - 1u; };
     auto load = [&](int j, uint4 (&vv)[4][kHD / 64]) {
         const int64_t row = __shfl_sync(0xffffffffu, page.row, j & 31);
         t.load_k(kp + row * (kHD * 2), seen_of(info), g4, q4);
@@ -797,7 +948,7 @@ __device__ __forceinline__ void own_warp(const SharedArgs& a, const Plan& P, con
         const int seg_now = seg;
         fresh = info & 32;
         if (j + 1 < n) {
-            if (((j + 1) & 31) == 0) page = look_up(j + 1);
+            if (((j + 1) & 31) == 0) page = OwnPage(a, P, lens, begin + j + 1, end);
             seg = __shfl_sync(0xffffffffu, page.seg, (j + 1) & 31);
             info = __shfl_sync(0xffffffffu, page.info, (j + 1) & 31);
             load(j + 1, vnext);
@@ -842,12 +993,120 @@ __device__ __forceinline__ void own_warp(const SharedArgs& a, const Plan& P, con
     }
 }
 
-template <int kHD>
+// ... of fp8 pages, through two places of `ring` (fp8_tile.cuh has the fragments).
+__device__ __forceinline__ void own_warp_fp8(const SharedArgs& a, const Plan& P, const int* lens, int c, int begin, int end,
+                                             int lg, unsigned char* ring)
+{
+    constexpr int kRing = 2;
+    const int lane = threadIdx.x & 31, g4 = lane >> 2, q4 = lane & 3;
+    const int rk0 = (g4 >> 1) * 4 + (g4 & 1), rk1 = rk0 + 2;
+    const int G = 1 << lg, n = end - begin;
+    OwnPage now(a, P, lens, begin, end), next(a, P, lens, begin + 32, end);  // batches `batch` and the one after
+    int batch = 0;
+    auto seg_of = [&](int j) { return __shfl_sync(0xffffffffu, j >> 5 == batch ? now.seg : next.seg, j & 31); };
+    auto info_of = [&](int j) { return __shfl_sync(0xffffffffu, j >> 5 == batch ? now.info : next.info, j & 31); };
+    auto row_of = [&](int j) { return __shfl_sync(0xffffffffu, j >> 5 == batch ? now.row : next.row, j & 31); };
+    auto fetch = [&](int j) {  // page j on its way to its place: one group of copies, empty past the end
+        if (j < n) {
+            const unsigned char* src = (const unsigned char*)a.d.k_pool + (int64_t)(row_of(j) / kPage) * kF8Page + 16 * lane;
+            const uint32_t dst = smem_addr(ring + j % kRing * kF8Page + 16 * lane);
+            auto copy = [](uint32_t to, const void* from) {
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+            };
+#pragma unroll
+            for (int i = 0; i < kF8Page / 512; ++i) copy(dst + 512 * i, src + 512 * i);
+            if (lane < kF8Page % 512 / 16) copy(dst + kF8Page / 512 * 512, src + kF8Page / 512 * 512);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int j = 0; j < kRing; ++j) fetch(j);
+    uint32_t q[8][2];
+    uint4 qn[4];  // the next segment's queries, as they are
+    auto load_q = [&](int seg) {
+        const __nv_bfloat16* qh = reinterpret_cast<const __nv_bfloat16*>(a.d.q) + (((int64_t)seg << lg) + g4) * 128;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            qn[i] = g4 < G ? ldg16(qh + 16 * (q4 + 4 * (i >> 1)) + 8 * (i & 1)) : make_uint4(0, 0, 0, 0);
+    };
+    load_q(seg_of(0));
+    Fp8Softmax st;
+    float o[8][4];
+    bool fresh = true;
+    for (int j = 0; j < n; ++j) {
+        if (j >> 5 != batch) {
+            ++batch;
+            now = next;
+            next = OwnPage(a, P, lens, begin + 32 * (batch + 1), end);
+        }
+        if (fresh) {  // scaled by 2^-4 into f16's range (the scores are scaled back)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t u[4] = {qn[i].x, qn[i].y, qn[i].z, qn[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    q[2 * i + (k >> 1)][k & 1] = pack_f16_rn(bf16lo(u[k]) * 0.0625f, bf16hi(u[k]) * 0.0625f);
+            }
+            st.init();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        }
+        const int seg = seg_of(j), info = info_of(j);
+        fresh = info & 32;
+        if (fresh && j + 1 < n) load_q(seg_of(j + 1));
+        asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+        __syncwarp();  // every lane's copies of page j are there
+        Fp8Tile t;
+        t.load(ring + j % kRing * kF8Page, rk0, g4, q4);
+        __syncwarp();  // and every lane has read it
+        fetch(j + kRing);
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        t.scores(s, q);
+        const uint32_t seen = seen_of(info);
+        const float sl2 = a.d.scale_log2 * 16.f, k0 = t.ks[0] * sl2, k1 = t.ks[1] * sl2;
+        const bool in0 = seen >> rk0 & 1u, in1 = seen >> rk1 & 1u;
+        const float x[4] = {in0 ? s[0] * k0 : -INFINITY, in0 ? s[1] * k0 : -INFINITY, in1 ? s[2] * k1 : -INFINITY,
+                            in1 ? s[3] * k1 : -INFINITY};
+        const float sv0 = in0 ? t.vs[0] : 0.f, sv1 = in1 ? t.vs[1] : 0.f;
+        uint32_t vmask = 0xffffffffu;  // the bytes of this lane's words whose tokens are seen
+        if (seen != (1u << kPage) - 1u) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (!(seen >> (4 * q4 + i) & 1u)) vmask &= ~(0xffu << (8 * i));
+        }
+        float w[4];
+        st.step(x, sv0, sv1, lane, [&](int i) { return t.v[i] & vmask; }, o, w);
+        t.add(o, movmatrix_trans(pack_f16_rn(w[0], w[1])), movmatrix_trans(pack_f16_rn(w[2], w[3])), vmask);
+        if (fresh) {  // the segment's end, or the range's: its state
+#pragma unroll
+            for (int i = 4; i < 32; i <<= 1) {
+                st.l[0] += __shfl_xor_sync(0xffffffffu, st.l[0], i);
+                st.l[1] += __shfl_xor_sync(0xffffffffu, st.l[1], i);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int g = 2 * q4 + e;
+                if (g >= G) continue;
+                const int64_t row = (((int64_t)c + seg) << lg) + g;
+                float* out = a.own_o + row * 128 + g4;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    out[16 * i] = o[i][e] * st.ref[e];
+                    out[16 * i + 8] = o[i][2 + e] * st.ref[e];
+                }
+                if (g4 == 0) *reinterpret_cast<float2*>(a.own_ml + row * 2) = make_float2(st.m[e], st.l[e]);
+            }
+        }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+template <int kHD, bool kF8>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_shared_kernel(const __grid_constant__ SharedArgs a, const __grid_constant__ Maps maps)
 {
     pdl_wait();
-    using GE = Geo<kHD>;
+    using GE = Geo<kHD, kF8>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     Plan& P = *reinterpret_cast<Plan*>(smem + GE::kOffPlan);
@@ -855,8 +1114,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int* len = reinterpret_cast<int*>(smem);  // (where Q will be)
     make_plan(a, P, len, lg);
     const int shared = P.first[a.num_groups], own = a.d.hkv * P.own[a.d.batch];
-    const Ranges ranges = ranges_of(shared, P.segment[a.num_groups], own, gridDim.x, kSetUpBytes / (2 * GE::kPageBytes),
-                                    kSegmentBytes / (2 * GE::kPageBytes), kOwnWarps);
+    const Ranges ranges = ranges_of(shared, P.segment[a.num_groups], own, gridDim.x, kSetUpBytes / GE::kCost,
+                                    kSegmentBytes / GE::kCost, own_warps<kF8>());
     // where the merge finds each sequence's partial results
     for (int b = (int)blockIdx.x + (int)gridDim.x * threadIdx.x; b < a.d.batch; b += (int)gridDim.x * kThreads) {
         SharedOf o{};
@@ -880,17 +1139,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if ((int)blockIdx.x < ranges.ctas) {
         const int r = min(shared, (int)blockIdx.x * ranges.per), end = min(shared, r + ranges.per);
-        if (r < end) prefix_cta<kHD>(a, maps, P, Walk{r, end, 0}, lg, smem);
+        if (r < end) prefix_cta<kHD, kF8>(a, maps, P, Walk{r, end, 0}, lg, smem);
     } else {
         const int warp = threadIdx.x >> 5;
-        if (warp < 4 || warp >= 4 + kOwnWarps) {
-            setmaxnreg_dec<kRegsIdle>();
-            return;
+        constexpr int kWarps = own_warps<kF8>(), kFirst = kF8 ? 0 : 4;
+        if constexpr (!kF8) {
+            if (warp < kFirst || warp >= kFirst + kWarps) {
+                setmaxnreg_dec<kRegsIdle>();
+                return;
+            }
+            setmaxnreg_inc<kRegsOwn>();
         }
-        setmaxnreg_inc<kRegsOwn>();
-        const int c = ((int)blockIdx.x - ranges.ctas) * kOwnWarps + warp - 4;
+        const int c = ((int)blockIdx.x - ranges.ctas) * kWarps + warp - kFirst;
         const int r = min(own, c * ranges.own_per), end = min(own, r + ranges.own_per);
-        if (r < end) own_warp<kHD>(a, P, len, c, r, end, lg);
+        if (r >= end) return;
+        if constexpr (kF8) own_warp_fp8(a, P, len, c, r, end, lg, smem + GE::kOffRing + warp * 2 * kF8Page);
+        else own_warp<kHD>(a, P, len, c, r, end, lg);
     }
 }
 
@@ -989,7 +1253,7 @@ __global__ void __launch_bounds__(128) decode_shared_merge_kernel(const __grid_c
         *out = pack_bf16_rn(acc[0] * inv, acc[1] * inv);
 }
 
-template <int kHD>
+template <int kHD, bool kF8>
 bool make_maps(const DecodeArgs& a, Maps& m)
 {
     std::memset(&m, 0, sizeof(m));
@@ -999,7 +1263,8 @@ bool make_maps(const DecodeArgs& a, Maps& m)
     const cuuint32_t qbox[3] = {64, G, (cuuint32_t)kBM / G};
     if (!encode(&m.q, a.q, 3, dims, strides, qbox)) return false;
     const int64_t rows = (int64_t)a.num_blocks * a.hkv * a.block_size;
-    if constexpr (kHD == 128) return pool_maps(a.k_pool, a.v_pool, rows, false, &m.k, &m.v);
+    if constexpr (kF8) return true;  // (pages are copied whole)
+    else if constexpr (kHD == 128) return pool_maps(a.k_pool, a.v_pool, rows, false, &m.k, &m.v);
     // (64 columns, rows): a box of (64, 16) is one 16-row page, [16 rows][128 B]
     const cuuint64_t pdims[2] = {64, (cuuint64_t)rows};
     const cuuint64_t pstrides[1] = {64 * 2};
@@ -1007,16 +1272,16 @@ bool make_maps(const DecodeArgs& a, Maps& m)
     return encode(&m.k, a.k_pool, 2, pdims, pstrides, pbox) && encode(&m.v, a.v_pool, 2, pdims, pstrides, pbox);
 }
 
-template <int kHD>
+template <int kHD, bool kF8>
 kvattn_status launch(const SharedArgs& a, cudaStream_t s)
 {
     Maps maps;
-    if (!make_maps<kHD>(a.d, maps)) return KVATTN_ERR_CUDA;
-    constexpr int kSmem = Geo<kHD>::kSmemBytes;
+    if (!make_maps<kHD, kF8>(a.d, maps)) return KVATTN_ERR_CUDA;
+    constexpr int kSmem = Geo<kHD, kF8>::kSmemBytes;
     static_assert(kSmem <= 232448, "shared memory of a block");
     static SmemLimit limit;
-    if (limit.ensure(reinterpret_cast<const void*>(decode_shared_kernel<kHD>), kSmem) != cudaSuccess) return KVATTN_ERR_CUDA;
-    const cudaError_t e = launch_pdl(decode_shared_kernel<kHD>, dim3((unsigned)num_sms()), dim3(kThreads), kSmem, s, a, maps);
+    if (limit.ensure(reinterpret_cast<const void*>(decode_shared_kernel<kHD, kF8>), kSmem) != cudaSuccess) return KVATTN_ERR_CUDA;
+    const cudaError_t e = launch_pdl(decode_shared_kernel<kHD, kF8>, dim3((unsigned)num_sms()), dim3(kThreads), kSmem, s, a, maps);
     if (e != cudaSuccess) return KVATTN_ERR_CUDA;
     const int rows = a.d.batch * a.d.hq;
     // four warps a row where that leaves the GPU's warps room, for rows of many pieces
@@ -1029,7 +1294,8 @@ kvattn_status launch(const SharedArgs& a, cudaStream_t s)
 
 kvattn_status launch_decode_shared(const SharedArgs& a, cudaStream_t s)
 {
-    return a.d.d == 128 ? launch<128>(a, s) : a.d.d == 64 ? launch<64>(a, s) : KVATTN_ERR_UNSUPPORTED;
+    if (a.d.fp8) return a.d.d == 128 ? launch<128, true>(a, s) : KVATTN_ERR_UNSUPPORTED;
+    return a.d.d == 128 ? launch<128, false>(a, s) : a.d.d == 64 ? launch<64, false>(a, s) : KVATTN_ERR_UNSUPPORTED;
 }
 
 }  // namespace kvattn

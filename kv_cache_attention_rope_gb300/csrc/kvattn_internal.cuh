@@ -254,7 +254,7 @@ struct SharedArgs {
 kvattn_status launch_decode_shared(const SharedArgs& a, cudaStream_t s);
 // Most groups and sequences of a call that reads prefixes once (others read each
 // sequence by itself): the kernel keeps them in shared memory.
-constexpr int32_t kMaxGroups = 256, kMaxSharedBatch = 2048;
+constexpr int32_t kMaxGroups = 192, kMaxSharedBatch = 2048;
 // Pieces that a call may have: one per range, and one more per segment.  Groups of
 // fewer than two sequences share nothing.
 inline int64_t shared_pieces(int32_t hq, int32_t hkv, int32_t batch, int32_t num_groups, int32_t ctas)

@@ -1,8 +1,9 @@
 """GPU tests of decode over shared prefixes against the formula in 64 bits, every sequence by itself.
 
 Slots that no sequence sees hold NaN and table entries without a seen token are -1.  Tolerances:
-_window_support.check_attention; the merge of the two parts of a sequence is in fp32 and adds less than the exp2 that it
-counts.
+_window_support.check_attention, for fp8 pages as for bf16 (over a prefix a weight times its V scale is rounded to bf16,
+2^-8; codes and scores are exact or fp32); the merge of the two parts of a sequence is in fp32 and adds less than the
+exp2 that it counts.
 """
 import numpy as np
 import pytest
@@ -21,7 +22,7 @@ def _want(c, q):
 
 def _check(c, q, got, dtype, what=""):
     for r, (want, mag) in enumerate(_want(c, q.double().cpu().numpy())):
-        check_attention(got[r:r + 1], want, mag, dtype, f"{what} sequence {r} of length {c.lens[r]}")
+        check_attention(got[r:r + 1], want, mag, "f32" if dtype == "f32" else "bf16", f"{what} sequence {r} of length {c.lens[r]}")
         if c.lens[r] == 0:
             assert np.all(got[r] == 0.0)
 
