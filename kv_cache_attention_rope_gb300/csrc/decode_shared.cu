@@ -44,9 +44,9 @@
 // 1500 cycles of work and 2000 to issue its cp.async copies, or as long for its two TMA
 // boxes; own parts of 64 sequences of up to 4096, 537 MB: 123 and 113 us.)
 //
-// fp8 pages.  On prefixes, warp 0 copies whole pages and the output warps, which have
-// time, make the operands of them: K's codes exactly in f16 (Q goes in f16 over 16), V's, in
-// the transposed order that the page has, exactly in bf16.  K's scales multiply the
+// fp8 pages.  On prefixes, warp 0 copies whole pages and others make the operands of
+// them: warps 2 and 3 K's codes exactly in f16 (and Q in f16 over 16), the output warps, which
+// have time, V's, in the transposed order that the page has, exactly in bf16.  K's scales multiply the
 // scores' columns, V's the weights before they are rounded to bf16, whose range is the scales'
 // own.  Own keys go as in decode_direct.cu, pages through two buffers per warp.
 //
@@ -74,7 +74,7 @@ constexpr int kPanel = kBM * 128;  // 16 KB: 128 rows x 64 columns (one 128-byte
 constexpr int kMinShared = 128;  // tokens of a prefix that is worth pieces of its own
 constexpr int kMinPer = 8;     // fewest shared pages of a CTA's range
 constexpr int kMinOwn = 2;     // fewest own pages of a warp's range
-constexpr float kSetUpBytes = 180000.f, kSegmentBytes = 80000.f, kOwnWeight = 1.0f;  // of K and V that take as long (ranges_of)
+constexpr float kSetUpBytes = 180000.f, kSegmentBytes = 80000.f, kOwnSegment = 2.0f;  // of K and V that take as long (ranges_of)
 constexpr int kPast = 4;       // pieces whose sums may be waiting for the output warps
 constexpr int kRaw = 2;        // fp8: stages of pages
 constexpr int kSeqs = kMaxSharedBatch / kThreads;  // sequences a thread plans
@@ -256,16 +256,17 @@ __device__ __forceinline__ void make_plan(const SharedArgs& a, Plan& P, int* len
 struct Ranges {
     int ctas, per, own_per;
 };
-// In times of a shared page: an own page takes kOwnWeight, a prefix CTA `set_up` besides
-// its pages (tensor memory, the pipeline's filling) and `segment` for each of its
+// In times of a shared page: an own segment takes kOwnSegment besides its pages (state, queries),
+// a prefix CTA `set_up` besides its own (tensor memory, the pipeline's filling) and `segment` for each of its
 // segments (256 rows of output); so with t for all,
-// (shared + segment segments) / (t - set_up) + kOwnWeight own / t = ctas.
-__device__ __forceinline__ Ranges ranges_of(int shared, int segments, int own, int ctas, float set_up, float segment,
-                                            int warps)
+// (shared + segment segments) / (t - set_up) + (own + kOwnSegment own_segments) / t = ctas.
+__device__ __forceinline__ Ranges ranges_of(int shared, int segments, int own, int own_segments, int ctas,
+                                            float set_up, float segment, int warps)
 {
     Ranges r{0, 0, 0};
     if (shared > 0) {
-        const float c = (float)ctas, p = (float)shared + segment * (float)segments, o = kOwnWeight * (float)own, u = set_up * c + p + o;
+        const float c = (float)ctas, p = (float)shared + segment * (float)segments, o = (float)own + kOwnSegment * (float)own_segments,
+                    u = set_up * c + p + o;
         const float t = (u + sqrtf(fmaxf(u * u - 4.f * c * set_up * o, 0.f))) / (2.f * c);
         r.ctas = min((int)ceilf(p / fmaxf(t - set_up, 1.f)), (shared + kMinPer - 1) / kMinPer);
         r.ctas = max(1, min(r.ctas, own > 0 ? ctas - 1 : ctas));
@@ -315,14 +316,13 @@ struct Walk {
     }
 };
 
-// fp8, by the 128 threads of the output warps (thread r).  Q tile `q` of the CTA, as
-// loaded: to f16 over 16, in place.
+// fp8: Q tile `q` of the CTA, as loaded, to f16 over 16 in place, by 64 threads r.
 __device__ __forceinline__ bool convert_q(Bars& B, unsigned char* tile, int q, int r, volatile int* abort_flag, int* status)
 {
     if (!long_wait(&B.q_full[q % kStages], (q / kStages) & 1, 0, abort_flag, status)) return false;
     uint4* p = reinterpret_cast<uint4*>(tile);
 #pragma unroll 4
-    for (int i = r; i < kBM * 128 * 2 / 16; i += 128) {
+    for (int i = r; i < kBM * 128 * 2 / 16; i += 64) {
         const uint4 v = p[i];
         auto half2 = [](uint32_t u) { return pack_f16_rn(bf16lo(u) * 0.0625f, bf16hi(u) * 0.0625f); };
         p[i] = make_uint4(half2(v.x), half2(v.y), half2(v.z), half2(v.w));
@@ -332,57 +332,72 @@ __device__ __forceinline__ bool convert_q(Bars& B, unsigned char* tile, int q, i
     return true;
 }
 
-// Tile g of the CTA, `pages` pages: K's codes to f16 and V's to bf16 (both exact), in
-// 64-column panels of 128 rows with 128-byte swizzle, K's rows the keys and V's the
-// dims; and the scales, K's times `mul`.
-__device__ __forceinline__ bool convert_tile(Bars& B, unsigned char* smem, float mul, int pages, int g, int r,
-                                             volatile int* abort_flag, int* status)
+// Tile g of the CTA, `pages` pages: K's codes to f16 (exact), in 64-column panels of 128
+// rows (keys) with 128-byte swizzle, and the scales, K's times `mul`, by 64 threads r.
+__device__ __forceinline__ bool convert_k(Bars& B, unsigned char* smem, float mul, int pages, int g, int r,
+                                          volatile int* abort_flag, int* status)
 {
     using GE = Geo<128, true>;
     const int s = g % kRaw;
     if (!long_wait(&B.raw_full[s], (g / kRaw) & 1, 1, abort_flag, status)) return false;
     const unsigned char* raw = smem + GE::kOffRaw + s * GE::kRawBytes;
+    if (g > 0 && !long_wait(&B.k_empty[0], (g - 1) & 1, 1, abort_flag, status)) return false;
+    // (S of tile g - 1 was issued after the P.V of tile g - 3, whose softmax has read the
+    // scales of tile g - kPast)
     float* sc = reinterpret_cast<float*>(smem + GE::kOffScales + (g % kPast) * 1024);
-    if (r < pages * kPage) {  // (the softmax has read the scales of kPast tiles ago: its P was for a P.V before this tile's S)
-        const unsigned char* pg = raw + (r >> 4) * kF8Page;
-        sc[r] = reinterpret_cast<const float*>(pg + kF8KsOff)[r & 15] * mul;
-        sc[128 + r] = reinterpret_cast<const float*>(pg + kF8VsOff)[r & 15];
+    for (int i = r; i < pages * kPage; i += 64) {
+        const unsigned char* pg = raw + (i >> 4) * kF8Page;
+        sc[i] = reinterpret_cast<const float*>(pg + kF8KsOff)[i & 15] * mul;
+        sc[128 + i] = reinterpret_cast<const float*>(pg + kF8VsOff)[i & 15];
     }
     mbar_arrive(&B.scales[g % kPast]);
-    // K: thread r has chunk place r % 8 of token r / 8 of each page
-    if (g > 0 && !long_wait(&B.k_empty[0], (g - 1) & 1, 1, abort_flag, status)) return false;
-    {
-        const int tok = r >> 3, c = (r & 7) ^ f8_swz(tok);
-        unsigned char* dst = smem + GE::kOffK + (c >> 2) * kPanel + tok * 128;
-        const int i0 = ((2 * (c & 3)) ^ (tok & 7)) << 4;
+    // thread r has chunk place r % 8 of tokens r / 8 and r / 8 + 8 of each page
+    const int t0 = r >> 3;
+    unsigned char* dst = smem + GE::kOffK + t0 * 128;
+    const int c0 = (r & 7) ^ f8_swz(t0), c1 = (r & 7) ^ f8_swz(t0 + 8);  // their dims' chunks
+    auto put = [&](unsigned char* row, int c, const uint4& w) {
+        unsigned char* at = row + (c >> 2) * kPanel;
+        const int i0 = ((2 * (c & 3)) ^ (t0 & 7)) << 4;
+        *reinterpret_cast<uint4*>(at + i0) = make_uint4(e4m3x2_to_f16x2(w.x), e4m3x2_to_f16x2(w.x >> 16),
+                                                        e4m3x2_to_f16x2(w.y), e4m3x2_to_f16x2(w.y >> 16));
+        *reinterpret_cast<uint4*>(at + (i0 ^ 16)) = make_uint4(e4m3x2_to_f16x2(w.z), e4m3x2_to_f16x2(w.z >> 16),
+                                                               e4m3x2_to_f16x2(w.w), e4m3x2_to_f16x2(w.w >> 16));
+    };
 #pragma unroll 2
-        for (int p = 0; p < pages; ++p) {
-            const uint4 w = *reinterpret_cast<const uint4*>(raw + p * kF8Page + 16 * r);
-            *reinterpret_cast<uint4*>(dst + p * (kPage * 128) + i0) = make_uint4(
-                e4m3x2_to_f16x2(w.x), e4m3x2_to_f16x2(w.x >> 16), e4m3x2_to_f16x2(w.y), e4m3x2_to_f16x2(w.y >> 16));
-            *reinterpret_cast<uint4*>(dst + p * (kPage * 128) + (i0 ^ 16)) = make_uint4(
-                e4m3x2_to_f16x2(w.z), e4m3x2_to_f16x2(w.z >> 16), e4m3x2_to_f16x2(w.w), e4m3x2_to_f16x2(w.w >> 16));
-        }
+    for (int p = 0; p < pages; ++p) {
+        const uint4 x = *reinterpret_cast<const uint4*>(raw + p * kF8Page + 16 * r);
+        const uint4 y = *reinterpret_cast<const uint4*>(raw + p * kF8Page + 16 * r + 1024);
+        put(dst + p * (kPage * 128), c0, x);
+        put(dst + p * (kPage * 128) + 1024, c1, y);
     }
     fence_async_smem();
     mbar_arrive(&B.k_full[0]);
-    // V: thread r has dim r
+    mbar_arrive(&B.raw_empty[s]);
+    return true;
+}
+
+// ... and V's to bf16 (exact), in panels of 128 rows (dims) of 64 keys, by 128 threads r.
+__device__ __forceinline__ bool convert_v(Bars& B, unsigned char* smem, int pages, int g, int r, volatile int* abort_flag,
+                                          int* status)
+{
+    using GE = Geo<128, true>;
+    const int s = g % kRaw;
+    if (!long_wait(&B.raw_full[s], (g / kRaw) & 1, 1, abort_flag, status)) return false;
     if (g > 0 && !long_wait(&B.v_empty[0], (g - 1) & 1, 1, abort_flag, status)) return false;
-    {
-        auto bf16x2 = [](uint32_t two) {
-            const uint32_t h = e4m3x2_to_f16x2(two);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-            return pack_bf16_rn(f.x, f.y);
-        };
-        unsigned char* dst = smem + GE::kOffV + r * 128;
+    const unsigned char* raw = smem + GE::kOffRaw + s * GE::kRawBytes + kF8VOff + 16 * r;  // dim r
+    unsigned char* dst = smem + GE::kOffV + r * 128;
+    auto bf16x2 = [](uint32_t two) {
+        const uint32_t h = e4m3x2_to_f16x2(two);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        return pack_bf16_rn(f.x, f.y);
+    };
 #pragma unroll 2
-        for (int p = 0; p < pages; ++p) {
-            const uint4 w = *reinterpret_cast<const uint4*>(raw + p * kF8Page + kF8VOff + 16 * r);
-            unsigned char* at = dst + (p >> 2) * kPanel;
-            const int i0 = ((2 * (p & 3)) ^ (r & 7)) << 4;
-            *reinterpret_cast<uint4*>(at + i0) = make_uint4(bf16x2(w.x), bf16x2(w.x >> 16), bf16x2(w.y), bf16x2(w.y >> 16));
-            *reinterpret_cast<uint4*>(at + (i0 ^ 16)) = make_uint4(bf16x2(w.z), bf16x2(w.z >> 16), bf16x2(w.w), bf16x2(w.w >> 16));
-        }
+    for (int p = 0; p < pages; ++p) {
+        const uint4 w = *reinterpret_cast<const uint4*>(raw + p * kF8Page);
+        unsigned char* at = dst + (p >> 2) * kPanel;
+        const int i0 = ((2 * (p & 3)) ^ (r & 7)) << 4;
+        *reinterpret_cast<uint4*>(at + i0) = make_uint4(bf16x2(w.x), bf16x2(w.x >> 16), bf16x2(w.y), bf16x2(w.y >> 16));
+        *reinterpret_cast<uint4*>(at + (i0 ^ 16)) = make_uint4(bf16x2(w.z), bf16x2(w.z >> 16), bf16x2(w.w), bf16x2(w.w >> 16));
     }
     fence_async_smem();
     mbar_arrive(&B.v_full[0]);
@@ -405,7 +420,7 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
         for (int x = 0; x < 2; ++x) {
             mbar_init(&B.q_full[x], 1);
             mbar_init(&B.q_empty[x], 1);
-            mbar_init(&B.k_full[x], kF8 ? 128 : 1);
+            mbar_init(&B.k_full[x], kF8 ? 64 : 1);
             mbar_init(&B.k_empty[x], 1);
             mbar_init(&B.v_full[x], kF8 ? 128 : 1);
             mbar_init(&B.v_empty[x], 1);
@@ -416,12 +431,12 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
         }
         for (int x = 0; x < kPast; ++x) {
             mbar_init(&B.l_full[x], 256);
-            mbar_init(&B.scales[x], 128);
+            mbar_init(&B.scales[x], 64);
         }
         for (int x = 0; x < kRaw; ++x) {
             mbar_init(&B.raw_full[x], 1);
-            mbar_init(&B.raw_empty[x], 128);
-            mbar_init(&B.q_f16[x], 128);
+            mbar_init(&B.raw_empty[x], 192);
+            mbar_init(&B.q_f16[x], 64);
         }
         mbar_init(&B.drain, 1);
         *abort_flag = 0;
@@ -635,6 +650,20 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
             if (elect_one()) tc_commit(&B.drain);
             __syncwarp();
             mbar_wait(&B.drain, 0, status);
+        } else if (kF8) {
+            // ============================= K and Q to f16 =============================
+            const int r = threadIdx.x - 64;
+            int g = 0, q = 0;
+            Walk w = walk0;
+            Piece p;
+            bool ok = true;
+            while (ok && w.next(a, P, lg, p)) {
+                for (int x = 0; ok && x < (p.two() ? 2 : 1); ++x, ++q)
+                    ok = convert_q(B, smem + kOffQ + q % kStages * kTileBytes, q, r, abort_flag, status);
+                const int n = p.tiles();
+                for (int t = 0; ok && t < n; ++t, ++g)
+                    ok = convert_k(B, smem, a.d.scale_log2 * 16.f, p.pages(t), g, r, abort_flag, status);
+            }
         }
     } else if (warp < 12) {
         setmaxnreg_inc<kRegsSoftmax>();
@@ -801,15 +830,9 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
         Walk w = walk0;
         Piece p, ahead;
         bool ok = true, more = w.next(a, P, lg, ahead);
-        // fp8: before a piece's output comes the first tile of the next, whose S is
-        // issued before this one's last P.V is
-        [[maybe_unused]] int g = 0, qg = 0;  // tiles and Q tiles converted so far
+        [[maybe_unused]] int g = 0;  // fp8: tiles converted so far
         auto convert = [&](const Piece& c, int t) {
-            if (!kF8) return true;
-            if (t == 0)
-                for (int x = 0; x < (c.two() ? 2 : 1); ++x, ++qg)
-                    if (!convert_q(B, smem + kOffQ + qg % kStages * kTileBytes, qg, r, abort_flag, status)) return false;
-            return convert_tile(B, smem, a.d.scale_log2 * 16.f, c.pages(t), g++, r, abort_flag, status);
+            return !kF8 || convert_v(B, smem, c.pages(t), g++, r, abort_flag, status);
         };
         ok = convert(ahead, 0);
         while (ok && more) {
@@ -820,7 +843,7 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
                 for (int t = 1; ok && t < n; ++t) ok = convert(p, t);
             }
             more = w.next(a, P, lg, ahead);
-            if (ok && more) ok = convert(ahead, 0);
+            if (ok && more) ok = convert(ahead, 0);  // (the next piece's P.V do not wait for this one's output)
             if (!ok) break;
             if (!long_wait(&B.l_full[ii % kPast], (ii / kPast) & 1, p.tiles(), abort_flag, status)) break;
             const float* lx = xchg + 512 + (ii % kPast) * 768;
@@ -1114,7 +1137,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int* len = reinterpret_cast<int*>(smem);  // (where Q will be)
     make_plan(a, P, len, lg);
     const int shared = P.first[a.num_groups], own = a.d.hkv * P.own[a.d.batch];
-    const Ranges ranges = ranges_of(shared, P.segment[a.num_groups], own, gridDim.x, kSetUpBytes / GE::kCost,
+    const Ranges ranges = ranges_of(shared, P.segment[a.num_groups], own, a.d.hkv * a.d.batch, gridDim.x, kSetUpBytes / GE::kCost,
                                     kSegmentBytes / GE::kCost, own_warps<kF8>());
     // where the merge finds each sequence's partial results
     for (int b = (int)blockIdx.x + (int)gridDim.x * threadIdx.x; b < a.d.batch; b += (int)gridDim.x * kThreads) {
