@@ -455,7 +455,7 @@ kvattn_status rotary_append_any(const kvattn_config* cfg, const kvattn_rotary* r
     if (axes) {
         a.slots = slots;
         a.num_axes = axes->num_axes;
-        std::memcpy(a.axis, axis, sizeof(axis));
+        for (int i = 0; i < 64; ++i) a.axis[i / 32] |= (uint64_t)axis[i] << (2 * (i % 32));
     }
     const kvattn_status kst = axes ? launch_rotary_append_axes(a, static_cast<cudaStream_t>(stream))
                                    : launch_rotary_append(a, static_cast<cudaStream_t>(stream));

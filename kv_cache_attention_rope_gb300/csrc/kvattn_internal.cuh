@@ -144,7 +144,7 @@ struct RotaryArgs {
     // launch_rotary_append_axes only: positions is [num_axes][num_tokens]
     const int32_t* slots;
     int32_t num_axes;
-    uint8_t axis[64];  // of each pair
+    uint64_t axis[2];  // of each pair, 2 bits (read with indexes that are a warp's: no constant loads that differ by lane)
 };
 constexpr int kMaxAxes = 4;
 kvattn_status launch_rotary_append(const RotaryArgs& a, cudaStream_t s);

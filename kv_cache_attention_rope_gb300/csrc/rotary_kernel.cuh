@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, (kHalf ? 7 : 8)) rotary_append_kerne
         if (i < a.rot / 2) {
             int pos = at[0];
             if constexpr (kAxes) {
-                const int x = a.axis[i];
+                const int x = (int)((i < 32 ? a.axis[0] : a.axis[1]) >> (2 * (i & 31))) & 3;
 #pragma unroll
                 for (int y = 1; y < kMaxAxes; ++y) pos = x == y ? at[y] : pos;
             }
