@@ -74,12 +74,11 @@ constexpr int kPanel = kBM * 128;  // 16 KB: 128 rows x 64 columns (one 128-byte
 constexpr int kMinShared = 128;  // tokens of a prefix that is worth pieces of its own
 constexpr int kMinPer = 8;     // fewest shared pages of a CTA's range
 constexpr int kMinOwn = 2;     // fewest own pages of a warp's range
-constexpr float kSetUpBytes = 180000.f, kSegmentBytes = 80000.f, kOwnSegment = 2.0f;  // of K and V that take as long (ranges_of)
+constexpr float kSetUpBytes = 180000.f, kSegmentBytes = 80000.f;  // of K and V that take as long (ranges_of)
 constexpr int kPast = 4;       // pieces whose sums may be waiting for the output warps
 constexpr int kRaw = 2;        // fp8: stages of pages
-constexpr int kSeqs = kMaxSharedBatch / kThreads;  // sequences a thread plans
 static_assert(kSharedRows == 2 * kBM, "a prefix piece's rows");
-static_assert(kMaxGroups <= kThreads && kMaxSharedBatch % kThreads == 0, "a thread per group");
+static_assert(kMaxGroups <= kThreads, "a thread per group");
 // Registers per thread of the warpgroups (the block starts with 128 each:
 // 96 + 2 x 168 + 80 = 4 x 128).
 constexpr int kRegsIssue = 96, kRegsSoftmax = 168, kRegsOutput = 80;
@@ -173,11 +172,10 @@ __device__ __forceinline__ int group_of(const Plan& P, int n, int b)
 // fewer than two sequences have it all.
 __device__ __forceinline__ void make_plan(const SharedArgs& a, Plan& P, int* len, int lg)
 {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.num_groups, b0 = tid * kSeqs;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.num_groups;
+    const int per = (a.d.batch + kThreads - 1) / kThreads;  // sequences of a thread, mostly one
+    const int b0 = tid * per, b1 = min(b0 + per, a.d.batch);
     const int64_t room = (int64_t)a.d.max_blocks * a.d.block_size;
-    int L[kSeqs];
-#pragma unroll
-    for (int j = 0; j < kSeqs; ++j) L[j] = b0 + j < a.d.batch ? a.d.seq_lens[b0 + j] : 0;
     bool ok = true;
     if (tid < n) {
         const int c0 = a.cu_groups[tid], c1 = a.cu_groups[tid + 1], s = a.shared_lens[tid];
@@ -188,27 +186,31 @@ __device__ __forceinline__ void make_plan(const SharedArgs& a, Plan& P, int* len
         P.leader[tid] = INT_MAX;
         P.members[tid] = 0;
     }
-#pragma unroll
-    for (int j = 0; j < kSeqs; ++j) {
-        if (L[j] < 0 || L[j] > a.d.max_seq_len || L[j] > room) {
+    // (loops are not unrolled: the instructions of this are fetched once per call, which is
+    // what it waits for)
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+        int L = a.d.seq_lens[b];
+        if (L < 0 || L > a.d.max_seq_len || L > room) {
             if (blockIdx.x == 0) record_error(a.d.status, KVATTN_ERR_BAD_INDEX);
-            L[j] = 0;
+            L = 0;
         }
-        if (b0 + j < a.d.batch) len[b0 + j] = L[j];
+        len[b] = L;
     }
     ok = __syncthreads_and(ok);
     if (!ok && blockIdx.x == 0 && tid == 0) record_error(a.d.status, KVATTN_ERR_BAD_INDEX);
-    int group[kSeqs];  // -1: none that it shares with
-#pragma unroll
-    for (int j = 0; j < kSeqs; ++j) {
-        group[j] = -1;
-        if (ok && b0 + j < P.cu[n]) {
-            const int g = group_of(P, n, b0 + j);
-            if (P.tokens[g] > 0 && L[j] >= P.tokens[g]) {
-                group[j] = g;
-                atomicMin(&P.leader[g], b0 + j);
-                atomicAdd(&P.members[g], 1);
-            }
+    auto has = [&](int b) {  // the group whose shared tokens sequence b has, -1: none
+        if (!ok || b >= P.cu[n]) return -1;
+        const int g = group_of(P, n, b);
+        return P.tokens[g] > 0 && len[b] >= P.tokens[g] ? g : -1;
+    };
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+        const int g = has(b);
+        P.own[b + 1] = g;
+        if (g >= 0) {
+            atomicMin(&P.leader[g], b);
+            atomicAdd(&P.members[g], 1);
         }
     }
     __syncthreads();
@@ -220,10 +222,11 @@ __device__ __forceinline__ void make_plan(const SharedArgs& a, Plan& P, int* len
         v[1] = tokens > 0 ? blocks_of(P.cu[tid + 1] - P.cu[tid], lg) * a.d.hkv : 0;
         v[0] = v[1] * (tokens / kPage);
     }
-    int own[kSeqs];
-#pragma unroll
-    for (int j = 0; j < kSeqs; ++j)
-        own[j] = v[2] += (L[j] + kPage - 1) / kPage - (group[j] >= 0 ? shared(group[j]) : 0);
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+        const int g = P.own[b + 1];
+        P.own[b + 1] = v[2] += (len[b] + kPage - 1) / kPage - (g >= 0 ? shared(g) : 0);
+    }
     const int mine = v[2];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1)
@@ -237,17 +240,14 @@ __device__ __forceinline__ void make_plan(const SharedArgs& a, Plan& P, int* len
         for (int i = 0; i < 3; ++i) P.sums[i][warp] = v[i];
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w)
-#pragma unroll
-        for (int i = 0; i < 3; ++i) v[i] += w < warp ? P.sums[i][w] : 0;
+    for (int i = 0; i < 3; ++i) v[i] += __reduce_add_sync(0xffffffffu, lane < warp ? P.sums[i][lane] : 0);
     if (tid < n) {
         P.first[tid + 1] = v[0];
         P.segment[tid + 1] = v[1];
         P.tokens[tid] = tokens;
     }
-#pragma unroll
-    for (int j = 0; j < kSeqs; ++j)
-        if (b0 + j < a.d.batch) P.own[b0 + j + 1] = v[2] - mine + own[j];
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) P.own[b + 1] += v[2] - mine;
     if (tid == 0) P.first[0] = P.segment[0] = P.own[0] = 0;
     __syncthreads();
 }
@@ -256,16 +256,31 @@ __device__ __forceinline__ void make_plan(const SharedArgs& a, Plan& P, int* len
 struct Ranges {
     int ctas, per, own_per;
 };
-// In times of a shared page: an own segment takes kOwnSegment besides its pages (state, queries),
-// a prefix CTA `set_up` besides its own (tensor memory, the pipeline's filling) and `segment` for each of its
+// In times of a shared page: an own page takes page + more x^2, x the prefixes' part of the
+// work (a CTA on a prefix has more of its copies under way, so own pages take longer the more
+// such CTAs share HBM with them), an own segment kSegment besides (state, queries), a prefix CTA `set_up`
+// besides its own (tensor memory, the pipeline's filling) and `segment` for each of its
 // segments (256 rows of output); so with t for all,
-// (shared + segment segments) / (t - set_up) + (own + kOwnSegment own_segments) / t = ctas.
+// (shared + segment segments) / (t - set_up) + (page own + kSegment own_segments) / t = ctas.
+// Measured, us (64 sequences but for the last): bf16, 2048 shared and up to 512 own
+// tokens | 12 prompts of up to 8191, 192 sequences, 1024 own | 32 x (65536, 256): page 1, more 0,
+// kSegment 1: 27.2 | 129 | 72; 1, 0.9, 1: 27.9 | 133 | 55; 0.8, 1.1, 1: 27.0 | 126 | 56; 0.8, 0.9, 0:
+// 27 | 125 | 59.  fp8, 16384 and 1024 | 8192 and 2048 | 65536 and 1: 1, 0, 2: 89 | - | 99; 0.5, 0, 1: 74 | 77 | 100;
+// 0.4, 0.2, 2: 71 | 69 | 99; 0.35, 0.1, 1: 78 | 69 | 99; 0.3, 0.2, 0: 77 | 76 | 137.
+template <bool kF8>
+struct OwnCost {
+    static constexpr float kPage = kF8 ? 0.4f : 0.85f, kMore = kF8 ? 0.1f : 1.0f, kSegment = kF8 ? 2.f : 1.f;
+};
+template <bool kF8>
 __device__ __forceinline__ Ranges ranges_of(int shared, int segments, int own, int own_segments, int ctas,
-                                            float set_up, float segment, int warps)
+                                            float set_up, float segment)
 {
+    using C = OwnCost<kF8>;
+    constexpr int warps = own_warps<kF8>();
     Ranges r{0, 0, 0};
     if (shared > 0) {
-        const float c = (float)ctas, p = (float)shared + segment * (float)segments, o = (float)own + kOwnSegment * (float)own_segments,
+        const float c = (float)ctas, p = (float)shared + segment * (float)segments, part = p / (p + (float)own),
+                    o = (C::kPage + C::kMore * part * part) * (float)own + C::kSegment * (float)own_segments,
                     u = set_up * c + p + o;
         const float t = (u + sqrtf(fmaxf(u * u - 4.f * c * set_up * o, 0.f))) / (2.f * c);
         r.ctas = min((int)ceilf(p / fmaxf(t - set_up, 1.f)), (shared + kMinPer - 1) / kMinPer);
@@ -1137,8 +1152,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int* len = reinterpret_cast<int*>(smem);  // (where Q will be)
     make_plan(a, P, len, lg);
     const int shared = P.first[a.num_groups], own = a.d.hkv * P.own[a.d.batch];
-    const Ranges ranges = ranges_of(shared, P.segment[a.num_groups], own, a.d.hkv * a.d.batch, gridDim.x, kSetUpBytes / GE::kCost,
-                                    kSegmentBytes / GE::kCost, own_warps<kF8>());
+    const Ranges ranges = ranges_of<kF8>(shared, P.segment[a.num_groups], own, a.d.hkv * a.d.batch, gridDim.x,
+                                         kSetUpBytes / GE::kCost, kSegmentBytes / GE::kCost);
     // where the merge finds each sequence's partial results
     for (int b = (int)blockIdx.x + (int)gridDim.x * threadIdx.x; b < a.d.batch; b += (int)gridDim.x * kThreads) {
         SharedOf o{};
