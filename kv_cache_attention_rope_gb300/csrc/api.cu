@@ -891,20 +891,21 @@ bool groups_ok(int32_t batch, int32_t num_groups, int32_t max_shared_len)
 
 // Whether prefixes are read once: if they save enough, by the call's bounds.  That form
 // starts with a plan and ends with a merge, 12 us together at least, and reads own fp8
-// pages at half the rate of decode_direct.cu.  Measured over batches of 2 to 64,
-// prefixes of 128 to 8192 tokens and own parts of up to 32 to 2048 (us, once / each
-// sequence by itself): bf16, saved MB 25 (2 x 8192, 12/12 heads of 64): 16.8 / 12.6;
-// 33 (64 x 128, 32/8 heads of 128): 13.7 / 8.0; 94 (16 x 2048, 12/12 heads): 19.9 / 30.4
-// with 2048 own tokens and 12.0 / 18.8 with 512; 528 (64 x 2048, 32/8): 32.1 / 93.8.  fp8
-// (64/8 heads), saved and own MB 65 and 69: 26.6 / 24.5; 68 and 69: 36.0 / 24.2;
-// 272 and 69: 44.8 / 52.8; 207 and 276: 127 / 72; 1089 and 276: 123 / 226.
+// pages slower than decode_direct.cu does; a prefix of a few rows costs it as much as one of 128.
+// Measured over batches of 2 to 64, prefixes of 128 to 8192 tokens and own parts of up
+// to 32 to 2048 (us, once / each sequence by itself): bf16, saved MB 25 (2 x 8192, 12/12
+// heads of 64): 16.8 / 12.6; 33 (64 x 128, 32/8 heads of 128): 13.7 / 8.0; 94 (16 x 2048,
+// 12/12 heads): 19.9 / 30.4 with 2048 own tokens and 12.0 / 18.8 with 512; 528 (64 x 2048,
+// 32/8): 32.1 / 93.8.  fp8 (64/8 heads), saved and own MB 65 and 69: 26.6 / 24.5; 68 and 69:
+// 36.0 / 24.2; 272 and 69: 36.1 / 52.8; 1089 and 276: 75 / 226; 16 groups of 4, 207 and 69: 71 / 51;
+// 829 and 276: 170 / 225.
 bool prefixes_once(const kvattn_config* cfg, bool fp8, int32_t batch, int32_t max_seq_len, int32_t num_groups,
                    int32_t max_shared_len)
 {
     const double token = (double)cfg->num_kv_heads * (fp8 ? kF8Page / 16 : 4 * cfg->head_dim);
     const double saved = token * (batch - num_groups) * max_shared_len;
     const double own = token * batch * std::max(0, max_seq_len - max_shared_len);
-    return fp8 ? saved >= 64e6 + 1.5 * own : saved >= 40e6;
+    return fp8 ? saved >= 64e6 + 1.5 * own + 1.1e6 * num_groups * cfg->num_kv_heads : saved >= 40e6;
 }
 
 // Workspace of the form that reads prefixes once (SharedArgs), each part 256-byte

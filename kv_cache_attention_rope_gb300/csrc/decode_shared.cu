@@ -112,7 +112,8 @@ struct Plan {
     int members[kMaxGroups];  // how many have them
     int first[kMaxGroups + 1], segment[kMaxGroups + 1];
     int own[kMaxSharedBatch + 1];
-    int sums[3][kThreads / 32];
+    int two_rows;  // shared pages of segments of two row tiles
+    int sums[4][kThreads / 32];
 };
 
 template <int kD, bool kF8>
@@ -215,12 +216,14 @@ __device__ __forceinline__ void make_plan(const SharedArgs& a, Plan& P, int* len
     }
     __syncthreads();
     auto shared = [&](int g) { return ok && P.members[g] >= 2 ? P.tokens[g] / kPage : 0; };  // pages
-    int v[3] = {0, 0, 0};  // pages of a group, its segments; own pages of this thread's sequences
+    int v[4] = {0, 0, 0, 0};  // pages of a group, its segments; own pages of this thread's sequences; two_rows
     int tokens = 0;
     if (tid < n) {
         tokens = shared(tid) * kPage;
         v[1] = tokens > 0 ? blocks_of(P.cu[tid + 1] - P.cu[tid], lg) * a.d.hkv : 0;
         v[0] = v[1] * (tokens / kPage);
+        const int rows = (P.cu[tid + 1] - P.cu[tid]) << lg;
+        v[3] = (rows + kSharedRows - kBM - 1) / kSharedRows * a.d.hkv * (tokens / kPage);
     }
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
@@ -231,16 +234,16 @@ __device__ __forceinline__ void make_plan(const SharedArgs& a, Plan& P, int* len
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < 4; ++i) {
             const int x = __shfl_up_sync(0xffffffffu, v[i], o);
             if (lane >= o) v[i] += x;
         }
     if (lane == 31)
 #pragma unroll
-        for (int i = 0; i < 3; ++i) P.sums[i][warp] = v[i];
+        for (int i = 0; i < 4; ++i) P.sums[i][warp] = v[i];
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 3; ++i) v[i] += __reduce_add_sync(0xffffffffu, lane < warp ? P.sums[i][lane] : 0);
+    for (int i = 0; i < 4; ++i) v[i] += __reduce_add_sync(0xffffffffu, lane < warp ? P.sums[i][lane] : 0);
     if (tid < n) {
         P.first[tid + 1] = v[0];
         P.segment[tid + 1] = v[1];
@@ -249,6 +252,7 @@ __device__ __forceinline__ void make_plan(const SharedArgs& a, Plan& P, int* len
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) P.own[b + 1] += v[2] - mine;
     if (tid == 0) P.first[0] = P.segment[0] = P.own[0] = 0;
+    if (tid == kThreads - 1) P.two_rows = v[3];
     __syncthreads();
 }
 
@@ -256,30 +260,34 @@ __device__ __forceinline__ void make_plan(const SharedArgs& a, Plan& P, int* len
 struct Ranges {
     int ctas, per, own_per;
 };
-// In times of a shared page: an own page takes page + more x^2, x the prefixes' part of the
-// work (a CTA on a prefix has more of its copies under way, so own pages take longer the more
-// such CTAs share HBM with them), an own segment kSegment besides (state, queries), a prefix CTA `set_up`
-// besides its own (tensor memory, the pipeline's filling) and `segment` for each of its
+// In times of a shared page of one row tile: one of two takes 1 + kTwo (fp8, whose conversion and
+// softmax bound it; bf16 pages are HBM's), an own page kPage + kMore x^2, x the prefixes' part of the
+// work (a CTA on a prefix has more of its copies under way, so own bf16 pages take longer the
+// more such CTAs share HBM with them), an own segment kSegment besides (state, queries), a prefix CTA `set_up`
+// besides its pages (tensor memory, the pipeline's filling) and `segment` for each of its
 // segments (256 rows of output); so with t for all,
-// (shared + segment segments) / (t - set_up) + (page own + kSegment own_segments) / t = ctas.
-// Measured, us (64 sequences but for the last): bf16, 2048 shared and up to 512 own
-// tokens | 12 prompts of up to 8191, 192 sequences, 1024 own | 32 x (65536, 256): page 1, more 0,
-// kSegment 1: 27.2 | 129 | 72; 1, 0.9, 1: 27.9 | 133 | 55; 0.8, 1.1, 1: 27.0 | 126 | 56; 0.8, 0.9, 0:
-// 27 | 125 | 59.  fp8, 16384 and 1024 | 8192 and 2048 | 65536 and 1: 1, 0, 2: 89 | - | 99; 0.5, 0, 1: 74 | 77 | 100;
-// 0.4, 0.2, 2: 71 | 69 | 99; 0.35, 0.1, 1: 78 | 69 | 99; 0.3, 0.2, 0: 77 | 76 | 137.
+// p / (t - set_up) + o / t = ctas.
+// Measured, us (64 sequences but for two): bf16 (kPage, kMore, kSegment), 2048 shared and up to 512 own
+// tokens | 12 prompts of up to 8191, 192 sequences, 1024 own | 32 x (65536, 256): 1, 0, 1: 27.2 | 129 |
+// 72; 1, 0.9, 1: 27.9 | 133 | 55; 0.85, 1, 1: 27 | 125 | 58; 0.9, 0.9, 0: 27 | 125 | 59.  fp8 (kPage, kSegment, kTwo), 16384
+// and 1024 | 8192 and 2048 | 16 x (8192, 2048): 1, 4, 1.4: 72 | 77 | 29; 1, 4, 1: 75 | 83 | 29; 0.8, 4, 1.2: 71 | 73 | 26;
+// 1.2, 4, 1.6: 74 | 78 | 28; a page of two row tiles counted as of one: 1, 2: 89 and 0.4, 2: 71 | 69 | -,
+// but 16 x 8192 shared by 4s, with 32 own, 56 instead of 40.
 template <bool kF8>
 struct OwnCost {
-    static constexpr float kPage = kF8 ? 0.4f : 0.85f, kMore = kF8 ? 0.1f : 1.0f, kSegment = kF8 ? 2.f : 1.f;
+    static constexpr float kPage = kF8 ? 0.8f : 0.85f, kMore = kF8 ? 0.f : 1.0f, kSegment = kF8 ? 4.f : 1.f,
+                           kTwo = kF8 ? 1.2f : 0.f;
 };
 template <bool kF8>
-__device__ __forceinline__ Ranges ranges_of(int shared, int segments, int own, int own_segments, int ctas,
+__device__ __forceinline__ Ranges ranges_of(int shared, int two_rows, int segments, int own, int own_segments, int ctas,
                                             float set_up, float segment)
 {
     using C = OwnCost<kF8>;
     constexpr int warps = own_warps<kF8>();
     Ranges r{0, 0, 0};
     if (shared > 0) {
-        const float c = (float)ctas, p = (float)shared + segment * (float)segments, part = p / (p + (float)own),
+        const float c = (float)ctas, p = (float)shared + C::kTwo * (float)two_rows + segment * (float)segments,
+                    part = p / (p + (float)own),
                     o = (C::kPage + C::kMore * part * part) * (float)own + C::kSegment * (float)own_segments,
                     u = set_up * c + p + o;
         const float t = (u + sqrtf(fmaxf(u * u - 4.f * c * set_up * o, 0.f))) / (2.f * c);
@@ -1152,7 +1160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int* len = reinterpret_cast<int*>(smem);  // (where Q will be)
     make_plan(a, P, len, lg);
     const int shared = P.first[a.num_groups], own = a.d.hkv * P.own[a.d.batch];
-    const Ranges ranges = ranges_of<kF8>(shared, P.segment[a.num_groups], own, a.d.hkv * a.d.batch, gridDim.x,
+    const Ranges ranges = ranges_of<kF8>(shared, P.two_rows, P.segment[a.num_groups], own, a.d.hkv * a.d.batch, gridDim.x,
                                          kSetUpBytes / GE::kCost, kSegmentBytes / GE::kCost);
     // where the merge finds each sequence's partial results
     for (int b = (int)blockIdx.x + (int)gridDim.x * threadIdx.x; b < a.d.batch; b += (int)gridDim.x * kThreads) {
