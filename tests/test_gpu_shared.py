@@ -226,6 +226,37 @@ def test_bad_lengths_and_blocks(kvattn_lib, dtype, hq, hkv, d):
         _check(SubCase(c, [0, 1, 3]), q[[0, 1, 3]], f64(got[[0, 1, 3]]), dtype)
 
 
+@pytest.mark.parametrize("dtype,hq,hkv,d", [("bf16", 32, 8, 128), ("bf16", 12, 12, 64), ("fp8", 32, 8, 128)])
+def test_offsets_past_32_bits(kvattn_lib, dtype, hq, hkv, d):
+    """The blocks of a batch at the end of a pool of over 4 GB, the prefix partly there."""
+    kv = kvattn_lib
+    c = SharedCache(kv, dtype, hkv, d, [(520, [521, 600, 533]), (0, [40])], seed=14)
+    small = [c.cache.pool] if dtype == "fp8" else [c.cache.k_pool, c.cache.v_pool]
+    count = 2 ** 32 // (small[0][0].numel() * small[0].element_size()) + 200
+    pools = [torch.empty((count,) + p.shape[1:], dtype=p.dtype, device="cuda") for p in small]
+    n = small[0].shape[0]
+    ids = torch.from_numpy(np.where(np.arange(n) % 3 == 0, np.arange(n), count - n + np.arange(n))).cuda()
+    for big, p in zip(pools, small):
+        big[ids] = p
+    c.cache = kv.CacheFP8(*pools) if dtype == "fp8" else kv.Cache(*pools)
+    c.d_table = torch.where(c.d_table >= 0, ids[c.d_table.clamp(min=0).long()], -1).int()
+    q = _q(np.random.default_rng(15), (len(c.lens), hq, d), dtype)
+    cfg = kv.make_config(hq, hkv, d, kv.BF16)
+    call = kv.decode_shared_fp8 if dtype == "fp8" else kv.decode_shared
+    for most in (520, LOOSE):
+        got = call(cfg, c.cache, q.cuda(), c.d_table, c.d_lens, max(c.lens), c.d_cu, c.d_shared, most)
+        assert kv.get_device_status() == 0
+        _check(c, q, f64(got), dtype, f"bound {most}")
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,d", [("bf16", 4, 1, 64), ("fp8", 4, 1, 128)])
+@pytest.mark.parametrize("groups,n", [(192, 2), (193, 2), (1, 2048), (1, 2049), (100, 20)])
+def test_many_groups_and_sequences(kvattn_lib, dtype, hq, hkv, d, groups, n):
+    """The most groups and sequences whose prefixes are read once, and one more of each."""
+    _run(kvattn_lib, dtype, hq, hkv, d, [(128 + 16 * (g % 3), [130 + 16 * (g % 3) + i % 5 for i in range(n)])
+                                         for g in range(groups)], seed=16)
+
+
 class SubCase:
     def __init__(self, c, rows):
         self.k, self.v, self.lens = [c.k[r] for r in rows], [c.v[r] for r in rows], [c.lens[r] for r in rows]
