@@ -589,14 +589,22 @@ kvattn_status kvattn_decode_window_fp8(const kvattn_config* cfg, const kvattn_ca
  *   workspace   >= kvattn_decode_shared_workspace_size(...) bytes, any contents,
  *               256-byte aligned; calls that may overlap on the GPU need one each
  * Every dtype, head layout and block size of kvattn_decode.  Prefixes are read
- * once in bf16 caches whose block_size is a multiple of 16; other calls, and those too short to gain, read
- * each sequence by itself.  What a sequence sees counts as in kvattn_decode_window: a NaN score makes
- * its query head's output NaN.
+ * once in bf16 and fp8 caches whose block_size is a multiple of 16 (pools of fewer
+ * than 2^31 / Hkv tokens), for at most 192 groups and 2 to 2048 sequences, if that
+ * saves enough by the call's bounds (40 MB of K and V; fp8: 64 MB and more with long
+ * own parts and many groups); then a group's first 128 tokens or more, down to a
+ * multiple of 16, that at least two sequences have.  Other calls read each sequence
+ * by itself, as kvattn_decode_window without a window does.
+ * What a sequence sees counts as in kvattn_decode_window: a NaN score makes
+ * its query head's output NaN.  Weights over a prefix are rounded to bf16 before
+ * their product with V.
  * The other arguments, results and errors as kvattn_decode.  Groups that are none
  * of these, or a shared length above max_shared_len, share nothing: the results
  * are right all the same, and a call that reads prefixes once records BAD_INDEX.
  *
- * kvattn_decode_shared_fp8: the same over a kvattn_cache_fp8, as kvattn_decode_window_fp8.
+ * kvattn_decode_shared_fp8: the same over a kvattn_cache_fp8, as kvattn_decode_window_fp8;
+ * over a prefix read once, q is rounded to f16 (of q / 16, so that it has f16's range) and a
+ * weight times its token's V scale to bf16.
  */
 size_t kvattn_decode_shared_workspace_size(const kvattn_config* cfg, int32_t batch, int32_t max_seq_len,
                                            int32_t num_groups, int32_t max_shared_len);
