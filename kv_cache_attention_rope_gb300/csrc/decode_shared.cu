@@ -37,12 +37,14 @@
 //
 // Own keys (own_warp): the pages of all (sequence, KV head) segments form a stream
 // too, cut into equal ranges, one per warp.  A warp loads its pages straight from
-// global memory into mma.sync fragments (bf16_tile.cuh), a page ahead, and writes a
+// global memory into mma.sync fragments (bf16_tile.cuh), a page ahead and prefetched into
+// L2 a page before that, and writes a
 // state where a segment ends: no warp waits for another, and nothing is paid per
 // segment but its state.  That takes 230 registers, so eight warps of the CTA do it
 // and the others give theirs up.  (Twelve warps with rings in shared memory: a page took
 // 1500 cycles of work and 2000 to issue its cp.async copies, or as long for its two TMA
-// boxes; own parts of 64 sequences of up to 4096, 537 MB: 123 and 113 us.)
+// boxes; own parts of 64 sequences of up to 4096, 537 MB, behind 2048 shared tokens: 123 and 113 us,
+// now 105, without the prefetch 134.)
 //
 // fp8 pages.  On prefixes, warp 0 copies whole pages and others make the operands of
 // them: warps 2 and 3 K's codes exactly in f16 (and Q in f16 over 16), the output warps, which
@@ -75,6 +77,7 @@ constexpr int kMinShared = 128;  // tokens of a prefix that is worth pieces of i
 constexpr int kMinPer = 8;     // fewest shared pages of a CTA's range
 constexpr int kMinOwn = 2;     // fewest own pages of a warp's range
 constexpr float kSetUpBytes = 180000.f, kSegmentBytes = 80000.f;  // of K and V that take as long (ranges_of)
+constexpr int kOwnAhead = 1;  // bf16: pages between the one a warp loads and the one it prefetches into L2
 constexpr int kPast = 4;       // pieces whose sums may be waiting for the output warps
 constexpr int kRaw = 2;        // fp8: stages of pages
 static_assert(kSharedRows == 2 * kBM, "a prefix piece's rows");
@@ -267,15 +270,16 @@ struct Ranges {
 // besides its pages (tensor memory, the pipeline's filling) and `segment` for each of its
 // segments (256 rows of output); so with t for all,
 // p / (t - set_up) + o / t = ctas.
-// Measured, us (64 sequences but for two): bf16 (kPage, kMore, kSegment), 2048 shared and up to 512 own
-// tokens | 12 prompts of up to 8191, 192 sequences, 1024 own | 32 x (65536, 256): 1, 0, 1: 27.2 | 129 |
-// 72; 1, 0.9, 1: 27.9 | 133 | 55; 0.85, 1, 1: 27 | 125 | 58; 0.9, 0.9, 0: 27 | 125 | 59.  fp8 (kPage, kSegment, kTwo), 16384
+// Measured, us (64 sequences but for two): bf16 (kPage, kMore), 2048 shared and up to 512 own
+// tokens | 12 prompts of up to 8191, 192 sequences, 1024 own | 32 x (65536, 256): 0.6, 1: 23.4 | 104 |
+// 55; 0.85, 1: 26.5 | 127 | 55; 0.4, 1.2: 26.4 | 112 | 55; 0.95, 0.8: 26.7 | 136 | 55; before own pages came
+// by way of L2, 1, 0: 27.2 | 129 | 72.  fp8 (kPage, kSegment, kTwo), 16384
 // and 1024 | 8192 and 2048 | 16 x (8192, 2048): 1, 4, 1.4: 72 | 77 | 29; 1, 4, 1: 75 | 83 | 29; 0.8, 4, 1.2: 71 | 73 | 26;
 // 1.2, 4, 1.6: 74 | 78 | 28; a page of two row tiles counted as of one: 1, 2: 89 and 0.4, 2: 71 | 69 | -,
 // but 16 x 8192 shared by 4s, with 32 own, 56 instead of 40.
 template <bool kF8>
 struct OwnCost {
-    static constexpr float kPage = kF8 ? 0.8f : 0.85f, kMore = kF8 ? 0.f : 1.0f, kSegment = kF8 ? 4.f : 1.f,
+    static constexpr float kPage = kF8 ? 0.8f : 0.6f, kMore = kF8 ? 0.f : 1.0f, kSegment = kF8 ? 4.f : 1.f,
                            kTwo = kF8 ? 1.2f : 0.f;
 };
 template <bool kF8>
@@ -971,8 +975,23 @@ __device__ __forceinline__ void own_warp(const SharedArgs& a, const Plan& P, con
         t.load_k(kp + row * (kHD * 2), seen_of(info), g4, q4);
         t.load_v(vv, vp + row * (kHD * 2), seen_of(info), g4, q4);
     };
+    // Page j on its way to L2, if it is of the looked up batch: a page is loaded one page's
+    // time ahead, less than memory takes while all SMs read.  (One, two, three, five pages before
+    // its load: 114, 120, 124, 137 us for 64 sequences of up to 4096 own tokens, without 134.)
+    auto prefetch = [&](int j) {
+        if ((j & 31) < kOwnAhead || j >= n) return;
+        const int64_t row = __shfl_sync(0xffffffffu, page.row, j & 31);
+        constexpr int kLines = kPage * kHD * 2 / 128;
+#pragma unroll
+        for (int i = 0; i < 2 * kLines / 32; ++i) {
+            const int line = lane + 32 * i;
+            const char* at = (line < kLines ? kp : vp) + row * (kHD * 2) + line % kLines * 128;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+        }
+    };
     load(0, v[0]);
     load_q(seg);
+    prefetch(kOwnAhead);
     Softmax st;
     float o[kHD / 16][4];
     bool fresh = true;
@@ -998,6 +1017,7 @@ __device__ __forceinline__ void own_warp(const SharedArgs& a, const Plan& P, con
             seg = __shfl_sync(0xffffffffu, page.seg, (j + 1) & 31);
             info = __shfl_sync(0xffffffffu, page.info, (j + 1) & 31);
             load(j + 1, vnext);
+            prefetch(j + 1 + kOwnAhead);
             if (fresh) load_q(seg);
         }
         const float sl2 = a.d.scale_log2;
