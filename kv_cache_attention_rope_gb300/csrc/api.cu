@@ -393,7 +393,8 @@ bool axes_of_pairs(const kvattn_rope_axes* x, int pairs, uint8_t* axis)
 
 // axes null: `positions` are the slots too.
 kvattn_status rotary_append_any(const kvattn_config* cfg, const kvattn_rotary* rotary, const kvattn_rope_axes* axes,
-                                const int32_t* slots, const kvattn_cache* cache, bool fp8, void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                const int32_t* slots, const kvattn_cache* cache, bool fp8, void* q, int64_t q_stride,
+                                const void* k, int64_t k_stride, const void* v,
                                 int64_t v_stride, void* q_out, const int32_t* positions, const int32_t* seq_ids,
                                 const int32_t* block_table, int32_t num_seqs, int32_t max_blocks_per_seq,
                                 int32_t num_tokens, void* stream)
@@ -948,7 +949,8 @@ kvattn_status decode_shared_any(const kvattn_config* cfg, const kvattn_cache* ca
                                           max_seq_len, 0, out);
     if (st != KVATTN_OK || batch == 0) return st;
     const SharedLayout l = shared_layout(cfg, batch, max_seq_len, num_groups, max_shared_len);
-    const bool once = l.bytes > 0 && prefixes_once(cfg, fp8, batch, max_seq_len, num_groups, max_shared_len) && cache->block_size % 16 == 0 &&
+    const bool once = l.bytes > 0 && prefixes_once(cfg, fp8, batch, max_seq_len, num_groups, max_shared_len) &&
+                      cache->block_size % 16 == 0 &&
                       cache->num_blocks * cfg->num_kv_heads < ((int64_t)1 << 31) / cache->block_size;
     if (!once)  // every sequence by itself
         return decode_any(cfg, cache, fp8, {INT32_MAX, 0}, q, block_table, max_blocks_per_seq, seq_lens, batch,

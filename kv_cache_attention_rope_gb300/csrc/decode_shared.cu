@@ -136,7 +136,7 @@ struct Geo {
     static constexpr int kOffBar = kOffScales + (kF8 ? kPast * 1024 : 0);
     // fp32: row maxima of a tile [2][2 halves][128]; of kPast pieces, row sums [2 halves][2][128] and maxima [2][128]
     static constexpr int kOffX = kOffBar + 384;
-    static constexpr int kOffPlan = kOffX + 2048 + kPast * 3072;
+    static constexpr int kOffPlan = kOffX + 2048 + kPast * 768 * 4;
     static constexpr int kSmemBytes = kOffPlan + (int)sizeof(Plan) + 1024;  // + slack to align the base to 1 KB
     static constexpr int kOffRing = 4 * kMaxSharedBatch;  // own keys, fp8: pages of the warps, behind the lengths
     static_assert(kD == 64 || kD == 128, "head dim");
