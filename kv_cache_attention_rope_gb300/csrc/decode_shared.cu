@@ -275,12 +275,12 @@ struct Ranges {
 // 55; 0.85, 1: 26.5 | 127 | 55; 0.4, 1.2: 26.4 | 112 | 55; 0.95, 0.8: 26.7 | 136 | 55; before own pages came
 // by way of L2, 1, 0: 27.2 | 129 | 72.  fp8 (kPage, kSegment, kTwo), 16384
 // and 1024 | 8192 and 2048 | 16 x (8192, 2048): 1, 4, 1.4: 72 | 77 | 29; 1, 4, 1: 75 | 83 | 29; 0.8, 4, 1.2: 71 | 73 | 26;
-// 1.2, 4, 1.6: 74 | 78 | 28; a page of two row tiles counted as of one: 1, 2: 89 and 0.4, 2: 71 | 69 | -,
+// 0.8, 4, 2: 70 | 64 | -; 1, 4, 2.4: 69 | 67 | -; 0.6, 3, 1.6: 83 | 68 | -; 1.2, 4, 1.6: 74 | 78 | 28; a page of two row tiles counted as of one: 1, 2: 89 and 0.4, 2: 71 | 69 | -,
 // but 16 x 8192 shared by 4s, with 32 own, 56 instead of 40.
 template <bool kF8>
 struct OwnCost {
     static constexpr float kPage = kF8 ? 0.8f : 0.6f, kMore = kF8 ? 0.f : 1.0f, kSegment = kF8 ? 4.f : 1.f,
-                           kTwo = kF8 ? 1.2f : 0.f;
+                           kTwo = kF8 ? 2.0f : 0.f;
 };
 template <bool kF8>
 __device__ __forceinline__ Ranges ranges_of(int shared, int two_rows, int segments, int own, int own_segments, int ctas,
