@@ -598,6 +598,8 @@ kvattn_status kvattn_decode_window_fp8(const kvattn_config* cfg, const kvattn_ca
  * What a sequence sees counts as in kvattn_decode_window: a NaN score makes
  * its query head's output NaN.  Weights over a prefix are rounded to bf16 before
  * their product with V.
+ * A block that is not in the pool has no keys (BAD_INDEX): for a sequence whose row
+ * names it, and for a whole group if its prefix is read through that row.
  * The other arguments, results and errors as kvattn_decode.  Groups that are none
  * of these, or a shared length above max_shared_len, share nothing: the results
  * are right all the same, and a call that reads prefixes once records BAD_INDEX.

@@ -10,7 +10,8 @@
 // (section 3.4 of the same page: states over parts of the keys merge by their
 // maxima and sums; "Nano-vLLM Part 2" page, section 05: sequences with a common
 // prefix share its blocks).  Only whole 16-token pages of a prefix are shared, and a
-// sequence that is shorter takes no part, so no row has a mask of its own.
+// sequence that is shorter takes no part, so no row has a mask of its own.  A page whose block
+// is not in the pool is seen by nobody: its scores are -infinity, its V is zero.
 //
 // What bounds it.  A KV head's queries over a prefix are (sequences of the group) x
 // G rows of one matrix product, so the prefix's K and V are read once, 4 D e bytes a
@@ -80,6 +81,10 @@ constexpr float kSetUpBytes = 180000.f, kSegmentBytes = 80000.f;  // of K and V 
 constexpr int kOwnAhead = 1;  // bf16: pages between the one a warp loads and the one it prefetches into L2
 constexpr int kPast = 4;       // pieces whose sums may be waiting for the output warps
 constexpr int kRaw = 2;        // fp8: stages of pages
+// Tiles whose pages' presence is kept.  It is written when the tile is copied and read by its
+// softmax: a K stage is free after S of two tiles before, which was issued after the P.V, and so after
+// the softmax, of four tiles before; fp8's conversion may be a tile behind that.
+constexpr int kHave = 8;
 static_assert(kSharedRows == 2 * kBM, "a prefix piece's rows");
 static_assert(kMaxGroups <= kThreads, "a thread per group");
 // Registers per thread of the warpgroups (the block starts with 128 each:
@@ -100,6 +105,7 @@ struct Bars {
     // fp8: pages loaded, read; scales and Q converted (K and V: k_full[0], v_full[0] then)
     uint64_t raw_full[kRaw], raw_empty[kRaw], scales[kPast], q_f16[kStages];
     uint64_t drain;
+    uint32_t have[kHave];  // bit i: page i of the tile is there
     uint32_t tmem;
     int abort_flag;
 };
@@ -487,13 +493,20 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
                 if (!kF8) tma_prefetch_map(is_k ? &maps.k : &maps.v);
             }
             bool go = true;
-            // lane 0 waits for `empty` (unless the buffer is new) and arms `full`
-            auto arm = [&](uint64_t* full, uint64_t* empty, int use, uint32_t bytes) -> bool {
-                if (lane == 0) {
-                    go = use == 0 ? !*abort_flag : wait_or_abort(empty, (use - 1) & 1, abort_flag, status);
-                    if (go) mbar_arrive_expect_tx(full, bytes);
-                }
+            // lane 0 waits for `empty` (unless the buffer is new)
+            auto wait_empty = [&](uint64_t* empty, int use) -> bool {
+                if (lane == 0) go = use == 0 ? !*abort_flag : wait_or_abort(empty, (use - 1) & 1, abort_flag, status);
                 return go = __shfl_sync(0xffffffffu, go, 0);
+            };
+            // Zeros in the places of a tile's pages that are not there, before the tile is armed: V's
+            // weights are 0 (and 0 * NaN would not be), and fp8 pages have scales.
+            auto zero_missing = [&](unsigned char* stage, int bytes, int pages, uint32_t have) {
+                for (int i = 0; i < pages; ++i)
+                    if (!(have >> i & 1u))
+                        for (int x = lane; x < bytes / 16; x += 32)
+                            reinterpret_cast<uint4*>(stage + i * bytes)[x] = make_uint4(0, 0, 0, 0);
+                fence_async_smem();
+                __syncwarp();
             };
             // Lane i < 8 copies page i of a tile; its block's id comes from the table a
             // tile ahead (lanes without a page read their row's first entry).
@@ -520,12 +533,20 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
                 const int n = p.tiles();
                 for (int t = 0; t < n; ++t) {
                     const int row = pool_row(p, t, blk_next);
-                    const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, row >= 0)) *
-                                           (uint32_t)(kF8 ? kF8Page : kPageBytes);
+                    const uint32_t have = __ballot_sync(0xffffffffu, row >= 0);
+                    constexpr int kBytes = kF8 ? kF8Page : kPageBytes;
                     static_assert(kRaw == kStages, "stages of pages as of tiles");
                     const int s = g % kStages;
                     uint64_t* full = kF8 ? &B.raw_full[s] : is_k ? &B.k_full[s] : &B.v_full[s];
-                    if (!arm(full, kF8 ? &B.raw_empty[s] : is_k ? &B.k_empty[s] : &B.v_empty[s], g / kStages, bytes)) break;
+                    if (!wait_empty(kF8 ? &B.raw_empty[s] : is_k ? &B.k_empty[s] : &B.v_empty[s], g / kStages)) break;
+                    if ((kF8 || !is_k) && have != (1u << p.pages(t)) - 1u)
+                        zero_missing(smem + (kF8 ? GE::kOffRaw + s * GE::kRawBytes : kOffV + s * kTileBytes), kBytes, p.pages(t),
+                                     have);
+                    if (lane == 0) {
+                        if (is_k) B.have[g % kHave] = have;
+                        mbar_arrive_expect_tx(full, (uint32_t)__popc(have) * (uint32_t)kBytes);
+                    }
+                    __syncwarp();
                     if (kF8 && row >= 0)
                         bulk_load(smem + GE::kOffRaw + s * GE::kRawBytes + lane * kF8Page,
                                   (const char*)a.d.k_pool + (int64_t)(row / kPage) * kF8Page, kF8Page, full, pol);
@@ -543,7 +564,9 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
                         const int tiles = p.two() ? 2 : 1;
                         for (int x = 0; x < tiles; ++x) {
                             const int qs = qg % kStages;
-                            if (!arm(&B.q_full[qs], &B.q_empty[qs], qg / kStages, (uint32_t)kTileBytes)) break;
+                            if (!wait_empty(&B.q_empty[qs], qg / kStages)) break;
+                            if (lane == 0) mbar_arrive_expect_tx(&B.q_full[qs], (uint32_t)kTileBytes);
+                            __syncwarp();
                             if (lane < GE::kPanels)
                                 tma_load_3d(smem + kOffQ + qs * kTileBytes + lane * kPanel, &maps.q, 64 * lane, p.h << lg,
                                             p.b0 + x * (kBM >> lg), &B.q_full[qs], pol);
@@ -721,7 +744,7 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
                 const int y = j & 1;
                 const uint32_t tS = tmem + lane_base + x * 128 + hf * 64;
                 const uint32_t tO = tmem + lane_base + 256 + (two ? y : z) * 128 + hf * (kHD / 2);
-                const int keys = p.pages(p.tile(j)) * kPage - hf * 64;  // of this half's columns
+                const int u = v + p.tile(j);
                 wait_or_abort(&B.s_full[x], steps >> x & 1u, abort_flag, status);
                 __syncwarp();
                 steps ^= 1u << x;
@@ -734,7 +757,6 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
                     tmem_ld_wait();
                     [[maybe_unused]] const float4* vs = nullptr;  // V's scales of this half's columns
                     if constexpr (kF8) {
-                        const int u = v + p.tile(j);
                         const float4* ks = reinterpret_cast<const float4*>(smem + GE::kOffScales + (u % kPast) * 1024) + hf * 16;
                         vs = ks + 32;
                         wait_or_abort(&B.scales[u % kPast], (u / kPast) & 1, abort_flag, status);
@@ -747,10 +769,14 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
                             sv[4 * e + 3] = __float_as_uint(__uint_as_float(sv[4 * e + 3]) * k.w);
                         }
                     }
-                    if (keys < 64) {
+                    const uint32_t have = B.have[u % kHave] >> (4 * hf) & 0xfu;  // pages of this half's columns
+                    if (have != 0xfu) {
 #pragma unroll
-                        for (int e = 0; e < 64; ++e)
-                            if (e >= keys) sv[e] = __float_as_uint(-INFINITY);
+                        for (int i = 0; i < 4; ++i)
+                            if (!(have >> i & 1u)) {
+#pragma unroll
+                                for (int e = 0; e < kPage; ++e) sv[kPage * i + e] = __float_as_uint(-INFINITY);
+                            }
                     }
                     float m4[4];
 #pragma unroll
@@ -799,9 +825,8 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
                     // stage was free.  The whole warp rescales if any of its rows must (alpha is 1
                     // for the others).
                     if (__any_sync(0xffffffffu, rescale && j > (two ? 1 : 0))) {
-                        if (!two) {
-                            const int u = v + j - 1;
-                            wait_or_abort(&B.v_empty[u % kKV], (u / kKV) & 1, abort_flag, status);
+                        if (!two) {  // (tile u - 1)
+                            wait_or_abort(&B.v_empty[(u - 1) % kKV], ((u - 1) / kKV) & 1, abort_flag, status);
                             __syncwarp();
                             tc_fence_after();
                         }
