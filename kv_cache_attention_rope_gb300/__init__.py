@@ -365,8 +365,16 @@ def copy_blocks(cfg: Config, cache, src_ids, dst_ids, stream=None) -> None:
         if st is not None:
             return check(st, "kvattn_copy_blocks_fp8")
     dev = cache.pool.device if fp8 or isinstance(cache, LayeredCache) else cache.k_pool.device
-    src = src_ids if isinstance(src_ids, torch.Tensor) else torch.tensor(list(src_ids), dtype=torch.int32, device=dev)
-    dst = dst_ids if isinstance(dst_ids, torch.Tensor) else torch.tensor(list(dst_ids), dtype=torch.int32, device=dev)
+
+    def ids(x):
+        if isinstance(x, torch.Tensor):
+            return x
+        t = torch.tensor(list(x), dtype=torch.int32, device=dev)  # (there when this returns)
+        if stream is not None:  # the memory is the current stream's: not to be given away before the call has read it
+            t.record_stream(stream)
+        return t
+
+    src, dst = ids(src_ids), ids(dst_ids)
     if src.numel() != dst.numel():
         raise ValueError("src_ids and dst_ids differ in length")
     n = src.numel()
