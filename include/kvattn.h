@@ -29,7 +29,9 @@
  *     position past the block table) make the kernel skip that access and
  *     record KVATTN_ERR_BAD_INDEX in the device status word; a bounded wait
  *     that runs out records KVATTN_ERR_TIMEOUT.  Read and clear it with
- *     kvattn_get_device_status().
+ *     kvattn_get_device_status().  What a sequence or chunk whose table row
+ *     names such a block gets is unspecified, but for the calls that say it
+ *     (kvattn_decode_window, kvattn_decode_shared); the others keep theirs.
  *   - Element type: KVATTN_F32 or KVATTN_BF16 for q, k, v, the cache and the
  *     output alike; arithmetic is fp32 with fp32 accumulation.
  *   - Supported: head_dim 64 or 128, num_q_heads % num_kv_heads == 0 with
@@ -536,7 +538,7 @@ kvattn_status kvattn_decode_static_scratch(const kvattn_config* cfg, const kvatt
  * when they slid out of the window), and what their slots, or unseen slots of
  * blocks that are read, hold has no effect (NaN and infinities too).  What it
  * sees counts: a NaN score makes its query head's output NaN, one of -infinity
- * weighs nothing.
+ * weighs nothing.  A block of seen keys that is not in the pool (BAD_INDEX) has none.
  *   window      >= 1; INT32_MAX sees the whole cache
  *   num_sinks   >= 0
  *   num_splits  0: the library's choice, one launch when the keys are few;

@@ -127,12 +127,16 @@ struct Traits {
 };
 
 struct SharedLayout {
-    int ring_off, merge_off, pbuf_off, prefix_off, bar_off, flag_off, bytes;  // pbuf aliases merge
+    int ring_off, merge_off, pbuf_off, prefix_off, bar_off, flag_off, have_off, bytes;  // pbuf aliases merge
 };
 
 // Bytes of one ring stage: K and V pages of a tile (one fp8 page for an fp8 cache).
 template <bool kBF16, int kD, int kGT, bool kFP8>
 __host__ __device__ constexpr int stage_bytes() { return kFP8 ? kF8Page : Traits<kBF16, kD, kGT>::kStageBytes; }
+
+// Windowed form: V's scales of an fp8 page whose block is not in the pool (scales are positive).  A flag
+// per stage, which the consumers load besides, made the stream of 64 sequences of up to 32768 tokens 1.5 % slower.
+constexpr float kNoPage = -1.f;
 
 // Query heads a consumer warp merges per pass (its merge slot's size): a
 // GQA group of 8 on the tensor cores is merged in two passes of 4, which keeps
@@ -142,7 +146,7 @@ __host__ __device__ constexpr int stage_bytes() { return kFP8 ? kF8Page : Traits
 template <int kGT, bool kFP8 = false>
 __host__ __device__ constexpr int merge_heads() { return kFP8 ? 1 : kGT < 4 ? kGT : 4; }
 
-template <bool kBF16, int kD, int kGT, bool kFP8 = false>
+template <bool kBF16, int kD, int kGT, bool kFP8, bool kWin>
 __host__ __device__ inline SharedLayout shared_layout(int stages, int batch)
 {
     using T = Traits<kBF16, kD, kGT>;
@@ -165,6 +169,8 @@ __host__ __device__ inline SharedLayout shared_layout(int stages, int batch)
     off += 2 * stages * 8;
     L.flag_off = off;
     off += 16;
+    L.have_off = off;  // windowed form: whether the tile's block is there, per stage (fp8: kNoPage)
+    if (kWin && !kFP8) off += stages * 4;
     L.bytes = off;
     return L;
 }
@@ -276,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_sp
     extern __shared__ unsigned char smem_raw[];
     // 1 KB alignment: the tensor-core path's stages hold 128-byte-swizzled pages
     unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    const SharedLayout SL = shared_layout<kBF16, kD, kGT, kFP8>(stages, a.batch);
+    const SharedLayout SL = shared_layout<kBF16, kD, kGT, kFP8, kWin>(stages, a.batch);
     unsigned char* ring = smem + SL.ring_off;
     float* merge = reinterpret_cast<float*>(smem + SL.merge_off);
     int* prefix = reinterpret_cast<int*>(smem + SL.prefix_off);
@@ -284,6 +290,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_sp
     uint64_t* empty = full + stages;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SL.flag_off);
     int* max_nt_sh = reinterpret_cast<int*>(smem + SL.flag_off + 4);
+    [[maybe_unused]] int* have = reinterpret_cast<int*>(smem + SL.have_off);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = a.hq / a.hkv;
@@ -383,13 +390,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_sp
         while (iter.next(pc, a)) {
             const int h = pc.hh / nsub;
             const int32_t* trow = a.block_table + (int64_t)pc.b * a.max_blocks;
-            // block id of tile t (one lane per tile, 32 at a time, next batch prefetched)
+            // block id of tile t (one lane per tile, 32 at a time, next batch prefetched); in the
+            // place of a bad one block 0, whose keys the windowed form does not see
             auto fetch = [&](int t) -> int64_t {
                 if (t >= pc.t1) return 0;
                 const int32_t v = trow[first_token(pc, t) / a.block_size];
                 if (v < 0 || v >= a.num_blocks) {
                     record_error(a.status, KVATTN_ERR_BAD_INDEX);
-                    return 0;
+                    return kWin ? -1 : 0;
                 }
                 return v;
             };
@@ -422,13 +430,20 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_sp
                             const int tok = first_token(pc, base + j);
                             const int nvalid = min(kTile, pc.len - tok);
                             const uint32_t bytes = (uint32_t)nvalid * kD * T::kE;
-                            const int64_t row = (bj * a.hkv + h) * a.block_size + tok % a.block_size;
+                            if constexpr (kWin && !kFP8) have[stage] = bj >= 0;
+                            const int64_t row = ((kWin && bj < 0 ? 0 : bj) * a.hkv + h) * a.block_size + tok % a.block_size;
                             unsigned char* dst = ring + (size_t)stage * kStageB;
                             if constexpr (kFP8) {
                                 // the fp8 page of these 16 tokens: K, V^T and scales, one copy
-                                const int64_t page = row / kTile;
-                                mbar_arrive_expect_tx(&full[stage], kF8Page);
-                                bulk_load(dst, (const char*)a.k_pool + page * kF8Page, kF8Page, &full[stage], policy);
+                                if (kWin && bj < 0) {
+                                    for (int i = 0; i < kTile; ++i) reinterpret_cast<float*>(dst + kF8VsOff)[i] = kNoPage;
+                                    fence_async_smem();  // before the next copy into this stage
+                                    mbar_arrive(&full[stage]);
+                                } else {
+                                    const int64_t page = row / kTile;
+                                    mbar_arrive_expect_tx(&full[stage], kF8Page);
+                                    bulk_load(dst, (const char*)a.k_pool + page * kF8Page, kF8Page, &full[stage], policy);
+                                }
                             } else if constexpr (kMma) {
                                 // whole 16-row pages (rows past the sequence end are
                                 // masked out of S and zeroed in V by the consumer)
@@ -577,8 +592,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_sp
                 const unsigned char* pg = ring + (size_t)stage * kStageB;
                 const int tok0 = first_token(pc, pc.t0 + li);
                 const int nvalid = min(kTile, pc.len - tok0);
-                const uint32_t seen = kWin ? seen_bits(tok0, pc, a) : 0u;
-                const bool whole = kWin ? seen == (1u << kTile) - 1u : nvalid == kTile;
+                uint32_t seen = kWin ? seen_bits(tok0, pc, a) : 0u;
+                bool whole = kWin ? seen == (1u << kTile) - 1u : nvalid == kTile;
                 auto sees = [&](int i) { return kWin ? (seen >> i & 1u) != 0 : i < nvalid; };
                 float s[4] = {0.f, 0.f, 0.f, 0.f};  // S^T: (rk0, 2q4), (rk0, 2q4+1), (rk1, 2q4), (rk1, 2q4+1)
 #pragma unroll
@@ -595,6 +610,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_sp
                 const float* vsc = reinterpret_cast<const float*>(pg + kF8VsOff);
                 const float k0 = ksc[rk0] * sl2, k1 = ksc[rk1] * sl2;
                 float sv0 = vsc[rk0], sv1 = vsc[rk1];
+                if (kWin && sv0 == kNoPage) {
+                    seen = 0u;
+                    whole = false;
+                }
                 float x[4] = {s[0] * k0, s[1] * k0, s[2] * k1, s[3] * k1};
                 uint32_t vmask = 0xffffffffu;  // bytes of this lane's V words that belong to valid tokens
                 if (!whole) {
@@ -756,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_sp
                 unsigned char* vst = kst + T::kTileBytes;
                 const int tok0 = first_token(pc, pc.t0 + li);
                 const int nvalid = min(kTile, pc.len - tok0);
-                const uint32_t seen = kWin ? seen_bits(tok0, pc, a) : 0u;
+                const uint32_t seen = kWin && have[stage] ? seen_bits(tok0, pc, a) : 0u;
                 const bool whole = kWin ? seen == (1u << kTile) - 1u : nvalid == kTile;
                 auto sees = [&](int i) { return kWin ? (seen >> i & 1u) != 0 : i < nvalid; };
                 // page rows past the sequence end are stale (and rows outside the
@@ -886,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_sp
             const unsigned char* vs = ks + T::kTileBytes;
             const int tok0 = first_token(pc, pc.t0 + li);
             const int nvalid = min(kTile, pc.len - tok0);
-            const uint32_t seen = kWin ? seen_bits(tok0, pc, a) : 0u;
+            const uint32_t seen = kWin && have[stage] ? seen_bits(tok0, pc, a) : 0u;
             auto sees = [&](int i) { return kWin ? (seen >> i & 1u) != 0 : i < nvalid; };
 
             // ---- partial scores, slot (g, t) holding head g^hm, token t^tm
@@ -1092,12 +1111,12 @@ kvattn_status run(const DecodeArgs& a, cudaStream_t s)
     // always consumed by warp s % kConsumerWarps, in order, which keeps every
     // mbarrier wait at most one phase away from the phase it names (parity
     // waits cannot tell phase u from phase u - 2).
-    const int fixed = shared_layout<kBF16, kD, kGT, kFP8>(0, a.batch).bytes + 1024;  // + base alignment slack
-    const int per_stage = kStageB + 16;  // + two mbarriers
+    const int fixed = shared_layout<kBF16, kD, kGT, kFP8, kWin>(0, a.batch).bytes + 1024;  // + base alignment slack
+    const int per_stage = kStageB + 16 + (kWin && !kFP8 ? 4 : 0);  // + two mbarriers, and `have`
     const int budget = smem_sm / ctas_per_sm<kMma, kFP8>() - smem_reserved - fixed;
     int stages = std::min(65536 / kStageB, budget / per_stage);
     stages = std::max(kConsumerWarps, stages / kConsumerWarps * kConsumerWarps);
-    const SharedLayout SL = shared_layout<kBF16, kD, kGT, kFP8>(stages, a.batch);
+    const SharedLayout SL = shared_layout<kBF16, kD, kGT, kFP8, kWin>(stages, a.batch);
     const int smem_bytes = SL.bytes + 1024;
     auto kern = decode_split_kernel<kBF16, kD, kGT, kMma, kRowBoxes, kFP8, kWin>;
     static Residency residency;

@@ -76,3 +76,34 @@ def test_missing_of_one(kvattn_lib, dtype, hq, hkv, d):
         assert kv.get_device_status() == kv.STATUS_CODE["KVATTN_ERR_BAD_INDEX"]
         lacks = {0} if most == 512 else {0, 1, 2}  # (row 0 is the first that has them all)
         _check(c, q.double().numpy(), got, dtype, lambda r: range(80, 96) if r in lacks else [], range(6), f"bound {most}")
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,d", [("bf16", 32, 8, 128), ("bf16", 64, 8, 128), ("bf16", 8, 8, 128),
+                                            ("bf16", 16, 8, 128), ("fp8", 64, 8, 128), ("fp8", 32, 8, 128),
+                                            ("f32", 16, 8, 128), ("f32", 64, 8, 64)])
+def test_missing_under_long_bounds(kvattn_lib, dtype, hq, hkv, d):
+    """Calls that go to the balanced stream by their bound: a block that is not in the pool is seen by nobody there either,
+    in decode_shared without groups and in decode_window."""
+    kv = kvattn_lib
+    c = SharedCache(kv, dtype, hkv, d, [(0, [701, 760, 33, 640, 16])], seed=5)
+    cfg = kv.make_config(hq, hkv, d, kv.F32 if dtype == "f32" else kv.BF16)
+    call = kv.decode_shared_fp8 if dtype == "fp8" else kv.decode_shared
+    window = kv.decode_window_fp8 if dtype == "fp8" else kv.decode_window
+    q = _q(np.random.default_rng(6), (5, hq, d), dtype)
+    bound, none = 16 * 4200, torch.zeros(0, dtype=torch.int32, device="cuda")  # 5 * 8 * 4200 tiles: 65536 and more
+    gone = {0: [0, 7, 43], 1: [20, 21, 22, 23, 47], 4: [0]}
+    for block in (-1, c.cache.num_blocks):
+        table = c.d_table.clone()
+        for r, cols in gone.items():
+            table[r, cols] = block
+        # (block 0 is another sequence's: its keys must not stand in for the missing ones)
+        got = f64(call(cfg, c.cache, q.cuda(), table, c.d_lens, bound, torch.zeros(1, dtype=torch.int32, device="cuda"), none,
+                       0))
+        assert kv.get_device_status() == kv.STATUS_CODE["KVATTN_ERR_BAD_INDEX"]
+        lacks = lambda r: [16 * b + t for b in gone.get(r, []) for t in range(16)]  # noqa: E731
+        _check(c, q.double().numpy(), got, dtype, lacks, range(4), f"block {block}")
+        assert np.all(got[4] == 0)
+        got = f64(window(cfg, c.cache, q.cuda(), table, c.d_lens, bound, bound - 5))
+        assert kv.get_device_status() == kv.STATUS_CODE["KVATTN_ERR_BAD_INDEX"]
+        _check(c, q.double().numpy(), got, dtype, lacks, range(4), f"window, block {block}")
+        assert np.all(got[4] == 0)
