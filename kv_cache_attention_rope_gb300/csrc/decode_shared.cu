@@ -81,9 +81,9 @@ constexpr float kSetUpBytes = 180000.f, kSegmentBytes = 80000.f;  // of K and V 
 constexpr int kOwnAhead = 1;  // bf16: pages between the one a warp loads and the one it prefetches into L2
 constexpr int kPast = 4;       // pieces whose sums may be waiting for the output warps
 constexpr int kRaw = 2;        // fp8: stages of pages
-// Tiles whose pages' presence is kept.  It is written when the tile is copied and read by its
-// softmax: a K stage is free after S of two tiles before, which was issued after the P.V, and so after
-// the softmax, of four tiles before; fp8's conversion may be a tile behind that.
+// Tiles whose pages' presence is kept.  It is written before the wait for the tile's stage and read by the
+// tile's softmax: the stage of the tile before was free after S of three tiles before, which was issued after
+// the P.V, and so after the softmax, of five tiles before; fp8's conversion may be a tile behind that.
 constexpr int kHave = 8;
 static_assert(kSharedRows == 2 * kBM, "a prefix piece's rows");
 static_assert(kMaxGroups <= kThreads, "a thread per group");
@@ -493,20 +493,29 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
                 if (!kF8) tma_prefetch_map(is_k ? &maps.k : &maps.v);
             }
             bool go = true;
-            // lane 0 waits for `empty` (unless the buffer is new)
-            auto wait_empty = [&](uint64_t* empty, int use) -> bool {
-                if (lane == 0) go = use == 0 ? !*abort_flag : wait_or_abort(empty, (use - 1) & 1, abort_flag, status);
+            // lane 0 waits for `empty` (unless the buffer is new) and arms `full`
+            auto arm = [&](uint64_t* full, uint64_t* empty, int use, uint32_t bytes) -> bool {
+                if (lane == 0) {
+                    go = use == 0 ? !*abort_flag : wait_or_abort(empty, (use - 1) & 1, abort_flag, status);
+                    if (go) mbar_arrive_expect_tx(full, bytes);
+                }
                 return go = __shfl_sync(0xffffffffu, go, 0);
             };
-            // Zeros in the places of a tile's pages that are not there, before the tile is armed: V's
-            // weights are 0 (and 0 * NaN would not be), and fp8 pages have scales.
-            auto zero_missing = [&](unsigned char* stage, int bytes, int pages, uint32_t have) {
+            // ... of a tile without all its pages, with zeros in their places: V's weights are 0 (and
+            // 0 * NaN would not be), and fp8 pages have scales.
+            auto arm_gaps = [&](uint64_t* full, uint64_t* empty, int use, uint32_t bytes, unsigned char* stage, int page_bytes,
+                                int pages, uint32_t have) -> bool {
+                if (lane == 0) go = use == 0 ? !*abort_flag : wait_or_abort(empty, (use - 1) & 1, abort_flag, status);
+                if (!(go = __shfl_sync(0xffffffffu, go, 0))) return false;
                 for (int i = 0; i < pages; ++i)
                     if (!(have >> i & 1u))
-                        for (int x = lane; x < bytes / 16; x += 32)
-                            reinterpret_cast<uint4*>(stage + i * bytes)[x] = make_uint4(0, 0, 0, 0);
+                        for (int x = lane; x < page_bytes / 16; x += 32)
+                            reinterpret_cast<uint4*>(stage + i * page_bytes)[x] = make_uint4(0, 0, 0, 0);
                 fence_async_smem();
                 __syncwarp();
+                if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+                __syncwarp();
+                return true;
             };
             // Lane i < 8 copies page i of a tile; its block's id comes from the table a
             // tile ahead (lanes without a page read their row's first entry).
@@ -535,18 +544,18 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
                     const int row = pool_row(p, t, blk_next);
                     const uint32_t have = __ballot_sync(0xffffffffu, row >= 0);
                     constexpr int kBytes = kF8 ? kF8Page : kPageBytes;
+                    const uint32_t bytes = (uint32_t)__popc(have) * (uint32_t)kBytes;
+                    const bool gaps = (kF8 || !is_k) && have != (1u << p.pages(t)) - 1u;
+                    if (is_k && lane == 0) B.have[g % kHave] = have;
                     static_assert(kRaw == kStages, "stages of pages as of tiles");
                     const int s = g % kStages;
                     uint64_t* full = kF8 ? &B.raw_full[s] : is_k ? &B.k_full[s] : &B.v_full[s];
-                    if (!wait_empty(kF8 ? &B.raw_empty[s] : is_k ? &B.k_empty[s] : &B.v_empty[s], g / kStages)) break;
-                    if ((kF8 || !is_k) && have != (1u << p.pages(t)) - 1u)
-                        zero_missing(smem + (kF8 ? GE::kOffRaw + s * GE::kRawBytes : kOffV + s * kTileBytes), kBytes, p.pages(t),
-                                     have);
-                    if (lane == 0) {
-                        if (is_k) B.have[g % kHave] = have;
-                        mbar_arrive_expect_tx(full, (uint32_t)__popc(have) * (uint32_t)kBytes);
-                    }
-                    __syncwarp();
+                    uint64_t* empty = kF8 ? &B.raw_empty[s] : is_k ? &B.k_empty[s] : &B.v_empty[s];
+                    unsigned char* stage = smem + (kF8 ? GE::kOffRaw + s * GE::kRawBytes : kOffV + s * kTileBytes);
+                    if (__builtin_expect(gaps, 0)
+                            ? !arm_gaps(full, empty, g / kStages, bytes, stage, kBytes, p.pages(t), have)
+                            : !arm(full, empty, g / kStages, bytes))
+                        break;
                     if (kF8 && row >= 0)
                         bulk_load(smem + GE::kOffRaw + s * GE::kRawBytes + lane * kF8Page,
                                   (const char*)a.d.k_pool + (int64_t)(row / kPage) * kF8Page, kF8Page, full, pol);
@@ -564,9 +573,7 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
                         const int tiles = p.two() ? 2 : 1;
                         for (int x = 0; x < tiles; ++x) {
                             const int qs = qg % kStages;
-                            if (!wait_empty(&B.q_empty[qs], qg / kStages)) break;
-                            if (lane == 0) mbar_arrive_expect_tx(&B.q_full[qs], (uint32_t)kTileBytes);
-                            __syncwarp();
+                            if (!arm(&B.q_full[qs], &B.q_empty[qs], qg / kStages, (uint32_t)kTileBytes)) break;
                             if (lane < GE::kPanels)
                                 tma_load_3d(smem + kOffQ + qs * kTileBytes + lane * kPanel, &maps.q, 64 * lane, p.h << lg,
                                             p.b0 + x * (kBM >> lg), &B.q_full[qs], pol);
@@ -750,6 +757,7 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
                 steps ^= 1u << x;
                 const int rows = p.rows - (two ? y * kBM : 0);  // of the tile (P of others may be anything)
                 if (quarter * 32 < rows) {
+                    const uint32_t have = B.have[u % kHave] >> (4 * hf) & 0xfu;  // pages of this half's columns
                     uint32_t sv[64];
                     tc_fence_after();
                     tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
@@ -769,7 +777,6 @@ __device__ __forceinline__ void prefix_cta(const SharedArgs& a, const Maps& maps
                             sv[4 * e + 3] = __float_as_uint(__uint_as_float(sv[4 * e + 3]) * k.w);
                         }
                     }
-                    const uint32_t have = B.have[u % kHave] >> (4 * hf) & 0xfu;  // pages of this half's columns
                     if (have != 0xfu) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
