@@ -926,12 +926,13 @@ SharedLayout shared_layout(const kvattn_config* cfg, int32_t batch, int32_t max_
     // (the streams' pages are counted in 32 bits)
     const int64_t pages = pieces * ((int64_t)max_shared_len / 16 + 1) + (int64_t)batch * hkv * ((int64_t)max_seq_len / 16 + 1);
     if (pages > (1 << 30)) return l;
-    const size_t rows = (size_t)pieces * kSharedRows;
+    const size_t rows = (size_t)ctas * kSharedRows + (size_t)batch * cfg->num_q_heads;
+    if (rows > INT32_MAX) return l;
     const size_t own_rows = (size_t)own_pieces(hkv, batch, ctas) * (cfg->num_q_heads / hkv);
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     l.o_off = up((size_t)batch * sizeof(SharedOf));
-    l.ml_off = l.o_off + rows * cfg->head_dim * 4;
-    l.own_o_off = l.ml_off + rows * 2 * 4;
+    l.ml_off = l.o_off + up(rows * cfg->head_dim * 4);
+    l.own_o_off = l.ml_off + up(rows * 2 * 4);
     l.own_ml_off = l.own_o_off + up(own_rows * cfg->head_dim * 4);
     l.bytes = l.own_ml_off + up(own_rows * 2 * 4);
     return l;
@@ -982,7 +983,10 @@ size_t kvattn_decode_shared_workspace_size(const kvattn_config* cfg, int32_t bat
 {
     if (batch < 0 || max_seq_len < 0 || !groups_ok(batch, num_groups, max_shared_len)) return 0;
     const size_t alone = kvattn_decode_window_workspace_size(cfg, batch, max_seq_len, INT32_MAX, 0, 0);
-    return alone == 0 ? 0 : std::max(alone, shared_layout(cfg, batch, max_seq_len, num_groups, max_shared_len).bytes);
+    if (alone == 0) return 0;
+    auto once = [&](bool fp8) { return prefixes_once(cfg, fp8, batch, max_seq_len, num_groups, max_shared_len); };
+    if (!once(false) && !(cfg->head_dim == 128 && once(true))) return alone;
+    return std::max(alone, shared_layout(cfg, batch, max_seq_len, num_groups, max_shared_len).bytes);
 }
 
 kvattn_status kvattn_decode_shared(const kvattn_config* cfg, const kvattn_cache* cache, const void* q,

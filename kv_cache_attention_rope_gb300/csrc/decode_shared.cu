@@ -112,17 +112,18 @@ struct Bars {
 static_assert(sizeof(Bars) <= 384, "the barriers fit before the exchange area");
 
 // The call's groups and sequences, and the streams of pages: group g's shared ones are
-// first[g] .. first[g+1] - 1 (its segments segment[g] ..: KV heads outermost, then
-// row blocks), sequence b's own Hkv own[b] .. Hkv own[b+1] - 1.
+// first[g] .. first[g+1] - 1 (segments: KV heads outermost, then row blocks; their rows
+// rows[g] ..), sequence b's own Hkv own[b] .. Hkv own[b+1] - 1.
 struct Plan {
     int cu[kMaxGroups + 1];
     int tokens[kMaxGroups];   // shared, whole pages; 0: shares nothing
     int leader[kMaxGroups];   // a sequence of the group that has them
     int members[kMaxGroups];  // how many have them
-    int first[kMaxGroups + 1], segment[kMaxGroups + 1];
+    int first[kMaxGroups + 1], rows[kMaxGroups + 1];
     int own[kMaxSharedBatch + 1];
+    int segments;  // of all groups
     int two_rows;  // shared pages of segments of two row tiles
-    int sums[4][kThreads / 32];
+    int sums[3][kThreads / 32];
 };
 
 template <int kD, bool kF8>
@@ -196,6 +197,7 @@ __device__ __forceinline__ void make_plan(const SharedArgs& a, Plan& P, int* len
         P.leader[tid] = INT_MAX;
         P.members[tid] = 0;
     }
+    if (tid == 0) P.segments = P.two_rows = 0;
     // (loops are not unrolled: the instructions of this are fetched once per call, which is
     // what it waits for)
 #pragma unroll 1
@@ -225,14 +227,14 @@ __device__ __forceinline__ void make_plan(const SharedArgs& a, Plan& P, int* len
     }
     __syncthreads();
     auto shared = [&](int g) { return ok && P.members[g] >= 2 ? P.tokens[g] / kPage : 0; };  // pages
-    int v[4] = {0, 0, 0, 0};  // pages of a group, its segments; own pages of this thread's sequences; two_rows
+    int v[3] = {0, 0, 0};  // pages of a group, rows of its segments; own pages of this thread's sequences
     int tokens = 0;
-    if (tid < n) {
-        tokens = shared(tid) * kPage;
-        v[1] = tokens > 0 ? blocks_of(P.cu[tid + 1] - P.cu[tid], lg) * a.d.hkv : 0;
-        v[0] = v[1] * (tokens / kPage);
-        const int rows = (P.cu[tid + 1] - P.cu[tid]) << lg;
-        v[3] = (rows + kSharedRows - kBM - 1) / kSharedRows * a.d.hkv * (tokens / kPage);
+    if (tid < n && (tokens = shared(tid) * kPage) > 0) {
+        const int seqs = P.cu[tid + 1] - P.cu[tid], rows = seqs << lg, segments = blocks_of(seqs, lg) * a.d.hkv;
+        v[0] = segments * (tokens / kPage);
+        v[1] = rows * a.d.hkv;
+        atomicAdd(&P.segments, segments);
+        atomicAdd(&P.two_rows, (rows + kSharedRows - kBM - 1) / kSharedRows * a.d.hkv * (tokens / kPage));
     }
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
@@ -243,25 +245,24 @@ __device__ __forceinline__ void make_plan(const SharedArgs& a, Plan& P, int* len
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 3; ++i) {
             const int x = __shfl_up_sync(0xffffffffu, v[i], o);
             if (lane >= o) v[i] += x;
         }
     if (lane == 31)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) P.sums[i][warp] = v[i];
+        for (int i = 0; i < 3; ++i) P.sums[i][warp] = v[i];
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += __reduce_add_sync(0xffffffffu, lane < warp ? P.sums[i][lane] : 0);
+    for (int i = 0; i < 3; ++i) v[i] += __reduce_add_sync(0xffffffffu, lane < warp ? P.sums[i][lane] : 0);
     if (tid < n) {
         P.first[tid + 1] = v[0];
-        P.segment[tid + 1] = v[1];
+        P.rows[tid + 1] = v[1];
         P.tokens[tid] = tokens;
     }
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) P.own[b + 1] += v[2] - mine;
-    if (tid == 0) P.first[0] = P.segment[0] = P.own[0] = 0;
-    if (tid == kThreads - 1) P.two_rows = v[3];
+    if (tid == 0) P.first[0] = P.rows[0] = P.own[0] = 0;
     __syncthreads();
 }
 
@@ -343,7 +344,7 @@ struct Walk {
         p.row = P.leader[g];
         p.b0 = P.cu[g] + rb * (kSharedRows >> lg);
         p.rows = min(kSharedRows, (seqs << lg) - rb * kSharedRows);
-        p.out = ((int)blockIdx.x + P.segment[g] + seg) * kSharedRows;
+        p.out = (int)blockIdx.x * kSharedRows + P.rows[g] + p.h * (seqs << lg) + rb * kSharedRows;
         r += p.p1 - p.p0;
         return true;
     }
@@ -1212,7 +1213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int* len = reinterpret_cast<int*>(smem);  // (where Q will be)
     make_plan(a, P, len, lg);
     const int shared = P.first[a.num_groups], own = a.d.hkv * P.own[a.d.batch];
-    const Ranges ranges = ranges_of<kF8>(shared, P.two_rows, P.segment[a.num_groups], own, a.d.hkv * a.d.batch, gridDim.x,
+    const Ranges ranges = ranges_of<kF8>(shared, P.two_rows, P.segments, own, a.d.hkv * a.d.batch, gridDim.x,
                                          kSetUpBytes / GE::kCost, kSegmentBytes / GE::kCost);
     // where the merge finds each sequence's partial results
     for (int b = (int)blockIdx.x + (int)gridDim.x * threadIdx.x; b < a.d.batch; b += (int)gridDim.x * kThreads) {
@@ -1224,13 +1225,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (shared > 0 && b < P.cu[a.num_groups]) {
             const int g = group_of(P, a.num_groups, b), pages = P.tokens[g] / kPage;
             if (pages > 0 && len[b] >= P.tokens[g]) {
-                const int r = (b - P.cu[g]) << lg, rb = r / kSharedRows;
+                const int seqs = P.cu[g + 1] - P.cu[g], r = (b - P.cu[g]) << lg;
                 o.pages = pages;
-                o.head_segments = blocks_of(P.cu[g + 1] - P.cu[g], lg);
-                o.first = P.first[g] + rb * pages;
-                o.head_pages = o.head_segments * pages;
-                o.segment = P.segment[g] + rb;
-                o.row = r - rb * kSharedRows;
+                o.first = P.first[g] + r / kSharedRows * pages;
+                o.head_pages = blocks_of(seqs, lg) * pages;
+                o.row = P.rows[g] + r;
+                o.head_rows = seqs << lg;
             }
         }
         a.of[b] = o;
@@ -1274,7 +1274,7 @@ __global__ void __launch_bounds__(128) decode_shared_merge_kernel(const __grid_c
     if (s.pages > 0) {
         const int first = s.first + h * s.head_pages, c = first / s.per;
         np = (first + s.pages - 1) / s.per - c + 1;
-        shared0 = (int64_t)(c + s.segment + h * s.head_segments) * kSharedRows + s.row + g;
+        shared0 = (int64_t)c * kSharedRows + s.row + h * s.head_rows + g;
     }
     if (s.own_pages > 0) {
         const int first = s.own_first + h * s.own_pages, c = first / s.own_per;

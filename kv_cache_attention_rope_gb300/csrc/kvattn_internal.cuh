@@ -232,15 +232,17 @@ bool launch_decode_direct(const DecodeArgs& a, int32_t max_tiles, cudaStream_t s
 // pages, one per warp.  The pages of a (row block of a group, KV head) or (sequence, KV
 // head) are contiguous, and a piece is what of them lies in one range.  The shared pages of
 // (the sequence's row block, KV head h) are first + h head_pages .. + pages - 1 (pages 0:
-// it shares nothing), and the piece of range c is rows (c + segment + h head_segments)
-// kSharedRows + row .. of SharedArgs::o and ml.  The own pages are own_first + h own_pages
-// .. + own_pages - 1, and the piece of range c rows (c + b Hkv + h) G .. of own_o and own_ml.
+// it shares nothing), and its G rows of the piece of range c are c kSharedRows + row + h
+// head_rows .. of SharedArgs::o and ml: pieces follow each other with the rows of their
+// segments, and one range further on at kSharedRows, the most that a segment has.  The own
+// pages are own_first + h own_pages .. + own_pages - 1, and the piece of range c rows
+// (c + b Hkv + h) G .. of own_o and own_ml.
 struct SharedOf {
-    int32_t first, pages, head_pages, segment;
-    int32_t head_segments, row, own_first, own_pages;
-    int32_t per, own_per, pad[2];
+    int32_t first, pages, head_pages, row;
+    int32_t head_rows, own_first, own_pages, per;
+    int32_t own_per, pad[3];
 };
-constexpr int kSharedRows = 256;    // of a prefix piece
+constexpr int kSharedRows = 256;    // of a prefix piece, at most
 constexpr int kMostOwnWarps = 16;   // ranges of own pages per CTA, at most
 struct SharedArgs {
     DecodeArgs d;                   // (nslots, part_o, part_ml, splits unused)
@@ -255,7 +257,7 @@ kvattn_status launch_decode_shared(const SharedArgs& a, cudaStream_t s);
 // Most groups and sequences of a call that reads prefixes once (others read each
 // sequence by itself): the kernel keeps them in shared memory.
 constexpr int32_t kMaxGroups = 192, kMaxSharedBatch = 2048;
-// Pieces that a call may have: one per range, and one more per segment.  Groups of
+// Prefix pieces that a call may have: one per range, and one more per segment.  Groups of
 // fewer than two sequences share nothing.
 inline int64_t shared_pieces(int32_t hq, int32_t hkv, int32_t batch, int32_t num_groups, int32_t ctas)
 {
