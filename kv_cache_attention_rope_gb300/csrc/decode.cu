@@ -7,7 +7,7 @@ namespace kvattn {
 DecodePlan decode_plan(int32_t batch, int32_t hkv, int32_t group, int32_t max_seq_len, int32_t splits)
 {
     DecodePlan p;
-    const int max_tiles = std::max(1, (max_seq_len + kTile - 1) / kTile);
+    const int max_tiles = std::max(1, (int)(((int64_t)max_seq_len + kTile - 1) / kTile));  // (a bound may be INT32_MAX)
     if (splits > 0) {
         p.slots = splits;
     } else {

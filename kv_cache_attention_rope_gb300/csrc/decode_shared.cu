@@ -163,6 +163,9 @@ __device__ __forceinline__ void copy_page(void* dst, const CUtensorMap* m, int r
     else tma_load_2d(dst, m, 0, row, full, policy);
 }
 
+// Pages of `len` tokens, which may be up to INT_MAX.
+__device__ __forceinline__ int pages_of(int len) { return (int)(((unsigned)len + (kPage - 1)) / kPage); }
+
 __device__ __forceinline__ int blocks_of(int seqs, int lg) { return ((seqs << lg) + kSharedRows - 1) / kSharedRows; }
 
 // The last group g of n with cu[g] <= b: the one b is in.
@@ -239,7 +242,7 @@ __device__ __forceinline__ void make_plan(const SharedArgs& a, Plan& P, int* len
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
         const int g = P.own[b + 1];
-        P.own[b + 1] = v[2] += (len[b] + kPage - 1) / kPage - (g >= 0 ? shared(g) : 0);
+        P.own[b + 1] = v[2] += pages_of(len[b]) - (g >= 0 ? shared(g) : 0);
     }
     const int mine = v[2];
 #pragma unroll
@@ -965,7 +968,7 @@ struct OwnPage {
         }
         const int pages = P.own[b + 1] - P.own[b], in = r - hkv * P.own[b], h = in / pages, len = lens[b];
         const int left = pages - (in - h * pages);  // pages up to the segment's end
-        const int tok = ((len + kPage - 1) / kPage - left) * kPage;
+        const int tok = (pages_of(len) - left) * kPage;
         const int32_t blk = a.d.block_table[(int64_t)b * a.d.max_blocks + tok / a.d.block_size];
         seg = b * hkv + h;
         info = left == 1 || r + 1 == end ? 32 : 0;

@@ -33,3 +33,14 @@ def test_states_of_real_rows(kv, heads, batch, groups, most):
     rows = sms * 256 + batch * hq + (sms * 16 + batch * hkv) * (hq // hkv)
     assert got <= max(_alone(kv, cfg, batch, most + 256), rows * (d + 2) * 4 + batch * 48 + 2048)
     assert got >= batch * hq * (d + 2) * 4
+
+
+@pytest.mark.parametrize("heads", [(32, 8, 128), (12, 12, 64), (8, 1, 64)])
+@pytest.mark.parametrize("bound", [2 ** 31 - 1, 2 ** 31 - 8, 2 ** 31 - 15])
+def test_largest_bounds(kv, heads, bound):
+    """A bound whose last page would end past 2^31 is one like any other."""
+    cfg = kv.make_config(*heads, kv.BF16)
+    near = 2 ** 31 - 16
+    assert kv.decode_workspace_size(cfg, 2, bound) == kv.decode_workspace_size(cfg, 2, near) > 0
+    assert _alone(kv, cfg, 2, bound) == _alone(kv, cfg, 2, near) > 0
+    assert kv.decode_shared_workspace_size(cfg, 2, bound, 1, 1 << 20) == kv.decode_shared_workspace_size(cfg, 2, near, 1, 1 << 20)
