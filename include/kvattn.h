@@ -381,13 +381,17 @@ kvattn_status kvattn_copy_blocks_fp8(const kvattn_config* cfg, const kvattn_cach
  *   keep        device, [total_keep] int32: per sequence ascending positions from
  *               starts[s] on
  * Tokens before starts[s] and behind the last kept one's place stay as they were.
+ * Lists of like lengths go best, since thread blocks are laid out for the mean one: half of
+ * one list of 16384 tokens (8 heads of 128, bf16) takes 30 us alone and 209 beside 127 empty
+ * ones, so leave sequences out that nothing moves in.
  * The blocks that places lie in must belong to one sequence of the call only
  * (copy shared ones first, kvattn_table_prepare_append); the blocks that hold neither a
  * place nor a kept position are not looked at.
  * Errors: INVALID_ARG (null pointer, negative count, bad cache), UNSUPPORTED,
  * CUDA; device: BAD_INDEX (a place or kept position outside the table or pool
  * stays as it was; a list that does not ascend leaves the sequence's tokens
- * from starts[s] on unspecified; a list outside `keep` counts as empty).
+ * from starts[s] on unspecified; a list outside `keep`, with a negative starts[s], or
+ * of more tokens than the table has places for counts as empty).
  * num_seqs == 0 or total_keep == 0 launches nothing.
  *
  * kvattn_compact_tokens_fp8: the same in a kvattn_cache_fp8 (head_dim 128).
@@ -571,7 +575,8 @@ kvattn_status kvattn_decode_window_fp8(const kvattn_config* cfg, const kvattn_ca
 /*
  * kvattn_decode_shared -- kvattn_decode for a batch in which groups of sequences
  * begin with the same tokens (samples of one prompt, chats under one system
- * prompt): what a group has in common is read once for all of its queries.
+ * prompt): what a group has in common is read once for every 256 of its queries
+ * (256 / G sequences).
  *
  * [Nano-vLLM], section 05 (sequences with a common prefix share its blocks), and
  * [Engine page], section 3.4: the softmax over the common keys and the one over a
@@ -596,7 +601,11 @@ kvattn_status kvattn_decode_window_fp8(const kvattn_config* cfg, const kvattn_ca
  * saves enough by the call's bounds (40 MB of K and V; fp8: 64 MB and more with long
  * own parts and many groups); then a group's first 128 tokens or more, down to a
  * multiple of 16, that at least two sequences have.  Other calls read each sequence
- * by itself, as kvattn_decode_window without a window does.
+ * by itself, as kvattn_decode_window without a window does.  The host sees the bounds
+ * only, so they should be close: an fp8 call counts max_seq_len - max_shared_len as own
+ * tokens of every sequence (64 sequences of 64 / 8 heads behind 16384 tokens read them once
+ * up to a max_seq_len of about 26,700, and 64 times above it, 78 and 392 us); where a step
+ * is captured for what it may grow to, capture it again as that grows.
  * What a sequence sees counts as in kvattn_decode_window: a NaN score makes
  * its query head's output NaN.  Weights over a prefix are rounded to bf16 before
  * their product with V.

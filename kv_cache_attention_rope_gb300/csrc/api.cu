@@ -900,6 +900,11 @@ bool groups_ok(int32_t batch, int32_t num_groups, int32_t max_shared_len)
 // 32/8): 32.1 / 93.8.  fp8 (64/8 heads), saved and own MB 65 and 69: 26.6 / 24.5; 68 and 69:
 // 36.0 / 24.2; 272 and 69: 36.1 / 52.8; 1089 and 276: 75 / 226; 16 groups of 4, 207 and 69: 71 / 51;
 // 829 and 276: 170 / 225.
+// Own keys do not count for bf16: the stream of own pages is no slower than the other form's, saved
+// and own MB (bound) 41 and 1342 (80 x 128, 32/8 heads): 121 / 131; 65 and 1074 (32 x 512): 87 / 94; 50 and
+// 805 (128 x 128, 12/12 heads of 64): 72 / 79; 66 and 1074 (64 x 256) with 8/8, 16/8 and 64/8 heads:
+// 105 / 107, 106 / 110 and 109 / 123; and many sequences go better this way even where a bound of
+// 128 lets nothing be shared (256 of 127 and up to 512 own tokens, 32/8 heads: 61 / 89).
 bool prefixes_once(const kvattn_config* cfg, bool fp8, int32_t batch, int32_t max_seq_len, int32_t num_groups,
                    int32_t max_shared_len)
 {

@@ -319,6 +319,9 @@ kvattn_status run(void (*kern)(KArgs...), int64_t units, int threads, int cluste
 
 }  // namespace
 
+// Laid out for the mean list, which is all that the host knows: a long one among many short ones
+// gets as few blocks as these (half of 16384 tokens, 8 heads of 128, bf16: 30 us alone, 209
+// beside 127 empty lists).
 kvattn_status launch_compact(const CompactArgs& a, cudaStream_t s)
 {
     const int64_t mean = std::max<int64_t>(1, a.total_keep / a.num_seqs);

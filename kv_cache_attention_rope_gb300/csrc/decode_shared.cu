@@ -1,5 +1,5 @@
 // Decode attention for a batch in which groups of sequences share their first
-// tokens: a prefix is read once for all the queries of its group.
+// tokens: a prefix is read once for every 256 queries of its group.
 //
 // What it computes: kvattn_decode's out[b][j], an online softmax over every key of
 // sequence b ("From-scratch AI inference engine" page, section 3.3: a query sees
@@ -14,10 +14,11 @@
 // is not in the pool is seen by nobody: its scores are -infinity, its V is zero.
 //
 // What bounds it.  A KV head's queries over a prefix are (sequences of the group) x
-// G rows of one matrix product, so the prefix's K and V are read once, 4 D e bytes a
-// key and KV head, for 4 D FLOPs a key and row: up to about 128 rows HBM has the
-// longer part, from 256 rows on the tensor cores and the softmax beside them.  Own
-// keys have G rows and are HBM's.
+// G rows of one matrix product, so the prefix's K and V are read once for up to 256 of
+// them, 4 D e bytes a key and KV head, for 4 D FLOPs a key and row: up to about 128 rows HBM
+// has the longer part, from 256 rows on the tensor cores and the softmax beside them.  (More
+// rows are more segments, each with its own pass over the pages, from L2 at best: one document
+// and 512 rows are loaded, and in fp8 converted, twice.)  Own keys have G rows and are HBM's.
 //
 // How.  One launch, a CTA per SM, some of them on prefixes and the others on own
 // keys, as many of each as make both end together; decode_shared_merge_kernel then
@@ -280,13 +281,16 @@ struct Ranges {
 // besides its pages (tensor memory, the pipeline's filling) and `segment` for each of its
 // segments (256 rows of output); so with t for all,
 // p / (t - set_up) + o / t = ctas.
-// Measured, us (64 sequences but for two): bf16 (kPage, kMore), 2048 shared and up to 512 own
+// Measured with inputs that change from call to call, us of this kernel alone (the merge has 4.5 to 6.5 besides;
+// 64 sequences but for two): bf16 (kPage, kMore), 2048 shared and up to 512 own
 // tokens | 12 prompts of up to 8191, 192 sequences, 1024 own | 32 x (65536, 256): 0.6, 1: 23.4 | 104 |
 // 55; 0.85, 1: 26.5 | 127 | 55; 0.4, 1.2: 26.4 | 112 | 55; 0.95, 0.8: 26.7 | 136 | 55; before own pages came
 // by way of L2, 1, 0: 27.2 | 129 | 72.  fp8 (kPage, kSegment, kTwo), 16384
 // and 1024 | 8192 and 2048 | 16 x (8192, 2048): 1, 4, 1.4: 72 | 77 | 29; 1, 4, 1: 75 | 83 | 29; 0.8, 4, 1.2: 71 | 73 | 26;
 // 0.8, 4, 2: 70 | 64 | -; 1, 4, 2.4: 69 | 67 | -; 0.6, 3, 1.6: 83 | 68 | -; 1.2, 4, 1.6: 74 | 78 | 28; a page of two row tiles counted as of one: 1, 2: 89 and 0.4, 2: 71 | 69 | -,
-// but 16 x 8192 shared by 4s, with 32 own, 56 instead of 40.
+// but 16 x 8192 shared by 4s, with 32 own, 56 instead of 40.  As the code is now: 22.6 | 101 | 54.5, and fp8 16384
+// and 1024 69.5.  The bf16 constants were chosen at 32 / 8 heads of 128 and serve D = 64 and groups of 1, 2 and 8
+// untuned (figures of those: prefixes_once in api.cu).
 template <bool kF8>
 struct OwnCost {
     static constexpr float kPage = kF8 ? 0.8f : 0.6f, kMore = kF8 ? 0.f : 1.0f, kSegment = kF8 ? 4.f : 1.f,
