@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(warps_per_sm(kKind, kD, kG) * 32, 1)
                 t.scores(s, q);
                 const float k0 = t.ks[0] * sl2, k1 = t.ks[1] * sl2;
                 const bool in0 = now >> rk0 & 1u, in1 = now >> rk1 & 1u;
-                const float x[4] = {in0 ? s[0] * k0 : -INFINITY, in0 ? s[1] * k0 : -INFINITY,
+                float x[4] = {in0 ? s[0] * k0 : -INFINITY, in0 ? s[1] * k0 : -INFINITY,
                                     in1 ? s[2] * k1 : -INFINITY, in1 ? s[3] * k1 : -INFINITY};
                 const float sv0 = in0 ? t.vs[0] : 0.f, sv1 = in1 ? t.vs[1] : 0.f;
                 uint32_t vmask = 0xffffffffu;  // the bytes of this lane's words whose tokens are seen

@@ -134,10 +134,6 @@ struct SharedLayout {
 template <bool kBF16, int kD, int kGT, bool kFP8>
 __host__ __device__ constexpr int stage_bytes() { return kFP8 ? kF8Page : Traits<kBF16, kD, kGT>::kStageBytes; }
 
-// Windowed form: V's scales of an fp8 page whose block is not in the pool (scales are positive).  A flag
-// per stage, which the consumers load besides, made the stream of 64 sequences of up to 32768 tokens 1.5 % slower.
-constexpr float kNoPage = -1.f;
-
 // Query heads a consumer warp merges per pass (its merge slot's size): a
 // GQA group of 8 on the tensor cores is merged in two passes of 4, which keeps
 // the slot, and with it the ring depth, as for groups of 4.  The fp8 path
@@ -169,7 +165,7 @@ __host__ __device__ inline SharedLayout shared_layout(int stages, int batch)
     off += 2 * stages * 8;
     L.flag_off = off;
     off += 16;
-    L.have_off = off;  // windowed form: whether the tile's block is there, per stage (fp8: kNoPage)
+    L.have_off = off;  // windowed form: whether the tile's block is there, per stage (fp8: in V's scales, kNoPage)
     if (kWin && !kFP8) off += stages * 4;
     L.bytes = off;
     return L;
@@ -435,8 +431,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_sp
                             unsigned char* dst = ring + (size_t)stage * kStageB;
                             if constexpr (kFP8) {
                                 // the fp8 page of these 16 tokens: K, V^T and scales, one copy
-                                if (kWin && bj < 0) {
-                                    for (int i = 0; i < kTile; ++i) reinterpret_cast<float*>(dst + kF8VsOff)[i] = kNoPage;
+                                if (kWin && bj < 0) {  // (V's codes: 0 * NaN would not be 0)
+                                    for (int i = 0; i < kTile; ++i) reinterpret_cast<uint32_t*>(dst + kF8VsOff)[i] = kNoPage;
+                                    for (int i = kF8VOff; i < kF8KsOff; i += 16)
+                                        *reinterpret_cast<uint4*>(dst + i) = make_uint4(0, 0, 0, 0);
                                     fence_async_smem();  // before the next copy into this stage
                                     mbar_arrive(&full[stage]);
                                 } else {
@@ -592,8 +590,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_sp
                 const unsigned char* pg = ring + (size_t)stage * kStageB;
                 const int tok0 = first_token(pc, pc.t0 + li);
                 const int nvalid = min(kTile, pc.len - tok0);
-                uint32_t seen = kWin ? seen_bits(tok0, pc, a) : 0u;
-                bool whole = kWin ? seen == (1u << kTile) - 1u : nvalid == kTile;
+                const uint32_t seen = kWin ? seen_bits(tok0, pc, a) : 0u;
+                const bool whole = kWin ? seen == (1u << kTile) - 1u : nvalid == kTile;
                 auto sees = [&](int i) { return kWin ? (seen >> i & 1u) != 0 : i < nvalid; };
                 float s[4] = {0.f, 0.f, 0.f, 0.f};  // S^T: (rk0, 2q4), (rk0, 2q4+1), (rk1, 2q4), (rk1, 2q4+1)
 #pragma unroll
@@ -610,10 +608,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_sp
                 const float* vsc = reinterpret_cast<const float*>(pg + kF8VsOff);
                 const float k0 = ksc[rk0] * sl2, k1 = ksc[rk1] * sl2;
                 float sv0 = vsc[rk0], sv1 = vsc[rk1];
-                if (kWin && sv0 == kNoPage) {
-                    seen = 0u;
-                    whole = false;
-                }
                 float x[4] = {s[0] * k0, s[1] * k0, s[2] * k1, s[3] * k1};
                 uint32_t vmask = 0xffffffffu;  // bytes of this lane's V words that belong to valid tokens
                 if (!whole) {
@@ -631,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kMma, kFP8>()) decode_sp
                 }
                 float w[4];  // weight * V scale over a reference
                 if constexpr (kWin) {
-                    win.step(x, sv0, sv1, lane, [&](int i) {
+                    win.step<true>(x, sv0, sv1, lane, [&](int i) {
                         return *reinterpret_cast<const uint32_t*>(pg + kF8VOff + g4 * 16 + 4 * q4 + i * 128) & vmask;
                     }, o, w);
                 } else {

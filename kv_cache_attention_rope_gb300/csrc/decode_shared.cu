@@ -1171,7 +1171,7 @@ __device__ __forceinline__ void own_warp_fp8(const SharedArgs& a, const Plan& P,
         const uint32_t seen = seen_of(info);
         const float sl2 = a.d.scale_log2 * 16.f, k0 = t.ks[0] * sl2, k1 = t.ks[1] * sl2;
         const bool in0 = seen >> rk0 & 1u, in1 = seen >> rk1 & 1u;
-        const float x[4] = {in0 ? s[0] * k0 : -INFINITY, in0 ? s[1] * k0 : -INFINITY, in1 ? s[2] * k1 : -INFINITY,
+        float x[4] = {in0 ? s[0] * k0 : -INFINITY, in0 ? s[1] * k0 : -INFINITY, in1 ? s[2] * k1 : -INFINITY,
                             in1 ? s[3] * k1 : -INFINITY};
         const float sv0 = in0 ? t.vs[0] : 0.f, sv1 = in1 ? t.vs[1] : 0.f;
         uint32_t vmask = 0xffffffffu;  // the bytes of this lane's words whose tokens are seen

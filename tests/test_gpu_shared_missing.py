@@ -6,7 +6,7 @@ import torch
 
 from _gpu_support import f64
 from _shared_support import SharedCache
-from _window_support import attend, check_attention
+from _window_support import WindowCache, attend, check_attention
 from test_gpu_shared import LOOSE, _q
 
 pytestmark = pytest.mark.gpu
@@ -107,3 +107,26 @@ def test_missing_under_long_bounds(kvattn_lib, dtype, hq, hkv, d):
         assert kv.get_device_status() == kv.STATUS_CODE["KVATTN_ERR_BAD_INDEX"]
         _check(c, q.double().numpy(), got, dtype, lacks, range(4), f"window, block {block}")
         assert np.all(got[4] == 0)
+
+
+@pytest.mark.parametrize("hq,hkv", [(64, 8), (32, 8)])
+@pytest.mark.parametrize("scale", [-1.0, 0.0, -3.0e38])
+def test_scales_of_unseen_slots(kvattn_lib, hq, hkv, scale):
+    """Whatever the scales of slots are that the window does not see, in pages of which it sees others: the balanced stream
+    over fp8 pages, which marks missing pages by scales of its own."""
+    kv = kvattn_lib
+    lens, window = [701, 760, 33, 640], 300
+    wanted = [np.arange(n) >= n - window for n in lens]
+    c = WindowCache(kv, "fp8", hkv, 128, lens, wanted, seed=hq)
+    scales = c.cache.pool.view(torch.float32)[..., 1024:]  # K's and V's
+    scales[torch.isnan(scales)] = scale
+    cfg = kv.make_config(hq, hkv, 128, kv.BF16)
+    q = _q(np.random.default_rng(7), (4, hq, 128), "fp8")
+    d_lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = f64(kv.decode_window_fp8(cfg, c.cache, q.cuda(), c.d_table, d_lens, 16 * 4200, window))
+    split = f64(kv.decode_window_fp8(cfg, c.cache, q.cuda(), c.d_table, d_lens, 16 * 4200, window, num_splits=3))
+    assert kv.get_device_status() == 0
+    for r in range(4):
+        want, mag = attend(q[r:r + 1].double().numpy(), c.k[r], c.v[r], wanted[r][None])
+        for x in (got, split):
+            check_attention(x[r:r + 1], want, mag, "bf16", f"sequence {r}")
