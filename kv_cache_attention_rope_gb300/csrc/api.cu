@@ -891,27 +891,37 @@ bool groups_ok(int32_t batch, int32_t num_groups, int32_t max_shared_len)
 }
 
 // Whether prefixes are read once: if they save enough, by the call's bounds.  That form
-// starts with a plan and ends with a merge, 12 us together at least, and reads own fp8
-// pages slower than decode_direct.cu does; a prefix of a few rows costs it as much as one of 128.
+// starts with a plan and ends with a merge, 12 us together at least; a prefix of a few rows costs
+// it as much as one of 128; and beside the prefixes of several groups it reads own fp8 pages slower
+// than decode_direct.cu does.
 // Measured over batches of 2 to 64, prefixes of 128 to 8192 tokens and own parts of up
 // to 32 to 2048 (us, once / each sequence by itself): bf16, saved MB 25 (2 x 8192, 12/12
 // heads of 64): 16.8 / 12.6; 33 (64 x 128, 32/8 heads of 128): 13.7 / 8.0; 94 (16 x 2048,
 // 12/12 heads): 19.9 / 30.4 with 2048 own tokens and 12.0 / 18.8 with 512; 528 (64 x 2048,
-// 32/8): 32.1 / 93.8.  fp8 (64/8 heads), saved and own MB 65 and 69: 26.6 / 24.5; 68 and 69:
-// 36.0 / 24.2; 272 and 69: 36.1 / 52.8; 1089 and 276: 75 / 226; 16 groups of 4, 207 and 69: 71 / 51;
-// 829 and 276: 170 / 225.
+// 32/8): 32.1 / 93.8.
 // Own keys do not count for bf16: the stream of own pages is no slower than the other form's, saved
 // and own MB (bound) 41 and 1342 (80 x 128, 32/8 heads): 121 / 131; 65 and 1074 (32 x 512): 87 / 94; 50 and
 // 805 (128 x 128, 12/12 heads of 64): 72 / 79; 66 and 1074 (64 x 256) with 8/8, 16/8 and 64/8 heads:
 // 105 / 107, 106 / 110 and 109 / 123; and many sequences go better this way even where a bound of
 // 128 lets nothing be shared (256 of 127 and up to 512 own tokens, 32/8 heads: 61 / 89).
+// fp8, 138 shapes of 64/8, 32/8 and 8/2 heads, 4 to 128 sequences in 1 to 16 groups, 512 to 8192 shared
+// and up to 64 to 4096 own tokens; saved and own MB.  One group: 52 and 9 (64/8) 23.0 / 17.5; 65 and 138 33.3 /
+// 32.3; 68 and 554 85 / 83; 137 and 17 34.3 / 26.9 (32/8: 20.5 / 25.5); 272 and 138 (8/2) 35.4 / 76.2; 272
+// and 554 84 / 110; 549 and 1107 132 / 176: own keys make no difference.  8 groups (64/8): 61 and 554
+// 113 / 79; 242 and 138 64 / 60; 242 and 554 124 / 106; 969 and 554 186 / 255; 16 groups, 121 and 17
+// 42 / 28; 484 and 277 101 / 102; 484 and 1107 218 / 178; 1938 and 1107 313 / 475.  The rule's choice
+// takes 0.4 % more than the better one on the mean, 28 % at most.  Since max_seq_len may be far above the lengths (a
+// step captured for what it may grow to), own keys count up to twice the saved bytes only, so that from
+// 200 MB and 5 for each group and KV head on prefixes are shared at any bound: by the bound alone
+// the choice takes 3 % more than the better one, 63 % at most.
 bool prefixes_once(const kvattn_config* cfg, bool fp8, int32_t batch, int32_t max_seq_len, int32_t num_groups,
                    int32_t max_shared_len)
 {
     const double token = (double)cfg->num_kv_heads * (fp8 ? kF8Page / 16 : 4 * cfg->head_dim);
     const double saved = token * (batch - num_groups) * max_shared_len;
-    const double own = token * batch * std::max(0, max_seq_len - max_shared_len);
-    return fp8 ? saved >= 64e6 + 1.5 * own + 1.1e6 * num_groups * cfg->num_kv_heads : saved >= 40e6;
+    if (!fp8) return saved >= 40e6;
+    const double own = num_groups > 1 ? token * batch * std::max(0, max_seq_len - max_shared_len) : 0.;
+    return saved >= 80e6 + 2e6 * num_groups * cfg->num_kv_heads + 0.3 * std::min(own, 2. * saved);
 }
 
 // Workspace of the form that reads prefixes once (SharedArgs), each part 256-byte
