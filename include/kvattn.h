@@ -598,11 +598,12 @@ kvattn_status kvattn_decode_window_fp8(const kvattn_config* cfg, const kvattn_ca
  * Every dtype, head layout and block size of kvattn_decode.  Prefixes are read
  * once in bf16 and fp8 caches whose block_size is a multiple of 16 (pools of fewer
  * than 2^31 / Hkv tokens), for at most 192 groups and 2 to 2048 sequences, if that
- * saves enough by the call's bounds (40 MB of K and V; fp8: 80 MB, 2 MB for each group and
- * KV head, and with several groups more for long own parts, up to 2.5 times that); then a group's first 128 tokens or more, down to a
- * multiple of 16, that at least two sequences have.  Other calls read each sequence
- * by itself, as kvattn_decode_window without a window does.  The host sees the bounds
- * only, so max_shared_len should be close to the shared lengths.
+ * saves enough by the call's bounds (40 MB of K and V; fp8: 80 MB, 2 MB for each
+ * group and KV head, and with several groups more for long own parts, up to 2.5
+ * times that); then a group's first 128 tokens or more, down to a multiple of 16,
+ * that at least two sequences have.  Other calls read each sequence by itself, as
+ * kvattn_decode_window without a window does.  The host sees the bounds only, so
+ * max_shared_len should be close to the shared lengths.
  * What a sequence sees counts as in kvattn_decode_window: a NaN score makes
  * its query head's output NaN.  Weights over a prefix are rounded to bf16 before
  * their product with V.
